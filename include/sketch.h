@@ -86,14 +86,21 @@ typedef enum {
     SKETCH_OP_PROJECT_INPUTS = 1,
     SKETCH_OP_ACCUMULATE = 2,
     SKETCH_OP_UPDATE_NORMSGD = 3,
-    SKETCH_OP_UPDATE_SGD = 4
+    SKETCH_OP_UPDATE_SGD = 4,
+    SKETCH_OP_LAYER_NORM_BACKWARD = 5,    /* T, k */
+    SKETCH_OP_CROSS_ENTROPY_FORWARD = 6,  /* T, d = V */
+    SKETCH_OP_CROSS_ENTROPY_BACKWARD = 7  /* T, d = V, k, r = the sketch's rank or 0 */
 } sketch_op;
+
+/* Element types of the training operators' tensors. */
+typedef enum { SKETCH_BF16 = 0, SKETCH_FP32 = 1 } sketch_dtype;
 
 /* Bits of the device status word (int32) written by the update calls. */
 #define SKETCH_DEV_H_ZERO 1        /* ||H||_F == 0: W left unchanged */
 #define SKETCH_DEV_H_NONFINITE 2   /* ||H||_F is inf or NaN: W left unchanged */
 #define SKETCH_DEV_W_NONFINITE 4   /* ||W||_F is inf or NaN: W left unchanged */
 #define SKETCH_DEV_QR_BREAKDOWN 8  /* non-positive pivot in the QR Cholesky */
+#define SKETCH_DEV_BAD_TARGET 16   /* a cross-entropy target >= V */
 
 /* Workspace bytes the call `op` needs for these sizes (0 = none).  Arguments
  * that an op does not use are ignored.  Returns 0 for invalid sizes too; the
@@ -327,6 +334,104 @@ SKETCH_API sketch_status sketch_apply_update_normsgd_batched(int n, const sketch
 SKETCH_API sketch_status sketch_apply_update_sgd_batched(int n, const sketch_update_problem* problems, int64_t r,
                                                          float alpha_eta, uint64_t seed, uint32_t step, void* ws,
                                                          size_t ws_bytes, void* stream);
+
+/* ---- Training operators around the sketched layers ---------------------------
+ * What a training step needs beside the sketched linear layers: the norm that
+ * makes their inputs, the loss that starts the backward pass, and the update of
+ * the tensors that are not sketched.  The pages describe none of these; the
+ * formulas are the operators' usual ones. */
+
+/* Layer norm of each row of X (T x k): mu = mean(x), rstd = 1/sqrt(mean((x -
+ * mu)^2) + eps), Y = (x - mu) rstd gamma + beta.  X and Y have type x_type and
+ * row strides ld_x, ld_y >= k (any value; rows that start on 16 bytes are the
+ * fast case); gamma and beta hold k contiguous values of w_type and may each be
+ * NULL (ones, zeros).  Y may be X.  mean and rstd (T fp32 each) are written for
+ * the backward pass.  Pointers are aligned to their element type; T, k >= 1;
+ * eps >= 0.  Statistics are fp32, the variance from deviations. */
+SKETCH_API sketch_status sketch_layer_norm_forward(const void* X, sketch_dtype x_type, int64_t T, int64_t k,
+                                                   int64_t ld_x, const void* gamma, const void* beta,
+                                                   sketch_dtype w_type, float eps, void* Y, int64_t ld_y,
+                                                   float* mean, float* rstd, void* stream);
+
+/* Its gradient.  With xh = (x - mu) rstd and dxh = dY gamma: dX = rstd (dxh -
+ * mean(dxh) - xh mean(dxh xh)), dgamma (+)= sum over rows of dY xh, dbeta (+)=
+ * sum over rows of dY.  dY and dX have X's type; dX (which may be dY), dgamma and
+ * dbeta (k fp32 each) may be NULL, not all three.  overwrite = 1 replaces dgamma
+ * and dbeta, 0 adds to them, as sketch_accumulate does for C. */
+SKETCH_API sketch_status sketch_layer_norm_backward(const void* dY, int64_t ld_dy, const void* X,
+                                                    sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
+                                                    const void* gamma, sketch_dtype w_type, const float* mean,
+                                                    const float* rstd, void* dX, int64_t ld_dx, float* dgamma,
+                                                    float* dbeta, int overwrite, void* ws, size_t ws_bytes,
+                                                    void* stream);
+
+/* Softmax cross entropy of a linear head, without storing its T x V logits l =
+ * scale X W^T: lse = log sum_v exp(l_v), loss = lse - l[target], per token, both
+ * fp32.  X: T x k BF16, W: V x k BF16 (row strides ld_x, ld_w as everywhere; k a
+ * multiple of 8); targets: T int64.  A negative target marks an ignored token:
+ * its loss is 0.  A target >= V gives that token loss NaN and sets
+ * SKETCH_DEV_BAD_TARGET in *dev_status (nullable; 0 otherwise).  scale, finite
+ * and > 0, is the inverse temperature.  The products are BF16 on the tensor
+ * cores with fp32 accumulation. */
+SKETCH_API sketch_status sketch_cross_entropy_forward(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x,
+                                                      const uint16_t* W, int64_t V, int64_t ld_w,
+                                                      const int64_t* targets, float scale, float* loss,
+                                                      float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                                      void* stream);
+
+/* Its gradient for the per-token upstream gradient g (T fp32: 1/n for a mean, an
+ * advantage for a policy gradient) and the forward call's lse.  With D = g scale
+ * (exp(l - lse) - onehot(target)), formed anew in pieces of the vocabulary and
+ * rounded to BF16 like every output derivative of this library:
+ *   dX = D W              (T x k BF16; nullable)
+ *   dW = D^T X            (V x k, BF16 or fp32 by dw_type; nullable)
+ *   C (+)= D^T XP         (V x r fp32, the head's gradient sketch for
+ *                          sketch_apply_update_*; XP = X P, T x r BF16; C and XP
+ *                          both or neither)
+ * at least one of the three.  overwrite = 1 replaces an fp32 dW and C, 0 adds to
+ * them; a BF16 dW is always replaced.  Tokens with a negative target, or one >=
+ * V (flagged as in the forward call), take no part: their rows of dX are zero and
+ * the values of X and XP there, NaN included, reach no result.  Outputs must not
+ * overlap inputs. */
+SKETCH_API sketch_status sketch_cross_entropy_backward(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x,
+                                                       const uint16_t* W, int64_t V, int64_t ld_w,
+                                                       const int64_t* targets, float scale, const float* lse,
+                                                       const float* g, uint16_t* dX, int64_t ld_dx, void* dW,
+                                                       sketch_dtype dw_type, int64_t ld_dw, const uint16_t* XP,
+                                                       int64_t ld_xp, int64_t r, float* C, int overwrite,
+                                                       int32_t* dev_status, void* ws, size_t ws_bytes,
+                                                       void* stream);
+
+/* One AdamW step of n >= 1 tensors, step counted from 0 (t = step + 1): with g =
+ * grad_scale G, m = beta1 m + (1 - beta1) g, v = beta2 v + (1 - beta2) g^2,
+ *   W = W (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps).
+ * A BF16 W is written by stochastic rounding with the bits of (seed, layer,
+ * step), as the sketch updates write theirs.  Tensors are contiguous and 16-byte
+ * aligned; n = 0 elements is allowed.  grad_scale (nullable) is a device scalar,
+ * for clipping by a norm that the host does not wait for.  lr, weight_decay
+ * finite, 0 <= beta < 1, eps > 0.
+ * The states of all tensors of a call have one form:
+ *   32 bits: m and v fp32, n values each; m_scale = v_scale = NULL.
+ *   8 bits: m and v hold E4M3 codes, n bytes each, and m_scale, v_scale an fp32
+ *   scale per 256 values, ceil(n / 256) each; m = code * scale, sqrt(v) = code *
+ *   scale, stochastically rounded with streams of (seed, layer, step) of their
+ *   own.  A positive sqrt(v) is never rounded to zero.  All zeros is the initial
+ *   state of both forms.
+ * A gradient that is not finite reaches its own weight and states only. */
+typedef struct {
+    void* W;
+    const void* G;
+    void* m;
+    void* v;
+    float* m_scale;
+    float* v_scale;
+    int64_t n;
+    uint32_t layer;       /* Philox counter word of the tensor's rounding streams */
+    sketch_dtype w_type, g_type;
+} sketch_adamw_problem;
+SKETCH_API sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem* problems, double lr, double beta1,
+                                              double beta2, double eps, double weight_decay,
+                                              const float* grad_scale, uint64_t seed, uint32_t step, void* stream);
 
 /* Read and clear the device error word of the current device: bits set by
  * kernels whose bounded internal waits gave up (a kernel that cannot make

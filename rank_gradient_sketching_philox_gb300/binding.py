@@ -27,11 +27,18 @@ OP_PROJECT_INPUTS = 1
 OP_ACCUMULATE = 2
 OP_UPDATE_NORMSGD = 3
 OP_UPDATE_SGD = 4
+OP_LAYER_NORM_BACKWARD = 5
+OP_CROSS_ENTROPY_FORWARD = 6
+OP_CROSS_ENTROPY_BACKWARD = 7
+
+DTYPE_BF16 = 0
+DTYPE_FP32 = 1
 
 DEV_H_ZERO = 1
 DEV_H_NONFINITE = 2
 DEV_W_NONFINITE = 4
 DEV_QR_BREAKDOWN = 8
+DEV_BAD_TARGET = 16
 
 EXPORTS = ("sketch_workspace_bytes", "sketch_sample_projection", "sketch_project_inputs",
            "sketch_accumulate", "sketch_apply_update_normsgd", "sketch_apply_update_sgd",
@@ -42,7 +49,9 @@ EXPORTS = ("sketch_workspace_bytes", "sketch_sample_projection", "sketch_project
            "sketch_read_device_errors", "sketch_read_exact_count", "sketch_kernel_launches",
            "sketch_projection_split_elems",
            "sketch_split_projection_batched", "sketch_project_inputs_fp32xp_batched",
-           "sketch_accumulate_fp32xp_batched", "sketch_split_projection_grouped", "sketch_status_string",
+           "sketch_accumulate_fp32xp_batched", "sketch_split_projection_grouped",
+           "sketch_layer_norm_forward", "sketch_layer_norm_backward", "sketch_cross_entropy_forward",
+           "sketch_cross_entropy_backward", "sketch_adamw_batched", "sketch_status_string",
            "sketch_last_error")
 
 
@@ -71,6 +80,12 @@ class UpdateProblem(ctypes.Structure):
                 ("ld_w", ctypes.c_int64), ("C", ctypes.c_void_p), ("P", ctypes.c_void_p),
                 ("layer", ctypes.c_uint32), ("wnorm2_in", ctypes.c_void_p),
                 ("wnorm2_out", ctypes.c_void_p), ("dev_status", ctypes.c_void_p)]
+
+
+class AdamWProblem(ctypes.Structure):
+    _fields_ = [("W", ctypes.c_void_p), ("G", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("layer", ctypes.c_uint32), ("w_type", ctypes.c_int), ("g_type", ctypes.c_int)]
 
 
 class SketchError(RuntimeError):
@@ -118,6 +133,16 @@ _SIGS = {
     "sketch_apply_update_normsgd_noalloc": (_c.c_int, [_vp, _i64, _i64, _i64, _vp, _vp, _i64, _c.c_float,
                                                        _u64, _u32, _u32, _vp, _vp, _vp, _vp]),
     "sketch_noalloc_scratch_bytes": (ctypes.c_size_t, []),
+    "sketch_layer_norm_forward": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _vp, _vp, _c.c_int, _c.c_float,
+                                             _vp, _i64, _vp, _vp, _vp]),
+    "sketch_layer_norm_backward": (_c.c_int, [_vp, _i64, _vp, _c.c_int, _i64, _i64, _i64, _vp, _c.c_int, _vp,
+                                              _vp, _vp, _i64, _vp, _vp, _c.c_int, _vp, _c.c_size_t, _vp]),
+    "sketch_cross_entropy_forward": (_c.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _c.c_float, _vp,
+                                                _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "sketch_cross_entropy_backward": (_c.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _c.c_float, _vp,
+                                                 _vp, _vp, _i64, _vp, _c.c_int, _i64, _vp, _i64, _i64, _vp,
+                                                 _c.c_int, _vp, _vp, _c.c_size_t, _vp]),
+    "sketch_adamw_batched": (_c.c_int, [_c.c_int, _vp] + [_c.c_double] * 5 + [_vp, _u64, _u32, _vp]),
     "sketch_status_string": (_c.c_char_p, [_c.c_int]),
     "sketch_last_error": (_c.c_char_p, []),
 }
@@ -536,3 +561,195 @@ def apply_update_sgd_batched(Ws, Cs, Ps, alpha_eta, seed, layers, step, dev_stat
                              stream=None):
     return _update_batched(False, Ws, Cs, Ps, alpha_eta, seed, layers, step, None, None, dev_status,
                            ws, stream)
+
+
+# --------------------------------------------------------------------------
+# Training operators around the sketched layers
+# --------------------------------------------------------------------------
+
+_DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
+
+
+def _dtype(t, name):
+    try:
+        return _DTYPES[t.dtype]
+    except KeyError:
+        raise ValueError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
+
+
+def _norm_rows(t, like, name):
+    """Row stride of a 2-D CUDA activation tensor of ``like``'s shape, type and device."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a 2-D CUDA tensor with unit column stride" % name)
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError("%s must have X's shape, type and device" % name)
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _vector(t, n, dtype, device, name):
+    """Contiguous vector of n values on ``device``; of ``dtype``, or BF16 or fp32 when that is None."""
+    if not t.is_contiguous() or t.numel() != n or t.device != device or (dtype is not None and t.dtype != dtype):
+        raise ValueError("%s must be a contiguous %s vector of %d on %s" % (name, dtype or "", n, device))
+
+
+def _norm_weights(gamma, beta, k, device):
+    for t, name in ((gamma, "gamma"), (beta, "beta")):
+        if t is not None:
+            _vector(t, k, None, device, name)
+    if gamma is not None and beta is not None and gamma.dtype != beta.dtype:
+        raise ValueError("gamma and beta must have one type")
+    t = gamma if gamma is not None else beta
+    return DTYPE_FP32 if t is None else _dtype(t, "gamma and beta")
+
+
+def layer_norm_forward(X, gamma, beta, Y, mean, rstd, eps=1e-5, stream=None):
+    """Y = (X - mean) rstd gamma + beta over the rows of X (T x k, BF16 or fp32);
+    mean and rstd (T fp32) are written for the backward pass.  gamma and beta
+    (k, BF16 or fp32) may be None.  Y may be X."""
+    x_type = _dtype(X, "X")
+    ld_x, ld_y = _norm_rows(X, X, "X"), _norm_rows(Y, X, "Y")
+    T, k = X.shape
+    dev = X.device
+    w_type = _norm_weights(gamma, beta, k, dev)
+    _vector(mean, T, torch.float32, dev, "mean")
+    _vector(rstd, T, torch.float32, dev, "rstd")
+    h, _ = _stream_handle(stream, dev)
+    _check(lib().sketch_layer_norm_forward(_ptr(X), x_type, T, k, ld_x, _ptr(gamma), _ptr(beta), w_type, eps,
+                                           _ptr(Y), ld_y, _ptr(mean), _ptr(rstd), h))
+    return Y
+
+
+def layer_norm_backward(dY, X, gamma, mean, rstd, dX=None, dgamma=None, dbeta=None, overwrite=False, ws=None,
+                        stream=None):
+    """dX (X's type, may be dY), and dgamma, dbeta (k fp32; replaced with
+    overwrite, else added to) of layer_norm_forward; each may be None."""
+    x_type = _dtype(X, "X")
+    ld_x, ld_dy = _norm_rows(X, X, "X"), _norm_rows(dY, X, "dY")
+    T, k = X.shape
+    dev = X.device
+    ld_dx = 0 if dX is None else _norm_rows(dX, X, "dX")
+    w_type = _norm_weights(gamma, None, k, dev)
+    _vector(mean, T, torch.float32, dev, "mean")
+    _vector(rstd, T, torch.float32, dev, "rstd")
+    for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
+        if t is not None:
+            _vector(t, k, torch.float32, dev, name)
+    h, s = _stream_handle(stream, dev)
+    nbytes = workspace_bytes(OP_LAYER_NORM_BACKWARD, T, 0, k)
+    wsb = _workspace(nbytes, dev, s, ws)
+    _check(lib().sketch_layer_norm_backward(_ptr(dY), ld_dy, _ptr(X), x_type, T, k, ld_x, _ptr(gamma), w_type,
+                                            _ptr(mean), _ptr(rstd), _ptr(dX), ld_dx, _ptr(dgamma), _ptr(dbeta),
+                                            1 if overwrite else 0, _ptr(wsb), nbytes, h))
+    return dX
+
+
+def _head(X, W, targets):
+    ld_x, ld_w = _rows(X, torch.bfloat16, "X"), _rows(W, torch.bfloat16, "W")
+    if W.shape[1] != X.shape[1] or W.device != X.device:
+        raise ValueError("shape or device mismatch: X %s, W %s" % (tuple(X.shape), tuple(W.shape)))
+    _vector(targets, X.shape[0], torch.int64, X.device, "targets")
+    return ld_x, ld_w
+
+
+def _status_word(t, device):
+    if t is not None:
+        _vector(t, 1, torch.int32, device, "dev_status")
+
+
+def cross_entropy_forward(X, W, targets, loss, lse, scale=1.0, dev_status=None, ws=None, stream=None):
+    """Per-token loss = lse - l[target] and lse = log sum exp(l) (T fp32 each) of
+    the logits l = scale X W^T, which are not stored; X (T x k) and W (V x k)
+    BF16, targets T int64.  A negative target: loss 0."""
+    ld_x, ld_w = _head(X, W, targets)
+    T, k = X.shape
+    V = W.shape[0]
+    dev = X.device
+    _vector(loss, T, torch.float32, dev, "loss")
+    _vector(lse, T, torch.float32, dev, "lse")
+    _status_word(dev_status, dev)
+    h, s = _stream_handle(stream, dev)
+    nbytes = workspace_bytes(OP_CROSS_ENTROPY_FORWARD, T, V)
+    wsb = _workspace(nbytes, dev, s, ws)
+    _check(lib().sketch_cross_entropy_forward(_ptr(X), T, k, ld_x, _ptr(W), V, ld_w, _ptr(targets), scale,
+                                              _ptr(loss), _ptr(lse), _ptr(dev_status), _ptr(wsb), nbytes, h))
+    return loss
+
+
+def cross_entropy_backward(X, W, targets, lse, g, dX=None, dW=None, XP=None, C=None, overwrite=False, scale=1.0,
+                           dev_status=None, ws=None, stream=None):
+    """Gradients of cross_entropy_forward for the per-token upstream gradient g
+    (T fp32): dX (T x k BF16), dW (V x k; BF16, or fp32) and the head's gradient
+    sketch C (+)= D^T XP (V x r fp32, with XP = X P, T x r BF16); each may be
+    None.  An fp32 dW and C are replaced with overwrite, else added to."""
+    ld_x, ld_w = _head(X, W, targets)
+    T, k = X.shape
+    V = W.shape[0]
+    dev = X.device
+    _vector(lse, T, torch.float32, dev, "lse")
+    _vector(g, T, torch.float32, dev, "g")
+    _status_word(dev_status, dev)
+    ld_dx = ld_dw = ld_xp = r = dw_type = 0
+    if dX is not None:
+        ld_dx = _rows(dX, torch.bfloat16, "dX")
+    if dW is not None:
+        dw_type = _dtype(dW, "dW")
+        ld_dw = _rows(dW, dW.dtype, "dW")
+    if (dX is not None and (dX.shape != X.shape or dX.device != dev)) or (
+            dW is not None and (dW.shape != W.shape or dW.device != dev)):
+        raise ValueError("dX and dW must have the shapes and the device of X and W")
+    if (C is None) != (XP is None):
+        raise ValueError("C and XP are given together")
+    if C is not None:
+        _contig(C, torch.float32, "C")
+        ld_xp = _rows(XP, torch.bfloat16, "XP")
+        r = C.shape[1]
+        if C.dim() != 2 or C.shape[0] != V or XP.shape[0] != T or XP.shape[1] < r or C.device != dev or XP.device != dev:
+            raise ValueError("shape or device mismatch: XP %s, C %s" % (tuple(XP.shape), tuple(C.shape)))
+    h, s = _stream_handle(stream, dev)
+    nbytes = workspace_bytes(OP_CROSS_ENTROPY_BACKWARD, T, V, k, r)
+    wsb = _workspace(nbytes, dev, s, ws)
+    _check(lib().sketch_cross_entropy_backward(_ptr(X), T, k, ld_x, _ptr(W), V, ld_w, _ptr(targets), scale,
+                                               _ptr(lse), _ptr(g), _ptr(dX), ld_dx, _ptr(dW), dw_type, ld_dw,
+                                               _ptr(XP), ld_xp, r, _ptr(C), 1 if overwrite else 0,
+                                               _ptr(dev_status), _ptr(wsb), nbytes, h))
+    return dX
+
+
+def adamw_problems(Ws, Gs, ms, vs, m_scales=None, v_scales=None, layers=None):
+    """The problem table of adamw_batched: lists of contiguous tensors of one
+    size per problem.  States: fp32 m and v, or float8_e4m3fn codes of m and
+    sqrt(v) with an fp32 scale per 256 values each."""
+    n = len(Ws)
+    eight = m_scales is not None
+    if not (len(Gs) == len(ms) == len(vs) == n > 0) or (v_scales is not None) != eight or (
+            eight and not (len(m_scales) == len(v_scales) == n)) or (layers is not None and len(layers) != n):
+        raise ValueError("the lists of a batch have one length, and at least one tensor")
+    probs = (AdamWProblem * n)()
+    state = torch.float8_e4m3fn if eight else torch.float32
+    for i in range(n):
+        W, G, dev = Ws[i], Gs[i], Ws[i].device
+        if dev.type != "cuda" or dev != Ws[0].device:
+            raise ValueError("tensor %d must be a CUDA tensor on one device with the others" % i)
+        size = W.numel()
+        _vector(W, size, None, dev, "W")
+        _vector(G, size, None, dev, "G")
+        _vector(ms[i], size, state, dev, "m")
+        _vector(vs[i], size, state, dev, "v")
+        scales = (None, None)
+        if eight:
+            for t in (m_scales[i], v_scales[i]):
+                _vector(t, (size + 255) // 256, torch.float32, dev, "a state's scales")
+            scales = (m_scales[i].data_ptr(), v_scales[i].data_ptr())
+            if size == 0:  # an empty tensor has no address; any non-NULL one keeps the call's form
+                scales = (W.element_size(), W.element_size())
+        probs[i] = AdamWProblem(W.data_ptr(), G.data_ptr(), ms[i].data_ptr(), vs[i].data_ptr(), scales[0], scales[1],
+                                size, i if layers is None else layers[i], _dtype(W, "W"), _dtype(G, "G"))
+    return probs
+
+
+def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=None, device=None, stream=None):
+    """One AdamW step (counted from 0) of the tensors of adamw_problems."""
+    dev = device if device is not None else torch.cuda.current_device()
+    h, _ = _stream_handle(stream, dev)
+    _check(lib().sketch_adamw_batched(len(probs), probs, lr, betas[0], betas[1], eps, weight_decay,
+                                      _ptr(grad_scale), seed & 0xFFFFFFFFFFFFFFFF, step, h))

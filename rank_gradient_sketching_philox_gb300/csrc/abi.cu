@@ -102,7 +102,24 @@ size_t update_ws_bytes(bool normsgd, int64_t d, int64_t k, int64_t r) {
   return rgs::carve_update_workspace(cur, d, k, (int)r, normsgd, nullptr);
 }
 
+// Cross entropy: tokens, vocabulary and width whose tile coordinates stay below 2^31.
+bool head_sizes_ok(int64_t T, int64_t V, int64_t k) {
+  return T >= 1 && T <= rgs::kMaxHeadDim && V >= 1 && V <= rgs::kMaxHeadDim && k >= 8 && k % 8 == 0 &&
+         k <= rgs::kMaxHeadDim;
+}
+
 size_t op_ws_bytes(sketch_op op, int64_t T, int64_t d, int64_t k, int64_t r) {
+  switch (op) {  // the training operators, whose sizes are checked as the calls check them
+    case SKETCH_OP_LAYER_NORM_BACKWARD:
+      return (T >= 1 && T <= kMaxDim && k >= 1 && k <= kMaxDim) ? rgs::norm_backward_workspace_bytes(T, k) : 0;
+    case SKETCH_OP_CROSS_ENTROPY_FORWARD:
+      return head_sizes_ok(T, d, 8) ? rgs::head_forward_workspace_bytes(T, d) : 0;
+    case SKETCH_OP_CROSS_ENTROPY_BACKWARD:
+      return (head_sizes_ok(T, d, k) && r >= 0 && r <= rgs::kMaxRank)
+                 ? rgs::head_backward_workspace_bytes(T, d, k, r)
+                 : 0;
+    default: break;
+  }
   if (r < 1 || r > rgs::kMaxRank) return 0;
   switch (op) {
     case SKETCH_OP_SAMPLE_PROJECTION: return (k >= 1) ? qr_ws_bytes(k, r) : 0;
@@ -110,6 +127,7 @@ size_t op_ws_bytes(sketch_op op, int64_t T, int64_t d, int64_t k, int64_t r) {
     case SKETCH_OP_ACCUMULATE: return (T >= 1 && d >= 1) ? rgs::accumulate_workspace_bytes(T, d, r) : 0;
     case SKETCH_OP_UPDATE_NORMSGD: return (d >= 1 && k >= 1) ? update_ws_bytes(true, d, k, r) : 0;
     case SKETCH_OP_UPDATE_SGD: return (d >= 1 && k >= 1) ? update_ws_bytes(false, d, k, r) : 0;
+    default: break;
   }
   return 0;
 }
@@ -308,6 +326,62 @@ sketch_status do_update(bool normsgd, int n, const sketch_update_problem* probs,
   return launch_result(err, normsgd ? "apply_update_normsgd" : "apply_update_sgd");
 }
 
+// ---- training operators ---------------------------------------------------------
+bool is_dtype(int t) { return t == SKETCH_BF16 || t == SKETCH_FP32; }
+
+#define CHECK_DTYPE(t)                                                                      \
+  do {                                                                                      \
+    if (!is_dtype((int)(t))) return fail(SKETCH_ERR_INVALID_ARG, "unknown %s %d", #t, (int)(t)); \
+  } while (0)
+
+#define CHECK_ELEM_PTR(p, type)                                                             \
+  do {                                                                                      \
+    if ((p) == nullptr) return fail(SKETCH_ERR_INVALID_ARG, "%s is NULL", #p);              \
+    CHECK_OPT_ALIGN(p, (type) == SKETCH_BF16 ? 2 : 4);                                      \
+  } while (0)
+
+// A row stride of the layer norm: at least the row, no alignment of its own.
+sketch_status check_row_stride(const char* name, int64_t ld, int64_t width) {
+  if (ld < width || ld > kMaxDim)
+    return fail(SKETCH_ERR_INVALID_ARG, "%s=%lld out of [%lld, 2^31)", name, (long long)ld, (long long)width);
+  return SKETCH_OK;
+}
+
+sketch_status check_head(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x, const uint16_t* W, int64_t V,
+                         int64_t ld_w, const int64_t* targets, float scale, const int32_t* dev_status) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("V", V));
+  TRY(check_k(k));
+  if (!head_sizes_ok(T, V, k))
+    return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld, V=%lld or k=%lld exceeds %lld", (long long)T, (long long)V,
+                (long long)k, (long long)rgs::kMaxHeadDim);
+  TRY(check_ld("ld_x", ld_x, k));
+  TRY(check_ld("ld_w", ld_w, k));
+  CHECK_PTR(X);
+  CHECK_PTR(W);
+  if (targets == nullptr) return fail(SKETCH_ERR_INVALID_ARG, "targets is NULL");
+  CHECK_OPT_ALIGN(targets, 8);
+  CHECK_OPT_ALIGN(dev_status, 4);
+  if (!std::isfinite(scale) || !(scale > 0.f)) return fail(SKETCH_ERR_INVALID_ARG, "scale is not finite and > 0");
+  return SKETCH_OK;
+}
+
+sketch_status check_adamw(const sketch_adamw_problem& p, bool states8) {
+  if (p.n < 0 || p.n > (int64_t(1) << 35)) return fail(SKETCH_ERR_INVALID_ARG, "n=%lld out of [0, 2^35]", (long long)p.n);
+  CHECK_DTYPE(p.w_type);
+  CHECK_DTYPE(p.g_type);
+  if ((p.m_scale != nullptr) != states8 || (p.v_scale != nullptr) != states8)
+    return fail(SKETCH_ERR_INVALID_ARG, "m_scale and v_scale are given for all tensors of a call or for none");
+  if (p.n == 0) return SKETCH_OK;
+  CHECK_PTR(p.W);
+  CHECK_PTR(p.G);
+  CHECK_PTR(p.m);
+  CHECK_PTR(p.v);
+  CHECK_OPT_ALIGN(p.m_scale, 4);
+  CHECK_OPT_ALIGN(p.v_scale, 4);
+  return SKETCH_OK;
+}
+
 }  // namespace
 
 namespace rgs {
@@ -473,6 +547,127 @@ sketch_status sketch_apply_update_sgd_batched(int n, const sketch_update_problem
 }
 
 uint64_t sketch_kernel_launches(void) { return rgs::launches_issued(); }
+
+sketch_status sketch_layer_norm_forward(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
+                                        const void* gamma, const void* beta, sketch_dtype w_type, float eps, void* Y,
+                                        int64_t ld_y, float* mean, float* rstd, void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("k", k));
+  CHECK_DTYPE(x_type);
+  CHECK_DTYPE(w_type);
+  TRY(check_row_stride("ld_x", ld_x, k));
+  TRY(check_row_stride("ld_y", ld_y, k));
+  if (!std::isfinite(eps) || eps < 0.f) return fail(SKETCH_ERR_INVALID_ARG, "eps is not finite and >= 0");
+  CHECK_ELEM_PTR(X, x_type);
+  CHECK_ELEM_PTR(Y, x_type);
+  CHECK_OPT_ALIGN(gamma, w_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_OPT_ALIGN(beta, w_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_ELEM_PTR(mean, SKETCH_FP32);
+  CHECK_ELEM_PTR(rstd, SKETCH_FP32);
+  const rgs::NormForward a = {X, (int)x_type, T, k, ld_x, gamma, beta, (int)w_type, eps, Y, ld_y, mean, rstd};
+  return launch_result(rgs::launch_norm_forward(a, static_cast<cudaStream_t>(stream)), "layer_norm_forward");
+}
+
+sketch_status sketch_layer_norm_backward(const void* dY, int64_t ld_dy, const void* X, sketch_dtype x_type, int64_t T,
+                                         int64_t k, int64_t ld_x, const void* gamma, sketch_dtype w_type,
+                                         const float* mean, const float* rstd, void* dX, int64_t ld_dx, float* dgamma,
+                                         float* dbeta, int overwrite, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("k", k));
+  CHECK_DTYPE(x_type);
+  CHECK_DTYPE(w_type);
+  TRY(check_row_stride("ld_dy", ld_dy, k));
+  TRY(check_row_stride("ld_x", ld_x, k));
+  if (dX) TRY(check_row_stride("ld_dx", ld_dx, k));
+  if (overwrite != 0 && overwrite != 1) return fail(SKETCH_ERR_INVALID_ARG, "overwrite must be 0 or 1");
+  CHECK_ELEM_PTR(dY, x_type);
+  CHECK_ELEM_PTR(X, x_type);
+  CHECK_OPT_ALIGN(gamma, w_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_ELEM_PTR(mean, SKETCH_FP32);
+  CHECK_ELEM_PTR(rstd, SKETCH_FP32);
+  if (!dX && !dgamma && !dbeta) return fail(SKETCH_ERR_INVALID_ARG, "dX, dgamma and dbeta are all NULL");
+  CHECK_OPT_ALIGN(dX, x_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_OPT_ALIGN(dgamma, 4);
+  CHECK_OPT_ALIGN(dbeta, 4);
+  TRY(check_ws(ws, ws_bytes, rgs::norm_backward_workspace_bytes(T, k)));
+  const rgs::NormBackward a = {dY,   X,    (int)x_type, T,  k,     ld_dy,  ld_x,  gamma,     (int)w_type,
+                               mean, rstd, dX,          ld_dx, dgamma, dbeta, overwrite, static_cast<float*>(ws)};
+  return launch_result(rgs::launch_norm_backward(a, static_cast<cudaStream_t>(stream)), "layer_norm_backward");
+}
+
+sketch_status sketch_cross_entropy_forward(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x, const uint16_t* W,
+                                           int64_t V, int64_t ld_w, const int64_t* targets, float scale, float* loss,
+                                           float* lse, int32_t* dev_status, void* ws, size_t ws_bytes,
+                                           void* stream) {
+  TRY(check_head(X, T, k, ld_x, W, V, ld_w, targets, scale, dev_status));
+  CHECK_ELEM_PTR(loss, SKETCH_FP32);
+  CHECK_ELEM_PTR(lse, SKETCH_FP32);
+  TRY(check_ws(ws, ws_bytes, rgs::head_forward_workspace_bytes(T, V)));
+  const rgs::HeadForward a = {X, T, k, ld_x, W, V, ld_w, targets, scale, loss, lse, dev_status};
+  return launch_result(rgs::launch_head_forward(a, ws, static_cast<cudaStream_t>(stream)), "cross_entropy_forward");
+}
+
+sketch_status sketch_cross_entropy_backward(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x, const uint16_t* W,
+                                            int64_t V, int64_t ld_w, const int64_t* targets, float scale,
+                                            const float* lse, const float* g, uint16_t* dX, int64_t ld_dx, void* dW,
+                                            sketch_dtype dw_type, int64_t ld_dw, const uint16_t* XP, int64_t ld_xp,
+                                            int64_t r, float* C, int overwrite, int32_t* dev_status, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  TRY(check_head(X, T, k, ld_x, W, V, ld_w, targets, scale, dev_status));
+  CHECK_ELEM_PTR(lse, SKETCH_FP32);
+  CHECK_ELEM_PTR(g, SKETCH_FP32);
+  if (overwrite != 0 && overwrite != 1) return fail(SKETCH_ERR_INVALID_ARG, "overwrite must be 0 or 1");
+  if (!dX && !dW && !C) return fail(SKETCH_ERR_INVALID_ARG, "dX, dW and C are all NULL");
+  if (dX) {
+    TRY(check_ld("ld_dx", ld_dx, k));
+    CHECK_PTR(dX);
+  }
+  if (dW) {
+    CHECK_DTYPE(dw_type);
+    TRY(check_ld("ld_dw", ld_dw, k));
+    CHECK_PTR(dW);
+  }
+  if ((C != nullptr) != (XP != nullptr)) return fail(SKETCH_ERR_INVALID_ARG, "C and XP are given together");
+  if (C) {
+    TRY(check_rank(r));
+    TRY(check_ld("ld_xp", ld_xp, r));
+    CHECK_PTR(C);
+    CHECK_PTR(XP);
+  }
+  TRY(check_ws(ws, ws_bytes, rgs::head_backward_workspace_bytes(T, V, k, C ? r : 0)));
+  const rgs::HeadBackward a = {X,  T,  k,     ld_x, W,            V,     ld_w, targets, scale, lse, g,         dX,
+                               ld_dx, dW, (int)dw_type, ld_dw, XP,   ld_xp,   r,     C,   overwrite, dev_status};
+  return launch_result(rgs::launch_head_backward(a, ws, static_cast<cudaStream_t>(stream)), "cross_entropy_backward");
+}
+
+sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem* problems, double lr, double beta1,
+                                   double beta2, double eps, double weight_decay, const float* grad_scale,
+                                   uint64_t seed, uint32_t step, void* stream) {
+  TRY(check_n(n));
+  if (problems == nullptr) return fail(SKETCH_ERR_INVALID_ARG, "problems is NULL");
+  if (!std::isfinite(lr) || !std::isfinite(weight_decay))
+    return fail(SKETCH_ERR_INVALID_ARG, "lr or weight_decay is not finite");
+  // in fp32 a beta just below 1 would round to 1
+  if (!(beta1 >= 0.0 && (float)beta1 < 1.f) || !(beta2 >= 0.0 && (float)beta2 < 1.f))
+    return fail(SKETCH_ERR_INVALID_ARG, "beta1 or beta2 out of [0, 1)");
+  if (!std::isfinite(eps) || !((float)eps > 0.f)) return fail(SKETCH_ERR_INVALID_ARG, "eps is not finite and > 0");
+  CHECK_OPT_ALIGN(grad_scale, 4);
+  const bool states8 = problems[0].m_scale != nullptr;
+  for (int i = 0; i < n; ++i) TRY(check_adamw(problems[i], states8));
+  const double t = (double)step + 1.0;
+  rgs::AdamStep h = {};
+  h.decay = (float)(1.0 - lr * weight_decay);
+  h.lr_m = (float)(lr / (1.0 - std::pow(beta1, t)));
+  h.root_v = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, t)));
+  h.beta1 = (float)beta1;
+  h.beta2 = (float)beta2;
+  h.one_beta1 = (float)(1.0 - beta1);
+  h.one_beta2 = (float)(1.0 - beta2);
+  h.eps = (float)eps;
+  h.grad_scale = grad_scale;
+  return launch_result(rgs::launch_adamw(n, problems, states8, h, seed, step, static_cast<cudaStream_t>(stream)),
+                       "adamw");
+}
 
 sketch_status sketch_read_device_errors(int32_t* flags, void* stream) {
   if (flags == nullptr) return fail(SKETCH_ERR_INVALID_ARG, "flags is NULL");

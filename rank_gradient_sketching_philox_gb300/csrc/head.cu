@@ -1,0 +1,834 @@
+// Softmax cross entropy of a linear head over a large vocabulary, without
+// storing its logits.
+//
+//   l = scale X W^T,  lse = log sum_v exp l_v,  loss = lse - l[target]
+//   D = g scale (exp(l - lse) - onehot(target))
+//   dX = D W,   dW = D^T X   (or the sketch C (+)= D^T XP of dW)
+//
+// X: T x k and W: V x k BF16; a token whose target is negative is ignored
+// (loss 0, no gradient).  Every product runs in one persistent kernel,
+// head_gemm_kernel: pairs of CTAs (cta_group::2) on 256 x 256 tiles, K streamed
+// in 64-wide chunks by TMA into a ring of stages, tcgen05 BF16 MMAs into two
+// TMEM accumulators in turn, so that one tile's epilogue overlaps the next
+// tile's MMAs.  Its epilogues:
+//   stats   each row's maximum and sum of exponentials over 128 columns, the
+//           target's left out; head_combine_kernel joins them per row
+//   dlogit  D from the logits and the row's lse, rounded to BF16 (as every D of
+//           this library is: the tensor cores take 16-bit operands; 2^-9 of each
+//           entry, independent over the terms that dX and dW add up)
+//   dx      rows of dX, added up over the vocabulary's pieces in fp32
+//   dw      rows of dW
+// The backward pass walks the vocabulary in pieces, so that only T x piece
+// logit gradients exist at a time.  One launch forms a piece's rows of dW, its
+// part of dX and the next piece's D.  Ignored tokens are dropped beforehand: the
+// kept rows of X are gathered to the front (head_gather_kernel), the products
+// run over those alone, and what an ignored row of X holds, infinities or NaN
+// too, reaches no result.
+//
+// Softmax statistics and every sum are fp32.  A tile's result is written by one
+// thread after a fixed-order accumulation, so results do not depend on timing.
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "tc.cuh"
+
+namespace rgs {
+namespace {
+
+constexpr int kChunk = 64;                  // K elements per stage: one 128-byte swizzle row
+constexpr int kTile = 256;                  // rows and columns of a pair's tile
+constexpr int kHalf = 128;                  // rows of A and of B that each CTA of the pair loads
+constexpr uint32_t kOperandBytes = kHalf * kChunk * 2;
+constexpr uint32_t kStageBytes = 2 * kOperandBytes;
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;                // four lane quarters x two column halves
+constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
+constexpr int kMaxProducts = 3;
+constexpr int kGroupM = 8;                  // tile rows walked together, so that their operands stay in L2
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+enum Epilogue { kEpiStats = 0, kEpiDlogit = 1, kEpiDx = 2, kEpiDw = 3 };
+
+// One product A B^T (M x N, K): operands K-major (rows x K) or MN-major (K x rows).
+struct Product {
+  CUtensorMap tmA, tmB;
+  int a_mn, b_mn;
+  int a_row, a_k;       // coordinates of A's first row and K element
+  int b_row, b_k;
+  int M, N, K;          // M or K is replaced by the number of kept rows where kept_m / kept_k says so
+  int kept_m, kept_k;
+  int epi;
+};
+
+struct HeadLaunch {
+  Product p[kMaxProducts];
+  int n;
+  const int* kept;      // device: number of kept rows, null where all are
+  int* err;
+  int64_t T;
+  // stats
+  const int64_t* targets;
+  float scale_log2;     // scale * log2(e)
+  float2* partials;     // [128-column block][T]: (maximum, sum) in log2 units, without the target's
+  // dlogit
+  const float* lse_log2;  // per kept row: lse * log2(e)
+  const float* weight;    // per kept row: g * scale
+  const int* target;      // per kept row
+  uint16_t* D;
+  int64_t ld_d;
+  int d_first;            // the vocabulary entry of D's first column
+  // dx
+  const int* row_of;      // the row of X that each kept row came from
+  float* acc;             // kept rows x k, fp32
+  int dx_first, dx_last;  // this is the vocabulary's first / last piece
+  uint16_t* dX;
+  int64_t ld_dx;
+  // dw
+  void* dW;               // of the piece's first row
+  int64_t ld_dw;
+  int dw_mode;            // 0: BF16; 1: fp32; 2: added to fp32
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+struct Tile {
+  int p, m, n;  // product, first row, first column
+};
+
+struct TileOrder {
+  int begin[kMaxProducts + 1];
+  int m_tiles[kMaxProducts], n_tiles[kMaxProducts];
+  int kchunks[kMaxProducts];
+  __device__ Tile at(int n_products, int item) const {
+    Tile t;
+    t.p = 0;
+    while (t.p + 1 < n_products && begin[t.p + 1] <= item) ++t.p;
+    const int local = item - begin[t.p];
+    const int per_group = kGroupM * n_tiles[t.p];
+    const int g = local / per_group, rem = local - g * per_group;
+    const int left = m_tiles[t.p] - g * kGroupM;
+    const int gm = left < kGroupM ? left : kGroupM;
+    t.n = rem / gm;
+    t.m = (g * kGroupM + (rem - t.n * gm)) * kTile;
+    t.n *= kTile;
+    return t;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
+    head_gemm_kernel(const __grid_constant__ HeadLaunch a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full_bar[kStages];   // the even CTA's: both CTAs' tiles have landed
+  __shared__ __align__(8) uint64_t empty_bar[kStages];  // each CTA's: the stage may be refilled
+  __shared__ __align__(8) uint64_t tfull_bar[2];        // each CTA's: an accumulator is complete
+  __shared__ __align__(8) uint64_t tempty_bar[2];       // the even CTA's: both CTAs have read an accumulator
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile int issued, consumed;
+  __shared__ TileOrder order;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+  const int pair = (int)blockIdx.x >> 1, n_pairs = (int)gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    issued = 0;
+    consumed = 0;
+    // with no kept row at all one tile of zero rows still runs, so that dW is written
+    int kept = a.kept ? *a.kept : 0;
+    if (kept < 1) kept = 1;
+    order.begin[0] = 0;
+    for (int p = 0; p < a.n; ++p) {
+      const Product& pr = a.p[p];
+      order.m_tiles[p] = ((pr.kept_m ? kept : pr.M) + kTile - 1) / kTile;
+      order.n_tiles[p] = (pr.N + kTile - 1) / kTile;
+      order.kchunks[p] = ((pr.kept_k ? kept : pr.K) + kChunk - 1) / kChunk;
+      order.begin[p + 1] = order.begin[p] + order.m_tiles[p] * order.n_tiles[p];
+    }
+    for (int s = 0; s < kStages; ++s) {
+      tc::mbar_init(&full_bar[s], 1);
+      tc::mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&tfull_bar[b], 1);
+      tc::mbar_init(&tempty_bar[b], 2 * kEpiWarps);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers exist before either signals one
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const int n_items = order.begin[a.n];
+
+  if (warp == 0 && lane == 0) {
+    // ---- producer: this CTA's half of each operand ----
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    bool stop = false;
+    for (int item = pair; item < n_items && !stop; item += n_pairs) {
+      const Tile t = order.at(a.n, item);
+      const Product& pr = a.p[t.p];
+      const int ar = pr.a_row + t.m + kHalf * (int)rank, br = pr.b_row + t.n + kHalf * (int)rank;
+      const int kchunks = order.kchunks[t.p];
+      for (int c = 0; c < kchunks; ++c, ++it) {
+        if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
+          stop = true;
+          break;
+        }
+        uint8_t* st = smem + (size_t)s * kStageBytes;
+        if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], 2 * kStageBytes);
+        const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full_bar[s]), 0);
+        const int ak = pr.a_k + c * kChunk, bk = pr.b_k + c * kChunk;
+        if (pr.a_mn) {  // two boxes of [64 k][64 rows]
+          tc::tma_load_2d_pair(st, &pr.tmA, bar, ar, ak);
+          tc::tma_load_2d_pair(st + kOperandBytes / 2, &pr.tmA, bar, ar + 64, ak);
+        } else {  // one box of [128 rows][64 k]
+          tc::tma_load_2d_pair(st, &pr.tmA, bar, ak, ar);
+        }
+        uint8_t* bt = st + kOperandBytes;
+        if (pr.b_mn) {
+          tc::tma_load_2d_pair(bt, &pr.tmB, bar, br, bk);
+          tc::tma_load_2d_pair(bt + kOperandBytes / 2, &pr.tmB, bar, br + 64, bk);
+        } else {
+          tc::tma_load_2d_pair(bt, &pr.tmB, bar, bk, br);
+        }
+        issued = it + 1;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- MMA issuer, for both CTAs ----
+    int s = 0, it = 0, j = 0;
+    uint32_t ph = 0;
+    bool stop = false;
+    for (int item = pair; item < n_items && !stop; item += n_pairs, ++j) {
+      const int p = order.at(a.n, item).p;
+      const bool a_mn = a.p[p].a_mn != 0, b_mn = a.p[p].b_mn != 0;
+      const uint32_t idesc = tc::idesc_bf16(kTile, kTile, a_mn, b_mn);
+      // a 16-wide K step: 32 bytes along a K-major swizzle row, 16 rows of 128 bytes of an MN-major tile
+      const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
+      const uint32_t a_lbo = a_mn ? 8192u : 16u, b_lbo = b_mn ? 8192u : 16u;
+      const int kchunks = order.kchunks[p];
+      const int b = j & 1;
+      if (j >= 2 && !tc::mbar_wait(&tempty_bar[b], ((j >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
+        break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + (uint32_t)(b * kTile);
+      for (int c = 0; c < kchunks; ++c, ++it) {
+        if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) {
+          stop = true;
+          break;
+        }
+        tc::tc_fence_after();
+        const uint32_t sa = tc::smem_u32(smem + (size_t)s * kStageBytes);
+        const uint64_t ad = tc::sdesc_sw128(sa, a_lbo, 1024), bd = tc::sdesc_sw128(sa + kOperandBytes, b_lbo, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kChunk / 16; ++kk)
+          tc::mma_bf16_pair(acc, ad + kk * a_step, bd + kk * b_step, idesc, (c > 0 || kk > 0) ? 1u : 0u);
+        tc::mma_commit_pair(&empty_bar[s]);
+        consumed = it + 1;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+      if (!stop) tc::mma_commit_pair(&tfull_bar[b]);
+    }
+  } else if (warp >= 2) {
+    // ---- epilogue: one row per thread, half of the tile's columns ----
+    const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
+    const int half = (warp - 2) >> 2;
+    const int q = quarter * 32 + lane;
+    int j = 0;
+    for (int item = pair; item < n_items; item += n_pairs, ++j) {
+      const Tile t = order.at(a.n, item);
+      const Product& pr = a.p[t.p];
+      const int b = j & 1;
+      const int row = t.m + kHalf * (int)rank + q;
+      const int col0 = t.n + half * kHalf;
+      const int N = pr.N;
+      const bool live = tc::mbar_wait(&tfull_bar[b], (j >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutMma);
+      if (!__all_sync(0xFFFFFFFFu, live)) break;
+      tc::tc_fence_after();
+      const uint32_t acc = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * kTile + half * kHalf);
+      uint32_t v[32];
+      if (pr.epi == kEpiStats) {
+        const int M = pr.M;
+        const int64_t target = row < M ? a.targets[row] : -1;
+        const int tcol = (target >= col0 && target < col0 + kHalf && target < N) ? (int)(target - col0) : -1;
+        float mx = -INFINITY, sum = 0.f;
+        for (int cg = 0; cg < kHalf / 32; ++cg) {
+          tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
+          tc::tmem_wait_ld_regs(v);
+          const int c0 = col0 + cg * 32;
+          if (c0 + 32 > N) {  // past the vocabulary: no logits
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c0 + i >= N) v[i] = __float_as_uint(-INFINITY);
+          }
+          if (tcol >= 0 && (tcol >> 5) == cg) {  // the target's own term is added by head_combine_kernel
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if ((tcol & 31) == i) v[i] = __float_as_uint(-INFINITY);
+          }
+          float g = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g = fmaxf(g, __uint_as_float(v[i]) * a.scale_log2);
+          const float top = fmaxf(mx, g);
+          const float ref = top == -INFINITY ? 0.f : top;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            s0 += ex2(fmaf(__uint_as_float(v[i]), a.scale_log2, -ref));
+            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), a.scale_log2, -ref));
+          }
+          sum = sum * ex2(mx - ref) + (s0 + s1);
+          mx = top;
+        }
+        if (row < M && col0 < N) a.partials[(int64_t)(col0 / kHalf) * a.T + row] = make_float2(mx, sum);
+      } else if (pr.epi == kEpiDlogit) {
+        // rows past the kept ones are written as zeros up to the tile's end,
+        // since they take part in dW's sum over rows
+        const bool in = row < *a.kept;
+        const float w = in ? a.weight[row] : 0.f, l2 = in ? a.lse_log2[row] : 0.f;
+        const int tcol = in ? a.target[row] - (a.d_first + col0) : -1;
+        uint16_t* out = a.D + (int64_t)row * a.ld_d + col0;
+        for (int cg = 0; cg < kHalf / 32; ++cg) {
+          tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
+          tc::tmem_wait_ld_regs(v);
+          uint32_t d[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), a.scale_log2, -l2));
+            float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), a.scale_log2, -l2));
+            if (tcol == cg * 32 + 2 * i) p0 -= 1.f;
+            if (tcol == cg * 32 + 2 * i + 1) p1 -= 1.f;
+            d[i] = in ? pack_bf16(p0 * w, p1 * w) : 0u;
+          }
+          // D's row stride is a multiple of the tile's width
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(out + cg * 32)[i] = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+        }
+      } else if (pr.epi == kEpiDx) {
+        const bool in = row < *a.kept;
+        float* sum = a.acc + (int64_t)row * N + col0;
+        uint16_t* out = (in && a.dx_last) ? a.dX + (int64_t)a.row_of[row] * a.ld_dx + col0 : nullptr;
+        for (int cg = 0; cg < kHalf / 32; ++cg) {
+          tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
+          tc::tmem_wait_ld_regs(v);
+          if (!in) continue;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {  // k is a multiple of 8
+            const int c = cg * 32 + 8 * i;
+            if (col0 + c >= N) break;
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * i + e]);
+            if (!a.dx_first) {
+              const float4 x = *reinterpret_cast<const float4*>(sum + c), y = *reinterpret_cast<const float4*>(sum + c + 4);
+              f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+              f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+            }
+            if (a.dx_last) {
+              *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
+                                                              pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+            } else {
+              *reinterpret_cast<float4*>(sum + c) = make_float4(f[0], f[1], f[2], f[3]);
+              *reinterpret_cast<float4*>(sum + c + 4) = make_float4(f[4], f[5], f[6], f[7]);
+            }
+          }
+        }
+      } else {
+        const bool in = row < pr.M;
+        for (int cg = 0; cg < kHalf / 32; ++cg) {
+          tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
+          tc::tmem_wait_ld_regs(v);
+          if (!in) continue;
+          const int64_t at = (int64_t)row * a.ld_dw + col0 + cg * 32;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (col0 + cg * 32 + 8 * i >= N) break;
+            const uint32_t* f = v + 8 * i;
+            if (a.dw_mode == 0) {
+              uint32_t d[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) d[e] = pack_bf16(__uint_as_float(f[2 * e]), __uint_as_float(f[2 * e + 1]));
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dW) + at + 8 * i) = make_uint4(d[0], d[1], d[2], d[3]);
+            } else {
+              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dW) + at + 8 * i);
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float4 x = make_float4(__uint_as_float(f[4 * e]), __uint_as_float(f[4 * e + 1]),
+                                       __uint_as_float(f[4 * e + 2]), __uint_as_float(f[4 * e + 3]));
+                if (a.dw_mode == 2) {
+                  const float4 y = o[e];
+                  x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+                }
+                o[e] = x;
+              }
+            }
+          }
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tempty_bar[b]), 0));
+    }
+  }
+  __syncwarp();
+  // ---- on a timeout, give copies still in flight a bounded chance to land ----
+  tc::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_flag) {
+    volatile int dummy = 0;
+    if (rank == 0) {
+      for (int i = consumed; i < issued; ++i)
+        tc::mbar_wait(&full_bar[i % kStages], (i / kStages) & 1, &dummy, nullptr, 0, 100000000ull);
+    } else {
+      const uint64_t t0 = tc::globaltimer();
+      while (tc::globaltimer() - t0 < 100000000ull) {
+      }
+    }
+  }
+  __syncthreads();
+  tc::cluster_sync();  // neither CTA leaves while the other may still signal it
+  if (warp == 0) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+__device__ __forceinline__ void join(float& mx, float& sum, float mx1, float sum1) {
+  const float top = fmaxf(mx, mx1);
+  const float ref = top == -INFINITY ? 0.f : top;
+  sum = sum * ex2(mx - ref) + sum1 * ex2(mx1 - ref);
+  mx = top;
+}
+
+// Join a row's partial statistics with its target's logit.  That logit is a dot
+// product of its own in fp32 (the tensor cores' accumulation truncates, which
+// the loss would show at a relative 1.5e-6 for k = 4096; so 6e-7) and stands
+// both in the sum and in loss = lse - logit, so that a confident token's small
+// loss keeps its digits.  Block: eight rows; a warp for each dot product, and
+// 32 threads for each row's partials.
+constexpr int kCombineRows = 8;
+__global__ void __launch_bounds__(256) head_combine_kernel(const float2* partials, const uint16_t* X, int64_t ld_x,
+                                                           const uint16_t* W, int64_t ld_w, int64_t k,
+                                                           const int64_t* targets, float scale_log2, int64_t T,
+                                                           int64_t V, int blocks, float* loss, float* lse,
+                                                           int32_t* status) {
+  __shared__ float2 part[32][kCombineRows];
+  __shared__ float hit[kCombineRows];
+  __shared__ int bad;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t row0 = (int64_t)blockIdx.x * kCombineRows;
+  const int64_t row = row0 + (threadIdx.x & 7);
+  float mx = -INFINITY, sum = 0.f;
+  if (row < T) {
+#pragma unroll 4
+    for (int i = threadIdx.x >> 3; i < blocks; i += 32) {
+      const float2 v = partials[(int64_t)i * T + row];
+      join(mx, sum, v.x, v.y);
+    }
+  }
+  part[threadIdx.x >> 3][threadIdx.x & 7] = make_float2(mx, sum);
+  const int64_t drow = row0 + warp;
+  const int64_t target = drow < T ? targets[drow] : -1;
+  float dot = 0.f;
+  if (target >= 0 && target < V) {
+    const uint4* x = reinterpret_cast<const uint4*>(X + drow * ld_x);
+    const uint4* w = reinterpret_cast<const uint4*>(W + target * ld_w);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+    for (int64_t i = lane; i < k / 8; i += 32) {
+      const uint4 a = x[i], b = w[i];
+      const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s0 = fmaf(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16), s0);
+        s1 = fmaf(__uint_as_float(p[e] & 0xFFFF0000u), __uint_as_float(q[e] & 0xFFFF0000u), s1);
+      }
+    }
+    dot = s0 + s1;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  }
+  if (lane == 0) hit[warp] = dot * scale_log2;
+  if (threadIdx.x == 0) bad = 0;
+  __syncthreads();
+  if (threadIdx.x < kCombineRows && row < T) {
+    for (int i = 1; i < 32; ++i) join(mx, sum, part[i][threadIdx.x].x, part[i][threadIdx.x].y);
+    const int64_t t = targets[row];
+    const float h = hit[threadIdx.x];
+    if (t >= 0 && t < V) join(mx, sum, h, 1.f);
+    const float l2 = (mx == -INFINITY ? 0.f : mx) + log2f(sum);
+    lse[row] = l2 * kLn2;
+    loss[row] = t < 0 ? 0.f : t >= V ? NAN : (((mx - h) + log2f(sum)) * kLn2);
+  }
+  if (status != nullptr && blockIdx.x == 0) {
+    int found = 0;
+    for (int64_t i = threadIdx.x; i < T; i += blockDim.x) found |= targets[i] >= V;
+    if (found) bad = 1;
+    __syncthreads();
+    if (threadIdx.x == 0) *status = bad ? SKETCH_DEV_BAD_TARGET : 0;
+  }
+}
+
+// Gather the kept tokens' rows to the front, in order.  Block: eight rows, one
+// per warp.  Each block counts the kept tokens before its own, so that no pass
+// over the targets comes first.  Compact rows past the kept ones, up to `fill`
+// (a multiple of the tile's rows), are zeroed.
+struct Gather {
+  const uint16_t* X;
+  int64_t T, k, ld_x;
+  const uint16_t* XP;  // nullable
+  int64_t ld_xp, r;
+  int64_t V;
+  const int64_t* targets;
+  const float* lse;
+  const float* g;
+  float scale;
+  uint16_t* Xc;   // rows x k
+  uint16_t* XPc;  // rows x ld_xpc
+  int64_t ld_xpc;
+  float* lse_log2;
+  float* weight;
+  int* target;
+  int* row_of;
+  int* kept;
+  uint16_t* dX;  // nullable
+  int64_t ld_dx;
+  int64_t rows;  // compact rows the buffers hold
+  int all_rows;  // zero every compact row past the kept ones, not only the last tile's
+  int32_t* status;
+};
+
+__global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ Gather a) {
+  __shared__ int before_s, total_s, bad_s;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t base = (int64_t)blockIdx.x * 8;
+  if (threadIdx.x == 0) before_s = total_s = bad_s = 0;
+  __syncthreads();
+  int before = 0, total = 0, bad = 0;
+  for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
+    const int64_t t = a.targets[i];
+    const int keep = t >= 0 && t < a.V;
+    total += keep;
+    before += keep && i < base;
+    bad |= t >= a.V;
+  }
+  before = __reduce_add_sync(0xFFFFFFFFu, before);
+  total = __reduce_add_sync(0xFFFFFFFFu, total);
+  bad = __any_sync(0xFFFFFFFFu, bad);
+  if (lane == 0) {  // integer sums: the same in any order
+    atomicAdd(&before_s, before);
+    atomicAdd(&total_s, total);
+    if (bad) bad_s = 1;
+  }
+  __syncthreads();
+  total = total_s;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    *a.kept = total;
+    if (a.status) *a.status = bad_s ? SKETCH_DEV_BAD_TARGET : 0;
+  }
+  const int64_t row = base + warp;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (row < a.T) {
+    int64_t dst = before_s;
+    int64_t t = 0;
+    for (int w = 0; w <= warp; ++w) {
+      t = a.targets[base + w];
+      if (w < warp) dst += t >= 0 && t < a.V;
+    }
+    if (t >= 0 && t < a.V) {
+      const uint4* x = reinterpret_cast<const uint4*>(a.X + row * a.ld_x);
+      uint4* y = reinterpret_cast<uint4*>(a.Xc + dst * a.k);
+      for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = x[i];
+      if (a.XP)
+        for (int64_t i = lane; i < a.r; i += 32) a.XPc[dst * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
+      if (lane == 0) {
+        a.lse_log2[dst] = a.lse[row] * kLog2e;
+        a.weight[dst] = a.g[row] * a.scale;
+        a.target[dst] = (int)t;
+        a.row_of[dst] = (int)row;
+      }
+    } else if (a.dX) {
+      uint4* y = reinterpret_cast<uint4*>(a.dX + row * a.ld_dx);
+      for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
+    }
+  }
+  int64_t fill = (int64_t)(total < 1 ? 1 : total);
+  fill = a.all_rows ? a.rows : (fill + kTile - 1) / kTile * kTile;
+  if (row >= total && row < fill) {
+    uint4* y = reinterpret_cast<uint4*>(a.Xc + row * a.k);
+    for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
+    if (a.XP)
+      for (int64_t i = lane; i < a.r; i += 32) a.XPc[row * a.ld_xpc + i] = 0;
+  }
+}
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Vocabulary entries per piece: as many whole tiles as 256 MB of BF16 logit
+// gradients hold.
+int64_t piece_width(int64_t T, int64_t V) {
+  const int64_t rows = round_up(T, kTile);
+  int64_t w = (int64_t(256) << 20) / (2 * rows) / kTile * kTile;
+  if (w < 4 * kTile) w = 4 * kTile;
+  const int64_t all = round_up(V, kTile);
+  return w < all ? w : all;
+}
+
+constexpr size_t kHeadSmem = (size_t)kStages * kStageBytes + 1024;
+
+// CTA pairs that the device holds at once (its SMs need not all pair up).
+cudaError_t head_pairs(int* out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> pairs[kMaxDevices];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (pairs[dev] == 0) {
+    err = cudaFuncSetAttribute(head_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kHeadSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)num_sms(), 1, 1);
+    cfg.blockDim = dim3(kHeadThreads, 1, 1);
+    cfg.dynamicSmemBytes = kHeadSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    err = cudaOccupancyMaxActiveClusters(&n, head_gemm_kernel, &cfg);
+    if (err != cudaSuccess) return err;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    pairs[dev] = n;
+  }
+  *out = pairs[dev];
+  return cudaSuccess;
+}
+
+cudaError_t launch_products(const HeadLaunch& a, cudaStream_t stream) {
+  int64_t items = 0;
+  for (int p = 0; p < a.n; ++p) items += ceil_div(a.p[p].M, kTile) * ceil_div(a.p[p].N, kTile);
+  if (items > (int64_t(1) << 30)) return cudaErrorInvalidValue;
+  int pairs = 0;
+  cudaError_t err = head_pairs(&pairs);
+  if (err != cudaSuccess) return err;
+  if (items < pairs) pairs = (int)items;
+  count_launch();
+  head_gemm_kernel<<<2 * pairs, kHeadThreads, kHeadSmem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// Operand rows x K, K contiguous (box 64 x 128), or K x rows, rows contiguous (box 64 x 64).
+cudaError_t k_major(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t K, int64_t ld) {
+  return encode_tmap_bf16_2d(map, p, (uint64_t)K, (uint64_t)rows, (uint64_t)ld * 2, kChunk, kHalf);
+}
+cudaError_t mn_major(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t K, int64_t ld) {
+  return encode_tmap_bf16_2d(map, p, (uint64_t)rows, (uint64_t)K, (uint64_t)ld * 2, 64, kChunk);
+}
+
+struct BackwardWorkspace {
+  uint16_t* Xc;
+  uint16_t* XPc;
+  int64_t ld_xpc;
+  uint16_t* D[2];
+  float* acc;
+  float* lse_log2;
+  float* weight;
+  int* target;
+  int* row_of;
+  int* kept;
+  size_t bytes;
+};
+BackwardWorkspace carve_backward(void* base, int64_t T, int64_t V, int64_t k, int64_t r) {
+  WsCursor cur;
+  cur.base = static_cast<char*>(base);
+  const int64_t rows = round_up(T, kTile), piece = piece_width(T, V);
+  const bool pieces = piece < V;
+  BackwardWorkspace w;
+  w.Xc = cur.take<uint16_t>((size_t)(rows * k));
+  w.ld_xpc = round_up(r, 8);
+  w.XPc = cur.take<uint16_t>((size_t)(rows * w.ld_xpc));
+  for (int i = 0; i < 2; ++i) w.D[i] = cur.take<uint16_t>((size_t)((i == 0 || pieces) ? rows * piece : 0));
+  w.acc = cur.take<float>((size_t)(pieces ? rows * k : 0));
+  w.lse_log2 = cur.take<float>((size_t)rows);
+  w.weight = cur.take<float>((size_t)rows);
+  w.target = cur.take<int>((size_t)rows);
+  w.row_of = cur.take<int>((size_t)rows);
+  w.kept = cur.take<int>(1);
+  cur.take<char>(0);
+  w.bytes = cur.offset;
+  return w;
+}
+
+}  // namespace
+
+size_t head_forward_workspace_bytes(int64_t T, int64_t V) {
+  WsCursor cur;
+  cur.take<float2>((size_t)(ceil_div(V, kHalf) * T));
+  cur.take<char>(0);
+  return cur.offset;
+}
+
+cudaError_t launch_head_forward(const HeadForward& f, void* ws, cudaStream_t stream) {
+  WsCursor cur;
+  cur.base = static_cast<char*>(ws);
+  const int blocks = (int)ceil_div(f.V, kHalf);
+  HeadLaunch a = {};
+  a.partials = cur.take<float2>((size_t)(blocks * f.T));
+  cudaError_t err = device_error_word(&a.err);
+  if (err != cudaSuccess) return err;
+  a.n = 1;
+  a.T = f.T;
+  a.targets = f.targets;
+  a.scale_log2 = f.scale * kLog2e;
+  Product& p = a.p[0];
+  p.M = (int)f.T;
+  p.N = (int)f.V;
+  p.K = (int)f.k;
+  p.epi = kEpiStats;
+  err = k_major(&p.tmA, f.X, f.T, f.k, f.ld_x);
+  if (err == cudaSuccess) err = k_major(&p.tmB, f.W, f.V, f.k, f.ld_w);
+  if (err == cudaSuccess) err = launch_products(a, stream);
+  if (err != cudaSuccess) return err;
+  count_launch();
+  head_combine_kernel<<<(unsigned)ceil_div(f.T, kCombineRows), 256, 0, stream>>>(
+      a.partials, f.X, f.ld_x, f.W, f.ld_w, f.k, f.targets, a.scale_log2, f.T, f.V, blocks, f.loss, f.lse,
+      f.dev_status);
+  return cudaGetLastError();
+}
+
+size_t head_backward_workspace_bytes(int64_t T, int64_t V, int64_t k, int64_t r) {
+  return carve_backward(nullptr, T, V, k, r).bytes;
+}
+
+cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t stream) {
+  const bool sketch = f.C != nullptr;
+  const BackwardWorkspace w = carve_backward(ws, f.T, f.V, f.k, sketch ? f.r : 0);
+  const int64_t rows = round_up(f.T, kTile), piece = piece_width(f.T, f.V);
+  const int pieces = (int)ceil_div(f.V, piece);
+
+  Gather g = {};
+  g.X = f.X; g.T = f.T; g.k = f.k; g.ld_x = f.ld_x;
+  g.XP = sketch ? f.XP : nullptr; g.ld_xp = f.ld_xp; g.r = f.r;
+  g.V = f.V; g.targets = f.targets; g.lse = f.lse; g.g = f.g; g.scale = f.scale;
+  g.Xc = w.Xc; g.XPc = w.XPc; g.ld_xpc = w.ld_xpc;
+  g.lse_log2 = w.lse_log2; g.weight = w.weight; g.target = w.target; g.row_of = w.row_of; g.kept = w.kept;
+  g.dX = f.dX; g.ld_dx = f.ld_dx;
+  g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
+  count_launch();
+  head_gather_kernel<<<(unsigned)(rows / 8), 256, 0, stream>>>(g);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess) return err;
+
+  HeadLaunch a = {};
+  err = device_error_word(&a.err);
+  if (err != cudaSuccess) return err;
+  a.kept = w.kept;
+  a.T = f.T;
+  a.scale_log2 = f.scale * kLog2e;
+  a.lse_log2 = w.lse_log2;
+  a.weight = w.weight;
+  a.target = w.target;
+  a.row_of = w.row_of;
+  a.ld_d = piece;
+  a.acc = w.acc;
+  a.dX = f.dX;
+  a.ld_dx = f.ld_dx;
+  a.ld_dw = f.ld_dw;
+  a.dw_mode = f.dw_type == SKETCH_BF16 ? 0 : f.overwrite ? 1 : 2;
+  // step i: dX and dW of piece i - 1, and D of piece i
+  for (int i = 0; i <= pieces; ++i) {
+    a.n = 0;
+    if (i > 0) {
+      const int64_t v0 = (i - 1) * piece, width = f.V - v0 < piece ? f.V - v0 : piece;
+      const uint16_t* D = w.D[(i - 1) & 1];
+      if (f.dX) {
+        Product& p = a.p[a.n++];
+        p = Product{};
+        err = k_major(&p.tmA, D, rows, width, piece);
+        if (err == cudaSuccess) err = mn_major(&p.tmB, f.W, f.k, f.V, f.ld_w);
+        if (err != cudaSuccess) return err;
+        p.b_mn = 1;
+        p.b_k = (int)v0;
+        p.M = (int)f.T;
+        p.kept_m = 1;
+        p.N = (int)f.k;
+        p.K = (int)width;
+        p.epi = kEpiDx;
+        a.dx_first = i == 1;
+        a.dx_last = i == pieces;
+      }
+      if (f.dW) {
+        Product& p = a.p[a.n++];
+        p = Product{};
+        err = mn_major(&p.tmA, D, width, rows, piece);
+        if (err == cudaSuccess) err = mn_major(&p.tmB, w.Xc, f.k, rows, f.k);
+        if (err != cudaSuccess) return err;
+        p.a_mn = p.b_mn = 1;
+        p.M = (int)width;
+        p.N = (int)f.k;
+        p.K = (int)f.T;
+        p.kept_k = 1;
+        p.epi = kEpiDw;
+        const size_t size = f.dw_type == SKETCH_BF16 ? 2 : 4;
+        a.dW = static_cast<char*>(f.dW) + (size_t)(v0 * f.ld_dw) * size;
+      }
+      if (sketch) {
+        AccumulateProblem ap = {D, rows, width, piece, w.XPc, w.ld_xpc, f.C + v0 * f.r};
+        err = launch_accumulate(1, &ap, (int)f.r, f.overwrite, stream);
+        if (err != cudaSuccess) return err;
+      }
+    }
+    if (i < pieces) {
+      const int64_t v0 = i * piece, width = f.V - v0 < piece ? f.V - v0 : piece;
+      Product& p = a.p[a.n++];
+      p = Product{};
+      err = k_major(&p.tmA, w.Xc, rows, f.k, f.k);
+      if (err == cudaSuccess) err = k_major(&p.tmB, f.W, f.V, f.k, f.ld_w);
+      if (err != cudaSuccess) return err;
+      p.b_row = (int)v0;
+      p.M = (int)(sketch ? rows : f.T);
+      p.kept_m = !sketch;  // the sketch's sum runs over every compact row
+      p.N = (int)width;
+      p.K = (int)f.k;
+      p.epi = kEpiDlogit;
+      a.D = w.D[i & 1];
+      a.d_first = (int)v0;
+    }
+    if (a.n > 0) {
+      err = launch_products(a, stream);
+      if (err != cudaSuccess) return err;
+    }
+  }
+  return cudaSuccess;
+}
+
+}  // namespace rgs

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "sketch.h"
+
 namespace rgs {
 
 constexpr int kMaxRank = 256;
@@ -28,6 +30,9 @@ struct WsCursor {
 // BF16 2-D tensor map, 128-byte swizzle, zero fill outside the tensor.
 cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                               uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// The same map encoded anew for this call, not looked up or kept.
+cudaError_t encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                                uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 // Device address of the current device's error word (bits from tc.cuh).
 cudaError_t device_error_word(int** out);
 // Device address of the current device's count of weights the update kernels
@@ -213,5 +218,88 @@ cudaError_t launch_update_normsgd(int n, const UpdateProblem* probs, const Updat
                                   uint64_t seed, uint32_t step, cudaStream_t stream);
 cudaError_t launch_update_sgd(int n, const UpdateProblem* probs, const UpdateWorkspace* ws, int r, float alpha_eta,
                               uint64_t seed, uint32_t step, cudaStream_t stream);
+
+// ---- layer norm (norm.cu) ---------------------------------------------------
+struct NormForward {
+  const void* X;  // T x k, BF16 or fp32
+  int x_type;     // sketch_dtype of X and Y
+  int64_t T, k, ld_x;
+  const void* gamma;  // k values of w_type, nullable (ones)
+  const void* beta;   // k values of w_type, nullable (zeros)
+  int w_type;
+  float eps;
+  void* Y;
+  int64_t ld_y;
+  float* mean;
+  float* rstd;
+};
+cudaError_t launch_norm_forward(const NormForward& a, cudaStream_t stream);
+struct NormBackward {
+  const void* dY;
+  const void* X;
+  int x_type;  // sketch_dtype of dY, X and dX
+  int64_t T, k, ld_dy, ld_x;
+  const void* gamma;  // nullable (ones)
+  int w_type;
+  const float* mean;
+  const float* rstd;
+  void* dX;  // nullable
+  int64_t ld_dx;
+  float* dgamma;  // nullable
+  float* dbeta;   // nullable
+  int overwrite;
+  float* ws;
+};
+size_t norm_backward_workspace_bytes(int64_t T, int64_t k);
+cudaError_t launch_norm_backward(const NormBackward& a, cudaStream_t stream);
+
+// ---- cross entropy of a linear head (head.cu) --------------------------------
+constexpr int64_t kMaxHeadDim = int64_t(1) << 24;  // tokens, vocabulary, width
+struct HeadForward {
+  const uint16_t* X;  // T x k BF16
+  int64_t T, k, ld_x;
+  const uint16_t* W;  // V x k BF16
+  int64_t V, ld_w;
+  const int64_t* targets;
+  float scale;
+  float* loss;
+  float* lse;
+  int32_t* dev_status;  // nullable
+};
+size_t head_forward_workspace_bytes(int64_t T, int64_t V);
+cudaError_t launch_head_forward(const HeadForward& a, void* ws, cudaStream_t stream);
+struct HeadBackward {
+  const uint16_t* X;
+  int64_t T, k, ld_x;
+  const uint16_t* W;
+  int64_t V, ld_w;
+  const int64_t* targets;
+  float scale;
+  const float* lse;
+  const float* g;
+  uint16_t* dX;  // nullable
+  int64_t ld_dx;
+  void* dW;      // nullable
+  int dw_type;
+  int64_t ld_dw;
+  const uint16_t* XP;  // nullable, with C: the head's sketch
+  int64_t ld_xp, r;
+  float* C;
+  int overwrite;        // of an fp32 dW and of C
+  int32_t* dev_status;  // nullable
+};
+size_t head_backward_workspace_bytes(int64_t T, int64_t V, int64_t k, int64_t r);
+cudaError_t launch_head_backward(const HeadBackward& a, void* ws, cudaStream_t stream);
+
+// ---- AdamW (adamw.cu) ----------------------------------------------------------
+struct AdamStep {
+  float decay;    // 1 - lr * weight_decay
+  float lr_m;     // lr / (1 - beta1^t)
+  float root_v;   // 1 / sqrt(1 - beta2^t)
+  float beta1, beta2, one_beta1, one_beta2, eps;
+  const float* grad_scale;  // nullable device scalar
+};
+cudaError_t launch_adamw(int n, const sketch_adamw_problem* probs, bool states8, const AdamStep& h, uint64_t seed,
+                         uint32_t step, cudaStream_t stream);
 
 }  // namespace rgs

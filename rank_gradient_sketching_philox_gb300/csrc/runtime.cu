@@ -100,6 +100,11 @@ cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner
   return cudaSuccess;
 }
 
+cudaError_t encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                                uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return encode_bf16_2d(map, base, inner, outer, row_stride_bytes, box_inner, box_outer);
+}
+
 cudaError_t device_error_word(int** out) {
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
