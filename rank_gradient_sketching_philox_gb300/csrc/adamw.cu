@@ -27,75 +27,242 @@ namespace {
 
 constexpr uint32_t kTagMoment1 = 3u;
 constexpr uint32_t kTagMoment2 = 4u;
-constexpr int kBlock = 256;      // values that share a scale; threads per block
-constexpr int kAdamBatch = 256;  // tensors per launch
+constexpr int kAdamThreads = 256;
+constexpr int kUnit = 8;                         // values per thread: one Philox block of 16-bit lanes
+constexpr int kStep = kAdamThreads * kUnit;      // values per block and pass
+constexpr int kAdamBatch = 256;                  // tensors per launch
 
 struct AdamBatch {
   sketch_adamw_problem p[kAdamBatch];
-  int64_t begin[kAdamBatch + 1];  // prefix of the tensors' blocks of kBlock values
+  int begin[kAdamBatch + 1];  // prefix of the tensors' chunks
   int n;
+  int chunk;                  // values per block, a multiple of kStep
   AdamStep h;
-  uint64_t seed;
   uint32_t step;
+  uint32_t rk0[10], rk1[10];  // Philox round keys of the seed
 };
 
-// 16 random bits of value e.
-__device__ __forceinline__ uint32_t random16(const AdamBatch& a, uint32_t layer, uint32_t tag, int64_t e) {
-  const Philox4 r = stream_block(a.seed, layer, a.step, tag, (uint32_t)(e >> 3));
-  const int lane = (int)(e & 7);
-  const uint32_t w = lane < 4 ? (lane < 2 ? r.w0 : r.w1) : (lane < 6 ? r.w2 : r.w3);
-  return (lane & 1) ? w >> 16 : w & 0xFFFFu;
-}
+// What a thread loads for its eight values; converted once the values of the
+// pass before are done.
+template <bool STATES8, bool WF32, bool GF32>
+struct Loaded {
+  uint4 w[WF32 ? 2 : 1], g[GF32 ? 2 : 1];
+  uint4 m[STATES8 ? 1 : 2], v[STATES8 ? 1 : 2];  // 8-bit states: eight codes in x and y
+  float ms, vs;
+};
 
-// y in [0, 448] to E4M3 with 16 random bits below the kept mantissa.  Below 2^-6
-// E4M3's steps are 2^-9, which are those of y + 2^-6.
-__device__ __forceinline__ uint32_t sr_e4m3(float y, uint32_t rand16) {
-  const bool small = y < 0.015625f;
-  const uint32_t bits = __float_as_uint(small ? y + 0.015625f : y) + (rand16 << 4);
-  return (bits >> 20) - (small ? 968u : 960u);
-}
-
-__device__ __forceinline__ float e4m3_value(uint8_t c) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(c, __NV_E4M3);
-  return __half2float(*reinterpret_cast<const __half*>(&h));
-}
-
-__device__ __forceinline__ float block_max(float v) {
-  __shared__ float part[kBlock / 32];
+template <bool F32>
+__device__ __forceinline__ void load_values(const void* base, int64_t e, int64_t n, uint4* out) {
+  if (e + kUnit <= n) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + e * (F32 ? 4 : 2));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = part[0];
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) out[i] = __ldcs(p + i);
+    return;
+  }
+  uint32_t r[F32 ? 8 : 4] = {};
 #pragma unroll
-  for (int w = 1; w < kBlock / 32; ++w) v = fmaxf(v, part[w]);
-  return v;
+  for (int i = 0; i < kUnit; ++i) {  // the tensor's ragged end
+    if (e + i < n) {
+      if (F32) r[i] = static_cast<const uint32_t*>(base)[e + i];
+      else r[i >> 1] |= (uint32_t)static_cast<const uint16_t*>(base)[e + i] << (16 * (i & 1));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (F32 ? 2 : 1); ++i) out[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+}
+template <bool F32>
+__device__ __forceinline__ void store_values(void* base, int64_t e, int64_t n, const uint4* v) {
+  if (e + kUnit <= n) {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + e * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 2 : 1); ++i) __stcs(p + i, v[i]);
+    return;
+  }
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) {
+    if (e + i < n) {
+      if (F32) static_cast<uint32_t*>(base)[e + i] = r[i];
+      else static_cast<uint16_t*>(base)[e + i] = (uint16_t)(r[i >> 1] >> (16 * (i & 1)));
+    }
+  }
+}
+__device__ __forceinline__ uint2 load_codes(const void* base, int64_t e, int64_t n) {
+  const uint8_t* c = static_cast<const uint8_t*>(base) + e;
+  if (e + kUnit <= n) return __ldcs(reinterpret_cast<const uint2*>(c));
+  uint64_t r = 0;
+  for (int i = 0; e + i < n; ++i) r |= (uint64_t)c[i] << (8 * i);
+  return make_uint2((uint32_t)r, (uint32_t)(r >> 32));
+}
+__device__ __forceinline__ void store_codes(void* base, int64_t e, int64_t n, uint2 v) {
+  uint8_t* c = static_cast<uint8_t*>(base) + e;
+  if (e + kUnit <= n) {
+    __stcs(reinterpret_cast<uint2*>(c), v);
+    return;
+  }
+  const uint64_t r = ((uint64_t)v.y << 32) | v.x;
+  for (int i = 0; e + i < n; ++i) c[i] = (uint8_t)(r >> (8 * i));
+}
+
+template <bool F32>
+__device__ __forceinline__ void unpack(const uint4* v, float (&f)[kUnit]) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i)
+    f[i] = F32 ? __uint_as_float(r[i]) : __uint_as_float((i & 1) ? r[i >> 1] & 0xFFFF0000u : r[i >> 1] << 16);
+}
+__device__ __forceinline__ void unpack_codes(uint32_t x, uint32_t y, float (&f)[kUnit]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((i < 2 ? x : y) >> (16 * (i & 1))), __NV_E4M3);
+    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[2 * i] = v.x;
+    f[2 * i + 1] = v.y;
+  }
+}
+
+// The 16 random bits of value i as the stream lays them out, shifted left by 4.
+__device__ __forceinline__ uint32_t bits16_x16(const Philox4& r, int i) {
+  const uint32_t w = i < 4 ? (i < 2 ? r.w0 : r.w1) : (i < 6 ? r.w2 : r.w3);
+  return (i & 1) ? (w >> 12) & 0xFFFF0u : (w << 4) & 0xFFFF0u;
 }
 
 // Magnitudes below this are dropped from an 8-bit first moment whose whole block
 // is as small (the reciprocal of its scale would overflow).
 constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
+constexpr uint32_t kInfBits = 0x7F800000u;
 
-__device__ __forceinline__ void hold8(const AdamBatch& a, const sketch_adamw_problem& p, uint32_t tag, int64_t e, float x,
-                                      uint32_t least, uint8_t* codes, float* scales) {
-  const bool in = e < p.n;
-  const bool finite = in && fabsf(x) <= 3.402823466e38f;
-  const float top = block_max(finite ? fabsf(x) : 0.f);
-  const float inv = top >= kLeast ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
-  if (threadIdx.x == 0) scales[e / kBlock] = inv > 0.f ? __fmul_rn(top, 1.f / 448.f) : 0.f;
-  if (!in) return;
-  uint32_t c = 0x7Fu;
-  if (finite) {
-    c = sr_e4m3(fminf(__fmul_rn(fabsf(x), inv), 448.f), random16(a, p.layer, tag, e));
-    if (x != 0.f && inv > 0.f && c < least) c = least;
+// A block's 256 values, eight per lane, to E4M3 codes and a scale: stochastic
+// rounding adds 16 random bits below the three kept mantissa bits and truncates.
+// Below 2^-6 E4M3's steps are 2^-9, which are those of y + 2^-6.  KEEP: what is
+// not zero gets a code of at least 1.
+template <bool KEEP>
+__device__ __forceinline__ uint2 hold8(const float (&x)[kUnit], const Philox4& r, float* scale) {
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
+  top = __reduce_max_sync(0xFFFFFFFFu, top);
+  const bool odd = top >= kInfBits;  // the same in every lane
+  if (odd) {  // a value of the block is not finite: the scale is that of the others
+    top = 0;
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
+      top = max(top, b < kInfBits ? b : 0u);
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
   }
-  codes[e] = (uint8_t)(c | (x < 0.f ? 0x80u : 0u));
+  const float t = __uint_as_float(top);
+  const float inv = t >= kLeast ? __fmul_rn(__frcp_rn(t), 448.f) : 0.f;
+  if ((threadIdx.x & 31) == 0) *scale = inv > 0.f ? __fmul_rn(t, 1.f / 448.f) : 0.f;
+  uint32_t out[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < kUnit; ++i) {
+    const float y = fminf(__fmul_rn(fabsf(x[i]), inv), 448.f);
+    const bool small = y < 0.015625f;
+    uint32_t c = ((__float_as_uint(small ? y + 0.015625f : y) + bits16_x16(r, i)) >> 20) - (small ? 968u : 960u);
+    if (KEEP) c = max(c, (x[i] > 0.f && inv > 0.f) ? 1u : 0u);
+    if (odd && (__float_as_uint(x[i]) & 0x7FFFFFFFu) >= kInfBits) c = 0x7Fu;
+    if (!KEEP) c |= x[i] < 0.f ? 0x80u : 0u;
+    out[i >> 2] |= c << (8 * (i & 3));
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// One chunk of one tensor: passes of kStep values, a pass's loads issued before
+// the values of the pass before are worked on.
+template <bool STATES8, bool WF32, bool GF32>
+__device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_adamw_problem& p, int64_t begin) {
+  const int64_t n = p.n;
+  const int64_t left = n - begin;
+  const int passes = (int)(((left < a.chunk ? left : a.chunk) + kStep - 1) / kStep);
+  int64_t e = begin + (int64_t)threadIdx.x * kUnit;
+  const float gs = a.h.grad_scale ? *a.h.grad_scale : 1.f;
+  using L = Loaded<STATES8, WF32, GF32>;
+  auto load = [&](L& l, int64_t at) {
+    load_values<WF32>(p.W, at, n, l.w);
+    load_values<GF32>(p.G, at, n, l.g);
+    if constexpr (STATES8) {
+      const uint2 m = load_codes(p.m, at, n), v = load_codes(p.v, at, n);
+      l.m[0] = make_uint4(m.x, m.y, 0, 0);
+      l.v[0] = make_uint4(v.x, v.y, 0, 0);
+      const bool block = (at & ~int64_t(255)) < n;
+      l.ms = block ? p.m_scale[at >> 8] : 0.f;
+      l.vs = block ? p.v_scale[at >> 8] : 0.f;
+    } else {
+      load_values<true>(p.m, at, n, l.m);
+      load_values<true>(p.v, at, n, l.v);
+    }
+  };
+  L next;
+  load(next, e);
+  for (int i = 0; i < passes; ++i, e += kStep) {
+    const L l = next;
+    if (i + 1 < passes) load(next, e + kStep);
+    if ((e & ~int64_t(255)) >= n) break;  // the warp's values lie past the end
+    float w[kUnit], g[kUnit], m[kUnit], v[kUnit];
+    unpack<WF32>(l.w, w);
+    unpack<GF32>(l.g, g);
+    if constexpr (STATES8) {
+      unpack_codes(l.m[0].x, l.m[0].y, m);
+      unpack_codes(l.v[0].x, l.v[0].y, v);
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) {
+        m[j] = __fmul_rn(m[j], l.ms);
+        v[j] = __fmul_rn(v[j], l.vs);
+        v[j] = __fmul_rn(v[j], v[j]);
+      }
+    } else {
+      unpack<true>(l.m, m);
+      unpack<true>(l.v, v);
+    }
+    float u[kUnit];
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      const float x = g[j] * gs;
+      m[j] = __fadd_rn(__fmul_rn(a.h.beta1, m[j]), __fmul_rn(a.h.one_beta1, x));
+      v[j] = __fadd_rn(__fmul_rn(a.h.beta2, v[j]), __fmul_rn(__fmul_rn(a.h.one_beta2, x), x));
+      u[j] = __fsqrt_rn(v[j]);
+      w[j] = w[j] * a.h.decay - __fdividef(a.h.lr_m * m[j], fmaf(u[j], a.h.root_v, a.h.eps));
+    }
+    const uint32_t block = (uint32_t)(e >> 3);
+    if constexpr (WF32) {
+      uint4 o[2];
+      float* f = reinterpret_cast<float*>(o);
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) f[j] = w[j];
+      store_values<true>(p.W, e, n, o);
+    } else {
+      const Philox4 r = philox4x32_10_rk(block, a.step, p.layer, kTagSR, a.rk0, a.rk1);
+      const uint32_t words[4] = {r.w0, r.w1, r.w2, r.w3};
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        o[j] = sr_bf16_bits(w[2 * j], words[j] & 0xFFFFu) | (sr_bf16_bits(w[2 * j + 1], words[j] >> 16) << 16);
+      const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
+      store_values<false>(p.W, e, n, &ov);
+    }
+    if constexpr (STATES8) {
+      const Philox4 rm = philox4x32_10_rk(block, a.step, p.layer, kTagMoment1, a.rk0, a.rk1);
+      store_codes(p.m, e, n, hold8<false>(m, rm, p.m_scale + (e >> 8)));
+      const Philox4 ru = philox4x32_10_rk(block, a.step, p.layer, kTagMoment2, a.rk0, a.rk1);
+      store_codes(p.v, e, n, hold8<true>(u, ru, p.v_scale + (e >> 8)));
+    } else {
+      uint4 o[2];
+      float* f = reinterpret_cast<float*>(o);
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) f[j] = m[j];
+      store_values<true>(p.m, e, n, o);
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) f[j] = v[j];
+      store_values<true>(p.v, e, n, o);
+    }
+  }
 }
 
 template <bool STATES8>
-__global__ void __launch_bounds__(kBlock) adamw_kernel(const __grid_constant__ AdamBatch a) {
-  const int64_t block = blockIdx.x;
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamBatch a) {
+  const int block = blockIdx.x;
   int lo = 0, hi = a.n;  // the last tensor that begins at or before this block
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -103,41 +270,13 @@ __global__ void __launch_bounds__(kBlock) adamw_kernel(const __grid_constant__ A
     else hi = mid;
   }
   const sketch_adamw_problem& p = a.p[lo];
-  const int64_t e = (block - a.begin[lo]) * kBlock + threadIdx.x;
-  const bool in = e < p.n;
-  float w = 0.f, g = 0.f, m = 0.f, v = 0.f;
-  if (in) {
-    w = p.w_type == SKETCH_BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p.W)[e])
-                                : static_cast<const float*>(p.W)[e];
-    g = p.g_type == SKETCH_BF16 ? bf16_bits_to_float(static_cast<const uint16_t*>(p.G)[e])
-                                : static_cast<const float*>(p.G)[e];
-    if (STATES8) {
-      m = __fmul_rn(e4m3_value(static_cast<const uint8_t*>(p.m)[e]), p.m_scale[e / kBlock]);
-      v = __fmul_rn(e4m3_value(static_cast<const uint8_t*>(p.v)[e]), p.v_scale[e / kBlock]);
-      v = __fmul_rn(v, v);
-    } else {
-      m = static_cast<const float*>(p.m)[e];
-      v = static_cast<const float*>(p.v)[e];
-    }
-  }
-  if (a.h.grad_scale) g *= *a.h.grad_scale;
-  m = __fadd_rn(__fmul_rn(a.h.beta1, m), __fmul_rn(a.h.one_beta1, g));
-  v = __fadd_rn(__fmul_rn(a.h.beta2, v), __fmul_rn(__fmul_rn(a.h.one_beta2, g), g));
-  const float u = __fsqrt_rn(v);
-  w = w * a.h.decay - a.h.lr_m * m / (u * a.h.root_v + a.h.eps);
-  if (in) {
-    if (p.w_type == SKETCH_BF16)
-      static_cast<uint16_t*>(p.W)[e] = (uint16_t)sr_bf16_bits(w, random16(a, p.layer, kTagSR, e));
-    else
-      static_cast<float*>(p.W)[e] = w;
-  }
-  if (STATES8) {
-    __syncthreads();  // the block's scales are read before they are replaced
-    hold8(a, p, kTagMoment1, e, m, 0u, static_cast<uint8_t*>(p.m), p.m_scale);
-    hold8(a, p, kTagMoment2, e, u, 1u, static_cast<uint8_t*>(p.v), p.v_scale);
-  } else if (in) {
-    static_cast<float*>(p.m)[e] = m;
-    static_cast<float*>(p.v)[e] = v;
+  const int64_t begin = (int64_t)(block - a.begin[lo]) * a.chunk;
+  if (p.w_type == SKETCH_BF16) {
+    if (p.g_type == SKETCH_BF16) adamw_chunk<STATES8, false, false>(a, p, begin);
+    else adamw_chunk<STATES8, false, true>(a, p, begin);
+  } else {
+    if (p.g_type == SKETCH_BF16) adamw_chunk<STATES8, true, false>(a, p, begin);
+    else adamw_chunk<STATES8, true, true>(a, p, begin);
   }
 }
 
@@ -147,24 +286,29 @@ cudaError_t launch_adamw(int n, const sketch_adamw_problem* probs, bool states8,
                          uint32_t step, cudaStream_t stream) {
   static thread_local AdamBatch a;
   a.h = h;
-  a.seed = seed;
+  philox_round_keys(seed, a.rk0, a.rk1);
   a.step = step;
+  // a block per kStep values while that leaves no SM without one; else longer
+  // chunks, whose passes overlap
+  int64_t total = 0;
+  for (int i = 0; i < n; ++i) total += probs[i].n;
+  a.chunk = total <= (int64_t)num_sms() * 8 * kStep ? kStep : 4 * kStep;
   int i = 0;
   while (i < n) {
     a.n = 0;
     a.begin[0] = 0;
     for (; i < n && a.n < kAdamBatch; ++i) {
       if (probs[i].n == 0) continue;
-      const int64_t blocks = ceil_div(probs[i].n, kBlock);
-      if (a.n > 0 && a.begin[a.n] + blocks > (int64_t(1) << 30)) break;
+      const int64_t blocks = ceil_div(probs[i].n, a.chunk);  // at most 2^24
+      if (a.begin[a.n] + blocks > (int64_t(1) << 30)) break;
       a.p[a.n] = probs[i];
-      a.begin[a.n + 1] = a.begin[a.n] + blocks;
+      a.begin[a.n + 1] = (int)(a.begin[a.n] + blocks);
       ++a.n;
     }
     if (a.n == 0) continue;
     count_launch();
-    if (states8) adamw_kernel<true><<<(unsigned)a.begin[a.n], kBlock, 0, stream>>>(a);
-    else adamw_kernel<false><<<(unsigned)a.begin[a.n], kBlock, 0, stream>>>(a);
+    if (states8) adamw_kernel<true><<<(unsigned)a.begin[a.n], kAdamThreads, 0, stream>>>(a);
+    else adamw_kernel<false><<<(unsigned)a.begin[a.n], kAdamThreads, 0, stream>>>(a);
     const cudaError_t err = cudaGetLastError();
     if (err != cudaSuccess) return err;
   }
