@@ -409,7 +409,7 @@ SKETCH_API sketch_status sketch_cross_entropy_backward(const uint16_t* X, int64_
  * step), as the sketch updates write theirs.  Tensors are contiguous and 16-byte
  * aligned; n = 0 elements is allowed.  grad_scale (nullable) is a device scalar,
  * for clipping by a norm that the host does not wait for.  lr, weight_decay
- * finite, 0 <= beta < 1, eps > 0.
+ * finite, 0 <= beta < 1, eps at least the smallest normal fp32.
  * The states of all tensors of a call have one form:
  *   32 bits: m and v fp32, n values each; m_scale = v_scale = NULL.
  *   8 bits: m and v hold E4M3 codes, n bytes each, and m_scale, v_scale an fp32

@@ -1,6 +1,7 @@
 // C ABI of the sketching library: argument checks, workspace carving and
 // dispatch to the kernels.  Every check happens on the host before anything is
 // launched; see include/sketch.h for the contract of each entry point.
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -650,7 +651,8 @@ sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem* problems, 
   // in fp32 a beta just below 1 would round to 1
   if (!(beta1 >= 0.0 && (float)beta1 < 1.f) || !(beta2 >= 0.0 && (float)beta2 < 1.f))
     return fail(SKETCH_ERR_INVALID_ARG, "beta1 or beta2 out of [0, 1)");
-  if (!std::isfinite(eps) || !((float)eps > 0.f)) return fail(SKETCH_ERR_INVALID_ARG, "eps is not finite and > 0");
+  if (!std::isfinite(eps) || !((float)eps >= FLT_MIN))
+    return fail(SKETCH_ERR_INVALID_ARG, "eps is not finite and at least the smallest normal fp32");
   CHECK_OPT_ALIGN(grad_scale, 4);
   const bool states8 = problems[0].m_scale != nullptr;
   for (int i = 0; i < n; ++i) TRY(check_adamw(problems[i], states8));

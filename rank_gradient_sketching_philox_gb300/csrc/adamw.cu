@@ -121,10 +121,23 @@ __device__ __forceinline__ void unpack_codes(uint32_t x, uint32_t y, float (&f)[
   }
 }
 
-// The 16 random bits of value i as the stream lays them out, shifted left by 4.
-__device__ __forceinline__ uint32_t bits16_x16(const Philox4& r, int i) {
-  const uint32_t w = i < 4 ? (i < 2 ? r.w0 : r.w1) : (i < 6 ? r.w2 : r.w3);
-  return (i & 1) ? (w >> 12) & 0xFFFF0u : (w << 4) & 0xFFFF0u;
+// t plus the 16 random bits of value i, as the stream lays them out.
+__device__ __forceinline__ uint32_t plus_random(uint32_t t, const uint32_t (&r)[4], int i) {
+  return (i & 1) ? mad_hi(r[i >> 1], 65536u, t) : t + (r[i >> 1] & 0xFFFFu);
+}
+
+// Maximum of top and the magnitudes of a and b; NaN when one of them is.
+__device__ __forceinline__ float max3_abs(float top, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(top), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
+__device__ __forceinline__ float max8_abs(const float (&x)[kUnit]) {
+  float top = fabsf(x[0]);
+  top = max3_abs(top, x[1], x[2]);
+  top = max3_abs(top, x[3], x[4]);
+  top = max3_abs(top, x[5], x[6]);
+  return max3_abs(top, x[7], x[7]);
 }
 
 // Magnitudes below this are dropped from an 8-bit first moment whose whole block
@@ -132,20 +145,17 @@ __device__ __forceinline__ uint32_t bits16_x16(const Philox4& r, int i) {
 constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// A block's 256 values, eight per lane, to E4M3 codes and a scale: stochastic
-// rounding adds 16 random bits below the three kept mantissa bits and truncates.
-// Below 2^-6 E4M3's steps are 2^-9, which are those of y + 2^-6.  KEEP: what is
-// not zero gets a code of at least 1.
-template <bool KEEP>
-__device__ __forceinline__ uint2 hold8(const float (&x)[kUnit], const Philox4& r, float* scale) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kUnit; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-  top = __reduce_max_sync(0xFFFFFFFFu, top);
+// A block's 256 values, eight per lane, to E4M3 codes and a scale.  y = |x| /
+// scale lies in [0, 448]; times 2^-120 its exponent field is E4M3's (bias 7 for
+// 127) and its subnormals are E4M3's, so that the code is bits 20 to 26, with 16
+// random bits added below them and the rest cut off.  ROOT: x is a root of v, not
+// negative, and one that is not zero gets a code of at least 1.
+template <bool ROOT>
+__device__ __forceinline__ uint2 hold8(const float (&x)[kUnit], const uint32_t (&r)[4], float* scale) {
+  uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(max8_abs(x)));
   const bool odd = top >= kInfBits;  // the same in every lane
   if (odd) {  // a value of the block is not finite: the scale is that of the others
     top = 0;
-#pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
       top = max(top, b < kInfBits ? b : 0u);
@@ -155,18 +165,39 @@ __device__ __forceinline__ uint2 hold8(const float (&x)[kUnit], const Philox4& r
   const float t = __uint_as_float(top);
   const float inv = t >= kLeast ? __fmul_rn(__frcp_rn(t), 448.f) : 0.f;
   if ((threadIdx.x & 31) == 0) *scale = inv > 0.f ? __fmul_rn(t, 1.f / 448.f) : 0.f;
-  uint32_t out[2] = {0u, 0u};
+  uint32_t c[kUnit], out[2];
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) {
-    const float y = fminf(__fmul_rn(fabsf(x[i]), inv), 448.f);
-    const bool small = y < 0.015625f;
-    uint32_t c = ((__float_as_uint(small ? y + 0.015625f : y) + bits16_x16(r, i)) >> 20) - (small ? 968u : 960u);
-    if (KEEP) c = max(c, (x[i] > 0.f && inv > 0.f) ? 1u : 0u);
-    if (odd && (__float_as_uint(x[i]) & 0x7FFFFFFFu) >= kInfBits) c = 0x7Fu;
-    if (!KEEP) c |= x[i] < 0.f ? 0x80u : 0u;
-    out[i >> 2] |= c << (8 * (i & 3));
+    const float y = __fmul_rn(__fmul_rn(fabsf(x[i]), inv), 7.523163845262640e-37f);  // 2^-120
+    c[i] = plus_random(__float_as_uint(y) >> 4, r, i);                               // the code in bits 16 to 22
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __byte_perm(c[4 * h], c[4 * h + 1], 0x0062), hi = __byte_perm(c[4 * h + 2], c[4 * h + 3], 0x6200);
+    out[h] = __byte_perm(lo, hi, 0x7610);
+    if (!ROOT) {  // the values' signs
+      const uint32_t sl = __byte_perm(__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), 0x0073);
+      const uint32_t sh = __byte_perm(__float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3]), 0x7300);
+      out[h] |= __byte_perm(sl, sh, 0x7610) & 0x80808080u;
+    }
+  }
+  // rare values, looked for once per lane: roots that got the code 0, values that are not finite
+  const bool zero = ROOT && ((((out[0] - 0x01010101u) & ~out[0]) | ((out[1] - 0x01010101u) & ~out[1])) & 0x80808080u);
+  if (zero || odd) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) {
+      const uint32_t at = 8 * (i & 3);
+      if (ROOT && x[i] > 0.f && inv > 0.f && ((out[i >> 2] >> at) & 0xFFu) == 0) out[i >> 2] |= 1u << at;
+      if ((__float_as_uint(x[i]) & 0x7FFFFFFFu) >= kInfBits) out[i >> 2] |= 0x7Fu << at;
+    }
   }
   return make_uint2(out[0], out[1]);
+}
+
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // One chunk of one tensor: passes of kStep values, a pass's loads issued before
@@ -177,7 +208,6 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
   const int64_t left = n - begin;
   const int passes = (int)(((left < a.chunk ? left : a.chunk) + kStep - 1) / kStep);
   int64_t e = begin + (int64_t)threadIdx.x * kUnit;
-  const float gs = a.h.grad_scale ? *a.h.grad_scale : 1.f;
   using L = Loaded<STATES8, WF32, GF32>;
   auto load = [&](L& l, int64_t at) {
     load_values<WF32>(p.W, at, n, l.w);
@@ -216,14 +246,19 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
       unpack<true>(l.m, m);
       unpack<true>(l.v, v);
     }
+    if (a.h.grad_scale) {
+      const float gs = *a.h.grad_scale;
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) g[j] *= gs;
+    }
     float u[kUnit];
 #pragma unroll
     for (int j = 0; j < kUnit; ++j) {
-      const float x = g[j] * gs;
-      m[j] = __fadd_rn(__fmul_rn(a.h.beta1, m[j]), __fmul_rn(a.h.one_beta1, x));
-      v[j] = __fadd_rn(__fmul_rn(a.h.beta2, v[j]), __fmul_rn(__fmul_rn(a.h.one_beta2, x), x));
+      m[j] = __fadd_rn(__fmul_rn(a.h.beta1, m[j]), __fmul_rn(a.h.one_beta1, g[j]));
+      v[j] = __fadd_rn(__fmul_rn(a.h.beta2, v[j]), __fmul_rn(__fmul_rn(a.h.one_beta2, g[j]), g[j]));
       u[j] = __fsqrt_rn(v[j]);
-      w[j] = w[j] * a.h.decay - __fdividef(a.h.lr_m * m[j], fmaf(u[j], a.h.root_v, a.h.eps));
+      // the divisor is at least eps, a normal number
+      w[j] = fmaf(-a.h.lr_m * m[j], rcp_approx(fmaf(u[j], a.h.root_v, a.h.eps)), w[j] * a.h.decay);
     }
     const uint32_t block = (uint32_t)(e >> 3);
     if constexpr (WF32) {
@@ -233,19 +268,27 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
       for (int j = 0; j < kUnit; ++j) f[j] = w[j];
       store_values<true>(p.W, e, n, o);
     } else {
-      const Philox4 r = philox4x32_10_rk(block, a.step, p.layer, kTagSR, a.rk0, a.rk1);
-      const uint32_t words[4] = {r.w0, r.w1, r.w2, r.w3};
+      const Philox4 rw = philox4x32_10_rk(block, a.step, p.layer, kTagSR, a.rk0, a.rk1);
+      const uint32_t r[4] = {rw.w0, rw.w1, rw.w2, rw.w3};
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[j] = sr_bf16_bits(w[2 * j], words[j] & 0xFFFFu) | (sr_bf16_bits(w[2 * j + 1], words[j] >> 16) << 16);
+        o[j] = __byte_perm(plus_random(__float_as_uint(w[2 * j]), r, 2 * j),
+                           plus_random(__float_as_uint(w[2 * j + 1]), r, 2 * j + 1), 0x7632);
+      if (__float_as_uint(max8_abs(w)) > kInfBits) {  // a NaN among the eight
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          o[j] = sr_bf16_bits(w[2 * j], r[j] & 0xFFFFu) | (sr_bf16_bits(w[2 * j + 1], r[j] >> 16) << 16);
+      }
       const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
       store_values<false>(p.W, e, n, &ov);
     }
     if constexpr (STATES8) {
-      const Philox4 rm = philox4x32_10_rk(block, a.step, p.layer, kTagMoment1, a.rk0, a.rk1);
+      const Philox4 pm = philox4x32_10_rk(block, a.step, p.layer, kTagMoment1, a.rk0, a.rk1);
+      const uint32_t rm[4] = {pm.w0, pm.w1, pm.w2, pm.w3};
       store_codes(p.m, e, n, hold8<false>(m, rm, p.m_scale + (e >> 8)));
-      const Philox4 ru = philox4x32_10_rk(block, a.step, p.layer, kTagMoment2, a.rk0, a.rk1);
+      const Philox4 pu = philox4x32_10_rk(block, a.step, p.layer, kTagMoment2, a.rk0, a.rk1);
+      const uint32_t ru[4] = {pu.w0, pu.w1, pu.w2, pu.w3};
       store_codes(p.v, e, n, hold8<true>(u, ru, p.v_scale + (e >> 8)));
     } else {
       uint4 o[2];
