@@ -19,6 +19,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "internal.h"
 
@@ -51,9 +53,10 @@ struct Loaded {
   float ms, vs;
 };
 
-template <bool F32>
+// FULL: all of the chunk's values lie inside the tensor.
+template <bool F32, bool FULL>
 __device__ __forceinline__ void load_values(const void* base, int64_t e, int64_t n, uint4* out) {
-  if (e + kUnit <= n) {
+  if (FULL || e + kUnit <= n) {
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + e * (F32 ? 4 : 2));
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) out[i] = __ldcs(p + i);
@@ -70,9 +73,9 @@ __device__ __forceinline__ void load_values(const void* base, int64_t e, int64_t
 #pragma unroll
   for (int i = 0; i < (F32 ? 2 : 1); ++i) out[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
 }
-template <bool F32>
+template <bool F32, bool FULL>
 __device__ __forceinline__ void store_values(void* base, int64_t e, int64_t n, const uint4* v) {
-  if (e + kUnit <= n) {
+  if (FULL || e + kUnit <= n) {
     uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + e * (F32 ? 4 : 2));
 #pragma unroll
     for (int i = 0; i < (F32 ? 2 : 1); ++i) __stcs(p + i, v[i]);
@@ -87,16 +90,18 @@ __device__ __forceinline__ void store_values(void* base, int64_t e, int64_t n, c
     }
   }
 }
+template <bool FULL>
 __device__ __forceinline__ uint2 load_codes(const void* base, int64_t e, int64_t n) {
   const uint8_t* c = static_cast<const uint8_t*>(base) + e;
-  if (e + kUnit <= n) return __ldcs(reinterpret_cast<const uint2*>(c));
+  if (FULL || e + kUnit <= n) return __ldcs(reinterpret_cast<const uint2*>(c));
   uint64_t r = 0;
   for (int i = 0; e + i < n; ++i) r |= (uint64_t)c[i] << (8 * i);
   return make_uint2((uint32_t)r, (uint32_t)(r >> 32));
 }
+template <bool FULL>
 __device__ __forceinline__ void store_codes(void* base, int64_t e, int64_t n, uint2 v) {
   uint8_t* c = static_cast<uint8_t*>(base) + e;
-  if (e + kUnit <= n) {
+  if (FULL || e + kUnit <= n) {
     __stcs(reinterpret_cast<uint2*>(c), v);
     return;
   }
@@ -140,60 +145,114 @@ __device__ __forceinline__ float max8_abs(const float (&x)[kUnit]) {
   return max3_abs(top, x[7], x[7]);
 }
 
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Magnitudes below this are dropped from an 8-bit first moment whose whole block
 // is as small (the reciprocal of its scale would overflow).
 constexpr float kLeast = 7.888609052210118e-31f;  // 2^-100
 constexpr uint32_t kInfBits = 0x7F800000u;
 
-// A block's 256 values, eight per lane, to E4M3 codes and a scale.  y = |x| /
-// scale lies in [0, 448]; times 2^-120 its exponent field is E4M3's (bias 7 for
-// 127) and its subnormals are E4M3's, so that the code is bits 20 to 26, with 16
-// random bits added below them and the rest cut off.  ROOT: x is a root of v, not
-// negative, and one that is not zero gets a code of at least 1.
-template <bool ROOT>
-__device__ __forceinline__ uint2 hold8(const float (&x)[kUnit], const uint32_t (&r)[4], float* scale) {
-  uint32_t top = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(max8_abs(x)));
-  const bool odd = top >= kInfBits;  // the same in every lane
-  if (odd) {  // a value of the block is not finite: the scale is that of the others
-    top = 0;
+// A block's largest finite magnitude from each lane's largest magnitude (or NaN)
+// `top`; `odd`: some value of the block is not finite.
+__device__ __forceinline__ float block_top(const float (&x)[kUnit], float top, bool& odd) {
+  uint32_t t = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));
+  odd = t >= kInfBits;  // the same in every lane
+  if (odd) {
+    t = 0;
     for (int i = 0; i < kUnit; ++i) {
       const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-      top = max(top, b < kInfBits ? b : 0u);
+      t = max(t, b < kInfBits ? b : 0u);
     }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    t = __reduce_max_sync(0xFFFFFFFFu, t);
   }
-  const float t = __uint_as_float(top);
-  const float inv = t >= kLeast ? __fmul_rn(__frcp_rn(t), 448.f) : 0.f;
-  if ((threadIdx.x & 31) == 0) *scale = inv > 0.f ? __fmul_rn(t, 1.f / 448.f) : 0.f;
-  uint32_t c[kUnit], out[2];
+  return __uint_as_float(t);
+}
+
+// A block's reciprocal scale (0: the block is held as zeros); lane 0 stores the scale.
+__device__ __forceinline__ float block_scale(float top, float* scale) {
+  const float inv = top >= kLeast ? __fmul_rn(__frcp_rn(top), 448.f) : 0.f;
+  if ((threadIdx.x & 31) == 0) *scale = inv > 0.f ? __fmul_rn(top, 1.f / 448.f) : 0.f;
+  return inv;
+}
+
+// Magnitudes to E4M3 codes in bits 16 to 22 of c.  y = |x| / scale lies in [0,
+// 448]; times 2^-120 its exponent field is E4M3's (bias 7 for 127) and its
+// subnormals are E4M3's, so that the code is bits 20 to 26, with 16 random bits
+// added below them and the rest cut off.
+__device__ __forceinline__ void codes8(const float (&x)[kUnit], float inv, const uint32_t (&r)[4], uint32_t (&c)[kUnit]) {
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) {
     const float y = __fmul_rn(__fmul_rn(fabsf(x[i]), inv), 7.523163845262640e-37f);  // 2^-120
-    c[i] = plus_random(__float_as_uint(y) >> 4, r, i);                               // the code in bits 16 to 22
+    c[i] = plus_random(__float_as_uint(y) >> 4, r, i);
   }
+}
+// Bytes B of four words.
+template <int B>
+__device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, B | (B + 4) << 4), __byte_perm(c, d, B << 8 | (B + 4) << 12), 0x7610);
+}
+__device__ __forceinline__ uint32_t any_zero_byte(uint32_t x) { return (x - 0x01010101u) & ~x & 0x80808080u; }
+
+__device__ __forceinline__ uint2 hold_m(const float (&m)[kUnit], const uint32_t (&r)[4], float* scale) {
+  bool odd;
+  const float inv = block_scale(block_top(m, max8_abs(m), odd), scale);
+  uint32_t c[kUnit], out[2];
+  codes8(m, inv, r, c);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const uint32_t lo = __byte_perm(c[4 * h], c[4 * h + 1], 0x0062), hi = __byte_perm(c[4 * h + 2], c[4 * h + 3], 0x6200);
-    out[h] = __byte_perm(lo, hi, 0x7610);
-    if (!ROOT) {  // the values' signs
-      const uint32_t sl = __byte_perm(__float_as_uint(x[4 * h]), __float_as_uint(x[4 * h + 1]), 0x0073);
-      const uint32_t sh = __byte_perm(__float_as_uint(x[4 * h + 2]), __float_as_uint(x[4 * h + 3]), 0x7300);
-      out[h] |= __byte_perm(sl, sh, 0x7610) & 0x80808080u;
-    }
+    out[h] = gather_bytes<2>(c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]) |
+             (gather_bytes<3>(__float_as_uint(m[4 * h]), __float_as_uint(m[4 * h + 1]), __float_as_uint(m[4 * h + 2]),
+                              __float_as_uint(m[4 * h + 3])) &
+              0x80808080u);
   }
-  // rare values, looked for once per lane: roots that got the code 0, values that are not finite
-  const bool zero = ROOT && ((((out[0] - 0x01010101u) & ~out[0]) | ((out[1] - 0x01010101u) & ~out[1])) & 0x80808080u);
-  if (zero || odd) {
+  if (odd) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i)
+      if ((__float_as_uint(m[i]) & 0x7FFFFFFFu) >= kInfBits) out[i >> 2] |= 0x7Fu << (8 * (i & 3));
+  }
+  return make_uint2(out[0], out[1]);
+}
+
+// The roots u of v, good to 2^-22, as codes.  A code is that of the correctly
+// rounded root all the same: where the approximate one leaves the random bits'
+// sum at an edge (one lane in 4000), the roots are taken again, and the scale
+// comes from the correctly rounded root of the largest v, which is the largest
+// of the roots.
+__device__ __forceinline__ uint2 hold_u(const float (&v)[kUnit], float (&u)[kUnit], const uint32_t (&r)[4], float* scale) {
+  bool odd;
+  const float inv = block_scale(__fsqrt_rn(block_top(v, max8_abs(v), odd)), scale);
+  uint32_t c[kUnit], out[2], edge = 0xFFFFFFFFu;
+  codes8(u, inv, r, c);
+#pragma unroll
+  for (int i = 0; i < kUnit; i += 2)  // two sums' low halves, plus one: 0 or 1 at an edge
+    edge = __viaddmin_u16x2(__byte_perm(c[i], c[i + 1], 0x5410), 0x00010001u, edge);
+  if ((edge & 0xFFFFu) < 2u || (edge >> 16) < 2u) {
+#pragma unroll
+    for (int i = 0; i < kUnit; ++i) u[i] = __fsqrt_rn(v[i]);
+    codes8(u, inv, r, c);
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) out[h] = gather_bytes<2>(c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]);
+  if (odd || any_zero_byte(out[0]) || any_zero_byte(out[1])) {
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) {
       const uint32_t at = 8 * (i & 3);
-      if (ROOT && x[i] > 0.f && inv > 0.f && ((out[i >> 2] >> at) & 0xFFu) == 0) out[i >> 2] |= 1u << at;
-      if ((__float_as_uint(x[i]) & 0x7FFFFFFFu) >= kInfBits) out[i >> 2] |= 0x7Fu << at;
+      if (v[i] > 0.f && inv > 0.f && ((out[i >> 2] >> at) & 0xFFu) == 0) out[i >> 2] |= 1u << at;  // never zero
+      if ((__float_as_uint(v[i]) & 0x7FFFFFFFu) >= kInfBits) out[i >> 2] |= 0x7Fu << at;
     }
   }
   return make_uint2(out[0], out[1]);
 }
 
+__device__ __forceinline__ float sqrt_approx(float x) {
+  float y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -202,26 +261,26 @@ __device__ __forceinline__ float rcp_approx(float x) {
 
 // One chunk of one tensor: passes of kStep values, a pass's loads issued before
 // the values of the pass before are worked on.
-template <bool STATES8, bool WF32, bool GF32>
+template <bool STATES8, bool WF32, bool GF32, bool FULL>
 __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_adamw_problem& p, int64_t begin) {
   const int64_t n = p.n;
-  const int64_t left = n - begin;
-  const int passes = (int)(((left < a.chunk ? left : a.chunk) + kStep - 1) / kStep);
+  const int64_t left = n - begin < a.chunk ? n - begin : a.chunk;
+  const int passes = (int)(((FULL ? a.chunk : left) + kStep - 1) / kStep);
   int64_t e = begin + (int64_t)threadIdx.x * kUnit;
   using L = Loaded<STATES8, WF32, GF32>;
   auto load = [&](L& l, int64_t at) {
-    load_values<WF32>(p.W, at, n, l.w);
-    load_values<GF32>(p.G, at, n, l.g);
+    load_values<WF32, FULL>(p.W, at, n, l.w);
+    load_values<GF32, FULL>(p.G, at, n, l.g);
     if constexpr (STATES8) {
-      const uint2 m = load_codes(p.m, at, n), v = load_codes(p.v, at, n);
+      const uint2 m = load_codes<FULL>(p.m, at, n), v = load_codes<FULL>(p.v, at, n);
       l.m[0] = make_uint4(m.x, m.y, 0, 0);
       l.v[0] = make_uint4(v.x, v.y, 0, 0);
-      const bool block = (at & ~int64_t(255)) < n;
+      const bool block = FULL || (at & ~int64_t(255)) < n;
       l.ms = block ? p.m_scale[at >> 8] : 0.f;
       l.vs = block ? p.v_scale[at >> 8] : 0.f;
     } else {
-      load_values<true>(p.m, at, n, l.m);
-      load_values<true>(p.v, at, n, l.v);
+      load_values<true, FULL>(p.m, at, n, l.m);
+      load_values<true, FULL>(p.v, at, n, l.v);
     }
   };
   L next;
@@ -229,7 +288,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
   for (int i = 0; i < passes; ++i, e += kStep) {
     const L l = next;
     if (i + 1 < passes) load(next, e + kStep);
-    if ((e & ~int64_t(255)) >= n) break;  // the warp's values lie past the end
+    if (!FULL && (e & ~int64_t(255)) >= n) break;  // the warp's values lie past the end
     float w[kUnit], g[kUnit], m[kUnit], v[kUnit];
     unpack<WF32>(l.w, w);
     unpack<GF32>(l.g, g);
@@ -256,7 +315,15 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
     for (int j = 0; j < kUnit; ++j) {
       m[j] = __fadd_rn(__fmul_rn(a.h.beta1, m[j]), __fmul_rn(a.h.one_beta1, g[j]));
       v[j] = __fadd_rn(__fmul_rn(a.h.beta2, v[j]), __fmul_rn(__fmul_rn(a.h.one_beta2, g[j]), g[j]));
-      u[j] = __fsqrt_rn(v[j]);
+      u[j] = sqrt_approx(v[j]);
+    }
+    // the approximate root takes subnormals for zeros
+    if (fminf(min3(min3(v[0], v[1], v[2]), v[3], v[4]), min3(v[5], v[6], v[7])) < FLT_MIN) {
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) u[j] = __fsqrt_rn(v[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
       // the divisor is at least eps, a normal number
       w[j] = fmaf(-a.h.lr_m * m[j], rcp_approx(fmaf(u[j], a.h.root_v, a.h.eps)), w[j] * a.h.decay);
     }
@@ -266,7 +333,7 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
       float* f = reinterpret_cast<float*>(o);
 #pragma unroll
       for (int j = 0; j < kUnit; ++j) f[j] = w[j];
-      store_values<true>(p.W, e, n, o);
+      store_values<true, FULL>(p.W, e, n, o);
     } else {
       const Philox4 rw = philox4x32_10_rk(block, a.step, p.layer, kTagSR, a.rk0, a.rk1);
       const uint32_t r[4] = {rw.w0, rw.w1, rw.w2, rw.w3};
@@ -281,30 +348,36 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
           o[j] = sr_bf16_bits(w[2 * j], r[j] & 0xFFFFu) | (sr_bf16_bits(w[2 * j + 1], r[j] >> 16) << 16);
       }
       const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
-      store_values<false>(p.W, e, n, &ov);
+      store_values<false, FULL>(p.W, e, n, &ov);
     }
     if constexpr (STATES8) {
       const Philox4 pm = philox4x32_10_rk(block, a.step, p.layer, kTagMoment1, a.rk0, a.rk1);
       const uint32_t rm[4] = {pm.w0, pm.w1, pm.w2, pm.w3};
-      store_codes(p.m, e, n, hold8<false>(m, rm, p.m_scale + (e >> 8)));
+      store_codes<FULL>(p.m, e, n, hold_m(m, rm, p.m_scale + (e >> 8)));
       const Philox4 pu = philox4x32_10_rk(block, a.step, p.layer, kTagMoment2, a.rk0, a.rk1);
       const uint32_t ru[4] = {pu.w0, pu.w1, pu.w2, pu.w3};
-      store_codes(p.v, e, n, hold8<true>(u, ru, p.v_scale + (e >> 8)));
+      store_codes<FULL>(p.v, e, n, hold_u(v, u, ru, p.v_scale + (e >> 8)));
     } else {
       uint4 o[2];
       float* f = reinterpret_cast<float*>(o);
 #pragma unroll
       for (int j = 0; j < kUnit; ++j) f[j] = m[j];
-      store_values<true>(p.m, e, n, o);
+      store_values<true, FULL>(p.m, e, n, o);
 #pragma unroll
       for (int j = 0; j < kUnit; ++j) f[j] = v[j];
-      store_values<true>(p.v, e, n, o);
+      store_values<true, FULL>(p.v, e, n, o);
     }
   }
 }
 
+template <bool STATES8, bool WF32, bool GF32>
+__device__ __forceinline__ void adamw_block(const AdamBatch& a, const sketch_adamw_problem& p, int64_t begin) {
+  if (begin + a.chunk <= p.n) adamw_chunk<STATES8, WF32, GF32, true>(a, p, begin);
+  else adamw_chunk<STATES8, WF32, GF32, false>(a, p, begin);
+}
+
 template <bool STATES8>
-__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamBatch a) {
+__global__ void __launch_bounds__(kAdamThreads, STATES8 ? 4 : 2) adamw_kernel(const __grid_constant__ AdamBatch a) {
   const int block = blockIdx.x;
   int lo = 0, hi = a.n;  // the last tensor that begins at or before this block
   while (hi - lo > 1) {
@@ -315,11 +388,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   const sketch_adamw_problem& p = a.p[lo];
   const int64_t begin = (int64_t)(block - a.begin[lo]) * a.chunk;
   if (p.w_type == SKETCH_BF16) {
-    if (p.g_type == SKETCH_BF16) adamw_chunk<STATES8, false, false>(a, p, begin);
-    else adamw_chunk<STATES8, false, true>(a, p, begin);
+    if (p.g_type == SKETCH_BF16) adamw_block<STATES8, false, false>(a, p, begin);
+    else adamw_block<STATES8, false, true>(a, p, begin);
   } else {
-    if (p.g_type == SKETCH_BF16) adamw_chunk<STATES8, true, false>(a, p, begin);
-    else adamw_chunk<STATES8, true, true>(a, p, begin);
+    if (p.g_type == SKETCH_BF16) adamw_block<STATES8, true, false>(a, p, begin);
+    else adamw_block<STATES8, true, true>(a, p, begin);
   }
 }
 
