@@ -204,6 +204,8 @@ def _workspace(nbytes, device, stream, given=None):
         if not given.is_cuda or given.numel() * given.element_size() < nbytes:
             raise ValueError("workspace needs %d bytes" % nbytes)
         return given
+    if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 

@@ -6,18 +6,35 @@
 //   dgamma (+)= sum over tokens of dy xh,  dbeta (+)= sum over tokens of dy
 //
 // Activations are BF16 or fp32, weights BF16 or fp32; statistics, sums and the
-// weights' gradients are fp32.  Both passes are bound by HBM: each row is read
-// once and stays in registers while its statistics are formed.
+// weights' gradients are fp32.
 //
-// A row belongs to `tpr` threads (a power of two, 8 to 1024), each with NV
-// vectors of VE elements (16 bytes; VE = 1 where rows do not start on 16 bytes
-// or end inside a vector).  The backward pass keeps a thread's columns fixed over
-// the rows that its block walks, so that dgamma and dbeta add up in registers;
-// each block leaves one partial row, and norm_grad_sum_kernel adds those.  Rows
-// wider than 16384 take the kernels at the end, which read a row again for each
-// pass.
+// Both passes are bound by HBM, once the instructions for each element are few:
+// arithmetic goes two values at a time (packed fp32 pairs).
 //
-// Every sum has a fixed order, so results repeat bit for bit.
+// Forward: a row belongs to `tpr` threads (a power of two, 8 to 256), each with
+// up to 128 bytes of it in registers, so that a row is read once; gamma and beta
+// lie in shared memory as fp32, laid out so that a warp's reads of them have no
+// bank conflicts.  Blocks walk over the rows.
+//
+// Backward: a thread's columns stay the same over the rows that its block walks,
+// so that dgamma and dbeta add up in registers; with those and gamma there, rows
+// come through shared memory: a warp of its own brings them by bulk copies into a
+// ring of slots, several sets of rows ahead (HBM wants some 60 KB per SM under
+// way), and the others read them there, once for each of the two passes over a
+// row.  B rows are worked on side by side, so that their sums' shuffles, and the
+// one barrier that joins the warps' sums, overlap.
+//
+// Elements come in vectors of 16 bytes (VE of them).  VE = 1 serves rows that do
+// not start on 16 bytes or end inside a vector.  Forward they are read one by one;
+// backward their copies start and end at the 16-byte boundaries around them (the
+// bytes beyond belong to the neighbouring rows; a row at an end of the matrix,
+// which has none, is brought in exactly), and elements are picked one by one in
+// shared memory.
+//
+// Backward: each block leaves one partial row of dgamma and dbeta, and
+// norm_grad_sum_kernel adds those.  Rows wider than 16384 take the kernels at the
+// end, which read a row again for each pass.  Every sum has a fixed order, so
+// results repeat bit for bit.
 #include <cuda_bf16.h>
 
 #include "common.cuh"
@@ -29,336 +46,614 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPartials = 320;  // partial rows of the weights' gradients
+constexpr int kMaxSlots = 8;
 
-// VE elements of a row, as loaded.
-template <typename X, int VE>
-struct Vec {
-  uint4 r;
-};
+// ---- pairs of fp32 values in one register pair --------------------------------------
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+  return p;
+}
+__device__ __forceinline__ float2 split(Pair p) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+  return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum2(Pair p) {
+  const float2 f = split(p);
+  return f.x + f.y;
+}
+// Two BF16 values of a word.
+__device__ __forceinline__ Pair pair_bf16(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+// The pairs of a 16-byte vector of X.
 template <typename X>
-struct Vec<X, 1> {
-  X r;
-};
-template <typename X, int VE>
-__device__ __forceinline__ Vec<X, VE> load_vec(const X* row, int idx) {
-  Vec<X, VE> v;
-  if constexpr (VE == 1) v.r = row[idx];
-  else v.r = __ldcs(reinterpret_cast<const uint4*>(row) + idx);
+__device__ __forceinline__ void vec_pairs(const uint4& v, Pair (&p)[8 / sizeof(X)]) {
+  const uint32_t r[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < (int)(8 / sizeof(X)); ++i)
+    p[i] = sizeof(X) == 2 ? pair_bf16(r[i]) : pair(__uint_as_float(r[(2 * i) & 3]), __uint_as_float(r[(2 * i + 1) & 3]));
+}
+template <typename X>
+__device__ __forceinline__ void store_vec(X* row, int idx, const Pair (&p)[8 / sizeof(X)]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < (int)(8 / sizeof(X)); ++i) {
+    const float2 f = split(p[i]);
+    if constexpr (sizeof(X) == 2) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+      r[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      r[(2 * i) & 3] = __float_as_uint(f.x);
+      r[(2 * i + 1) & 3] = __float_as_uint(f.y);
+    }
+  }
+  reinterpret_cast<uint4*>(row)[idx] = make_uint4(r[0], r[1], r[2], r[3]);
+}
+__device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// One element in shared memory.
+template <typename X>
+__device__ __forceinline__ float read_one(uint32_t at) {
+  if constexpr (sizeof(X) == 4) return tc::lds_f32(at);
+  uint16_t h;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(h) : "r"(at));
+  return bf16_bits_to_float(h);
+}
+__device__ __forceinline__ float weight(const void* w, int type, int64_t i, float none) {
+  if (w == nullptr) return none;
+  return type == SKETCH_FP32 ? static_cast<const float*>(w)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(w)[i]);
+}
+// Sum over the tpr lanes (of up to a warp) that share a row.
+__device__ __forceinline__ float lane_sum(float v, int tpr) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   return v;
 }
-__device__ __forceinline__ float to_float(float v) { return v; }
-__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <typename X, int VE>
-__device__ __forceinline__ void unpack(const Vec<X, VE>& v, float (&f)[VE]) {
-  if constexpr (VE == 1) {
-    f[0] = to_float(v.r);
-  } else {
-    const uint32_t r[4] = {v.r.x, v.r.y, v.r.z, v.r.w};
-#pragma unroll
-    for (int i = 0; i < VE; ++i)
-      f[i] = VE == 4 ? __uint_as_float(r[i & 3]) : __uint_as_float((i & 1) ? r[i >> 1] & 0xFFFF0000u : r[i >> 1] << 16);
-  }
+
+// ---- the ring of row sets -----------------------------------------------------------
+// One of the matrices that a set's rows come from.
+struct RowSource {
+  const char* base;
+  int64_t ld;         // bytes between rows
+  int64_t T;
+  uint32_t width;     // bytes of a row
+  __device__ const char* end() const { return base + (T - 1) * ld + width; }
+};
+
+struct Ring {
+  uint32_t smem;      // shared address of the first slot
+  uint32_t slot;      // bytes per slot
+  uint32_t pitch;     // bytes per row
+  int slots;
+  int rows;           // rows per set
+  int each;           // of them, rows per group of tpr threads
+};
+
+// Where row `row` starts inside its place in the slot: its own 16-byte phase.
+__device__ __forceinline__ uint32_t phase(const RowSource& m, int64_t row) {
+  return (uint32_t)(reinterpret_cast<uintptr_t>(m.base) + (uint64_t)(row * m.ld)) & 15u;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-template <typename X, int VE>
-__device__ __forceinline__ void store_vec(X* row, int idx, const float (&f)[VE]) {
-  if constexpr (VE == 1) {
-    if constexpr (sizeof(X) == 4) row[idx] = f[0];
-    else row[idx] = __float2bfloat16_rn(f[0]);
-  } else if constexpr (VE == 4) {
-    reinterpret_cast<float4*>(row)[idx] = make_float4(f[0], f[1], f[2], f[3]);
-  } else {
-    reinterpret_cast<uint4*>(row)[idx] = make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
-  }
-}
-// VE weights at vector idx; `none` where there are no weights.
-template <int VE>
-__device__ __forceinline__ void load_weights(const void* w, int type, int idx, float none, float (&f)[VE]) {
-  if (w == nullptr) {
+
+// A warp: start the copies of one set of rows into slot `s`, N matrices one after
+// another, completing on `bar`.
+template <int VE, int N>
+__device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N], int s, int64_t first, uint64_t* bar) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t dst0 = r.smem + (uint32_t)s * r.slot;
+  const int rows = (int)(m[0].T - first < r.rows ? m[0].T - first : r.rows);
+  if constexpr (VE > 1) {
+    if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(N * rows) * m[0].width);
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < VE; ++i) f[i] = none;
-  } else if (type == SKETCH_FP32) {
-    if constexpr (VE == 1) {
-      f[0] = __ldg(static_cast<const float*>(w) + idx);
-    } else {
-      const float4* p = reinterpret_cast<const float4*>(w) + (int64_t)idx * (VE / 4);
-#pragma unroll
-      for (int i = 0; i < VE / 4; ++i) {
-        const float4 v = __ldg(p + i);
-        f[4 * i] = v.x;
-        f[4 * i + 1] = v.y;
-        f[4 * i + 2] = v.z;
-        f[4 * i + 3] = v.w;
+    for (int i = 0; i < N; ++i) {
+      const char* src = m[i].base + first * m[i].ld;
+      const uint32_t dst = dst0 + (uint32_t)(i * r.rows) * r.pitch;
+      if (m[i].ld == m[i].width) {  // rows back to back: one copy
+        if (lane == 0) tc::bulk_load_1d(dst, src, (uint32_t)rows * m[i].width, bar);
+      } else {
+        for (int q = lane; q < rows; q += 32)
+          tc::bulk_load_1d(dst + (uint32_t)q * r.pitch, src + q * m[i].ld, m[i].width, bar);
       }
     }
   } else {
-    if constexpr (VE == 1) {
-      f[0] = bf16_bits_to_float(__ldg(static_cast<const uint16_t*>(w) + idx));
-    } else {
-      const uint2* p = reinterpret_cast<const uint2*>(w) + (int64_t)idx * (VE / 4);
+    // twice over the rows: their bytes (and the single elements), then the copies
+    uint32_t sum = 0;
 #pragma unroll
-      for (int i = 0; i < VE / 4; ++i) {
-        const uint2 v = __ldg(p + i);
-        f[4 * i] = __uint_as_float(v.x << 16);
-        f[4 * i + 1] = __uint_as_float(v.x & 0xFFFF0000u);
-        f[4 * i + 2] = __uint_as_float(v.y << 16);
-        f[4 * i + 3] = __uint_as_float(v.y & 0xFFFF0000u);
+    for (int turn = 0; turn < 2; ++turn) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        for (int q = lane; q < rows; q += 32) {
+          const uint32_t ph = phase(m[i], first + q);
+          const char* src = m[i].base + (first + q) * m[i].ld - ph;
+          uint32_t at = dst0 + (uint32_t)(i * r.rows + q) * r.pitch;
+          uint32_t bytes = (ph + m[i].width + 15u) & ~15u;
+          if (src < m[i].base || src + bytes > m[i].end()) {  // whole 16 bytes inside the row, the rest singly
+            const uint32_t lo = (ph + 15u) & ~15u, hi = (ph + m[i].width) & ~15u;
+            if (turn == 0) {
+              for (uint32_t b = ph; b < ph + m[i].width; b += 2)
+                if (b < lo || b >= hi) tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
+            }
+            src += lo;
+            at += lo;
+            bytes = hi > lo ? hi - lo : 0u;
+          }
+          if (turn == 0) sum += bytes;
+          else if (bytes) tc::bulk_load_1d(at, src, bytes, bar);
+        }
+      }
+      if (turn == 0) {
+        sum = __reduce_add_sync(0xFFFFFFFFu, sum);
+        __syncwarp();  // the single elements are written before the slot's barrier can complete
+        if (lane == 0) tc::mbar_arrive_expect_tx(bar, sum);
+        __syncwarp();
       }
     }
   }
 }
 
-// Sums over the tpr threads of a row, the same in each.  `slots` (one per warp)
-// alternate between calls, so that one barrier per call is enough: a thread
-// that writes a slot again has passed the barrier of the call between, after
-// which nobody reads the old value.
-template <int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], int tpr, float (*slots)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      if (o < tpr) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+// The producer warp: every set of rows of this block into the ring, a slot again
+// when the `readers` have arrived on its barrier.
+template <int VE, int N>
+__device__ __forceinline__ void produce(const Ring& r, const RowSource (&m)[N], int64_t first, int64_t stride, int passes,
+                                        uint64_t* full, uint64_t* empty, volatile int* abort_flag, int* err) {
+  int s = 0, filled = 0;
+  uint32_t ph = 1;
+  for (; filled < passes; ++filled) {
+    const bool ok = filled < r.slots || tc::mbar_wait(&empty[s], ph, abort_flag, err, tc::kErrTimeoutStage);
+    if (!__all_sync(0xFFFFFFFFu, ok)) break;
+    fill_slot<VE, N>(r, m, s, first + filled * stride, &full[s]);
+    if (++s == r.slots) {
+      s = 0;
+      ph ^= 1u;
+    }
   }
-  if (tpr > 32) {
-    const int warp = threadIdx.x >> 5, first = (threadIdx.x & ~(tpr - 1)) >> 5;
-    if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) slots[warp][i] = v[i];
-    }
-    if (tpr == (int)blockDim.x) __syncthreads();
-    else tc::named_barrier(1 + first / (tpr >> 5), tpr);
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = 0.f;
-    for (int w = 0; w < tpr >> 5; ++w) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] += slots[first + w][i];
-    }
+  __syncwarp();
+  // if a copy never landed: wait, with a limit, for those still under way
+  if (*abort_flag && (threadIdx.x & 31) == 0) {
+    volatile int none = 0;
+    for (int i = filled > r.slots ? filled - r.slots : 0; i < filled; ++i)
+      tc::mbar_wait(&full[i % r.slots], (i / r.slots) & 1, &none, nullptr, 0, 100000000ull);
   }
 }
 
 // ---- forward ---------------------------------------------------------------------
-template <typename X, int VE, int NV, int THREADS>
-__global__ void __launch_bounds__(THREADS) norm_forward_kernel(const NormForward a, int tpr) {
-  __shared__ float slots[2][THREADS / 32][1];
-  const int t = threadIdx.x & (tpr - 1);
-  const int64_t row = (int64_t)blockIdx.x * (THREADS / tpr) + threadIdx.x / tpr;
-  const bool in = row < a.T;
-  const int nvec = (int)(a.k / VE);
-  const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
-  Vec<X, VE> raw[NV];
-  float s[1] = {0.f};
+// 16-byte vectors of a row per thread, and blocks per SM.
+constexpr int forward_vecs(int threads) { return threads == 256 ? 8 : 4; }
+constexpr int forward_blocks(int threads) { return threads == 256 ? 3 : 1; }
+
+// Where column c of a weight lies in shared memory: for eight-element vectors
+// the first and the second four columns of each go to halves of their own, so that
+// a thread's two 16-byte reads are 16 bytes from its neighbour's.
+template <int VE>
+__device__ __forceinline__ int weight_at(int c, int k) {
+  return VE == 8 ? (c >> 3) * 4 + (c & 3) + ((c & 4) ? k / 2 : 0) : c;
+}
+// The pairs of the weights of vector idx.
+template <int VE>
+__device__ __forceinline__ void weight_pairs(uint32_t base, int idx, int k, Pair (&p)[VE / 2]) {
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (in && j * tpr + t < nvec) raw[j] = load_vec<X, VE>(x, j * tpr + t);
-  const float inv_k = 1.f / (float)a.k;
+  for (int h = 0; h < VE / 4; ++h) {
+    const uint4 v = tc::lds128(base + 16u * idx + (h ? 2u * k : 0u));
+    p[2 * h] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    p[2 * h + 1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+  }
+}
+
+// Statistics of the row whose elements this thread's share sums to `sum` and,
+// around a mean, to dev(mean): first the warp's mean and squared deviations from
+// it, then the row's from its warps', n (mean_w - mean)^2 more each (no difference
+// of squares, so that a row far from zero loses nothing).  `part` alternates
+// between rows: a thread that writes it again has passed the barrier of the row
+// between, after which nobody reads the old values.
+template <typename Dev>
+__device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float inv_n, float inv_k, const float* counts,
+                                            float2* part, float& mu, float& m2) {
+  mu = lane_sum(sum, tpr) * inv_n;
+  m2 = lane_sum(dev(mu), tpr);
+  const int warps = tpr >> 5;
+  if (warps > 1) {
+    const int lane = threadIdx.x & 31, warp0 = (threadIdx.x & ~(tpr - 1)) >> 5;
+    if (lane == 0) part[threadIdx.x >> 5] = make_float2(mu, m2);
+    if (tpr == (int)blockDim.x) __syncthreads();
+    else tc::named_barrier(1 + warp0 / warps, tpr);
+    const int w = warp0 + (lane & (warps - 1));  // every `warps` lanes join the row's warps
+    const float2 v = part[w];
+    mu = lane_sum(counts[w] * v.x, warps) * inv_k;
+    m2 = lane_sum(fmaf(counts[w] * (v.x - mu), v.x - mu, v.y), warps);
+  }
+}
+
+// FULL: every thread has forward_vecs vectors.
+template <typename X, int THREADS, bool FULL>
+__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_kernel(const NormForward a, int tpr) {
+  constexpr int VE = 16 / sizeof(X), NV = forward_vecs(THREADS);
+  extern __shared__ __align__(128) float weights[];
+  __shared__ float2 part[2][THREADS / 32];
+  __shared__ float counts[THREADS / 32];
+  const int t = threadIdx.x & (tpr - 1), groups = THREADS / tpr, k = (int)a.k;
+  const int nvec = k / VE;
+  for (int c = threadIdx.x; c < k; c += THREADS) {
+    weights[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
+    weights[k + weight_at<VE>(c, k)] = weight(a.beta, a.w_type, c, 0.f);
+  }
+  const uint32_t gamma = tc::smem_u32(weights), beta = gamma + 4u * k;
+  // elements of the row that this warp holds (the whole row's, where it is one of several in the warp)
+  int mine = 0;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (in && j * tpr + t < nvec) {
-      float f[VE];
-      unpack<X, VE>(raw[j], f);
+  for (int j = 0; j < NV; ++j) mine += j * tpr + t < nvec ? VE : 0;
 #pragma unroll
-      for (int i = 0; i < VE; ++i) s[0] += f[i];
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  const float inv_n = mine > 0 ? 1.f / (float)mine : 0.f, inv_k = 1.f / (float)k;
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = (float)mine;
+  __syncthreads();
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  int p = 0;
+  for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += stride, p ^= 1) {
+    const int64_t row = base + threadIdx.x / tpr;
+    const bool in = row < a.T;
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const X*>(a.X) + row * a.ld_x);
+    uint4 raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (in && (FULL || j * tpr + t < nvec)) raw[j] = __ldcs(x + j * tpr + t);
+    }
+    Pair s = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Pair v[VE / 2];
+      vec_pairs<X>(raw[j], v);
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) s = add2(s, v[i]);
+    }
+    float mu, m2;
+    row_moments(
+        sum2(s),
+        [&](float m) {
+          const Pair neg = pair(-m, -m);
+          Pair q = 0;
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if (FULL || j * tpr + t < nvec) {
+              Pair v[VE / 2];
+              vec_pairs<X>(raw[j], v);
+#pragma unroll
+              for (int i = 0; i < VE / 2; ++i) {
+                v[i] = add2(v[i], neg);
+                q = fma2(v[i], v[i], q);
+              }
+            }
+          }
+          return sum2(q);
+        },
+        tpr, inv_n, inv_k, counts, part[p], mu, m2);
+    const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
+    if (!in) continue;
+    const Pair r2 = pair(rstd, rstd), c2 = pair(-mu * rstd, -mu * rstd);
+    X* y = static_cast<X*>(a.Y) + row * a.ld_y;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (FULL || j * tpr + t < nvec) {
+        Pair v[VE / 2], g[VE / 2], b[VE / 2];
+        vec_pairs<X>(raw[j], v);
+        weight_pairs<VE>(gamma, j * tpr + t, k, g);
+        weight_pairs<VE>(beta, j * tpr + t, k, b);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) v[i] = fma2(fma2(v[i], r2, c2), g[i], b[i]);
+        store_vec<X>(y, j * tpr + t, v);
+      }
+    }
+    if (t == 0) {
+      a.mean[row] = mu;
+      a.rstd[row] = rstd;
     }
   }
-  row_sums<1>(s, tpr, slots[0]);
-  const float mu = s[0] * inv_k;
-  s[0] = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (in && j * tpr + t < nvec) {
-      float f[VE];
-      unpack<X, VE>(raw[j], f);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) s[0] = fmaf(f[i] - mu, f[i] - mu, s[0]);
-    }
+}
+
+// Rows whose elements are read one by one: NV of them per thread.
+template <typename X, int NV, int THREADS>
+__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_single_kernel(const NormForward a, int tpr) {
+  extern __shared__ __align__(128) float weights[];
+  __shared__ float2 part[2][THREADS / 32];
+  __shared__ float counts[THREADS / 32];
+  const int t = threadIdx.x & (tpr - 1), groups = THREADS / tpr, k = (int)a.k;
+  for (int c = threadIdx.x; c < k; c += THREADS) {
+    weights[c] = weight(a.gamma, a.w_type, c, 1.f);
+    weights[k + c] = weight(a.beta, a.w_type, c, 0.f);
   }
-  row_sums<1>(s, tpr, slots[1]);
-  const float rstd = 1.f / sqrtf(s[0] * inv_k + a.eps);
-  if (!in) return;
-  X* y = static_cast<X*>(a.Y) + row * a.ld_y;
+  int mine = (k - t + tpr - 1) / tpr;  // this thread's elements: columns t, t + tpr, ...
+  if (mine < 0) mine = 0;
+  int warp_n = mine;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    if (j * tpr + t < nvec) {
-      float f[VE], g[VE], b[VE];
-      load_weights<VE>(a.gamma, a.w_type, j * tpr + t, 1.f, g);
-      load_weights<VE>(a.beta, a.w_type, j * tpr + t, 0.f, b);
-      unpack<X, VE>(raw[j], f);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < tpr) warp_n += __shfl_xor_sync(0xFFFFFFFFu, warp_n, o);
+  const float inv_n = warp_n > 0 ? 1.f / (float)warp_n : 0.f, inv_k = 1.f / (float)k;
+  if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = (float)warp_n;
+  __syncthreads();
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  int p = 0;
+  for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += stride, p ^= 1) {
+    const int64_t row = base + threadIdx.x / tpr;
+    const bool in = row < a.T;
+    const X* x = static_cast<const X*>(a.X) + row * a.ld_x + t;
+    float f[NV];
 #pragma unroll
-      for (int i = 0; i < VE; ++i) f[i] = fmaf((f[i] - mu) * rstd, g[i], b[i]);
-      store_vec<X, VE>(y, j * tpr + t, f);
+    for (int j = 0; j < NV; ++j) f[j] = (in && j < mine) ? (float)__ldcs(x + j * tpr) : 0.f;
+    float sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) sum += f[j];
+    float mu, m2;
+    row_moments(
+        sum,
+        [&](float m) {
+          float q = 0.f;
+#pragma unroll
+          for (int j = 0; j < NV; ++j)
+            if (j < mine) q = fmaf(f[j] - m, f[j] - m, q);
+          return q;
+        },
+        tpr, inv_n, inv_k, counts, part[p], mu, m2);
+    const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
+    if (!in) continue;
+    X* y = static_cast<X*>(a.Y) + row * a.ld_y + t;
+    const float c = -mu * rstd;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+      if (j < mine) store_one(y + j * tpr, fmaf(fmaf(f[j], rstd, c), weights[j * tpr + t], weights[k + j * tpr + t]));
+    if (t == 0) {
+      a.mean[row] = mu;
+      a.rstd[row] = rstd;
     }
-  }
-  if (t == 0) {
-    a.mean[row] = mu;
-    a.rstd[row] = rstd;
   }
 }
 
 // ---- backward --------------------------------------------------------------------
-// THREADS per block, one or more rows at a time.  SHARED: rows of more than
-// 8192 leave 64 registers a thread, too few for a thread's 16 columns of dgamma
-// and dbeta beside its row, so those lie in shared memory.  PREFETCH: the next
-// row's loads are issued before this row's sums (BF16 vectors; fp32 rows are
-// twice the bytes and have enough in flight without, single elements would take
-// a register each).
-template <typename X, int VE, int NV, int THREADS, bool SHARED>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) norm_backward_kernel(const NormBackward a, int tpr) {
-  constexpr int E = NV * VE;
-  constexpr bool PREFETCH = VE == 8;
-  extern __shared__ float4 acc_raw[];
-  float* acc = reinterpret_cast<float*>(acc_raw);
-  __shared__ float slots[2][THREADS / 32][2];
-  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr;
-  const int nvec = (int)(a.k / VE), k = (int)a.k;
-  const int64_t stride = (int64_t)gridDim.x * groups;
-  const int64_t row0 = (int64_t)blockIdx.x * groups + group;
-  const int passes = (int)((a.T - (int64_t)blockIdx.x * groups + stride - 1) / stride);  // the same for the whole block
-  float dg[SHARED ? 1 : E], db[SHARED ? 1 : E], gamma[SHARED ? 1 : E];
-  if constexpr (SHARED) {
-    for (int i = threadIdx.x; i < 2 * k; i += THREADS) acc[i] = 0.f;  // each thread's own columns follow after a barrier
-    __syncthreads();
-  } else {
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      float g[VE];
-#pragma unroll
-      for (int i = 0; i < VE; ++i) g[i] = 0.f;
-      if (j * tpr + t < nvec) load_weights<VE>(a.gamma, a.w_type, j * tpr + t, 1.f, g);
-#pragma unroll
-      for (int i = 0; i < VE; ++i) {
-        gamma[j * VE + i] = g[i];
-        dg[j * VE + i] = db[j * VE + i] = 0.f;
-      }
+constexpr int blocks_per_sm(int threads) { return threads == 256 ? 2 : 1; }
+constexpr int backward_rows_each(size_t size, int threads) { return threads == 256 && size == 2 ? 2 : 1; }
+
+// A thread's columns: NV vectors of VE elements, as E / 2 pairs.  With VE = 1 a pair
+// is the thread's elements 2 q and 2 q + 1, tpr columns apart.
+template <typename X, int VE, int NV, int THREADS, bool FULL>
+__global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
+    norm_backward_kernel(const NormBackward a, const Ring ring, int tpr, int* err) {
+  constexpr int E = NV * VE, B = backward_rows_each(sizeof(X), THREADS);
+  constexpr int VP = VE == 1 ? 1 : VE / 2, NP = E / 2 / VP;  // pairs per step, steps
+  constexpr bool HOLD = E <= 16;  // gamma stays in registers
+  extern __shared__ __align__(128) uint8_t ring_mem[];
+  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots];
+  __shared__ float2 part[2][B][THREADS / 32];
+  __shared__ volatile int abort_flag;
+  Ring r = ring;
+  r.smem = tc::smem_u32(ring_mem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const RowSource m[2] = {
+      {static_cast<const char*>(a.X), a.ld_x * (int64_t)sizeof(X), a.T, (uint32_t)(a.k * sizeof(X))},
+      {static_cast<const char*>(a.dY), a.ld_dy * (int64_t)sizeof(X), a.T, (uint32_t)(a.k * sizeof(X))}};
+  const int64_t stride = (int64_t)gridDim.x * r.rows;
+  const int64_t first = (int64_t)blockIdx.x * r.rows;
+  const int passes = (int)((a.T - first + stride - 1) / stride);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < r.slots; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], THREADS / 32);
     }
+    tc::fence_mbar_init();
   }
-  const float inv_k = 1.f / (float)a.k;
-  Vec<X, VE> nx[NV], ny[NV];
-  float nmu = 0.f, nrs = 0.f;
-  auto load = [&](int64_t row) {
-    if (row >= a.T) return;
-    const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
-    const X* y = static_cast<const X*>(a.dY) + row * a.ld_dy;
-    nmu = a.mean[row];
-    nrs = a.rstd[row];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (j * tpr + t < nvec) {
-        nx[j] = load_vec<X, VE>(x, j * tpr + t);
-        ny[j] = load_vec<X, VE>(y, j * tpr + t);
-      }
+  __syncthreads();
+  const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr, k = (int)a.k;
+  const int warps = tpr >> 5, warp0 = (threadIdx.x & ~(tpr - 1)) >> 5;
+  const int nvec = k / VE;
+  // column of element i of pair q of step j; whether the thread has it
+  auto column = [&](int j, int q, int i) { return VE == 1 ? (2 * j + i) * tpr + t : (j * tpr + t) * VE + 2 * q + i; };
+  auto has = [&](int j) { return FULL || (VE == 1 ? 2 * j * tpr + t < k : j * tpr + t < nvec); };
+  // VE = 1: the pair's second element may lie past the row; a zero stands for it
+  auto read = [&](uint32_t at, int j, Pair (&v)[VP]) {
+    if constexpr (VE == 1) {
+      const int c = 2 * j * tpr + t;
+      v[0] = pair(read_one<X>(at + (uint32_t)(c * sizeof(X))),
+                  c + tpr < k ? read_one<X>(at + (uint32_t)((c + tpr) * sizeof(X))) : 0.f);
+    } else {
+      vec_pairs<X>(tc::lds128(at + 16u * (uint32_t)(j * tpr + t)), v);
     }
   };
-  if (PREFETCH) load(row0);
-  for (int p = 0; p < passes; ++p) {
-    const int64_t row = row0 + p * stride;
-    if (!PREFETCH) load(row);
-    Vec<X, VE> rx[NV], ry[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      rx[j] = nx[j];
-      ry[j] = ny[j];
+  Pair dg[E / 2], db[E / 2], gamma[HOLD ? E / 2 : 1];
+  // wide rows: gamma behind the ring, as the forward pass lays it out
+  const uint32_t gbase = r.smem + (uint32_t)r.slots * r.slot;
+  if (warp == THREADS / 32) {
+    produce<VE, 2>(r, m, first, stride, passes, full, empty, &abort_flag, err);
+  } else {
+    auto gamma_pairs = [&](int j, Pair (&g)[VP]) {
+      if constexpr (VE == 1) {
+        const int c = 2 * j * tpr + t;
+        g[0] = pair(tc::lds_f32(gbase + 4u * c), c + tpr < k ? tc::lds_f32(gbase + 4u * (c + tpr)) : 0.f);
+      } else {
+        weight_pairs<VE>(gbase, j * tpr + t, k, g);
+      }
+    };
+    if constexpr (!HOLD) {
+      float* g = reinterpret_cast<float*>(ring_mem + (size_t)r.slots * r.slot);
+      for (int c = threadIdx.x; c < k; c += THREADS) g[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
+      tc::named_barrier(1, THREADS);
     }
-    const float mu = nmu, rs = nrs;
-    if (PREFETCH && p + 1 < passes) load(row + stride);
-    const bool in = row < a.T;
-    float s[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (in && j * tpr + t < nvec) {
-        float x[VE], y[VE], g[VE];
-        unpack<X, VE>(rx[j], x);
-        unpack<X, VE>(ry[j], y);
-        if constexpr (SHARED) load_weights<VE>(a.gamma, a.w_type, j * tpr + t, 1.f, g);
+    for (int j = 0; j < NP; ++j) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float xh = (x[i] - mu) * rs;
-          const float d = y[i] * (SHARED ? g[i] : gamma[SHARED ? 0 : j * VE + i]);
-          s[0] += d;
-          s[1] = fmaf(d, xh, s[1]);
-          if constexpr (!SHARED) {
-            dg[j * VE + i] = fmaf(y[i], xh, dg[j * VE + i]);
-            db[j * VE + i] += y[i];
-          }
-        }
-        if constexpr (SHARED) {
-          float* pg = acc + (j * tpr + t) * VE;
+      for (int q = 0; q < VP; ++q) {
+        const int c0 = column(j, q, 0), c1 = column(j, q, 1);
+        if constexpr (HOLD)
+          gamma[j * VP + q] = pair(FULL || c0 < k ? weight(a.gamma, a.w_type, c0, 1.f) : 0.f,
+                                   FULL || c1 < k ? weight(a.gamma, a.w_type, c1, 1.f) : 0.f);
+        dg[j * VP + q] = db[j * VP + q] = 0;
+      }
+    }
+    const float inv_k = 1.f / (float)k;
+    float nmu[B], nrs[B];  // the next set's
+    auto load_stats = [&](int64_t row) {
 #pragma unroll
-          for (int i = 0; i < VE; i += (VE == 1 ? 1 : 4)) {
-            if constexpr (VE == 1) {
-              pg[0] = fmaf(y[0], (x[0] - mu) * rs, pg[0]);
-              pg[k] += y[0];
-            } else {
-              float4 u = *reinterpret_cast<float4*>(pg + i), v = *reinterpret_cast<float4*>(pg + k + i);
-              u.x = fmaf(y[i], (x[i] - mu) * rs, u.x);
-              u.y = fmaf(y[i + 1], (x[i + 1] - mu) * rs, u.y);
-              u.z = fmaf(y[i + 2], (x[i + 2] - mu) * rs, u.z);
-              u.w = fmaf(y[i + 3], (x[i + 3] - mu) * rs, u.w);
-              v.x += y[i];
-              v.y += y[i + 1];
-              v.z += y[i + 2];
-              v.w += y[i + 3];
-              *reinterpret_cast<float4*>(pg + i) = u;
-              *reinterpret_cast<float4*>(pg + k + i) = v;
+      for (int b = 0; b < B; ++b) {
+        const bool in = b < r.each && row + b < a.T;
+        nmu[b] = in ? a.mean[row + b] : 0.f;
+        nrs[b] = in ? a.rstd[row + b] : 0.f;
+      }
+    };
+    load_stats(first + group * r.each);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int p = 0; p < passes; ++p) {
+      const int64_t row = first + p * stride + group * r.each;
+      Pair rs[B], mrs[B], s0[B], s1[B];
+      float rstd[B];
+      uint32_t ax[B], ay[B];
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        rstd[b] = nrs[b];
+        rs[b] = pair(nrs[b], nrs[b]);
+        mrs[b] = pair(-nmu[b] * nrs[b], -nmu[b] * nrs[b]);  // xh = x rstd - mu rstd
+      }
+      if (p + 1 < passes) load_stats(row + stride);
+      tc::mbar_wait(&full[s], ph, &abort_flag, err, tc::kErrTimeoutLoad);
+      // what lies past the last row is worked on like a row (in shared memory that
+      // a row before left) and not kept
+      const uint32_t slot = r.smem + (uint32_t)s * r.slot + (uint32_t)(group * r.each) * r.pitch;
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int q = b < r.each ? b : 0;
+        ax[b] = slot + (uint32_t)q * r.pitch + (VE == 1 ? phase(m[0], row + q) : 0u);
+        ay[b] = slot + (uint32_t)(r.rows + q) * r.pitch + (VE == 1 ? phase(m[1], row + q) : 0u);
+        s0[b] = s1[b] = 0;
+      }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        if (has(j)) {
+          Pair g[VP];
+          if constexpr (!HOLD) gamma_pairs(j, g);
+#pragma unroll
+          for (int b = 0; b < B; ++b) {
+            Pair x[VP], y[VP];
+            read(ax[b], j, x);
+            read(ay[b], j, y);
+#pragma unroll
+            for (int q = 0; q < VP; ++q) {
+              const Pair d = mul2(y[q], HOLD ? gamma[HOLD ? j * VP + q : 0] : g[q]);
+              s0[b] = add2(s0[b], d);
+              s1[b] = fma2(d, fma2(x[q], rs[b], mrs[b]), s1[b]);
             }
           }
         }
       }
-    }
-    if (a.dX == nullptr) continue;
-    row_sums<2>(s, tpr, slots[p & 1]);
-    const float s0 = s[0] * inv_k, s1 = s[1] * inv_k;
-    if (!in) continue;
-    X* dx = static_cast<X*>(a.dX) + row * a.ld_dx;
+      float v0[B], v1[B];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      if (j * tpr + t < nvec) {
-        float x[VE], y[VE], g[VE];
-        unpack<X, VE>(rx[j], x);
-        unpack<X, VE>(ry[j], y);
-        if constexpr (SHARED) load_weights<VE>(a.gamma, a.w_type, j * tpr + t, 1.f, g);
+      for (int b = 0; b < B; ++b) {
+        v0[b] = lane_sum(sum2(s0[b]), tpr);
+        v1[b] = lane_sum(sum2(s1[b]), tpr);
+      }
+      if (warps > 1) {
+        float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
+        if (lane == 0) {
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-          const float xh = (x[i] - mu) * rs;
-          const float d = y[i] * (SHARED ? g[i] : gamma[SHARED ? 0 : j * VE + i]);
-          y[i] = rs * (d - s0 - xh * s1);
+          for (int b = 0; b < B; ++b) q[b][warp] = make_float2(v0[b], v1[b]);
         }
-        store_vec<X, VE>(dx, j * tpr + t, y);
+        if (tpr == THREADS) tc::named_barrier(1, THREADS);
+        else tc::named_barrier(2 + warp0 / warps, tpr);
+        const int b = lane >> (31 - __clz(warps)), w = lane & (warps - 1);  // lane (row, warp) joins
+        const float2 v = b < B ? q[b][warp0 + w] : make_float2(0.f, 0.f);
+        const float w0 = lane_sum(v.x, warps), w1 = lane_sum(v.y, warps);
+#pragma unroll
+        for (int i = 0; i < B; ++i) {
+          v0[i] = __shfl_sync(0xFFFFFFFFu, w0, i * warps);
+          v1[i] = __shfl_sync(0xFFFFFFFFu, w1, i * warps);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        if (b >= r.each || row + b >= a.T) continue;
+        X* dx = static_cast<X*>(a.dX) + (row + b) * a.ld_dx;
+        const float f0 = -v0[b] * inv_k * rstd[b], f1 = -v1[b] * inv_k * rstd[b];
+        const Pair c0 = pair(f0, f0), c1 = pair(f1, f1);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+          if (has(j)) {
+            Pair x[VP], y[VP], g[VP];
+            read(ax[b], j, x);
+            read(ay[b], j, y);
+            if constexpr (!HOLD) gamma_pairs(j, g);
+#pragma unroll
+            for (int q = 0; q < VP; ++q) {
+              const int e = j * VP + q;
+              x[q] = fma2(x[q], rs[b], mrs[b]);
+              dg[e] = fma2(y[q], x[q], dg[e]);
+              db[e] = add2(db[e], y[q]);
+              y[q] = fma2(mul2(y[q], HOLD ? gamma[HOLD ? e : 0] : g[q]), rs[b], fma2(x[q], c1, c0));
+            }
+            if (a.dX) {
+              if constexpr (VE == 1) {
+                const float2 f = split(y[0]);
+                const int c = 2 * j * tpr + t;
+                store_one(dx + c, f.x);
+                if (c + tpr < k) store_one(dx + c + tpr, f.y);
+              } else {
+                store_vec<X>(dx, j * tpr + t, y);
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      if (++s == r.slots) {
+        s = 0;
+        ph ^= 1u;
       }
     }
   }
   if (a.dgamma == nullptr && a.dbeta == nullptr) return;
-  // this block's partial row: the groups' sums added in their order
+  // this block's partial row: the groups' sums added in their order, in the ring's memory
   float* out = a.ws + (int64_t)blockIdx.x * 2 * k;
-  if constexpr (SHARED) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < 2 * k; i += THREADS) out[i] = acc[i];
-  } else {
+  float* acc = reinterpret_cast<float*>(ring_mem);
+  __syncthreads();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if (groups > 1) {
+  for (int half = 0; half < 2; ++half) {
+    if (warp < THREADS / 32) {
+      float* to = groups > 1 ? acc + group * k : out + half * k;
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
+      for (int j = 0; j < NP; ++j) {
 #pragma unroll
-          for (int i = 0; i < VE; ++i)
-            if (j * tpr + t < nvec) acc[group * k + (j * tpr + t) * VE + i] = half ? db[j * VE + i] : dg[j * VE + i];
-        __syncthreads();
-        for (int c = threadIdx.x; c < k; c += THREADS) {
-          float v = 0.f;
-          for (int g = 0; g < groups; ++g) v += acc[g * k + c];
-          out[half * k + c] = v;
+        for (int q = 0; q < VP; ++q) {
+          const float2 f = split(half ? db[j * VP + q] : dg[j * VP + q]);
+          const int c0 = column(j, q, 0), c1 = column(j, q, 1);
+          if (FULL || c0 < k) to[c0] = f.x;
+          if (FULL || c1 < k) to[c1] = f.y;
         }
-        __syncthreads();
-      } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll
-          for (int i = 0; i < VE; ++i)
-            if (j * tpr + t < nvec) out[half * k + (j * tpr + t) * VE + i] = half ? db[j * VE + i] : dg[j * VE + i];
       }
+    }
+    if (groups > 1) {
+      __syncthreads();
+      for (int c = threadIdx.x; c < k; c += THREADS + 32) {
+        float v = 0.f;
+        for (int g = 0; g < groups; ++g) v += acc[g * k + c];
+        out[half * k + c] = v;
+      }
+      __syncthreads();
     }
   }
 }
@@ -393,25 +688,29 @@ __device__ __forceinline__ float get(const float* p, int64_t i) { return p[i]; }
 __device__ __forceinline__ float get(const __nv_bfloat16* p, int64_t i) { return __bfloat162float(p[i]); }
 __device__ __forceinline__ void put(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
-__device__ __forceinline__ float weight(const void* w, int type, int64_t i, float none) {
-  if (w == nullptr) return none;
-  return type == SKETCH_FP32 ? static_cast<const float*>(w)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(w)[i]);
+
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = lane_sum(v, 32);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += part[w];
+  return v;
 }
 
 template <typename X>
 __global__ void __launch_bounds__(kThreads) norm_forward_wide_kernel(const NormForward a) {
-  __shared__ float slots[2][kThreads / 32][1];
+  __shared__ float part[2][kThreads / 32];
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
   X* y = static_cast<X*>(a.Y) + row * a.ld_y;
-  float s[1] = {0.f};
-  for (int64_t i = threadIdx.x; i < a.k; i += kThreads) s[0] += get(x, i);
-  row_sums<1>(s, kThreads, slots[0]);
-  const float mu = s[0] / (float)a.k;
-  s[0] = 0.f;
-  for (int64_t i = threadIdx.x; i < a.k; i += kThreads) s[0] = fmaf(get(x, i) - mu, get(x, i) - mu, s[0]);
-  row_sums<1>(s, kThreads, slots[1]);
-  const float rstd = 1.f / sqrtf(s[0] / (float)a.k + a.eps);
+  float s = 0.f;
+  for (int64_t i = threadIdx.x; i < a.k; i += kThreads) s += get(x, i);
+  const float mu = block_sum(s, part[0]) / (float)a.k;
+  s = 0.f;
+  for (int64_t i = threadIdx.x; i < a.k; i += kThreads) s = fmaf(get(x, i) - mu, get(x, i) - mu, s);
+  const float rstd = 1.f / sqrtf(block_sum(s, part[1]) / (float)a.k + a.eps);
   for (int64_t i = threadIdx.x; i < a.k; i += kThreads)
     put(y, i, fmaf((get(x, i) - mu) * rstd, weight(a.gamma, a.w_type, i, 1.f), weight(a.beta, a.w_type, i, 0.f)));
   if (threadIdx.x == 0) {
@@ -441,20 +740,20 @@ __global__ void __launch_bounds__(kThreads) norm_grad_wide_kernel(const NormBack
 
 template <typename X>
 __global__ void __launch_bounds__(kThreads) norm_dx_wide_kernel(const NormBackward a) {
-  __shared__ float slots[kThreads / 32][2];
+  __shared__ float part[2][kThreads / 32];
   const int64_t row = blockIdx.x;
   const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
   const X* dy = static_cast<const X*>(a.dY) + row * a.ld_dy;
   X* dx = static_cast<X*>(a.dX) + row * a.ld_dx;
   const float mu = a.mean[row], rs = a.rstd[row];
-  float s[2] = {0.f, 0.f};
+  float s0 = 0.f, s1 = 0.f;
   for (int64_t i = threadIdx.x; i < a.k; i += kThreads) {
     const float d = get(dy, i) * weight(a.gamma, a.w_type, i, 1.f);
-    s[0] += d;
-    s[1] = fmaf(d, (get(x, i) - mu) * rs, s[1]);
+    s0 += d;
+    s1 = fmaf(d, (get(x, i) - mu) * rs, s1);
   }
-  row_sums<2>(s, kThreads, slots);
-  const float s0 = s[0] / (float)a.k, s1 = s[1] / (float)a.k;
+  s0 = block_sum(s0, part[0]) / (float)a.k;
+  s1 = block_sum(s1, part[1]) / (float)a.k;
   for (int64_t i = threadIdx.x; i < a.k; i += kThreads) {
     const float d = get(dy, i) * weight(a.gamma, a.w_type, i, 1.f);
     put(dx, i, rs * (d - s0 - ((get(x, i) - mu) * rs) * s1));
@@ -468,41 +767,89 @@ bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // Whether every row of the matrix starts on 16 bytes and ends with a whole vector.
 bool whole_vectors(const void* p, int64_t ld, int64_t k, int ve) { return on16(p) && ld % ve == 0 && k % ve == 0; }
 
-// Threads per row: the fewest that hold a row at `most` vectors each, then more
-// while the launch would leave SMs without a block.
+// Threads per row: the fewest (of at most `limit`) that hold a row at `most`
+// vectors each, then more while the launch would leave SMs without a block.
 int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
   int tpr = 8;
   while (tpr < limit && (int64_t)tpr * most < nvec) tpr *= 2;
-  while (tpr < limit && tpr < 256 && tpr < nvec && T * tpr < 2 * (int64_t)num_sms() * kThreads) tpr *= 2;
+  while (tpr < 256 && tpr < nvec && T * tpr < 2 * (int64_t)num_sms() * kThreads) tpr *= 2;
   return tpr;
 }
 
-template <typename X, int VE, int NV, int THREADS = kThreads>
-cudaError_t forward_rows(const NormForward& a, int tpr, cudaStream_t stream) {
-  const int64_t blocks = ceil_div(a.T, THREADS / tpr);
+template <int THREADS, typename Kernel>
+cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, cudaStream_t stream) {
+  const size_t smem = (size_t)a.k * 8;
+  if (smem > 48u * 1024u) {
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
+  }
+  int64_t blocks = ceil_div(a.T, THREADS / tpr);
+  const int64_t most = (int64_t)num_sms() * forward_blocks(THREADS);
+  if (blocks > most) blocks = most;
   count_launch();
-  norm_forward_kernel<X, VE, NV, THREADS><<<(unsigned)blocks, THREADS, 0, stream>>>(a, tpr);
+  kernel<<<(unsigned)blocks, THREADS, smem, stream>>>(a, tpr);
   return cudaGetLastError();
 }
 
-template <typename X, int VE>
-cudaError_t forward(const NormForward& a, cudaStream_t stream) {
-  const int64_t nvec = a.k / VE;
-  if constexpr (VE == 1) {  // 16 elements of a row per thread
-    const int tpr = threads_per_row(nvec, 16, a.T, 1024);
-    const int nv = (int)ceil_div(nvec, tpr);
-    if (tpr > kThreads) return forward_rows<X, VE, 16, 1024>(a, 1024, stream);
-    return nv <= 4 ? forward_rows<X, VE, 4>(a, tpr, stream) : forward_rows<X, VE, 16>(a, tpr, stream);
-  } else {  // 64
-    constexpr int kMost = 64 / VE;
-    const int tpr = threads_per_row(nvec, kMost, a.T, kThreads);
-    const int nv = (int)ceil_div(nvec, tpr);
-    if (nv <= 1) return forward_rows<X, VE, 1>(a, tpr, stream);
-    if (nv <= 2) return forward_rows<X, VE, 2>(a, tpr, stream);
-    if (nv <= 4) return forward_rows<X, VE, 4>(a, tpr, stream);
-    if (kMost > 8 && nv <= 8) return forward_rows<X, VE, 8>(a, tpr, stream);
-    return forward_rows<X, VE, kMost>(a, tpr, stream);
+// Blocks of 256 threads, three to an SM, while three copies of the weights leave
+// room there, else one of 1024 (whose threads have half the registers).
+template <typename X, int THREADS>
+cudaError_t forward_vectors(const NormForward& a, int tpr, cudaStream_t stream) {
+  return a.k == (int64_t)(16 / sizeof(X)) * forward_vecs(THREADS) * tpr
+             ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true>, a, tpr, stream)
+             : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false>, a, tpr, stream);
+}
+template <typename X>
+cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
+  const int64_t nvec = a.k / (int64_t)(16 / sizeof(X));
+  if (a.k <= 4096) return forward_vectors<X, 256>(a, threads_per_row(nvec, forward_vecs(256), a.T, 256), stream);
+  return forward_vectors<X, 1024>(a, threads_per_row(nvec, forward_vecs(1024), a.T, 1024), stream);
+}
+template <typename X>
+cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
+  const int tpr = threads_per_row(a.k, 16, a.T, 1024);
+  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256>, a, tpr, stream);
+  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024>, a, tpr, stream);
+}
+
+// The ring for sets of rows of `matrices` matrices, with `beside` bytes of shared
+// memory behind it; 0 slots where not even one fits.
+Ring make_ring(int64_t k, size_t size, int ve, int groups, int each, int matrices, int threads, size_t beside) {
+  Ring r = {};
+  r.rows = groups * each;
+  r.each = each;
+  // VE = 1: room for 16-byte boundaries around a row
+  r.pitch = ve > 1 ? (uint32_t)(k * size) : (uint32_t)((k * size + 15) / 16 * 16 + 16);
+  r.slot = r.pitch * (uint32_t)(r.rows * matrices);
+  const uint32_t room = ((blocks_per_sm(threads) == 2 ? 108u : 216u) << 10) - (uint32_t)beside;
+  r.slots = (int)(room / r.slot < kMaxSlots ? room / r.slot : kMaxSlots);
+  return r;
+}
+
+// Rows side by side: as many as `most` while every block still has a set.
+int rows_each(int most, int64_t T, int groups, int threads) {
+  const int64_t sets = (int64_t)num_sms() * blocks_per_sm(threads) * groups;
+  int each = 1;
+  while (each < most && T >= 2 * each * sets) each *= 2;
+  return each;
+}
+
+// A launch of `kernel` over row sets; `room`: shared memory that it needs at least.
+template <typename Args, typename Kernel>
+cudaError_t launch_rows(Kernel kernel, const Args& a, const Ring& r, int tpr, int threads, int64_t blocks, size_t room,
+                        cudaStream_t stream) {
+  int* err_word = nullptr;
+  cudaError_t err = device_error_word(&err_word);
+  if (err != cudaSuccess) return err;
+  size_t smem = (size_t)r.slots * r.slot;
+  if (smem < room) smem = room;
+  if (smem > 48u * 1024u) {
+    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (err != cudaSuccess) return err;
   }
+  count_launch();
+  kernel<<<(unsigned)blocks, threads + 32, smem, stream>>>(a, r, tpr, err_word);
+  return cudaGetLastError();
 }
 
 cudaError_t launch_grad_sum(const NormBackward& a, int partials, cudaStream_t stream) {
@@ -520,41 +867,37 @@ cudaError_t launch_grad_sum(const NormBackward& a, int partials, cudaStream_t st
                             a.overwrite);
 }
 
-template <typename X, int VE, int NV, int THREADS, bool SHARED>
-cudaError_t backward_rows(const NormBackward& a, int tpr, cudaStream_t stream) {
+template <typename X, int VE, int NV, int THREADS>
+cudaError_t backward_rows(const NormBackward& a, int tpr, bool& done, cudaStream_t stream) {
   const int groups = THREADS / tpr;
-  int64_t blocks = ceil_div(a.T, groups);
-  const int64_t most = (int64_t)num_sms() * (THREADS == 256 ? 2 : 1);
+  const int each = rows_each(backward_rows_each(sizeof(X), THREADS), a.T, groups, THREADS);
+  int64_t blocks = ceil_div(a.T, groups * each);
+  const int64_t most = (int64_t)num_sms() * blocks_per_sm(THREADS);
   if (blocks > most) blocks = most;
   if (blocks > kMaxPartials) blocks = kMaxPartials;
-  const size_t smem = SHARED ? (size_t)(2 * a.k) * 4 : groups > 1 ? (size_t)groups * a.k * 4 : 0;
-  auto kernel = norm_backward_kernel<X, VE, NV, THREADS, SHARED>;
-  if (SHARED) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
+  const size_t beside = VE * NV > 16 ? (size_t)a.k * 4 : 0;  // gamma
+  const Ring r = make_ring(a.k, sizeof(X), VE, groups, each, 2, THREADS, beside);
+  if (r.slots < 1) return cudaSuccess;
+  done = true;
+  const size_t room = groups > 1 ? (size_t)groups * a.k * 4 : (size_t)r.slots * r.slot + beside;
+  cudaError_t err;
+  bool full = false;
+  if constexpr (VE > 1) {
+    full = a.k == (int64_t)VE * NV * tpr;
+    if (full) err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, true>, a, r, tpr, THREADS, blocks, room, stream);
   }
-  count_launch();
-  kernel<<<(unsigned)blocks, THREADS, smem, stream>>>(a, tpr);
-  cudaError_t err = cudaGetLastError();
+  if (!full) err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false>, a, r, tpr, THREADS, blocks, room, stream);
   if (err == cudaSuccess && (a.dgamma || a.dbeta)) err = launch_grad_sum(a, (int)blocks, stream);
   return err;
 }
 
 template <typename X, int VE>
-cudaError_t backward(const NormBackward& a, cudaStream_t stream) {
-  const int64_t nvec = a.k / VE;
-  if constexpr (VE == 1) {  // eight elements of a row per thread
-    const int tpr = threads_per_row(nvec, 8, a.T, 2048);
-    if (tpr <= 256) return backward_rows<X, VE, 8, 256, false>(a, tpr, stream);
-    if (tpr <= 1024) return backward_rows<X, VE, 8, 1024, false>(a, 1024, stream);
-    return backward_rows<X, VE, 16, 1024, true>(a, 1024, stream);
-  } else {  // 16
-    constexpr int kNV = 16 / VE;
-    const int tpr = threads_per_row(nvec, kNV, a.T, 1024);
-    if (tpr <= 256) return backward_rows<X, VE, kNV, 256, false>(a, tpr, stream);
-    if (tpr == 512) return backward_rows<X, VE, kNV, 512, false>(a, tpr, stream);
-    return backward_rows<X, VE, kNV, 1024, true>(a, tpr, stream);
-  }
+cudaError_t backward(const NormBackward& a, bool& done, cudaStream_t stream) {
+  constexpr int kNV = 16 / VE;  // 16 elements of a row per thread, 32 above 8192
+  const int tpr = threads_per_row(a.k / VE, kNV, a.T, 512);
+  if (tpr <= 256) return backward_rows<X, VE, kNV, 256>(a, tpr, done, stream);
+  if (a.k <= 8192) return backward_rows<X, VE, kNV, 512>(a, 512, done, stream);
+  return backward_rows<X, VE, 2 * kNV, 512>(a, 512, done, stream);
 }
 
 template <typename X>
@@ -577,24 +920,26 @@ cudaError_t backward_wide(const NormBackward& a, cudaStream_t stream) {
 template <typename X>
 cudaError_t forward_any(const NormForward& a, cudaStream_t stream) {
   constexpr int VE = 16 / sizeof(X);
-  if (a.k > kMaxRowWidth) {
-    count_launch();
-    norm_forward_wide_kernel<X><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+  if (a.k <= kMaxRowWidth) {
+    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.Y, a.ld_y, a.k, VE);
+    return vectors ? forward_vectors<X>(a, stream) : forward_singles<X>(a, stream);
   }
-  if (whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.Y, a.ld_y, a.k, VE) && on16(a.gamma) && on16(a.beta))
-    return forward<X, VE>(a, stream);
-  return forward<X, 1>(a, stream);
+  count_launch();
+  norm_forward_wide_kernel<X><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename X>
 cudaError_t backward_any(const NormBackward& a, cudaStream_t stream) {
   constexpr int VE = 16 / sizeof(X);
-  if (a.k > kMaxRowWidth) return backward_wide<X>(a, stream);
-  if (whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.dY, a.ld_dy, a.k, VE) && on16(a.gamma) &&
-      (a.dX == nullptr || whole_vectors(a.dX, a.ld_dx, a.k, VE)))
-    return backward<X, VE>(a, stream);
-  return backward<X, 1>(a, stream);
+  bool done = false;
+  cudaError_t err = cudaSuccess;
+  if (a.k <= kMaxRowWidth) {
+    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.dY, a.ld_dy, a.k, VE) &&
+                         (a.dX == nullptr || whole_vectors(a.dX, a.ld_dx, a.k, VE));
+    err = vectors ? backward<X, VE>(a, done, stream) : backward<X, 1>(a, done, stream);
+  }
+  return (done || err != cudaSuccess) ? err : backward_wide<X>(a, stream);
 }
 
 }  // namespace
