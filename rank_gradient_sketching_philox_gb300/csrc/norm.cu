@@ -37,6 +37,8 @@
 // results repeat bit for bit.
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
@@ -120,12 +122,35 @@ __device__ __forceinline__ float weight(const void* w, int type, int64_t i, floa
   if (w == nullptr) return none;
   return type == SKETCH_FP32 ? static_cast<const float*>(w)[i] : bf16_bits_to_float(static_cast<const uint16_t*>(w)[i]);
 }
-// Sum over the tpr lanes (of up to a warp) that share a row.
-__device__ __forceinline__ float lane_sum(float v, int tpr) {
+// Sums of N values over the lanes that share a row: a whole warp (WARP) or `tpr`
+// lanes of it.  The values' shuffles go side by side.
+template <bool WARP, int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int tpr) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (o < tpr) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+  for (int o = 16; o > 0; o >>= 1) {
+    if (WARP || o < tpr) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    }
+  }
+}
+template <bool WARP>
+__device__ __forceinline__ float lane_sum(float v, int tpr) {
+  float a[1] = {v};
+  lane_sums<WARP, 1>(a, tpr);
+  return a[0];
+}
+// Sums of the values of the `warps` warps (2 to 32, a power of two) of a row, held
+// by as many neighbouring lanes.
+template <int N>
+__device__ __forceinline__ void join_sums(float (&v)[N], int warps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o < warps) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
+    }
+  }
 }
 
 // ---- the ring of row sets -----------------------------------------------------------
@@ -263,26 +288,30 @@ __device__ __forceinline__ void weight_pairs(uint32_t base, int idx, int k, Pair
 // of squares, so that a row far from zero loses nothing).  `part` alternates
 // between rows: a thread that writes it again has passed the barrier of the row
 // between, after which nobody reads the old values.
-template <typename Dev>
+template <bool WARP, typename Dev>
 __device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float inv_n, float inv_k, const float* counts,
                                             float2* part, float& mu, float& m2) {
-  mu = lane_sum(sum, tpr) * inv_n;
-  m2 = lane_sum(dev(mu), tpr);
+  mu = lane_sum<WARP>(sum, tpr) * inv_n;
+  m2 = lane_sum<WARP>(dev(mu), tpr);
   const int warps = tpr >> 5;
-  if (warps > 1) {
+  if (WARP && warps > 1) {
     const int lane = threadIdx.x & 31, warp0 = (threadIdx.x & ~(tpr - 1)) >> 5;
     if (lane == 0) part[threadIdx.x >> 5] = make_float2(mu, m2);
     if (tpr == (int)blockDim.x) __syncthreads();
     else tc::named_barrier(1 + warp0 / warps, tpr);
     const int w = warp0 + (lane & (warps - 1));  // every `warps` lanes join the row's warps
     const float2 v = part[w];
-    mu = lane_sum(counts[w] * v.x, warps) * inv_k;
-    m2 = lane_sum(fmaf(counts[w] * (v.x - mu), v.x - mu, v.y), warps);
+    float j[1] = {counts[w] * v.x};
+    join_sums(j, warps);
+    mu = j[0] * inv_k;
+    j[0] = fmaf(counts[w] * (v.x - mu), v.x - mu, v.y);
+    join_sums(j, warps);
+    m2 = j[0];
   }
 }
 
-// FULL: every thread has forward_vecs vectors.
-template <typename X, int THREADS, bool FULL>
+// FULL: every thread has forward_vecs vectors.  WARP: a row has a warp at least.
+template <typename X, int THREADS, bool FULL, bool WARP>
 __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_kernel(const NormForward a, int tpr) {
   constexpr int VE = 16 / sizeof(X), NV = forward_vecs(THREADS);
   extern __shared__ __align__(128) float weights[];
@@ -326,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
       for (int i = 0; i < VE / 2; ++i) s = add2(s, v[i]);
     }
     float mu, m2;
-    row_moments(
+    row_moments<WARP>(
         sum2(s),
         [&](float m) {
           const Pair neg = pair(-m, -m);
@@ -370,7 +399,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
 }
 
 // Rows whose elements are read one by one: NV of them per thread.
-template <typename X, int NV, int THREADS>
+template <typename X, int NV, int THREADS, bool WARP>
 __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_single_kernel(const NormForward a, int tpr) {
   extern __shared__ __align__(128) float weights[];
   __shared__ float2 part[2][THREADS / 32];
@@ -402,7 +431,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
 #pragma unroll
     for (int j = 0; j < NV; ++j) sum += f[j];
     float mu, m2;
-    row_moments(
+    row_moments<WARP>(
         sum,
         [&](float m) {
           float q = 0.f;
@@ -432,7 +461,7 @@ constexpr int backward_rows_each(size_t size, int threads) { return threads == 2
 
 // A thread's columns: NV vectors of VE elements, as E / 2 pairs.  With VE = 1 a pair
 // is the thread's elements 2 q and 2 q + 1, tpr columns apart.
-template <typename X, int VE, int NV, int THREADS, bool FULL>
+template <typename X, int VE, int NV, int THREADS, bool FULL, bool WARP>
 __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
     norm_backward_kernel(const NormBackward a, const Ring ring, int tpr, int* err) {
   constexpr int E = NV * VE, B = backward_rows_each(sizeof(X), THREADS);
@@ -470,29 +499,32 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
   auto read = [&](uint32_t at, int j, Pair (&v)[VP]) {
     if constexpr (VE == 1) {
       const int c = 2 * j * tpr + t;
-      v[0] = pair(read_one<X>(at + (uint32_t)(c * sizeof(X))),
-                  c + tpr < k ? read_one<X>(at + (uint32_t)((c + tpr) * sizeof(X))) : 0.f);
+      const uint32_t p = r.smem + at + (uint32_t)(c * sizeof(X));
+      v[0] = pair(read_one<X>(p), c + tpr < k ? read_one<X>(p + (uint32_t)(tpr * sizeof(X))) : 0.f);
     } else {
-      vec_pairs<X>(tc::lds128(at + 16u * (uint32_t)(j * tpr + t)), v);
+      // `at` is the thread's first vector; plain loads, which the compiler may move
+      // ahead, where registers allow it
+      const uint32_t p = at + (uint32_t)j * (16u * tpr);
+      if constexpr (FULL && HOLD) vec_pairs<X>(*reinterpret_cast<const uint4*>(ring_mem + p), v);
+      else vec_pairs<X>(tc::lds128(r.smem + p), v);
     }
   };
   Pair dg[E / 2], db[E / 2], gamma[HOLD ? E / 2 : 1];
   // wide rows: gamma behind the ring, as the forward pass lays it out
-  const uint32_t gbase = r.smem + (uint32_t)r.slots * r.slot;
+  float* gmem = reinterpret_cast<float*>(ring_mem + (size_t)r.slots * r.slot);
   if (warp == THREADS / 32) {
     produce<VE, 2>(r, m, first, stride, passes, full, empty, &abort_flag, err);
   } else {
     auto gamma_pairs = [&](int j, Pair (&g)[VP]) {
       if constexpr (VE == 1) {
         const int c = 2 * j * tpr + t;
-        g[0] = pair(tc::lds_f32(gbase + 4u * c), c + tpr < k ? tc::lds_f32(gbase + 4u * (c + tpr)) : 0.f);
+        g[0] = pair(gmem[c], c + tpr < k ? gmem[c + tpr] : 0.f);
       } else {
-        weight_pairs<VE>(gbase, j * tpr + t, k, g);
+        weight_pairs<VE>(tc::smem_u32(gmem), j * tpr + t, k, g);
       }
     };
     if constexpr (!HOLD) {
-      float* g = reinterpret_cast<float*>(ring_mem + (size_t)r.slots * r.slot);
-      for (int c = threadIdx.x; c < k; c += THREADS) g[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
+      for (int c = threadIdx.x; c < k; c += THREADS) gmem[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
       tc::named_barrier(1, THREADS);
     }
 #pragma unroll
@@ -507,20 +539,27 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
       }
     }
     const float inv_k = 1.f / (float)k;
+    // rows, row strides (below 2^31) and their products in 32 x 32 -> 64 bits
+    const uint32_t T = (uint32_t)a.T, step = (uint32_t)stride, ld_dx = (uint32_t)(a.ld_dx * sizeof(X) >> 1);
+    uint32_t row = (uint32_t)first + group * r.each;
     float nmu[B], nrs[B];  // the next set's
-    auto load_stats = [&](int64_t row) {
+    auto load_stats = [&](uint32_t at) {
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const bool in = b < r.each && row + b < a.T;
-        nmu[b] = in ? a.mean[row + b] : 0.f;
-        nrs[b] = in ? a.rstd[row + b] : 0.f;
+        nmu[b] = nrs[b] = 0.f;
+        if (b < r.each && at + b < T) {
+          nmu[b] = a.mean[at + b];
+          nrs[b] = a.rstd[at + b];
+        }
       }
     };
-    load_stats(first + group * r.each);
+    load_stats(row);
+    const uint32_t vec0 = 16u * t;
+    const uint32_t set_at = (uint32_t)(group * r.each) * r.pitch, y_at = (uint32_t)r.rows * r.pitch;
+    uint32_t slot = set_at;  // in the ring
     int s = 0;
     uint32_t ph = 0;
-    for (int p = 0; p < passes; ++p) {
-      const int64_t row = first + p * stride + group * r.each;
+    for (int p = 0; p < passes; ++p, row += step) {
       Pair rs[B], mrs[B], s0[B], s1[B];
       float rstd[B];
       uint32_t ax[B], ay[B];
@@ -530,16 +569,22 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
         rs[b] = pair(nrs[b], nrs[b]);
         mrs[b] = pair(-nmu[b] * nrs[b], -nmu[b] * nrs[b]);  // xh = x rstd - mu rstd
       }
-      if (p + 1 < passes) load_stats(row + stride);
+      if (p + 1 < passes) load_stats(row + step);
       tc::mbar_wait(&full[s], ph, &abort_flag, err, tc::kErrTimeoutLoad);
       // what lies past the last row is worked on like a row (in shared memory that
       // a row before left) and not kept
-      const uint32_t slot = r.smem + (uint32_t)s * r.slot + (uint32_t)(group * r.each) * r.pitch;
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        const int q = b < r.each ? b : 0;
-        ax[b] = slot + (uint32_t)q * r.pitch + (VE == 1 ? phase(m[0], row + q) : 0u);
-        ay[b] = slot + (uint32_t)(r.rows + q) * r.pitch + (VE == 1 ? phase(m[1], row + q) : 0u);
+        const uint32_t q = b < r.each ? b : 0;
+        ax[b] = slot + q * r.pitch;
+        ay[b] = ax[b] + y_at;
+        if constexpr (VE == 1) {
+          ax[b] += phase(m[0], row + q);
+          ay[b] += phase(m[1], row + q);
+        } else {
+          ax[b] += vec0;
+          ay[b] += vec0;
+        }
         s0[b] = s1[b] = 0;
       }
 #pragma unroll
@@ -561,68 +606,78 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
           }
         }
       }
-      float v0[B], v1[B];
+      float v[2 * B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
-        v0[b] = lane_sum(sum2(s0[b]), tpr);
-        v1[b] = lane_sum(sum2(s1[b]), tpr);
+        v[2 * b] = sum2(s0[b]);
+        v[2 * b + 1] = sum2(s1[b]);
       }
-      if (warps > 1) {
+      lane_sums<WARP, 2 * B>(v, tpr);
+      if (WARP && warps > 1) {
         float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
         if (lane == 0) {
 #pragma unroll
-          for (int b = 0; b < B; ++b) q[b][warp] = make_float2(v0[b], v1[b]);
+          for (int b = 0; b < B; ++b) q[b][warp] = make_float2(v[2 * b], v[2 * b + 1]);
         }
         if (tpr == THREADS) tc::named_barrier(1, THREADS);
         else tc::named_barrier(2 + warp0 / warps, tpr);
         const int b = lane >> (31 - __clz(warps)), w = lane & (warps - 1);  // lane (row, warp) joins
-        const float2 v = b < B ? q[b][warp0 + w] : make_float2(0.f, 0.f);
-        const float w0 = lane_sum(v.x, warps), w1 = lane_sum(v.y, warps);
+        const float2 u = q[b < B ? b : 0][warp0 + w];
+        float j[2] = {u.x, u.y};
+        join_sums(j, warps);
 #pragma unroll
         for (int i = 0; i < B; ++i) {
-          v0[i] = __shfl_sync(0xFFFFFFFFu, w0, i * warps);
-          v1[i] = __shfl_sync(0xFFFFFFFFu, w1, i * warps);
+          v[2 * i] = __shfl_sync(0xFFFFFFFFu, j[0], i * warps);
+          v[2 * i + 1] = __shfl_sync(0xFFFFFFFFu, j[1], i * warps);
         }
       }
+      // the gradients; WHOLE: all of the block's rows of this set exist
+      auto second = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
 #pragma unroll
-      for (int b = 0; b < B; ++b) {
-        if (b >= r.each || row + b >= a.T) continue;
-        X* dx = static_cast<X*>(a.dX) + (row + b) * a.ld_dx;
-        const float f0 = -v0[b] * inv_k * rstd[b], f1 = -v1[b] * inv_k * rstd[b];
-        const Pair c0 = pair(f0, f0), c1 = pair(f1, f1);
+        for (int b = 0; b < B; ++b) {
+          if (!WHOLE && (b >= r.each || row + b >= T)) continue;
+          X* dx = reinterpret_cast<X*>(static_cast<char*>(a.dX) + 2 * ((uint64_t)(row + b) * ld_dx));
+          const float f0 = -v[2 * b] * inv_k * rstd[b], f1 = -v[2 * b + 1] * inv_k * rstd[b];
+          const Pair c0 = pair(f0, f0), c1 = pair(f1, f1);
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          if (has(j)) {
-            Pair x[VP], y[VP], g[VP];
-            read(ax[b], j, x);
-            read(ay[b], j, y);
-            if constexpr (!HOLD) gamma_pairs(j, g);
+          for (int j = 0; j < NP; ++j) {
+            if (has(j)) {
+              Pair x[VP], y[VP], g[VP];
+              read(ax[b], j, x);
+              read(ay[b], j, y);
+              if constexpr (!HOLD) gamma_pairs(j, g);
 #pragma unroll
-            for (int q = 0; q < VP; ++q) {
-              const int e = j * VP + q;
-              x[q] = fma2(x[q], rs[b], mrs[b]);
-              dg[e] = fma2(y[q], x[q], dg[e]);
-              db[e] = add2(db[e], y[q]);
-              y[q] = fma2(mul2(y[q], HOLD ? gamma[HOLD ? e : 0] : g[q]), rs[b], fma2(x[q], c1, c0));
-            }
-            if (a.dX) {
+              for (int q = 0; q < VP; ++q) {
+                const int e = j * VP + q;
+                x[q] = fma2(x[q], rs[b], mrs[b]);
+                dg[e] = fma2(y[q], x[q], dg[e]);
+                db[e] = add2(db[e], y[q]);
+                y[q] = fma2(mul2(y[q], HOLD ? gamma[HOLD ? e : 0] : g[q]), rs[b], fma2(x[q], c1, c0));
+              }
               if constexpr (VE == 1) {
-                const float2 f = split(y[0]);
-                const int c = 2 * j * tpr + t;
-                store_one(dx + c, f.x);
-                if (c + tpr < k) store_one(dx + c + tpr, f.y);
+                if (a.dX) {
+                  const float2 f = split(y[0]);
+                  const int c = 2 * j * tpr + t;
+                  store_one(dx + c, f.x);
+                  if (c + tpr < k) store_one(dx + c + tpr, f.y);
+                }
               } else {
-                store_vec<X>(dx, j * tpr + t, y);
+                if (a.dX) store_vec<X>(dx, j * tpr + t, y);
               }
             }
           }
         }
-      }
+      };
+      if (FULL && HOLD && r.each == B && row - group * r.each + r.rows <= T) second(std::bool_constant<FULL && HOLD>{});
+      else second(std::false_type{});
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&empty[s]);
+      slot += r.slot;
       if (++s == r.slots) {
         s = 0;
         ph ^= 1u;
+        slot = set_at;
       }
     }
   }
@@ -690,7 +745,7 @@ __device__ __forceinline__ void put(float* p, int64_t i, float v) { p[i] = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, int64_t i, float v) { p[i] = __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ float block_sum(float v, float* part) {
-  v = lane_sum(v, 32);
+  v = lane_sum<true>(v, 32);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
   __syncthreads();
   v = 0.f;
@@ -795,9 +850,12 @@ cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, cudaStr
 // room there, else one of 1024 (whose threads have half the registers).
 template <typename X, int THREADS>
 cudaError_t forward_vectors(const NormForward& a, int tpr, cudaStream_t stream) {
-  return a.k == (int64_t)(16 / sizeof(X)) * forward_vecs(THREADS) * tpr
-             ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true>, a, tpr, stream)
-             : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false>, a, tpr, stream);
+  const bool full = a.k == (int64_t)(16 / sizeof(X)) * forward_vecs(THREADS) * tpr;
+  if constexpr (THREADS == 256) {
+    if (tpr < 32) return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, false>, a, tpr, stream);
+  }
+  return full ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true, true>, a, tpr, stream)
+              : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, true>, a, tpr, stream);
 }
 template <typename X>
 cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
@@ -808,8 +866,9 @@ cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
 template <typename X>
 cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
   const int tpr = threads_per_row(a.k, 16, a.T, 1024);
-  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256>, a, tpr, stream);
-  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024>, a, tpr, stream);
+  if (tpr < 32) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, false>, a, tpr, stream);
+  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, true>, a, tpr, stream);
+  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024, true>, a, tpr, stream);
 }
 
 // The ring for sets of rows of `matrices` matrices, with `beside` bytes of shared
@@ -880,13 +939,21 @@ cudaError_t backward_rows(const NormBackward& a, int tpr, bool& done, cudaStream
   if (r.slots < 1) return cudaSuccess;
   done = true;
   const size_t room = groups > 1 ? (size_t)groups * a.k * 4 : (size_t)r.slots * r.slot + beside;
-  cudaError_t err;
+  cudaError_t err = cudaSuccess;
   bool full = false;
   if constexpr (VE > 1) {
-    full = a.k == (int64_t)VE * NV * tpr;
-    if (full) err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, true>, a, r, tpr, THREADS, blocks, room, stream);
+    full = a.k == (int64_t)VE * NV * tpr && tpr >= 32;
+    if (full)
+      err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, true, true>, a, r, tpr, THREADS, blocks, room, stream);
   }
-  if (!full) err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false>, a, r, tpr, THREADS, blocks, room, stream);
+  if constexpr (THREADS == 256) {
+    if (tpr < 32) {
+      full = true;
+      err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, false>, a, r, tpr, THREADS, blocks, room, stream);
+    }
+  }
+  if (!full)
+    err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, true>, a, r, tpr, THREADS, blocks, room, stream);
   if (err == cudaSuccess && (a.dgamma || a.dbeta)) err = launch_grad_sum(a, (int)blocks, stream);
   return err;
 }
