@@ -181,43 +181,45 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each operand ----
+    // This thread paces the kernel once its loop holds more than the waits and
+    // the copies: what a product needs is read once per tile (looked up for each
+    // chunk it took 700 cycles a chunk, whose MMAs take 512).
+    const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
     int s = 0, it = 0;
     uint32_t ph = 0;
-    bool stop = false;
-    for (int item = pair; item < n_items && !stop; item += n_pairs) {
+    for (int item = pair; item < n_items; item += n_pairs) {
       const Tile t = order.at(a.n, item);
       const Product& pr = a.p[t.p];
+      const int a_mn = pr.a_mn, b_mn = pr.b_mn;
       const int ar = pr.a_row + t.m + kHalf * (int)rank, br = pr.b_row + t.n + kHalf * (int)rank;
-      const int kchunks = order.kchunks[t.p];
-      for (int c = 0; c < kchunks; ++c, ++it) {
-        if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
-          stop = true;
-          break;
-        }
-        uint8_t* st = smem + (size_t)s * kStageBytes;
+      const CUtensorMap *tmA = &pr.tmA, *tmB = &pr.tmB;
+      int ak = pr.a_k, bk = pr.b_k;
+      const int end = it + order.kchunks[t.p];
+      for (; it < end; ++it, ak += kChunk, bk += kChunk) {
+        if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
+        uint8_t* st = smem + s * kStageBytes;
         if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], 2 * kStageBytes);
-        const uint32_t bar = tc::mapa_shared(tc::smem_u32(&full_bar[s]), 0);
-        const int ak = pr.a_k + c * kChunk, bk = pr.b_k + c * kChunk;
-        if (pr.a_mn) {  // two boxes of [64 k][64 rows]
-          tc::tma_load_2d_pair(st, &pr.tmA, bar, ar, ak);
-          tc::tma_load_2d_pair(st + kOperandBytes / 2, &pr.tmA, bar, ar + 64, ak);
+        const uint32_t bar = full0 + 8u * s;
+        if (a_mn) {  // two boxes of [64 k][64 rows]
+          tc::tma_load_2d_pair(st, tmA, bar, ar, ak);
+          tc::tma_load_2d_pair(st + kOperandBytes / 2, tmA, bar, ar + 64, ak);
         } else {  // one box of [128 rows][64 k]
-          tc::tma_load_2d_pair(st, &pr.tmA, bar, ak, ar);
+          tc::tma_load_2d_pair(st, tmA, bar, ak, ar);
         }
-        uint8_t* bt = st + kOperandBytes;
-        if (pr.b_mn) {
-          tc::tma_load_2d_pair(bt, &pr.tmB, bar, br, bk);
-          tc::tma_load_2d_pair(bt + kOperandBytes / 2, &pr.tmB, bar, br + 64, bk);
+        if (b_mn) {
+          tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, br, bk);
+          tc::tma_load_2d_pair(st + kOperandBytes + kOperandBytes / 2, tmB, bar, br + 64, bk);
         } else {
-          tc::tma_load_2d_pair(bt, &pr.tmB, bar, bk, br);
+          tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, bk, br);
         }
-        issued = it + 1;
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
         }
       }
+      if (it < end) break;  // a wait gave up
     }
+    issued = it;
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // ---- MMA issuer, for both CTAs ----
     int s = 0, it = 0, j = 0;
@@ -236,19 +238,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * kTile);
+      const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), a_lbo, 1024);
+      const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kOperandBytes, b_lbo, 1024);
       for (int c = 0; c < kchunks; ++c, ++it) {
         if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) {
           stop = true;
           break;
         }
         tc::tc_fence_after();
-        const uint32_t sa = tc::smem_u32(smem + (size_t)s * kStageBytes);
-        const uint64_t ad = tc::sdesc_sw128(sa, a_lbo, 1024), bd = tc::sdesc_sw128(sa + kOperandBytes, b_lbo, 1024);
+        // a stage further: its size in the descriptors' address fields (16-byte units)
+        const uint64_t ad = ad0 + (uint32_t)s * (kStageBytes >> 4), bd = bd0 + (uint32_t)s * (kStageBytes >> 4);
 #pragma unroll
         for (int kk = 0; kk < kChunk / 16; ++kk)
           tc::mma_bf16_pair(acc, ad + kk * a_step, bd + kk * b_step, idesc, (c > 0 || kk > 0) ? 1u : 0u);
         tc::mma_commit_pair(&empty_bar[s]);
-        consumed = it + 1;
         if (++s == kStages) {
           s = 0;
           ph ^= 1u;
@@ -256,6 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       }
       if (!stop) tc::mma_commit_pair(&tfull_bar[b]);
     }
+    consumed = it;
   } else if (warp >= 2) {
     // ---- epilogue: one row per thread, half of the tile's columns ----
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
