@@ -204,8 +204,6 @@ def _workspace(nbytes, device, stream, given=None):
         if not given.is_cuda or given.numel() * given.element_size() < nbytes:
             raise ValueError("workspace needs %d bytes" % nbytes)
         return given
-    if stream.cuda_stream == torch.cuda.current_stream(device).cuda_stream:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
@@ -571,6 +569,10 @@ def apply_update_sgd_batched(Ws, Cs, Ps, alpha_eta, seed, layers, step, dev_stat
 
 _DTYPES = {torch.bfloat16: DTYPE_BF16, torch.float32: DTYPE_FP32}
 
+# These calls are short enough for Python's share to show, so their checks and
+# marshalling are lean: addresses and the stream's handle as plain numbers, each
+# property of a tensor asked once.
+
 
 def _dtype(t, name):
     try:
@@ -579,17 +581,48 @@ def _dtype(t, name):
         raise ValueError("%s must be bfloat16 or float32, got %s" % (name, t.dtype)) from None
 
 
-def _norm_rows(t, like, name):
-    """Row stride of a 2-D CUDA activation tensor of ``like``'s shape, type and device."""
-    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError("%s must be a 2-D CUDA tensor with unit column stride" % name)
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream_of(stream, device):
+    """Handle of the given stream, or of the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _scratch(op, T, d, k, r, device, stream, given):
+    """(workspace of a call, its address, its size): the caller's, or one that belongs to the call's stream."""
+    nbytes = lib().sketch_workspace_bytes(op, T, d, k, r)
+    if given is not None:
+        if not given.is_cuda or given.numel() * given.element_size() < nbytes:
+            raise ValueError("workspace needs %d bytes" % nbytes)
+    elif nbytes == 0:
+        return None, None, 0
+    elif stream is None:
+        given = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        given = _workspace(nbytes, device, stream)
+    return given, given.data_ptr(), nbytes
+
+
+def _norm_rows(t, shape, dtype, device, name):
+    """Row stride of a 2-D CUDA activation tensor with X's shape, type and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device:
         raise ValueError("%s must have X's shape, type and device" % name)
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _norm_x(X):
+    if not X.is_cuda or X.dim() != 2:
+        raise ValueError("X must be a 2-D CUDA tensor")
+    return X.shape, X.dtype, X.device
 
 
 def _vector(t, n, dtype, device, name):
-    """Contiguous vector of n values on ``device``; of ``dtype``, or BF16 or fp32 when that is None."""
+    """Check a contiguous vector of n values on ``device``, of ``dtype`` (any when that is None)."""
     if not t.is_contiguous() or t.numel() != n or t.device != device or (dtype is not None and t.dtype != dtype):
         raise ValueError("%s must be a contiguous %s vector of %d on %s" % (name, dtype or "", n, device))
 
@@ -609,15 +642,17 @@ def layer_norm_forward(X, gamma, beta, Y, mean, rstd, eps=1e-5, stream=None):
     mean and rstd (T fp32) are written for the backward pass.  gamma and beta
     (k, BF16 or fp32) may be None.  Y may be X."""
     x_type = _dtype(X, "X")
-    ld_x, ld_y = _norm_rows(X, X, "X"), _norm_rows(Y, X, "Y")
-    T, k = X.shape
-    dev = X.device
+    shape, dtype, dev = _norm_x(X)
+    T, k = shape
+    ld_x, ld_y = _norm_rows(X, shape, dtype, dev, "X"), _norm_rows(Y, shape, dtype, dev, "Y")
     w_type = _norm_weights(gamma, beta, k, dev)
     _vector(mean, T, torch.float32, dev, "mean")
     _vector(rstd, T, torch.float32, dev, "rstd")
-    h, _ = _stream_handle(stream, dev)
-    _check(lib().sketch_layer_norm_forward(_ptr(X), x_type, T, k, ld_x, _ptr(gamma), _ptr(beta), w_type, eps,
-                                           _ptr(Y), ld_y, _ptr(mean), _ptr(rstd), h))
+    st = lib().sketch_layer_norm_forward(X.data_ptr(), x_type, T, k, ld_x, _addr(gamma), _addr(beta), w_type, eps,
+                                         Y.data_ptr(), ld_y, mean.data_ptr(), rstd.data_ptr(),
+                                         _stream_of(stream, dev))
+    if st:
+        _check(st)
     return Y
 
 
@@ -626,22 +661,23 @@ def layer_norm_backward(dY, X, gamma, mean, rstd, dX=None, dgamma=None, dbeta=No
     """dX (X's type, may be dY), and dgamma, dbeta (k fp32; replaced with
     overwrite, else added to) of layer_norm_forward; each may be None."""
     x_type = _dtype(X, "X")
-    ld_x, ld_dy = _norm_rows(X, X, "X"), _norm_rows(dY, X, "dY")
-    T, k = X.shape
-    dev = X.device
-    ld_dx = 0 if dX is None else _norm_rows(dX, X, "dX")
+    shape, dtype, dev = _norm_x(X)
+    T, k = shape
+    ld_x, ld_dy = _norm_rows(X, shape, dtype, dev, "X"), _norm_rows(dY, shape, dtype, dev, "dY")
+    ld_dx = 0 if dX is None else _norm_rows(dX, shape, dtype, dev, "dX")
     w_type = _norm_weights(gamma, None, k, dev)
     _vector(mean, T, torch.float32, dev, "mean")
     _vector(rstd, T, torch.float32, dev, "rstd")
     for t, name in ((dgamma, "dgamma"), (dbeta, "dbeta")):
         if t is not None:
             _vector(t, k, torch.float32, dev, name)
-    h, s = _stream_handle(stream, dev)
-    nbytes = workspace_bytes(OP_LAYER_NORM_BACKWARD, T, 0, k)
-    wsb = _workspace(nbytes, dev, s, ws)
-    _check(lib().sketch_layer_norm_backward(_ptr(dY), ld_dy, _ptr(X), x_type, T, k, ld_x, _ptr(gamma), w_type,
-                                            _ptr(mean), _ptr(rstd), _ptr(dX), ld_dx, _ptr(dgamma), _ptr(dbeta),
-                                            1 if overwrite else 0, _ptr(wsb), nbytes, h))
+    keep, ws_at, nbytes = _scratch(OP_LAYER_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
+    st = lib().sketch_layer_norm_backward(dY.data_ptr(), ld_dy, X.data_ptr(), x_type, T, k, ld_x, _addr(gamma),
+                                          w_type, mean.data_ptr(), rstd.data_ptr(), _addr(dX), ld_dx,
+                                          _addr(dgamma), _addr(dbeta), 1 if overwrite else 0, ws_at, nbytes,
+                                          _stream_of(stream, dev))
+    if st:
+        _check(st)
     return dX
 
 
@@ -669,11 +705,12 @@ def cross_entropy_forward(X, W, targets, loss, lse, scale=1.0, dev_status=None, 
     _vector(loss, T, torch.float32, dev, "loss")
     _vector(lse, T, torch.float32, dev, "lse")
     _status_word(dev_status, dev)
-    h, s = _stream_handle(stream, dev)
-    nbytes = workspace_bytes(OP_CROSS_ENTROPY_FORWARD, T, V)
-    wsb = _workspace(nbytes, dev, s, ws)
-    _check(lib().sketch_cross_entropy_forward(_ptr(X), T, k, ld_x, _ptr(W), V, ld_w, _ptr(targets), scale,
-                                              _ptr(loss), _ptr(lse), _ptr(dev_status), _ptr(wsb), nbytes, h))
+    keep, ws_at, nbytes = _scratch(OP_CROSS_ENTROPY_FORWARD, T, V, k, 0, dev, stream, ws)
+    st = lib().sketch_cross_entropy_forward(X.data_ptr(), T, k, ld_x, W.data_ptr(), V, ld_w, targets.data_ptr(), scale,
+                                            loss.data_ptr(), lse.data_ptr(), _addr(dev_status), ws_at, nbytes,
+                                            _stream_of(stream, dev))
+    if st:
+        _check(st)
     return loss
 
 
@@ -707,13 +744,13 @@ def cross_entropy_backward(X, W, targets, lse, g, dX=None, dW=None, XP=None, C=N
         r = C.shape[1]
         if C.dim() != 2 or C.shape[0] != V or XP.shape[0] != T or XP.shape[1] < r or C.device != dev or XP.device != dev:
             raise ValueError("shape or device mismatch: XP %s, C %s" % (tuple(XP.shape), tuple(C.shape)))
-    h, s = _stream_handle(stream, dev)
-    nbytes = workspace_bytes(OP_CROSS_ENTROPY_BACKWARD, T, V, k, r)
-    wsb = _workspace(nbytes, dev, s, ws)
-    _check(lib().sketch_cross_entropy_backward(_ptr(X), T, k, ld_x, _ptr(W), V, ld_w, _ptr(targets), scale,
-                                               _ptr(lse), _ptr(g), _ptr(dX), ld_dx, _ptr(dW), dw_type, ld_dw,
-                                               _ptr(XP), ld_xp, r, _ptr(C), 1 if overwrite else 0,
-                                               _ptr(dev_status), _ptr(wsb), nbytes, h))
+    keep, ws_at, nbytes = _scratch(OP_CROSS_ENTROPY_BACKWARD, T, V, k, r, dev, stream, ws)
+    st = lib().sketch_cross_entropy_backward(X.data_ptr(), T, k, ld_x, W.data_ptr(), V, ld_w, targets.data_ptr(),
+                                             scale, lse.data_ptr(), g.data_ptr(), _addr(dX), ld_dx, _addr(dW),
+                                             dw_type, ld_dw, _addr(XP), ld_xp, r, _addr(C), 1 if overwrite else 0,
+                                             _addr(dev_status), ws_at, nbytes, _stream_of(stream, dev))
+    if st:
+        _check(st)
     return dX
 
 
@@ -751,7 +788,8 @@ def adamw_problems(Ws, Gs, ms, vs, m_scales=None, v_scales=None, layers=None):
 
 def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=None, device=None, stream=None):
     """One AdamW step (counted from 0) of the tensors of adamw_problems."""
-    dev = device if device is not None else torch.cuda.current_device()
-    h, _ = _stream_handle(stream, dev)
-    _check(lib().sketch_adamw_batched(len(probs), probs, lr, betas[0], betas[1], eps, weight_decay,
-                                      _ptr(grad_scale), seed & 0xFFFFFFFFFFFFFFFF, step, h))
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    st = lib().sketch_adamw_batched(len(probs), probs, lr, betas[0], betas[1], eps, weight_decay, _addr(grad_scale),
+                                    seed & 0xFFFFFFFFFFFFFFFF, step, _stream_of(stream, dev))
+    if st:
+        _check(st)

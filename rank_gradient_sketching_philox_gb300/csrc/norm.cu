@@ -213,8 +213,10 @@ __device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N]
           if (src < m[i].base || src + bytes > m[i].end()) {  // whole 16 bytes inside the row, the rest singly
             const uint32_t lo = (ph + 15u) & ~15u, hi = (ph + m[i].width) & ~15u;
             if (turn == 0) {
-              for (uint32_t b = ph; b < ph + m[i].width; b += 2)
-                if (b < lo || b >= hi) tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
+              const uint32_t end = ph + m[i].width;
+              for (uint32_t b = ph; b < end && b < lo; b += 2) tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
+              for (uint32_t b = hi > lo ? hi : lo; b < end; b += 2)
+                tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
             }
             src += lo;
             at += lo;
