@@ -25,6 +25,11 @@
 // run over those alone, and what an ignored row of X holds, infinities or NaN
 // too, reaches no result.
 //
+// Tiles of different lengths share a launch, so pairs take them from a counter,
+// the longest kind first.  Where dX has too few tiles for the pairs, the
+// vocabulary of a tile is split over several, whose fp32 parts head_dx_sum_kernel
+// adds.
+//
 // Softmax statistics and every sum are fp32.  A tile's result is written by one
 // thread after a fixed-order accumulation, so results do not depend on timing.
 #include <cuda_bf16.h>
@@ -48,6 +53,7 @@ constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;                // four lane quarters x two column halves
 constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
 constexpr int kMaxProducts = 3;
+constexpr int kItemSlots = 16;               // tiles that the taker may be ahead of the slowest reader, and some
 constexpr int kGroupM = 8;                  // tile rows walked together, so that their operands stay in L2
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -63,6 +69,7 @@ struct Product {
   int b_row, b_k;
   int M, N, K;          // M or K is replaced by the number of kept rows where kept_m / kept_k says so
   int kept_m, kept_k;
+  int splits;           // parts of K, each a tile of its own (1 or more)
   int epi;
 };
 
@@ -70,6 +77,7 @@ struct HeadLaunch {
   Product p[kMaxProducts];
   int n;
   const int* kept;      // device: number of kept rows, null where all are
+  int* counter;         // device, 0: tiles taken beyond the pairs' first ones; null: every n-th tile
   int* err;
   int64_t T;
   // stats
@@ -85,8 +93,9 @@ struct HeadLaunch {
   int d_first;            // the vocabulary entry of D's first column
   // dx
   const int* row_of;      // the row of X that each kept row came from
-  float* acc;             // kept rows x k, fp32
-  int dx_first, dx_last;  // this is the vocabulary's first / last piece
+  float* acc;             // kept rows x k, fp32; of the piece's first part where K is split
+  int64_t acc_part;       // values of a part
+  int dx_first, dx_last;  // no value to add to / the sum is complete and goes to dX
   uint16_t* dX;
   int64_t ld_dx;
   // dw
@@ -106,18 +115,23 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 struct Tile {
-  int p, m, n;  // product, first row, first column
+  int p, m, n;        // product, first row, first column
+  int part, c0, c1;   // part of K and its chunks
 };
 
 struct TileOrder {
   int begin[kMaxProducts + 1];
   int m_tiles[kMaxProducts], n_tiles[kMaxProducts];
-  int kchunks[kMaxProducts];
+  int kchunks[kMaxProducts], splits[kMaxProducts];
   __device__ Tile at(int n_products, int item) const {
     Tile t;
     t.p = 0;
     while (t.p + 1 < n_products && begin[t.p + 1] <= item) ++t.p;
-    const int local = item - begin[t.p];
+    const int tiles = m_tiles[t.p] * n_tiles[t.p];
+    t.part = (item - begin[t.p]) / tiles;
+    t.c0 = (int)((int64_t)kchunks[t.p] * t.part / splits[t.p]);
+    t.c1 = (int)((int64_t)kchunks[t.p] * (t.part + 1) / splits[t.p]);
+    const int local = item - begin[t.p] - t.part * tiles;
     const int per_group = kGroupM * n_tiles[t.p];
     const int g = local / per_group, rem = local - g * per_group;
     const int left = m_tiles[t.p] - g * kGroupM;
@@ -137,6 +151,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[kStages];  // each CTA's: the stage may be refilled
   __shared__ __align__(8) uint64_t tfull_bar[2];        // each CTA's: an accumulator is complete
   __shared__ __align__(8) uint64_t tempty_bar[2];       // the even CTA's: both CTAs have read an accumulator
+  __shared__ __align__(8) uint64_t item_bar[kItemSlots];  // each CTA's: items[slot] is there
+  __shared__ volatile int items[kItemSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int issued, consumed;
@@ -159,7 +175,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       order.m_tiles[p] = ((pr.kept_m ? kept : pr.M) + kTile - 1) / kTile;
       order.n_tiles[p] = (pr.N + kTile - 1) / kTile;
       order.kchunks[p] = ((pr.kept_k ? kept : pr.K) + kChunk - 1) / kChunk;
-      order.begin[p + 1] = order.begin[p] + order.m_tiles[p] * order.n_tiles[p];
+      order.splits[p] = pr.splits;
+      order.begin[p + 1] = order.begin[p] + order.m_tiles[p] * order.n_tiles[p] * pr.splits;
     }
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&full_bar[s], 1);
@@ -169,6 +186,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       tc::mbar_init(&tfull_bar[b], 1);
       tc::mbar_init(&tempty_bar[b], 2 * kEpiWarps);
     }
+    for (int i = 0; i < kItemSlots; ++i) tc::mbar_init(&item_bar[i], 1);
     tc::fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
@@ -178,6 +196,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int n_items = order.begin[a.n];
+  // The pair's j-th tile, n_items when there is none.  The even CTA's producer
+  // takes tiles from the counter and passes each on to the other roles of both
+  // CTAs through a slot.  Nobody acknowledges a slot: the producer is at most
+  // kStages tiles ahead of the MMAs (each tile has a chunk), those two ahead of
+  // the slowest epilogue, and a slot comes round after kItemSlots.
+  auto item_of = [&](int j) -> int {
+    if (a.counter == nullptr) return pair + j * n_pairs;
+    if (j == 0) return pair;
+    const int slot = j & (kItemSlots - 1);
+    // slot 0 is first used for the tile after a round of slots
+    const uint32_t use = (uint32_t)(j / kItemSlots) - (slot ? 0u : 1u);
+    if (!tc::mbar_wait<true>(&item_bar[slot], use & 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) return n_items;
+    return items[slot];
+  };
 
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each operand ----
@@ -185,16 +217,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     // the copies: what a product needs is read once per tile (looked up for each
     // chunk it took 700 cycles a chunk, whose MMAs take 512).
     const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
+    const bool taker = a.counter != nullptr && rank == 0;
     int s = 0, it = 0;
     uint32_t ph = 0;
-    for (int item = pair; item < n_items; item += n_pairs) {
+    int item = pair;
+    for (int j = 0; item < n_items; ++j) {
+      // the next tile is asked for now and needed after this one's chunks
+      const int taken = taker ? atomicAdd(a.counter, 1) : 0;
       const Tile t = order.at(a.n, item);
       const Product& pr = a.p[t.p];
       const int a_mn = pr.a_mn, b_mn = pr.b_mn;
       const int ar = pr.a_row + t.m + kHalf * (int)rank, br = pr.b_row + t.n + kHalf * (int)rank;
       const CUtensorMap *tmA = &pr.tmA, *tmB = &pr.tmB;
-      int ak = pr.a_k, bk = pr.b_k;
-      const int end = it + order.kchunks[t.p];
+      int ak = pr.a_k + t.c0 * kChunk, bk = pr.b_k + t.c0 * kChunk;
+      const int end = it + t.c1 - t.c0;
       for (; it < end; ++it, ak += kChunk, bk += kChunk) {
         if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
         uint8_t* st = smem + s * kStageBytes;
@@ -218,6 +254,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         }
       }
       if (it < end) break;  // a wait gave up
+      if (taker) {
+        item = n_pairs + taken < n_items ? n_pairs + taken : n_items;
+        const int slot = (j + 1) & (kItemSlots - 1);
+        items[slot] = item;
+        const uint32_t there = tc::mapa_shared(tc::smem_u32(const_cast<int*>(&items[slot])), 1);
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(item) : "memory");
+        tc::mbar_arrive(&item_bar[slot]);
+        tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&item_bar[slot]), 1));
+      } else {
+        item = item_of(j + 1);
+      }
     }
     issued = it;
   } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -225,16 +272,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     int s = 0, it = 0, j = 0;
     uint32_t ph = 0;
     bool stop = false;
-    for (int item = pair; item < n_items && !stop; item += n_pairs, ++j) {
-      const int p = order.at(a.n, item).p;
+    for (int item = pair; item < n_items && !stop; item = item_of(++j)) {
+      const Tile t = order.at(a.n, item);
+      const int p = t.p;
       const bool a_mn = a.p[p].a_mn != 0, b_mn = a.p[p].b_mn != 0;
       const uint32_t idesc = tc::idesc_bf16(kTile, kTile, a_mn, b_mn);
       // a 16-wide K step: 32 bytes along a K-major swizzle row, 16 rows of 128 bytes of an MN-major tile
       const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
       const uint32_t a_lbo = a_mn ? 8192u : 16u, b_lbo = b_mn ? 8192u : 16u;
-      const int kchunks = order.kchunks[p];
+      const int kchunks = t.c1 - t.c0;
       const int b = j & 1;
-      if (j >= 2 && !tc::mbar_wait(&tempty_bar[b], ((j >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
+      if (j >= 2 && !tc::mbar_wait<true>(&tempty_bar[b], ((j >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
         break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * kTile);
@@ -266,7 +314,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     const int half = (warp - 2) >> 2;
     const int q = quarter * 32 + lane;
     int j = 0;
-    for (int item = pair; item < n_items; item += n_pairs, ++j) {
+    for (int item = pair; item < n_items; item = __shfl_sync(0xFFFFFFFFu, item_of(++j), 0)) {
       const Tile t = order.at(a.n, item);
       const Product& pr = a.p[t.p];
       const int b = j & 1;
@@ -338,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         }
       } else if (pr.epi == kEpiDx) {
         const bool in = row < *a.kept;
-        float* sum = a.acc + (int64_t)row * N + col0;
+        float* sum = a.acc + t.part * a.acc_part + (int64_t)row * N + col0;
         uint16_t* out = (in && a.dx_last) ? a.dX + (int64_t)a.row_of[row] * a.ld_dx + col0 : nullptr;
         for (int cg = 0; cg < kHalf / 32; ++cg) {
           tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
@@ -520,6 +568,8 @@ struct Gather {
   int* target;
   int* row_of;
   int* kept;
+  int* counters;  // n_counters of them, set to 0
+  int n_counters;
   uint16_t* dX;  // nullable
   int64_t ld_dx;
   int64_t rows;  // compact rows the buffers hold
@@ -551,6 +601,9 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
   }
   __syncthreads();
   total = total_s;
+  if (blockIdx.x == 0) {
+    for (int i = threadIdx.x; i < a.n_counters; i += blockDim.x) a.counters[i] = 0;
+  }
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *a.kept = total;
     if (a.status) *a.status = bad_s ? SKETCH_DEV_BAD_TARGET : 0;
@@ -591,6 +644,27 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
   }
 }
 
+// dX's kept rows from their `parts` fp32 parts, eight columns per thread.
+__global__ void __launch_bounds__(256) head_dx_sum_kernel(const float* acc, int64_t part, int parts, int64_t k,
+                                                          const int* kept, const int* row_of, uint16_t* dX,
+                                                          int64_t ld_dx) {
+  const int64_t per_row = k / 8, n = *kept * per_row;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t row = i / per_row, c = (i - row * per_row) * 8;
+    const float4* p = reinterpret_cast<const float4*>(acc + row * k + c);
+    float4 x = p[0], y = p[1];
+#pragma unroll 4
+    for (int q = 1; q < parts; ++q) {
+      const float4* r = reinterpret_cast<const float4*>(acc + q * part + row * k + c);
+      const float4 u = r[0], v = r[1];
+      x.x += u.x; x.y += u.y; x.z += u.z; x.w += u.w;
+      y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+    }
+    *reinterpret_cast<uint4*>(dX + (int64_t)row_of[row] * ld_dx + c) =
+        make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  }
+}
+
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
 // Vocabulary entries per piece: as many whole tiles as 256 MB of BF16 logit
@@ -601,6 +675,17 @@ int64_t piece_width(int64_t T, int64_t V) {
   if (w < 4 * kTile) w = 4 * kTile;
   const int64_t all = round_up(V, kTile);
   return w < all ? w : all;
+}
+
+// Parts that a dX tile's sum over a piece's vocabulary is split into: as many as
+// give every pair a tile, of 16 chunks (1024 entries) at least.  (T = 1000, k =
+// 2048, V = 32771: 32 tiles of 513 chunks, beside 1032 tiles of dW of 16.)
+int dx_parts(int64_t T, int64_t V, int64_t k) {
+  const int64_t tiles = ceil_div(T, kTile) * ceil_div(k, kTile), pairs = num_sms() / 2;
+  const int64_t chunks = ceil_div(piece_width(T, V) < V ? piece_width(T, V) : V, kChunk);
+  int parts = 1;
+  while (tiles * parts * 2 <= pairs && chunks / (parts * 2) >= 16) parts *= 2;
+  return parts;
 }
 
 constexpr size_t kHeadSmem = (size_t)kStages * kStageBytes + 1024;
@@ -639,7 +724,7 @@ cudaError_t head_pairs(int* out) {
 
 cudaError_t launch_products(const HeadLaunch& a, cudaStream_t stream) {
   int64_t items = 0;
-  for (int p = 0; p < a.n; ++p) items += ceil_div(a.p[p].M, kTile) * ceil_div(a.p[p].N, kTile);
+  for (int p = 0; p < a.n; ++p) items += ceil_div(a.p[p].M, kTile) * ceil_div(a.p[p].N, kTile) * a.p[p].splits;
   if (items > (int64_t(1) << 30)) return cudaErrorInvalidValue;
   int pairs = 0;
   cudaError_t err = head_pairs(&pairs);
@@ -669,24 +754,29 @@ struct BackwardWorkspace {
   int* target;
   int* row_of;
   int* kept;
+  int* counters;
+  int parts;  // of dX's sum over a piece
   size_t bytes;
 };
 BackwardWorkspace carve_backward(void* base, int64_t T, int64_t V, int64_t k, int64_t r) {
   WsCursor cur;
   cur.base = static_cast<char*>(base);
   const int64_t rows = round_up(T, kTile), piece = piece_width(T, V);
-  const bool pieces = piece < V;
+  const int64_t pieces = ceil_div(V, piece);
   BackwardWorkspace w;
+  w.parts = dx_parts(T, V, k);
   w.Xc = cur.take<uint16_t>((size_t)(rows * k));
   w.ld_xpc = round_up(r, 8);
   w.XPc = cur.take<uint16_t>((size_t)(rows * w.ld_xpc));
-  for (int i = 0; i < 2; ++i) w.D[i] = cur.take<uint16_t>((size_t)((i == 0 || pieces) ? rows * piece : 0));
-  w.acc = cur.take<float>((size_t)(pieces ? rows * k : 0));
+  for (int i = 0; i < 2; ++i) w.D[i] = cur.take<uint16_t>((size_t)((i == 0 || pieces > 1) ? rows * piece : 0));
+  // split sums keep a part per piece and split, others are added up over the pieces
+  w.acc = cur.take<float>((size_t)(w.parts > 1 ? pieces * w.parts * rows * k : pieces > 1 ? rows * k : 0));
   w.lse_log2 = cur.take<float>((size_t)rows);
   w.weight = cur.take<float>((size_t)rows);
   w.target = cur.take<int>((size_t)rows);
   w.row_of = cur.take<int>((size_t)rows);
   w.kept = cur.take<int>(1);
+  w.counters = cur.take<int>((size_t)(pieces + 1));
   cur.take<char>(0);
   w.bytes = cur.offset;
   return w;
@@ -718,6 +808,7 @@ cudaError_t launch_head_forward(const HeadForward& f, void* ws, cudaStream_t str
   p.N = (int)f.V;
   p.K = (int)f.k;
   p.epi = kEpiStats;
+  p.splits = 1;
   err = k_major(&p.tmA, f.X, f.T, f.k, f.ld_x);
   if (err == cudaSuccess) err = k_major(&p.tmB, f.W, f.V, f.k, f.ld_w);
   if (err == cudaSuccess) err = launch_products(a, stream);
@@ -746,6 +837,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   g.Xc = w.Xc; g.XPc = w.XPc; g.ld_xpc = w.ld_xpc;
   g.lse_log2 = w.lse_log2; g.weight = w.weight; g.target = w.target; g.row_of = w.row_of; g.kept = w.kept;
   g.dX = f.dX; g.ld_dx = f.ld_dx;
+  g.counters = w.counters; g.n_counters = pieces + 1;
   g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
   count_launch();
   head_gather_kernel<<<(unsigned)(rows / 8), 256, 0, stream>>>(g);
@@ -763,14 +855,15 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   a.target = w.target;
   a.row_of = w.row_of;
   a.ld_d = piece;
-  a.acc = w.acc;
   a.dX = f.dX;
   a.ld_dx = f.ld_dx;
   a.ld_dw = f.ld_dw;
   a.dw_mode = f.dw_type == SKETCH_BF16 ? 0 : f.overwrite ? 1 : 2;
+  int dx_sum_parts = 0;
   // step i: dX and dW of piece i - 1, and D of piece i
   for (int i = 0; i <= pieces; ++i) {
     a.n = 0;
+    a.counter = w.counters + i;
     if (i > 0) {
       const int64_t v0 = (i - 1) * piece, width = f.V - v0 < piece ? f.V - v0 : piece;
       const uint16_t* D = w.D[(i - 1) & 1];
@@ -787,8 +880,12 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
         p.N = (int)f.k;
         p.K = (int)width;
         p.epi = kEpiDx;
-        a.dx_first = i == 1;
-        a.dx_last = i == pieces;
+        p.splits = w.parts < ceil_div(width, kChunk) ? w.parts : (int)ceil_div(width, kChunk);  // a chunk each at least
+        dx_sum_parts += p.splits;
+        a.acc = w.acc + (w.parts > 1 ? (i - 1) * w.parts * rows * f.k : 0);
+        a.acc_part = rows * f.k;
+        a.dx_first = i == 1 || w.parts > 1;
+        a.dx_last = i == pieces && w.parts == 1;
       }
       if (f.dW) {
         Product& p = a.p[a.n++];
@@ -802,6 +899,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
         p.K = (int)f.T;
         p.kept_k = 1;
         p.epi = kEpiDw;
+        p.splits = 1;
         const size_t size = f.dw_type == SKETCH_BF16 ? 2 : 4;
         a.dW = static_cast<char*>(f.dW) + (size_t)(v0 * f.ld_dw) * size;
       }
@@ -824,6 +922,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
       p.N = (int)width;
       p.K = (int)f.k;
       p.epi = kEpiDlogit;
+      p.splits = 1;
       a.D = w.D[i & 1];
       a.d_first = (int)v0;
     }
@@ -831,6 +930,13 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
       err = launch_products(a, stream);
       if (err != cudaSuccess) return err;
     }
+  }
+  if (f.dX && w.parts > 1) {
+    const int64_t blocks = ceil_div(f.T * (f.k / 8), 256), most = 8 * (int64_t)num_sms();
+    count_launch();
+    head_dx_sum_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(
+        w.acc, rows * f.k, dx_sum_parts, f.k, w.kept, w.row_of, f.dX, f.ld_dx);
+    return cudaGetLastError();
   }
   return cudaSuccess;
 }
