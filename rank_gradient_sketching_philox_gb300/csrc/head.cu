@@ -51,9 +51,10 @@ constexpr uint32_t kOperandBytes = kHalf * kChunk * 2;
 constexpr uint32_t kStageBytes = 2 * kOperandBytes;
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;                // four lane quarters x two column halves
-constexpr int kHeadThreads = 64 + 32 * kEpiWarps;
+constexpr int kHeadThreads = 64 + 32 * kEpiWarps + 32;  // copies, MMAs, epilogue, tiles
 constexpr int kMaxProducts = 3;
-constexpr int kItemSlots = 16;               // tiles that the taker may be ahead of the slowest reader, and some
+constexpr int kTileSlots = 4;                // tiles handed out ahead of the slowest reader
+constexpr int kTileReaders = 2 * (1 + kEpiWarps) + 1;  // both CTAs' copies and epilogues, the MMAs
 constexpr int kGroupM = 8;                  // tile rows walked together, so that their operands stay in L2
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -115,22 +116,26 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 struct Tile {
-  int p, m, n;        // product, first row, first column
-  int part, c0, c1;   // part of K and its chunks
+  int p, m, n;              // product (-1: no more tiles), first row, first column
+  int part;                 // of a split K
+  int a_row, a_k, b_row, b_k;  // the even CTA's first coordinates
+  int chunks;
+  int a_mn, b_mn;
+  int pad;
 };
 
 struct TileOrder {
   int begin[kMaxProducts + 1];
   int m_tiles[kMaxProducts], n_tiles[kMaxProducts];
   int kchunks[kMaxProducts], splits[kMaxProducts];
-  __device__ Tile at(int n_products, int item) const {
+  __device__ Tile at(const HeadLaunch& a, int item) const {
     Tile t;
     t.p = 0;
-    while (t.p + 1 < n_products && begin[t.p + 1] <= item) ++t.p;
+    while (t.p + 1 < a.n && begin[t.p + 1] <= item) ++t.p;
     const int tiles = m_tiles[t.p] * n_tiles[t.p];
     t.part = (item - begin[t.p]) / tiles;
-    t.c0 = (int)((int64_t)kchunks[t.p] * t.part / splits[t.p]);
-    t.c1 = (int)((int64_t)kchunks[t.p] * (t.part + 1) / splits[t.p]);
+    const int c0 = (int)((int64_t)kchunks[t.p] * t.part / splits[t.p]);
+    t.chunks = (int)((int64_t)kchunks[t.p] * (t.part + 1) / splits[t.p]) - c0;
     const int local = item - begin[t.p] - t.part * tiles;
     const int per_group = kGroupM * n_tiles[t.p];
     const int g = local / per_group, rem = local - g * per_group;
@@ -139,6 +144,14 @@ struct TileOrder {
     t.n = rem / gm;
     t.m = (g * kGroupM + (rem - t.n * gm)) * kTile;
     t.n *= kTile;
+    const Product& pr = a.p[t.p];
+    t.a_row = pr.a_row + t.m;
+    t.b_row = pr.b_row + t.n;
+    t.a_k = pr.a_k + c0 * kChunk;
+    t.b_k = pr.b_k + c0 * kChunk;
+    t.a_mn = pr.a_mn;
+    t.b_mn = pr.b_mn;
+    t.pad = 0;
     return t;
   }
 };
@@ -151,8 +164,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[kStages];  // each CTA's: the stage may be refilled
   __shared__ __align__(8) uint64_t tfull_bar[2];        // each CTA's: an accumulator is complete
   __shared__ __align__(8) uint64_t tempty_bar[2];       // the even CTA's: both CTAs have read an accumulator
-  __shared__ __align__(8) uint64_t item_bar[kItemSlots];  // each CTA's: items[slot] is there
-  __shared__ volatile int items[kItemSlots];
+  __shared__ __align__(8) uint64_t tile_bar[kTileSlots];  // each CTA's: tiles[slot] is there
+  __shared__ __align__(8) uint64_t read_bar[kTileSlots];  // the even CTA's: every role of both CTAs has read it
+  __shared__ __align__(16) Tile tiles[kTileSlots];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int issued, consumed;
@@ -186,7 +200,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       tc::mbar_init(&tfull_bar[b], 1);
       tc::mbar_init(&tempty_bar[b], 2 * kEpiWarps);
     }
-    for (int i = 0; i < kItemSlots; ++i) tc::mbar_init(&item_bar[i], 1);
+    for (int i = 0; i < kTileSlots; ++i) {
+      tc::mbar_init(&tile_bar[i], 1);
+      tc::mbar_init(&read_bar[i], kTileReaders);
+    }
     tc::fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
@@ -196,19 +213,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const int n_items = order.begin[a.n];
-  // The pair's j-th tile, n_items when there is none.  The even CTA's producer
-  // takes tiles from the counter and passes each on to the other roles of both
-  // CTAs through a slot.  Nobody acknowledges a slot: the producer is at most
-  // kStages tiles ahead of the MMAs (each tile has a chunk), those two ahead of
-  // the slowest epilogue, and a slot comes round after kItemSlots.
-  auto item_of = [&](int j) -> int {
-    if (a.counter == nullptr) return pair + j * n_pairs;
-    if (j == 0) return pair;
-    const int slot = j & (kItemSlots - 1);
-    // slot 0 is first used for the tile after a round of slots
-    const uint32_t use = (uint32_t)(j / kItemSlots) - (slot ? 0u : 1u);
-    if (!tc::mbar_wait<true>(&item_bar[slot], use & 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) return n_items;
-    return items[slot];
+  // The pair's j-th tile.  The even CTA's tile warp works tiles out ahead and
+  // hands them to the other roles of both CTAs through slots (worked out by each
+  // role itself, between one tile's chunks and the next one's, it held the copies
+  // and the MMAs up by some 4000 cycles a tile).  A thread that has read a slot
+  // says so, one per warp.
+  auto next_tile = [&](int j) -> Tile {
+    const int slot = j & (kTileSlots - 1);
+    Tile t;
+    t.p = -1;
+    if (tc::mbar_wait<true>(&tile_bar[slot], (uint32_t)(j / kTileSlots) & 1u, &abort_flag, a.err, tc::kErrTimeoutStage))
+      t = tiles[slot];
+    return t;
+  };
+  auto tile_read = [&](int j) {
+    tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&read_bar[j & (kTileSlots - 1)]), 0));
   };
 
   if (warp == 0 && lane == 0) {
@@ -217,32 +236,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     // the copies: what a product needs is read once per tile (looked up for each
     // chunk it took 700 cycles a chunk, whose MMAs take 512).
     const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
-    const bool taker = a.counter != nullptr && rank == 0;
     int s = 0, it = 0;
     uint32_t ph = 0;
-    int item = pair;
-    for (int j = 0; item < n_items; ++j) {
-      // the next tile is asked for now and needed after this one's chunks
-      const int taken = taker ? atomicAdd(a.counter, 1) : 0;
-      const Tile t = order.at(a.n, item);
-      const Product& pr = a.p[t.p];
-      const int a_mn = pr.a_mn, b_mn = pr.b_mn;
-      const int ar = pr.a_row + t.m + kHalf * (int)rank, br = pr.b_row + t.n + kHalf * (int)rank;
-      const CUtensorMap *tmA = &pr.tmA, *tmB = &pr.tmB;
-      int ak = pr.a_k + t.c0 * kChunk, bk = pr.b_k + t.c0 * kChunk;
-      const int end = it + t.c1 - t.c0;
+    for (int j = 0;; ++j) {
+      const Tile t = next_tile(j);
+      if (t.p < 0) break;
+      tile_read(j);
+      const CUtensorMap *tmA = &a.p[t.p].tmA, *tmB = &a.p[t.p].tmB;
+      const int ar = t.a_row + kHalf * (int)rank, br = t.b_row + kHalf * (int)rank;
+      int ak = t.a_k, bk = t.b_k;
+      const int end = it + t.chunks;
       for (; it < end; ++it, ak += kChunk, bk += kChunk) {
         if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
         uint8_t* st = smem + s * kStageBytes;
         if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], 2 * kStageBytes);
         const uint32_t bar = full0 + 8u * s;
-        if (a_mn) {  // two boxes of [64 k][64 rows]
+        if (t.a_mn) {  // two boxes of [64 k][64 rows]
           tc::tma_load_2d_pair(st, tmA, bar, ar, ak);
           tc::tma_load_2d_pair(st + kOperandBytes / 2, tmA, bar, ar + 64, ak);
         } else {  // one box of [128 rows][64 k]
           tc::tma_load_2d_pair(st, tmA, bar, ak, ar);
         }
-        if (b_mn) {
+        if (t.b_mn) {
           tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, br, bk);
           tc::tma_load_2d_pair(st + kOperandBytes + kOperandBytes / 2, tmB, bar, br + 64, bk);
         } else {
@@ -254,17 +269,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         }
       }
       if (it < end) break;  // a wait gave up
-      if (taker) {
-        item = n_pairs + taken < n_items ? n_pairs + taken : n_items;
-        const int slot = (j + 1) & (kItemSlots - 1);
-        items[slot] = item;
-        const uint32_t there = tc::mapa_shared(tc::smem_u32(const_cast<int*>(&items[slot])), 1);
-        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(there), "r"(item) : "memory");
-        tc::mbar_arrive(&item_bar[slot]);
-        tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&item_bar[slot]), 1));
-      } else {
-        item = item_of(j + 1);
-      }
     }
     issued = it;
   } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -272,15 +276,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     int s = 0, it = 0, j = 0;
     uint32_t ph = 0;
     bool stop = false;
-    for (int item = pair; item < n_items && !stop; item = item_of(++j)) {
-      const Tile t = order.at(a.n, item);
-      const int p = t.p;
-      const bool a_mn = a.p[p].a_mn != 0, b_mn = a.p[p].b_mn != 0;
+    for (; !stop; ++j) {
+      const Tile t = next_tile(j);
+      if (t.p < 0) break;
+      tile_read(j);
+      const bool a_mn = t.a_mn != 0, b_mn = t.b_mn != 0;
       const uint32_t idesc = tc::idesc_bf16(kTile, kTile, a_mn, b_mn);
       // a 16-wide K step: 32 bytes along a K-major swizzle row, 16 rows of 128 bytes of an MN-major tile
       const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
       const uint32_t a_lbo = a_mn ? 8192u : 16u, b_lbo = b_mn ? 8192u : 16u;
-      const int kchunks = t.c1 - t.c0;
       const int b = j & 1;
       if (j >= 2 && !tc::mbar_wait<true>(&tempty_bar[b], ((j >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
         break;
@@ -288,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       const uint32_t acc = tmem + (uint32_t)(b * kTile);
       const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), a_lbo, 1024);
       const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kOperandBytes, b_lbo, 1024);
-      for (int c = 0; c < kchunks; ++c, ++it) {
+      for (int c = 0; c < t.chunks; ++c, ++it) {
         if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) {
           stop = true;
           break;
@@ -308,14 +312,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       if (!stop) tc::mma_commit_pair(&tfull_bar[b]);
     }
     consumed = it;
+  } else if (warp == 2 + kEpiWarps) {
+    // ---- tiles: every n-th, or as a counter deals them out ----
+    if (lane == 0 && rank == 0) {
+      int item = pair;
+      for (int j = 0;; ++j) {
+        const int slot = j & (kTileSlots - 1);
+        if (j >= kTileSlots && !tc::mbar_wait<true>(&read_bar[slot], (uint32_t)(j / kTileSlots - 1) & 1u, &abort_flag,
+                                                    a.err, tc::kErrTimeoutStage))
+          break;
+        Tile t = {};
+        t.p = -1;
+        if (item < n_items) t = order.at(a, item);
+        tiles[slot] = t;
+        const uint32_t there = tc::mapa_shared(tc::smem_u32(&tiles[slot]), 1);
+        const int4* q = reinterpret_cast<const int4*>(&tiles[slot]);
+#pragma unroll
+        for (int i = 0; i < (int)(sizeof(Tile) / 16); ++i) {
+          const int4 v = q[i];
+          asm volatile("st.shared::cluster.v4.s32 [%0], {%1, %2, %3, %4};" ::"r"(there + 16 * i), "r"(v.x), "r"(v.y),
+                       "r"(v.z), "r"(v.w)
+                       : "memory");
+        }
+        tc::mbar_arrive(&tile_bar[slot]);
+        tc::mbar_arrive_cluster(tc::mapa_shared(tc::smem_u32(&tile_bar[slot]), 1));
+        if (item >= n_items) break;
+        item = a.counter ? n_pairs + atomicAdd(a.counter, 1) : item + n_pairs;
+      }
+    }
   } else if (warp >= 2) {
     // ---- epilogue: one row per thread, half of the tile's columns ----
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
     const int half = (warp - 2) >> 2;
     const int q = quarter * 32 + lane;
     int j = 0;
-    for (int item = pair; item < n_items; item = __shfl_sync(0xFFFFFFFFu, item_of(++j), 0)) {
-      const Tile t = order.at(a.n, item);
+    for (;; ++j) {
+      const Tile t = next_tile(j);
+      if (!__all_sync(0xFFFFFFFFu, t.p >= 0)) break;
+      if (lane == 0) tile_read(j);
       const Product& pr = a.p[t.p];
       const int b = j & 1;
       const int row = t.m + kHalf * (int)rank + q;
