@@ -71,6 +71,7 @@ struct Product {
   int M, N, K;          // M or K is replaced by the number of kept rows where kept_m / kept_k says so
   int kept_m, kept_k;
   int splits;           // parts of K, each a tile of its own (1 or more)
+  int a_box;            // rows of K-major A that the even CTA loads; where M <= 128 fewer than 128, and the odd CTA none
   int epi;
 };
 
@@ -121,7 +122,7 @@ struct Tile {
   int a_row, a_k, b_row, b_k;  // the even CTA's first coordinates
   int chunks;
   int a_mn, b_mn;
-  int pad;
+  int a_box;
 };
 
 struct TileOrder {
@@ -151,7 +152,7 @@ struct TileOrder {
     t.b_k = pr.b_k + c0 * kChunk;
     t.a_mn = pr.a_mn;
     t.b_mn = pr.b_mn;
-    t.pad = 0;
+    t.a_box = pr.a_box;
     return t;
   }
 };
@@ -180,18 +181,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     abort_flag = 0;
     issued = 0;
     consumed = 0;
-    // with no kept row at all one tile of zero rows still runs, so that dW is written
-    int kept = a.kept ? *a.kept : 0;
-    if (kept < 1) kept = 1;
-    order.begin[0] = 0;
-    for (int p = 0; p < a.n; ++p) {
-      const Product& pr = a.p[p];
-      order.m_tiles[p] = ((pr.kept_m ? kept : pr.M) + kTile - 1) / kTile;
-      order.n_tiles[p] = (pr.N + kTile - 1) / kTile;
-      order.kchunks[p] = ((pr.kept_k ? kept : pr.K) + kChunk - 1) / kChunk;
-      order.splits[p] = pr.splits;
-      order.begin[p + 1] = order.begin[p] + order.m_tiles[p] * order.n_tiles[p] * pr.splits;
-    }
     for (int s = 0; s < kStages; ++s) {
       tc::mbar_init(&full_bar[s], 1);
       tc::mbar_init(&empty_bar[s], 1);
@@ -207,6 +196,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     tc::fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
+  // the kernel after this one may come up as this one's blocks leave, and this
+  // one has come up while the one before it ends: now its results are needed
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  if (threadIdx.x == 0) {
+    // with no kept row at all one tile of zero rows still runs, so that dW is written
+    int kept = a.kept ? *a.kept : 0;
+    if (kept < 1) kept = 1;
+    order.begin[0] = 0;
+    for (int p = 0; p < a.n; ++p) {
+      const Product& pr = a.p[p];
+      order.m_tiles[p] = ((pr.kept_m ? kept : pr.M) + kTile - 1) / kTile;
+      order.n_tiles[p] = (pr.N + kTile - 1) / kTile;
+      order.kchunks[p] = ((pr.kept_k ? kept : pr.K) + kChunk - 1) / kChunk;
+      order.splits[p] = pr.splits;
+      order.begin[p + 1] = order.begin[p] + order.m_tiles[p] * order.n_tiles[p] * pr.splits;
+    }
+  }
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();  // both CTAs' barriers exist before either signals one
@@ -245,13 +252,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       const CUtensorMap *tmA = &a.p[t.p].tmA, *tmB = &a.p[t.p].tmB;
       const int ar = t.a_row + kHalf * (int)rank, br = t.b_row + kHalf * (int)rank;
       int ak = t.a_k, bk = t.b_k;
+      // few rows: the rest of A's tile keeps what it holds, which reaches only
+      // rows of the product that are not kept
+      const bool load_a = rank == 0 || t.a_box == kHalf;
+      const uint32_t bytes = kOperandBytes * 2 + (t.a_box == kHalf ? 2 * kOperandBytes : (uint32_t)t.a_box * kChunk * 2);
       const int end = it + t.chunks;
       for (; it < end; ++it, ak += kChunk, bk += kChunk) {
         if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
         uint8_t* st = smem + s * kStageBytes;
-        if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], 2 * kStageBytes);
+        if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], bytes);
         const uint32_t bar = full0 + 8u * s;
-        if (t.a_mn) {  // two boxes of [64 k][64 rows]
+        if (!load_a) {
+        } else if (t.a_mn) {  // two boxes of [64 k][64 rows]
           tc::tma_load_2d_pair(st, tmA, bar, ar, ak);
           tc::tma_load_2d_pair(st + kOperandBytes / 2, tmA, bar, ar + 64, ak);
         } else {  // one box of [128 rows][64 k]
@@ -523,6 +535,7 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
                                                            const int64_t* targets, float scale_log2, int64_t T,
                                                            int64_t V, int blocks, float* loss, float* lse,
                                                            int32_t* status) {
+  cudaGridDependencySynchronize();
   __shared__ float2 part[32][kCombineRows];
   __shared__ float hit[kCombineRows];
   __shared__ int bad;
@@ -612,6 +625,8 @@ struct Gather {
 };
 
 __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ Gather a) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   __shared__ int before_s, total_s, bad_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t base = (int64_t)blockIdx.x * 8;
@@ -682,6 +697,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
 __global__ void __launch_bounds__(256) head_dx_sum_kernel(const float* acc, int64_t part, int parts, int64_t k,
                                                           const int* kept, const int* row_of, uint16_t* dX,
                                                           int64_t ld_dx) {
+  cudaGridDependencySynchronize();
   const int64_t per_row = k / 8, n = *kept * per_row;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i / per_row, c = (i - row * per_row) * 8;
@@ -756,6 +772,25 @@ cudaError_t head_pairs(int* out) {
   return cudaSuccess;
 }
 
+// A launch whose blocks may come up while the kernel before it in the stream ends
+// (each kernel here waits for that one's results itself).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(void (*kernel)(Params...), unsigned blocks, unsigned threads, size_t smem, cudaStream_t stream,
+                         const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+}
+
 cudaError_t launch_products(const HeadLaunch& a, cudaStream_t stream) {
   int64_t items = 0;
   for (int p = 0; p < a.n; ++p) items += ceil_div(a.p[p].M, kTile) * ceil_div(a.p[p].N, kTile) * a.p[p].splits;
@@ -764,15 +799,15 @@ cudaError_t launch_products(const HeadLaunch& a, cudaStream_t stream) {
   cudaError_t err = head_pairs(&pairs);
   if (err != cudaSuccess) return err;
   if (items < pairs) pairs = (int)items;
-  count_launch();
-  head_gemm_kernel<<<2 * pairs, kHeadThreads, kHeadSmem, stream>>>(a);
-  return cudaGetLastError();
+  return launch_after(head_gemm_kernel, 2 * (unsigned)pairs, kHeadThreads, kHeadSmem, stream, a);
 }
 
 // Operand rows x K, K contiguous (box 64 x 128), or K x rows, rows contiguous (box 64 x 64).
-cudaError_t k_major(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t K, int64_t ld) {
-  return encode_tmap_bf16_2d(map, p, (uint64_t)K, (uint64_t)rows, (uint64_t)ld * 2, kChunk, kHalf);
+cudaError_t k_major(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t K, int64_t ld, int box = kHalf) {
+  return encode_tmap_bf16_2d(map, p, (uint64_t)K, (uint64_t)rows, (uint64_t)ld * 2, kChunk, (uint32_t)box);
 }
+// Rows of a K-major A of M rows that a tile's even CTA loads.
+int a_box(int64_t M) { return M <= kHalf ? (int)((M + 7) / 8 * 8) : kHalf; }
 cudaError_t mn_major(CUtensorMap* map, const uint16_t* p, int64_t rows, int64_t K, int64_t ld) {
   return encode_tmap_bf16_2d(map, p, (uint64_t)rows, (uint64_t)K, (uint64_t)ld * 2, 64, kChunk);
 }
@@ -843,15 +878,13 @@ cudaError_t launch_head_forward(const HeadForward& f, void* ws, cudaStream_t str
   p.K = (int)f.k;
   p.epi = kEpiStats;
   p.splits = 1;
-  err = k_major(&p.tmA, f.X, f.T, f.k, f.ld_x);
+  p.a_box = a_box(f.T);
+  err = k_major(&p.tmA, f.X, f.T, f.k, f.ld_x, p.a_box);
   if (err == cudaSuccess) err = k_major(&p.tmB, f.W, f.V, f.k, f.ld_w);
   if (err == cudaSuccess) err = launch_products(a, stream);
   if (err != cudaSuccess) return err;
-  count_launch();
-  head_combine_kernel<<<(unsigned)ceil_div(f.T, kCombineRows), 256, 0, stream>>>(
-      a.partials, f.X, f.ld_x, f.W, f.ld_w, f.k, f.targets, a.scale_log2, f.T, f.V, blocks, f.loss, f.lse,
-      f.dev_status);
-  return cudaGetLastError();
+  return launch_after(head_combine_kernel, (unsigned)ceil_div(f.T, kCombineRows), 256, 0, stream, a.partials, f.X,
+                      f.ld_x, f.W, f.ld_w, f.k, f.targets, a.scale_log2, f.T, f.V, blocks, f.loss, f.lse, f.dev_status);
 }
 
 size_t head_backward_workspace_bytes(int64_t T, int64_t V, int64_t k, int64_t r) {
@@ -873,9 +906,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   g.dX = f.dX; g.ld_dx = f.ld_dx;
   g.counters = w.counters; g.n_counters = pieces + 1;
   g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
-  count_launch();
-  head_gather_kernel<<<(unsigned)(rows / 8), 256, 0, stream>>>(g);
-  cudaError_t err = cudaGetLastError();
+  cudaError_t err = launch_after(head_gather_kernel, (unsigned)(rows / 8), 256, 0, stream, g);
   if (err != cudaSuccess) return err;
 
   HeadLaunch a = {};
@@ -904,7 +935,8 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
       if (f.dX) {
         Product& p = a.p[a.n++];
         p = Product{};
-        err = k_major(&p.tmA, D, rows, width, piece);
+        p.a_box = a_box(f.T);
+        err = k_major(&p.tmA, D, rows, width, piece, p.a_box);
         if (err == cudaSuccess) err = mn_major(&p.tmB, f.W, f.k, f.V, f.ld_w);
         if (err != cudaSuccess) return err;
         p.b_mn = 1;
@@ -924,6 +956,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
       if (f.dW) {
         Product& p = a.p[a.n++];
         p = Product{};
+        p.a_box = kHalf;
         err = mn_major(&p.tmA, D, width, rows, piece);
         if (err == cudaSuccess) err = mn_major(&p.tmB, w.Xc, f.k, rows, f.k);
         if (err != cudaSuccess) return err;
@@ -947,7 +980,8 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
       const int64_t v0 = i * piece, width = f.V - v0 < piece ? f.V - v0 : piece;
       Product& p = a.p[a.n++];
       p = Product{};
-      err = k_major(&p.tmA, w.Xc, rows, f.k, f.k);
+      p.a_box = a_box(sketch ? rows : f.T);
+      err = k_major(&p.tmA, w.Xc, rows, f.k, f.k, p.a_box);
       if (err == cudaSuccess) err = k_major(&p.tmB, f.W, f.V, f.k, f.ld_w);
       if (err != cudaSuccess) return err;
       p.b_row = (int)v0;
@@ -967,10 +1001,8 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   }
   if (f.dX && w.parts > 1) {
     const int64_t blocks = ceil_div(f.T * (f.k / 8), 256), most = 8 * (int64_t)num_sms();
-    count_launch();
-    head_dx_sum_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(
-        w.acc, rows * f.k, dx_sum_parts, f.k, w.kept, w.row_of, f.dX, f.ld_dx);
-    return cudaGetLastError();
+    return launch_after(head_dx_sum_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, w.acc,
+                        rows * f.k, dx_sum_parts, f.k, w.kept, w.row_of, f.dX, f.ld_dx);
   }
   return cudaSuccess;
 }
