@@ -16,6 +16,13 @@
 // none fused: a code that a last bit decides is the same on any fp32 machine
 // (a state that differs by a code is a step apart ever after).  A value that is not finite gets the code NaN and takes no
 // part in its block's scale.
+//
+// A thread works on eight values at a time, one Philox block for each stream; a
+// warp's 256 values are one block of an 8-bit state.  fp32 states are bound by HBM
+// (268M BF16 weights: 855 us, 1.02 of the copy rate over 22 bytes a value); 8-bit
+// states by instruction issue: 68 instructions a value, 15 of them the three
+// Philox streams, against the 55 that the 10 bytes' time would allow at a full
+// issue rate (638 us, 0.62 of the copy rate).  Arithmetic goes in packed pairs.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
@@ -109,18 +116,27 @@ __device__ __forceinline__ void store_codes(void* base, int64_t e, int64_t n, ui
   for (int i = 0; e + i < n; ++i) c[i] = (uint8_t)(r >> (8 * i));
 }
 
+constexpr int kPairs = kUnit / 2;
 template <bool F32>
-__device__ __forceinline__ void unpack(const uint4* v, float (&f)[kUnit]) {
+__device__ __forceinline__ void unpack(const uint4* v, Pair (&f)[kPairs]) {
   const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i)
-    f[i] = F32 ? __uint_as_float(r[i]) : __uint_as_float((i & 1) ? r[i >> 1] & 0xFFFF0000u : r[i >> 1] << 16);
+  for (int i = 0; i < kPairs; ++i)
+    f[i] = F32 ? pair(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]))
+               : pair(__uint_as_float(r[i] << 16), __uint_as_float(r[i] & 0xFFFF0000u));
 }
-__device__ __forceinline__ void unpack_codes(uint32_t x, uint32_t y, float (&f)[kUnit]) {
+__device__ __forceinline__ void unpack_codes(uint32_t x, uint32_t y, Pair (&f)[kPairs]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < kPairs; ++i) {
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((i < 2 ? x : y) >> (16 * (i & 1))), __NV_E4M3);
     const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    f[i] = pair(v.x, v.y);
+  }
+}
+__device__ __forceinline__ void values(const Pair (&p)[kPairs], float (&f)[kUnit]) {
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 v = split(p[i]);
     f[2 * i] = v.x;
     f[2 * i + 1] = v.y;
   }
@@ -179,15 +195,17 @@ __device__ __forceinline__ float block_scale(float top, float* scale) {
   return inv;
 }
 
-// Magnitudes to E4M3 codes in bits 16 to 22 of c.  y = |x| / scale lies in [0,
-// 448]; times 2^-120 its exponent field is E4M3's (bias 7 for 127) and its
-// subnormals are E4M3's, so that the code is bits 20 to 26, with 16 random bits
-// added below them and the rest cut off.
-__device__ __forceinline__ void codes8(const float (&x)[kUnit], float inv, const uint32_t (&r)[4], uint32_t (&c)[kUnit]) {
+// E4M3 codes in bits 16 to 22 of c.  y = x / scale lies in [-448, 448]; times
+// 2^-120 its exponent field is E4M3's (bias 7 for 127) and its subnormals are
+// E4M3's, so that the code of |y| is bits 20 to 26, with 16 random bits added below
+// them and the rest cut off; the sign stays clear of it.
+__device__ __forceinline__ void codes8(const Pair (&x)[kPairs], float inv, const uint32_t (&r)[4], uint32_t (&c)[kUnit]) {
+  const Pair inv2 = pair(inv, inv), shift = pair(7.523163845262640e-37f, 7.523163845262640e-37f);  // 2^-120
 #pragma unroll
-  for (int i = 0; i < kUnit; ++i) {
-    const float y = __fmul_rn(__fmul_rn(fabsf(x[i]), inv), 7.523163845262640e-37f);  // 2^-120
-    c[i] = plus_random(__float_as_uint(y) >> 4, r, i);
+  for (int i = 0; i < kPairs; ++i) {
+    const float2 y = split(mul2(mul2(x[i], inv2), shift));
+    c[2 * i] = plus_random(__float_as_uint(y.x) >> 4, r, 2 * i);
+    c[2 * i + 1] = plus_random(__float_as_uint(y.y) >> 4, r, 2 * i + 1);
   }
 }
 // Bytes B of four words.
@@ -197,11 +215,13 @@ __device__ __forceinline__ uint32_t gather_bytes(uint32_t a, uint32_t b, uint32_
 }
 __device__ __forceinline__ uint32_t any_zero_byte(uint32_t x) { return (x - 0x01010101u) & ~x & 0x80808080u; }
 
-__device__ __forceinline__ uint2 hold_m(const float (&m)[kUnit], const uint32_t (&r)[4], float* scale) {
+__device__ __forceinline__ uint2 hold_m(const Pair (&m2)[kPairs], const uint32_t (&r)[4], float* scale) {
+  float m[kUnit];
+  values(m2, m);
   bool odd;
   const float inv = block_scale(block_top(m, max8_abs(m), odd), scale);
   uint32_t c[kUnit], out[2];
-  codes8(m, inv, r, c);
+  codes8(m2, inv, r, c);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     out[h] = gather_bytes<2>(c[4 * h], c[4 * h + 1], c[4 * h + 2], c[4 * h + 3]) |
@@ -222,7 +242,9 @@ __device__ __forceinline__ uint2 hold_m(const float (&m)[kUnit], const uint32_t 
 // sum at an edge (one lane in 4000), the roots are taken again, and the scale
 // comes from the correctly rounded root of the largest v, which is the largest
 // of the roots.
-__device__ __forceinline__ uint2 hold_u(const float (&v)[kUnit], float (&u)[kUnit], const uint32_t (&r)[4], float* scale) {
+__device__ __forceinline__ uint2 hold_u(const Pair (&v2)[kPairs], Pair (&u)[kPairs], const uint32_t (&r)[4], float* scale) {
+  float v[kUnit];
+  values(v2, v);
   bool odd;
   const float inv = block_scale(__fsqrt_rn(block_top(v, max8_abs(v), odd)), scale);
   uint32_t c[kUnit], out[2], edge = 0xFFFFFFFFu;
@@ -232,7 +254,7 @@ __device__ __forceinline__ uint2 hold_u(const float (&v)[kUnit], float (&u)[kUni
     edge = __viaddmin_u16x2(__byte_perm(c[i], c[i + 1], 0x5410), 0x00010001u, edge);
   if ((edge & 0xFFFFu) < 2u || (edge >> 16) < 2u) {
 #pragma unroll
-    for (int i = 0; i < kUnit; ++i) u[i] = __fsqrt_rn(v[i]);
+    for (int i = 0; i < kPairs; ++i) u[i] = pair(__fsqrt_rn(v[2 * i]), __fsqrt_rn(v[2 * i + 1]));
     codes8(u, inv, r, c);
   }
 #pragma unroll
@@ -253,6 +275,13 @@ __device__ __forceinline__ float sqrt_approx(float x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// a + b with scalar additions: a packed addition of a packed product is compiled
+// to a fused multiply-add (a fifth of the scales came out a last bit apart).
+__device__ __forceinline__ Pair add_unfused(Pair a, Pair b) {
+  const float2 x = split(a), y = split(b);
+  return pair(__fadd_rn(x.x, y.x), __fadd_rn(x.y, y.y));
+}
+
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -289,17 +318,18 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
     const L l = next;
     if (i + 1 < passes) load(next, e + kStep);
     if (!FULL && (e & ~int64_t(255)) >= n) break;  // the warp's values lie past the end
-    float w[kUnit], g[kUnit], m[kUnit], v[kUnit];
+    Pair w[kPairs], g[kPairs], m[kPairs], v[kPairs], u[kPairs];
     unpack<WF32>(l.w, w);
     unpack<GF32>(l.g, g);
     if constexpr (STATES8) {
       unpack_codes(l.m[0].x, l.m[0].y, m);
       unpack_codes(l.v[0].x, l.v[0].y, v);
+      const Pair ms = pair(l.ms, l.ms), vs = pair(l.vs, l.vs);
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) {
-        m[j] = __fmul_rn(m[j], l.ms);
-        v[j] = __fmul_rn(v[j], l.vs);
-        v[j] = __fmul_rn(v[j], v[j]);
+      for (int j = 0; j < kPairs; ++j) {
+        m[j] = mul2(m[j], ms);
+        v[j] = mul2(v[j], vs);
+        v[j] = mul2(v[j], v[j]);
       }
     } else {
       unpack<true>(l.m, m);
@@ -308,31 +338,41 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
     if (a.h.grad_scale) {
       const float gs = *a.h.grad_scale;
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) g[j] *= gs;
+      for (int j = 0; j < kPairs; ++j) g[j] = mul2(g[j], pair(gs, gs));
     }
-    float u[kUnit];
+    const Pair beta1 = pair(a.h.beta1, a.h.beta1), one_beta1 = pair(a.h.one_beta1, a.h.one_beta1);
+    const Pair beta2 = pair(a.h.beta2, a.h.beta2), one_beta2 = pair(a.h.one_beta2, a.h.one_beta2);
+    const Pair decay = pair(a.h.decay, a.h.decay), lr = pair(-a.h.lr_m, -a.h.lr_m);
+    const Pair root = pair(a.h.root_v, a.h.root_v), eps = pair(a.h.eps, a.h.eps);
+    float least = FLT_MAX;
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) {
-      m[j] = __fadd_rn(__fmul_rn(a.h.beta1, m[j]), __fmul_rn(a.h.one_beta1, g[j]));
-      v[j] = __fadd_rn(__fmul_rn(a.h.beta2, v[j]), __fmul_rn(__fmul_rn(a.h.one_beta2, g[j]), g[j]));
-      u[j] = sqrt_approx(v[j]);
+    for (int j = 0; j < kPairs; ++j) {
+      m[j] = add_unfused(mul2(beta1, m[j]), mul2(one_beta1, g[j]));
+      v[j] = add_unfused(mul2(beta2, v[j]), mul2(mul2(one_beta2, g[j]), g[j]));
+      const float2 f = split(v[j]);
+      u[j] = pair(sqrt_approx(f.x), sqrt_approx(f.y));
+      least = min3(least, f.x, f.y);
     }
-    // the approximate root takes subnormals for zeros
-    if (fminf(min3(min3(v[0], v[1], v[2]), v[3], v[4]), min3(v[5], v[6], v[7])) < FLT_MIN) {
+    if (least < FLT_MIN) {  // the approximate root takes subnormals for zeros
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) u[j] = __fsqrt_rn(v[j]);
+      for (int j = 0; j < kPairs; ++j) {
+        const float2 f = split(v[j]);
+        u[j] = pair(__fsqrt_rn(f.x), __fsqrt_rn(f.y));
+      }
     }
 #pragma unroll
-    for (int j = 0; j < kUnit; ++j) {
-      // the divisor is at least eps, a normal number
-      w[j] = fmaf(-a.h.lr_m * m[j], rcp_approx(fmaf(u[j], a.h.root_v, a.h.eps)), w[j] * a.h.decay);
+    for (int j = 0; j < kPairs; ++j) {
+      const float2 d = split(fma2(u[j], root, eps));  // at least eps, a normal number
+      w[j] = fma2(mul2(lr, m[j]), pair(rcp_approx(d.x), rcp_approx(d.y)), mul2(w[j], decay));
     }
+    float wf[kUnit];
+    values(w, wf);
     const uint32_t block = (uint32_t)(e >> 3);
     if constexpr (WF32) {
       uint4 o[2];
       float* f = reinterpret_cast<float*>(o);
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) f[j] = w[j];
+      for (int j = 0; j < kUnit; ++j) f[j] = wf[j];
       store_values<true, FULL>(p.W, e, n, o);
     } else {
       const Philox4 rw = philox4x32_10_rk(block, a.step, p.layer, kTagSR, a.rk0, a.rk1);
@@ -340,12 +380,12 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        o[j] = __byte_perm(plus_random(__float_as_uint(w[2 * j]), r, 2 * j),
-                           plus_random(__float_as_uint(w[2 * j + 1]), r, 2 * j + 1), 0x7632);
-      if (__float_as_uint(max8_abs(w)) > kInfBits) {  // a NaN among the eight
+        o[j] = __byte_perm(plus_random(__float_as_uint(wf[2 * j]), r, 2 * j),
+                           plus_random(__float_as_uint(wf[2 * j + 1]), r, 2 * j + 1), 0x7632);
+      if (__float_as_uint(max8_abs(wf)) > kInfBits) {  // a NaN among the eight
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          o[j] = sr_bf16_bits(w[2 * j], r[j] & 0xFFFFu) | (sr_bf16_bits(w[2 * j + 1], r[j] >> 16) << 16);
+          o[j] = sr_bf16_bits(wf[2 * j], r[j] & 0xFFFFu) | (sr_bf16_bits(wf[2 * j + 1], r[j] >> 16) << 16);
       }
       const uint4 ov = make_uint4(o[0], o[1], o[2], o[3]);
       store_values<false, FULL>(p.W, e, n, &ov);
@@ -359,12 +399,14 @@ __device__ __forceinline__ void adamw_chunk(const AdamBatch& a, const sketch_ada
       store_codes<FULL>(p.v, e, n, hold_u(v, u, ru, p.v_scale + (e >> 8)));
     } else {
       uint4 o[2];
-      float* f = reinterpret_cast<float*>(o);
+      float f[kUnit];
+      values(m, f);
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) f[j] = m[j];
+      for (int j = 0; j < kUnit; ++j) reinterpret_cast<float*>(o)[j] = f[j];
       store_values<true, FULL>(p.m, e, n, o);
+      values(v, f);
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) f[j] = v[j];
+      for (int j = 0; j < kUnit; ++j) reinterpret_cast<float*>(o)[j] = f[j];
       store_values<true, FULL>(p.v, e, n, o);
     }
   }
@@ -404,11 +446,13 @@ cudaError_t launch_adamw(int n, const sketch_adamw_problem* probs, bool states8,
   a.h = h;
   philox_round_keys(seed, a.rk0, a.rk1);
   a.step = step;
-  // a block per kStep values while that leaves no SM without one; else longer
-  // chunks, whose passes overlap
+  // a block's passes overlap, so it makes up to eight, as long as every SM gets
+  // some sixteen blocks (268M values: 638 us with eight passes, 650 with four)
   int64_t total = 0;
   for (int i = 0; i < n; ++i) total += probs[i].n;
-  a.chunk = total <= (int64_t)num_sms() * 8 * kStep ? kStep : 4 * kStep;
+  int64_t passes = total / ((int64_t)num_sms() * 16 * kStep);
+  passes = passes < 1 ? 1 : passes > 8 ? 8 : passes;
+  a.chunk = (int)passes * kStep;
   int i = 0;
   while (i < n) {
     a.n = 0;
