@@ -18,11 +18,12 @@
 //
 // Backward: a thread's columns stay the same over the rows that its block walks,
 // so that dgamma and dbeta add up in registers; with those and gamma there, rows
-// come through shared memory: a warp of its own brings them by bulk copies into a
-// ring of slots, several sets of rows ahead (HBM wants some 60 KB per SM under
-// way), and the others read them there, once for each of the two passes over a
-// row.  B rows are worked on side by side, so that their sums' shuffles, and the
-// one barrier that joins the warps' sums, overlap.
+// come through shared memory: bulk copies bring them into a ring of slots, several
+// sets of rows ahead (HBM wants some 60 KB per SM under way), and threads read them
+// there, once for each of the two passes over a row.  B rows are worked on side by
+// side, so that their sums' shuffles overlap, and one block barrier a set both
+// joins the warps' sums and tells that the slot of the set before can be filled
+// again.
 //
 // Elements come in vectors of 16 bytes (VE of them).  VE = 1 serves rows that do
 // not start on 16 bytes or end inside a vector.  Forward they are read one by one;
@@ -209,29 +210,11 @@ __device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N]
   }
 }
 
-// The producer warp: every set of rows of this block into the ring, a slot again
-// when the `readers` have arrived on its barrier.
-template <int VE, int N>
-__device__ __forceinline__ void produce(const Ring& r, const RowSource (&m)[N], int64_t first, int64_t stride, int passes,
-                                        uint64_t* full, uint64_t* empty, volatile int* abort_flag, int* err) {
-  int s = 0, filled = 0;
-  uint32_t ph = 1;
-  for (; filled < passes; ++filled) {
-    const bool ok = filled < r.slots || tc::mbar_wait(&empty[s], ph, abort_flag, err, tc::kErrTimeoutStage);
-    if (!__all_sync(0xFFFFFFFFu, ok)) break;
-    fill_slot<VE, N>(r, m, s, first + filled * stride, &full[s]);
-    if (++s == r.slots) {
-      s = 0;
-      ph ^= 1u;
-    }
-  }
-  __syncwarp();
-  // if a copy never landed: wait, with a limit, for those still under way
-  if (*abort_flag && (threadIdx.x & 31) == 0) {
-    volatile int none = 0;
-    for (int i = filled > r.slots ? filled - r.slots : 0; i < filled; ++i)
-      tc::mbar_wait(&full[i % r.slots], (i / r.slots) & 1, &none, nullptr, 0, 100000000ull);
-  }
+// If a copy never landed: wait, with a limit, for those still under way.
+__device__ __forceinline__ void drain(uint64_t* full, int slots, int filled) {
+  volatile int none = 0;
+  for (int i = filled > slots ? filled - slots : 0; i < filled; ++i)
+    tc::mbar_wait(&full[i % slots], (i / slots) & 1, &none, nullptr, 0, 100000000ull);
 }
 
 // ---- forward ---------------------------------------------------------------------
@@ -437,13 +420,13 @@ constexpr int backward_rows_each(size_t size, int threads) { return threads == 2
 // A thread's columns: NV vectors of VE elements, as E / 2 pairs.  With VE = 1 a pair
 // is the thread's elements 2 q and 2 q + 1, tpr columns apart.
 template <typename X, int VE, int NV, int THREADS, bool FULL, bool WARP>
-__global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
+__global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
     norm_backward_kernel(const NormBackward a, const Ring ring, int tpr, int* err) {
   constexpr int E = NV * VE, B = backward_rows_each(sizeof(X), THREADS);
   constexpr int VP = VE == 1 ? 1 : VE / 2, NP = E / 2 / VP;  // pairs per step, steps
   constexpr bool HOLD = E <= 16;  // gamma stays in registers
   extern __shared__ __align__(128) uint8_t ring_mem[];
-  __shared__ __align__(8) uint64_t full[kMaxSlots], empty[kMaxSlots];
+  __shared__ __align__(8) uint64_t full[kMaxSlots];
   __shared__ float2 part[2][B][THREADS / 32];
   __shared__ volatile int abort_flag;
   Ring r = ring;
@@ -457,13 +440,13 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
   const int passes = (int)((a.T - first + stride - 1) / stride);
   if (threadIdx.x == 0) {
     abort_flag = 0;
-    for (int s = 0; s < r.slots; ++s) {
-      tc::mbar_init(&full[s], 1);
-      tc::mbar_init(&empty[s], THREADS / 32);
-    }
+    for (int s = 0; s < r.slots; ++s) tc::mbar_init(&full[s], 1);
     tc::fence_mbar_init();
   }
   __syncthreads();
+  int filled = 0;  // warp 0's: sets whose copies have begun
+  if (warp == 0)
+    for (; filled < passes && filled < r.slots; ++filled) fill_slot<VE, 2>(r, m, filled, first + filled * stride, &full[filled]);
   const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr, k = (int)a.k;
   const int warps = tpr >> 5, warp0 = (threadIdx.x & ~(tpr - 1)) >> 5;
   const int nvec = k / VE;
@@ -487,9 +470,7 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
   Pair dg[E / 2], db[E / 2], gamma[HOLD ? E / 2 : 1];
   // wide rows: gamma behind the ring, as the forward pass lays it out
   float* gmem = reinterpret_cast<float*>(ring_mem + (size_t)r.slots * r.slot);
-  if (warp == THREADS / 32) {
-    produce<VE, 2>(r, m, first, stride, passes, full, empty, &abort_flag, err);
-  } else {
+  {
     auto gamma_pairs = [&](int j, Pair (&g)[VP]) {
       if constexpr (VE == 1) {
         const int c = 2 * j * tpr + t;
@@ -500,7 +481,7 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
     };
     if constexpr (!HOLD) {
       for (int c = threadIdx.x; c < k; c += THREADS) gmem[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
-      tc::named_barrier(1, THREADS);
+      __syncthreads();
     }
 #pragma unroll
     for (int j = 0; j < NP; ++j) {
@@ -588,14 +569,18 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
         v[2 * b + 1] = sum2(s1[b]);
       }
       lane_sums<WARP, 2 * B>(v, tpr);
-      if (WARP && warps > 1) {
-        float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
-        if (lane == 0) {
+      float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
+      if (WARP && lane == 0) {
 #pragma unroll
-          for (int b = 0; b < B; ++b) q[b][warp] = make_float2(v[2 * b], v[2 * b + 1]);
-        }
-        if (tpr == THREADS) tc::named_barrier(1, THREADS);
-        else tc::named_barrier(2 + warp0 / warps, tpr);
+        for (int b = 0; b < B; ++b) q[b][warp] = make_float2(v[2 * b], v[2 * b + 1]);
+      }
+      __syncthreads();
+      if (warp == 0 && p > 0 && filled < passes && r.slots > 1) {  // every thread is done with the set before
+        const int before = s ? s - 1 : r.slots - 1;
+        fill_slot<VE, 2>(r, m, before, first + filled * stride, &full[before]);
+        ++filled;
+      }
+      if (WARP && warps > 1) {
         const int b = lane >> (31 - __clz(warps)), w = lane & (warps - 1);  // lane (row, warp) joins
         const float2 u = q[b < B ? b : 0][warp0 + w];
         float j[2] = {u.x, u.y};
@@ -646,8 +631,11 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
       };
       if (FULL && HOLD && r.each == B && row - group * r.each + r.rows <= T) second(std::bool_constant<FULL && HOLD>{});
       else second(std::false_type{});
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      if (r.slots == 1 && p + 1 < passes) {  // fp32 rows too wide for two slots
+        __syncthreads();
+        if (warp == 0) fill_slot<VE, 2>(r, m, 0, first + filled * stride, &full[0]);
+        ++filled;
+      }
       slot += r.slot;
       if (++s == r.slots) {
         s = 0;
@@ -656,6 +644,7 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
       }
     }
   }
+  if (threadIdx.x == 0 && abort_flag) drain(full, r.slots, filled);
   if (a.dgamma == nullptr && a.dbeta == nullptr) return;
   // this block's partial row: the groups' sums added in their order, in the ring's memory
   float* out = a.ws + (int64_t)blockIdx.x * 2 * k;
@@ -663,7 +652,7 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
   __syncthreads();
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    if (warp < THREADS / 32) {
+    {
       float* to = groups > 1 ? acc + group * k : out + half * k;
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
@@ -678,7 +667,7 @@ __global__ void __launch_bounds__(THREADS + 32, blocks_per_sm(THREADS))
     }
     if (groups > 1) {
       __syncthreads();
-      for (int c = threadIdx.x; c < k; c += THREADS + 32) {
+      for (int c = threadIdx.x; c < k; c += THREADS) {
         float v = 0.f;
         for (int g = 0; g < groups; ++g) v += acc[g * k + c];
         out[half * k + c] = v;
@@ -882,7 +871,7 @@ cudaError_t launch_rows(Kernel kernel, const Args& a, const Ring& r, int tpr, in
     if (err != cudaSuccess) return err;
   }
   count_launch();
-  kernel<<<(unsigned)blocks, threads + 32, smem, stream>>>(a, r, tpr, err_word);
+  kernel<<<(unsigned)blocks, threads, smem, stream>>>(a, r, tpr, err_word);
   return cudaGetLastError();
 }
 
