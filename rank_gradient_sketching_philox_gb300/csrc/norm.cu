@@ -218,9 +218,12 @@ __device__ __forceinline__ void drain(uint64_t* full, int slots, int filled) {
 }
 
 // ---- forward ---------------------------------------------------------------------
-// 16-byte vectors of a row per thread, and blocks per SM.
+// 16-byte vectors of a row per thread, and blocks per SM (three left 80 registers
+// and spilled: 96.8 against 92.1 us; threads that read single elements hold less
+// and do better with three, 133 against 199 us for 16384 x 4095 BF16).
 constexpr int forward_vecs(int threads) { return threads == 256 ? 8 : 4; }
-constexpr int forward_blocks(int threads) { return threads == 256 ? 3 : 1; }
+constexpr int forward_blocks(int threads) { return threads == 256 ? 2 : 1; }
+constexpr int single_blocks(int threads) { return threads == 256 ? 3 : 1; }
 
 // Where column c of a weight lies in shared memory: for eight-element vectors
 // the first and the second four columns of each go to halves of their own, so that
@@ -358,7 +361,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
 
 // Rows whose elements are read one by one: NV of them per thread.
 template <typename X, int NV, int THREADS, bool WARP>
-__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_single_kernel(const NormForward a, int tpr) {
+__global__ void __launch_bounds__(THREADS, single_blocks(THREADS)) norm_forward_single_kernel(const NormForward a, int tpr) {
   extern __shared__ __align__(128) float weights[];
   __shared__ float2 part[2][THREADS / 32];
   __shared__ float counts[THREADS / 32];
@@ -796,30 +799,29 @@ int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
 }
 
 template <int THREADS, typename Kernel>
-cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, cudaStream_t stream) {
+cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, int per_sm, cudaStream_t stream) {
   const size_t smem = (size_t)a.k * 8;
   if (smem > 48u * 1024u) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
   }
   int64_t blocks = ceil_div(a.T, THREADS / tpr);
-  const int64_t most = (int64_t)num_sms() * forward_blocks(THREADS);
+  const int64_t most = (int64_t)num_sms() * per_sm;
   if (blocks > most) blocks = most;
   count_launch();
   kernel<<<(unsigned)blocks, THREADS, smem, stream>>>(a, tpr);
   return cudaGetLastError();
 }
 
-// Blocks of 256 threads, three to an SM, while three copies of the weights leave
-// room there, else one of 1024 (whose threads have half the registers).
+// Blocks of 256 threads, two to an SM, up to rows of 4096, else one of 1024 (whose threads have half the registers).
 template <typename X, int THREADS>
 cudaError_t forward_vectors(const NormForward& a, int tpr, cudaStream_t stream) {
   const bool full = a.k == (int64_t)(16 / sizeof(X)) * forward_vecs(THREADS) * tpr;
   if constexpr (THREADS == 256) {
-    if (tpr < 32) return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, false>, a, tpr, stream);
+    if (tpr < 32) return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, false>, a, tpr, forward_blocks(THREADS), stream);
   }
-  return full ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true, true>, a, tpr, stream)
-              : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, true>, a, tpr, stream);
+  return full ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true, true>, a, tpr, forward_blocks(THREADS), stream)
+              : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, true>, a, tpr, forward_blocks(THREADS), stream);
 }
 template <typename X>
 cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
@@ -830,9 +832,9 @@ cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
 template <typename X>
 cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
   const int tpr = threads_per_row(a.k, 16, a.T, 1024);
-  if (tpr < 32) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, false>, a, tpr, stream);
-  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, true>, a, tpr, stream);
-  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024, true>, a, tpr, stream);
+  if (tpr < 32) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, false>, a, tpr, single_blocks(256), stream);
+  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, true>, a, tpr, single_blocks(256), stream);
+  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024, true>, a, tpr, single_blocks(1024), stream);
 }
 
 // The ring for sets of rows of `matrices` matrices, with `beside` bytes of shared
