@@ -202,6 +202,10 @@ __device__ __forceinline__ Pair mul2(Pair a, Pair b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ float sum2(Pair p) {
+  const float2 f = split(p);
+  return f.x + f.y;
+}
 
 __host__ __device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) {
   return (a + b - 1) / b;

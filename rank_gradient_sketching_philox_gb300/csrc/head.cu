@@ -36,6 +36,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -111,6 +112,15 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Columns 2 i and 2 i + 1 of a row's 32 in registers.
+__device__ __forceinline__ Pair columns(const uint32_t (&v)[32], int i) {
+  return pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -175,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
-  const int pair = (int)blockIdx.x >> 1, n_pairs = (int)gridDim.x >> 1;
+  const int my_pair = (int)blockIdx.x >> 1, n_pairs = (int)gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
@@ -229,6 +239,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     const int slot = j & (kTileSlots - 1);
     Tile t;
     t.p = -1;
+    t.chunks = 0;
     if (tc::mbar_wait<true>(&tile_bar[slot], (uint32_t)(j / kTileSlots) & 1u, &abort_flag, a.err, tc::kErrTimeoutStage))
       t = tiles[slot];
     return t;
@@ -239,48 +250,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ---- producer: this CTA's half of each operand ----
-    // This thread paces the kernel once its loop holds more than the waits and
-    // the copies: what a product needs is read once per tile (looked up for each
-    // chunk it took 700 cycles a chunk, whose MMAs take 512).
+    // This thread paces the kernel: its time for a chunk has to stay below that of
+    // the chunk's MMAs, 512 cycles, and every instruction in its loop shows (with a
+    // product's fields looked up for each chunk it took 700 cycles, with the next
+    // tile read in the loop 780).
     const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
+    const uint32_t empty0 = tc::smem_u32(empty_bar), stage0 = tc::smem_u32(smem);
     int s = 0, it = 0;
     uint32_t ph = 0;
-    for (int j = 0;; ++j) {
+    bool stop = false;
+    for (int j = 0; !stop; ++j) {
       const Tile t = next_tile(j);
       if (t.p < 0) break;
       tile_read(j);
       const CUtensorMap *tmA = &a.p[t.p].tmA, *tmB = &a.p[t.p].tmB;
       const int ar = t.a_row + kHalf * (int)rank, br = t.b_row + kHalf * (int)rank;
-      int ak = t.a_k, bk = t.b_k;
       // few rows: the rest of A's tile keeps what it holds, which reaches only
       // rows of the product that are not kept
-      const bool load_a = rank == 0 || t.a_box == kHalf;
       const uint32_t bytes = kOperandBytes * 2 + (t.a_box == kHalf ? 2 * kOperandBytes : (uint32_t)t.a_box * kChunk * 2);
-      const int end = it + t.chunks;
-      for (; it < end; ++it, ak += kChunk, bk += kChunk) {
-        if (it >= kStages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
-        uint8_t* st = smem + s * kStageBytes;
-        if (rank == 0) tc::mbar_arrive_expect_tx(&full_bar[s], bytes);
-        const uint32_t bar = full0 + 8u * s;
-        if (!load_a) {
-        } else if (t.a_mn) {  // two boxes of [64 k][64 rows]
-          tc::tma_load_2d_pair(st, tmA, bar, ar, ak);
-          tc::tma_load_2d_pair(st + kOperandBytes / 2, tmA, bar, ar + 64, ak);
-        } else {  // one box of [128 rows][64 k]
-          tc::tma_load_2d_pair(st, tmA, bar, ak, ar);
+      auto run = [&](auto a_is_mn, auto b_is_mn, auto loads_a) {
+        constexpr bool A_MN = decltype(a_is_mn)::value, B_MN = decltype(b_is_mn)::value;
+        int ak = t.a_k, bk = t.b_k;
+        for (int c = t.chunks; c > 0; --c, ++it, ak += kChunk, bk += kChunk) {
+          if (it >= kStages && !tc::mbar_wait(empty0 + 8u * s, ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
+            stop = true;
+            break;
+          }
+          const uint32_t st = stage0 + (uint32_t)s * kStageBytes, bar = full0 + 8u * s;
+          if (rank == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(full_bar) + 8u * s, bytes);
+          if constexpr (decltype(loads_a)::value) {
+            if constexpr (A_MN) {  // two boxes of [64 k][64 rows]
+              tc::tma_load_2d_pair(st, tmA, bar, ar, ak);
+              tc::tma_load_2d_pair(st + kOperandBytes / 2, tmA, bar, ar + 64, ak);
+            } else {  // one box of [128 rows][64 k]
+              tc::tma_load_2d_pair(st, tmA, bar, ak, ar);
+            }
+          }
+          if constexpr (B_MN) {
+            tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, br, bk);
+            tc::tma_load_2d_pair(st + kOperandBytes + kOperandBytes / 2, tmB, bar, br + 64, bk);
+          } else {
+            tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, bk, br);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-        if (t.b_mn) {
-          tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, br, bk);
-          tc::tma_load_2d_pair(st + kOperandBytes + kOperandBytes / 2, tmB, bar, br + 64, bk);
-        } else {
-          tc::tma_load_2d_pair(st + kOperandBytes, tmB, bar, bk, br);
-        }
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
-        }
-      }
-      if (it < end) break;  // a wait gave up
+      };
+      const bool loads_a = rank == 0 || t.a_box == kHalf;
+      if (t.a_mn) run(std::true_type{}, std::true_type{}, std::true_type{});
+      else if (t.b_mn && loads_a) run(std::false_type{}, std::true_type{}, std::true_type{});
+      else if (t.b_mn) run(std::false_type{}, std::true_type{}, std::false_type{});
+      else if (loads_a) run(std::false_type{}, std::false_type{}, std::true_type{});
+      else run(std::false_type{}, std::false_type{}, std::false_type{});
     }
     issued = it;
   } else if (warp == 1 && lane == 0 && rank == 0) {
@@ -288,46 +311,59 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
     int s = 0, it = 0, j = 0;
     uint32_t ph = 0;
     bool stop = false;
+    const uint32_t full0 = tc::smem_u32(full_bar);
     for (; !stop; ++j) {
       const Tile t = next_tile(j);
       if (t.p < 0) break;
       tile_read(j);
-      const bool a_mn = t.a_mn != 0, b_mn = t.b_mn != 0;
-      const uint32_t idesc = tc::idesc_bf16(kTile, kTile, a_mn, b_mn);
-      // a 16-wide K step: 32 bytes along a K-major swizzle row, 16 rows of 128 bytes of an MN-major tile
-      const uint32_t a_step = (a_mn ? 2048u : 32u) >> 4, b_step = (b_mn ? 2048u : 32u) >> 4;
-      const uint32_t a_lbo = a_mn ? 8192u : 16u, b_lbo = b_mn ? 8192u : 16u;
       const int b = j & 1;
       if (j >= 2 && !tc::mbar_wait<true>(&tempty_bar[b], ((j >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
         break;
       tc::tc_fence_after();
       const uint32_t acc = tmem + (uint32_t)(b * kTile);
-      const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), a_lbo, 1024);
-      const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kOperandBytes, b_lbo, 1024);
-      for (int c = 0; c < t.chunks; ++c, ++it) {
-        if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) {
-          stop = true;
-          break;
-        }
-        tc::tc_fence_after();
-        // a stage further: its size in the descriptors' address fields (16-byte units)
-        const uint64_t ad = ad0 + (uint32_t)s * (kStageBytes >> 4), bd = bd0 + (uint32_t)s * (kStageBytes >> 4);
+      // the chunks' MMAs, with everything but the stage fixed at compile time: this
+      // thread shares its scheduler with two warps of the epilogue
+      auto run = [&](auto a_is_mn, auto b_is_mn) {
+        constexpr bool A_MN = decltype(a_is_mn)::value, B_MN = decltype(b_is_mn)::value;
+        // a 16-wide K step: 32 bytes along a K-major swizzle row, 16 rows of 128 bytes of an MN-major tile
+        constexpr uint32_t kStepA = (A_MN ? 2048u : 32u) >> 4, kStepB = (B_MN ? 2048u : 32u) >> 4;
+        constexpr uint32_t idesc = tc::idesc_bf16(kTile, kTile, A_MN, B_MN);
+        const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), A_MN ? 8192u : 16u, 1024);
+        const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kOperandBytes, B_MN ? 8192u : 16u, 1024);
+        const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32);
+        uint32_t more = 0;  // the tile's first MMA overwrites the accumulator
+        for (int c = t.chunks; c > 0; --c) {
+          if (!tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) {
+            stop = true;
+            break;
+          }
+          tc::tc_fence_after();
+          // a stage further: its size in the descriptors' address fields (16-byte units)
+          const uint32_t al = (uint32_t)ad0 + (uint32_t)s * (kStageBytes >> 4);
+          const uint32_t bl = (uint32_t)bd0 + (uint32_t)s * (kStageBytes >> 4);
 #pragma unroll
-        for (int kk = 0; kk < kChunk / 16; ++kk)
-          tc::mma_bf16_pair(acc, ad + kk * a_step, bd + kk * b_step, idesc, (c > 0 || kk > 0) ? 1u : 0u);
-        tc::mma_commit_pair(&empty_bar[s]);
-        if (++s == kStages) {
-          s = 0;
-          ph ^= 1u;
+          for (int kk = 0; kk < kChunk / 16; ++kk) {
+            tc::mma_bf16_pair(acc, al + kk * kStepA, a_hi, bl + kk * kStepB, b_hi, idesc, kk == 0 ? more : 1u);
+          }
+          more = 1;
+          tc::mma_commit_pair(&empty_bar[s]);
+          ++it;
+          if (++s == kStages) {
+            s = 0;
+            ph ^= 1u;
+          }
         }
-      }
+      };
+      if (t.a_mn) run(std::true_type{}, std::true_type{});  // dW
+      else if (t.b_mn) run(std::false_type{}, std::true_type{});
+      else run(std::false_type{}, std::false_type{});
       if (!stop) tc::mma_commit_pair(&tfull_bar[b]);
     }
     consumed = it;
   } else if (warp == 2 + kEpiWarps) {
     // ---- tiles: every n-th, or as a counter deals them out ----
     if (lane == 0 && rank == 0) {
-      int item = pair;
+      int item = my_pair;
       for (int j = 0;; ++j) {
         const int slot = j & (kTileSlots - 1);
         if (j >= kTileSlots && !tc::mbar_wait<true>(&read_bar[slot], (uint32_t)(j / kTileSlots - 1) & 1u, &abort_flag,
@@ -376,7 +412,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         const int M = pr.M;
         const int64_t target = row < M ? a.targets[row] : -1;
         const int tcol = (target >= col0 && target < col0 + kHalf && target < N) ? (int)(target - col0) : -1;
-        float mx = -INFINITY, sum = 0.f;
+        const Pair scale2 = pair(a.scale_log2, a.scale_log2);
+        float mx = -INFINITY;
+        Pair sum = 0;
         for (int cg = 0; cg < kHalf / 32; ++cg) {
           tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
           tc::tmem_wait_ld_regs(v);
@@ -391,21 +429,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
             for (int i = 0; i < 32; ++i)
               if ((tcol & 31) == i) v[i] = __float_as_uint(-INFINITY);
           }
-          float g = -INFINITY;
+          float g = max3(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[31]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) g = fmaxf(g, __uint_as_float(v[i]) * a.scale_log2);
-          const float top = fmaxf(mx, g);
+          for (int i = 2; i < 30; i += 2) g = max3(g, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          const float top = fmaxf(mx, fmaxf(g, __uint_as_float(v[30])) * a.scale_log2);  // scale > 0
           const float ref = top == -INFINITY ? 0.f : top;
-          float s0 = 0.f, s1 = 0.f;
+          const Pair neg = pair(-ref, -ref);
+          const float keep = ex2(mx - ref);
+          sum = mul2(sum, pair(keep, keep));
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            s0 += ex2(fmaf(__uint_as_float(v[i]), a.scale_log2, -ref));
-            s1 += ex2(fmaf(__uint_as_float(v[i + 1]), a.scale_log2, -ref));
+          for (int i = 0; i < 16; ++i) {
+            const float2 e = split(fma2(columns(v, i), scale2, neg));
+            sum = add2(sum, pair(ex2(e.x), ex2(e.y)));
           }
-          sum = sum * ex2(mx - ref) + (s0 + s1);
           mx = top;
         }
-        if (row < M && col0 < N) a.partials[(int64_t)(col0 / kHalf) * a.T + row] = make_float2(mx, sum);
+        if (row < M && col0 < N) a.partials[(int64_t)(col0 / kHalf) * a.T + row] = make_float2(mx, sum2(sum));
       } else if (pr.epi == kEpiDlogit) {
         // rows past the kept ones are written as zeros up to the tile's end,
         // since they take part in dW's sum over rows

@@ -51,10 +51,6 @@ constexpr int kThreads = 256;
 constexpr int kMaxPartials = 320;  // partial rows of the weights' gradients
 constexpr int kMaxSlots = 8;
 
-__device__ __forceinline__ float sum2(Pair p) {
-  const float2 f = split(p);
-  return f.x + f.y;
-}
 // Two BF16 values of a word.
 __device__ __forceinline__ Pair pair_bf16(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
