@@ -632,10 +632,12 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
   }
 }
 
-// Gather the kept tokens' rows to the front, in order.  Block: eight rows, one
-// per warp.  Each block counts the kept tokens before its own, so that no pass
-// over the targets comes first.  Compact rows past the kept ones, up to `fill`
-// (a multiple of the tile's rows), are zeroed.
+// Gather the kept tokens' rows to the front, in order.  Block: `per_block` rows,
+// eight at a time, one per warp.  Each block counts the kept tokens before its own,
+// so that no pass over the targets comes first; blocks are longer for many tokens,
+// so that this counting stays small (T = 131072: 1 GB read from L2 in all, beside
+// 1 GB of X).  Compact rows past the kept ones, up to `fill` (a multiple of the
+// tile's rows), are zeroed.
 struct Gather {
   const uint16_t* X;
   int64_t T, k, ld_x;
@@ -659,6 +661,7 @@ struct Gather {
   uint16_t* dX;  // nullable
   int64_t ld_dx;
   int64_t rows;  // compact rows the buffers hold
+  int per_block;
   int all_rows;  // zero every compact row past the kept ones, not only the last tile's
   int32_t* status;
 };
@@ -668,7 +671,7 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
   cudaGridDependencySynchronize();
   __shared__ int before_s, total_s, bad_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t base = (int64_t)blockIdx.x * 8;
+  const int64_t base = (int64_t)blockIdx.x * a.per_block;
   if (threadIdx.x == 0) before_s = total_s = bad_s = 0;
   __syncthreads();
   int before = 0, total = 0, bad = 0;
@@ -691,44 +694,51 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
   total = total_s;
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < a.n_counters; i += blockDim.x) a.counters[i] = 0;
+    if (threadIdx.x == 0) {
+      *a.kept = total;
+      if (a.status) *a.status = bad_s ? SKETCH_DEV_BAD_TARGET : 0;
+    }
   }
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    *a.kept = total;
-    if (a.status) *a.status = bad_s ? SKETCH_DEV_BAD_TARGET : 0;
-  }
-  const int64_t row = base + warp;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (row < a.T) {
-    int64_t dst = before_s;
-    int64_t t = 0;
-    for (int w = 0; w <= warp; ++w) {
-      t = a.targets[base + w];
-      if (w < warp) dst += t >= 0 && t < a.V;
-    }
-    if (t >= 0 && t < a.V) {
-      const uint4* x = reinterpret_cast<const uint4*>(a.X + row * a.ld_x);
-      uint4* y = reinterpret_cast<uint4*>(a.Xc + dst * a.k);
-      for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = x[i];
-      if (a.XP)
-        for (int64_t i = lane; i < a.r; i += 32) a.XPc[dst * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
-      if (lane == 0) {
-        a.lse_log2[dst] = a.lse[row] * kLog2e;
-        a.weight[dst] = a.g[row] * a.scale;
-        a.target[dst] = (int)t;
-        a.row_of[dst] = (int)row;
-      }
-    } else if (a.dX) {
-      uint4* y = reinterpret_cast<uint4*>(a.dX + row * a.ld_dx);
-      for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
-    }
-  }
-  int64_t fill = (int64_t)(total < 1 ? 1 : total);
+  int64_t fill = total < 1 ? 1 : total;
   fill = a.all_rows ? a.rows : (fill + kTile - 1) / kTile * kTile;
-  if (row >= total && row < fill) {
-    uint4* y = reinterpret_cast<uint4*>(a.Xc + row * a.k);
-    for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
-    if (a.XP)
-      for (int64_t i = lane; i < a.r; i += 32) a.XPc[row * a.ld_xpc + i] = 0;
+  int64_t next = before_s;  // compact row of the first kept one among the eight rows
+  const int64_t end = base + a.per_block < a.rows ? base + a.per_block : a.rows;
+  for (int64_t first = base; first < end; first += 8) {
+    const int64_t row = first + warp;
+    int64_t dst = next, t = -1;
+    for (int w = 0; w < 8; ++w) {
+      const int64_t u = first + w < a.T ? a.targets[first + w] : -1;
+      const int keep = u >= 0 && u < a.V;
+      next += keep;
+      if (w < warp) dst += keep;
+      if (w == warp) t = u;
+    }
+    if (row < a.T) {
+      if (t >= 0 && t < a.V) {
+        const uint4* x = reinterpret_cast<const uint4*>(a.X + row * a.ld_x);
+        uint4* y = reinterpret_cast<uint4*>(a.Xc + dst * a.k);
+#pragma unroll 4
+        for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = x[i];
+        if (a.XP)
+          for (int64_t i = lane; i < a.r; i += 32) a.XPc[dst * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
+        if (lane == 0) {
+          a.lse_log2[dst] = a.lse[row] * kLog2e;
+          a.weight[dst] = a.g[row] * a.scale;
+          a.target[dst] = (int)t;
+          a.row_of[dst] = (int)row;
+        }
+      } else if (a.dX) {
+        uint4* y = reinterpret_cast<uint4*>(a.dX + row * a.ld_dx);
+        for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
+      }
+    }
+    if (row >= total && row < fill) {
+      uint4* y = reinterpret_cast<uint4*>(a.Xc + row * a.k);
+      for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = zero;
+      if (a.XP)
+        for (int64_t i = lane; i < a.r; i += 32) a.XPc[row * a.ld_xpc + i] = 0;
+    }
   }
 }
 
@@ -945,7 +955,8 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   g.dX = f.dX; g.ld_dx = f.ld_dx;
   g.counters = w.counters; g.n_counters = pieces + 1;
   g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
-  cudaError_t err = launch_after(head_gather_kernel, (unsigned)(rows / 8), 256, 0, stream, g);
+  g.per_block = 8 * (int)(ceil_div(rows, 8192) < 64 ? ceil_div(rows, 8192) : 64);
+  cudaError_t err = launch_after(head_gather_kernel, (unsigned)ceil_div(rows, g.per_block), 256, 0, stream, g);
   if (err != cudaSuccess) return err;
 
   HeadLaunch a = {};

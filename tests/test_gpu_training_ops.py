@@ -191,6 +191,49 @@ def test_norm_backward(T, k, x, w):
     assert torch.equal(inplace, dX)
 
 
+LONG_SHAPES = [(40000, 24), (9000, 100), (3000, 520), (2500, 4096), (2500, 4100), (2011, 4099), (900, 8192),
+               (700, 8200), (400, 8201), (500, 12288), (400, 12289), (330, 16384), (330, 16383)]
+
+
+@pytest.mark.parametrize("x", [BF, F32])
+@pytest.mark.parametrize("T,k", LONG_SHAPES)
+def test_norm_many_rows_of_every_width(T, k, x):
+    """More rows than the blocks in flight: each block walks over several sets of them."""
+    g = gen(T + k)
+    X, dY = randn(g, T, k, dtype=x) + 0.25, randn(g, T, k, dtype=x)
+    gamma, beta = randn(g, k), randn(g, k)
+    eps = 1e-5
+    Y, dX = torch.full_like(X, float("nan")), torch.full_like(X, float("nan"))
+    mean, rstd, dg, db = (torch.full((n,), float("nan"), device=DEV) for n in (T, T, k, k))
+    rgs.layer_norm_forward(X, gamma, beta, Y, mean, rstd, eps=eps)
+    rgs.layer_norm_backward(dY, X, gamma, mean, rstd, dX, dg, db, overwrite=True)
+    y, m, r = norm64(X, gamma, beta, eps)
+    dmean, drel = norm_bounds(X, eps, k)
+    within(mean, m, dmean)
+    within(rstd, r, drel * r)
+    xh = (X.to(F64) - m[:, None]).abs() * r[:, None]
+    bound = ((dmean * r)[:, None] + xh * (drel[:, None] + 2.0 ** -22)) * gamma.to(F64).abs()
+    bound = bound + (y.abs() + beta.to(F64).abs()) * 2.0 ** -23
+    half = 2.0 ** -8 if x == BF else 0.0
+    within(Y, y, bound * 1.01 + y.abs() * half)
+    # the gradients of the formula at the kernel's own mean and rstd
+    m, r = mean.to(F64), rstd.to(F64)
+    xs, dy = X.to(F64), dY.to(F64)
+    xh = (xs - m[:, None]) * r[:, None]
+    d = dy * gamma.to(F64)
+    s0, s1 = d.mean(1, keepdim=True), (d * xh).mean(1, keepdim=True)
+    dx = r[:, None] * (d - s0 - xh * s1)
+    exh = 2.0 ** -22 * (xh.abs() + (m.abs() * r)[:, None])
+    n = (k + 16) * 2.0 ** -24
+    e0 = n * d.abs().mean(1, keepdim=True)
+    e1 = n * (d * xh).abs().mean(1, keepdim=True) + (d.abs() * exh).mean(1, keepdim=True)
+    ex = r[:, None] * (e0 + exh * s1.abs() + xh.abs() * e1 + 2.0 ** -21 * (d.abs() + s0.abs() + xh.abs() * s1.abs()))
+    within(dX, dx, ex * 1.01 + dx.abs() * half)
+    nt = (T + 16) * 2.0 ** -24
+    within(dg, (dy * xh).sum(0), nt * (dy * xh).abs().sum(0) + (dy.abs() * exh).sum(0))
+    within(db, dy.sum(0), nt * dy.abs().sum(0))
+
+
 def test_norm_gradient_against_differences():
     """<dX, u>, <dgamma, a> and <dbeta, b> against central differences of sum(dY * LN(X)) in 64 bits."""
     g = gen(11)
@@ -369,6 +412,27 @@ def test_cross_entropy_in_pieces_of_the_vocabulary():
         within(dW, want, product_bound(d.t(), ed.t(), x) * 1.01 + want.abs() * (2.0 ** -8 if out_type == BF else 2.0 ** -22) + 1e-30)
         want = d.t() @ XP.to(F64)
         within(C, want, product_bound(d.t(), ed.t(), XP.to(F64)) * 1.01 + 1e-30)
+
+
+@pytest.mark.parametrize("T,k,V", [(20001, 64, 300), (9000, 8, 1300), (640, 4096, 300), (40, 512, 70001)])
+def test_cross_entropy_long_and_narrow(T, k, V):
+    """Many tokens (blocks of the gather that take several rows a warp), wide rows, and a vocabulary split for dX."""
+    X, W, targets, up = ce_inputs(T, k, V, seed=11, ignored=0.5)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse)
+    logits, elog, want, want_loss = ce64(X, W, targets, 1.0)
+    bound = elog.amax(1) + 2.0 ** -20 * (1 + want.abs() + logits.abs().amax(1)) + V * 2.0 ** -24
+    within(lse, want, bound)
+    within(loss, want_loss, 2 * bound)
+    del logits, elog
+    dX, dW = torch.full_like(X, float("nan")), torch.full_like(W, float("nan"))
+    rgs.cross_entropy_backward(X, W, targets, lse, up, dX=dX, dW=dW)
+    d, ed, x, w = ce_grads64(X, W, targets, up, lse, 1.0)
+    want = d @ w
+    within(dX, want, product_bound(d, ed, w) * 1.01 + want.abs() * 2.0 ** -8 + 1e-30)
+    assert (dX[targets < 0] == 0).all()
+    want = d.t() @ x
+    within(dW, want, product_bound(d.t(), ed.t(), x) * 1.01 + want.abs() * 2.0 ** -8 + 1e-30)
 
 
 @pytest.mark.parametrize("V", [100, 3000])
