@@ -442,6 +442,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
     for (int s = 0; s < r.slots; ++s) tc::mbar_init(&full[s], 1);
     tc::fence_mbar_init();
   }
+  cudaTriggerProgrammaticLaunchCompletion();  // norm_grad_sum_kernel may come up as blocks leave
   __syncthreads();
   int filled = 0;  // warp 0's: sets whose copies have begun
   if (warp == 0)
