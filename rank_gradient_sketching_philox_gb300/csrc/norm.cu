@@ -25,12 +25,13 @@
 // joins the warps' sums and tells that the slot of the set before can be filled
 // again.
 //
-// Elements come in vectors of 16 bytes (VE of them).  VE = 1 serves rows that do
-// not start on 16 bytes or end inside a vector.  Forward they are read one by one;
-// backward their copies start and end at the 16-byte boundaries around them (the
-// bytes beyond belong to the neighbouring rows; a row at an end of the matrix,
-// which has none, is brought in exactly), and elements are picked one by one in
-// shared memory.
+// Elements come in vectors of 16 bytes (VE of them).  Rows that do not start on 16
+// bytes or end inside a vector: the forward pass takes the widest vector, of 8 or 4
+// bytes, that all rows start on and end with, or single elements; the backward
+// pass's copies start and end at the 16-byte boundaries around a row (the bytes
+// beyond belong to the neighbouring rows; a row at an end of the matrix, which has
+// none, is brought in exactly), and elements are picked one by one in shared memory
+// (VE = 1).
 //
 // Backward: each block leaves one partial row of dgamma and dbeta, and
 // norm_grad_sum_kernel adds those.  Rows wider than 16384 take the kernels at the
@@ -54,29 +55,56 @@ constexpr int kMaxSlots = 8;
 // Two BF16 values of a word.
 __device__ __forceinline__ Pair pair_bf16(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
-// The pairs of a 16-byte vector of X.
+// A vector of 16, 8 or 4 bytes: the widest that all rows start on and end with.
+template <int BYTES>
+struct Words {
+  uint32_t w[BYTES / 4];
+};
+template <int BYTES>
+__device__ __forceinline__ Words<BYTES> load_words(const void* base, int idx) {
+  Words<BYTES> r;
+  if constexpr (BYTES == 16) {
+    const uint4 v = __ldcs(static_cast<const uint4*>(base) + idx);
+    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+  } else if constexpr (BYTES == 8) {
+    const uint2 v = __ldcs(static_cast<const uint2*>(base) + idx);
+    r.w[0] = v.x; r.w[1] = v.y;
+  } else {
+    r.w[0] = __ldcs(static_cast<const uint32_t*>(base) + idx);
+  }
+  return r;
+}
+// The pairs of a vector's words.
+template <typename X, int N, int W>
+__device__ __forceinline__ void vec_pairs(const uint32_t (&r)[W], Pair (&p)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    p[i] = sizeof(X) == 2 ? pair_bf16(r[i & (W - 1)])
+                          : pair(__uint_as_float(r[(2 * i) & (W - 1)]), __uint_as_float(r[(2 * i + 1) & (W - 1)]));
+}
 template <typename X>
 __device__ __forceinline__ void vec_pairs(const uint4& v, Pair (&p)[8 / sizeof(X)]) {
   const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < (int)(8 / sizeof(X)); ++i)
-    p[i] = sizeof(X) == 2 ? pair_bf16(r[i]) : pair(__uint_as_float(r[(2 * i) & 3]), __uint_as_float(r[(2 * i + 1) & 3]));
+  vec_pairs<X, (int)(8 / sizeof(X)), 4>(r, p);
 }
-template <typename X>
-__device__ __forceinline__ void store_vec(X* row, int idx, const Pair (&p)[8 / sizeof(X)]) {
-  uint32_t r[4];
+template <typename X, int N>
+__device__ __forceinline__ void store_vec(X* row, int idx, const Pair (&p)[N]) {
+  constexpr int W = N * 2 * (int)sizeof(X) / 4;
+  uint32_t r[W];
 #pragma unroll
-  for (int i = 0; i < (int)(8 / sizeof(X)); ++i) {
+  for (int i = 0; i < N; ++i) {
     const float2 f = split(p[i]);
     if constexpr (sizeof(X) == 2) {
       const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
       r[i] = *reinterpret_cast<const uint32_t*>(&h);
     } else {
-      r[(2 * i) & 3] = __float_as_uint(f.x);
-      r[(2 * i + 1) & 3] = __float_as_uint(f.y);
+      r[2 * i] = __float_as_uint(f.x);
+      r[2 * i + 1] = __float_as_uint(f.y);
     }
   }
-  reinterpret_cast<uint4*>(row)[idx] = make_uint4(r[0], r[1], r[2], r[3]);
+  if constexpr (W == 4) reinterpret_cast<uint4*>(row)[idx] = make_uint4(r[0], r[1], r[2], r[3]);
+  else if constexpr (W == 2) reinterpret_cast<uint2*>(row)[idx] = make_uint2(r[0], r[1]);
+  else reinterpret_cast<uint32_t*>(row)[idx] = r[0];
 }
 __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
@@ -214,11 +242,12 @@ __device__ __forceinline__ void drain(uint64_t* full, int slots, int filled) {
 }
 
 // ---- forward ---------------------------------------------------------------------
-// 16-byte vectors of a row per thread, and blocks per SM (three left 80 registers
+// Bytes of a row per thread, and blocks per SM (three left 80 registers
 // and spilled: 96.8 against 92.1 us; threads that read single elements hold less
 // and do better with three, 133 against 199 us for 16384 x 4095 BF16).
-constexpr int forward_vecs(int threads) { return threads == 256 ? 8 : 4; }
+constexpr int forward_bytes(int threads) { return threads == 256 ? 128 : 64; }
 constexpr int forward_blocks(int threads) { return threads == 256 ? 2 : 1; }
+constexpr int kSingles = 32;  // elements per thread
 constexpr int single_blocks(int threads) { return threads == 256 ? 3 : 1; }
 
 // Where column c of a weight lies in shared memory: for eight-element vectors
@@ -231,11 +260,15 @@ __device__ __forceinline__ int weight_at(int c, int k) {
 // The pairs of the weights of vector idx.
 template <int VE>
 __device__ __forceinline__ void weight_pairs(uint32_t base, int idx, int k, Pair (&p)[VE / 2]) {
+  if constexpr (VE == 2) {
+    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(p[0]) : "r"(base + 8u * idx) : "memory");
+  } else {
 #pragma unroll
-  for (int h = 0; h < VE / 4; ++h) {
-    const uint4 v = tc::lds128(base + 16u * idx + (h ? 2u * k : 0u));
-    p[2 * h] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
-    p[2 * h + 1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+    for (int h = 0; h < VE / 4; ++h) {
+      const uint4 v = tc::lds128(base + 16u * idx + (h ? 2u * k : 0u));
+      p[2 * h] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+      p[2 * h + 1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
+    }
   }
 }
 
@@ -267,10 +300,11 @@ __device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float i
   }
 }
 
-// FULL: every thread has forward_vecs vectors.  WARP: a row has a warp at least.
-template <typename X, int THREADS, bool FULL, bool WARP>
+// Vectors of VE elements.  FULL: every thread has NV of them.  WARP: a row has a
+// warp at least.
+template <typename X, int VE, int THREADS, bool FULL, bool WARP>
 __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_kernel(const NormForward a, int tpr) {
-  constexpr int VE = 16 / sizeof(X), NV = forward_vecs(THREADS);
+  constexpr int BYTES = VE * (int)sizeof(X), NV = forward_bytes(THREADS) / BYTES;
   extern __shared__ __align__(128) float weights[];
   __shared__ float2 part[2][THREADS / 32];
   __shared__ float counts[THREADS / 32];
@@ -296,18 +330,18 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
   for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += stride, p ^= 1) {
     const int64_t row = base + threadIdx.x / tpr;
     const bool in = row < a.T;
-    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const X*>(a.X) + row * a.ld_x);
-    uint4 raw[NV];
+    const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
+    Words<BYTES> raw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      raw[j] = make_uint4(0, 0, 0, 0);
-      if (in && (FULL || j * tpr + t < nvec)) raw[j] = __ldcs(x + j * tpr + t);
+      raw[j] = Words<BYTES>{};
+      if (in && (FULL || j * tpr + t < nvec)) raw[j] = load_words<BYTES>(x, j * tpr + t);
     }
     Pair s = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       Pair v[VE / 2];
-      vec_pairs<X>(raw[j], v);
+      vec_pairs<X>(raw[j].w, v);
 #pragma unroll
       for (int i = 0; i < VE / 2; ++i) s = add2(s, v[i]);
     }
@@ -321,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
           for (int j = 0; j < NV; ++j) {
             if (FULL || j * tpr + t < nvec) {
               Pair v[VE / 2];
-              vec_pairs<X>(raw[j], v);
+              vec_pairs<X>(raw[j].w, v);
 #pragma unroll
               for (int i = 0; i < VE / 2; ++i) {
                 v[i] = add2(v[i], neg);
@@ -340,7 +374,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
     for (int j = 0; j < NV; ++j) {
       if (FULL || j * tpr + t < nvec) {
         Pair v[VE / 2], g[VE / 2], b[VE / 2];
-        vec_pairs<X>(raw[j], v);
+        vec_pairs<X>(raw[j].w, v);
         weight_pairs<VE>(gamma, j * tpr + t, k, g);
         weight_pairs<VE>(beta, j * tpr + t, k, b);
 #pragma unroll
@@ -781,10 +815,10 @@ __global__ void __launch_bounds__(kThreads) norm_dx_wide_kernel(const NormBackwa
 
 constexpr int64_t kMaxRowWidth = 16384;
 
-bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Whether every row of the matrix starts on 16 bytes and ends with a whole vector.
-bool whole_vectors(const void* p, int64_t ld, int64_t k, int ve) { return on16(p) && ld % ve == 0 && k % ve == 0; }
+// Whether every row of the matrix starts on a vector of ve elements and ends with a whole one.
+bool whole_vectors(const void* p, int64_t ld, int64_t k, int ve, size_t size) {
+  return reinterpret_cast<uintptr_t>(p) % (ve * size) == 0 && ld % ve == 0 && k % ve == 0;
+}
 
 // Threads per row: the fewest (of at most `limit`) that hold a row at `most`
 // vectors each, then more while the launch would leave SMs without a block.
@@ -810,28 +844,32 @@ cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, int per
   return cudaGetLastError();
 }
 
-// Blocks of 256 threads, two to an SM, up to rows of 4096, else one of 1024 (whose threads have half the registers).
-template <typename X, int THREADS>
-cudaError_t forward_vectors(const NormForward& a, int tpr, cudaStream_t stream) {
-  const bool full = a.k == (int64_t)(16 / sizeof(X)) * forward_vecs(THREADS) * tpr;
-  if constexpr (THREADS == 256) {
-    if (tpr < 32) return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, false>, a, tpr, forward_blocks(THREADS), stream);
-  }
-  return full ? launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true, true>, a, tpr, forward_blocks(THREADS), stream)
-              : launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, true>, a, tpr, forward_blocks(THREADS), stream);
-}
-template <typename X>
+// Blocks of 256 threads, two to an SM, up to rows of 4096, else one of 1024
+// (whose threads have half the registers).
+template <typename X, int VE, int THREADS>
 cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
-  const int64_t nvec = a.k / (int64_t)(16 / sizeof(X));
-  if (a.k <= 4096) return forward_vectors<X, 256>(a, threads_per_row(nvec, forward_vecs(256), a.T, 256), stream);
-  return forward_vectors<X, 1024>(a, threads_per_row(nvec, forward_vecs(1024), a.T, 1024), stream);
+  constexpr int kMost = forward_bytes(THREADS) / (VE * (int)sizeof(X)), kPerSm = forward_blocks(THREADS);
+  const int tpr = threads_per_row(a.k / VE, kMost, a.T, THREADS);
+  if constexpr (THREADS == 256) {
+    if (tpr < 32)
+      return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, false, false>, a, tpr, kPerSm, stream);
+  }
+  if constexpr (VE * sizeof(X) == 16) {
+    if (a.k == (int64_t)VE * kMost * tpr)
+      return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, true, true>, a, tpr, kPerSm, stream);
+  }
+  return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, false, true>, a, tpr, kPerSm, stream);
+}
+template <typename X, int VE>
+cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
+  return a.k <= 4096 ? forward_vectors<X, VE, 256>(a, stream) : forward_vectors<X, VE, 1024>(a, stream);
 }
 template <typename X>
 cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
-  const int tpr = threads_per_row(a.k, 16, a.T, 1024);
-  if (tpr < 32) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, false>, a, tpr, single_blocks(256), stream);
-  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, 16, 256, true>, a, tpr, single_blocks(256), stream);
-  return launch_forward<1024>(norm_forward_single_kernel<X, 16, 1024, true>, a, tpr, single_blocks(1024), stream);
+  const int tpr = threads_per_row(a.k, kSingles, a.T, 512);
+  if (tpr < 32) return launch_forward<256>(norm_forward_single_kernel<X, kSingles, 256, false>, a, tpr, single_blocks(256), stream);
+  if (tpr <= 256) return launch_forward<256>(norm_forward_single_kernel<X, kSingles, 256, true>, a, tpr, single_blocks(256), stream);
+  return launch_forward<512>(norm_forward_single_kernel<X, kSingles, 512, true>, a, tpr, single_blocks(512), stream);
 }
 
 // The ring for sets of rows of `matrices` matrices, with `beside` bytes of shared
@@ -949,10 +987,15 @@ cudaError_t backward_wide(const NormBackward& a, cudaStream_t stream) {
 
 template <typename X>
 cudaError_t forward_any(const NormForward& a, cudaStream_t stream) {
-  constexpr int VE = 16 / sizeof(X);
+  auto vectors = [&](int ve) { return whole_vectors(a.X, a.ld_x, a.k, ve, sizeof(X)) && whole_vectors(a.Y, a.ld_y, a.k, ve, sizeof(X)); };
   if (a.k <= kMaxRowWidth) {
-    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.Y, a.ld_y, a.k, VE);
-    return vectors ? forward_vectors<X>(a, stream) : forward_singles<X>(a, stream);
+    constexpr int kWide = 16 / (int)sizeof(X);
+    if (vectors(kWide)) return forward_vectors<X, kWide>(a, stream);
+    if (vectors(kWide / 2)) return forward_vectors<X, kWide / 2>(a, stream);
+    if constexpr (kWide == 8) {
+      if (vectors(2)) return forward_vectors<X, 2>(a, stream);
+    }
+    return forward_singles<X>(a, stream);
   }
   count_launch();
   norm_forward_wide_kernel<X><<<(unsigned)a.T, kThreads, 0, stream>>>(a);
@@ -965,8 +1008,9 @@ cudaError_t backward_any(const NormBackward& a, cudaStream_t stream) {
   bool done = false;
   cudaError_t err = cudaSuccess;
   if (a.k <= kMaxRowWidth) {
-    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE) && whole_vectors(a.dY, a.ld_dy, a.k, VE) &&
-                         (a.dX == nullptr || whole_vectors(a.dX, a.ld_dx, a.k, VE));
+    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE, sizeof(X)) &&
+                         whole_vectors(a.dY, a.ld_dy, a.k, VE, sizeof(X)) &&
+                         (a.dX == nullptr || whole_vectors(a.dX, a.ld_dx, a.k, VE, sizeof(X)));
     err = vectors ? backward<X, VE>(a, done, stream) : backward<X, 1>(a, done, stream);
   }
   return (done || err != cudaSuccess) ? err : backward_wide<X>(a, stream);
