@@ -11,10 +11,11 @@
 // Both passes are bound by HBM, once the instructions for each element are few:
 // arithmetic goes two values at a time (packed fp32 pairs).
 //
-// Forward: a row belongs to `tpr` threads (a power of two, 8 to 256), each with
+// Forward: a row belongs to `tpr` threads (a power of two, 8 to 1024), each with
 // up to 128 bytes of it in registers, so that a row is read once; gamma and beta
 // lie in shared memory as fp32, laid out so that a warp's reads of them have no
-// bank conflicts.  Blocks walk over the rows.
+// bank conflicts.  Blocks walk over the rows.  32768 x 4096 BF16: 90 us, 0.88 of the
+// copy rate over the 4 bytes an element that have to move.
 //
 // Backward: a thread's columns stay the same over the rows that its block walks,
 // so that dgamma and dbeta add up in registers; with those and gamma there, rows
@@ -23,15 +24,16 @@
 // there, once for each of the two passes over a row.  B rows are worked on side by
 // side, so that their sums' shuffles overlap, and one block barrier a set both
 // joins the warps' sums and tells that the slot of the set before can be filled
-// again.
+// again.  32768 x 4096 BF16: 141 us, 0.84 of the copy rate over 6 bytes an element.
 //
 // Elements come in vectors of 16 bytes (VE of them).  Rows that do not start on 16
-// bytes or end inside a vector: the forward pass takes the widest vector, of 8 or 4
-// bytes, that all rows start on and end with, or single elements; the backward
-// pass's copies start and end at the 16-byte boundaries around a row (the bytes
-// beyond belong to the neighbouring rows; a row at an end of the matrix, which has
-// none, is brought in exactly), and elements are picked one by one in shared memory
-// (VE = 1).
+// bytes or end inside a vector: the forward pass takes the vectors between a row's
+// first and last boundary, and the elements beside those one by one (16384 x 4095
+// BF16: 58 us, 0.68 of the copy rate; single elements all along take 150).  The
+// backward pass's copies start and end at the 16-byte boundaries around a row (the
+// bytes beyond belong to the neighbouring rows; a row at an end of the matrix, which
+// has none, is brought in exactly), and elements are picked one by one in shared
+// memory (VE = 1).
 //
 // Backward: each block leaves one partial row of dgamma and dbeta, and
 // norm_grad_sum_kernel adds those.  Rows wider than 16384 take the kernels at the
@@ -55,42 +57,19 @@ constexpr int kMaxSlots = 8;
 // Two BF16 values of a word.
 __device__ __forceinline__ Pair pair_bf16(uint32_t w) { return pair(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
-// A vector of 16, 8 or 4 bytes: the widest that all rows start on and end with.
-template <int BYTES>
-struct Words {
-  uint32_t w[BYTES / 4];
-};
-template <int BYTES>
-__device__ __forceinline__ Words<BYTES> load_words(const void* base, int idx) {
-  Words<BYTES> r;
-  if constexpr (BYTES == 16) {
-    const uint4 v = __ldcs(static_cast<const uint4*>(base) + idx);
-    r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
-  } else if constexpr (BYTES == 8) {
-    const uint2 v = __ldcs(static_cast<const uint2*>(base) + idx);
-    r.w[0] = v.x; r.w[1] = v.y;
-  } else {
-    r.w[0] = __ldcs(static_cast<const uint32_t*>(base) + idx);
-  }
-  return r;
-}
-// The pairs of a vector's words.
-template <typename X, int N, int W>
-__device__ __forceinline__ void vec_pairs(const uint32_t (&r)[W], Pair (&p)[N]) {
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    p[i] = sizeof(X) == 2 ? pair_bf16(r[i & (W - 1)])
-                          : pair(__uint_as_float(r[(2 * i) & (W - 1)]), __uint_as_float(r[(2 * i + 1) & (W - 1)]));
-}
+// The pairs of a 16-byte vector, and a vector from pairs.
 template <typename X>
 __device__ __forceinline__ void vec_pairs(const uint4& v, Pair (&p)[8 / sizeof(X)]) {
   const uint32_t r[4] = {v.x, v.y, v.z, v.w};
-  vec_pairs<X, (int)(8 / sizeof(X)), 4>(r, p);
+#pragma unroll
+  for (int i = 0; i < (int)(8 / sizeof(X)); ++i)
+    p[i] = sizeof(X) == 2 ? pair_bf16(r[i & 3])
+                          : pair(__uint_as_float(r[(2 * i) & 3]), __uint_as_float(r[(2 * i + 1) & 3]));
 }
 template <typename X, int N>
 __device__ __forceinline__ void store_vec(X* row, int idx, const Pair (&p)[N]) {
-  constexpr int W = N * 2 * (int)sizeof(X) / 4;
-  uint32_t r[W];
+  static_assert(N * 2 * sizeof(X) == 16);
+  uint32_t r[4];
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float2 f = split(p[i]);
@@ -102,9 +81,7 @@ __device__ __forceinline__ void store_vec(X* row, int idx, const Pair (&p)[N]) {
       r[2 * i + 1] = __float_as_uint(f.y);
     }
   }
-  if constexpr (W == 4) reinterpret_cast<uint4*>(row)[idx] = make_uint4(r[0], r[1], r[2], r[3]);
-  else if constexpr (W == 2) reinterpret_cast<uint2*>(row)[idx] = make_uint2(r[0], r[1]);
-  else reinterpret_cast<uint32_t*>(row)[idx] = r[0];
+  reinterpret_cast<uint4*>(row)[idx] = make_uint4(r[0], r[1], r[2], r[3]);
 }
 __device__ __forceinline__ void store_one(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_one(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
@@ -215,6 +192,7 @@ __device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N]
               for (uint32_t b = ph; b < end && b < lo; b += 2) tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
               for (uint32_t b = hi > lo ? hi : lo; b < end; b += 2)
                 tc::sts16(at + b, *reinterpret_cast<const uint16_t*>(src + b));
+              tc::fence_proxy_async_smem();  // a later set's copy writes over them
             }
             src += lo;
             at += lo;
@@ -242,9 +220,10 @@ __device__ __forceinline__ void drain(uint64_t* full, int slots, int filled) {
 }
 
 // ---- forward ---------------------------------------------------------------------
-// Bytes of a row per thread, and blocks per SM (three left 80 registers
-// and spilled: 96.8 against 92.1 us; threads that read single elements hold less
-// and do better with three, 133 against 199 us for 16384 x 4095 BF16).
+// Bytes of a row per thread, and blocks per SM: two, with three the threads have 80
+// registers and spill (32768 x 4096 BF16: 96 against 91 us); threads that read
+// single elements hold less and do better with three (16384 x 4095 BF16: 148 against
+// 187 us).
 constexpr int forward_bytes(int threads) { return threads == 256 ? 128 : 64; }
 constexpr int forward_blocks(int threads) { return threads == 256 ? 2 : 1; }
 constexpr int kSingles = 32;  // elements per thread
@@ -260,16 +239,18 @@ __device__ __forceinline__ int weight_at(int c, int k) {
 // The pairs of the weights of vector idx.
 template <int VE>
 __device__ __forceinline__ void weight_pairs(uint32_t base, int idx, int k, Pair (&p)[VE / 2]) {
-  if constexpr (VE == 2) {
-    asm volatile("ld.shared.b64 %0, [%1];" : "=l"(p[0]) : "r"(base + 8u * idx) : "memory");
-  } else {
 #pragma unroll
-    for (int h = 0; h < VE / 4; ++h) {
-      const uint4 v = tc::lds128(base + 16u * idx + (h ? 2u * k : 0u));
-      p[2 * h] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
-      p[2 * h + 1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
-    }
+  for (int h = 0; h < VE / 4; ++h) {
+    const uint4 v = tc::lds128(base + 16u * idx + (h ? 2u * k : 0u));
+    p[2 * h] = pair(__uint_as_float(v.x), __uint_as_float(v.y));
+    p[2 * h + 1] = pair(__uint_as_float(v.z), __uint_as_float(v.w));
   }
+}
+
+__device__ __forceinline__ float2 lds_f32x2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
 }
 
 // Statistics of the row whose elements this thread's share sums to `sum` and,
@@ -278,8 +259,8 @@ __device__ __forceinline__ void weight_pairs(uint32_t base, int idx, int k, Pair
 // of squares, so that a row far from zero loses nothing).  `part` alternates
 // between rows: a thread that writes it again has passed the barrier of the row
 // between, after which nobody reads the old values.
-template <bool WARP, typename Dev>
-__device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float inv_n, float inv_k, const float* counts,
+template <bool WARP, typename Dev, typename Count>
+__device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float inv_n, float inv_k, Count counts,
                                             float2* part, float& mu, float& m2) {
   mu = lane_sum<WARP>(sum, tpr) * inv_n;
   m2 = lane_sum<WARP>(dev(mu), tpr);
@@ -291,20 +272,21 @@ __device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float i
     else tc::named_barrier(1 + warp0 / warps, tpr);
     const int w = warp0 + (lane & (warps - 1));  // every `warps` lanes join the row's warps
     const float2 v = part[w];
-    float j[1] = {counts[w] * v.x};
+    const float n = counts(w);
+    float j[1] = {n * v.x};
     join_sums(j, warps);
     mu = j[0] * inv_k;
-    j[0] = fmaf(counts[w] * (v.x - mu), v.x - mu, v.y);
+    j[0] = fmaf(n * (v.x - mu), v.x - mu, v.y);
     join_sums(j, warps);
     m2 = j[0];
   }
 }
 
-// Vectors of VE elements.  FULL: every thread has NV of them.  WARP: a row has a
+// Rows of whole 16-byte vectors.  FULL: every thread has NV of them.  WARP: a row has a
 // warp at least.
-template <typename X, int VE, int THREADS, bool FULL, bool WARP>
+template <typename X, int THREADS, bool FULL, bool WARP>
 __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_kernel(const NormForward a, int tpr) {
-  constexpr int BYTES = VE * (int)sizeof(X), NV = forward_bytes(THREADS) / BYTES;
+  constexpr int VE = 16 / (int)sizeof(X), NV = forward_bytes(THREADS) / 16;
   extern __shared__ __align__(128) float weights[];
   __shared__ float2 part[2][THREADS / 32];
   __shared__ float counts[THREADS / 32];
@@ -330,18 +312,18 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
   for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += stride, p ^= 1) {
     const int64_t row = base + threadIdx.x / tpr;
     const bool in = row < a.T;
-    const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
-    Words<BYTES> raw[NV];
+    const uint4* x = reinterpret_cast<const uint4*>(static_cast<const X*>(a.X) + row * a.ld_x);
+    uint4 raw[NV];
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      raw[j] = Words<BYTES>{};
-      if (in && (FULL || j * tpr + t < nvec)) raw[j] = load_words<BYTES>(x, j * tpr + t);
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (in && (FULL || j * tpr + t < nvec)) raw[j] = __ldcs(x + j * tpr + t);
     }
     Pair s = 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       Pair v[VE / 2];
-      vec_pairs<X>(raw[j].w, v);
+      vec_pairs<X>(raw[j], v);
 #pragma unroll
       for (int i = 0; i < VE / 2; ++i) s = add2(s, v[i]);
     }
@@ -355,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
           for (int j = 0; j < NV; ++j) {
             if (FULL || j * tpr + t < nvec) {
               Pair v[VE / 2];
-              vec_pairs<X>(raw[j].w, v);
+              vec_pairs<X>(raw[j], v);
 #pragma unroll
               for (int i = 0; i < VE / 2; ++i) {
                 v[i] = add2(v[i], neg);
@@ -365,7 +347,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
           }
           return sum2(q);
         },
-        tpr, inv_n, inv_k, counts, part[p], mu, m2);
+        tpr, inv_n, inv_k, [&](int w) { return counts[w]; }, part[p], mu, m2);
     const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
     if (!in) continue;
     const Pair r2 = pair(rstd, rstd), c2 = pair(-mu * rstd, -mu * rstd);
@@ -374,7 +356,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
     for (int j = 0; j < NV; ++j) {
       if (FULL || j * tpr + t < nvec) {
         Pair v[VE / 2], g[VE / 2], b[VE / 2];
-        vec_pairs<X>(raw[j].w, v);
+        vec_pairs<X>(raw[j], v);
         weight_pairs<VE>(gamma, j * tpr + t, k, g);
         weight_pairs<VE>(beta, j * tpr + t, k, b);
 #pragma unroll
@@ -389,7 +371,118 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
   }
 }
 
-// Rows whose elements are read one by one: NV of them per thread.
+// Rows of X and Y that start on the same, any, place between two 16-byte
+// boundaries: the vectors between a row's first and last boundary, and the elements
+// before and behind those, one to a thread.  gamma and beta lie side by side, column
+// c at [c % VE][c / VE]: whichever column the vectors start at, a warp reads 32
+// neighbours.
+template <typename X, int THREADS, bool WARP>
+__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward_shifted_kernel(const NormForward a, int tpr) {
+  constexpr int VE = 16 / (int)sizeof(X), NV = forward_bytes(THREADS) / 16;
+  extern __shared__ __align__(128) float weights[];
+  __shared__ float2 part[2][THREADS / 32];
+  const int t = threadIdx.x & (tpr - 1), groups = THREADS / tpr, k = (int)a.k;
+  const int pitch = k / VE + 1;
+  float2* gb = reinterpret_cast<float2*>(weights);
+  for (int c = threadIdx.x; c < k; c += THREADS)
+    gb[(c & (VE - 1)) * pitch + c / VE] = make_float2(weight(a.gamma, a.w_type, c, 1.f), weight(a.beta, a.w_type, c, 0.f));
+  __syncthreads();
+  const uint32_t gb0 = tc::smem_u32(weights) + 8u * t;
+  const float inv_k = 1.f / (float)k;
+  const int64_t stride = (int64_t)gridDim.x * groups;
+  const int log_tpr = 31 - __clz(tpr);
+  int p = 0;
+  for (int64_t base = (int64_t)blockIdx.x * groups; base < a.T; base += stride, p ^= 1) {
+    const int64_t row = base + threadIdx.x / tpr;
+    const bool in = row < a.T;
+    const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
+    const int ahead = (int)(-(reinterpret_cast<uintptr_t>(x) / sizeof(X)) & (VE - 1));  // elements before the first vector
+    const int lead = ahead < k ? ahead : k, nvec = (k - lead) / VE, behind = k - lead - nvec * VE;
+    // this thread's single element: one of the first `lead`, or of the last
+    const int one = t < lead ? t : t - VE;
+    const bool has_one = t < lead || (t >= VE && t < VE + behind);
+    const int col = t < lead ? one : lead + nvec * VE + one;
+    const bool take = in && has_one;
+    X single = X(0.f);
+    if (take) single = __ldcs(x + col);
+    uint4 raw[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if (in && j * tpr + t < nvec) raw[j] = __ldcs(reinterpret_cast<const uint4*>(x + lead) + j * tpr + t);
+    }
+    Pair s = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      Pair v[VE / 2];
+      vec_pairs<X>(raw[j], v);
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) s = add2(s, v[i]);
+    }
+    const float e = (float)single;
+    // elements of the row's warp `w` of the block
+    auto count = [&](int w) {
+      const int t0 = (w * 32) & (tpr - 1), whole = nvec >> log_tpr;
+      const int rest = min(max(nvec - (whole << log_tpr) - t0, 0), 32);
+      return (float)((whole * 32 + rest) * VE + (t0 == 0 ? lead + behind : 0));
+    };
+    const float n = WARP ? count(threadIdx.x >> 5) : (float)k;
+    float mu, m2;
+    row_moments<WARP>(
+        sum2(s) + e,
+        [&](float m) {
+          const Pair neg = pair(-m, -m);
+          Pair q = 0;
+#pragma unroll
+          for (int j = 0; j < NV; ++j) {
+            if (j * tpr + t < nvec) {
+              Pair v[VE / 2];
+              vec_pairs<X>(raw[j], v);
+#pragma unroll
+              for (int i = 0; i < VE / 2; ++i) {
+                v[i] = add2(v[i], neg);
+                q = fma2(v[i], v[i], q);
+              }
+            }
+          }
+          return has_one ? fmaf(e - m, e - m, sum2(q)) : sum2(q);
+        },
+        tpr, n > 0.f ? 1.f / n : 0.f, inv_k, count, part[p], mu, m2);
+    const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
+    if (!in) continue;
+    const float shift = -mu * rstd;
+    const Pair r2 = pair(rstd, rstd), c2 = pair(shift, shift);
+    X* y = static_cast<X*>(a.Y) + row * a.ld_y;
+    uint32_t at[VE];  // of the weights of the thread's first vector
+#pragma unroll
+    for (int i = 0; i < VE; ++i) at[i] = gb0 + 8u * (uint32_t)(((lead + i) & (VE - 1)) * pitch + ((lead + i) / VE));
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (j * tpr + t < nvec) {
+        Pair v[VE / 2];
+        vec_pairs<X>(raw[j], v);
+#pragma unroll
+        for (int i = 0; i < VE / 2; ++i) {
+          const float2 f = split(fma2(v[i], r2, c2));
+          const float2 w0 = lds_f32x2(at[2 * i] + 8u * (uint32_t)(j * tpr)), w1 = lds_f32x2(at[2 * i + 1] + 8u * (uint32_t)(j * tpr));
+          v[i] = pair(fmaf(f.x, w0.x, w0.y), fmaf(f.y, w1.x, w1.y));
+        }
+        store_vec<X>(y + lead, j * tpr + t, v);
+      }
+    }
+    if (take) {
+      const float2 w = gb[(col & (VE - 1)) * pitch + col / VE];
+      store_one(y + col, fmaf(fmaf(e, rstd, shift), w.x, w.y));
+    }
+    if (t == 0) {
+      a.mean[row] = mu;
+      a.rstd[row] = rstd;
+    }
+  }
+}
+
+// Rows of X and of Y that start on different places: elements one by one, NV of them
+// per thread.
 template <typename X, int NV, int THREADS, bool WARP>
 __global__ void __launch_bounds__(THREADS, single_blocks(THREADS)) norm_forward_single_kernel(const NormForward a, int tpr) {
   extern __shared__ __align__(128) float weights[];
@@ -431,7 +524,7 @@ __global__ void __launch_bounds__(THREADS, single_blocks(THREADS)) norm_forward_
             if (j < mine) q = fmaf(f[j] - m, f[j] - m, q);
           return q;
         },
-        tpr, inv_n, inv_k, counts, part[p], mu, m2);
+        tpr, inv_n, inv_k, [&](int w) { return counts[w]; }, part[p], mu, m2);
     const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
     if (!in) continue;
     X* y = static_cast<X*>(a.Y) + row * a.ld_y + t;
@@ -820,6 +913,11 @@ bool whole_vectors(const void* p, int64_t ld, int64_t k, int ve, size_t size) {
   return reinterpret_cast<uintptr_t>(p) % (ve * size) == 0 && ld % ve == 0 && k % ve == 0;
 }
 
+// Whether each row of Y starts as far from a 16-byte boundary as the one of X.
+bool same_places(const void* x, int64_t ld_x, const void* y, int64_t ld_y, size_t size) {
+  return (reinterpret_cast<uintptr_t>(x) - reinterpret_cast<uintptr_t>(y)) % 16 == 0 && (ld_x - ld_y) * (int64_t)size % 16 == 0;
+}
+
 // Threads per row: the fewest (of at most `limit`) that hold a row at `most`
 // vectors each, then more while the launch would leave SMs without a block.
 int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
@@ -831,7 +929,7 @@ int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
 
 template <int THREADS, typename Kernel>
 cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, int per_sm, cudaStream_t stream) {
-  const size_t smem = (size_t)a.k * 8;
+  const size_t smem = ((size_t)a.k + 8) * 8;  // the shifted kernel's pitch rounds up
   if (smem > 48u * 1024u) {
     const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
@@ -846,23 +944,28 @@ cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, int per
 
 // Blocks of 256 threads, two to an SM, up to rows of 4096, else one of 1024
 // (whose threads have half the registers).
-template <typename X, int VE, int THREADS>
+template <typename X, int THREADS>
 cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
-  constexpr int kMost = forward_bytes(THREADS) / (VE * (int)sizeof(X)), kPerSm = forward_blocks(THREADS);
+  constexpr int VE = 16 / (int)sizeof(X), kMost = forward_bytes(THREADS) / 16, kPerSm = forward_blocks(THREADS);
   const int tpr = threads_per_row(a.k / VE, kMost, a.T, THREADS);
   if constexpr (THREADS == 256) {
     if (tpr < 32)
-      return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, false, false>, a, tpr, kPerSm, stream);
+      return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, false>, a, tpr, kPerSm, stream);
   }
-  if constexpr (VE * sizeof(X) == 16) {
-    if (a.k == (int64_t)VE * kMost * tpr)
-      return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, true, true>, a, tpr, kPerSm, stream);
-  }
-  return launch_forward<THREADS>(norm_forward_kernel<X, VE, THREADS, false, true>, a, tpr, kPerSm, stream);
+  if (a.k == (int64_t)VE * kMost * tpr)
+    return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, true, true>, a, tpr, kPerSm, stream);
+  return launch_forward<THREADS>(norm_forward_kernel<X, THREADS, false, true>, a, tpr, kPerSm, stream);
 }
-template <typename X, int VE>
-cudaError_t forward_vectors(const NormForward& a, cudaStream_t stream) {
-  return a.k <= 4096 ? forward_vectors<X, VE, 256>(a, stream) : forward_vectors<X, VE, 1024>(a, stream);
+template <typename X, int THREADS>
+cudaError_t forward_shifted(const NormForward& a, cudaStream_t stream) {
+  constexpr int VE = 16 / (int)sizeof(X);
+  int tpr = threads_per_row(a.k / VE, forward_bytes(THREADS) / 16, a.T, THREADS);
+  if (tpr < 2 * VE) tpr = 2 * VE;  // a thread for each of the elements beside the vectors
+  if constexpr (THREADS == 256) {
+    if (tpr < 32)
+      return launch_forward<THREADS>(norm_forward_shifted_kernel<X, THREADS, false>, a, tpr, forward_blocks(THREADS), stream);
+  }
+  return launch_forward<THREADS>(norm_forward_shifted_kernel<X, THREADS, true>, a, tpr, forward_blocks(THREADS), stream);
 }
 template <typename X>
 cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
@@ -987,14 +1090,12 @@ cudaError_t backward_wide(const NormBackward& a, cudaStream_t stream) {
 
 template <typename X>
 cudaError_t forward_any(const NormForward& a, cudaStream_t stream) {
-  auto vectors = [&](int ve) { return whole_vectors(a.X, a.ld_x, a.k, ve, sizeof(X)) && whole_vectors(a.Y, a.ld_y, a.k, ve, sizeof(X)); };
+  constexpr int VE = 16 / (int)sizeof(X);
   if (a.k <= kMaxRowWidth) {
-    constexpr int kWide = 16 / (int)sizeof(X);
-    if (vectors(kWide)) return forward_vectors<X, kWide>(a, stream);
-    if (vectors(kWide / 2)) return forward_vectors<X, kWide / 2>(a, stream);
-    if constexpr (kWide == 8) {
-      if (vectors(2)) return forward_vectors<X, 2>(a, stream);
-    }
+    if (whole_vectors(a.X, a.ld_x, a.k, VE, sizeof(X)) && whole_vectors(a.Y, a.ld_y, a.k, VE, sizeof(X)))
+      return a.k <= 4096 ? forward_vectors<X, 256>(a, stream) : forward_vectors<X, 1024>(a, stream);
+    if (same_places(a.X, a.ld_x, a.Y, a.ld_y, sizeof(X)))
+      return a.k <= 4096 ? forward_shifted<X, 256>(a, stream) : forward_shifted<X, 1024>(a, stream);
     return forward_singles<X>(a, stream);
   }
   count_launch();

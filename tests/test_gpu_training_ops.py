@@ -234,6 +234,33 @@ def test_norm_many_rows_of_every_width(T, k, x):
     within(db, dy.sum(0), nt * dy.abs().sum(0))
 
 
+@pytest.mark.parametrize("x", [BF, F32])
+@pytest.mark.parametrize("ox,oy,pad_x,pad_y", [(1, 1, 0, 0), (3, 3, 9, 17), (0, 1, 0, 0), (2, 1, 1, 4), (5, 0, 3, 0)])
+@pytest.mark.parametrize("T,k", [(3, 1), (40, 5), (9000, 33), (3000, 259), (700, 2050), (40, 4098), (330, 6001), (9, 16384)])
+def test_norm_forward_rows_on_any_place(T, k, ox, oy, pad_x, pad_y, x):
+    """X and Y may start on the same place between two 16-byte boundaries or on different ones, rows too."""
+    g = gen(T + 7 * k)
+    X = randn(g, T, k, dtype=x) + 0.25
+    gamma, beta = randn(g, k), randn(g, k)
+    eps = 1e-5
+    mean, rstd = (torch.full((T,), float("nan"), device=DEV) for _ in range(2))
+    Xp = rows(X, k + pad_x, ox)
+    buf = torch.full((oy + T * (k + pad_y) + 16,), 7.0, dtype=x, device=DEV)
+    Y = torch.as_strided(buf, (T, k), (k + pad_y, 1), oy)
+    rgs.layer_norm_forward(Xp, gamma, beta, Y, mean, rstd, eps=eps)
+    y, m, r = norm64(X, gamma, beta, eps)
+    dmean, drel = norm_bounds(X, eps, k)
+    within(mean, m, dmean + 1e-30)
+    within(rstd, r, drel * r)
+    xh = (X.to(F64) - m[:, None]).abs() * r[:, None]
+    bound = ((dmean * r)[:, None] + xh * (drel[:, None] + 2.0 ** -22)) * gamma.to(F64).abs()
+    bound = bound + (y.abs() + beta.to(F64).abs()) * 2.0 ** -23
+    within(Y, y, bound * 1.01 + y.abs() * (2.0 ** -8 if x == BF else 0.0) + 1e-30)
+    kept = torch.zeros(buf.numel(), dtype=torch.bool, device=DEV)
+    torch.as_strided(kept, Y.shape, Y.stride(), oy).fill_(True)
+    assert (buf[~kept] == 7.0).all()
+
+
 def test_norm_gradient_against_differences():
     """<dX, u>, <dgamma, a> and <dbeta, b> against central differences of sum(dY * LN(X)) in 64 bits."""
     g = gen(11)
