@@ -27,13 +27,16 @@
 // again.  32768 x 4096 BF16: 141 us, 0.84 of the copy rate over 6 bytes an element.
 //
 // Elements come in vectors of 16 bytes (VE of them).  Rows that do not start on 16
-// bytes or end inside a vector: the forward pass takes the vectors between a row's
-// first and last boundary, and the elements beside those one by one (16384 x 4095
-// BF16: 58 us, 0.68 of the copy rate; single elements all along take 150).  The
-// backward pass's copies start and end at the 16-byte boundaries around a row (the
-// bytes beyond belong to the neighbouring rows; a row at an end of the matrix, which
-// has none, is brought in exactly), and elements are picked one by one in shared
-// memory (VE = 1).
+// bytes or end inside a vector: both passes take the vectors between a row's first
+// and last boundary, and the elements beside those one by one, as long as all
+// matrices' rows start on the same place between two boundaries (16384 x 4095 BF16:
+// 58 us forward, 0.68 of the copy rate, and 97 us backward, 0.61; single elements all
+// along take 148 and 136).  The place comes again after at most 8 rows, and the
+// backward pass gives a block rows that far apart, so that its threads' columns stay
+// the same.  Its copies start and end at the boundaries around a row (the bytes beyond
+// belong to the neighbouring rows; a row at an end of the matrix, which has none, is
+// brought in exactly).  Where the matrices' rows start on different places, elements
+// are read one by one (backward: VE = 1, from shared memory).
 //
 // Backward: each block leaves one partial row of dgamma and dbeta, and
 // norm_grad_sum_kernel adds those.  Rows wider than 16384 take the kernels at the
@@ -145,6 +148,7 @@ struct Ring {
   int slots;
   int rows;           // rows per set
   int each;           // of them, rows per group of tpr threads
+  int classes;        // SHIFT: rows this far apart start on the same place between two 16-byte boundaries
 };
 
 // Where row `row` starts inside its place in the slot: its own 16-byte phase.
@@ -153,13 +157,14 @@ __device__ __forceinline__ uint32_t phase(const RowSource& m, int64_t row) {
 }
 
 // A warp: start the copies of one set of rows into slot `s`, N matrices one after
-// another, completing on `bar`.
-template <int VE, int N>
+// another, completing on `bar`.  EDGES: rows that do not start and end on 16 bytes;
+// SHIFT: all of them on the same place between two boundaries.
+template <bool EDGES, bool SHIFT, int N>
 __device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N], int s, int64_t first, uint64_t* bar) {
   const int lane = threadIdx.x & 31;
   const uint32_t dst0 = r.smem + (uint32_t)s * r.slot;
   const int rows = (int)(m[0].T - first < r.rows ? m[0].T - first : r.rows);
-  if constexpr (VE > 1) {
+  if constexpr (!EDGES) {
     if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(N * rows) * m[0].width);
     __syncwarp();
 #pragma unroll
@@ -173,6 +178,14 @@ __device__ __forceinline__ void fill_slot(const Ring& r, const RowSource (&m)[N]
           tc::bulk_load_1d(dst + (uint32_t)q * r.pitch, src + q * m[i].ld, m[i].width, bar);
       }
     }
+  } else if (SHIFT && first > 0 && first + r.rows < m[0].T) {  // no row at an end of the matrix
+    const uint32_t ph = phase(m[0], 0), bytes = (ph + m[0].width + 15u) & ~15u;
+    if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(N * rows) * bytes);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      for (int q = lane; q < rows; q += 32)
+        tc::bulk_load_1d(dst0 + (uint32_t)(i * r.rows + q) * r.pitch, m[i].base + (first + q) * m[i].ld - ph, bytes, bar);
   } else {
     // twice over the rows: their bytes (and the single elements), then the copies
     uint32_t sum = 0;
@@ -544,8 +557,10 @@ constexpr int blocks_per_sm(int threads) { return threads == 256 ? 2 : 1; }
 constexpr int backward_rows_each(size_t size, int threads) { return threads == 256 && size == 2 ? 2 : 1; }
 
 // A thread's columns: NV vectors of VE elements, as E / 2 pairs.  With VE = 1 a pair
-// is the thread's elements 2 q and 2 q + 1, tpr columns apart.
-template <typename X, int VE, int NV, int THREADS, bool FULL, bool WARP>
+// is the thread's elements 2 q and 2 q + 1, tpr columns apart.  SHIFT: the vectors
+// between a row's first and last 16-byte boundary, and one of the elements beside
+// those; a block keeps to rows that start on the same place, `classes` apart.
+template <typename X, int VE, int NV, int THREADS, bool FULL, bool WARP, bool SHIFT = false>
 __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
     norm_backward_kernel(const NormBackward a, const Ring ring, int tpr, int* err) {
   constexpr int E = NV * VE, B = backward_rows_each(sizeof(X), THREADS);
@@ -558,12 +573,19 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
   Ring r = ring;
   r.smem = tc::smem_u32(ring_mem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const RowSource m[2] = {
-      {static_cast<const char*>(a.X), a.ld_x * (int64_t)sizeof(X), a.T, (uint32_t)(a.k * sizeof(X))},
-      {static_cast<const char*>(a.dY), a.ld_dy * (int64_t)sizeof(X), a.T, (uint32_t)(a.k * sizeof(X))}};
-  const int64_t stride = (int64_t)gridDim.x * r.rows;
-  const int64_t first = (int64_t)blockIdx.x * r.rows;
-  const int passes = (int)((a.T - first + stride - 1) / stride);
+  // SHIFT: the block's class of rows as matrices of their own
+  const int classes = SHIFT ? r.classes : 1, cls = SHIFT ? (int)blockIdx.x % classes : 0;
+  const int64_t block = SHIFT ? blockIdx.x / classes : blockIdx.x, blocks = SHIFT ? gridDim.x / classes : gridDim.x;
+  const int64_t rows_in = SHIFT ? (a.T - cls + classes - 1) / classes : a.T;
+  auto source = [&](const void* p, int64_t ld) {
+    ld *= (int64_t)sizeof(X);
+    return RowSource{static_cast<const char*>(p) + cls * ld, ld * classes, rows_in, (uint32_t)(a.k * sizeof(X))};
+  };
+  const RowSource m[2] = {source(a.X, a.ld_x), source(a.dY, a.ld_dy)};
+  const float *mean = a.mean + cls, *row_rstd = a.rstd + cls;
+  const int64_t stride = blocks * r.rows;
+  const int64_t first = block * r.rows;
+  const int passes = first < rows_in ? (int)((rows_in - first + stride - 1) / stride) : 0;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     for (int s = 0; s < r.slots; ++s) tc::mbar_init(&full[s], 1);
@@ -573,12 +595,20 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
   __syncthreads();
   int filled = 0;  // warp 0's: sets whose copies have begun
   if (warp == 0)
-    for (; filled < passes && filled < r.slots; ++filled) fill_slot<VE, 2>(r, m, filled, first + filled * stride, &full[filled]);
+    for (; filled < passes && filled < r.slots; ++filled) fill_slot<VE == 1 || SHIFT, SHIFT, 2>(r, m, filled, first + filled * stride, &full[filled]);
   const int t = threadIdx.x & (tpr - 1), group = threadIdx.x / tpr, groups = THREADS / tpr, k = (int)a.k;
   const int warps = tpr >> 5, warp0 = (threadIdx.x & ~(tpr - 1)) >> 5;
-  const int nvec = k / VE;
+  // SHIFT: elements before the first vector; the place of a row's first element, of its first vector
+  const uint32_t place = SHIFT ? phase(m[0], 0) : 0u, vec_place = (place + 15u) & ~15u;
+  const int lead = SHIFT ? min((int)((vec_place - place) / sizeof(X)), k) : 0;
+  const int nvec = (k - lead) / VE, end = SHIFT ? lead + nvec * VE : k;
+  // this thread's element beside the vectors: one of the first `lead`, or of those
+  // behind; the row's last threads have them, the first warp having the copies
+  const int u = t - (tpr - 2 * VE);
+  const bool has_one = SHIFT && u >= 0 && (u < lead || (u >= VE && u < VE + k - end));
+  const int one = u < lead ? u : end + u - VE;
   // column of element i of pair q of step j; whether the thread has it
-  auto column = [&](int j, int q, int i) { return VE == 1 ? (2 * j + i) * tpr + t : (j * tpr + t) * VE + 2 * q + i; };
+  auto column = [&](int j, int q, int i) { return VE == 1 ? (2 * j + i) * tpr + t : lead + (j * tpr + t) * VE + 2 * q + i; };
   auto has = [&](int j) { return FULL || (VE == 1 ? 2 * j * tpr + t < k : j * tpr + t < nvec); };
   // VE = 1: the pair's second element may lie past the row; a zero stands for it
   auto read = [&](uint32_t at, int j, Pair (&v)[VP]) {
@@ -595,6 +625,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
     }
   };
   Pair dg[E / 2], db[E / 2], gamma[HOLD ? E / 2 : 1];
+  float dg_one = 0.f, db_one = 0.f;
   // wide rows: gamma behind the ring, as the forward pass lays it out
   float* gmem = reinterpret_cast<float*>(ring_mem + (size_t)r.slots * r.slot);
   {
@@ -603,11 +634,12 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
         const int c = 2 * j * tpr + t;
         g[0] = pair(gmem[c], c + tpr < k ? gmem[c + tpr] : 0.f);
       } else {
-        weight_pairs<VE>(tc::smem_u32(gmem), j * tpr + t, k, g);
+        weight_pairs<VE>(tc::smem_u32(gmem), j * tpr + t, end - lead, g);
       }
     };
     if constexpr (!HOLD) {
-      for (int c = threadIdx.x; c < k; c += THREADS) gmem[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
+      for (int c = lead + threadIdx.x; c < end; c += THREADS)
+        gmem[weight_at<VE>(c - lead, end - lead)] = weight(a.gamma, a.w_type, c, 1.f);
       __syncthreads();
     }
 #pragma unroll
@@ -616,14 +648,21 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
       for (int q = 0; q < VP; ++q) {
         const int c0 = column(j, q, 0), c1 = column(j, q, 1);
         if constexpr (HOLD)
-          gamma[j * VP + q] = pair(FULL || c0 < k ? weight(a.gamma, a.w_type, c0, 1.f) : 0.f,
-                                   FULL || c1 < k ? weight(a.gamma, a.w_type, c1, 1.f) : 0.f);
+          gamma[j * VP + q] = pair(FULL || c0 < end ? weight(a.gamma, a.w_type, c0, 1.f) : 0.f,
+                                   FULL || c1 < end ? weight(a.gamma, a.w_type, c1, 1.f) : 0.f);
         dg[j * VP + q] = db[j * VP + q] = 0;
       }
     }
+    const float gamma_one = has_one ? weight(a.gamma, a.w_type, one, 1.f) : 0.f;
     const float inv_k = 1.f / (float)k;
     // rows, row strides (below 2^31) and their products in 32 x 32 -> 64 bits
-    const uint32_t T = (uint32_t)a.T, step = (uint32_t)stride, ld_dx = (uint32_t)(a.ld_dx * sizeof(X) >> 1);
+    const uint32_t T = (uint32_t)rows_in, step = (uint32_t)stride;
+    using Stride = std::conditional_t<SHIFT, uint64_t, uint32_t>;
+    const Stride ld_dx = (Stride)((a.ld_dx * sizeof(X) >> 1) * classes);
+    auto row_dx = [&](uint32_t i) {
+      char* p = static_cast<char*>(a.dX) + 2 * ((uint64_t)i * ld_dx);
+      return reinterpret_cast<X*>(SHIFT ? p + cls * a.ld_dx * (int64_t)sizeof(X) : p);
+    };
     uint32_t row = (uint32_t)first + group * r.each;
     float nmu[B], nrs[B];  // the next set's
     auto load_stats = [&](uint32_t at) {
@@ -631,13 +670,14 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
       for (int b = 0; b < B; ++b) {
         nmu[b] = nrs[b] = 0.f;
         if (b < r.each && at + b < T) {
-          nmu[b] = a.mean[at + b];
-          nrs[b] = a.rstd[at + b];
+          nmu[b] = mean[(at + b) * classes];
+          nrs[b] = row_rstd[(at + b) * classes];
         }
       }
     };
     load_stats(row);
-    const uint32_t vec0 = 16u * t;
+    const uint32_t vec0 = 16u * t + vec_place;
+    const uint32_t one_at = r.smem + place + (uint32_t)(one * (int)sizeof(X)) - vec0;  // from the thread's first vector
     const uint32_t set_at = (uint32_t)(group * r.each) * r.pitch, y_at = (uint32_t)r.rows * r.pitch;
     uint32_t slot = set_at;  // in the ring
     int s = 0;
@@ -694,6 +734,11 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
       for (int b = 0; b < B; ++b) {
         v[2 * b] = sum2(s0[b]);
         v[2 * b + 1] = sum2(s1[b]);
+        if (SHIFT && has_one) {
+          const float d = read_one<X>(ay[b] + one_at) * gamma_one;
+          v[2 * b] += d;
+          v[2 * b + 1] = fmaf(d, fmaf(read_one<X>(ax[b] + one_at), rstd[b], split(mrs[b]).x), v[2 * b + 1]);
+        }
       }
       lane_sums<WARP, 2 * B>(v, tpr);
       float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
@@ -704,7 +749,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
       __syncthreads();
       if (warp == 0 && p > 0 && filled < passes && r.slots > 1) {  // every thread is done with the set before
         const int before = s ? s - 1 : r.slots - 1;
-        fill_slot<VE, 2>(r, m, before, first + filled * stride, &full[before]);
+        fill_slot<VE == 1 || SHIFT, SHIFT, 2>(r, m, before, first + filled * stride, &full[before]);
         ++filled;
       }
       if (WARP && warps > 1) {
@@ -724,7 +769,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
 #pragma unroll
         for (int b = 0; b < B; ++b) {
           if (!WHOLE && (b >= r.each || row + b >= T)) continue;
-          X* dx = reinterpret_cast<X*>(static_cast<char*>(a.dX) + 2 * ((uint64_t)(row + b) * ld_dx));
+          X* dx = row_dx(row + b);
           const float f0 = -v[2 * b] * inv_k * rstd[b], f1 = -v[2 * b + 1] * inv_k * rstd[b];
           const Pair c0 = pair(f0, f0), c1 = pair(f1, f1);
 #pragma unroll
@@ -750,9 +795,15 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
                   if (c + tpr < k) store_one(dx + c + tpr, f.y);
                 }
               } else {
-                if (a.dX) store_vec<X>(dx, j * tpr + t, y);
+                if (a.dX) store_vec<X>(dx + lead, j * tpr + t, y);
               }
             }
+          }
+          if (SHIFT && has_one) {
+            const float x = fmaf(read_one<X>(ax[b] + one_at), rstd[b], split(mrs[b]).x), y = read_one<X>(ay[b] + one_at);
+            dg_one = fmaf(y, x, dg_one);
+            db_one += y;
+            if (a.dX) store_one(dx + one, fmaf(y * gamma_one, rstd[b], fmaf(x, f1, f0)));
           }
         }
       };
@@ -760,7 +811,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
       else second(std::false_type{});
       if (r.slots == 1 && p + 1 < passes) {  // fp32 rows too wide for two slots
         __syncthreads();
-        if (warp == 0) fill_slot<VE, 2>(r, m, 0, first + filled * stride, &full[0]);
+        if (warp == 0) fill_slot<VE == 1 || SHIFT, SHIFT, 2>(r, m, 0, first + filled * stride, &full[0]);
         ++filled;
       }
       slot += r.slot;
@@ -787,10 +838,11 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
         for (int q = 0; q < VP; ++q) {
           const float2 f = split(half ? db[j * VP + q] : dg[j * VP + q]);
           const int c0 = column(j, q, 0), c1 = column(j, q, 1);
-          if (FULL || c0 < k) to[c0] = f.x;
-          if (FULL || c1 < k) to[c1] = f.y;
+          if (FULL || c0 < end) to[c0] = f.x;
+          if (FULL || c1 < end) to[c1] = f.y;
         }
       }
+      if (has_one) to[one] = half ? db_one : dg_one;
     }
     if (groups > 1) {
       __syncthreads();
@@ -977,12 +1029,12 @@ cudaError_t forward_singles(const NormForward& a, cudaStream_t stream) {
 
 // The ring for sets of rows of `matrices` matrices, with `beside` bytes of shared
 // memory behind it; 0 slots where not even one fits.
-Ring make_ring(int64_t k, size_t size, int ve, int groups, int each, int matrices, int threads, size_t beside) {
+Ring make_ring(int64_t k, size_t size, bool edges, int groups, int each, int matrices, int threads, size_t beside) {
   Ring r = {};
   r.rows = groups * each;
   r.each = each;
-  // VE = 1: room for 16-byte boundaries around a row
-  r.pitch = ve > 1 ? (uint32_t)(k * size) : (uint32_t)((k * size + 15) / 16 * 16 + 16);
+  // edges: room for 16-byte boundaries around a row
+  r.pitch = !edges ? (uint32_t)(k * size) : (uint32_t)((k * size + 15) / 16 * 16 + 16);
   r.slot = r.pitch * (uint32_t)(r.rows * matrices);
   const uint32_t room = ((blocks_per_sm(threads) == 2 ? 108u : 216u) << 10) - (uint32_t)beside;
   r.slots = (int)(room / r.slot < kMaxSlots ? room / r.slot : kMaxSlots);
@@ -1030,22 +1082,24 @@ cudaError_t launch_grad_sum(const NormBackward& a, int partials, cudaStream_t st
                             a.overwrite);
 }
 
-template <typename X, int VE, int NV, int THREADS>
-cudaError_t backward_rows(const NormBackward& a, int tpr, bool& done, cudaStream_t stream) {
+template <typename X, int VE, int NV, int THREADS, bool SHIFT>
+cudaError_t backward_rows(const NormBackward& a, int tpr, int classes, bool& done, cudaStream_t stream) {
   const int groups = THREADS / tpr;
   const int each = rows_each(backward_rows_each(sizeof(X), THREADS), a.T, groups, THREADS);
   int64_t blocks = ceil_div(a.T, groups * each);
   const int64_t most = (int64_t)num_sms() * blocks_per_sm(THREADS);
   if (blocks > most) blocks = most;
   if (blocks > kMaxPartials) blocks = kMaxPartials;
+  if (SHIFT) blocks = blocks < classes ? classes : blocks / classes * classes;
   const size_t beside = VE * NV > 16 ? (size_t)a.k * 4 : 0;  // gamma
-  const Ring r = make_ring(a.k, sizeof(X), VE, groups, each, 2, THREADS, beside);
+  Ring r = make_ring(a.k, sizeof(X), VE == 1 || SHIFT, groups, each, 2, THREADS, beside);
+  r.classes = classes;
   if (r.slots < 1) return cudaSuccess;
   done = true;
   const size_t room = groups > 1 ? (size_t)groups * a.k * 4 : (size_t)r.slots * r.slot + beside;
   cudaError_t err = cudaSuccess;
   bool full = false;
-  if constexpr (VE > 1) {
+  if constexpr (VE > 1 && !SHIFT) {
     full = a.k == (int64_t)VE * NV * tpr && tpr >= 32;
     if (full)
       err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, true, true>, a, r, tpr, THREADS, blocks, room, stream);
@@ -1053,22 +1107,23 @@ cudaError_t backward_rows(const NormBackward& a, int tpr, bool& done, cudaStream
   if constexpr (THREADS == 256) {
     if (tpr < 32) {
       full = true;
-      err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, false>, a, r, tpr, THREADS, blocks, room, stream);
+      err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, false, SHIFT>, a, r, tpr, THREADS, blocks, room, stream);
     }
   }
   if (!full)
-    err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, true>, a, r, tpr, THREADS, blocks, room, stream);
+    err = launch_rows(norm_backward_kernel<X, VE, NV, THREADS, false, true, SHIFT>, a, r, tpr, THREADS, blocks, room, stream);
   if (err == cudaSuccess && (a.dgamma || a.dbeta)) err = launch_grad_sum(a, (int)blocks, stream);
   return err;
 }
 
-template <typename X, int VE>
-cudaError_t backward(const NormBackward& a, bool& done, cudaStream_t stream) {
+template <typename X, int VE, bool SHIFT>
+cudaError_t backward(const NormBackward& a, int classes, bool& done, cudaStream_t stream) {
   constexpr int kNV = 16 / VE;  // 16 elements of a row per thread, 32 above 8192
-  const int tpr = threads_per_row(a.k / VE, kNV, a.T, 512);
-  if (tpr <= 256) return backward_rows<X, VE, kNV, 256>(a, tpr, done, stream);
-  if (a.k <= 8192) return backward_rows<X, VE, kNV, 512>(a, 512, done, stream);
-  return backward_rows<X, VE, 2 * kNV, 512>(a, 512, done, stream);
+  int tpr = threads_per_row(a.k / VE, kNV, a.T, 512);
+  if (SHIFT && tpr < 2 * VE) tpr = 2 * VE;  // a thread for each of the elements beside the vectors
+  if (tpr <= 256) return backward_rows<X, VE, kNV, 256, SHIFT>(a, tpr, classes, done, stream);
+  if (a.k <= 8192) return backward_rows<X, VE, kNV, 512, SHIFT>(a, 512, classes, done, stream);
+  return backward_rows<X, VE, 2 * kNV, 512, SHIFT>(a, 512, classes, done, stream);
 }
 
 template <typename X>
@@ -1109,10 +1164,16 @@ cudaError_t backward_any(const NormBackward& a, cudaStream_t stream) {
   bool done = false;
   cudaError_t err = cudaSuccess;
   if (a.k <= kMaxRowWidth) {
-    const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE, sizeof(X)) &&
-                         whole_vectors(a.dY, a.ld_dy, a.k, VE, sizeof(X)) &&
-                         (a.dX == nullptr || whole_vectors(a.dX, a.ld_dx, a.k, VE, sizeof(X)));
-    err = vectors ? backward<X, VE>(a, done, stream) : backward<X, 1>(a, done, stream);
+    auto vectors = [&](const void* p, int64_t ld) { return p == nullptr || whole_vectors(p, ld, a.k, VE, sizeof(X)); };
+    auto same = [&](const void* p, int64_t ld) { return p == nullptr || same_places(a.X, a.ld_x, p, ld, sizeof(X)); };
+    int classes = 1;  // rows after which the place between two boundaries comes again
+    while (a.ld_x * (int64_t)sizeof(X) * classes % 16 != 0) classes *= 2;
+    if (vectors(a.X, a.ld_x) && vectors(a.dY, a.ld_dy) && vectors(a.dX, a.ld_dx))
+      err = backward<X, VE, false>(a, 1, done, stream);
+    else if (a.T >= classes && same(a.dY, a.ld_dy) && same(a.dX, a.ld_dx))
+      err = backward<X, VE, true>(a, classes, done, stream);
+    else
+      err = backward<X, 1, false>(a, 1, done, stream);
   }
   return (done || err != cudaSuccess) ? err : backward_wide<X>(a, stream);
 }

@@ -261,6 +261,44 @@ def test_norm_forward_rows_on_any_place(T, k, ox, oy, pad_x, pad_y, x):
     assert (buf[~kept] == 7.0).all()
 
 
+@pytest.mark.parametrize("x", [BF, F32])
+@pytest.mark.parametrize("offsets,pads", [((1, 1, 1), (0, 0, 0)), ((3, 3, 3), (1, 9, 17)), ((0, 1, 0), (0, 0, 0)),
+                                          ((2, 2, 1), (3, 3, 2)), ((0, 0, 0), (2, 2, 10))])
+@pytest.mark.parametrize("T,k", [(7, 33), (8, 16), (9000, 37), (3000, 261), (700, 2051), (400, 4098), (330, 6001),
+                                 (17, 16381)])
+def test_norm_backward_rows_on_any_place(T, k, offsets, pads, x):
+    """dY, X and dX may start on the same place between two 16-byte boundaries or on different ones, rows too."""
+    g = gen(T + 11 * k)
+    X, dY, gamma = randn(g, T, k, dtype=x), randn(g, T, k, dtype=x), randn(g, k)
+    eps = 1e-3
+    _, m, r = norm64(X, None, None, eps)
+    mean, rstd = m.float(), r.float()
+    dx, dg, db, xh, d, r = norm_grads64(dY, X, gamma, eps)
+    bufs, views = [], []
+    for t, o, p in zip((X, dY, torch.zeros_like(X)), offsets, pads):
+        buf = torch.full((o + T * (k + p) + 16,), float("nan"), dtype=x, device=DEV)
+        view = torch.as_strided(buf, (T, k), (k + p, 1), o)
+        view.copy_(t)
+        bufs.append(buf)
+        views.append(view)
+    Xp, dYp, dX = views
+    dgamma, dbeta = torch.empty(k, device=DEV), torch.empty(k, device=DEV)
+    rgs.layer_norm_backward(dYp, Xp, gamma, mean, rstd, dX, dgamma, dbeta, overwrite=True)
+    exh = 2.0 ** -22 * (xh.abs() + (m.abs() * r)[:, None])
+    n = (k + 16) * 2.0 ** -24
+    e0 = n * d.abs().mean(1, keepdim=True)
+    e1 = n * (d * xh).abs().mean(1, keepdim=True) + (d.abs() * exh).mean(1, keepdim=True)
+    s1 = (d * xh).mean(1, keepdim=True).abs()
+    ex = r[:, None] * (e0 + exh * s1 + xh.abs() * e1 + 2.0 ** -21 * (d.abs() + d.mean(1, keepdim=True).abs() + xh.abs() * s1))
+    within(dX, dx, ex * 1.01 + (dx.abs() * 2.0 ** -8 if x == BF else 0.0) + 1e-30)
+    nt = (T + 16) * 2.0 ** -24
+    within(dgamma, dg, nt * (dY.to(F64) * xh).abs().sum(0) + (dY.to(F64).abs() * exh).sum(0) + 1e-30)
+    within(dbeta, db, nt * dY.to(F64).abs().sum(0) + 1e-30)
+    kept = torch.zeros(bufs[2].numel(), dtype=torch.bool, device=DEV)
+    torch.as_strided(kept, dX.shape, dX.stride(), offsets[2]).fill_(True)
+    assert torch.isnan(bufs[2][~kept]).all()
+
+
 def test_norm_gradient_against_differences():
     """<dX, u>, <dgamma, a> and <dbeta, b> against central differences of sum(dY * LN(X)) in 64 bits."""
     g = gen(11)
