@@ -15,7 +15,12 @@
 //           target's left out; head_combine_kernel joins them per row
 //   dlogit  D from the logits and the row's lse, rounded to BF16 (as every D of
 //           this library is: the tensor cores take 16-bit operands; 2^-9 of each
-//           entry, independent over the terms that dX and dW add up)
+//           entry, independent over the terms that dX and dW add up).  D is in
+//           units of the largest |g scale|, which its products' results are
+//           multiplied by in fp32: with the usual mean over tokens all weights are
+//           that one, and the targets' entries, close to -1 for a small exp(l - lse),
+//           keep their values, where -g scale would be rounded the same way for
+//           every token (up to 0.2% of all gradients)
 //   dx      rows of dX, added up over the vocabulary's pieces in fp32
 //   dw      rows of dW
 // The backward pass walks the vocabulary in pieces, so that only T x piece
@@ -35,6 +40,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <type_traits>
 
@@ -93,6 +99,7 @@ struct HeadLaunch {
   // dlogit
   const float* lse_log2;  // per kept row: lse * log2(e)
   const float* weight;    // per kept row: g * scale
+  const float* factor;    // D is in units of it
   const int* target;      // per kept row
   uint16_t* D;
   int64_t ld_d;
@@ -454,7 +461,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         // rows past the kept ones are written as zeros up to the tile's end,
         // since they take part in dW's sum over rows
         const bool in = row < *a.kept;
-        const float w = in ? a.weight[row] : 0.f, l2 = in ? a.lse_log2[row] : 0.f;
+        const float w = in ? a.weight[row] / *a.factor : 0.f, l2 = in ? a.lse_log2[row] : 0.f;
         const int tcol = in ? a.target[row] - (a.d_first + col0) : -1;
         uint16_t* out = a.D + (int64_t)row * a.ld_d + col0;
         for (int cg = 0; cg < kHalf / 32; ++cg) {
@@ -477,6 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         }
       } else if (pr.epi == kEpiDx) {
         const bool in = row < *a.kept;
+        const float unit = *a.factor;
         float* sum = a.acc + t.part * a.acc_part + (int64_t)row * N + col0;
         uint16_t* out = (in && a.dx_last) ? a.dX + (int64_t)a.row_of[row] * a.ld_dx + col0 : nullptr;
         for (int cg = 0; cg < kHalf / 32; ++cg) {
@@ -497,6 +505,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
               f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
             }
             if (a.dx_last) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] *= unit;
               *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]),
                                                               pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
             } else {
@@ -507,11 +517,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
         }
       } else {
         const bool in = row < pr.M;
+        const float unit = *a.factor;
         for (int cg = 0; cg < kHalf / 32; ++cg) {
           __syncwarp();  // the load is the whole warp's
           tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
           tc::tmem_wait_ld_regs(v);
           if (!in) continue;
+#pragma unroll
+          for (int i = 0; i < 32; ++i)  // unfused: adding a gradient to itself doubles it
+            v[i] = __float_as_uint(__fmul_rn(__uint_as_float(v[i]), unit));
           const int64_t at = (int64_t)row * a.ld_dw + col0 + cg * 32;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -661,6 +675,7 @@ struct Gather {
   int64_t ld_xpc;
   float* lse_log2;
   float* weight;
+  float* factor;  // the largest finite |weight|, 1 where that is 0
   int* target;
   int* row_of;
   int* kept;
@@ -677,18 +692,23 @@ struct Gather {
 __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant__ Gather a) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
-  __shared__ int before_s, total_s, bad_s;
+  __shared__ int before_s, total_s, bad_s, top_s;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t base = (int64_t)blockIdx.x * a.per_block;
-  if (threadIdx.x == 0) before_s = total_s = bad_s = 0;
+  if (threadIdx.x == 0) before_s = total_s = bad_s = top_s = 0;
   __syncthreads();
   int before = 0, total = 0, bad = 0;
+  float top = 0.f;
   for (int64_t i = threadIdx.x; i < a.T; i += blockDim.x) {
     const int64_t t = a.targets[i];
     const int keep = t >= 0 && t < a.V;
     total += keep;
     before += keep && i < base;
     bad |= t >= a.V;
+    if (blockIdx.x == 0 && keep) {
+      const float w = fabsf(a.g[i] * a.scale);
+      if (w <= FLT_MAX) top = fmaxf(top, w);
+    }
   }
   before = __reduce_add_sync(0xFFFFFFFFu, before);
   total = __reduce_add_sync(0xFFFFFFFFu, total);
@@ -698,12 +718,14 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
     atomicAdd(&total_s, total);
     if (bad) bad_s = 1;
   }
+  if (top > 0.f) atomicMax(&top_s, __float_as_int(top));  // block 0's alone; positive floats compare as integers do
   __syncthreads();
   total = total_s;
   if (blockIdx.x == 0) {
     for (int i = threadIdx.x; i < a.n_counters; i += blockDim.x) a.counters[i] = 0;
     if (threadIdx.x == 0) {
       *a.kept = total;
+      *a.factor = top_s > 0 ? __int_as_float(top_s) : 1.f;
       if (a.status) *a.status = bad_s ? SKETCH_DEV_BAD_TARGET : 0;
     }
   }
@@ -752,9 +774,10 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
 
 // dX's kept rows from their `parts` fp32 parts, eight columns per thread.
 __global__ void __launch_bounds__(256) head_dx_sum_kernel(const float* acc, int64_t part, int parts, int64_t k,
-                                                          const int* kept, const int* row_of, uint16_t* dX,
-                                                          int64_t ld_dx) {
+                                                          const int* kept, const float* factor, const int* row_of,
+                                                          uint16_t* dX, int64_t ld_dx) {
   cudaGridDependencySynchronize();
+  const float unit = *factor;
   const int64_t per_row = k / 8, n = *kept * per_row;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i / per_row, c = (i - row * per_row) * 8;
@@ -768,8 +791,17 @@ __global__ void __launch_bounds__(256) head_dx_sum_kernel(const float* acc, int6
       y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
     }
     *reinterpret_cast<uint4*>(dX + (int64_t)row_of[row] * ld_dx + c) =
-        make_uint4(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w), pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+        make_uint4(pack_bf16(x.x * unit, x.y * unit), pack_bf16(x.z * unit, x.w * unit), pack_bf16(y.x * unit, y.y * unit),
+                   pack_bf16(y.z * unit, y.w * unit));
   }
+}
+
+// C (+)= factor S, for a piece of the vocabulary.
+__global__ void __launch_bounds__(256) head_sketch_add_kernel(const float* S, int64_t n, const float* factor, int overwrite,
+                                                              float* C) {
+  const float unit = *factor;
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x)
+    C[i] = overwrite ? unit * S[i] : __fadd_rn(C[i], __fmul_rn(unit, S[i]));  // unfused, as dW's sum
 }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
@@ -875,8 +907,10 @@ struct BackwardWorkspace {
   int64_t ld_xpc;
   uint16_t* D[2];
   float* acc;
+  float* S;           // a piece of the sketch, in units of the factor
   float* lse_log2;
   float* weight;
+  float* factor;
   int* target;
   int* row_of;
   int* kept;
@@ -897,8 +931,10 @@ BackwardWorkspace carve_backward(void* base, int64_t T, int64_t V, int64_t k, in
   for (int i = 0; i < 2; ++i) w.D[i] = cur.take<uint16_t>((size_t)((i == 0 || pieces > 1) ? rows * piece : 0));
   // split sums keep a part per piece and split, others are added up over the pieces
   w.acc = cur.take<float>((size_t)(w.parts > 1 ? pieces * w.parts * rows * k : pieces > 1 ? rows * k : 0));
+  w.S = cur.take<float>((size_t)((piece < V ? piece : V) * r));
   w.lse_log2 = cur.take<float>((size_t)rows);
   w.weight = cur.take<float>((size_t)rows);
+  w.factor = cur.take<float>(1);
   w.target = cur.take<int>((size_t)rows);
   w.row_of = cur.take<int>((size_t)rows);
   w.kept = cur.take<int>(1);
@@ -959,7 +995,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   g.XP = sketch ? f.XP : nullptr; g.ld_xp = f.ld_xp; g.r = f.r;
   g.V = f.V; g.targets = f.targets; g.lse = f.lse; g.g = f.g; g.scale = f.scale;
   g.Xc = w.Xc; g.XPc = w.XPc; g.ld_xpc = w.ld_xpc;
-  g.lse_log2 = w.lse_log2; g.weight = w.weight; g.target = w.target; g.row_of = w.row_of; g.kept = w.kept;
+  g.lse_log2 = w.lse_log2; g.weight = w.weight; g.factor = w.factor; g.target = w.target; g.row_of = w.row_of; g.kept = w.kept;
   g.dX = f.dX; g.ld_dx = f.ld_dx;
   g.counters = w.counters; g.n_counters = pieces + 1;
   g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
@@ -975,6 +1011,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   a.scale_log2 = f.scale * kLog2e;
   a.lse_log2 = w.lse_log2;
   a.weight = w.weight;
+  a.factor = w.factor;
   a.target = w.target;
   a.row_of = w.row_of;
   a.ld_d = piece;
@@ -1029,8 +1066,14 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
         a.dW = static_cast<char*>(f.dW) + (size_t)(v0 * f.ld_dw) * size;
       }
       if (sketch) {
-        AccumulateProblem ap = {D, rows, width, piece, w.XPc, w.ld_xpc, f.C + v0 * f.r};
-        err = launch_accumulate(1, &ap, (int)f.r, f.overwrite, stream);
+        AccumulateProblem ap = {D, rows, width, piece, w.XPc, w.ld_xpc, w.S};
+        err = launch_accumulate(1, &ap, (int)f.r, 1, stream);
+        if (err != cudaSuccess) return err;
+        const int64_t n = width * f.r, blocks = ceil_div(n, 256), most = 8 * (int64_t)num_sms();
+        count_launch();
+        head_sketch_add_kernel<<<(unsigned)(blocks < most ? blocks : most), 256, 0, stream>>>(w.S, n, w.factor, f.overwrite,
+                                                                                            f.C + v0 * f.r);
+        err = cudaGetLastError();
         if (err != cudaSuccess) return err;
       }
     }
@@ -1060,7 +1103,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   if (f.dX && w.parts > 1) {
     const int64_t blocks = ceil_div(f.T * (f.k / 8), 256), most = 8 * (int64_t)num_sms();
     return launch_after(head_dx_sum_kernel, (unsigned)(blocks < most ? blocks : most), 256, 0, stream, w.acc,
-                        rows * f.k, dx_sum_parts, f.k, w.kept, w.row_of, f.dX, f.ld_dx);
+                        rows * f.k, dx_sum_parts, f.k, w.kept, w.factor, w.row_of, f.dX, f.ld_dx);
   }
   return cudaSuccess;
 }

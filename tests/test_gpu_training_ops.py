@@ -451,6 +451,58 @@ def test_cross_entropy_head_sketch():
     assert torch.equal(only, dX)
 
 
+@pytest.mark.parametrize("V", [20000, 70001])
+@pytest.mark.parametrize("T", [3, 48])
+def test_cross_entropy_equal_weights_keep_the_targets_entries(T, V):
+    """The mean over tokens: -g (1 - p) of a target keeps its value to p or 2^-9 of g, whatever g's last bits are."""
+    k, r, up = 128, 16, 1.0 / 3.0
+    g = gen(T + V)
+    X, W, XP = randn(g, T, k, dtype=BF), randn(g, V, k, std=0.02, dtype=BF), randn(g, T, r, dtype=BF)
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV)
+    ups = torch.full((T,), up, device=DEV)
+    x, w = X.to(F64), W.to(F64)
+    logits = x @ w.t()
+    lse = torch.logsumexp(logits, 1)
+    p = torch.exp(logits - lse[:, None])
+    hit = torch.zeros(T, V, dtype=torch.bool, device=DEV)
+    hit[torch.arange(T, device=DEV), targets] = True
+    d = (p - hit.to(F64)) * float(ups[0])
+    # p from fp32 logits (magnitudes below 64) and fp32 exponentials: 2^-15; BF16: 2^-8 of p, of 1 - p at most p or 2^-9
+    ed = float(ups[0]) * (p * 2.0 ** -15 + torch.where(hit, p.clamp(max=2.0 ** -9), p * 2.0 ** -8) + 2.0 ** -22)
+    dX, dW, C = torch.empty_like(X), torch.empty(V, k, device=DEV), torch.empty(V, r, device=DEV)
+    rgs.cross_entropy_backward(X, W, targets, lse.float(), ups, dX=dX, dW=dW, overwrite=True)
+    rgs.cross_entropy_backward(X, W, targets, lse.float(), ups, XP=XP, C=C, overwrite=True)
+    for got, b in ((dW, x), (C, XP.to(F64))):
+        want = d.t() @ b
+        within(got, want, product_bound(d.t(), ed.t(), b) * 1.01 + want.abs() * 2.0 ** -22 + 1e-30)
+    want = d @ w
+    within(dX, want, product_bound(d, ed, w) * 1.01 + want.abs() * 2.0 ** -8)
+
+
+def test_cross_entropy_weights_of_every_size():
+    """Zero, tiny, huge, infinite and NaN weights: each token's dX follows its own weight."""
+    T, k, V = 6, 64, 700
+    X, W, targets, _ = ce_inputs(T, k, V, seed=6)
+    targets = targets.clamp(min=0)
+    _, _, lse, _ = ce64(X, W, targets, 1.0)
+    lse = lse.float()
+    nan, inf = float("nan"), float("inf")
+    zero = torch.zeros(T, device=DEV)
+    dX, dW = torch.full_like(X, nan), torch.full_like(W, nan)
+    rgs.cross_entropy_backward(X, W, targets, lse, zero, dX=dX, dW=dW, overwrite=True)
+    assert (dX == 0).all() and (dW == 0).all()
+    for weights in ([1e-30] * T, [1e30, 3e29, -1e30, 0.0, 7e28, 1e30], [1.0, inf, -0.5, 0.25, 0.0, 3.0],
+                    [nan, 1.0, 1.0, nan, 2.0, 0.5]):
+        up = torch.tensor(weights, device=DEV)
+        fine = torch.isfinite(up)
+        d, ed, x, w = ce_grads64(X, W, targets, torch.where(fine, up, 0.0), lse, 1.0)
+        dX = torch.empty_like(X)
+        rgs.cross_entropy_backward(X, W, targets, lse, up, dX=dX)
+        want = d @ w
+        within(dX[fine], want[fine], (product_bound(d, ed, w) * 1.01 + want.abs() * 2.0 ** -8 + 1e-37)[fine])
+        assert not torch.isfinite(dX[~fine]).any()
+
+
 def test_cross_entropy_in_pieces_of_the_vocabulary():
     """Sizes whose logit gradients take several pieces, the last one ragged."""
     T, k, V = 8200, 64, 40_003
