@@ -479,6 +479,41 @@ def test_cross_entropy_equal_weights_keep_the_targets_entries(T, V):
     within(dX, want, product_bound(d, ed, w) * 1.01 + want.abs() * 2.0 ** -8)
 
 
+@pytest.mark.parametrize("T,V", [(1, 40), (3, 700), (128, 1300), (129, 700), (2, 140001)])
+def test_cross_entropy_gradients_beyond_bf16_logit_gradients(T, V):
+    """dX has its tokens' target entries in fp32; up to 128 tokens, dW and C have every entry in two BF16 terms."""
+    k, r = 136, 24
+    X, W, targets, up = ce_inputs(T, k, V, seed=8, ignored=0.2 if T > 3 else 0.0)
+    XP = randn(gen(9), T, r, dtype=BF)
+    _, elog, lse, _ = ce64(X, W, targets, 1.0)
+    lse = lse.float()
+    d, _, x, w = ce_grads64(X, W, targets, up, lse, 1.0)
+    kept = targets >= 0
+    p = torch.exp(x @ w.t() - lse.to(F64)[:, None])
+    logits = x @ w.t()
+    # as ce_grads64 has it, before the rounding to BF16
+    ed = up.to(F64).abs()[:, None] * (p * (torch.expm1(elog) + 2.0 ** -21 * (1 + logits.abs() + lse.to(F64).abs()[:, None]))
+                                      + 2.0 ** -22)
+    ed = torch.where(kept[:, None], ed, 0.0)
+    hit = torch.zeros(T, V, dtype=torch.bool, device=DEV)
+    hit[torch.arange(T, device=DEV), targets.clamp(min=0)] = True
+    hit &= kept[:, None]
+    dX, dW, C = torch.empty_like(X), torch.empty(V, k, device=DEV), torch.empty(V, r, device=DEV)
+    rgs.cross_entropy_backward(X, W, targets, lse, up, dX=dX, dW=dW, overwrite=True)
+    again = torch.empty_like(X)
+    rgs.cross_entropy_backward(X, W, targets, lse, up, dX=again, XP=XP, C=C, overwrite=True)
+    assert torch.equal(dX, again)
+    want = d @ w
+    ex = ed + torch.where(hit, 2.0 ** -20, 2.0 ** -8) * (d.abs() + ed)
+    within(dX, want, product_bound(d, ex, w) * 1.01 + want.abs() * 2.0 ** -8 + 1e-30)
+    if T > 128:
+        return
+    ew = ed + 2.0 ** -16 * (d.abs() + ed)
+    for got, b in ((dW, x), (C, XP.to(F64))):
+        want = d.t() @ b
+        within(got, want, product_bound(d.t(), ew.t(), b) * 1.01 + want.abs() * 2.0 ** -22 + 1e-30)
+
+
 def test_cross_entropy_weights_of_every_size():
     """Zero, tiny, huge, infinite and NaN weights: each token's dX follows its own weight."""
     T, k, V = 6, 64, 700
