@@ -158,6 +158,27 @@ __device__ __forceinline__ void add_scaled(float (&f)[8], float c, const uint16_
   }
 }
 
+// Four 16-byte pieces of a row in each lane, dealt anew among every four lanes: piece
+// i then belongs to the row of the four's lane i, and is the one whose number is the
+// lane's own.  A warp's store then covers 64 bytes of eight rows, not 16 of 32.
+__device__ __forceinline__ void deal_rows(uint32_t (&d)[16], int lane) {
+#pragma unroll
+  for (int o = 1; o <= 2; o *= 2) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & o) continue;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t &lo = d[4 * i + w], &hi = d[4 * (i + o) + w];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, o);
+        if (up) lo = got;
+        else hi = got;
+      }
+    }
+  }
+}
+
 struct Tile {
   int p, m, n;              // product (-1: no more tiles), first row, first column
   int part;                 // of a split K
@@ -567,28 +588,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
             __syncwarp();  // the load is the whole warp's
             tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
             tc::tmem_wait_ld_regs(v);
-            if (!in) continue;
-            const int64_t at = (int64_t)row * a.ld_dw + col0 + cg * 32;
+            const int col = col0 + cg * 32;
+            // unfused: adding a gradient to itself doubles it
+            auto value = [&](int i) { return __fmul_rn(__uint_as_float(v[i]), unit); };
+            if constexpr (decltype(bf16)::value) {
+              uint32_t d[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (col0 + cg * 32 + 8 * i >= N) break;
-              float f[8];  // unfused: adding a gradient to itself doubles it
+              for (int i = 0; i < 16; ++i) d[i] = pack_bf16(value(2 * i), value(2 * i + 1));
+              deal_rows(d, lane);
+              const int first = row - (lane & 3), c = col + 8 * (lane & 3);
+              uint16_t* out = static_cast<uint16_t*>(a.dW) + (int64_t)first * a.ld_dw + c;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __fmul_rn(__uint_as_float(v[8 * i + e]), unit);
-              if constexpr (decltype(bf16)::value) {
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.dW) + at + 8 * i) = make_uint4(
-                    pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
-              } else {
-                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dW) + at + 8 * i);
+              for (int i = 0; i < 4; ++i)
+                if (first + i < pr.M && c < N)
+                  *reinterpret_cast<uint4*>(out + i * a.ld_dw) = make_uint4(d[4 * i], d[4 * i + 1], d[4 * i + 2], d[4 * i + 3]);
+            } else {
+              if (!in) continue;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float4 x = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-                  if (a.dw_mode == 2) {
-                    const float4 y = o[e];
-                    x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
-                  }
-                  o[e] = x;
+              for (int i = 0; i < 8; ++i) {
+                if (col + 4 * i >= N) break;
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.dW) + (int64_t)row * a.ld_dw + col) + i;
+                float4 x = make_float4(value(4 * i), value(4 * i + 1), value(4 * i + 2), value(4 * i + 3));
+                if (a.dw_mode == 2) {
+                  const float4 y = *o;
+                  x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
                 }
+                *o = x;
               }
             }
           }
