@@ -382,7 +382,9 @@ SKETCH_API sketch_status sketch_cross_entropy_forward(const uint16_t* X, int64_t
 /* Its gradient for the per-token upstream gradient g (T fp32: 1/n for a mean, an
  * advantage for a policy gradient) and the forward call's lse.  With D = g scale
  * (exp(l - lse) - onehot(target)), formed anew in pieces of the vocabulary and
- * rounded to BF16 like every output derivative of this library:
+ * rounded to BF16, in units of the largest |g|, like every output derivative of
+ * this library (what a target's entry loses is added to dX in fp32; with at most
+ * 128 tokens, dW and C have every entry in two BF16 terms):
  *   dX = D W              (T x k BF16; nullable)
  *   dW = D^T X            (V x k, BF16 or fp32 by dw_type; nullable)
  *   C (+)= D^T XP         (V x r fp32, the head's gradient sketch for

@@ -14,12 +14,12 @@
 // rounding would never let it move.  A u that is not zero never rounds to zero,
 // since it divides.  On the way to a code every operation is rounded by itself,
 // none fused: a code that a last bit decides is the same on any fp32 machine
-// (a state that differs by a code is a step apart ever after).  A value that is not finite gets the code NaN and takes no
-// part in its block's scale.
+// (a state that differs by a code is a step apart ever after).  A value that is not
+// finite gets the code NaN and takes no part in its block's scale.
 //
 // A thread works on eight values at a time, one Philox block for each stream; a
 // warp's 256 values are one block of an 8-bit state.  fp32 states are bound by HBM
-// (268M BF16 weights: 855 us, 1.02 of the copy rate over 22 bytes a value); 8-bit
+// (268M BF16 weights: 866 us, 1.01 of the copy rate over 22 bytes a value); 8-bit
 // states by instruction issue: 68 instructions a value, 15 of them the three
 // Philox streams, against the 55 that the 10 bytes' time would allow at a full
 // issue rate (638 us, 0.62 of the copy rate).  Arithmetic goes in packed pairs.

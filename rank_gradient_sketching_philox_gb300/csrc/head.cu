@@ -24,7 +24,8 @@
 //           lost all the same is added to dX at the end, in fp32; up to 128 tokens
 //           the rest of every entry takes part in dW's sum as a row of its own
 //   dx      rows of dX, added up over the vocabulary's pieces in fp32
-//   dw      rows of dW
+//   dw      rows of dW; BF16 ones in 64-byte pieces (single 16-byte ones: 314 us for
+//           300 at 1000 x 2048 x 32771)
 // The backward pass walks the vocabulary in pieces, so that only T x piece
 // logit gradients exist at a time.  One launch forms a piece's rows of dW, its
 // part of dX and the next piece's D.  Ignored tokens are dropped beforehand: the
@@ -36,6 +37,15 @@
 // the longest kind first.  Where dX has too few tiles for the pairs, the
 // vocabulary of a tile is split over several, whose fp32 parts head_dx_sum_kernel
 // adds.
+//
+// What bounds it, tokens x k x vocabulary: many tokens the tensor cores' rate, which
+// the power limit sets (8192 x 4096 x 131072 forward 5.2 ms, 1.70 PFLOP/s; 4096 x 4096
+// x 65536 backward 3.71 ms, 1.78 PFLOP/s; a plain matrix product of that length runs at
+// 1.72); few tokens the stream of W (16 x 2048 x 32768 forward: 38 us, 0.52 of the copy
+// rate: 128 tiles are two rounds for 76 pairs, and 11 us go to starts, ends and the
+// join); 1000 x 2048 x 32771 backward (300 us, 0.70 of the MMAs' time) the stores of
+// dW, 16 chunks of MMAs to a tile; small k the epilogues' reads of TMEM, beside which
+// MMAs run slower (8192 x 512 x 32768 forward: 285 us, 195 without them).
 //
 // Softmax statistics and every sum are fp32.  A tile's result is written by one
 // thread after a fixed-order accumulation, so results do not depend on timing.
@@ -64,9 +74,9 @@ constexpr int kHeadThreads = 64 + 32 * kEpiWarps + 32;  // copies, MMAs, epilogu
 constexpr int kMaxProducts = 3;
 constexpr int kTileSlots = 4;                // tiles handed out ahead of the slowest reader
 constexpr int kTileReaders = 2 * (1 + kEpiWarps) + 1;  // both CTAs' copies and epilogues, the MMAs
-// Tile rows walked together, so that their operands stay in L2: 16 take 5.25 ms
-// forward (8192 x 4096 x 131072) and 3.82 backward (4096 x 4096 x 65536), 8 took 5.36
-// and 3.80, 4 and 32 more of both.
+// Tile rows walked together, so that their operands stay in L2: with 16 the forward
+// pass takes 5.25 ms (8192 x 4096 x 131072), with 8 5.36, with 4 and 32 more; the
+// backward pass the same with 8 and 16.
 constexpr int kGroupM = 16;
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -1073,7 +1083,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   const int pieces = (int)ceil_div(f.V, piece);
 
   // Few tokens' rounding errors do not average out in dW, and D's tile has room
-  // beside them for what its entries lose: 300 us with it and without it (1000 x 2048 x 32771 with 120 tokens)
+  // beside them for what its entries lose (120 x 2048 x 32768: 219 us, 211 without)
   const int two_terms = f.T <= kHalf && (f.dW || sketch);
   Gather g = {};
   g.X = f.X; g.T = f.T; g.k = f.k; g.ld_x = f.ld_x;
