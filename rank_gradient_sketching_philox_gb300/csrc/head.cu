@@ -43,9 +43,12 @@
 // x 65536 backward 3.71 ms, 1.78 PFLOP/s; a plain matrix product of that length runs at
 // 1.72); few tokens the stream of W (16 x 2048 x 32768 forward: 38 us, 0.52 of the copy
 // rate: 128 tiles are two rounds for 76 pairs, and 11 us go to starts, ends and the
-// join); 1000 x 2048 x 32771 backward (300 us, 0.70 of the MMAs' time) the stores of
-// dW, 16 chunks of MMAs to a tile; small k the epilogues' reads of TMEM, beside which
-// MMAs run slower (8192 x 512 x 32768 forward: 285 us, 195 without them).
+// join); a backward pass over few tokens the epilogues of dW, whose tiles have few
+// chunks of MMAs (19 x 3624 x 47943: 382 us, 0.27 of the copy rate; a tile costs its
+// pair some 4 us, 2.5 of them reading TMEM and packing, 1.8 storing); 1000 x 2048 x
+// 32771 backward (300 us, 0.70 of the MMAs' time) the same, with 16 chunks to a tile;
+// small k the epilogues' reads of TMEM, beside which MMAs run slower (8192 x 512 x
+// 32768 forward: 285 us, 195 without them).
 //
 // Softmax statistics and every sum are fp32.  A tile's result is written by one
 // thread after a fixed-order accumulation, so results do not depend on timing.
