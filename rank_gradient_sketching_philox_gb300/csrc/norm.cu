@@ -8,6 +8,10 @@
 // Activations are BF16 or fp32, weights BF16 or fp32; statistics, sums and the
 // weights' gradients are fp32.
 //
+// xh is formed as the formula has it, the difference first: x - mu is exact where
+// the two are close, while x rstd - mu rstd would be off by 2^-24 |mu| rstd, which a
+// row of little variance far from zero shows (a constant row has xh = 0).
+//
 // Both passes are bound by HBM, once the instructions for each element are few:
 // arithmetic goes two values at a time (packed fp32 pairs).
 //
@@ -267,15 +271,17 @@ __device__ __forceinline__ float2 lds_f32x2(uint32_t at) {
 }
 
 // Statistics of the row whose elements this thread's share sums to `sum` and,
-// around a mean, to dev(mean): first the warp's mean and squared deviations from
-// it, then the row's from its warps', n (mean_w - mean)^2 more each (no difference
-// of squares, so that a row far from zero loses nothing).  `part` alternates
+// around a mean, to dev(mean): first the warp's mean over its `n` elements and
+// squared deviations from it, then the row's from its warps', n (mean_w - mean)^2
+// more each (no difference of squares, so that a row far from zero loses nothing).
+// Means are quotients, not products with a rounded 1 / n: where the sum is exact, as
+// for a row of equal integers, so is the mean if it can be.  `part` alternates
 // between rows: a thread that writes it again has passed the barrier of the row
 // between, after which nobody reads the old values.
 template <bool WARP, typename Dev, typename Count>
-__device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float inv_n, float inv_k, Count counts,
+__device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float n_warp, float k, Count counts,
                                             float2* part, float& mu, float& m2) {
-  mu = lane_sum<WARP>(sum, tpr) * inv_n;
+  mu = lane_sum<WARP>(sum, tpr) / (n_warp > 0.f ? n_warp : 1.f);
   m2 = lane_sum<WARP>(dev(mu), tpr);
   const int warps = tpr >> 5;
   if (WARP && warps > 1) {
@@ -288,7 +294,7 @@ __device__ __forceinline__ void row_moments(float sum, Dev dev, int tpr, float i
     const float n = counts(w);
     float j[1] = {n * v.x};
     join_sums(j, warps);
-    mu = j[0] * inv_k;
+    mu = j[0] / k;
     j[0] = fmaf(n * (v.x - mu), v.x - mu, v.y);
     join_sums(j, warps);
     m2 = j[0];
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o < tpr) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  const float inv_n = mine > 0 ? 1.f / (float)mine : 0.f, inv_k = 1.f / (float)k;
+  const float inv_k = 1.f / (float)k;
   if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = (float)mine;
   __syncthreads();
   const int64_t stride = (int64_t)gridDim.x * groups;
@@ -360,10 +366,10 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
           }
           return sum2(q);
         },
-        tpr, inv_n, inv_k, [&](int w) { return counts[w]; }, part[p], mu, m2);
+        tpr, (float)mine, (float)k, [&](int w) { return counts[w]; }, part[p], mu, m2);
     const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
     if (!in) continue;
-    const Pair r2 = pair(rstd, rstd), c2 = pair(-mu * rstd, -mu * rstd);
+    const Pair r2 = pair(rstd, rstd), neg = pair(-mu, -mu);
     X* y = static_cast<X*>(a.Y) + row * a.ld_y;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -373,7 +379,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
         weight_pairs<VE>(gamma, j * tpr + t, k, g);
         weight_pairs<VE>(beta, j * tpr + t, k, b);
 #pragma unroll
-        for (int i = 0; i < VE / 2; ++i) v[i] = fma2(fma2(v[i], r2, c2), g[i], b[i]);
+        for (int i = 0; i < VE / 2; ++i) v[i] = fma2(mul2(add2(v[i], neg), r2), g[i], b[i]);
         store_vec<X>(y, j * tpr + t, v);
       }
     }
@@ -460,11 +466,10 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
           }
           return has_one ? fmaf(e - m, e - m, sum2(q)) : sum2(q);
         },
-        tpr, n > 0.f ? 1.f / n : 0.f, inv_k, count, part[p], mu, m2);
+        tpr, n, (float)k, count, part[p], mu, m2);
     const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
     if (!in) continue;
-    const float shift = -mu * rstd;
-    const Pair r2 = pair(rstd, rstd), c2 = pair(shift, shift);
+    const Pair r2 = pair(rstd, rstd), neg = pair(-mu, -mu);
     X* y = static_cast<X*>(a.Y) + row * a.ld_y;
     uint32_t at[VE];  // of the weights of the thread's first vector
 #pragma unroll
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
         vec_pairs<X>(raw[j], v);
 #pragma unroll
         for (int i = 0; i < VE / 2; ++i) {
-          const float2 f = split(fma2(v[i], r2, c2));
+          const float2 f = split(mul2(add2(v[i], neg), r2));
           const float2 w0 = lds_f32x2(at[2 * i] + 8u * (uint32_t)(j * tpr)), w1 = lds_f32x2(at[2 * i + 1] + 8u * (uint32_t)(j * tpr));
           v[i] = pair(fmaf(f.x, w0.x, w0.y), fmaf(f.y, w1.x, w1.y));
         }
@@ -485,7 +490,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) norm_forward
     }
     if (take) {
       const float2 w = gb[(col & (VE - 1)) * pitch + col / VE];
-      store_one(y + col, fmaf(fmaf(e, rstd, shift), w.x, w.y));
+      store_one(y + col, fmaf((e - mu) * rstd, w.x, w.y));
     }
     if (t == 0) {
       a.mean[row] = mu;
@@ -512,7 +517,7 @@ __global__ void __launch_bounds__(THREADS, single_blocks(THREADS)) norm_forward_
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (o < tpr) warp_n += __shfl_xor_sync(0xFFFFFFFFu, warp_n, o);
-  const float inv_n = warp_n > 0 ? 1.f / (float)warp_n : 0.f, inv_k = 1.f / (float)k;
+  const float inv_k = 1.f / (float)k;
   if ((threadIdx.x & 31) == 0) counts[threadIdx.x >> 5] = (float)warp_n;
   __syncthreads();
   const int64_t stride = (int64_t)gridDim.x * groups;
@@ -537,14 +542,13 @@ __global__ void __launch_bounds__(THREADS, single_blocks(THREADS)) norm_forward_
             if (j < mine) q = fmaf(f[j] - m, f[j] - m, q);
           return q;
         },
-        tpr, inv_n, inv_k, [&](int w) { return counts[w]; }, part[p], mu, m2);
+        tpr, (float)warp_n, (float)k, [&](int w) { return counts[w]; }, part[p], mu, m2);
     const float rstd = 1.f / sqrtf(m2 * inv_k + a.eps);
     if (!in) continue;
     X* y = static_cast<X*>(a.Y) + row * a.ld_y + t;
-    const float c = -mu * rstd;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
-      if (j < mine) store_one(y + j * tpr, fmaf(fmaf(f[j], rstd, c), weights[j * tpr + t], weights[k + j * tpr + t]));
+      if (j < mine) store_one(y + j * tpr, fmaf((f[j] - mu) * rstd, weights[j * tpr + t], weights[k + j * tpr + t]));
     if (t == 0) {
       a.mean[row] = mu;
       a.rstd[row] = rstd;
@@ -683,14 +687,15 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
     int s = 0;
     uint32_t ph = 0;
     for (int p = 0; p < passes; ++p, row += step) {
-      Pair rs[B], mrs[B], s0[B], s1[B];
-      float rstd[B];
+      Pair rs[B], neg[B], s0[B], s1[B];
+      float rstd[B], mu[B];
       uint32_t ax[B], ay[B];
 #pragma unroll
       for (int b = 0; b < B; ++b) {
         rstd[b] = nrs[b];
+        mu[b] = nmu[b];
         rs[b] = pair(nrs[b], nrs[b]);
-        mrs[b] = pair(-nmu[b] * nrs[b], -nmu[b] * nrs[b]);  // xh = x rstd - mu rstd
+        neg[b] = pair(-nmu[b], -nmu[b]);
       }
       if (p + 1 < passes) load_stats(row + step);
       tc::mbar_wait(&full[s], ph, &abort_flag, err, tc::kErrTimeoutLoad);
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
             for (int q = 0; q < VP; ++q) {
               const Pair d = mul2(y[q], HOLD ? gamma[HOLD ? j * VP + q : 0] : g[q]);
               s0[b] = add2(s0[b], d);
-              s1[b] = fma2(d, fma2(x[q], rs[b], mrs[b]), s1[b]);
+              s1[b] = fma2(d, add2(x[q], neg[b]), s1[b]);  // times rstd once it is summed up
             }
           }
         }
@@ -737,8 +742,9 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
         if (SHIFT && has_one) {
           const float d = read_one<X>(ay[b] + one_at) * gamma_one;
           v[2 * b] += d;
-          v[2 * b + 1] = fmaf(d, fmaf(read_one<X>(ax[b] + one_at), rstd[b], split(mrs[b]).x), v[2 * b + 1]);
+          v[2 * b + 1] = fmaf(d, read_one<X>(ax[b] + one_at) - mu[b], v[2 * b + 1]);
         }
+        v[2 * b + 1] *= rstd[b];
       }
       lane_sums<WARP, 2 * B>(v, tpr);
       float2(*q)[THREADS / 32] = part[p & 1];  // alternates, as in row_moments
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
 #pragma unroll
               for (int q = 0; q < VP; ++q) {
                 const int e = j * VP + q;
-                x[q] = fma2(x[q], rs[b], mrs[b]);
+                x[q] = mul2(add2(x[q], neg[b]), rs[b]);
                 dg[e] = fma2(y[q], x[q], dg[e]);
                 db[e] = add2(db[e], y[q]);
                 y[q] = fma2(mul2(y[q], HOLD ? gamma[HOLD ? e : 0] : g[q]), rs[b], fma2(x[q], c1, c0));
@@ -800,7 +806,7 @@ __global__ void __launch_bounds__(THREADS, blocks_per_sm(THREADS))
             }
           }
           if (SHIFT && has_one) {
-            const float x = fmaf(read_one<X>(ax[b] + one_at), rstd[b], split(mrs[b]).x), y = read_one<X>(ay[b] + one_at);
+            const float x = (read_one<X>(ax[b] + one_at) - mu[b]) * rstd[b], y = read_one<X>(ay[b] + one_at);
             dg_one = fmaf(y, x, dg_one);
             db_one += y;
             if (a.dX) store_one(dx + one, fmaf(y * gamma_one, rstd[b], fmaf(x, f1, f0)));

@@ -1031,3 +1031,92 @@ def test_training_example_learns():
     losses = train_example.main(["--steps", "60", "--tokens", "1024"])
     assert 6.0 < losses[0] < 9.0
     assert losses[-1] < 1.0
+
+
+# ---- layer norm far from zero ---------------------------------------------------------
+
+# how X's and the outputs' rows lie: contiguous, from an element off a 16-byte boundary alike, or on different places
+PLACES = {"whole": (0, 0), "same": (1, 1), "different": (0, 1)}
+
+
+def placed(t, offset):
+    """t's values, contiguous, ``offset`` elements into a buffer."""
+    buf = torch.empty(offset + t.numel(), dtype=t.dtype, device=DEV)
+    view = buf[offset:].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+FAR_SHAPES = [(700, 24), (40, 128), (9, 1000), (300, 1001), (9, 1024), (40, 4096), (9, 5000), (40, 8192), (9, 8200),
+              (9, 16384), (3, 16387)]
+
+
+@pytest.mark.parametrize("x", [BF, F32])
+@pytest.mark.parametrize("places", list(PLACES))
+@pytest.mark.parametrize("T,k", FAR_SHAPES)
+def test_norm_constant_rows_are_their_mean(T, k, places, x):
+    """Sums of these values are exact below 2^24, so the mean is the value: xh = 0, Y = beta, dgamma = 0."""
+    ox, oy = PLACES[places]
+    g = gen(T + 13 * k)
+    value = torch.tensor([37.0, 100.0, 255.0, 1000.0], device=DEV)[torch.arange(T, device=DEV) % 4]
+    X = placed(value[:, None].expand(T, k).to(x), ox)
+    gamma, beta = randn(g, k) + 2.0, randn(g, k)
+    mean, rstd = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    Y = placed(torch.full_like(X, float("nan")), oy)
+    rgs.layer_norm_forward(X, gamma, beta, Y, mean, rstd, eps=1e-5)
+    assert torch.equal(mean, value)
+    r = float(torch.tensor(1e-5)) ** -0.5
+    within(rstd, torch.full_like(rstd, r).to(F64), r * 2.0 ** -22)
+    assert torch.equal(Y, beta.to(x).expand(T, k))
+    dY = placed(randn(g, T, k, dtype=x), oy)
+    dX, dgamma, dbeta = torch.empty_like(dY), torch.empty(k, device=DEV), torch.empty(k, device=DEV)
+    rgs.layer_norm_backward(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, overwrite=True)
+    assert torch.equal(dgamma, torch.zeros_like(dgamma))
+    # dX = rstd (d - mean(d)): the product, the sum over k, the factors
+    d = dY.to(F64) * gamma.to(F64)
+    want = rstd.to(F64)[:, None] * (d - d.mean(1, keepdim=True))
+    bound = rstd.to(F64)[:, None] * ((k + 16) * 2.0 ** -24 * d.abs().mean(1, keepdim=True) + 2.0 ** -22 * (
+        d.abs() + d.mean(1, keepdim=True).abs()))
+    within(dX, want, bound * 1.01 + (want.abs() * 2.0 ** -8 if x == BF else 0.0) + 1e-30)
+
+
+@pytest.mark.parametrize("x,size,spread", [(F32, 1e3, 1.0), (F32, 1e4, 1.0), (BF, 1e3, 8.0)])
+@pytest.mark.parametrize("places", list(PLACES))
+@pytest.mark.parametrize("T,k", FAR_SHAPES)
+def test_norm_rows_far_from_zero(T, k, places, x, size, spread):
+    """Means of 100 to 10000 deviations: x - mean is exact, so xh's error stays relative to xh, whatever |mean|."""
+    ox, oy = PLACES[places]
+    g = gen(T + 17 * k)
+    sign = torch.where(torch.arange(T, device=DEV) % 2 == 0, 1.0, -1.0)[:, None]
+    X = placed((sign * size + spread * randn(g, T, k)).to(x), ox)
+    gamma, beta = randn(g, k), randn(g, k)
+    mean, rstd = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    Y = placed(torch.full_like(X, float("nan")), oy)
+    rgs.layer_norm_forward(X, gamma, beta, Y, mean, rstd, eps=1e-5)
+    _, m, r = norm64(X, None, None, 1e-5)
+    dmean, drel = norm_bounds(X, 1e-5, k)
+    within(mean, m, dmean)
+    # of rstd: the variance around a mean that is off by dmean; a relative error of 2^-20 where that is small
+    within(rstd, r, drel * r)
+    # with the mean and rstd that the kernel gives: the difference, two products and a sum, each rounded once
+    half = 2.0 ** -8 if x == BF else 0.0
+    mk, rk = mean.to(F64)[:, None], rstd.to(F64)[:, None]
+    xh = (X.to(F64) - mk) * rk
+    want = xh * gamma.to(F64) + beta.to(F64)
+    bound = 2.0 ** -22 * (xh * gamma.to(F64)).abs() + 2.0 ** -23 * want.abs()
+    within(Y, want, bound * 1.01 + want.abs() * half + 1e-30)
+    dY = placed(randn(g, T, k, dtype=x), oy)
+    dX, dgamma, dbeta = torch.empty_like(dY), torch.empty(k, device=DEV), torch.empty(k, device=DEV)
+    rgs.layer_norm_backward(dY, X, gamma, mean, rstd, dX, dgamma, dbeta, overwrite=True)
+    dy = dY.to(F64)
+    d = dy * gamma.to(F64)
+    s0, s1 = d.mean(1, keepdim=True), (d * xh).mean(1, keepdim=True)
+    want = rk * (d - s0 - xh * s1)
+    n = (k + 16) * 2.0 ** -24
+    exh = 2.0 ** -22 * xh.abs()
+    e0 = n * d.abs().mean(1, keepdim=True)
+    e1 = n * (d * xh).abs().mean(1, keepdim=True) + (d.abs() * exh).mean(1, keepdim=True)
+    ex = rk * (e0 + exh * s1.abs() + xh.abs() * e1 + 2.0 ** -21 * (d.abs() + s0.abs() + xh.abs() * s1.abs()))
+    within(dX, want, ex * 1.01 + want.abs() * half)
+    nt = (T + 16) * 2.0 ** -24
+    within(dgamma, (dy * xh).sum(0), nt * (dy * xh).abs().sum(0) + (dy.abs() * exh).sum(0))
