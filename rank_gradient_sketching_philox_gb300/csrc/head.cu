@@ -669,14 +669,16 @@ __device__ __forceinline__ void join(float& mx, float& sum, float mx1, float sum
 // Join a row's partial statistics with its target's logit.  That logit is a dot
 // product of its own in fp32 (the tensor cores' accumulation truncates, which
 // the loss would show at a relative 1.5e-6 for k = 4096; so 6e-7) and stands
-// both in the sum and in loss = lse - logit, so that a confident token's small
-// loss keeps its digits.  Block: eight rows; a warp for each dot product, and
-// 32 threads for each row's partials.
+// both in the sum and in loss = lse - logit.  Where it is the largest, the loss is
+// log(1 + s), s the other exponentials' sum over its own: taken from s itself, so
+// that a confident token's small loss keeps its digits (1 + s loses all of an s
+// below 2^-24).  Block: eight rows; a warp for each dot product, and 32 threads for
+// each row's partials.
 constexpr int kCombineRows = 8;
 __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partials, const uint16_t* X, int64_t ld_x,
                                                            const uint16_t* W, int64_t ld_w, int64_t k,
-                                                           const int64_t* targets, float scale_log2, int64_t T,
-                                                           int64_t V, int blocks, float* loss, float* lse,
+                                                           const int64_t* targets, float scale, float scale_log2,
+                                                           int64_t T, int64_t V, int blocks, float* loss, float* lse,
                                                            int32_t* status) {
   cudaGridDependencySynchronize();
   __shared__ float2 part[32][kCombineRows];
@@ -715,17 +717,24 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
   }
-  if (lane == 0) hit[warp] = dot * scale_log2;
+  if (lane == 0) hit[warp] = dot;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
   if (threadIdx.x < kCombineRows && row < T) {
     for (int i = 1; i < 32; ++i) join(mx, sum, part[i][threadIdx.x].x, part[i][threadIdx.x].y);
     const int64_t t = targets[row];
-    const float h = hit[threadIdx.x];
-    if (t >= 0 && t < V) join(mx, sum, h, 1.f);
-    const float l2 = (mx == -INFINITY ? 0.f : mx) + log2f(sum);
-    lse[row] = l2 * kLn2;
-    loss[row] = t < 0 ? 0.f : t >= V ? NAN : (((mx - h) + log2f(sum)) * kLn2);
+    const bool is_logit = t >= 0 && t < V;
+    const float h = hit[threadIdx.x] * scale_log2;
+    if (is_logit && h >= mx) {
+      const float l = log1pf(sum * ex2(mx - h)) + (h - h);  // NaN for an infinite logit, as inf - inf is
+      lse[row] = fmaf(hit[threadIdx.x], scale, l);
+      loss[row] = l;
+    } else {
+      if (is_logit) join(mx, sum, h, 1.f);
+      const float l2 = (mx == -INFINITY ? 0.f : mx) + log2f(sum);
+      lse[row] = l2 * kLn2;
+      loss[row] = t < 0 ? 0.f : t >= V ? NAN : (((mx - h) + log2f(sum)) * kLn2);
+    }
   }
   if (status != nullptr && blockIdx.x == 0) {
     int found = 0;
@@ -1072,7 +1081,8 @@ cudaError_t launch_head_forward(const HeadForward& f, void* ws, cudaStream_t str
   if (err == cudaSuccess) err = launch_products(a, stream);
   if (err != cudaSuccess) return err;
   return launch_after(head_combine_kernel, (unsigned)ceil_div(f.T, kCombineRows), 256, 0, stream, a.partials, f.X,
-                      f.ld_x, f.W, f.ld_w, f.k, f.targets, a.scale_log2, f.T, f.V, blocks, f.loss, f.lse, f.dev_status);
+                      f.ld_x, f.W, f.ld_w, f.k, f.targets, f.scale, a.scale_log2, f.T, f.V, blocks, f.loss, f.lse,
+                      f.dev_status);
 }
 
 size_t head_backward_workspace_bytes(int64_t T, int64_t V, int64_t k, int64_t r) {

@@ -1120,3 +1120,49 @@ def test_norm_rows_far_from_zero(T, k, places, x, size, spread):
     within(dX, want, ex * 1.01 + want.abs() * half)
     nt = (T + 16) * 2.0 ** -24
     within(dgamma, (dy * xh).sum(0), nt * (dy * xh).abs().sum(0) + (dy.abs() * exh).sum(0))
+
+
+# ---- confident tokens ---------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [1.0, 0.7])
+@pytest.mark.parametrize("T", [5, 300])
+def test_cross_entropy_small_losses_keep_their_digits(T, scale):
+    """Losses of 1e-3 to 1e-9: W has one-hot rows and X one value b, so a token's logits are b scale and zeros."""
+    V = k = 1000
+    W = torch.eye(V, dtype=BF, device=DEV)
+    targets = (torch.arange(T, device=DEV) * 37) % V
+    b = (14.0 + torch.arange(T, device=DEV) % 29 * 0.5) / scale
+    X = torch.zeros(T, k, dtype=BF, device=DEV)
+    X[torch.arange(T, device=DEV), targets] = b.to(BF)
+    h = X[torch.arange(T, device=DEV), targets].to(F64) * float(np.float32(scale))
+    want = torch.log1p((V - 1) * torch.exp(-h))
+    assert want.min() < 2e-9 and want.max() > 5e-4 if T > 29 else want.max() > 5e-4
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse, scale=scale)
+    # the exponent h: two roundings and log2(e)'s own, 2.5 * 2^-24 of it; the exponential, logarithm and products 2^-20
+    within(loss, want, want * (h * 2.0 ** -22 + 2.0 ** -20))
+    within(lse, h + want, 2.0 ** -23 * (h + want))
+
+
+@pytest.mark.parametrize("T,V", [(20, 300), (300, 300), (20, 5000)])
+def test_cross_entropy_small_losses_of_wide_heads(T, V):
+    """The same with dense rows over several blocks of columns: the others' logits are off by the sum over k."""
+    k = 512
+    g = gen(T + V)
+    W = randn(g, V, k, std=0.05, dtype=BF)
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV)
+    X = (W[targets].float() * torch.linspace(14, 22, T, device=DEV)[:, None] / (k * 0.05 ** 2)).to(BF)
+    x, w = X.to(F64), W.to(F64)
+    logits, elog, lse64, _ = ce64(X, W, targets, 1.0)
+    hit = torch.arange(V, device=DEV)[None] == targets[:, None]
+    h = logits[hit]
+    others = torch.logsumexp(logits.masked_fill(hit, -math.inf), 1)
+    want = torch.nn.functional.softplus(others - h)
+    assert want.max() < 0.1
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse)
+    # the target's logit is an fp32 sum of k terms dealt over 32 lanes
+    eh = (k / 32 + 8) * 2.0 ** -24 * (x.abs() * w[targets].abs()).sum(1) + h.abs() * 2.0 ** -22
+    e = eh + elog.masked_fill(hit, 0.0).amax(1) + others.abs() * 2.0 ** -22 + V * 2.0 ** -24 + 2.0 ** -20
+    within(loss, want, want * torch.expm1(e))
+    within(lse, lse64, eh + want * torch.expm1(e) + 2.0 ** -23 * lse64.abs())
