@@ -20,8 +20,11 @@
 //           multiplied by in fp32: with the usual mean over tokens all weights are
 //           that one, and the targets' entries, close to -1 for a small exp(l - lse),
 //           keep their values, where -g scale would be rounded the same way for
-//           every token (up to 0.2% of all gradients).  What a target's entry
-//           lost all the same is added to dX at the end, in fp32; up to 128 tokens
+//           every token (up to 0.2% of all gradients).  A target's exp(l - lse) - 1
+//           comes from the fp32 dot product that the forward pass put into lse, so
+//           that 1 - p of a confident token is off by lse's own rounding (2^-24 of it),
+//           where the tensor cores' truncating sum leaves 1.5e-6 of l.  What a target's
+//           entry lost in rounding all the same is added to dX at the end, in fp32; up to 128 tokens
 //           the rest of every entry takes part in dW's sum as a row of its own
 //   dx      rows of dX, added up over the vocabulary's pieces in fp32
 //   dw      rows of dW; BF16 ones in 64-byte pieces (single 16-byte ones: 314 us for
@@ -116,6 +119,7 @@ struct HeadLaunch {
   const float* weight;    // per kept row: g * scale
   const float* factor;    // D is in units of it
   const int* target;      // per kept row
+  const float* hit;       // per kept row: its target's exp(l - lse) - 1
   uint16_t* D;
   int64_t ld_d;
   int two_terms;          // D's rows kHalf and on hold what its first kHalf rows lost in rounding
@@ -475,7 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       const int N = pr.N;
       // what the epilogue wants of its row, read while the MMAs run
       const bool in = pr.epi == kEpiStats || pr.epi == kEpiDw ? row < pr.M : row < kept;
-      float w = 0.f, l2 = 0.f;
+      float w = 0.f, l2 = 0.f, hit = 0.f;
       int tcol = -1;  // column of the row's target among the tile's
       if (pr.epi == kEpiStats) {
         const int64_t target = in ? a.targets[row] : -1;
@@ -483,6 +487,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
       } else if (pr.epi == kEpiDlogit && in) {
         w = a.weight[row] / unit;
         l2 = a.lse_log2[row];
+        hit = a.hit[row];
         tcol = a.target[row] - (a.d_first + col0);
       }
       const bool live = tc::mbar_wait(&tfull_bar[b], (j >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutMma);
@@ -536,13 +541,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kHeadThreads, 1)
             tc::tmem_ld_32x32b_x32(acc + cg * 32, v);
             tc::tmem_wait_ld_regs(v);
             uint32_t d[16], e[TWO ? 16 : 1];
-            float hit = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
               float p0 = ex2(fmaf(__uint_as_float(v[2 * i]), a.scale_log2, -l2));
               float p1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), a.scale_log2, -l2));
-              if (tcol == cg * 32 + 2 * i) hit = p0 -= 1.f;
-              if (tcol == cg * 32 + 2 * i + 1) hit = p1 -= 1.f;
+              if (tcol == cg * 32 + 2 * i) p0 = hit;
+              if (tcol == cg * 32 + 2 * i + 1) p1 = hit;
               d[i] = in ? pack_bf16(p0 * w, p1 * w) : 0u;
               if constexpr (TWO)
                 e[i] = in ? pack_bf16(rest_of(p0 * w, d[i] << 16), rest_of(p1 * w, d[i] & 0xFFFF0000u)) : 0u;
@@ -666,6 +670,25 @@ __device__ __forceinline__ void join(float& mx, float& sum, float mx1, float sum
   mx = top;
 }
 
+// Dot product of two BF16 rows by a warp, in fp32: the same bits wherever it is taken.
+__device__ __forceinline__ float warp_dot(const uint16_t* x, const uint16_t* w, int64_t k) {
+  float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x & 31; i < k / 8; i += 32) {
+    const uint4 a = reinterpret_cast<const uint4*>(x)[i], b = reinterpret_cast<const uint4*>(w)[i];
+    const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s0 = fmaf(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16), s0);
+      s1 = fmaf(__uint_as_float(p[e] & 0xFFFF0000u), __uint_as_float(q[e] & 0xFFFF0000u), s1);
+    }
+  }
+  float dot = s0 + s1;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
+  return dot;
+}
+
 // Join a row's partial statistics with its target's logit.  That logit is a dot
 // product of its own in fp32 (the tensor cores' accumulation truncates, which
 // the loss would show at a relative 1.5e-6 for k = 4096; so 6e-7) and stands
@@ -699,24 +722,7 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
   const int64_t drow = row0 + warp;
   const int64_t target = drow < T ? targets[drow] : -1;
   float dot = 0.f;
-  if (target >= 0 && target < V) {
-    const uint4* x = reinterpret_cast<const uint4*>(X + drow * ld_x);
-    const uint4* w = reinterpret_cast<const uint4*>(W + target * ld_w);
-    float s0 = 0.f, s1 = 0.f;
-#pragma unroll 4
-    for (int64_t i = lane; i < k / 8; i += 32) {
-      const uint4 a = x[i], b = w[i];
-      const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s0 = fmaf(__uint_as_float(p[e] << 16), __uint_as_float(q[e] << 16), s0);
-        s1 = fmaf(__uint_as_float(p[e] & 0xFFFF0000u), __uint_as_float(q[e] & 0xFFFF0000u), s1);
-      }
-    }
-    dot = s0 + s1;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(0xFFFFFFFFu, dot, o);
-  }
+  if (target >= 0 && target < V) dot = warp_dot(X + drow * ld_x, W + target * ld_w, k);
   if (lane == 0) hit[warp] = dot;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
@@ -749,14 +755,16 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
 // eight at a time, one per warp.  Each block counts the kept tokens before its own,
 // so that no pass over the targets comes first; blocks are longer for many tokens,
 // so that this counting stays small (T = 131072: 1 GB read from L2 in all, beside
-// 1 GB of X).  Compact rows past the kept ones, up to `fill` (a multiple of the
+// 1 GB of X).  A kept token's target gets its exp(l - lse) - 1 here, from the same
+// dot product as in the forward pass.  Compact rows past the kept ones, up to `fill` (a multiple of the
 // tile's rows), are zeroed.
 struct Gather {
   const uint16_t* X;
   int64_t T, k, ld_x;
   const uint16_t* XP;  // nullable
   int64_t ld_xp, r;
-  int64_t V;
+  const uint16_t* W;
+  int64_t V, ld_w;
   const int64_t* targets;
   const float* lse;
   const float* g;
@@ -768,6 +776,7 @@ struct Gather {
   float* weight;
   float* factor;  // the largest finite |weight|, 1 where that is 0
   int* target;
+  float* hit;
   int* row_of;
   int* kept;
   int* counters;  // n_counters of them, set to 0
@@ -850,7 +859,9 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
           if (a.XP)
             for (int64_t i = lane; i < a.r; i += 32) a.XPc[(dst + kHalf) * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
         }
+        const float dot = warp_dot(a.X + row * a.ld_x, a.W + t * a.ld_w, a.k);
         if (lane == 0) {
+          a.hit[dst] = expm1f(fmaf(dot, a.scale, -a.lse[row]));
           a.lse_log2[dst] = a.lse[row] * kLog2e;
           a.weight[dst] = a.g[row] * a.scale;
           a.target[dst] = (int)t;
@@ -1015,6 +1026,7 @@ struct BackwardWorkspace {
   float* factor;
   float* rest;
   int* target;
+  float* hit;
   int* row_of;
   int* kept;
   int* counters;
@@ -1040,6 +1052,7 @@ BackwardWorkspace carve_backward(void* base, int64_t T, int64_t V, int64_t k, in
   w.factor = cur.take<float>(1);
   w.rest = cur.take<float>((size_t)rows);
   w.target = cur.take<int>((size_t)rows);
+  w.hit = cur.take<float>((size_t)rows);
   w.row_of = cur.take<int>((size_t)rows);
   w.kept = cur.take<int>(1);
   w.counters = cur.take<int>((size_t)(pieces + 1));
@@ -1101,9 +1114,10 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   Gather g = {};
   g.X = f.X; g.T = f.T; g.k = f.k; g.ld_x = f.ld_x;
   g.XP = sketch ? f.XP : nullptr; g.ld_xp = f.ld_xp; g.r = f.r;
-  g.V = f.V; g.targets = f.targets; g.lse = f.lse; g.g = f.g; g.scale = f.scale;
+  g.W = f.W; g.V = f.V; g.ld_w = f.ld_w; g.targets = f.targets; g.lse = f.lse; g.g = f.g; g.scale = f.scale;
   g.Xc = w.Xc; g.XPc = w.XPc; g.ld_xpc = w.ld_xpc;
-  g.lse_log2 = w.lse_log2; g.weight = w.weight; g.factor = w.factor; g.target = w.target; g.row_of = w.row_of; g.kept = w.kept;
+  g.lse_log2 = w.lse_log2; g.weight = w.weight; g.factor = w.factor; g.target = w.target; g.hit = w.hit;
+  g.row_of = w.row_of; g.kept = w.kept;
   g.dX = f.dX; g.ld_dx = f.ld_dx;
   g.counters = w.counters; g.n_counters = pieces + 1;
   g.two_terms = two_terms; g.rows = rows; g.all_rows = sketch; g.status = f.dev_status;
@@ -1125,6 +1139,7 @@ cudaError_t launch_head_backward(const HeadBackward& f, void* ws, cudaStream_t s
   a.W = f.W;
   a.ld_w = f.ld_w;
   a.target = w.target;
+  a.hit = w.hit;
   a.row_of = w.row_of;
   a.ld_d = piece;
   a.dX = f.dX;

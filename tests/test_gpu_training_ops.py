@@ -1166,3 +1166,40 @@ def test_cross_entropy_small_losses_of_wide_heads(T, V):
     e = eh + elog.masked_fill(hit, 0.0).amax(1) + others.abs() * 2.0 ** -22 + V * 2.0 ** -24 + 2.0 ** -20
     within(loss, want, want * torch.expm1(e))
     within(lse, lse64, eh + want * torch.expm1(e) + 2.0 ** -23 * lse64.abs())
+
+
+@pytest.mark.parametrize("T,V", [(24, 500), (200, 500), (24, 40000)])
+def test_cross_entropy_backward_of_confident_tokens(T, V):
+    """The target's entry of D is -g (1 - p) with p from the same logit as the forward call's lse: off by lse's own
+    rounding, not by the tensor cores' sum over k (about 1.5e-6 of the logit), which for 1 - p of 1e-5 is more than it."""
+    k = 4096
+    g = gen(3 * T + V)
+    W = randn(g, V, k, std=0.02, dtype=BF)
+    targets = torch.randint(0, V, (T,), generator=g, device=DEV)
+    top = math.log(V)
+    X = (W[targets].float() * (top + torch.linspace(8, 12, T, device=DEV)[:, None]) / (k * 0.02 ** 2)).to(BF)
+    up = torch.full((T,), 1.0 / T, device=DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse)
+    dX, dW = torch.empty_like(X), torch.empty(V, k, device=DEV)
+    rgs.cross_entropy_backward(X, W, targets, lse, up, dX=dX, dW=dW, overwrite=True)
+    x, w = X.to(F64), W.to(F64)
+    logits, elog, lse64, want = ce64(X, W, targets, 1.0)
+    hit = torch.arange(V, device=DEV)[None] == targets[:, None]
+    others = torch.logsumexp(logits.masked_fill(hit, -math.inf), 1, keepdim=True)
+    assert want.max() < 2e-3
+    weight = up.to(F64)[:, None]
+    p = torch.exp(logits - lse64[:, None])
+    rest = -torch.expm1(-want)[:, None]  # 1 - p of the target
+    d = torch.where(hit, -rest, p) * weight
+    # p: its logit's error, and 2^-21 of the logit and lse.  The target: relative errors of the others' sum, and lse's
+    # rounding (2^-24 of it in the forward call, once more in the difference)
+    rel = torch.expm1(elog.masked_fill(hit, 0.0)) + 2.0 ** -21 * (1 + logits.abs() + lse64.abs()[:, None])
+    ed = weight * torch.where(hit, rest * (rel.masked_fill(hit, 0.0).amax(1, keepdim=True) + others.abs() * 2.0 ** -20)
+                              + 2.0 ** -23 * lse64.abs()[:, None], p * rel)
+    ex = ed + torch.where(hit, 2.0 ** -20, 2.0 ** -8) * (d.abs() + ed)
+    want = d @ w
+    within(dX, want, product_bound(d, ex, w) * 1.01 + want.abs() * 2.0 ** -8 + 1e-30)
+    ew = ed + 2.0 ** -8 * (d.abs() + ed)
+    want = d.t() @ x
+    within(dW, want, product_bound(d.t(), ew.t(), x) * 1.01 + want.abs() * 2.0 ** -22 + 1e-30)
