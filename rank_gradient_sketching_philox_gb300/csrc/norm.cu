@@ -985,13 +985,19 @@ int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
   return tpr;
 }
 
+// Let a kernel have `smem` bytes of dynamic shared memory.  Static and dynamic parts
+// of up to 48 KB together need no asking; the kernels' static parts stay below 1 KB.
+template <typename Kernel>
+cudaError_t allow_smem(Kernel kernel, size_t smem) {
+  if (smem <= (47u << 10)) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+}
+
 template <int THREADS, typename Kernel>
 cudaError_t launch_forward(Kernel kernel, const NormForward& a, int tpr, int per_sm, cudaStream_t stream) {
   const size_t smem = ((size_t)a.k + 8) * 8;  // the shifted kernel's pitch rounds up
-  if (smem > 48u * 1024u) {
-    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-  }
+  const cudaError_t err = allow_smem(kernel, smem);
+  if (err != cudaSuccess) return err;
   int64_t blocks = ceil_div(a.T, THREADS / tpr);
   const int64_t most = (int64_t)num_sms() * per_sm;
   if (blocks > most) blocks = most;
@@ -1064,10 +1070,8 @@ cudaError_t launch_rows(Kernel kernel, const Args& a, const Ring& r, int tpr, in
   if (err != cudaSuccess) return err;
   size_t smem = (size_t)r.slots * r.slot;
   if (smem < room) smem = room;
-  if (smem > 48u * 1024u) {
-    err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (err != cudaSuccess) return err;
-  }
+  err = allow_smem(kernel, smem);
+  if (err != cudaSuccess) return err;
   count_launch();
   kernel<<<(unsigned)blocks, threads, smem, stream>>>(a, r, tpr, err_word);
   return cudaGetLastError();

@@ -5,6 +5,9 @@ off by at most 2^-8 of the value, an fp32 operation by 2^-24, a tensor-core sum
 over K by at most 2^-23 of the sum of magnitudes for each 16-wide step.
 """
 import math
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -1203,3 +1206,48 @@ def test_cross_entropy_backward_of_confident_tokens(T, V):
     ew = ed + 2.0 ** -8 * (d.abs() + ed)
     want = d.t() @ x
     within(dW, want, product_bound(d.t(), ew.t(), x) * 1.01 + want.abs() * 2.0 ** -22 + 1e-30)
+
+
+# ---- calls of a fresh process ----------------------------------------------------------
+
+FIRST_CALLS = """
+import torch
+import rank_gradient_sketching_philox_gb300 as rgs
+failed = []
+for T, k, offset, dtype in [(4, 768, 0, torch.float32), (64, 1536, 0, torch.bfloat16), (4, 192, 0, torch.bfloat16),
+                            (4, 6112, 0, torch.bfloat16), (4, 6100, 0, torch.float32), (4, 6101, 1, torch.bfloat16),
+                            (64, 755, 1, torch.bfloat16), (8, 379, 1, torch.float32)]:
+    g = torch.Generator(device="cuda").manual_seed(T + k)
+    def rows():
+        buf = torch.empty(T * k + offset, dtype=dtype, device="cuda").normal_(generator=g)
+        return buf[offset:].view(T, k)
+    X, dY, Y, dX = rows(), rows(), rows(), rows()
+    x, dy = X.double(), dY.double()
+    m, r = x.mean(1, keepdim=True), (x.var(1, unbiased=False, keepdim=True) + 1e-5).rsqrt()
+    mean, rstd = torch.empty(T, device="cuda"), torch.empty(T, device="cuda")
+    dg, db = torch.empty(k, device="cuda"), torch.empty(k, device="cuda")
+    xh = (x - m) * r
+    dx = r * (dy - dy.mean(1, keepdim=True) - xh * (dy * xh).mean(1, keepdim=True))
+    step = 2.0 ** -8 if dtype == torch.bfloat16 else 0.0
+    def check(*results):
+        for got, want, e in results:
+            assert ((got.double() - want).abs() <= e * want.abs() + 1e-4 * (1 + want.abs().max())).all(), (T, k)
+    try:
+        rgs.layer_norm_forward(X, None, None, Y, mean, rstd)
+        check((Y, xh, step), (mean, m[:, 0], 0.0), (rstd, r[:, 0], 0.0))
+    except rgs.SketchError as e:
+        failed.append(("forward", T, k, str(e)))
+    try:
+        rgs.layer_norm_backward(dY, X, None, m[:, 0].float(), r[:, 0].float(), dX, dg, db, overwrite=True)
+        check((dX, dx, step), (dg, (dy * xh).sum(0), 0.0), (db, dy.sum(0), 0.0))
+    except rgs.SketchError as e:
+        failed.append(("backward", T, k, str(e)))
+assert not failed, failed
+"""
+
+
+def test_norm_sizes_whose_shared_memory_is_near_48_kb():
+    """First launches of a process, with dynamic shared memory that passes 48 KB only together with the static part."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    p = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert p.returncode == 0, p.stderr[-3000:]
