@@ -965,6 +965,7 @@ __global__ void __launch_bounds__(kThreads) norm_dx_wide_kernel(const NormBackwa
 }
 
 constexpr int64_t kMaxRowWidth = 16384;
+constexpr size_t kMostSmem = 216u << 10;  // dynamic shared memory of a launch
 
 // Whether every row of the matrix starts on a vector of ve elements and ends with a whole one.
 bool whole_vectors(const void* p, int64_t ld, int64_t k, int ve, size_t size) {
@@ -985,12 +986,15 @@ int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
   return tpr;
 }
 
-// Let a kernel have `smem` bytes of dynamic shared memory.  Static and dynamic parts
-// of up to 48 KB together need no asking; the kernels' static parts stay below 1 KB.
+// Let a kernel have `smem` bytes of dynamic shared memory, kMostSmem at most.  Static
+// and dynamic parts of up to 48 KB together need no asking; the kernels' static parts
+// stay below 1 KB.  The limit is the kernel's, not the launch's: it is the same for
+// every size, so that another host thread's launch never finds it lowered.
 template <typename Kernel>
 cudaError_t allow_smem(Kernel kernel, size_t smem) {
   if (smem <= (47u << 10)) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (smem > kMostSmem) return cudaErrorInvalidValue;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMostSmem);
 }
 
 template <int THREADS, typename Kernel>
@@ -1048,7 +1052,7 @@ Ring make_ring(int64_t k, size_t size, bool edges, int groups, int each, int mat
   // edges: room for 16-byte boundaries around a row
   r.pitch = !edges ? (uint32_t)(k * size) : (uint32_t)((k * size + 15) / 16 * 16 + 16);
   r.slot = r.pitch * (uint32_t)(r.rows * matrices);
-  const uint32_t room = ((blocks_per_sm(threads) == 2 ? 108u : 216u) << 10) - (uint32_t)beside;
+  const uint32_t room = (uint32_t)(kMostSmem / blocks_per_sm(threads) - beside);
   r.slots = (int)(room / r.slot < kMaxSlots ? room / r.slot : kMaxSlots);
   return r;
 }

@@ -8,6 +8,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import numpy as np
 import pytest
@@ -1251,3 +1252,33 @@ def test_norm_sizes_whose_shared_memory_is_near_48_kb():
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     p = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
     assert p.returncode == 0, p.stderr[-3000:]
+
+
+def test_norm_of_two_widths_from_several_threads():
+    """Host threads launch one kernel with different amounts of shared memory, each on a stream of its own."""
+    call, jobs = binding.lib().sketch_layer_norm_forward, []
+    for i in range(8):
+        k = (8192, 16384)[i & 1]  # one kernel, 64 and 128 KB
+        X = randn(gen(i), 4, k, dtype=BF)
+        out, stream = (torch.empty_like(X), torch.empty(4, device=DEV), torch.empty(4, device=DEV)), torch.cuda.Stream()
+        args = (X.data_ptr(), binding.DTYPE_BF16, 4, k, k, None, None, binding.DTYPE_FP32, 1e-5, out[0].data_ptr(), k,
+                out[1].data_ptr(), out[2].data_ptr(), stream.cuda_stream)
+        jobs.append((X, out, args))
+    torch.cuda.synchronize()
+    start, refused = threading.Barrier(len(jobs)), [0] * len(jobs)
+
+    def work(i):
+        start.wait()
+        for _ in range(5000):
+            refused[i] += call(*jobs[i][2]) != binding.OK
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(jobs))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert refused == [0] * len(jobs)
+    for X, out, _ in jobs:
+        want, _, _ = norm64(X, None, None, 1e-5)
+        within(out[0], want, want.abs() * 2.0 ** -8 + 1e-4)
