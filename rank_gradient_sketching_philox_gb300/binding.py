@@ -594,8 +594,8 @@ def _scratch(op, T, d, k, r, device, stream, given):
     """(workspace of a call, its address, its size): the caller's, or one that belongs to the call's stream."""
     nbytes = lib().sketch_workspace_bytes(op, T, d, k, r)
     if given is not None:
-        if not given.is_cuda or given.numel() * given.element_size() < nbytes:
-            raise ValueError("workspace needs %d bytes" % nbytes)
+        if given.device != device or not given.is_contiguous() or given.numel() * given.element_size() < nbytes:
+            raise ValueError("workspace needs %d contiguous bytes on %s" % (nbytes, device))
     elif nbytes == 0:
         return None, None, 0
     elif stream is None:

@@ -183,3 +183,17 @@ def test_exports_list_the_operators(lib):
                  "sketch_cross_entropy_backward", "sketch_adamw_batched"):
         assert name in binding.EXPORTS and hasattr(lib, name)
     assert ctypes.sizeof(binding.AdamWProblem) == 72
+
+
+@pytest.mark.parametrize("where,contiguous,size", [("cuda:1", True, 1 << 20), ("cpu", True, 1 << 20), ("cuda:0", False, 1 << 20),
+                                                   ("cuda:0", True, 1000)])
+def test_callers_workspace_is_refused(lib, where, contiguous, size):
+    """On another device, without storage of its own for every element (an expanded tensor), too small."""
+
+    class Workspace:
+        device, is_cuda = torch.device(where), where != "cpu"
+        numel, element_size, data_ptr = lambda self: size, lambda self: 1, lambda self: A
+        is_contiguous = lambda self: contiguous  # noqa: E731
+
+    with pytest.raises(ValueError, match="workspace"):
+        binding._scratch(binding.OP_CROSS_ENTROPY_FORWARD, 128, 1000, 64, 0, torch.device("cuda:0"), None, Workspace())
