@@ -787,8 +787,11 @@ def adamw_problems(Ws, Gs, ms, vs, m_scales=None, v_scales=None, layers=None):
 
 
 def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=None, device=None, stream=None):
-    """One AdamW step (counted from 0) of the tensors of adamw_problems."""
+    """One AdamW step (counted from 0) of the tensors of adamw_problems.  grad_scale:
+    a one-element fp32 tensor on their device that multiplies the gradients."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    if grad_scale is not None:
+        _vector(grad_scale, 1, torch.float32, dev, "grad_scale")
     st = lib().sketch_adamw_batched(len(probs), probs, lr, betas[0], betas[1], eps, weight_decay, _addr(grad_scale),
                                     seed & 0xFFFFFFFFFFFFFFFF, step, _stream_of(stream, dev))
     if st:

@@ -59,7 +59,5 @@ class AdamW:
         """Update every tensor with its gradient buffer; ``step`` counts from 0.
         grad_scale: a one-element fp32 device tensor that multiplies the
         gradients, or None."""
-        if grad_scale is not None:
-            binding._vector(grad_scale, 1, torch.float32, self._device, "grad_scale")
         binding.adamw_batched(self._problems, lr, self.betas, self.eps, self.weight_decay, self.seed, step,
                               grad_scale, self._device, stream)

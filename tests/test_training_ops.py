@@ -197,3 +197,18 @@ def test_callers_workspace_is_refused(lib, where, contiguous, size):
 
     with pytest.raises(ValueError, match="workspace"):
         binding._scratch(binding.OP_CROSS_ENTROPY_FORWARD, 128, 1000, 64, 0, torch.device("cuda:0"), None, Workspace())
+
+
+@pytest.mark.parametrize("scale", [torch.ones(1), torch.ones(2), torch.ones(1, dtype=torch.bfloat16), torch.tensor([1.0, 2.0])[:1]])
+def test_adamw_batched_refuses_a_grad_scale_that_a_kernel_cannot_read(lib, scale):
+    """The list function checks it as AdamW.step does (an empty tensor: nothing would be launched)."""
+
+    class Stream:
+        cuda_stream = 0
+
+    probs = (binding.AdamWProblem * 1)(binding.AdamWProblem(NULL, NULL, NULL, NULL, NULL, NULL, 0, 0, 0, 0))
+    call = lambda s: binding.adamw_batched(probs, 1e-3, (0.9, 0.999), 1e-8, 0.0, 0, 0, grad_scale=s,  # noqa: E731
+                                           device=torch.device("cuda:0"), stream=Stream())
+    call(None)
+    with pytest.raises(ValueError, match="grad_scale"):
+        call(scale)
