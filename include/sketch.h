@@ -368,9 +368,10 @@ SKETCH_API sketch_status sketch_layer_norm_backward(const void* dY, int64_t ld_d
 /* Softmax cross entropy of a linear head, without storing its T x V logits l =
  * scale X W^T: lse = log sum_v exp(l_v), loss = lse - l[target], per token, both
  * fp32.  X: T x k BF16, W: V x k BF16 (row strides ld_x, ld_w as everywhere; k a
- * multiple of 8); targets: T int64.  A negative target marks an ignored token:
- * its loss is 0.  A target >= V gives that token loss NaN and sets
- * SKETCH_DEV_BAD_TARGET in *dev_status (nullable; 0 otherwise).  scale, finite
+ * multiple of 8); targets: T int64.  T, V and k are at most 2^24 each, and any two
+ * of them span at most 2^28 tiles of 256 x 256 (else SKETCH_ERR_UNSUPPORTED).  A
+ * negative target marks an ignored token: its loss is 0.  A target >= V gives that
+ * token loss NaN and sets SKETCH_DEV_BAD_TARGET in *dev_status (nullable; 0 otherwise).  scale, finite
  * and > 0, is the inverse temperature.  The products are BF16 on the tensor
  * cores with fp32 accumulation. */
 SKETCH_API sketch_status sketch_cross_entropy_forward(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x,

@@ -103,10 +103,12 @@ size_t update_ws_bytes(bool normsgd, int64_t d, int64_t k, int64_t r) {
   return rgs::carve_update_workspace(cur, d, k, (int)r, normsgd, nullptr);
 }
 
-// Cross entropy: tokens, vocabulary and width whose tile coordinates stay below 2^31.
+// Cross entropy: tokens, vocabulary and width whose tile coordinates and numbers of tiles stay below 2^31.
 bool head_sizes_ok(int64_t T, int64_t V, int64_t k) {
-  return T >= 1 && T <= rgs::kMaxHeadDim && V >= 1 && V <= rgs::kMaxHeadDim && k >= 8 && k % 8 == 0 &&
-         k <= rgs::kMaxHeadDim;
+  if (T < 1 || T > rgs::kMaxHeadDim || V < 1 || V > rgs::kMaxHeadDim || k < 8 || k % 8 != 0 || k > rgs::kMaxHeadDim)
+    return false;
+  const int64_t t = rgs::ceil_div(T, 256), v = rgs::ceil_div(V, 256), w = rgs::ceil_div(k, 256);
+  return t * v <= rgs::kMaxHeadTiles && t * w <= rgs::kMaxHeadTiles && v * w <= rgs::kMaxHeadTiles;
 }
 
 size_t op_ws_bytes(sketch_op op, int64_t T, int64_t d, int64_t k, int64_t r) {
@@ -354,8 +356,8 @@ sketch_status check_head(const uint16_t* X, int64_t T, int64_t k, int64_t ld_x, 
   TRY(check_dim("V", V));
   TRY(check_k(k));
   if (!head_sizes_ok(T, V, k))
-    return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld, V=%lld or k=%lld exceeds %lld", (long long)T, (long long)V,
-                (long long)k, (long long)rgs::kMaxHeadDim);
+    return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld, V=%lld, k=%lld: one exceeds 2^24, or two have more than 2^28 tiles of 256 x 256",
+                (long long)T, (long long)V, (long long)k);
   TRY(check_ld("ld_x", ld_x, k));
   TRY(check_ld("ld_w", ld_w, k));
   CHECK_PTR(X);

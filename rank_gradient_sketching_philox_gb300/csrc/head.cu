@@ -996,7 +996,6 @@ cudaError_t launch_after(void (*kernel)(Params...), unsigned blocks, unsigned th
 cudaError_t launch_products(const HeadLaunch& a, cudaStream_t stream) {
   int64_t items = 0;
   for (int p = 0; p < a.n; ++p) items += ceil_div(a.p[p].M, kTile) * ceil_div(a.p[p].N, kTile) * a.p[p].splits;
-  if (items > (int64_t(1) << 30)) return cudaErrorInvalidValue;
   int pairs = 0;
   cudaError_t err = head_pairs(&pairs);
   if (err != cudaSuccess) return err;

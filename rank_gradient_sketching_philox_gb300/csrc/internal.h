@@ -254,7 +254,8 @@ size_t norm_backward_workspace_bytes(int64_t T, int64_t k);
 cudaError_t launch_norm_backward(const NormBackward& a, cudaStream_t stream);
 
 // ---- cross entropy of a linear head (head.cu) --------------------------------
-constexpr int64_t kMaxHeadDim = int64_t(1) << 24;  // tokens, vocabulary, width
+constexpr int64_t kMaxHeadDim = int64_t(1) << 24;    // tokens, vocabulary, width
+constexpr int64_t kMaxHeadTiles = int64_t(1) << 28;  // tiles of 256 x 256 of any two of them: a launch counts its own in 31 bits
 struct HeadForward {
   const uint16_t* X;  // T x k BF16
   int64_t T, k, ld_x;

@@ -212,3 +212,12 @@ def test_adamw_batched_refuses_a_grad_scale_that_a_kernel_cannot_read(lib, scale
     call(None)
     with pytest.raises(ValueError, match="grad_scale"):
         call(scale)
+
+
+@pytest.mark.parametrize("T,k,V", [(1 << 24, 16, 1 << 24), (1 << 24, 1 << 23, 256), (256, 1 << 24, 1 << 23)])
+def test_cross_entropy_refuses_more_tiles_than_a_launch_counts(lib, T, k, V):
+    """Sizes below 2^24 each, by either call, with any workspace; asked for one, the sizes are invalid too."""
+    kw = dict(T=T, k=k, V=V, ld_x=k, ld_w=k, ws_bytes=1 << 62)
+    refused(lib, ce_forward(lib, **kw), binding.ERR_UNSUPPORTED, "2^28 tiles")
+    refused(lib, ce_backward(lib, ld_dx=k, ld_dw=k, **kw), binding.ERR_UNSUPPORTED, "2^28 tiles")
+    assert binding.workspace_bytes(binding.OP_CROSS_ENTROPY_BACKWARD, T, V, k, 0) == 0
