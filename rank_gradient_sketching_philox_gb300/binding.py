@@ -755,8 +755,8 @@ def cross_entropy_backward(X, W, targets, lse, g, dX=None, dW=None, XP=None, C=N
 
 
 def adamw_problems(Ws, Gs, ms, vs, m_scales=None, v_scales=None, layers=None):
-    """The problem table of adamw_batched: lists of contiguous tensors of one
-    size per problem.  States: fp32 m and v, or float8_e4m3fn codes of m and
+    """The problem table of adamw_batched: lists of contiguous, 16-byte aligned
+    tensors of one size per problem.  States: fp32 m and v, or float8_e4m3fn codes of m and
     sqrt(v) with an fp32 scale per 256 values each."""
     n = len(Ws)
     eight = m_scales is not None
@@ -774,6 +774,9 @@ def adamw_problems(Ws, Gs, ms, vs, m_scales=None, v_scales=None, layers=None):
         _vector(G, size, None, dev, "G")
         _vector(ms[i], size, state, dev, "m")
         _vector(vs[i], size, state, dev, "v")
+        for t, name in ((W, "W"), (G, "G"), (ms[i], "m"), (vs[i], "v")):
+            if size and t.data_ptr() % 16:
+                raise ValueError("%s of tensor %d must be 16-byte aligned" % (name, i))
         scales = (None, None)
         if eight:
             for t in (m_scales[i], v_scales[i]):

@@ -1282,3 +1282,14 @@ def test_norm_of_two_widths_from_several_threads():
     for X, out, _ in jobs:
         want, _, _ = norm64(X, None, None, 1e-5)
         within(out[0], want, want.abs() * 2.0 ** -8 + 1e-4)
+
+
+def test_adamw_refuses_unaligned_tensors_when_it_is_built():
+    buf = torch.zeros(72, device=DEV)
+    good = lambda: torch.zeros(64, device=DEV)  # noqa: E731
+    for bad in range(4):
+        ts = [good() for _ in range(4)]
+        ts[bad] = buf[1:65]
+        with pytest.raises(ValueError, match="16-byte"):
+            rgs.AdamW([ts[0]], [ts[1]], state={"m": [ts[2]], "v": [ts[3]]})
+    rgs.AdamW([good()], [good()]).step(1e-3, step=0)
