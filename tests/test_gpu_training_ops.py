@@ -1293,3 +1293,123 @@ def test_adamw_refuses_unaligned_tensors_when_it_is_built():
         with pytest.raises(ValueError, match="16-byte"):
             rgs.AdamW([ts[0]], [ts[1]], state={"m": [ts[2]], "v": [ts[3]]})
     rgs.AdamW([good()], [good()]).step(1e-3, step=0)
+
+
+# ---- forms beside the usual ones -------------------------------------------------------
+
+@pytest.mark.parametrize("T", [1, 40, 128])
+@pytest.mark.parametrize("V", [100, 3000])
+def test_cross_entropy_few_tokens_all_ignored(T, V):
+    """At most 128 tokens, where every entry of D has two terms, and none is kept: zeros everywhere."""
+    k, r = 64, 8
+    X, W, _, up = ce_inputs(T, k, V, seed=12)
+    none = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    X[0, 0], nan = float("nan"), float("nan")
+    XP = randn(gen(1), T, r, dtype=BF)
+    lse = torch.zeros(T, device=DEV)
+    dX, dW = torch.full_like(X, nan), torch.full((V, k), nan, device=DEV)
+    C, status = torch.full((V, r), nan, device=DEV), torch.full((1,), -1, dtype=torch.int32, device=DEV)
+    rgs.cross_entropy_backward(X, W, none, lse, up, dX=dX, dW=dW, XP=XP, C=C, overwrite=True, dev_status=status)
+    assert (dX == 0).all() and (dW == 0).all() and (C == 0).all() and status.item() == 0
+    dW.fill_(2.0)
+    rgs.cross_entropy_backward(X, W, none, lse, up, dW=dW)
+    assert (dW == 2.0).all()
+
+
+def test_cross_entropy_forward_of_a_masked_out_entry():
+    """A row of W that makes an entry's logit -inf for positive X: as if the entry were not there."""
+    T, k, V = 70, 72, 500
+    X, W, targets, _ = ce_inputs(T, k, V, seed=13)
+    X = X.abs() + 0.25
+    targets = torch.where(targets == 7, 8, targets)
+    W[7] = -float("inf")
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse)
+    keep = torch.arange(V, device=DEV) != 7
+    shifted = torch.where(targets > 7, targets - 1, targets)
+    logits, elog, want, want_loss = ce64(X, W[keep], shifted, 1.0)
+    bound = elog.amax(1) + 2.0 ** -20 * (1 + want.abs() + logits.abs().amax(1)) + V * 2.0 ** -24
+    within(lse, want, bound)
+    within(loss, want_loss, 2 * bound)
+
+
+def test_cross_entropy_feeds_the_sketch_of_the_heads_weight():
+    """C from the backward call is what accumulate makes of the same D, rounded to BF16, and the projected inputs."""
+    T, k, V, r = 64, 128, 96, 16
+    X = synth.layer_x(T, k, 0, 0, device=DEV)
+    W = synth.layer_weight(V, k, 0, device=DEV)
+    targets = torch.arange(T, device=DEV)
+    loss, lse = torch.empty(T, device=DEV), torch.empty(T, device=DEV)
+    rgs.cross_entropy_forward(X, W, targets, loss, lse)
+    P = torch.empty(k, r, device=DEV)
+    rgs.sample_projection(rgs.PROJ_GAUSSIAN_QR, 3, 0, 0, P)
+    XP = torch.empty(T, r, dtype=BF, device=DEV)
+    rgs.project_inputs(X, P, XP)
+    up = torch.full((T,), 1.0 / T, device=DEV)
+    C = torch.full((V, r), float("nan"), device=DEV)
+    rgs.cross_entropy_backward(X, W, targets, lse, up, XP=XP, C=C, overwrite=True)
+    d, ed, _, _ = ce_grads64(X, W, targets, up, lse, 1.0)
+    want = d.t() @ XP.to(F64)
+    within(C, want, product_bound(d.t(), ed.t(), XP.to(F64)) * 1.01 + 1e-30)
+    D = d.to(F32).to(BF)
+    S = torch.empty(V, r, device=DEV)
+    rgs.accumulate(D, XP, S, overwrite=True)
+    both = product_bound(d.t(), (ed + d.abs() * 2.0 ** -8).t(), XP.to(F64)) * 2.02 + 1e-30
+    within(C, S.to(F64), both)
+
+
+def test_adamw_8_bit_codes_of_values_that_are_not_finite():
+    """NaN's code, apart from the sign, in both states: after the step that met the gradient and after the next."""
+    n = 1000
+    Ws, Gs = adam_tensors([n], BF, F32, seed=5)
+    Gs[0][3], Gs[0][300], Gs[0][999] = float("nan"), float("inf"), float("-inf")
+    hit = ~torch.isfinite(Gs[0])
+    opt = rgs.AdamW(Ws, Gs, state_bits=8, betas=BETAS, seed=6)
+    for step in range(2):
+        opt.step(LR, step=step)
+        for name in ("m", "u"):
+            code = opt.state_dict()[name][0].view(torch.uint8).to(torch.int64) & 0x7F
+            assert (code[hit] == 0x7F).all() and (code[~hit] < 0x7F).all()
+            assert torch.isfinite(opt.state_dict()[name + "_scale"][0]).all()
+        assert torch.isnan(Ws[0][hit]).all() and torch.isfinite(Ws[0][~hit]).all()
+
+
+def test_operators_on_two_streams_at_once():
+    """Calls of all operators on two streams side by side give the bits of calls on one."""
+    def inputs(seed):
+        T, k, V = 300, 512, 5000
+        X, W, targets, up = ce_inputs(T, k, V, seed=seed)
+        return X, W, targets, up, randn(gen(seed), k)
+
+    def run(X, W, targets, up, gamma, stream=None):
+        T, k = X.shape
+        o = [torch.empty(T, device=DEV) for _ in range(4)] + [torch.empty_like(X) for _ in range(3)] + [
+            torch.empty(W.shape, device=DEV), torch.empty(k, device=DEV), W.clone()]
+        mean, rstd, loss, lse, Y, dY, dX, dW, dg, Wn = o
+        opt = rgs.AdamW([Wn], [dW], state_bits=8, seed=1)
+
+        def calls():
+            rgs.layer_norm_forward(X, gamma, None, Y, mean, rstd, stream=stream)
+            rgs.cross_entropy_forward(Y, W, targets, loss, lse, stream=stream)
+            rgs.cross_entropy_backward(Y, W, targets, lse, up, dX=dY, dW=dW, overwrite=True, stream=stream)
+            rgs.layer_norm_backward(dY, X, gamma, mean, rstd, dX, dg, overwrite=True, stream=stream)
+            opt.step(1e-3, step=0, stream=stream)
+        return calls, o
+
+    sets = [inputs(s) for s in (21, 22)]
+    want = []
+    for s in sets:
+        calls, o = run(*s)
+        calls()
+        torch.cuda.synchronize()
+        want.append(o)
+    streams = [torch.cuda.Stream() for _ in sets]
+    made = [run(*s, stream=stream) for s, stream in zip(sets, streams)]
+    torch.cuda.synchronize()
+    for _ in range(3):  # the weights move on from call to call; the rest is the same each time
+        for (calls, o), w in zip(made, want):
+            calls()
+    torch.cuda.synchronize()
+    for (_, o), w in zip(made, want):
+        for a, b in zip(o[:-1], w[:-1]):
+            assert torch.equal(a, b)
