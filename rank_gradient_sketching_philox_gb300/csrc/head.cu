@@ -671,11 +671,15 @@ __device__ __forceinline__ void join(float& mx, float& sum, float mx1, float sum
 }
 
 // Dot product of two BF16 rows by a warp, in fp32: the same bits wherever it is taken.
-__device__ __forceinline__ float warp_dot(const uint16_t* x, const uint16_t* w, int64_t k) {
+// COPY: x is also copied to y.
+template <bool COPY>
+__device__ __forceinline__ float warp_dot(const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, int64_t k,
+                                          uint16_t* __restrict__ y) {
   float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
   for (int64_t i = threadIdx.x & 31; i < k / 8; i += 32) {
     const uint4 a = reinterpret_cast<const uint4*>(x)[i], b = reinterpret_cast<const uint4*>(w)[i];
+    if (COPY) reinterpret_cast<uint4*>(y)[i] = a;
     const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -722,7 +726,7 @@ __global__ void __launch_bounds__(256) head_combine_kernel(const float2* partial
   const int64_t drow = row0 + warp;
   const int64_t target = drow < T ? targets[drow] : -1;
   float dot = 0.f;
-  if (target >= 0 && target < V) dot = warp_dot(X + drow * ld_x, W + target * ld_w, k);
+  if (target >= 0 && target < V) dot = warp_dot<false>(X + drow * ld_x, W + target * ld_w, k, nullptr);
   if (lane == 0) hit[warp] = dot;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
@@ -847,19 +851,16 @@ __global__ void __launch_bounds__(256) head_gather_kernel(const __grid_constant_
     }
     if (row < a.T) {
       if (t >= 0 && t < a.V) {
-        const uint4* x = reinterpret_cast<const uint4*>(a.X + row * a.ld_x);
-        uint4* y = reinterpret_cast<uint4*>(a.Xc + dst * a.k);
-#pragma unroll 4
-        for (int64_t i = lane; i < a.k / 8; i += 32) y[i] = x[i];
+        const float dot = warp_dot<true>(a.X + row * a.ld_x, a.W + t * a.ld_w, a.k, a.Xc + dst * a.k);
         if (a.XP)
           for (int64_t i = lane; i < a.r; i += 32) a.XPc[dst * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
         if (a.two_terms) {
-          uint4* z = y + kHalf * (a.k / 8);
+          const uint4* x = reinterpret_cast<const uint4*>(a.X + row * a.ld_x);
+          uint4* z = reinterpret_cast<uint4*>(a.Xc + (dst + kHalf) * a.k);
           for (int64_t i = lane; i < a.k / 8; i += 32) z[i] = x[i];
           if (a.XP)
             for (int64_t i = lane; i < a.r; i += 32) a.XPc[(dst + kHalf) * a.ld_xpc + i] = a.XP[row * a.ld_xp + i];
         }
-        const float dot = warp_dot(a.X + row * a.ld_x, a.W + t * a.ld_w, a.k);
         if (lane == 0) {
           a.hit[dst] = expm1f(fmaf(dot, a.scale, -a.lse[row]));
           a.lse_log2[dst] = a.lse[row] * kLog2e;
