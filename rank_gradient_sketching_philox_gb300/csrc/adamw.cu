@@ -20,9 +20,9 @@
 // A thread works on eight values at a time, one Philox block for each stream; a
 // warp's 256 values are one block of an 8-bit state.  fp32 states are bound by HBM
 // (268M BF16 weights: 866 us, 1.01 of the copy rate over 22 bytes a value); 8-bit
-// states by instruction issue: 68 instructions a value, 15 of them the three
-// Philox streams, against the 55 that the 10 bytes' time would allow at a full
-// issue rate (638 us, 0.62 of the copy rate).  Arithmetic goes in packed pairs.
+// states by instruction issue: 68 instructions a value at 0.71 of the issue slots, 15
+// of them the three Philox streams, against the 55 that the 10 bytes' time would allow
+// at a full issue rate (638 us, 0.62 of the copy rate).  Arithmetic goes in packed pairs.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -41,17 +41,19 @@
 // vocabulary of a tile is split over several, whose fp32 parts head_dx_sum_kernel
 // adds.
 //
-// What bounds it, tokens x k x vocabulary: many tokens the tensor cores' rate, which
-// the power limit sets (8192 x 4096 x 131072 forward 5.2 ms, 1.70 PFLOP/s; 4096 x 4096
-// x 65536 backward 3.71 ms, 1.78 PFLOP/s; a plain matrix product of that length runs at
-// 1.72); few tokens the stream of W (16 x 2048 x 32768 forward: 38 us, 0.52 of the copy
-// rate: 128 tiles are two rounds for 76 pairs, and 11 us go to starts, ends and the
-// join); a backward pass over few tokens the epilogues of dW, whose tiles have few
-// chunks of MMAs (19 x 3624 x 47943: 382 us, 0.27 of the copy rate; a tile costs its
-// pair some 4 us, 2.5 of them reading TMEM and packing, 1.8 storing); 1000 x 2048 x
-// 32771 backward (300 us, 0.70 of the MMAs' time) the same, with 16 chunks to a tile;
-// small k the epilogues' reads of TMEM, beside which MMAs run slower (8192 x 512 x
-// 32768 forward: 285 us, 195 without them).
+// What bounds it, tokens x k x vocabulary, times in a long run of passes: many tokens
+// the tensor cores' rate, which the power limit sets (8192 x 4096 x 131072 forward 5.2
+// ms, 1.70 PFLOP/s, where a plain matrix product of that length runs at 1.72; 4096 x
+// 4096 x 65536 backward with a tenth of the tokens ignored 3.7 to 3.8 ms, 1.56 to 1.61
+// PFLOP/s over the kept ones, and 3.4 ms on a cool GPU); few tokens the stream of W (16
+// x 2048 x 32768 forward: 38 us, 0.52 of the copy rate: 128 tiles are two rounds for 76
+// pairs, and 11 us go to starts, ends and the join); a backward pass over few tokens
+// the epilogues of dW, whose tiles have few chunks of MMAs (19 x 3624 x 47943: 383 us,
+// 0.27 of the copy rate; logits and D take 83 of it, dX and dW 271, of which 2820
+// tiles of dW at some 4 us a pair, 2.5 of them reading TMEM and packing, 1.8 storing,
+// are 148); 1000 x 2048 x 32771 backward (300 us, 0.63 of the kept tokens' MMAs' time)
+// the same, with 16 chunks to a tile; small k the epilogues' reads of TMEM, beside which
+// MMAs run slower (8192 x 512 x 32768 forward: 295 us, 195 without them).
 //
 // Softmax statistics and every sum are fp32.  A tile's result is written by one
 // thread after a fixed-order accumulation, so results do not depend on timing.

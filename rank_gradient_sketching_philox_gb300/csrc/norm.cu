@@ -28,13 +28,13 @@
 // there, once for each of the two passes over a row.  B rows are worked on side by
 // side, so that their sums' shuffles overlap, and one block barrier a set both
 // joins the warps' sums and tells that the slot of the set before can be filled
-// again.  32768 x 4096 BF16: 141 us, 0.84 of the copy rate over 6 bytes an element.
+// again.  32768 x 4096 BF16: 139 us, 0.85 of the copy rate over 6 bytes an element.
 //
 // Elements come in vectors of 16 bytes (VE of them).  Rows that do not start on 16
 // bytes or end inside a vector: both passes take the vectors between a row's first
 // and last boundary, and the elements beside those one by one, as long as all
 // matrices' rows start on the same place between two boundaries (16384 x 4095 BF16:
-// 58 us forward, 0.68 of the copy rate, and 97 us backward, 0.61; single elements all
+// 57 us forward, 0.70 of the copy rate, and 97 us backward, 0.61; single elements all
 // along take 148 and 136).  The place comes again after at most 8 rows, and the
 // backward pass gives a block rows that far apart, so that its threads' columns stay
 // the same.  Its copies start and end at the boundaries around a row (the bytes beyond
