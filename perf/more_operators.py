@@ -279,7 +279,7 @@ def _mm8(s):
 
 def _gnorm(s):
     parts = s["flat"].view(-1, ALIGN).float()   # a long sum: parts in 32 bits, their sum in 64
-    norm = parts.square().sum(1).double().sum().sqrt()
+    norm = parts.square().sum(1).double().sum(0, keepdim=True).sqrt()
     scale = torch.where(norm <= MAX_NORM, 1.0, MAX_NORM / norm).float()
     out = {"norm": norm.float(), "scale": scale}
     if s["case"]["clip"]:
@@ -427,7 +427,7 @@ def _mm8_64(s):
 
 
 def _gnorm64(s):
-    norm = torch.linalg.vector_norm(s["flat"], dtype=torch.float64)
+    norm = torch.linalg.vector_norm(s["flat"], dtype=torch.float64).view(1)
     scale = (MAX_NORM / norm).clamp(max=1.0)
     out = {"norm": norm, "scale": scale}
     if s["case"]["clip"]:
