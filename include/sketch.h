@@ -89,7 +89,9 @@ typedef enum {
     SKETCH_OP_UPDATE_SGD = 4,
     SKETCH_OP_LAYER_NORM_BACKWARD = 5,    /* T, k */
     SKETCH_OP_CROSS_ENTROPY_FORWARD = 6,  /* T, d = V */
-    SKETCH_OP_CROSS_ENTROPY_BACKWARD = 7  /* T, d = V, k, r = the sketch's rank or 0 */
+    SKETCH_OP_CROSS_ENTROPY_BACKWARD = 7, /* T, d = V, k, r = the sketch's rank or 0 */
+    SKETCH_OP_RMS_NORM_BACKWARD = 8,      /* T, k */
+    SKETCH_OP_GRAD_NORM = 9               /* T = the number of tensors */
 } sketch_op;
 
 /* Element types of the training operators' tensors. */
@@ -435,6 +437,95 @@ typedef struct {
 SKETCH_API sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem* problems, double lr, double beta1,
                                               double beta2, double eps, double weight_decay,
                                               const float* grad_scale, uint64_t seed, uint32_t step, void* stream);
+
+/* Root-mean-square norm of each row of a residual stream: s = x + r, rstd = 1 /
+ * sqrt(mean(s^2) + eps), y = s rstd gamma.  X, R, S and Y (T x k) have type x_type and
+ * row strides >= k (any value; rows that start on 16 bytes are the fast case).  R
+ * (what a block adds to the stream) may be NULL: s = x.  S (nullable, only with R)
+ * receives the new stream, rounded once; it may be X or R.  Y (nullable) receives y; it
+ * may be X or R where S is not that one.  Q and scale (nullable, both or neither; Y or Q is given)
+ * receive y in 8 bits for sketch_matmul_blocks, rows on 16 bytes (ld_q a multiple of
+ * 16): E4M3 codes and an fp32 scale for each row's 128 columns, T x ceil(k / 128)
+ * contiguous, the block's largest magnitude over 448 (at least 2^-126).  A block that
+ * holds an infinity or a NaN has a NaN scale and NaN codes.  gamma: k contiguous
+ * values of w_type, or NULL (ones).  rstd (T fp32, nullable) is for the backward pass.
+ * All sums are fp32: S's rounding does not enter Y, nor Y's Q.  T, k >= 1; eps >= 0. */
+SKETCH_API sketch_status sketch_rms_norm_forward(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
+                                                 const void* R, int64_t ld_r, void* S, int64_t ld_s,
+                                                 const void* gamma, sketch_dtype w_type, float eps, void* Y,
+                                                 int64_t ld_y, uint8_t* Q, int64_t ld_q, float* scale, float* rstd,
+                                                 void* stream);
+
+/* Its gradient.  With xh = s rstd and dxh = dY gamma: dX = rstd (dxh - xh mean(dxh
+ * xh)) + dS, the gradient of x and of r alike; dgamma (+)= sum over rows of dY xh (k
+ * fp32).  dS (nullable, only with dX) is the gradient that reaches S from the rest of the stream.  dY,
+ * S, dS and dX have one type; dX may be dY or dS.  dX and dgamma may be NULL, not both.
+ * overwrite = 1 replaces dgamma, 0 adds to it. */
+SKETCH_API sketch_status sketch_rms_norm_backward(const void* dY, int64_t ld_dy, const void* S, sketch_dtype x_type,
+                                                  int64_t T, int64_t k, int64_t ld_s, const void* gamma,
+                                                  sketch_dtype w_type, const float* rstd, const void* dS,
+                                                  int64_t ld_ds, void* dX, int64_t ld_dx, float* dgamma,
+                                                  int overwrite, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- 8-bit products -----------------------------------------------------------
+ * The two dense products that a sketched layer still has, its output X W^T and its
+ * input's gradient D W, on 8-bit operands: E4M3 codes (uint8_t bit patterns), a
+ * value being its code times the fp32 scale of its block.  Activations and output
+ * derivatives have a scale for each row's 128 columns (what they vary by), weights one
+ * for each 128 rows and 128 columns, so that W and its transpose share them.
+ *
+ * Codes and scales of X (T x k of x_type, any row stride >= k): rows = 1, or 128 for
+ * weights; scale: ceil(T / rows) x ceil(k / 128) contiguous, the block's largest magnitude
+ * over 448 (at least 2^-126); codes round to nearest, ties to even.  Q: T x k.  Qt
+ * (nullable, rows = 128 only): the same codes transposed, k x T, for the product D W;
+ * its scales are those of Q, transposed.  Q may then be NULL.  Q and Qt are 16-byte
+ * aligned with row strides that are multiples of 16; what lies between rows is left as
+ * it is.  A block with an infinity or a NaN has a NaN scale and NaN codes. */
+SKETCH_API sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
+                                                int rows, uint8_t* Q, int64_t ld_q, float* scale, uint8_t* Qt,
+                                                int64_t ld_qt, void* stream);
+
+/* Y (+)= A B^T.  A: T x k codes with a_scale (T x ceil(k / 128), row stride ld_as);
+ * B: N x k codes with b_scale for each 128 rows and 128 columns, block (i, j) at
+ * b_scale[i bs_row + j bs_col].  So Y = X W^T with B = Q of W (bs_row = ceil(k / 128),
+ * bs_col = 1), and dX = D W with B = Qt of W and the scales' strides exchanged.  A and
+ * B are 16-byte aligned, ld_a and ld_b >= k and multiples of 16; k is any number >= 1, and what
+ * lies between rows reaches no result.  Y: T x N BF16 or fp32, 16-byte aligned, ld_y a
+ * multiple of 8.  overwrite = 1 replaces Y, 0 adds to an fp32 Y; a BF16 Y is always
+ * replaced.  T, N and k are at most 2^24 each, T and N spanning at most 2^28
+ * tiles of 256 x 256 (else SKETCH_ERR_UNSUPPORTED).  A block's products add up in fp32
+ * on the tensor cores, the blocks in fp32.  Y must not overlap an input. */
+SKETCH_API sketch_status sketch_matmul_blocks(const uint8_t* A, int64_t T, int64_t k, int64_t ld_a,
+                                              const float* a_scale, int64_t ld_as, const uint8_t* B, int64_t N,
+                                              int64_t ld_b, const float* b_scale, int64_t bs_row, int64_t bs_col,
+                                              void* Y, sketch_dtype y_type, int64_t ld_y, int overwrite,
+                                              void* stream);
+
+/* ---- Clipping by the global norm ------------------------------------------------
+ * Gradients (or sketches) G of n >= 1 tensors, contiguous, aligned to their elements
+ * (16 bytes are the fast case); count = 0 elements is allowed. */
+typedef struct {
+    const void* G;
+    void* out;            /* sketch_grad_scale_batched only; may be G */
+    int64_t count;
+    sketch_dtype type;    /* of G and out */
+} sketch_grad_problem;
+
+/* norm = sqrt(sum of g^2 over all tensors), and scale = 1 where norm <= max_norm, else
+ * max_norm / norm: a device scalar for sketch_adamw_batched's grad_scale or for
+ * sketch_grad_scale_batched (scale may be NULL, max_norm is then not used).  max_norm
+ * is finite and > 0.  Both are right for all finite gradients, of whatever size (a norm
+ * past fp32's range is written as infinity, its scale is right all the same);
+ * an infinity among them gives norm infinity and scale 0, a NaN gives NaN for both.
+ * The result depends on the tensors' values and sizes alone. */
+SKETCH_API sketch_status sketch_grad_norm_batched(int n, const sketch_grad_problem* problems, float max_norm,
+                                                  float* norm, float* scale, void* ws, size_t ws_bytes,
+                                                  void* stream);
+
+/* out = G * scale (a device scalar), rounded once to the tensor's type.  Where out is G
+ * and the scale is 1, nothing is read or written. */
+SKETCH_API sketch_status sketch_grad_scale_batched(int n, const sketch_grad_problem* problems, const float* scale,
+                                                   void* stream);
 
 /* Read and clear the device error word of the current device: bits set by
  * kernels whose bounded internal waits gave up (a kernel that cannot make

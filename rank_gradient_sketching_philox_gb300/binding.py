@@ -30,6 +30,8 @@ OP_UPDATE_SGD = 4
 OP_LAYER_NORM_BACKWARD = 5
 OP_CROSS_ENTROPY_FORWARD = 6
 OP_CROSS_ENTROPY_BACKWARD = 7
+OP_RMS_NORM_BACKWARD = 8
+OP_GRAD_NORM = 9
 
 DTYPE_BF16 = 0
 DTYPE_FP32 = 1
@@ -51,7 +53,9 @@ EXPORTS = ("sketch_workspace_bytes", "sketch_sample_projection", "sketch_project
            "sketch_split_projection_batched", "sketch_project_inputs_fp32xp_batched",
            "sketch_accumulate_fp32xp_batched", "sketch_split_projection_grouped",
            "sketch_layer_norm_forward", "sketch_layer_norm_backward", "sketch_cross_entropy_forward",
-           "sketch_cross_entropy_backward", "sketch_adamw_batched", "sketch_status_string",
+           "sketch_cross_entropy_backward", "sketch_adamw_batched", "sketch_rms_norm_forward",
+           "sketch_rms_norm_backward", "sketch_quantize_blocks", "sketch_matmul_blocks",
+           "sketch_grad_norm_batched", "sketch_grad_scale_batched", "sketch_status_string",
            "sketch_last_error")
 
 
@@ -86,6 +90,10 @@ class AdamWProblem(ctypes.Structure):
     _fields_ = [("W", ctypes.c_void_p), ("G", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
                 ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
                 ("layer", ctypes.c_uint32), ("w_type", ctypes.c_int), ("g_type", ctypes.c_int)]
+
+
+class GradProblem(ctypes.Structure):
+    _fields_ = [("G", ctypes.c_void_p), ("out", ctypes.c_void_p), ("count", ctypes.c_int64), ("type", ctypes.c_int)]
 
 
 class SketchError(RuntimeError):
@@ -143,6 +151,15 @@ _SIGS = {
                                                  _vp, _vp, _i64, _vp, _c.c_int, _i64, _vp, _i64, _i64, _vp,
                                                  _c.c_int, _vp, _vp, _c.c_size_t, _vp]),
     "sketch_adamw_batched": (_c.c_int, [_c.c_int, _vp] + [_c.c_double] * 5 + [_vp, _u64, _u32, _vp]),
+    "sketch_rms_norm_forward": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _c.c_int,
+                                           _c.c_float, _vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "sketch_rms_norm_backward": (_c.c_int, [_vp, _i64, _vp, _c.c_int, _i64, _i64, _i64, _vp, _c.c_int, _vp, _vp, _i64,
+                                            _vp, _i64, _vp, _c.c_int, _vp, _c.c_size_t, _vp]),
+    "sketch_quantize_blocks": (_c.c_int, [_vp, _c.c_int, _i64, _i64, _i64, _c.c_int, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "sketch_matmul_blocks": (_c.c_int, [_vp, _i64, _i64, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _vp,
+                                        _c.c_int, _i64, _c.c_int, _vp]),
+    "sketch_grad_norm_batched": (_c.c_int, [_c.c_int, _vp, _c.c_float, _vp, _vp, _vp, _c.c_size_t, _vp]),
+    "sketch_grad_scale_batched": (_c.c_int, [_c.c_int, _vp, _vp, _vp]),
     "sketch_status_string": (_c.c_char_p, [_c.c_int]),
     "sketch_last_error": (_c.c_char_p, []),
 }
@@ -797,5 +814,213 @@ def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=No
         _vector(grad_scale, 1, torch.float32, dev, "grad_scale")
     st = lib().sketch_adamw_batched(len(probs), probs, lr, betas[0], betas[1], eps, weight_decay, _addr(grad_scale),
                                     seed & 0xFFFFFFFFFFFFFFFF, step, _stream_of(stream, dev))
+    if st:
+        _check(st)
+
+
+# --------------------------------------------------------------------------
+# The residual stream's norm, 8-bit products, clipping
+# --------------------------------------------------------------------------
+
+SCALE_BLOCK = 128  # columns, or rows and columns of a weight, that share a scale
+
+
+class _on:
+    """The launches inside go to ``device``, whatever device is current."""
+    __slots__ = ("index", "before")
+
+    def __init__(self, device):
+        self.index = device.index
+
+    def __enter__(self):
+        self.before = torch._C._cuda_exchangeDevice(self.index)
+
+    def __exit__(self, *exc):
+        torch._C._cuda_maybeExchangeDevice(self.before)
+
+
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError("the stream is not one of %s" % device)
+
+
+def code_rows(T, k, device="cuda"):
+    """An uninitialised T x k matrix of E4M3 codes whose rows start on 16 bytes, as
+    the 8-bit calls want them."""
+    return torch.empty(T, (k + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=device)[:, :k]
+
+
+def _codes(t, T, k, device, name):
+    """Row stride of a T x k matrix of codes."""
+    if t.dtype != torch.float8_e4m3fn or t.device != device or t.shape != (T, k):
+        raise ValueError("%s must be a %d x %d float8_e4m3fn matrix on %s" % (name, T, k, device))
+    ld, unit = t.stride()
+    if unit != 1 and k > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return ld if T > 1 else (k + 15) // 16 * 16
+
+
+def _scales(t, rows, cols, device, name):
+    if t.dtype != torch.float32 or t.device != device or t.shape != (rows, cols):
+        raise ValueError("%s must be a %d x %d float32 matrix on %s" % (name, rows, cols, device))
+    return t.stride()
+
+
+def _groups(n):
+    return (n + SCALE_BLOCK - 1) // SCALE_BLOCK
+
+
+def rms_norm_forward(X, gamma, rstd=None, R=None, S=None, Y=None, Q=None, scale=None, eps=1e-6, stream=None):
+    """Root-mean-square norm of the rows of s = X + R (T x k, BF16 or fp32; R may be
+    None): y = s rstd gamma.  S (only with R; may be X or R) receives s, Y (may be X or R) receives
+    y, and Q with scale (T x ceil(k / 128) fp32) y as E4M3 codes with a scale for each
+    row's 128 columns; Y or Q is given.  rstd (T fp32) is for the backward pass.  gamma
+    (k, BF16 or fp32) may be None."""
+    x_type = _dtype(X, "X")
+    shape, dtype, dev = _norm_x(X)
+    T, k = shape
+    ld_x = _norm_rows(X, shape, dtype, dev, "X")
+    ld_r = 0 if R is None else _norm_rows(R, shape, dtype, dev, "R")
+    ld_s = 0 if S is None else _norm_rows(S, shape, dtype, dev, "S")
+    ld_y = 0 if Y is None else _norm_rows(Y, shape, dtype, dev, "Y")
+    ld_q = 0 if Q is None else _codes(Q, T, k, dev, "Q")
+    if scale is not None:
+        _vector(scale, T * _groups(k), torch.float32, dev, "scale")
+    w_type = _norm_weights(gamma, None, k, dev)
+    if rstd is not None:
+        _vector(rstd, T, torch.float32, dev, "rstd")
+    _check_stream(stream, dev)
+    with _on(dev):
+        st = lib().sketch_rms_norm_forward(X.data_ptr(), x_type, T, k, ld_x, _addr(R), ld_r, _addr(S), ld_s,
+                                           _addr(gamma), w_type, eps, _addr(Y), ld_y, _addr(Q), ld_q, _addr(scale),
+                                           _addr(rstd), _stream_of(stream, dev))
+    if st:
+        _check(st)
+    return Y if Y is not None else Q
+
+
+def rms_norm_backward(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, overwrite=False, ws=None, stream=None):
+    """dX (may be dY or dS) and dgamma (k fp32; replaced with overwrite, else added
+    to) of rms_norm_forward; each may be None.  dS: the gradient that reaches S
+    from the rest of the stream, added to dX, which is the gradient of X and of R."""
+    x_type = _dtype(S, "S")
+    shape, dtype, dev = _norm_x(S)
+    T, k = shape
+    ld_s, ld_dy = _norm_rows(S, shape, dtype, dev, "S"), _norm_rows(dY, shape, dtype, dev, "dY")
+    ld_ds = 0 if dS is None else _norm_rows(dS, shape, dtype, dev, "dS")
+    ld_dx = 0 if dX is None else _norm_rows(dX, shape, dtype, dev, "dX")
+    w_type = _norm_weights(gamma, None, k, dev)
+    _vector(rstd, T, torch.float32, dev, "rstd")
+    if dgamma is not None:
+        _vector(dgamma, k, torch.float32, dev, "dgamma")
+    _check_stream(stream, dev)
+    with _on(dev):
+        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
+        st = lib().sketch_rms_norm_backward(dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s, _addr(gamma), w_type,
+                                            rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
+                                            1 if overwrite else 0, ws_at, nbytes, _stream_of(stream, dev))
+    if st:
+        _check(st)
+    return dX
+
+
+def quantize_blocks(X, Q, scale, rows=1, Qt=None, stream=None):
+    """E4M3 codes of X (T x k, BF16 or fp32) with a scale for each row's 128 columns,
+    or with rows=128 (weights) for each 128 rows and 128 columns; scale:
+    ceil(T / rows) x ceil(k / 128) fp32.  Qt (k x T, rows=128 only): the same codes transposed,
+    with scales scale.t(); Q may then be None."""
+    x_type = _dtype(X, "X")
+    shape, dtype, dev = _norm_x(X)
+    T, k = shape
+    ld_x = _norm_rows(X, shape, dtype, dev, "X")
+    ld_q = 0 if Q is None else _codes(Q, T, k, dev, "Q")
+    ld_qt = 0 if Qt is None else _codes(Qt, k, T, dev, "Qt")
+    _vector(scale, (T + rows - 1) // rows * _groups(k) if rows > 0 else 0, torch.float32, dev, "scale")
+    _check_stream(stream, dev)
+    with _on(dev):
+        st = lib().sketch_quantize_blocks(X.data_ptr(), x_type, T, k, ld_x, rows, _addr(Q), ld_q, scale.data_ptr(),
+                                          _addr(Qt), ld_qt, _stream_of(stream, dev))
+    if st:
+        _check(st)
+    return Q
+
+
+def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
+    """Y = A B^T of codes with block scales: A (T x k) with a_scale (T x ceil(k /
+    128)), B (N x k) with b_scale (ceil(N / 128) x ceil(k / 128), any strides).  A layer's output
+    takes B = Q of its weight W and b_scale = scale, its input's gradient B = Qt
+    and b_scale = scale.t().  Y (T x N) BF16, or fp32, which overwrite=False adds to."""
+    dev = A.device
+    if not A.is_cuda or A.dim() != 2 or B.dim() != 2 or Y.dim() != 2:
+        raise ValueError("A, B and Y must be 2-D CUDA tensors")
+    T, k = A.shape
+    N = B.shape[0]
+    ld_a, ld_b = _codes(A, T, k, dev, "A"), _codes(B, N, k, dev, "B")
+    ld_as, unit = _scales(a_scale, T, _groups(k), dev, "a_scale")
+    if unit != 1 and _groups(k) > 1:
+        raise ValueError("a_scale must have unit column stride")
+    if T == 1:
+        ld_as = _groups(k)
+    bs_row, bs_col = _scales(b_scale, _groups(N), _groups(k), dev, "b_scale")
+    y_type = _dtype(Y, "Y")
+    if Y.shape != (T, N) or Y.device != dev or (N > 1 and Y.stride(1) != 1):
+        raise ValueError("Y must be a %d x %d matrix on %s with unit column stride" % (T, N, dev))
+    ld_y = Y.stride(0) if T > 1 else (N + 7) // 8 * 8
+    _check_stream(stream, dev)
+    with _on(dev):
+        st = lib().sketch_matmul_blocks(A.data_ptr(), T, k, ld_a, a_scale.data_ptr(), ld_as, B.data_ptr(), N, ld_b,
+                                        b_scale.data_ptr(), bs_row, bs_col, Y.data_ptr(), y_type, ld_y,
+                                        1 if overwrite else 0, _stream_of(stream, dev))
+    if st:
+        _check(st)
+    return Y
+
+
+def grad_problems(Gs, outs=None):
+    """The problem table of grad_norm_batched and grad_scale_batched: contiguous
+    tensors of any shapes, and those that receive the scaled ones (the same by default)."""
+    Gs = list(Gs)
+    outs = Gs if outs is None else list(outs)
+    if not Gs or len(outs) != len(Gs):
+        raise ValueError("the lists of a batch have one length, and at least one tensor")
+    probs = (GradProblem * len(Gs))()
+    for i, (G, out) in enumerate(zip(Gs, outs)):
+        dev = G.device
+        if dev.type != "cuda" or dev != Gs[0].device:
+            raise ValueError("tensor %d must be a CUDA tensor on one device with the others" % i)
+        _vector(G, G.numel(), None, dev, "G")
+        _vector(out, G.numel(), G.dtype, dev, "out")
+        probs[i] = GradProblem(G.data_ptr(), out.data_ptr(), G.numel(), _dtype(G, "G"))
+    return probs
+
+
+def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=None):
+    """norm = sqrt(sum of squares over the tensors of grad_problems), and scale = 1
+    where norm <= max_norm, else max_norm / norm (one-element fp32 tensors)."""
+    dev = norm.device
+    if not norm.is_cuda:
+        raise ValueError("norm must be a CUDA tensor")
+    _vector(norm, 1, torch.float32, dev, "norm")
+    if scale is not None:
+        _vector(scale, 1, torch.float32, dev, "scale")
+    _check_stream(stream, dev)
+    with _on(dev):
+        keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, dev, stream, ws)
+        st = lib().sketch_grad_norm_batched(len(probs), probs, max_norm, norm.data_ptr(), _addr(scale), ws_at, nbytes,
+                                            _stream_of(stream, dev))
+    if st:
+        _check(st)
+    return norm
+
+
+def grad_scale_batched(probs, scale, stream=None):
+    """out = G * scale for the tensors of grad_problems; scale: a one-element fp32 tensor."""
+    dev = scale.device
+    if not scale.is_cuda:
+        raise ValueError("scale must be a CUDA tensor")
+    _vector(scale, 1, torch.float32, dev, "scale")
+    _check_stream(stream, dev)
+    with _on(dev):
+        st = lib().sketch_grad_scale_batched(len(probs), probs, scale.data_ptr(), _stream_of(stream, dev))
     if st:
         _check(st)

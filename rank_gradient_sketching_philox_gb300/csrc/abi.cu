@@ -121,6 +121,9 @@ size_t op_ws_bytes(sketch_op op, int64_t T, int64_t d, int64_t k, int64_t r) {
       return (head_sizes_ok(T, d, k) && r >= 0 && r <= rgs::kMaxRank)
                  ? rgs::head_backward_workspace_bytes(T, d, k, r)
                  : 0;
+    case SKETCH_OP_RMS_NORM_BACKWARD:
+      return (T >= 1 && T <= kMaxDim && k >= 1 && k <= kMaxDim) ? rgs::rms_backward_workspace_bytes(T, k) : 0;
+    case SKETCH_OP_GRAD_NORM: return (T >= 1 && T <= (1 << 20)) ? rgs::grad_norm_workspace_bytes(T) : 0;
     default: break;
   }
   if (r < 1 || r > rgs::kMaxRank) return 0;
@@ -382,6 +385,29 @@ sketch_status check_adamw(const sketch_adamw_problem& p, bool states8) {
   CHECK_PTR(p.v);
   CHECK_OPT_ALIGN(p.m_scale, 4);
   CHECK_OPT_ALIGN(p.v_scale, 4);
+  return SKETCH_OK;
+}
+
+// Rows of 8-bit codes: 16-byte aligned, as TMA reads them.
+sketch_status check_ld_codes(const char* name, int64_t ld, int64_t width) {
+  if (ld < width || ld > kMaxDim)
+    return fail(SKETCH_ERR_INVALID_ARG, "%s=%lld out of [%lld, 2^31)", name, (long long)ld, (long long)width);
+  if (ld % 16 != 0) return fail(SKETCH_ERR_INVALID_ARG, "%s=%lld is not a multiple of 16", name, (long long)ld);
+  return SKETCH_OK;
+}
+
+sketch_status check_grads(int n, const sketch_grad_problem* problems, bool out) {
+  TRY(check_n(n));
+  if (problems == nullptr) return fail(SKETCH_ERR_INVALID_ARG, "problems is NULL");
+  for (int i = 0; i < n; ++i) {
+    const sketch_grad_problem& p = problems[i];
+    if (p.count < 0 || p.count > (int64_t(1) << 40))
+      return fail(SKETCH_ERR_INVALID_ARG, "count=%lld out of [0, 2^40]", (long long)p.count);
+    CHECK_DTYPE(p.type);
+    if (p.count == 0) continue;
+    CHECK_ELEM_PTR(p.G, p.type);
+    if (out) CHECK_ELEM_PTR(p.out, p.type);
+  }
   return SKETCH_OK;
 }
 
@@ -671,6 +697,153 @@ sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem* problems, 
   h.grad_scale = grad_scale;
   return launch_result(rgs::launch_adamw(n, problems, states8, h, seed, step, static_cast<cudaStream_t>(stream)),
                        "adamw");
+}
+
+sketch_status sketch_rms_norm_forward(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
+                                      const void* R, int64_t ld_r, void* S, int64_t ld_s, const void* gamma,
+                                      sketch_dtype w_type, float eps, void* Y, int64_t ld_y, uint8_t* Q, int64_t ld_q,
+                                      float* scale, float* rstd, void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("k", k));
+  CHECK_DTYPE(x_type);
+  CHECK_DTYPE(w_type);
+  TRY(check_row_stride("ld_x", ld_x, k));
+  CHECK_ELEM_PTR(X, x_type);
+  if (!std::isfinite(eps) || eps < 0.f) return fail(SKETCH_ERR_INVALID_ARG, "eps is not finite and >= 0");
+  if (R) {
+    TRY(check_row_stride("ld_r", ld_r, k));
+    CHECK_ELEM_PTR(R, x_type);
+  }
+  if (S) {
+    if (!R) return fail(SKETCH_ERR_INVALID_ARG, "S is given without R");
+    TRY(check_row_stride("ld_s", ld_s, k));
+    CHECK_ELEM_PTR(S, x_type);
+  }
+  if (!Y && !Q) return fail(SKETCH_ERR_INVALID_ARG, "Y and Q are both NULL");
+  if (Y) {
+    TRY(check_row_stride("ld_y", ld_y, k));
+    CHECK_ELEM_PTR(Y, x_type);
+    if (Y == S) return fail(SKETCH_ERR_INVALID_ARG, "Y and S are one buffer");
+  }
+  if ((Q != nullptr) != (scale != nullptr)) return fail(SKETCH_ERR_INVALID_ARG, "Q and scale are given together");
+  if (Q) {
+    TRY(check_ld_codes("ld_q", ld_q, k));
+    CHECK_PTR(Q);
+    CHECK_ELEM_PTR(scale, SKETCH_FP32);
+  }
+  CHECK_OPT_ALIGN(gamma, w_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_OPT_ALIGN(rstd, 4);
+  const rgs::RmsForward a = {X,   (int)x_type, T, k,    ld_x, R,    ld_r,  S,   ld_s, gamma, (int)w_type,
+                             eps, Y,           ld_y, Q, ld_q, scale, rstd};
+  return launch_result(rgs::launch_rms_forward(a, static_cast<cudaStream_t>(stream)), "rms_norm_forward");
+}
+
+sketch_status sketch_rms_norm_backward(const void* dY, int64_t ld_dy, const void* S, sketch_dtype x_type, int64_t T,
+                                       int64_t k, int64_t ld_s, const void* gamma, sketch_dtype w_type,
+                                       const float* rstd, const void* dS, int64_t ld_ds, void* dX, int64_t ld_dx,
+                                       float* dgamma, int overwrite, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("k", k));
+  CHECK_DTYPE(x_type);
+  CHECK_DTYPE(w_type);
+  TRY(check_row_stride("ld_dy", ld_dy, k));
+  TRY(check_row_stride("ld_s", ld_s, k));
+  CHECK_ELEM_PTR(dY, x_type);
+  CHECK_ELEM_PTR(S, x_type);
+  CHECK_OPT_ALIGN(gamma, w_type == SKETCH_BF16 ? 2 : 4);
+  CHECK_ELEM_PTR(rstd, SKETCH_FP32);
+  if (overwrite != 0 && overwrite != 1) return fail(SKETCH_ERR_INVALID_ARG, "overwrite must be 0 or 1");
+  if (!dX && !dgamma) return fail(SKETCH_ERR_INVALID_ARG, "dX and dgamma are both NULL");
+  if (dX) {
+    TRY(check_row_stride("ld_dx", ld_dx, k));
+    CHECK_ELEM_PTR(dX, x_type);
+  }
+  if (dS) {
+    if (!dX) return fail(SKETCH_ERR_INVALID_ARG, "dS is given without dX");
+    TRY(check_row_stride("ld_ds", ld_ds, k));
+    CHECK_ELEM_PTR(dS, x_type);
+  }
+  CHECK_OPT_ALIGN(dgamma, 4);
+  TRY(check_ws(ws, ws_bytes, rgs::rms_backward_workspace_bytes(T, k)));
+  const rgs::RmsBackward a = {dY,   S,  (int)x_type, T,  k,     ld_dy,  ld_s,      gamma, (int)w_type,
+                              rstd, dS, ld_ds,       dX, ld_dx, dgamma, overwrite, static_cast<float*>(ws)};
+  return launch_result(rgs::launch_rms_backward(a, static_cast<cudaStream_t>(stream)), "rms_norm_backward");
+}
+
+sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x, int rows,
+                                     uint8_t* Q, int64_t ld_q, float* scale, uint8_t* Qt, int64_t ld_qt,
+                                     void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("k", k));
+  CHECK_DTYPE(x_type);
+  TRY(check_row_stride("ld_x", ld_x, k));
+  CHECK_ELEM_PTR(X, x_type);
+  if (rows != 1 && rows != 128) return fail(SKETCH_ERR_INVALID_ARG, "rows=%d is neither 1 nor 128", rows);
+  if (rows == 1 && Qt) return fail(SKETCH_ERR_INVALID_ARG, "Qt needs rows=128");
+  if (!Q && !Qt) return fail(SKETCH_ERR_INVALID_ARG, "Q and Qt are both NULL");
+  if (Q) {
+    TRY(check_ld_codes("ld_q", ld_q, k));
+    CHECK_PTR(Q);
+  }
+  if (Qt) {
+    TRY(check_ld_codes("ld_qt", ld_qt, T));
+    CHECK_PTR(Qt);
+  }
+  CHECK_ELEM_PTR(scale, SKETCH_FP32);
+  if (rows == 128 && rgs::ceil_div(T, 128) * rgs::ceil_div(k, 128) > kMaxDim)
+    return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld and k=%lld span 2^31 blocks or more", (long long)T, (long long)k);
+  const rgs::Quantize a = {X, (int)x_type, T, k, ld_x, rows, Q, ld_q, scale, Qt, ld_qt};
+  return launch_result(rgs::launch_quantize(a, static_cast<cudaStream_t>(stream)), "quantize_blocks");
+}
+
+sketch_status sketch_matmul_blocks(const uint8_t* A, int64_t T, int64_t k, int64_t ld_a, const float* a_scale,
+                                   int64_t ld_as, const uint8_t* B, int64_t N, int64_t ld_b, const float* b_scale,
+                                   int64_t bs_row, int64_t bs_col, void* Y, sketch_dtype y_type, int64_t ld_y,
+                                   int overwrite, void* stream) {
+  TRY(check_dim("T", T));
+  TRY(check_dim("N", N));
+  TRY(check_dim("k", k));
+  if (T > rgs::kMaxHeadDim || N > rgs::kMaxHeadDim || k > rgs::kMaxHeadDim ||
+      rgs::ceil_div(T, 256) * rgs::ceil_div(N, 256) > rgs::kMaxHeadTiles)
+    return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld, N=%lld, k=%lld: at most 2^24 each and 2^28 tiles of 256 x 256",
+                (long long)T, (long long)N, (long long)k);
+  const int64_t groups = rgs::ceil_div(k, 128);
+  CHECK_DTYPE(y_type);
+  TRY(check_ld_codes("ld_a", ld_a, k));
+  TRY(check_ld_codes("ld_b", ld_b, k));
+  TRY(check_row_stride("ld_as", ld_as, groups));
+  if (bs_row < 0 || bs_row > kMaxDim || bs_col < 0 || bs_col > kMaxDim)
+    return fail(SKETCH_ERR_INVALID_ARG, "bs_row=%lld or bs_col=%lld out of [0, 2^31)", (long long)bs_row,
+                (long long)bs_col);
+  TRY(check_ld("ld_y", ld_y, N));
+  CHECK_PTR(A);
+  CHECK_ELEM_PTR(a_scale, SKETCH_FP32);
+  CHECK_PTR(B);
+  CHECK_ELEM_PTR(b_scale, SKETCH_FP32);
+  CHECK_PTR(Y);
+  if (overwrite != 0 && overwrite != 1) return fail(SKETCH_ERR_INVALID_ARG, "overwrite must be 0 or 1");
+  const rgs::MatmulBlocks a = {A,       T,      k,      ld_a, a_scale,     ld_as, B,        N,
+                               ld_b,    b_scale, bs_row, bs_col, Y, (int)y_type, ld_y, overwrite};
+  return launch_result(rgs::launch_matmul_blocks(a, static_cast<cudaStream_t>(stream)), "matmul_blocks");
+}
+
+sketch_status sketch_grad_norm_batched(int n, const sketch_grad_problem* problems, float max_norm, float* norm,
+                                       float* scale, void* ws, size_t ws_bytes, void* stream) {
+  TRY(check_grads(n, problems, false));
+  if (scale && !(std::isfinite(max_norm) && max_norm > 0.f))
+    return fail(SKETCH_ERR_INVALID_ARG, "max_norm is not finite and > 0");
+  CHECK_ELEM_PTR(norm, SKETCH_FP32);
+  CHECK_OPT_ALIGN(scale, 4);
+  TRY(check_ws(ws, ws_bytes, rgs::grad_norm_workspace_bytes(n)));
+  return launch_result(rgs::launch_grad_norm(n, problems, max_norm, norm, scale, static_cast<double*>(ws),
+                                             static_cast<cudaStream_t>(stream)),
+                       "grad_norm");
+}
+
+sketch_status sketch_grad_scale_batched(int n, const sketch_grad_problem* problems, const float* scale, void* stream) {
+  TRY(check_grads(n, problems, true));
+  CHECK_ELEM_PTR(scale, SKETCH_FP32);
+  return launch_result(rgs::launch_grad_scale(n, problems, scale, static_cast<cudaStream_t>(stream)), "grad_scale");
 }
 
 sketch_status sketch_read_device_errors(int32_t* flags, void* stream) {

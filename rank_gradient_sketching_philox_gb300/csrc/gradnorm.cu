@@ -1,0 +1,238 @@
+// The global norm of many gradients, the factor that clips it, and the gradients'
+// product with a factor on the device.
+//
+//   norm = sqrt(sum over all tensors of g^2),  scale = 1 where norm <= max_norm, else max_norm / norm
+//
+// Bound by HBM: the norm reads each gradient once.  The tensors are cut into units of
+// kUnit values, dealt in their order to at most kBlocks blocks, whatever the GPU's size, so
+// that the sums' order depends on the tensors' sizes alone.  A thread adds its 32
+// squares of a unit in fp32 (four chains), the rest in fp64.  Squares that fp32 cannot
+// hold (sums that overflow, or small ones of values that are not zero) are taken again
+// in fp64, so that the norm is right for every finite gradient.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rows.cuh"
+
+namespace rgs {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kEach = 32;                  // values of a unit per thread
+constexpr int kUnit = kThreads * kEach;
+constexpr int kBlocks = 1024;              // partial sums of a launch
+constexpr int kTensors = 256;              // per launch
+
+struct GradBatch {
+  sketch_grad_problem p[kTensors];
+  int64_t begin[kTensors + 1];  // prefix of the tensors' units
+  int n;
+};
+
+// Whether 16-byte vectors of the tensor start on 16 bytes.
+__device__ __forceinline__ bool on_vector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// The units of block `block` of `blocks`, one after another: f(problem, first value).
+template <typename F>
+__device__ __forceinline__ void walk_units(const GradBatch& a, int block, int blocks, F f) {
+  const int64_t units = a.begin[a.n];
+  int64_t u = units * block / blocks;
+  const int64_t end = units * (block + 1) / blocks;
+  if (u >= end) return;
+  int lo = 0, hi = a.n;  // the last tensor that begins at or before the unit
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.begin[mid] <= u) lo = mid;
+    else hi = mid;
+  }
+  for (; u < end; ++u) {
+    while (u >= a.begin[lo + 1]) ++lo;
+    f(a.p[lo], (u - a.begin[lo]) * kUnit);
+  }
+}
+
+// A thread's values of a unit: vectors threadIdx.x, + 256, ... of it, or single
+// elements where the tensor does not start on 16 bytes or ends.  Values past the end
+// are zeros.
+template <typename G>
+__device__ __forceinline__ void load_unit(const G* g, int64_t n, int64_t first, float (&v)[kEach]) {
+  constexpr int VE = 16 / (int)sizeof(G);
+  if (first + kUnit <= n && on_vector(g)) {
+    uint4 raw[kEach / VE];
+    const uint4* p = reinterpret_cast<const uint4*>(g + first) + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kEach / VE; ++j) raw[j] = __ldg(p + j * kThreads);
+#pragma unroll
+    for (int j = 0; j < kEach / VE; ++j) {
+      Pair q[VE / 2];
+      vec_pairs<G>(raw[j], q);
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) {
+        const float2 f = split(q[i]);
+        v[j * VE + 2 * i] = f.x;
+        v[j * VE + 2 * i + 1] = f.y;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t e = first + j * kThreads + threadIdx.x;
+      v[j] = e < n ? (float)g[e] : 0.f;
+    }
+  }
+}
+
+constexpr float kSmallSum = 8.2718061255302767e-25f;  // 2^-80: squares of 2^-126 and less are lost beside it at 2^-46
+
+__device__ __forceinline__ double unit_sum(const float (&v)[kEach]) {
+  Pair s[2] = {0, 0};
+  uint32_t any = 0;
+#pragma unroll
+  for (int j = 0; j < kEach; j += 2) {
+    const Pair p = pair(v[j], v[j + 1]);
+    s[(j >> 1) & 1] = fma2(p, p, s[(j >> 1) & 1]);
+    any |= __float_as_uint(v[j]) | __float_as_uint(v[j + 1]);
+  }
+  const float sum = sum2(add2(s[0], s[1]));
+  if (sum >= kSmallSum && sum < INFINITY) return (double)sum;
+  if ((any & 0x7FFFFFFFu) == 0) return 0.0;
+  double d = 0.0;
+  for (int j = 0; j < kEach; ++j) d = fma((double)v[j], (double)v[j], d);
+  return d;
+}
+
+__device__ __forceinline__ double block_sum(double v, double* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) v += part[w];
+  return v;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradBatch a, double* partials) {
+  __shared__ double part[kThreads / 32];
+  cudaTriggerProgrammaticLaunchCompletion();  // grad_norm_join_kernel may come up as blocks leave
+  double sum = 0.0;
+  walk_units(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+    float v[kEach];
+    if (p.type == SKETCH_BF16) load_unit(static_cast<const __nv_bfloat16*>(p.G), p.count, first, v);
+    else load_unit(static_cast<const float*>(p.G), p.count, first, v);
+    sum += unit_sum(v);
+  });
+  sum = block_sum(sum, part);
+  if (threadIdx.x == 0) partials[blockIdx.x] = sum;
+}
+
+__global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* partials, int64_t n, float max_norm,
+                                                                  float* norm, float* scale) {
+  __shared__ double part[kThreads / 32];
+  cudaGridDependencySynchronize();
+  double sum = 0.0;
+  for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += partials[i];
+  sum = sqrt(block_sum(sum, part));
+  if (threadIdx.x == 0) {
+    *norm = (float)sum;
+    if (scale) *scale = sum <= (double)max_norm ? 1.f : (float)((double)max_norm / sum);
+  }
+}
+
+template <typename G>
+__device__ __forceinline__ void scale_unit(const G* g, G* out, int64_t n, int64_t first, float scale) {
+  constexpr int VE = 16 / (int)sizeof(G);
+  if (first + kUnit <= n && on_vector(g) && on_vector(out)) {
+    uint4 raw[kEach / VE];
+    const uint4* p = reinterpret_cast<const uint4*>(g + first) + threadIdx.x;
+#pragma unroll
+    for (int j = 0; j < kEach / VE; ++j) raw[j] = p[j * kThreads];
+    const Pair s = pair(scale, scale);
+#pragma unroll
+    for (int j = 0; j < kEach / VE; ++j) {
+      Pair q[VE / 2];
+      vec_pairs<G>(raw[j], q);
+#pragma unroll
+      for (int i = 0; i < VE / 2; ++i) q[i] = mul2(q[i], s);
+      store_vec<G>(out + first, j * kThreads + threadIdx.x, q);
+    }
+  } else {
+    for (int j = 0; j < kEach; ++j) {
+      const int64_t e = first + j * kThreads + threadIdx.x;
+      if (e < n) store_one(out + e, (float)g[e] * scale);
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradBatch a, const float* scale) {
+  const float s = *scale;
+  walk_units(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+    if (s == 1.f && p.out == p.G) return;
+    if (p.type == SKETCH_BF16)
+      scale_unit(static_cast<const __nv_bfloat16*>(p.G), static_cast<__nv_bfloat16*>(p.out), p.count, first, s);
+    else
+      scale_unit(static_cast<const float*>(p.G), static_cast<float*>(p.out), p.count, first, s);
+  });
+}
+
+// The launches of a batch, up to kTensors tensors each: f(table, blocks).
+template <typename F>
+cudaError_t for_batches(int n, const sketch_grad_problem* probs, F f) {
+  static thread_local GradBatch a;
+  for (int i = 0; i < n;) {
+    a.n = 0;
+    a.begin[0] = 0;
+    for (; i < n && a.n < kTensors; ++i) {
+      a.p[a.n] = probs[i];
+      a.begin[a.n + 1] = a.begin[a.n] + ceil_div(probs[i].count, kUnit);
+      ++a.n;
+    }
+    const int64_t units = a.begin[a.n];
+    const cudaError_t err = f(a, (int)(units < 1 ? 1 : units < kBlocks ? units : kBlocks));
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+size_t grad_norm_workspace_bytes(int64_t n) {
+  WsCursor cur;
+  cur.take<double>((size_t)(ceil_div(n, kTensors) * kBlocks));
+  cur.take<char>(0);
+  return cur.offset;
+}
+
+cudaError_t launch_grad_norm(int n, const sketch_grad_problem* probs, float max_norm, float* norm, float* scale,
+                             double* ws, cudaStream_t stream) {
+  int64_t partials = 0;
+  const cudaError_t err = for_batches(n, probs, [&](const GradBatch& a, int blocks) {
+    count_launch();
+    grad_norm_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, ws + partials);
+    partials += blocks;
+    return cudaGetLastError();
+  });
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, grad_norm_join_kernel, (const double*)ws, partials, max_norm, norm, scale);
+}
+
+cudaError_t launch_grad_scale(int n, const sketch_grad_problem* probs, const float* scale, cudaStream_t stream) {
+  return for_batches(n, probs, [&](const GradBatch& a, int blocks) {
+    count_launch();
+    grad_scale_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, scale);
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace rgs

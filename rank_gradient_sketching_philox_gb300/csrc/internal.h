@@ -33,6 +33,9 @@ cudaError_t make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner
 // The same map encoded anew for this call, not looked up or kept.
 cudaError_t encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                                 uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// A 2-D map of bytes in the same form, encoded anew for each call.
+cudaError_t make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
+                            uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 // Device address of the current device's error word (bits from tc.cuh).
 cudaError_t device_error_word(int** out);
 // Device address of the current device's count of weights the update kernels
@@ -302,5 +305,79 @@ struct AdamStep {
 };
 cudaError_t launch_adamw(int n, const sketch_adamw_problem* probs, bool states8, const AdamStep& h, uint64_t seed,
                          uint32_t step, cudaStream_t stream);
+
+// ---- root-mean-square norm (rms.cu) ----------------------------------------------
+struct RmsForward {
+  const void* X;  // T x k, BF16 or fp32
+  int x_type;     // sketch_dtype of X, R, S and Y
+  int64_t T, k, ld_x;
+  const void* R;  // nullable
+  int64_t ld_r;
+  void* S;        // nullable
+  int64_t ld_s;
+  const void* gamma;  // k values of w_type, nullable (ones)
+  int w_type;
+  float eps;
+  void* Y;        // nullable
+  int64_t ld_y;
+  uint8_t* Q;     // nullable, with scale (T x ceil(k / 128))
+  int64_t ld_q;
+  float* scale;
+  float* rstd;    // nullable
+};
+cudaError_t launch_rms_forward(const RmsForward& a, cudaStream_t stream);
+struct RmsBackward {
+  const void* dY;
+  const void* S;
+  int x_type;  // sketch_dtype of dY, S, dS and dX
+  int64_t T, k, ld_dy, ld_s;
+  const void* gamma;  // nullable (ones)
+  int w_type;
+  const float* rstd;
+  const void* dS;  // nullable
+  int64_t ld_ds;
+  void* dX;        // nullable
+  int64_t ld_dx;
+  float* dgamma;   // nullable
+  int overwrite;
+  float* ws;
+};
+size_t rms_backward_workspace_bytes(int64_t T, int64_t k);
+cudaError_t launch_rms_backward(const RmsBackward& a, cudaStream_t stream);
+
+// ---- 8-bit matrices with block scales (quant.cu, matmul8.cu) ------------------------
+struct Quantize {
+  const void* X;  // T x k, BF16 or fp32
+  int x_type;
+  int64_t T, k, ld_x;
+  int rows;       // of X that share a scale: 1 or 128
+  uint8_t* Q;     // nullable where Qt is given
+  int64_t ld_q;
+  float* scale;   // ceil(T / rows) x ceil(k / 128)
+  uint8_t* Qt;    // nullable: k x T
+  int64_t ld_qt;
+};
+cudaError_t launch_quantize(const Quantize& a, cudaStream_t stream);
+struct MatmulBlocks {
+  const uint8_t* A;  // T x k
+  int64_t T, k, ld_a;
+  const float* a_scale;  // T x ceil(k / 128)
+  int64_t ld_as;
+  const uint8_t* B;  // N x k
+  int64_t N, ld_b;
+  const float* b_scale;  // ceil(N / 128) x ceil(k / 128)
+  int64_t bs_row, bs_col;
+  void* Y;           // T x N
+  int y_type;
+  int64_t ld_y;
+  int overwrite;     // of an fp32 Y
+};
+cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream);
+
+// ---- gradients' norm and scaling (gradnorm.cu) ---------------------------------------
+size_t grad_norm_workspace_bytes(int64_t n);
+cudaError_t launch_grad_norm(int n, const sketch_grad_problem* probs, float max_norm, float* norm, float* scale,
+                             double* ws, cudaStream_t stream);
+cudaError_t launch_grad_scale(int n, const sketch_grad_problem* probs, const float* scale, cudaStream_t stream);
 
 }  // namespace rgs

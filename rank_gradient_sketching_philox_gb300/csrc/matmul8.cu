@@ -1,0 +1,312 @@
+// Matrix product of two 8-bit matrices with block scales.
+//
+//   Y[t, n] (+)= sum over groups g of 128 columns  a_scale[t, g] b_scale[n / 128, g] P_g[t, n],
+//   P_g[t, n] = sum over the group's columns of A[t, j] B[n, j]
+//
+// A: T x k and B: N x k E4M3 codes.  The tensor cores (tcgen05, kind::f8f6f4) form a
+// group's P_g in TMEM from 128-byte rows that TMA brings in, one K = 32 slice after
+// another; each group's result is read back, multiplied by its scales and added up in
+// fp32 registers, groups in their order.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "internal.h"
+#include "rows.cuh"
+#include "tc.cuh"
+
+namespace rgs {
+namespace {
+
+constexpr int kChunk = 128;            // a group of columns: one 128-byte swizzle row
+constexpr uint32_t kRowsBytes = 128 * kChunk;  // 128 rows of a group
+
+struct Product8 {
+  CUtensorMap tmA, tmB;
+  const float* a_scale;
+  int64_t ld_as;
+  const float* b_scale;
+  int64_t bs_row, bs_col;
+  void* Y;
+  int64_t ld_y;
+  int y_type, overwrite;
+  int T, N, chunks;
+  int stages, n_tiles;
+  int* err;
+};
+
+// Four values of a row of Y from column `col` on, as far as N goes.
+__device__ __forceinline__ void put4(const Product8& a, int64_t row, int col, float4 v) {
+  if (a.y_type == SKETCH_BF16) {
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.Y) + row * a.ld_y + col;
+    if (col + 4 <= a.N) {
+      const __nv_bfloat162 lo = __floats2bfloat162_rn(v.x, v.y), hi = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(y) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+      return;
+    }
+    const float f[4] = {v.x, v.y, v.z, v.w};
+    for (int i = 0; i < 4 && col + i < a.N; ++i) y[i] = __float2bfloat16_rn(f[i]);
+    return;
+  }
+  float* y = static_cast<float*>(a.Y) + row * a.ld_y + col;
+  if (col + 4 <= a.N) {
+    if (!a.overwrite) {
+      const float4 o = *reinterpret_cast<const float4*>(y);
+      v = make_float4(o.x + v.x, o.y + v.y, o.z + v.z, o.w + v.w);
+    }
+    *reinterpret_cast<float4*>(y) = v;
+    return;
+  }
+  const float f[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 4 && col + i < a.N; ++i) y[i] = a.overwrite ? f[i] : y[i] + f[i];
+}
+
+// ---- few tokens --------------------------------------------------------------------
+// B's rows are the MMA's M (128 of them), TN tokens its N.  A cluster of S CTAs splits
+// the groups of a tile and joins its parts through distributed shared memory, each CTA
+// a share of the tokens, in the CTAs' order.
+constexpr int kFewThreads = 192;  // copies, MMAs, four warps of sums
+constexpr int kFewStages = 12;    // at most
+constexpr int few_buffers(int TN) { return TN >= 128 ? 2 : TN >= 64 ? 4 : 8; }
+constexpr int few_columns(int TN) { return TN * few_buffers(TN) < 32 ? 32 : TN * few_buffers(TN); }
+
+template <int TN>
+__global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __grid_constant__ Product8 a) {
+  constexpr int kBuffers = few_buffers(TN);
+  constexpr uint32_t kStageBytes = kRowsBytes + TN * kChunk;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full_bar[kFewStages], empty_bar[kFewStages];
+  __shared__ __align__(8) uint64_t tfull_bar[kBuffers], tempty_bar[kBuffers];
+  __shared__ __align__(16) float factor[4][2][TN];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile int issued, consumed;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t S, rank;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
+  rank = tc::cluster_ctarank();
+  const int tile = (int)(blockIdx.x / S);
+  const int n0 = tile % a.n_tiles * 128, t0 = tile / a.n_tiles * TN;
+  const int c0 = (int)((int64_t)a.chunks * rank / S), n_mine = (int)((int64_t)a.chunks * (rank + 1) / S) - c0;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    issued = 0;
+    consumed = 0;
+    for (int s = 0; s < a.stages; ++s) {
+      tc::mbar_init(&full_bar[s], 1);
+      tc::mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < kBuffers; ++b) {
+      tc::mbar_init(&tfull_bar[b], 1);
+      tc::mbar_init(&tempty_bar[b], 4);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc(&tmem_slot, few_columns(TN));
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  Pair acc[TN / 2];
+#pragma unroll
+  for (int i = 0; i < TN / 2; ++i) acc[i] = 0;
+
+  if (warp == 0 && lane == 0) {
+    // ---- copies ----
+    int s = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < n_mine; ++i) {
+      if (i >= a.stages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
+      uint8_t* st = smem + (size_t)s * kStageBytes;
+      tc::mbar_arrive_expect_tx(&full_bar[s], kStageBytes);
+      tc::tma_load_2d(st, &a.tmB, &full_bar[s], (c0 + i) * kChunk, n0);
+      tc::tma_load_2d(st + kRowsBytes, &a.tmA, &full_bar[s], (c0 + i) * kChunk, t0);
+      issued = i + 1;
+      if (++s == a.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+  } else if (warp == 1 && lane == 0) {
+    // ---- MMAs: a group to an accumulator ----
+    constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
+    int s = 0, b = 0;
+    uint32_t ph = 0, bph = 0;
+    for (int i = 0; i < n_mine; ++i) {
+      if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
+      if (i >= kBuffers && !tc::mbar_wait(&tempty_bar[b], bph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
+      tc::tc_fence_after();
+      const uint32_t sa = tc::smem_u32(smem + (size_t)s * kStageBytes);
+#pragma unroll
+      for (int kk = 0; kk < kChunk / 32; ++kk)
+        tc::mma_e4m3(tmem + (uint32_t)(b * TN), tc::sdesc_sw128(sa + kk * 32, 16, 1024),
+                     tc::sdesc_sw128(sa + kRowsBytes + kk * 32, 16, 1024), idesc, kk > 0);
+      tc::mma_commit(&empty_bar[s]);
+      tc::mma_commit(&tfull_bar[b]);
+      consumed = i + 1;
+      if (++s == a.stages) {
+        s = 0;
+        ph ^= 1u;
+      }
+      if (++b == kBuffers) {
+        b = 0;
+        bph ^= 1u;
+      }
+    }
+  } else if (warp >= 2) {
+    // ---- sums: a row of B to a thread ----
+    const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
+    float(*f)[TN] = factor[quarter];
+    const uint32_t f0 = tc::smem_u32(f);
+    constexpr int kMine = (TN + 31) / 32;
+    const float* as[kMine];
+    float next[kMine];
+    float next_b = 0.f;
+    const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int t = t0 + i * 32 + lane;
+      as[i] = (TN >= 32 || lane < TN) && t < a.T ? a.a_scale + t * a.ld_as : nullptr;
+    }
+    auto load = [&](int c) {
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) next[i] = as[i] ? as[i][c] : 0.f;
+      next_b = bs[c * a.bs_col];
+    };
+    if (n_mine > 0) load(c0);
+    int b = 0;
+    uint32_t bph = 0;
+    for (int i = 0; i < n_mine; ++i) {
+#pragma unroll
+      for (int j = 0; j < kMine; ++j)
+        if (TN >= 32 || lane < TN) f[i & 1][j * 32 + lane] = next[j] * next_b;
+      __syncwarp();
+      if (i + 1 < n_mine) load(c0 + i + 1);
+      const bool live = tc::mbar_wait(&tfull_bar[b], bph, &abort_flag, a.err, tc::kErrTimeoutMma);
+      if (!__all_sync(0xFFFFFFFFu, live)) break;
+      tc::tc_fence_after();
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * TN);
+      constexpr int kCols = TN < 32 ? TN : 32;
+#pragma unroll
+      for (int cg = 0; cg < TN / kCols; ++cg) {
+        uint32_t v[kCols];
+        tc::tmem_ld_32x32b<kCols>(at + cg * kCols, v);
+        tc::tmem_wait_ld_regs(v);
+#pragma unroll
+        for (int q = 0; q < kCols / 4; ++q) {
+          const uint4 w = tc::lds128(f0 + (uint32_t)(((i & 1) * TN + cg * kCols + 4 * q) * 4));
+          Pair* p = acc + (cg * kCols + 4 * q) / 2;
+          p[0] = fma2(pair(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])),
+                      pair(__uint_as_float(w.x), __uint_as_float(w.y)), p[0]);
+          p[1] = fma2(pair(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])),
+                      pair(__uint_as_float(w.z), __uint_as_float(w.w)), p[1]);
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&tempty_bar[b]);
+      if (++b == kBuffers) {
+        b = 0;
+        bph ^= 1u;
+      }
+    }
+  }
+  __syncwarp();
+  // ---- the parts' sum; the MMAs that read the stages are done once the sums' warps get here ----
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);  // [token][row of B]
+  if (warp >= 2) {
+    const int q = (warp & 3) * 32 + lane;
+#pragma unroll
+    for (int i = 0; i < TN / 2; ++i) {
+      const float2 v = split(acc[i]);
+      red[(2 * i) * 128 + q] = v.x;
+      red[(2 * i + 1) * 128 + q] = v.y;
+    }
+  }
+  if (S > 1) tc::cluster_sync();
+  else __syncthreads();
+  const int share = TN / (int)S;
+  const uint32_t red0 = tc::smem_u32(red);
+  for (int e = threadIdx.x; e < share * 32; e += kFewThreads) {
+    const int t = (int)rank * share + (e >> 5), n = (e & 31) * 4;
+    if (t0 + t >= a.T || n0 + n >= a.N) continue;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint32_t off = red0 + (uint32_t)(t * 128 + n) * 4;
+    for (uint32_t r = 0; r < S; ++r) {
+      const float4 v = tc::ld_dsmem_f4(tc::mapa_shared(off, r));
+      sum = make_float4(sum.x + v.x, sum.y + v.y, sum.z + v.z, sum.w + v.w);
+    }
+    if (!abort_flag) put4(a, t0 + t, n0 + n, sum);
+  }
+  // ---- on a timeout, give copies still in flight a bounded chance to land ----
+  if (threadIdx.x == 0 && abort_flag) {
+    volatile int dummy = 0;
+    for (int i = consumed; i < issued; ++i)
+      tc::mbar_wait(&full_bar[i % a.stages], (i / a.stages) & 1, &dummy, nullptr, 0, 100000000ull);
+  }
+  __syncthreads();
+  if (S > 1) tc::cluster_sync();  // no CTA leaves while its part may still be read
+  if (warp == 0) tc::tmem_dealloc(tmem, few_columns(TN));
+}
+
+template <int TN>
+cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) {
+  constexpr uint32_t kStageBytes = kRowsBytes + TN * kChunk;
+  cudaError_t err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, TN);
+  if (err == cudaSuccess)
+    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 128);
+  if (err != cudaSuccess) return err;
+  p.n_tiles = (int)ceil_div(a.N, 128);
+  const int64_t tiles = (int64_t)p.n_tiles * ceil_div(a.T, TN);
+  unsigned S = 1;
+  while (S < 8 && tiles * S < num_sms() && 2 * S <= (unsigned)p.chunks) S *= 2;
+  p.stages = (int)((200u << 10) / kStageBytes);
+  if (p.stages > kFewStages) p.stages = kFewStages;
+  const size_t smem = (size_t)p.stages * kStageBytes + 1024;
+  err = allow_smem(matmul8_few_kernel<TN>, smem);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
+  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = S;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, matmul8_few_kernel<TN>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
+  Product8 p = {};
+  cudaError_t err = device_error_word(&p.err);
+  if (err != cudaSuccess) return err;
+  p.a_scale = a.a_scale;
+  p.ld_as = a.ld_as;
+  p.b_scale = a.b_scale;
+  p.bs_row = a.bs_row;
+  p.bs_col = a.bs_col;
+  p.Y = a.Y;
+  p.ld_y = a.ld_y;
+  p.y_type = a.y_type;
+  p.overwrite = a.overwrite;
+  p.T = (int)a.T;
+  p.N = (int)a.N;
+  p.chunks = (int)ceil_div(a.k, kChunk);
+  if (a.T <= 16) return launch_few<16>(p, a, stream);
+  if (a.T <= 32) return launch_few<32>(p, a, stream);
+  if (a.T <= 64) return launch_few<64>(p, a, stream);
+  return launch_few<128>(p, a, stream);
+}
+
+}  // namespace rgs

@@ -1,5 +1,6 @@
 """AdamW for the tensors that are not sketched: norm weights, biases,
-embeddings, a dense head.
+embeddings, a dense head; and clipping by the global norm of any gradients or
+sketches.
 
 The optimizer is bound to its tensors and their gradient buffers once and keeps
 their states, in 32 bits or in 8; a step is one call of the library for all of
@@ -61,3 +62,35 @@ class AdamW:
         gradients, or None."""
         binding.adamw_batched(self._problems, lr, self.betas, self.eps, self.weight_decay, self.seed, step,
                               grad_scale, self._device, stream)
+
+
+class GradClip:
+    """Clipping of the gradients (or sketches) ``grads`` by their global norm.
+
+    ``step()`` writes ``norm`` = sqrt(sum of squares over all tensors) and ``scale`` =
+    1 where norm <= max_norm, else max_norm / norm, one-element fp32 tensors that
+    the host does not wait for: ``AdamW.step(..., grad_scale=clip.scale)``.  With
+    ``outs`` (tensors of the same sizes and types, or the gradients themselves) it
+    also writes the scaled gradients there.  The object is bound to its tensors
+    and keeps the call's workspace, so its steps are ordered on one stream.
+    """
+
+    def __init__(self, grads, max_norm, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        self.max_norm = float(max_norm)
+        if not 0.0 < self.max_norm < float("inf"):
+            raise ValueError("max_norm must be finite and > 0, got %r" % (max_norm,))
+        self._problems = binding.grad_problems(self.grads, self.outs)
+        dev = self.grads[0].device
+        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
+        self.scale = torch.ones(1, dtype=torch.float32, device=dev)
+        self._ws = torch.empty(binding.workspace_bytes(binding.OP_GRAD_NORM, len(self.grads)), dtype=torch.uint8,
+                               device=dev)
+
+    def step(self, stream=None):
+        """Measure the gradients, and scale them where there are ``outs``; returns the scale."""
+        binding.grad_norm_batched(self._problems, self.norm, self.scale, self.max_norm, ws=self._ws, stream=stream)
+        if self.outs is not None:
+            binding.grad_scale_batched(self._problems, self.scale, stream=stream)
+        return self.scale
