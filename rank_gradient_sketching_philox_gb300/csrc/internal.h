@@ -36,6 +36,9 @@ cudaError_t encode_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t inn
 // A 2-D map of bytes in the same form, encoded anew for each call.
 cudaError_t make_tmap_u8_2d(CUtensorMap* map, const void* base, uint64_t inner, uint64_t outer,
                             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
+// A map of BF16 or fp32 values (sketch_dtype), 64-byte swizzle, to store tiles with.
+cudaError_t make_tmap_out_2d(CUtensorMap* map, int type, const void* base, uint64_t inner, uint64_t outer,
+                             uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 // Device address of the current device's error word (bits from tc.cuh).
 cudaError_t device_error_word(int** out);
 // Device address of the current device's count of weights the update kernels

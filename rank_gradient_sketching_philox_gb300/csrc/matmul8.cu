@@ -9,6 +9,8 @@
 // fp32 registers, groups in their order.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
@@ -21,7 +23,7 @@ constexpr int kChunk = 128;            // a group of columns: one 128-byte swizz
 constexpr uint32_t kRowsBytes = 128 * kChunk;  // 128 rows of a group
 
 struct Product8 {
-  CUtensorMap tmA, tmB;
+  CUtensorMap tmA, tmB, tmY;
   const float* a_scale;
   int64_t ld_as;
   const float* b_scale;
@@ -30,7 +32,7 @@ struct Product8 {
   int64_t ld_y;
   int y_type, overwrite;
   int T, N, chunks;
-  int stages, n_tiles;
+  int stages, m_tiles, n_tiles;
   int* err;
 };
 
@@ -285,6 +287,335 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
   return cudaLaunchKernelEx(&cfg, matmul8_few_kernel<TN>, p);
 }
 
+// ---- many tokens -------------------------------------------------------------------
+// Pairs of CTAs (cta_group::2) on 256 x 256 tiles, persistent.  A group's MMAs fill one
+// of two accumulators in TMEM (all 512 columns) while 16 warps of each CTA add the other
+// one, times its scales, to the tile's sums in registers: 64 columns of a row to a
+// thread.
+constexpr int kTile = 256;
+constexpr int kTileStages = 5;
+constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
+constexpr int kSumWarps = 16;
+constexpr int kTileThreads = 64 + 32 * kSumWarps + 32;  // copies, MMAs, sums, scales
+constexpr int kSumCols = 64;                          // of a thread
+constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
+constexpr int kScaleSlots = 8;                        // groups whose scales lie in shared memory
+constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxBytes + 1024;
+constexpr int kGroupM = 16;                           // tile rows walked together
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+    matmul8_tile_kernel(const __grid_constant__ Product8 a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ __align__(8) uint64_t full_bar[kTileStages];   // the even CTA's: both CTAs' rows have landed
+  __shared__ __align__(8) uint64_t empty_bar[kTileStages];  // each CTA's: the stage may be refilled
+  __shared__ __align__(8) uint64_t tfull_bar[2];            // each CTA's: a group is complete
+  __shared__ __align__(8) uint64_t tempty_bar[2];           // the even CTA's: both CTAs have read it
+  __shared__ __align__(8) uint64_t scale_bar[kScaleSlots];  // each CTA's: a group's scales are there
+  __shared__ __align__(8) uint64_t read_bar[kScaleSlots];   // each CTA's: its sums' warps have read them
+  __shared__ float a_scales[kScaleSlots][128], b_scales[kScaleSlots][2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile int issued, consumed;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = tc::cluster_ctarank();
+  const int n_pairs = (int)gridDim.x >> 1, items = a.m_tiles * a.n_tiles;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    issued = 0;
+    consumed = 0;
+    for (int s = 0; s < kTileStages; ++s) {
+      tc::mbar_init(&full_bar[s], 1);
+      tc::mbar_init(&empty_bar[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&tfull_bar[b], 1);
+      tc::mbar_init(&tempty_bar[b], 2 * kSumWarps);
+    }
+    for (int i = 0; i < kScaleSlots; ++i) {
+      tc::mbar_init(&scale_bar[i], 1);
+      tc::mbar_init(&read_bar[i], kSumWarps);
+    }
+    tc::fence_mbar_init();
+  }
+  if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::cluster_sync();  // both CTAs' barriers exist before either signals one
+  tc::tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  // first row and column of a tile
+  auto place = [&](int item, int& m0, int& n0) {
+    const int per_group = kGroupM * a.n_tiles, g = item / per_group, rem = item - g * per_group;
+    const int left = a.m_tiles - g * kGroupM, gm = left < kGroupM ? left : kGroupM;
+    const int n = rem / gm;
+    n0 = n * kTile;
+    m0 = (g * kGroupM + rem - n * gm) * kTile;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // ---- copies: this CTA's half of each operand's rows ----
+    const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
+    const uint32_t empty0 = tc::smem_u32(empty_bar), stage0 = tc::smem_u32(smem);
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    bool stop = false;
+    for (int item = (int)blockIdx.x >> 1; item < items && !stop; item += n_pairs) {
+      int m0, n0;
+      place(item, m0, n0);
+      const int ar = m0 + 128 * (int)rank, br = n0 + 128 * (int)rank;
+      for (int c = 0; c < a.chunks; ++c, ++it) {
+        if (it >= kTileStages && !tc::mbar_wait(empty0 + 8u * s, ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
+          stop = true;
+          break;
+        }
+        const uint32_t st = stage0 + (uint32_t)s * kTileStageBytes, bar = full0 + 8u * s;
+        if (rank == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(full_bar) + 8u * s, 2 * kTileStageBytes);
+        tc::tma_load_2d_pair(st, &a.tmA, bar, c * kChunk, ar);
+        tc::tma_load_2d_pair(st + kRowsBytes, &a.tmB, bar, c * kChunk, br);
+        if (++s == kTileStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    issued = it;
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // ---- MMAs, for both CTAs ----
+    constexpr uint32_t idesc = tc::idesc_e4m3(kTile, kTile);
+    const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
+    const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kRowsBytes, 16, 1024);
+    const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32);
+    const uint32_t full0 = tc::smem_u32(full_bar), tempty0 = tc::smem_u32(tempty_bar);
+    int total = 0;
+    for (int item = (int)blockIdx.x >> 1; item < items; item += n_pairs) total += a.chunks;
+    int s = 0, it = 0;
+    uint32_t ph = 0;
+    for (; it < total; ++it) {
+      const int b = it & 1;
+      if (it >= 2 && !tc::mbar_wait<true>(tempty0 + 8u * b, ((it >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
+        break;
+      if (!tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
+      tc::tc_fence_after();
+      const uint32_t al = (uint32_t)ad0 + (uint32_t)s * (kTileStageBytes >> 4);
+      const uint32_t bl = (uint32_t)bd0 + (uint32_t)s * (kTileStageBytes >> 4);
+#pragma unroll
+      for (int kk = 0; kk < kChunk / 32; ++kk)
+        tc::mma_e4m3_pair(tmem + (uint32_t)(b * kTile), al + kk * 2, a_hi, bl + kk * 2, b_hi, idesc, kk > 0);
+      tc::mma_commit_pair(&tfull_bar[b]);
+      tc::mma_commit_pair(&empty_bar[s]);
+      if (++s == kTileStages) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    consumed = it;
+  } else if (warp == 2 + kSumWarps) {
+    // ---- scales: of the CTA's 128 rows and of the tile's two column blocks ----
+    int it = 0;
+    bool live = true;
+    for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
+      int m0, n0;
+      place(item, m0, n0);
+      const float* as[4];
+      const int row = m0 + 128 * (int)rank + lane;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as : nullptr;
+      const int col = n0 + (lane & 1) * kScaleBlock;
+      const float* bs = lane < 2 && col < a.N ? a.b_scale + (int64_t)(col / kScaleBlock) * a.bs_row : nullptr;
+      constexpr int kAhead = 4;  // groups read before they are written
+      float sa[kAhead][4], sb[kAhead];
+      auto load = [&](int c, float(&va)[4], float& vb) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) va[i] = as[i] && c < a.chunks ? as[i][c] : 0.f;
+        vb = bs && c < a.chunks ? bs[c * a.bs_col] : 0.f;
+      };
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) load(j, sa[j], sb[j]);
+      for (int c0 = 0; c0 < a.chunks && live; c0 += kAhead) {
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          if (c0 + j < a.chunks && live) {
+            const int slot = it % kScaleSlots;
+            if (it >= kScaleSlots)
+              live = tc::mbar_wait(&read_bar[slot], (it / kScaleSlots - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
+            live = __all_sync(0xFFFFFFFFu, live);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a_scales[slot][32 * i + lane] = sa[j][i];
+            if (lane < 2) b_scales[slot][lane] = sb[j];
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&scale_bar[slot]);
+            load(c0 + j + kAhead, sa[j], sb[j]);
+            ++it;
+          }
+        }
+      }
+    }
+  } else if (warp >= 2) {
+    // ---- sums: 64 columns of a row to a thread ----
+    const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
+    const int col = ((warp - 2) >> 2) * kSumCols;
+    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
+    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0), tfull0 = tc::smem_u32(tfull_bar);
+    const uint32_t scale0 = tc::smem_u32(scale_bar);
+    const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 2) * kBoxBytes;
+    const uint32_t sa0 = tc::smem_u32(a_scales) + (uint32_t)(quarter * 32 + lane) * 4u;
+    const uint32_t sb0 = tc::smem_u32(b_scales) + (col >= kScaleBlock ? 4u : 0u);
+    int it = 0;
+    bool live = true;
+    for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
+      int m0, n0;
+      place(item, m0, n0);
+      const int row0 = m0 + 128 * (int)rank + quarter * 32, col0 = n0 + col;
+      Pair acc[kSumCols / 2];
+#pragma unroll
+      for (int i = 0; i < kSumCols / 2; ++i) acc[i] = 0;
+      for (int c = 0; c < a.chunks; ++c, ++it) {
+        const uint32_t b = it & 1, slot = it % kScaleSlots;
+        live = tc::mbar_wait(scale0 + 8u * slot, (it / kScaleSlots) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
+        const float f = tc::lds_f32(sa0 + slot * 512u) * tc::lds_f32(sb0 + slot * 8u);
+        const Pair f2 = pair(f, f);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
+        live = tc::mbar_wait(tfull0 + 8u * b, (it >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
+        live = __all_sync(0xFFFFFFFFu, live);
+        if (!live) break;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int h = 0; h < kSumCols / 16; ++h) {
+          uint32_t v[16];
+          tc::tmem_ld_32x32b_x16(at + b * kTile + h * 16, v);
+          tc::tmem_wait_ld_regs(v);
+          if (h == kSumCols / 16 - 1) {  // the accumulator is read
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive_pair(tempty0 + 8u * b);
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[h * 8 + i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, acc[h * 8 + i]);
+        }
+      }
+      if (!live) break;
+      // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle
+      const bool fp32 = a.y_type == SKETCH_FP32;
+      const uint32_t mine = box + (uint32_t)lane * 64u, swizzle = (uint32_t)(lane >> 1) & 3u;
+      auto send = [&](int c, const uint4(&w)[4]) {
+        if (lane == 0) tc::bulk_wait_read<0>();  // the box's last copy has left
+        __syncwarp();
+#pragma unroll
+        for (uint32_t j = 0; j < 4; ++j) tc::sts128(mine + ((j ^ swizzle) << 4), w[j]);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < a.T && c < a.N) {
+          if (fp32 && !a.overwrite) tc::tma_add_2d(&a.tmY, box, c, row0);
+          else tc::tma_store_2d_at(&a.tmY, box, c, row0);
+          tc::bulk_commit();
+        }
+      };
+      uint4 w[4];
+      if (!fp32) {
+#pragma unroll
+        for (int h = 0; h < kSumCols / 32; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 v = split(acc[16 * h + 4 * j + i]);
+              const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+              r[i] = *reinterpret_cast<const uint32_t*>(&p);
+            }
+            w[j] = make_uint4(r[0], r[1], r[2], r[3]);
+          }
+          send(col0 + 32 * h, w);
+        }
+      } else {
+#pragma unroll
+        for (int h = 0; h < kSumCols / 16; ++h) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 lo = split(acc[8 * h + 2 * j]), hi = split(acc[8 * h + 2 * j + 1]);
+            w[j] = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
+          }
+          send(col0 + 16 * h, w);
+        }
+      }
+    }
+    if (lane == 0) tc::bulk_wait_all();
+  }
+  __syncwarp();
+  // ---- on a timeout, give copies still in flight a bounded chance to land ----
+  tc::tc_fence_before();
+  __syncthreads();
+  if (threadIdx.x == 0 && abort_flag) {
+    volatile int dummy = 0;
+    if (rank == 0) {
+      for (int i = consumed; i < issued; ++i)
+        tc::mbar_wait(&full_bar[i % kTileStages], (i / kTileStages) & 1, &dummy, nullptr, 0, 100000000ull);
+    } else {
+      const uint64_t t0 = tc::globaltimer();
+      while (tc::globaltimer() - t0 < 100000000ull) {
+      }
+    }
+  }
+  __syncthreads();
+  tc::cluster_sync();  // neither CTA leaves while the other may still signal it
+  if (warp == 0) tc::tmem_dealloc_pair(tmem, 512);
+}
+
+// CTA pairs that the device holds at once (its SMs need not all pair up).
+cudaError_t tile_pairs(int* out) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<int> pairs[kMaxDevices];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  if (pairs[dev] == 0) {
+    err = cudaFuncSetAttribute(matmul8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)num_sms(), 1, 1);
+    cfg.blockDim = dim3(kTileThreads, 1, 1);
+    cfg.dynamicSmemBytes = kTileSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    err = cudaOccupancyMaxActiveClusters(&n, matmul8_tile_kernel, &cfg);
+    if (err != cudaSuccess) return err;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    pairs[dev] = n;
+  }
+  *out = pairs[dev];
+  return cudaSuccess;
+}
+
+cudaError_t launch_tiles(Product8& p, const MatmulBlocks& a, cudaStream_t stream) {
+  int pairs = 0;
+  cudaError_t err = tile_pairs(&pairs);
+  if (err == cudaSuccess)
+    err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
+  if (err == cudaSuccess)
+    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 128);
+  const uint32_t size = a.y_type == SKETCH_BF16 ? 2 : 4;
+  if (err == cudaSuccess)
+    err = make_tmap_out_2d(&p.tmY, a.y_type, a.Y, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)a.ld_y * size, 64 / size, 32);
+  if (err != cudaSuccess) return err;
+  p.m_tiles = (int)ceil_div(a.T, kTile);
+  p.n_tiles = (int)ceil_div(a.N, kTile);
+  const int items = p.m_tiles * p.n_tiles;
+  count_launch();
+  matmul8_tile_kernel<<<2 * (unsigned)(items < pairs ? items : pairs), kTileThreads, kTileSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
@@ -303,6 +634,8 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   p.T = (int)a.T;
   p.N = (int)a.N;
   p.chunks = (int)ceil_div(a.k, kChunk);
+  // few tokens, or too few tiles of 256 x 256 for the pairs of CTAs
+  if (a.T > 128 && ceil_div(a.T, kTile) * ceil_div(a.N, kTile) * 4 >= num_sms()) return launch_tiles(p, a, stream);
   if (a.T <= 16) return launch_few<16>(p, a, stream);
   if (a.T <= 32) return launch_few<32>(p, a, stream);
   if (a.T <= 64) return launch_few<64>(p, a, stream);
