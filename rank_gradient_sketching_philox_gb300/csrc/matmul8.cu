@@ -296,10 +296,11 @@ constexpr int kTile = 256;
 constexpr int kTileStages = 5;
 constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
 constexpr int kSumWarps = 16;
-constexpr int kTileThreads = 64 + 32 * kSumWarps + 32;  // copies, MMAs, sums, scales
+constexpr int kTileThreads = 128 + 32 * kSumWarps;    // copies, MMAs, scales, an idle warp; sums
 constexpr int kSumCols = 64;                          // of a thread
+constexpr int kLoadCols = 16;                         // of a load from TMEM
 constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
-constexpr int kScaleSlots = 8;                        // groups whose scales lie in shared memory
+constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
 constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxBytes + 1024;
 constexpr int kGroupM = 16;                           // tile rows walked together
 
@@ -311,9 +312,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __shared__ __align__(8) uint64_t empty_bar[kTileStages];  // each CTA's: the stage may be refilled
   __shared__ __align__(8) uint64_t tfull_bar[2];            // each CTA's: a group is complete
   __shared__ __align__(8) uint64_t tempty_bar[2];           // the even CTA's: both CTAs have read it
-  __shared__ __align__(8) uint64_t scale_bar[kScaleSlots];  // each CTA's: a group's scales are there
-  __shared__ __align__(8) uint64_t read_bar[kScaleSlots];   // each CTA's: its sums' warps have read them
-  __shared__ float a_scales[kScaleSlots][128], b_scales[kScaleSlots][2];
+  __shared__ __align__(8) uint64_t scale_bar[2];  // each CTA's: the scales of some groups are there
+  __shared__ __align__(8) uint64_t read_bar[2];   // each CTA's: its sums' warps have read them
+  __shared__ float a_scales[2][kScaleGroups][128], b_scales[2][kScaleGroups][2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int issued, consumed;
@@ -332,10 +333,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&tfull_bar[b], 1);
       tc::mbar_init(&tempty_bar[b], 2 * kSumWarps);
-    }
-    for (int i = 0; i < kScaleSlots; ++i) {
-      tc::mbar_init(&scale_bar[i], 1);
-      tc::mbar_init(&read_bar[i], kSumWarps);
+      tc::mbar_init(&scale_bar[b], 1);
+      tc::mbar_init(&read_bar[b], kSumWarps);
     }
     tc::fence_mbar_init();
   }
@@ -411,9 +410,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       }
     }
     consumed = it;
-  } else if (warp == 2 + kSumWarps) {
+  } else if (warp == 2) {
     // ---- scales: of the CTA's 128 rows and of the tile's two column blocks ----
-    int it = 0;
+    int batch = 0;
     bool live = true;
     for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
       int m0, n0;
@@ -424,45 +423,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as : nullptr;
       const int col = n0 + (lane & 1) * kScaleBlock;
       const float* bs = lane < 2 && col < a.N ? a.b_scale + (int64_t)(col / kScaleBlock) * a.bs_row : nullptr;
-      constexpr int kAhead = 4;  // groups read before they are written
-      float sa[kAhead][4], sb[kAhead];
-      auto load = [&](int c, float(&va)[4], float& vb) {
+      for (int c0 = 0; c0 < a.chunks && live; c0 += kScaleGroups, ++batch) {
+        const int slot = batch & 1;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) va[i] = as[i] && c < a.chunks ? as[i][c] : 0.f;
-        vb = bs && c < a.chunks ? bs[c * a.bs_col] : 0.f;
-      };
+        for (int half = 0; half < kScaleGroups; half += kScaleGroups / 2) {
+          float sa[kScaleGroups / 2][4], sb[kScaleGroups / 2];
 #pragma unroll
-      for (int j = 0; j < kAhead; ++j) load(j, sa[j], sb[j]);
-      for (int c0 = 0; c0 < a.chunks && live; c0 += kAhead) {
+          for (int j = 0; j < kScaleGroups / 2; ++j) {
+            const int c = c0 + half + j;
 #pragma unroll
-        for (int j = 0; j < kAhead; ++j) {
-          if (c0 + j < a.chunks && live) {
-            const int slot = it % kScaleSlots;
-            if (it >= kScaleSlots)
-              live = tc::mbar_wait(&read_bar[slot], (it / kScaleSlots - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
-            live = __all_sync(0xFFFFFFFFu, live);
+            for (int i = 0; i < 4; ++i) sa[j][i] = as[i] && c < a.chunks ? as[i][c] : 0.f;
+            sb[j] = bs && c < a.chunks ? bs[c * a.bs_col] : 0.f;
+          }
+          if (half == 0 && batch >= 2)
+            live = tc::mbar_wait(&read_bar[slot], ((batch >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
+          live = __all_sync(0xFFFFFFFFu, live);
+          if (!live) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a_scales[slot][32 * i + lane] = sa[j][i];
-            if (lane < 2) b_scales[slot][lane] = sb[j];
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(&scale_bar[slot]);
-            load(c0 + j + kAhead, sa[j], sb[j]);
-            ++it;
+          for (int j = 0; j < kScaleGroups / 2; ++j) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a_scales[slot][half + j][32 * i + lane] = sa[j][i];
+            if (lane < 2) b_scales[slot][half + j][lane] = sb[j];
           }
         }
+        if (!live) break;
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&scale_bar[slot]);
       }
     }
-  } else if (warp >= 2) {
+  } else if (warp >= 4) {
     // ---- sums: 64 columns of a row to a thread ----
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
-    const int col = ((warp - 2) >> 2) * kSumCols;
+    const int col = ((warp - 4) >> 2) * kSumCols;
     const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
     const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0), tfull0 = tc::smem_u32(tfull_bar);
-    const uint32_t scale0 = tc::smem_u32(scale_bar);
-    const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 2) * kBoxBytes;
+    const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * kBoxBytes;
     const uint32_t sa0 = tc::smem_u32(a_scales) + (uint32_t)(quarter * 32 + lane) * 4u;
     const uint32_t sb0 = tc::smem_u32(b_scales) + (col >= kScaleBlock ? 4u : 0u);
-    int it = 0;
+    int it = 0, batch = 0;
     bool live = true;
     for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
       int m0, n0;
@@ -472,29 +470,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int i = 0; i < kSumCols / 2; ++i) acc[i] = 0;
       for (int c = 0; c < a.chunks; ++c, ++it) {
-        const uint32_t b = it & 1, slot = it % kScaleSlots;
-        live = tc::mbar_wait(scale0 + 8u * slot, (it / kScaleSlots) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
-        const float f = tc::lds_f32(sa0 + slot * 512u) * tc::lds_f32(sb0 + slot * 8u);
+        const uint32_t b = it & 1, slot = batch & 1, in_batch = c % kScaleGroups;
+        if (in_batch == 0) live = tc::mbar_wait(&scale_bar[slot], (batch >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
+        const uint32_t s = slot * kScaleGroups + in_batch;
+        const float f = tc::lds_f32(sa0 + s * 512u) * tc::lds_f32(sb0 + s * 8u);
         const Pair f2 = pair(f, f);
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
+        if (in_batch == kScaleGroups - 1 || c + 1 == a.chunks) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
+          ++batch;
+        }
         live = tc::mbar_wait(tfull0 + 8u * b, (it >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
         live = __all_sync(0xFFFFFFFFu, live);
         if (!live) break;
         tc::tc_fence_after();
 #pragma unroll
-        for (int h = 0; h < kSumCols / 16; ++h) {
-          uint32_t v[16];
-          tc::tmem_ld_32x32b_x16(at + b * kTile + h * 16, v);
+        for (int h = 0; h < kSumCols / kLoadCols; ++h) {
+          uint32_t v[kLoadCols];
+          tc::tmem_ld_32x32b<kLoadCols>(at + b * kTile + h * kLoadCols, v);
           tc::tmem_wait_ld_regs(v);
-          if (h == kSumCols / 16 - 1) {  // the accumulator is read
+          if (h == kSumCols / kLoadCols - 1) {  // the accumulator is read
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0) tc::mbar_arrive_pair(tempty0 + 8u * b);
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            acc[h * 8 + i] = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, acc[h * 8 + i]);
+          for (int i = 0; i < kLoadCols / 2; ++i) {
+            Pair& s = acc[h * (kLoadCols / 2) + i];
+            s = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, s);
+          }
         }
       }
       if (!live) break;
