@@ -310,8 +310,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kTileStages];   // the even CTA's: both CTAs' rows have landed
   __shared__ __align__(8) uint64_t empty_bar[kTileStages];  // each CTA's: the stage may be refilled
-  __shared__ __align__(8) uint64_t tfull_bar[2];            // each CTA's: a group is complete
-  __shared__ __align__(8) uint64_t tempty_bar[2];           // the even CTA's: both CTAs have read it
+  __shared__ __align__(8) uint64_t tfull_bar[2];            // each CTA's: a group's products are complete
+  __shared__ __align__(8) uint64_t tempty_bar[2];           // the even CTA's: both CTAs have read them
   __shared__ __align__(8) uint64_t scale_bar[2];  // each CTA's: the scales of some groups are there
   __shared__ __align__(8) uint64_t read_bar[2];   // each CTA's: its sums' warps have read them
   __shared__ float a_scales[2][kScaleGroups][128], b_scales[2][kScaleGroups][2];
@@ -380,8 +380,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       }
     }
     issued = it;
-  } else if (warp == 1 && lane == 0 && rank == 0) {
+  } else if (warp == 1 && rank == 0) {
     // ---- MMAs, for both CTAs ----
+    // The whole warp walks, one thread issues: descriptors stay in uniform registers (a
+    // loop of one thread took 900 cycles a group beside the sums' warps, the MMAs 512).
     constexpr uint32_t idesc = tc::idesc_e4m3(kTile, kTile);
     const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
     const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kRowsBytes, 16, 1024);
@@ -392,24 +394,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     int s = 0, it = 0;
     uint32_t ph = 0;
     for (; it < total; ++it) {
-      const int b = it & 1;
-      if (it >= 2 && !tc::mbar_wait<true>(tempty0 + 8u * b, ((it >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage))
-        break;
+      const uint32_t b = it & 1;
       if (!tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
+      if (it >= 2 && !tc::mbar_wait(tempty0 + 8u * b, ((it >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
       tc::tc_fence_after();
       const uint32_t al = (uint32_t)ad0 + (uint32_t)s * (kTileStageBytes >> 4);
       const uint32_t bl = (uint32_t)bd0 + (uint32_t)s * (kTileStageBytes >> 4);
+      if (tc::elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 32; ++kk)
-        tc::mma_e4m3_pair(tmem + (uint32_t)(b * kTile), al + kk * 2, a_hi, bl + kk * 2, b_hi, idesc, kk > 0);
-      tc::mma_commit_pair(&tfull_bar[b]);
-      tc::mma_commit_pair(&empty_bar[s]);
+        for (int kk = 0; kk < kChunk / 32; ++kk)
+          tc::mma_e4m3_pair(tmem + b * kTile, al + kk * 2, a_hi, bl + kk * 2, b_hi, idesc, kk > 0);
+        tc::mma_commit_pair(&tfull_bar[b]);
+        tc::mma_commit_pair(&empty_bar[s]);
+      }
+      __syncwarp();
       if (++s == kTileStages) {
         s = 0;
         ph ^= 1u;
       }
     }
-    consumed = it;
+    if (lane == 0) consumed = it;
   } else if (warp == 2) {
     // ---- scales: of the CTA's 128 rows and of the tile's two column blocks ----
     int batch = 0;
@@ -454,13 +458,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   } else if (warp >= 4) {
     // ---- sums: 64 columns of a row to a thread ----
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
+    const uint32_t half = (uint32_t)(warp - 4) >> 3;
     const int col = ((warp - 4) >> 2) * kSumCols;
-    const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
-    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0), tfull0 = tc::smem_u32(tfull_bar);
+    const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
+    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0);
+    const uint32_t tfull0 = tc::smem_u32(tfull_bar);
     const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * kBoxBytes;
     const uint32_t sa0 = tc::smem_u32(a_scales) + (uint32_t)(quarter * 32 + lane) * 4u;
-    const uint32_t sb0 = tc::smem_u32(b_scales) + (col >= kScaleBlock ? 4u : 0u);
-    int it = 0, batch = 0;
+    const uint32_t sb0 = tc::smem_u32(b_scales) + 4u * half;
+    uint32_t b = 0, ph = 0;  // accumulator of the next group, and its barriers' parity
+    uint32_t slot = 0, slot_ph = 0;
     bool live = true;
     for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
       int m0, n0;
@@ -469,25 +476,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       Pair acc[kSumCols / 2];
 #pragma unroll
       for (int i = 0; i < kSumCols / 2; ++i) acc[i] = 0;
-      for (int c = 0; c < a.chunks; ++c, ++it) {
-        const uint32_t b = it & 1, slot = batch & 1, in_batch = c % kScaleGroups;
-        if (in_batch == 0) live = tc::mbar_wait(&scale_bar[slot], (batch >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
-        const uint32_t s = slot * kScaleGroups + in_batch;
-        const float f = tc::lds_f32(sa0 + s * 512u) * tc::lds_f32(sb0 + s * 8u);
+      // A wait that gives up makes all later ones give up too; that is looked at once in
+      // eight groups.
+      auto group = [&](uint32_t sa, uint32_t sb) {
+        const float f = tc::lds_f32(sa) * tc::lds_f32(sb);
         const Pair f2 = pair(f, f);
-        if (in_batch == kScaleGroups - 1 || c + 1 == a.chunks) {
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
-          ++batch;
-        }
-        live = tc::mbar_wait(tfull0 + 8u * b, (it >> 1) & 1, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
-        live = __all_sync(0xFFFFFFFFu, live);
-        if (!live) break;
+        live = tc::mbar_wait(tfull0 + 8u * b, ph, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
+        __syncwarp();  // the loads are the whole warp's
         tc::tc_fence_after();
+        const uint32_t at = at0 + b * kTile;
 #pragma unroll
         for (int h = 0; h < kSumCols / kLoadCols; ++h) {
           uint32_t v[kLoadCols];
-          tc::tmem_ld_32x32b<kLoadCols>(at + b * kTile + h * kLoadCols, v);
+          tc::tmem_ld_32x32b<kLoadCols>(at + h * kLoadCols, v);
           tc::tmem_wait_ld_regs(v);
           if (h == kSumCols / kLoadCols - 1) {  // the accumulator is read
             tc::tc_fence_before();
@@ -500,6 +501,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             s = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, s);
           }
         }
+        b ^= 1u;
+        ph ^= b ^ 1u;
+      };
+      for (int c = 0; c < a.chunks; c += kScaleGroups) {
+        live = tc::mbar_wait(&scale_bar[slot], slot_ph, &abort_flag, a.err, tc::kErrTimeoutStage) && live;
+        const uint32_t sa = sa0 + slot * (kScaleGroups * 512u), sb = sb0 + slot * (kScaleGroups * 8u);
+        const int n = a.chunks - c;
+#pragma unroll
+        for (uint32_t j = 0; j < kScaleGroups; ++j)
+          if ((int)j < n) group(sa + j * 512u, sb + j * 8u);
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
+        slot ^= 1u;
+        slot_ph ^= slot ^ 1u;
+        live = __all_sync(0xFFFFFFFFu, live);
+        if (!live) break;
       }
       if (!live) break;
       // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle
