@@ -288,21 +288,47 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
 }
 
 // ---- many tokens -------------------------------------------------------------------
-// Pairs of CTAs (cta_group::2) on 256 x 256 tiles, persistent.  A group's MMAs fill one
-// of two accumulators in TMEM (all 512 columns) while 16 warps of each CTA add the other
-// one, times its scales, to the tile's sums in registers: 64 columns of a row to a
-// thread.
+// Pairs of CTAs (cta_group::2) on 256 x 256 tiles, persistent.  A group's MMAs fill two
+// of four accumulators in TMEM (256 x 128 each, 512 columns in all) while eight warps of
+// each CTA add the others, times their scales, to the tile's sums in registers: 128
+// columns of a row to a thread.
 constexpr int kTile = 256;
 constexpr int kTileStages = 5;
 constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
-constexpr int kSumWarps = 16;
+constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;    // copies, MMAs, scales, an idle warp; sums
-constexpr int kSumCols = 64;                          // of a thread
-constexpr int kLoadCols = 16;                         // of a load from TMEM
+constexpr int kSumCols = 128;                         // of a thread
+constexpr int kLoads = kSumCols / 16;                 // from TMEM, of 16 columns
+// Registers: the launch has 168 for each thread, 384 * 168 = 128 * 88 + 256 * 208; with
+// fewer for the first the waits of the copies and MMAs spill (72: 312 us, 56: 355).
+constexpr int kFewRegisters = 88, kSumRegisters = 208;
 constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
 constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
 constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxBytes + 1024;
 constexpr int kGroupM = 16;                           // tile rows walked together
+
+// acc += f * (16 columns in v), while the next 16 columns come from TMEM into w.  One
+// piece, so that nothing touches w between the load and its wait.
+__device__ __forceinline__ void add_and_load(Pair (&acc)[8], const uint32_t (&v)[16], Pair f, uint32_t (&w)[16], uint32_t taddr) {
+  asm volatile(
+      "{\n\t.reg .b64 p;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%41];\n\t"
+      "mov.b64 p, {%24, %25};\n\tfma.rn.f32x2 %16, p, %40, %16;\n\t"
+      "mov.b64 p, {%26, %27};\n\tfma.rn.f32x2 %17, p, %40, %17;\n\t"
+      "mov.b64 p, {%28, %29};\n\tfma.rn.f32x2 %18, p, %40, %18;\n\t"
+      "mov.b64 p, {%30, %31};\n\tfma.rn.f32x2 %19, p, %40, %19;\n\t"
+      "mov.b64 p, {%32, %33};\n\tfma.rn.f32x2 %20, p, %40, %20;\n\t"
+      "mov.b64 p, {%34, %35};\n\tfma.rn.f32x2 %21, p, %40, %21;\n\t"
+      "mov.b64 p, {%36, %37};\n\tfma.rn.f32x2 %22, p, %40, %22;\n\t"
+      "mov.b64 p, {%38, %39};\n\tfma.rn.f32x2 %23, p, %40, %23;\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : "=&r"(w[0]), "=&r"(w[1]), "=&r"(w[2]), "=&r"(w[3]), "=&r"(w[4]), "=&r"(w[5]), "=&r"(w[6]), "=&r"(w[7]), 
+        "=&r"(w[8]), "=&r"(w[9]), "=&r"(w[10]), "=&r"(w[11]), "=&r"(w[12]), "=&r"(w[13]), "=&r"(w[14]), "=&r"(w[15]),
+        "+l"(acc[0]), "+l"(acc[1]), "+l"(acc[2]), "+l"(acc[3]), "+l"(acc[4]), "+l"(acc[5]), "+l"(acc[6]), "+l"(acc[7])
+      : "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), 
+        "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "l"(f), "r"(taddr)
+      : "memory");
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     matmul8_tile_kernel(const __grid_constant__ Product8 a) {
@@ -310,14 +336,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kTileStages];   // the even CTA's: both CTAs' rows have landed
   __shared__ __align__(8) uint64_t empty_bar[kTileStages];  // each CTA's: the stage may be refilled
-  __shared__ __align__(8) uint64_t tfull_bar[2];            // each CTA's: a group's products are complete
-  __shared__ __align__(8) uint64_t tempty_bar[2];           // the even CTA's: both CTAs have read them
+  __shared__ __align__(8) uint64_t tfull_bar[4];            // each CTA's: half a group's products are complete
+  __shared__ __align__(8) uint64_t tempty_bar[4];           // the even CTA's: both CTAs have read them
   __shared__ __align__(8) uint64_t scale_bar[2];  // each CTA's: the scales of some groups are there
   __shared__ __align__(8) uint64_t read_bar[2];   // each CTA's: its sums' warps have read them
   __shared__ float a_scales[2][kScaleGroups][128], b_scales[2][kScaleGroups][2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ volatile int issued, consumed;
+  __shared__ volatile int issued, consumed[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = tc::cluster_ctarank();
@@ -325,14 +351,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     issued = 0;
-    consumed = 0;
+    consumed[0] = consumed[1] = 0;
     for (int s = 0; s < kTileStages; ++s) {
       tc::mbar_init(&full_bar[s], 1);
       tc::mbar_init(&empty_bar[s], 1);
     }
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < 4; ++b) {
       tc::mbar_init(&tfull_bar[b], 1);
-      tc::mbar_init(&tempty_bar[b], 2 * kSumWarps);
+      tc::mbar_init(&tempty_bar[b], kSumWarps);  // half of them, of both CTAs
+    }
+    for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&scale_bar[b], 1);
       tc::mbar_init(&read_bar[b], kSumWarps);
     }
@@ -353,67 +381,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     m0 = (g * kGroupM + rem - n * gm) * kTile;
   };
 
-  if (warp == 0 && lane == 0) {
+  if (warp < 4) {
+  tc::fewer_registers<kFewRegisters>();
+  if (warp == 0) {
     // ---- copies: this CTA's half of each operand's rows ----
+    // The whole warp walks, one thread issues: what it needs stays in uniform registers,
+    // and a stage takes it less than its MMAs' 512 cycles beside the sums' warps.
     const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
-    const uint32_t empty0 = tc::smem_u32(empty_bar), stage0 = tc::smem_u32(smem);
+    const uint32_t mine0 = tc::smem_u32(full_bar), empty0 = tc::smem_u32(empty_bar), stage0 = tc::smem_u32(smem);
     int s = 0, it = 0;
     uint32_t ph = 0;
     bool stop = false;
     for (int item = (int)blockIdx.x >> 1; item < items && !stop; item += n_pairs) {
       int m0, n0;
       place(item, m0, n0);
-      const int ar = m0 + 128 * (int)rank, br = n0 + 128 * (int)rank;
+      const int ar = m0 + 128 * (int)rank, br = n0 + 64 * (int)rank;  // of each 128 columns, half from each CTA
       for (int c = 0; c < a.chunks; ++c, ++it) {
         if (it >= kTileStages && !tc::mbar_wait(empty0 + 8u * s, ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
           stop = true;
           break;
         }
         const uint32_t st = stage0 + (uint32_t)s * kTileStageBytes, bar = full0 + 8u * s;
-        if (rank == 0) tc::mbar_arrive_expect_tx(tc::smem_u32(full_bar) + 8u * s, 2 * kTileStageBytes);
-        tc::tma_load_2d_pair(st, &a.tmA, bar, c * kChunk, ar);
-        tc::tma_load_2d_pair(st + kRowsBytes, &a.tmB, bar, c * kChunk, br);
+        if (tc::elect_one()) {
+          if (rank == 0) tc::mbar_arrive_expect_tx(mine0 + 8u * s, 2 * kTileStageBytes);
+          tc::tma_load_2d_pair(st, &a.tmA, bar, c * kChunk, ar);
+          tc::tma_load_2d_pair(st + kRowsBytes, &a.tmB, bar, c * kChunk, br);
+          tc::tma_load_2d_pair(st + kRowsBytes + kRowsBytes / 2, &a.tmB, bar, c * kChunk, br + 128);
+        }
+        __syncwarp();
         if (++s == kTileStages) {
           s = 0;
           ph ^= 1u;
         }
       }
+      stop = __any_sync(0xFFFFFFFFu, stop);
     }
-    issued = it;
-  } else if (warp == 1 && rank == 0) {
-    // ---- MMAs, for both CTAs ----
-    // The whole warp walks, one thread issues: descriptors stay in uniform registers (a
-    // loop of one thread took 900 cycles a group beside the sums' warps, the MMAs 512).
-    constexpr uint32_t idesc = tc::idesc_e4m3(kTile, kTile);
+    if (lane == 0) issued = it;
+  } else if ((warp & 1) && rank == 0) {
+    // ---- MMAs, for both CTAs: warp 1 the even groups, warp 3 the odd ones ----
+    // A group's waits, MMAs and commits take a warp some 800 cycles, one after another,
+    // the MMAs 512; the accumulators are not the same, so the order does not matter.
+    constexpr uint32_t idesc = tc::idesc_e4m3(kTile, kTile / 2);
     const uint64_t ad0 = tc::sdesc_sw128(tc::smem_u32(smem), 16, 1024);
     const uint64_t bd0 = tc::sdesc_sw128(tc::smem_u32(smem) + kRowsBytes, 16, 1024);
     const uint32_t a_hi = (uint32_t)(ad0 >> 32), b_hi = (uint32_t)(bd0 >> 32);
-    const uint32_t full0 = tc::smem_u32(full_bar), tempty0 = tc::smem_u32(tempty_bar);
+    const uint32_t b0 = (uint32_t)(warp & 2);  // the first of this warp's two accumulators
+    const uint32_t full0 = tc::smem_u32(full_bar), tempty0 = tc::smem_u32(tempty_bar) + 8u * b0;
     int total = 0;
     for (int item = (int)blockIdx.x >> 1; item < items; item += n_pairs) total += a.chunks;
-    int s = 0, it = 0;
-    uint32_t ph = 0;
-    for (; it < total; ++it) {
-      const uint32_t b = it & 1;
+    int s = warp >> 1, it = warp >> 1;
+    uint32_t ph = 0, tph = 1;
+    bool live = true;
+    for (; it < total; it += 2) {
       if (!tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
-      if (it >= 2 && !tc::mbar_wait(tempty0 + 8u * b, ((it >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
-      tc::tc_fence_after();
       const uint32_t al = (uint32_t)ad0 + (uint32_t)s * (kTileStageBytes >> 4);
       const uint32_t bl = (uint32_t)bd0 + (uint32_t)s * (kTileStageBytes >> 4);
-      if (tc::elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < kChunk / 32; ++kk)
-          tc::mma_e4m3_pair(tmem + b * kTile, al + kk * 2, a_hi, bl + kk * 2, b_hi, idesc, kk > 0);
-        tc::mma_commit_pair(&tfull_bar[b]);
-        tc::mma_commit_pair(&empty_bar[s]);
+      for (uint32_t h = 0; h < 2; ++h) {
+        if (it >= 2 && live) live = tc::mbar_wait(tempty0 + 8u * h, tph, &abort_flag, a.err, tc::kErrTimeoutStage);
+        if (!live) break;
+        tc::tc_fence_after();
+        if (tc::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < kChunk / 32; ++kk)
+            tc::mma_e4m3_pair(tmem + (b0 + h) * (kTile / 2), al + kk * 2, a_hi, bl + h * (kRowsBytes / 2 >> 4) + kk * 2,
+                              b_hi, idesc, kk > 0);
+          tc::mma_commit_pair(&tfull_bar[b0 + h]);
+          if (h == 1) tc::mma_commit_pair(&empty_bar[s]);
+        }
+        __syncwarp();
       }
-      __syncwarp();
-      if (++s == kTileStages) {
-        s = 0;
+      if (!live) break;
+      tph ^= 1u;
+      s += 2;
+      if (s >= kTileStages) {
+        s -= kTileStages;
         ph ^= 1u;
       }
     }
-    if (lane == 0) consumed = it;
+    if (lane == 0) consumed[warp >> 1] = it;
   } else if (warp == 2) {
     // ---- scales: of the CTA's 128 rows and of the tile's two column blocks ----
     int batch = 0;
@@ -455,51 +501,51 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (lane == 0) tc::mbar_arrive(&scale_bar[slot]);
       }
     }
-  } else if (warp >= 4) {
-    // ---- sums: 64 columns of a row to a thread ----
+  }
+  } else {
+    // ---- sums: 128 columns of a row to a thread ----
+    tc::more_registers<kSumRegisters>();
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
-    const uint32_t half = (uint32_t)(warp - 4) >> 3;
-    const int col = ((warp - 4) >> 2) * kSumCols;
+    const uint32_t half = (uint32_t)(warp - 4) >> 2;
+    const int col = (int)half * kSumCols;
     const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
-    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0);
-    const uint32_t tfull0 = tc::smem_u32(tfull_bar);
+    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0) + 8u * half;
+    const uint32_t tfull0 = tc::smem_u32(tfull_bar) + 8u * half;
     const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * kBoxBytes;
     const uint32_t sa0 = tc::smem_u32(a_scales) + (uint32_t)(quarter * 32 + lane) * 4u;
     const uint32_t sb0 = tc::smem_u32(b_scales) + 4u * half;
-    uint32_t b = 0, ph = 0;  // accumulator of the next group, and its barriers' parity
+    uint32_t b = 0, ph = 0;  // accumulators of the next group, and their barriers' parity
     uint32_t slot = 0, slot_ph = 0;
     bool live = true;
     for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
       int m0, n0;
       place(item, m0, n0);
       const int row0 = m0 + 128 * (int)rank + quarter * 32, col0 = n0 + col;
-      Pair acc[kSumCols / 2];
+      Pair acc[kLoads][8];
 #pragma unroll
-      for (int i = 0; i < kSumCols / 2; ++i) acc[i] = 0;
+      for (int i = 0; i < kSumCols / 2; ++i) acc[i / 8][i % 8] = 0;
       // A wait that gives up makes all later ones give up too; that is looked at once in
       // eight groups.
       auto group = [&](uint32_t sa, uint32_t sb) {
         const float f = tc::lds_f32(sa) * tc::lds_f32(sb);
         const Pair f2 = pair(f, f);
-        live = tc::mbar_wait(tfull0 + 8u * b, ph, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
+        live = tc::mbar_wait(tfull0 + 16u * b, ph, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
         __syncwarp();  // the loads are the whole warp's
         tc::tc_fence_after();
         const uint32_t at = at0 + b * kTile;
+        uint32_t v[2][16];
+        tc::tmem_ld_32x32b_x16(at, v[0]);
+        tc::tmem_wait_ld_regs(v[0]);
 #pragma unroll
-        for (int h = 0; h < kSumCols / kLoadCols; ++h) {
-          uint32_t v[kLoadCols];
-          tc::tmem_ld_32x32b<kLoadCols>(at + h * kLoadCols, v);
-          tc::tmem_wait_ld_regs(v);
-          if (h == kSumCols / kLoadCols - 1) {  // the accumulator is read
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive_pair(tempty0 + 8u * b);
-          }
+        for (int h = 0; h + 1 < kLoads; ++h) add_and_load(acc[h], v[h & 1], f2, v[(h + 1) & 1], at + 16 * (h + 1));
+        tc::tc_fence_before();  // the accumulator is read
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_pair(tempty0 + 16u * b);
+        const uint32_t* w = v[(kLoads - 1) & 1];
 #pragma unroll
-          for (int i = 0; i < kLoadCols / 2; ++i) {
-            Pair& s = acc[h * (kLoadCols / 2) + i];
-            s = fma2(pair(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, s);
-          }
+        for (int i = 0; i < 8; ++i) {
+          Pair& s = acc[kLoads - 1][i];
+          s = fma2(pair(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), f2, s);
         }
         b ^= 1u;
         ph ^= b ^ 1u;
@@ -544,7 +590,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             uint32_t r[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float2 v = split(acc[16 * h + 4 * j + i]);
+              const float2 v = split(acc[2 * h + j / 2][4 * (j % 2) + i]);
               const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
               r[i] = *reinterpret_cast<const uint32_t*>(&p);
             }
@@ -557,7 +603,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         for (int h = 0; h < kSumCols / 16; ++h) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 lo = split(acc[8 * h + 2 * j]), hi = split(acc[8 * h + 2 * j + 1]);
+            const float2 lo = split(acc[h][2 * j]), hi = split(acc[h][2 * j + 1]);
             w[j] = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
           }
           send(col0 + 16 * h, w);
@@ -573,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0 && abort_flag) {
     volatile int dummy = 0;
     if (rank == 0) {
-      for (int i = consumed; i < issued; ++i)
+      for (int i = consumed[0] < consumed[1] ? consumed[0] : consumed[1]; i < issued; ++i)
         tc::mbar_wait(&full_bar[i % kTileStages], (i / kTileStages) & 1, &dummy, nullptr, 0, 100000000ull);
     } else {
       const uint64_t t0 = tc::globaltimer();
@@ -624,7 +670,7 @@ cudaError_t launch_tiles(Product8& p, const MatmulBlocks& a, cudaStream_t stream
   if (err == cudaSuccess)
     err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
   if (err == cudaSuccess)
-    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 128);
+    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 64);
   const uint32_t size = a.y_type == SKETCH_BF16 ? 2 : 4;
   if (err == cudaSuccess)
     err = make_tmap_out_2d(&p.tmY, a.y_type, a.Y, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)a.ld_y * size, 64 / size, 32);

@@ -355,6 +355,18 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// ---- registers --------------------------------------------------------------------
+// A warpgroup gives registers up or takes some, out of those that the block was launched
+// with.  Inside the branch of the warps' role: where branches meet the fewer count holds.
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // ---- clusters ------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
