@@ -34,21 +34,27 @@ struct GradBatch {
 __device__ __forceinline__ bool on_vector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // The units of block `block` of `blocks`, one after another: f(problem, first value).
-template <typename F>
+// BACK: the last one first.
+template <bool BACK, typename F>
 __device__ __forceinline__ void walk_units(const GradBatch& a, int block, int blocks, F f) {
-  const int64_t units = a.begin[a.n];
-  int64_t u = units * block / blocks;
-  const int64_t end = units * (block + 1) / blocks;
-  if (u >= end) return;
+  const int64_t units = a.begin[a.n], begin = units * block / blocks, end = units * (block + 1) / blocks;
+  if (begin >= end) return;
+  int64_t u = BACK ? end - 1 : begin;
   int lo = 0, hi = a.n;  // the last tensor that begins at or before the unit
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (a.begin[mid] <= u) lo = mid;
     else hi = mid;
   }
-  for (; u < end; ++u) {
-    while (u >= a.begin[lo + 1]) ++lo;
+  for (int64_t left = end - begin; left > 0; --left) {
     f(a.p[lo], (u - a.begin[lo]) * kUnit);
+    if constexpr (BACK) {
+      --u;
+      while (lo > 0 && u < a.begin[lo]) --lo;
+    } else {
+      ++u;
+      while (lo + 1 < a.n && u >= a.begin[lo + 1]) ++lo;
+    }
   }
 }
 
@@ -117,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   __shared__ double part[kThreads / 32];
   cudaTriggerProgrammaticLaunchCompletion();  // grad_norm_join_kernel may come up as blocks leave
   double sum = 0.0;
-  walk_units(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+  walk_units<false>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
     float v[kEach];
     if (p.type == SKETCH_BF16) load_unit(static_cast<const __nv_bfloat16*>(p.G), p.count, first, v);
     else load_unit(static_cast<const float*>(p.G), p.count, first, v);
@@ -165,9 +171,11 @@ __device__ __forceinline__ void scale_unit(const G* g, G* out, int64_t n, int64_
   }
 }
 
+// Each block walks the units that it has in the norm, but from their end: what that
+// read last is still in L2.
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradBatch a, const float* scale) {
   const float s = *scale;
-  walk_units(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+  walk_units<true>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
     if (s == 1.f && p.out == p.G) return;
     if (p.type == SKETCH_BF16)
       scale_unit(static_cast<const __nv_bfloat16*>(p.G), static_cast<__nv_bfloat16*>(p.out), p.count, first, s);

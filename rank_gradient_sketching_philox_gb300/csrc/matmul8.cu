@@ -539,8 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int h = 0; h + 1 < kLoads; ++h) add_and_load(acc[h], v[h & 1], f2, v[(h + 1) & 1], at + 16 * (h + 1));
         tc::tc_fence_before();  // the accumulator is read
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive_pair(tempty0 + 16u * b);
+        if (tc::elect_one()) tc::mbar_arrive_pair(tempty0 + 16u * b);
         const uint32_t* w = v[(kLoads - 1) & 1];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
