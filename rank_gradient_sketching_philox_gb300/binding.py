@@ -825,18 +825,20 @@ def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=No
 SCALE_BLOCK = 128  # columns, or rows and columns of a weight, that share a scale
 
 
-class _on:
-    """The launches inside go to ``device``, whatever device is current."""
-    __slots__ = ("index", "before")
+_set_device = torch._C._cuda_exchangeDevice  # returns the one before
 
-    def __init__(self, device):
-        self.index = device.index
 
-    def __enter__(self):
-        self.before = torch._C._cuda_exchangeDevice(self.index)
-
-    def __exit__(self, *exc):
-        torch._C._cuda_maybeExchangeDevice(self.before)
+def _launch(device, fn, *args):
+    """Call the library with ``device`` current, whatever device was."""
+    index = device.index
+    before = _set_device(index)
+    try:
+        st = fn(*args)
+    finally:
+        if before != index:
+            _set_device(before)
+    if st:
+        _check(st)
 
 
 def _check_stream(stream, device):
@@ -890,12 +892,9 @@ def rms_norm_forward(X, gamma, rstd=None, R=None, S=None, Y=None, Q=None, scale=
     if rstd is not None:
         _vector(rstd, T, torch.float32, dev, "rstd")
     _check_stream(stream, dev)
-    with _on(dev):
-        st = lib().sketch_rms_norm_forward(X.data_ptr(), x_type, T, k, ld_x, _addr(R), ld_r, _addr(S), ld_s,
-                                           _addr(gamma), w_type, eps, _addr(Y), ld_y, _addr(Q), ld_q, _addr(scale),
-                                           _addr(rstd), _stream_of(stream, dev))
-    if st:
-        _check(st)
+    _launch(dev, lib().sketch_rms_norm_forward, X.data_ptr(), x_type, T, k, ld_x, _addr(R), ld_r, _addr(S),
+            ld_s, _addr(gamma), w_type, eps, _addr(Y), ld_y, _addr(Q), ld_q, _addr(scale), _addr(rstd),
+            _stream_of(stream, dev))
     return Y if Y is not None else Q
 
 
@@ -914,13 +913,10 @@ def rms_norm_backward(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, overwri
     if dgamma is not None:
         _vector(dgamma, k, torch.float32, dev, "dgamma")
     _check_stream(stream, dev)
-    with _on(dev):
-        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
-        st = lib().sketch_rms_norm_backward(dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s, _addr(gamma), w_type,
-                                            rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
-                                            1 if overwrite else 0, ws_at, nbytes, _stream_of(stream, dev))
-    if st:
-        _check(st)
+    keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
+    _launch(dev, lib().sketch_rms_norm_backward, dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
+            _addr(gamma), w_type, rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
+            1 if overwrite else 0, ws_at, nbytes, _stream_of(stream, dev))
     return dX
 
 
@@ -937,11 +933,8 @@ def quantize_blocks(X, Q, scale, rows=1, Qt=None, stream=None):
     ld_qt = 0 if Qt is None else _codes(Qt, k, T, dev, "Qt")
     _vector(scale, (T + rows - 1) // rows * _groups(k) if rows > 0 else 0, torch.float32, dev, "scale")
     _check_stream(stream, dev)
-    with _on(dev):
-        st = lib().sketch_quantize_blocks(X.data_ptr(), x_type, T, k, ld_x, rows, _addr(Q), ld_q, scale.data_ptr(),
-                                          _addr(Qt), ld_qt, _stream_of(stream, dev))
-    if st:
-        _check(st)
+    _launch(dev, lib().sketch_quantize_blocks, X.data_ptr(), x_type, T, k, ld_x, rows, _addr(Q), ld_q,
+            scale.data_ptr(), _addr(Qt), ld_qt, _stream_of(stream, dev))
     return Q
 
 
@@ -967,12 +960,9 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
         raise ValueError("Y must be a %d x %d matrix on %s with unit column stride" % (T, N, dev))
     ld_y = Y.stride(0) if T > 1 else (N + 7) // 8 * 8
     _check_stream(stream, dev)
-    with _on(dev):
-        st = lib().sketch_matmul_blocks(A.data_ptr(), T, k, ld_a, a_scale.data_ptr(), ld_as, B.data_ptr(), N, ld_b,
-                                        b_scale.data_ptr(), bs_row, bs_col, Y.data_ptr(), y_type, ld_y,
-                                        1 if overwrite else 0, _stream_of(stream, dev))
-    if st:
-        _check(st)
+    _launch(dev, lib().sketch_matmul_blocks, A.data_ptr(), T, k, ld_a, a_scale.data_ptr(), ld_as, B.data_ptr(),
+            N, ld_b, b_scale.data_ptr(), bs_row, bs_col, Y.data_ptr(), y_type, ld_y, 1 if overwrite else 0,
+            _stream_of(stream, dev))
     return Y
 
 
@@ -1004,12 +994,9 @@ def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=Non
     if scale is not None:
         _vector(scale, 1, torch.float32, dev, "scale")
     _check_stream(stream, dev)
-    with _on(dev):
-        keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, dev, stream, ws)
-        st = lib().sketch_grad_norm_batched(len(probs), probs, max_norm, norm.data_ptr(), _addr(scale), ws_at, nbytes,
-                                            _stream_of(stream, dev))
-    if st:
-        _check(st)
+    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, dev, stream, ws)
+    _launch(dev, lib().sketch_grad_norm_batched, len(probs), probs, max_norm, norm.data_ptr(), _addr(scale),
+            ws_at, nbytes, _stream_of(stream, dev))
     return norm
 
 
@@ -1020,7 +1007,4 @@ def grad_scale_batched(probs, scale, stream=None):
         raise ValueError("scale must be a CUDA tensor")
     _vector(scale, 1, torch.float32, dev, "scale")
     _check_stream(stream, dev)
-    with _on(dev):
-        st = lib().sketch_grad_scale_batched(len(probs), probs, scale.data_ptr(), _stream_of(stream, dev))
-    if st:
-        _check(st)
+    _launch(dev, lib().sketch_grad_scale_batched, len(probs), probs, scale.data_ptr(), _stream_of(stream, dev))

@@ -121,7 +121,7 @@ __device__ __forceinline__ double block_sum(double v, double* part) {
 
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ GradBatch a, double* partials) {
   __shared__ double part[kThreads / 32];
-  cudaTriggerProgrammaticLaunchCompletion();  // grad_norm_join_kernel may come up as blocks leave
+  start_early();
   double sum = 0.0;
   walk_units<false>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
     float v[kEach];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
 __global__ void __launch_bounds__(kThreads) grad_norm_join_kernel(const double* partials, int64_t n, float max_norm,
                                                                   float* norm, float* scale) {
   __shared__ double part[kThreads / 32];
-  cudaGridDependencySynchronize();
+  start_early();
   double sum = 0.0;
   for (int64_t i = threadIdx.x; i < n; i += kThreads) sum += partials[i];
   sum = sqrt(block_sum(sum, part));
@@ -174,6 +174,7 @@ __device__ __forceinline__ void scale_unit(const G* g, G* out, int64_t n, int64_
 // Each block walks the units that it has in the norm, but from their end: what that
 // read last is still in L2.
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradBatch a, const float* scale) {
+  start_early();
   const float s = *scale;
   walk_units<true>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
     if (s == 1.f && p.out == p.G) return;
@@ -216,30 +217,17 @@ cudaError_t launch_grad_norm(int n, const sketch_grad_problem* probs, float max_
                              double* ws, cudaStream_t stream) {
   int64_t partials = 0;
   const cudaError_t err = for_batches(n, probs, [&](const GradBatch& a, int blocks) {
-    count_launch();
-    grad_norm_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, ws + partials);
+    double* to = ws + partials;
     partials += blocks;
-    return cudaGetLastError();
+    return launch_early(grad_norm_kernel, blocks, kThreads, 0, stream, a, to);
   });
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, grad_norm_join_kernel, (const double*)ws, partials, max_norm, norm, scale);
+  return launch_early(grad_norm_join_kernel, 1, kThreads, 0, stream, (const double*)ws, partials, max_norm, norm, scale);
 }
 
 cudaError_t launch_grad_scale(int n, const sketch_grad_problem* probs, const float* scale, cudaStream_t stream) {
   return for_batches(n, probs, [&](const GradBatch& a, int blocks) {
-    count_launch();
-    grad_scale_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(a, scale);
-    return cudaGetLastError();
+    return launch_early(grad_scale_kernel, blocks, kThreads, 0, stream, a, scale);
   });
 }
 

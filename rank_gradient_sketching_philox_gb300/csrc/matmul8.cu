@@ -67,35 +67,49 @@ __device__ __forceinline__ void put4(const Product8& a, int64_t row, int col, fl
 // B's rows are the MMA's M (128 of them), TN tokens its N.  A cluster of S CTAs splits
 // the groups of a tile and joins its parts through distributed shared memory, each CTA
 // a share of the tokens, in the CTAs' order.
-constexpr int kFewThreads = 192;  // copies, MMAs, four warps of sums
-constexpr int kFewStages = 12;    // at most
-constexpr int few_buffers(int TN) { return TN >= 128 ? 2 : TN >= 64 ? 4 : 8; }
-constexpr int few_columns(int TN) { return TN * few_buffers(TN) < 32 ? 32 : TN * few_buffers(TN); }
+constexpr int kFewStages = 5;   // at most: 104 KB, for two CTAs per SM
+constexpr int few_buffers(int TN) { return TN == 64 ? 4 : 8; }
+constexpr int few_columns(int TN) { return TN * few_buffers(TN); }  // of TMEM: 128 or 256 of 512
+// Tokens of a thread of the sums' warps: 32 at most, then two warps share 32 rows of B.
+constexpr int few_cols(int TN) { return TN <= 32 ? TN : TN / 2; }
+constexpr int few_warps(int TN) { return 4 * (TN / few_cols(TN)); }
+constexpr int few_threads(int TN) { return 64 + 32 * few_warps(TN); }  // copies, MMAs, sums
+constexpr int kFewResident = 2;                                        // CTAs per SM
+constexpr uint32_t few_stage_bytes(int TN) { return kRowsBytes + TN * kChunk; }
 
 template <int TN>
-__global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __grid_constant__ Product8 a) {
-  constexpr int kBuffers = few_buffers(TN);
-  constexpr uint32_t kStageBytes = kRowsBytes + TN * kChunk;
+__global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_kernel(const __grid_constant__ Product8 a) {
+  constexpr int kBuffers = few_buffers(TN), kCols = few_cols(TN), kSums = few_warps(TN);
+  constexpr uint32_t kStageBytes = few_stage_bytes(TN);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kFewStages], empty_bar[kFewStages];
   __shared__ __align__(8) uint64_t tfull_bar[kBuffers], tempty_bar[kBuffers];
-  __shared__ __align__(16) float factor[4][2][TN];
+  __shared__ __align__(16) float factor[kSums][2][kCols];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int issued, consumed;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint32_t S, rank;
+  uint32_t S;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(S));
-  rank = tc::cluster_ctarank();
+  const uint32_t rank = tc::cluster_ctarank();
   const int tile = (int)(blockIdx.x / S);
   const int n0 = tile % a.n_tiles * 128, t0 = tile / a.n_tiles * TN;
   const int c0 = (int)((int64_t)a.chunks * rank / S), n_mine = (int)((int64_t)a.chunks * (rank + 1) / S) - c0;
 
+  auto fetch = [&](int i, int s) {
+    uint8_t* st = smem + (size_t)s * kStageBytes;
+    tc::mbar_arrive_expect_tx(&full_bar[s], kStageBytes);
+    tc::tma_load_2d(st, &a.tmB, &full_bar[s], (c0 + i) * kChunk, n0);
+    tc::tma_load_2d(st + kRowsBytes, &a.tmA, &full_bar[s], (c0 + i) * kChunk, t0);
+  };
+  const int early = n_mine < a.stages ? n_mine : a.stages;
   if (threadIdx.x == 0) {
+    tc::prefetch_tmap(&a.tmA);
+    tc::prefetch_tmap(&a.tmB);
     abort_flag = 0;
-    issued = 0;
+    issued = early;
     consumed = 0;
     for (int s = 0; s < a.stages; ++s) {
       tc::mbar_init(&full_bar[s], 1);
@@ -103,36 +117,39 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
     }
     for (int b = 0; b < kBuffers; ++b) {
       tc::mbar_init(&tfull_bar[b], 1);
-      tc::mbar_init(&tempty_bar[b], 4);
+      tc::mbar_init(&tempty_bar[b], kSums);
     }
     tc::fence_mbar_init();
+    tc::fence_proxy_async_smem();
+    cudaGridDependencySynchronize();
+    for (int i = 0; i < early; ++i) fetch(i, i);  // while the others set up
   }
-  if (warp == 0) tc::tmem_alloc(&tmem_slot, few_columns(TN));
+  if (warp == 1) tc::tmem_alloc(&tmem_slot, few_columns(TN));
+  start_early();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  Pair acc[TN / 2];
+  Pair acc[kCols / 2];
 #pragma unroll
-  for (int i = 0; i < TN / 2; ++i) acc[i] = 0;
+  for (int i = 0; i < kCols / 2; ++i) acc[i] = 0;
 
-  if (warp == 0 && lane == 0) {
+  if (warp == 0) {
     // ---- copies ----
-    int s = 0;
-    uint32_t ph = 0;
-    for (int i = 0; i < n_mine; ++i) {
-      if (i >= a.stages && !tc::mbar_wait(&empty_bar[s], ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
-      uint8_t* st = smem + (size_t)s * kStageBytes;
-      tc::mbar_arrive_expect_tx(&full_bar[s], kStageBytes);
-      tc::tma_load_2d(st, &a.tmB, &full_bar[s], (c0 + i) * kChunk, n0);
-      tc::tma_load_2d(st + kRowsBytes, &a.tmA, &full_bar[s], (c0 + i) * kChunk, t0);
-      issued = i + 1;
-      if (++s == a.stages) {
-        s = 0;
-        ph ^= 1u;
+    if (lane == 0) {
+      int s = early % a.stages;
+      uint32_t ph = 0;
+      for (int i = early; i < n_mine; ++i) {
+        if (!tc::mbar_wait(&empty_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
+        fetch(i, s);
+        issued = i + 1;
+        if (++s == a.stages) {
+          s = 0;
+          ph ^= 1u;
+        }
       }
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
     // ---- MMAs: a group to an accumulator ----
     constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
     int s = 0, b = 0;
@@ -142,13 +159,16 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
       if (i >= kBuffers && !tc::mbar_wait(&tempty_bar[b], bph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
       tc::tc_fence_after();
       const uint32_t sa = tc::smem_u32(smem + (size_t)s * kStageBytes);
+      if (tc::elect_one()) {
 #pragma unroll
-      for (int kk = 0; kk < kChunk / 32; ++kk)
-        tc::mma_e4m3(tmem + (uint32_t)(b * TN), tc::sdesc_sw128(sa + kk * 32, 16, 1024),
-                     tc::sdesc_sw128(sa + kRowsBytes + kk * 32, 16, 1024), idesc, kk > 0);
-      tc::mma_commit(&empty_bar[s]);
-      tc::mma_commit(&tfull_bar[b]);
-      consumed = i + 1;
+        for (int kk = 0; kk < kChunk / 32; ++kk)
+          tc::mma_e4m3(tmem + (uint32_t)(b * TN), tc::sdesc_sw128(sa + kk * 32, 16, 1024),
+                       tc::sdesc_sw128(sa + kRowsBytes + kk * 32, 16, 1024), idesc, kk > 0);
+        tc::mma_commit(&tfull_bar[b]);
+        tc::mma_commit(&empty_bar[s]);
+        consumed = i + 1;
+      }
+      __syncwarp();
       if (++s == a.stages) {
         s = 0;
         ph ^= 1u;
@@ -158,20 +178,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
         bph ^= 1u;
       }
     }
-  } else if (warp >= 2) {
+  } else {
     // ---- sums: a row of B to a thread ----
     const int quarter = warp & 3;  // TMEM lanes 32 (warp % 4) .. +31
-    float(*f)[TN] = factor[quarter];
+    const int col = (warp - 2) / 4 * kCols;
+    float(*f)[kCols] = factor[warp - 2];
     const uint32_t f0 = tc::smem_u32(f);
-    constexpr int kMine = (TN + 31) / 32;
+    constexpr int kMine = (kCols + 31) / 32;
     const float* as[kMine];
     float next[kMine];
     float next_b = 0.f;
     const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const int t = t0 + i * 32 + lane;
-      as[i] = (TN >= 32 || lane < TN) && t < a.T ? a.a_scale + t * a.ld_as : nullptr;
+      const int t = t0 + col + i * 32 + lane;
+      as[i] = (kCols >= 32 || lane < kCols) && t < a.T ? a.a_scale + t * a.ld_as : nullptr;
     }
     auto load = [&](int c) {
 #pragma unroll
@@ -184,32 +205,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
     for (int i = 0; i < n_mine; ++i) {
 #pragma unroll
       for (int j = 0; j < kMine; ++j)
-        if (TN >= 32 || lane < TN) f[i & 1][j * 32 + lane] = next[j] * next_b;
+        if (kCols >= 32 || lane < kCols) f[i & 1][j * 32 + lane] = next[j] * next_b;
       __syncwarp();
       if (i + 1 < n_mine) load(c0 + i + 1);
       const bool live = tc::mbar_wait(&tfull_bar[b], bph, &abort_flag, a.err, tc::kErrTimeoutMma);
       if (!__all_sync(0xFFFFFFFFu, live)) break;
       tc::tc_fence_after();
-      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * TN);
-      constexpr int kCols = TN < 32 ? TN : 32;
+      const uint32_t at = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(b * TN + col);
+      constexpr int kLoad = kCols < 32 ? kCols : 32;
 #pragma unroll
-      for (int cg = 0; cg < TN / kCols; ++cg) {
-        uint32_t v[kCols];
-        tc::tmem_ld_32x32b<kCols>(at + cg * kCols, v);
+      for (int cg = 0; cg < kCols / kLoad; ++cg) {
+        uint32_t v[kLoad];
+        tc::tmem_ld_32x32b<kLoad>(at + cg * kLoad, v);
         tc::tmem_wait_ld_regs(v);
+        if (cg == kCols / kLoad - 1) {  // the accumulator is read
+          tc::tc_fence_before();
+          if (tc::elect_one()) tc::mbar_arrive(&tempty_bar[b]);
+        }
 #pragma unroll
-        for (int q = 0; q < kCols / 4; ++q) {
-          const uint4 w = tc::lds128(f0 + (uint32_t)(((i & 1) * TN + cg * kCols + 4 * q) * 4));
-          Pair* p = acc + (cg * kCols + 4 * q) / 2;
+        for (int q = 0; q < kLoad / 4; ++q) {
+          const uint4 w = tc::lds128(f0 + (uint32_t)(((i & 1) * kCols + cg * kLoad + 4 * q) * 4));
+          Pair* p = acc + (cg * kLoad + 4 * q) / 2;
           p[0] = fma2(pair(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])),
                       pair(__uint_as_float(w.x), __uint_as_float(w.y)), p[0]);
           p[1] = fma2(pair(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])),
                       pair(__uint_as_float(w.z), __uint_as_float(w.w)), p[1]);
         }
       }
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&tempty_bar[b]);
       if (++b == kBuffers) {
         b = 0;
         bph ^= 1u;
@@ -221,21 +243,21 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);  // [token][row of B]
   if (warp >= 2) {
-    const int q = (warp & 3) * 32 + lane;
+    const int q = (warp & 3) * 32 + lane, col = (warp - 2) / 4 * kCols;
 #pragma unroll
-    for (int i = 0; i < TN / 2; ++i) {
+    for (int i = 0; i < kCols / 2; ++i) {
       const float2 v = split(acc[i]);
-      red[(2 * i) * 128 + q] = v.x;
-      red[(2 * i + 1) * 128 + q] = v.y;
+      red[(col + 2 * i) * 128 + q] = v.x;
+      red[(col + 2 * i + 1) * 128 + q] = v.y;
     }
   }
   if (S > 1) tc::cluster_sync();
   else __syncthreads();
-  const int share = TN / (int)S;
   const uint32_t red0 = tc::smem_u32(red);
-  for (int e = threadIdx.x; e < share * 32; e += kFewThreads) {
-    const int t = (int)rank * share + (e >> 5), n = (e & 31) * 4;
-    if (t0 + t >= a.T || n0 + n >= a.N) continue;
+  const int tokens = a.T - t0 < TN ? a.T - t0 : TN;
+  for (int e = threadIdx.x; e < tokens * 32; e += few_threads(TN)) {
+    const int t = e >> 5, n = (e & 31) * 4;
+    if (t % (int)S != (int)rank || n0 + n >= a.N) continue;
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     const uint32_t off = red0 + (uint32_t)(t * 128 + n) * 4;
     for (uint32_t r = 0; r < S; ++r) {
@@ -252,37 +274,58 @@ __global__ void __launch_bounds__(kFewThreads, 1) matmul8_few_kernel(const __gri
   }
   __syncthreads();
   if (S > 1) tc::cluster_sync();  // no CTA leaves while its part may still be read
-  if (warp == 0) tc::tmem_dealloc(tmem, few_columns(TN));
+  if (warp == 1) tc::tmem_dealloc(tmem, few_columns(TN));
+}
+
+// Clusters' size for `tiles` tiles: the one with the fewest groups one after another,
+// over the rounds that the CTAs take; of a tie's two the smaller one.
+unsigned few_split(int64_t tiles, int chunks, int64_t* steps) {
+  const int64_t slots = (int64_t)num_sms() * kFewResident;
+  unsigned S = 1;
+  *steps = INT64_MAX;
+  for (int s = 1; s <= 8 && s <= chunks; ++s) {
+    const int64_t n = ceil_div(tiles * s, slots) * ceil_div(chunks, s);
+    if (n < *steps) {
+      *steps = n;
+      S = (unsigned)s;
+    }
+  }
+  return S;
 }
 
 template <int TN>
 cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) {
-  constexpr uint32_t kStageBytes = kRowsBytes + TN * kChunk;
+  constexpr uint32_t kStageBytes = few_stage_bytes(TN);
   cudaError_t err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, TN);
   if (err == cudaSuccess)
     err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 128);
   if (err != cudaSuccess) return err;
   p.n_tiles = (int)ceil_div(a.N, 128);
   const int64_t tiles = (int64_t)p.n_tiles * ceil_div(a.T, TN);
-  unsigned S = 1;
-  while (S < 8 && tiles * S < num_sms() && 2 * S <= (unsigned)p.chunks) S *= 2;
-  p.stages = (int)((200u << 10) / kStageBytes);
-  if (p.stages > kFewStages) p.stages = kFewStages;
-  const size_t smem = (size_t)p.stages * kStageBytes + 1024;
+  int64_t steps;
+  const unsigned S = few_split(tiles, p.chunks, &steps);
+  p.stages = (int)ceil_div(p.chunks, S);
+  const int most = (int)((104u << 10) / kStageBytes);
+  if (p.stages > most) p.stages = most;
+  size_t smem = (size_t)p.stages * kStageBytes;
+  if (smem < (size_t)TN * 512) smem = (size_t)TN * 512;  // a part of the sum
+  smem += 1024;
   err = allow_smem(matmul8_few_kernel<TN>, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
-  cfg.blockDim = dim3(kFewThreads, 1, 1);
+  cfg.blockDim = dim3(few_threads(TN), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = S;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // comes up while the kernel before ends
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   count_launch();
   return cudaLaunchKernelEx(&cfg, matmul8_few_kernel<TN>, p);
 }
@@ -367,6 +410,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tc::fence_mbar_init();
   }
   if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
+  start_early();
   tc::tc_fence_before();
   __syncthreads();
   tc::cluster_sync();  // both CTAs' barriers exist before either signals one
@@ -564,10 +608,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (!live) break;
       }
       if (!live) break;
-      // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle
+      // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle; a row's last values
+      // singly where they do not fill 16 bytes, which TMA would write whole
       const bool fp32 = a.y_type == SKETCH_FP32;
       const uint32_t mine = box + (uint32_t)lane * 64u, swizzle = (uint32_t)(lane >> 1) & 3u;
       auto send = [&](int c, const uint4(&w)[4]) {
+        const int cols = fp32 ? 16 : 32;
+        if (c + cols > a.N && a.N % (fp32 ? 4 : 8) != 0) {
+          if (row0 + lane >= a.T) return;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t r[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (fp32) {
+                float* y = static_cast<float*>(a.Y) + (int64_t)(row0 + lane) * a.ld_y + c + 4 * j + i;
+                if (c + 4 * j + i < a.N) *y = a.overwrite ? __uint_as_float(r[i]) : *y + __uint_as_float(r[i]);
+              } else {
+                uint16_t* y = static_cast<uint16_t*>(a.Y) + (int64_t)(row0 + lane) * a.ld_y + c + 8 * j + 2 * i;
+                if (c + 8 * j + 2 * i < a.N) y[0] = (uint16_t)r[i];
+                if (c + 8 * j + 2 * i + 1 < a.N) y[1] = (uint16_t)(r[i] >> 16);
+              }
+            }
+          }
+          return;
+        }
         if (lane == 0) tc::bulk_wait_read<0>();  // the box's last copy has left
         __syncwarp();
 #pragma unroll
@@ -663,11 +728,8 @@ cudaError_t tile_pairs(int* out) {
   return cudaSuccess;
 }
 
-cudaError_t launch_tiles(Product8& p, const MatmulBlocks& a, cudaStream_t stream) {
-  int pairs = 0;
-  cudaError_t err = tile_pairs(&pairs);
-  if (err == cudaSuccess)
-    err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
+cudaError_t launch_tiles(Product8& p, int pairs, const MatmulBlocks& a, cudaStream_t stream) {
+  cudaError_t err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
   if (err == cudaSuccess)
     err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 64);
   const uint32_t size = a.y_type == SKETCH_BF16 ? 2 : 4;
@@ -677,9 +739,7 @@ cudaError_t launch_tiles(Product8& p, const MatmulBlocks& a, cudaStream_t stream
   p.m_tiles = (int)ceil_div(a.T, kTile);
   p.n_tiles = (int)ceil_div(a.N, kTile);
   const int items = p.m_tiles * p.n_tiles;
-  count_launch();
-  matmul8_tile_kernel<<<2 * (unsigned)(items < pairs ? items : pairs), kTileThreads, kTileSmem, stream>>>(p);
-  return cudaGetLastError();
+  return launch_early(matmul8_tile_kernel, 2 * (items < pairs ? items : pairs), kTileThreads, kTileSmem, stream, p);
 }
 
 }  // namespace
@@ -700,12 +760,20 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   p.T = (int)a.T;
   p.N = (int)a.N;
   p.chunks = (int)ceil_div(a.k, kChunk);
-  // few tokens, or too few tiles of 256 x 256 for the pairs of CTAs
-  if (a.T > 128 && ceil_div(a.T, kTile) * ceil_div(a.N, kTile) * 4 >= num_sms()) return launch_tiles(p, a, stream);
   if (a.T <= 16) return launch_few<16>(p, a, stream);
   if (a.T <= 32) return launch_few<32>(p, a, stream);
-  if (a.T <= 64) return launch_few<64>(p, a, stream);
-  return launch_few<128>(p, a, stream);
+  // Which takes less, in us as measured: few tokens' kernel 5 and 0.85 for each group one
+  // after another, the pairs of CTAs 5 and 0.37 for each group and 1.5 for each further
+  // round of tiles.  4096 x 4096 with 192 tokens 14.7 against 16.7, with 256 18.5
+  // against 16.8; 12288 x 4096 with 64 14.8 against 16.3, with 96 25 against 16.5.
+  int pairs = 0;
+  err = tile_pairs(&pairs);
+  if (err != cudaSuccess) return err;
+  int64_t steps;
+  few_split(ceil_div(a.T, 64) * ceil_div(a.N, 128), p.chunks, &steps);
+  const int64_t rounds = ceil_div(ceil_div(a.T, kTile) * ceil_div(a.N, kTile), pairs);
+  if (0.85 * (double)steps <= 0.37 * (double)(rounds * p.chunks) + 1.5 * (double)(rounds - 1)) return launch_few<64>(p, a, stream);
+  return launch_tiles(p, pairs, a, stream);
 }
 
 }  // namespace rgs

@@ -123,6 +123,7 @@ __global__ void __launch_bounds__(kThreads) quantize_row_vectors_kernel(const Qu
   const int t = threadIdx.x % LANES;
   const uint32_t groups = (uint32_t)ceil_div(a.k, kScaleBlock);
   const int64_t first = (int64_t)blockIdx.x * (PER_BLOCK * kPieces) + threadIdx.x / LANES;
+  start_early();
   uint4 raw[kPieces];
   int64_t row[kPieces], col[kPieces];
 #pragma unroll
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kThreads) quantize_tile_vectors_kernel(const Q
   const int64_t groups = ceil_div(a.k, kScaleBlock);
   const int64_t r0 = blockIdx.x / groups * kScaleBlock, c0 = blockIdx.x % groups * kScaleBlock;
   const bool has = c0 + t * VE < a.k;
+  start_early();
   uint4 raw[STEPS][4];
   uint32_t top = 0;
 #pragma unroll
@@ -245,15 +247,12 @@ cudaError_t quantize(const Quantize& a, cudaStream_t stream) {
   const int64_t groups = ceil_div(a.k, kScaleBlock);
   constexpr int VE = 16 / (int)sizeof(X), PER_BLOCK = kThreads / (kScaleBlock / VE) * kPieces;
   const bool vectors = whole_vectors(a.X, a.ld_x, a.k, VE, sizeof(X));
+  if (vectors && a.rows == 1 && ceil_div(a.T * groups, PER_BLOCK) < (int64_t(1) << 31))
+    return launch_early(quantize_row_vectors_kernel<X>, ceil_div(a.T * groups, PER_BLOCK), kThreads, 0, stream, a,
+                        a.T * groups);
+  if (vectors && a.rows == 128)
+    return launch_early(quantize_tile_vectors_kernel<X>, groups * ceil_div(a.T, kScaleBlock), kThreads, 0, stream, a);
   count_launch();
-  if (vectors && a.rows == 1 && ceil_div(a.T * groups, PER_BLOCK) < (int64_t(1) << 31)) {
-    quantize_row_vectors_kernel<X><<<(unsigned)ceil_div(a.T * groups, PER_BLOCK), kThreads, 0, stream>>>(a, a.T * groups);
-    return cudaGetLastError();
-  }
-  if (vectors && a.rows == 128) {
-    quantize_tile_vectors_kernel<X><<<(unsigned)(groups * ceil_div(a.T, kScaleBlock)), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
-  }
   if (a.rows == 1) {
     int64_t blocks = ceil_div(a.T * groups, kWarps);
     if (blocks > (int64_t)num_sms() * 64) blocks = (int64_t)num_sms() * 64;

@@ -130,17 +130,8 @@ __global__ void __launch_bounds__(kThreads) rms_grad_sum_kernel(const float* ws,
 }
 
 cudaError_t launch_grad_sum(const RmsBackward& a, int partials, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ceil_div(a.k, 32), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];  // its blocks may come up while the kernel before ends
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  count_launch();
-  return cudaLaunchKernelEx(&cfg, rms_grad_sum_kernel, (const float*)a.ws, a.k, partials, a.dgamma, a.overwrite);
+  return launch_early(rms_grad_sum_kernel, ceil_div(a.k, 32), kThreads, 0, stream, (const float*)a.ws, a.k, partials,
+                      a.dgamma, a.overwrite);
 }
 
 // ---- forward, rows in registers ----------------------------------------------------
@@ -176,6 +167,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) rms_forward_
   __shared__ float part[2][THREADS / 32];
   const int t = threadIdx.x & (tpr - 1), lane = threadIdx.x & 31, k = (int)a.k;
   const int nvec = k / VE, groups = (k + kScaleBlock - 1) / kScaleBlock;
+  start_early();
   for (int c = threadIdx.x; c < k; c += THREADS) weights[weight_at<VE>(c, k)] = weight(a.gamma, a.w_type, c, 1.f);
   const uint32_t gamma = tc::smem_u32(weights);
   const float inv_k = 1.f / (float)k;
@@ -286,6 +278,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 ? (G > 4 ? 2 : 3) : 1)
   const int groups = (k + kScaleBlock - 1) / kScaleBlock, rows = THREADS / 32 / wpr;
   const float inv_k = 1.f / (float)k;
   const int64_t stride = (int64_t)gridDim.x * rows;
+  start_early();
   int p = 0;
   for (int64_t base = (int64_t)blockIdx.x * rows; base < a.T; base += stride, p ^= 1) {
     const int64_t row = base + (threadIdx.x >> 5) / wpr;
@@ -361,10 +354,7 @@ cudaError_t forward_vectors(const RmsForward& a, int tpr, cudaStream_t stream) {
   if (blocks > most) blocks = most;
   auto launch = [&](auto kernel) {
     const cudaError_t err = allow_smem(kernel, smem);
-    if (err != cudaSuccess) return err;
-    count_launch();
-    kernel<<<(unsigned)blocks, THREADS, smem, stream>>>(a, tpr);
-    return cudaGetLastError();
+    return err == cudaSuccess ? launch_early(kernel, blocks, THREADS, smem, stream, a, tpr) : err;
   };
   if (a.R) return a.Q ? launch(rms_forward_kernel<X, THREADS, true, true>) : launch(rms_forward_kernel<X, THREADS, true, false>);
   return a.Q ? launch(rms_forward_kernel<X, THREADS, false, true>) : launch(rms_forward_kernel<X, THREADS, false, false>);
@@ -375,9 +365,7 @@ cudaError_t forward_singles(const RmsForward& a, int wpr, cudaStream_t stream) {
   int64_t blocks = ceil_div(a.T, THREADS / 32 / wpr);
   const int64_t most = (int64_t)num_sms() * (THREADS == 256 ? 6 : 2);
   if (blocks > most) blocks = most;
-  count_launch();
-  rms_forward_single_kernel<X, G, THREADS><<<(unsigned)blocks, THREADS, 0, stream>>>(a, wpr);
-  return cudaGetLastError();
+  return launch_early(rms_forward_single_kernel<X, G, THREADS>, blocks, THREADS, 0, stream, a, wpr);
 }
 
 template <typename X>
@@ -444,7 +432,7 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(THREADS))
     for (int s = 0; s < r.slots; ++s) tc::mbar_init(&full[s], 1);
     tc::fence_mbar_init();
   }
-  cudaTriggerProgrammaticLaunchCompletion();  // rms_grad_sum_kernel may come up as blocks leave
+  start_early();
   __syncthreads();
   int filled = 0;  // warp 0's: sets whose copies have begun
   if (warp == 0)
@@ -638,9 +626,7 @@ cudaError_t backward_rows(const RmsBackward& a, int tpr, bool& done, cudaStream_
   auto kernel = rms_backward_kernel<X, VE, NV, THREADS, DS>;
   err = allow_smem(kernel, smem);
   if (err != cudaSuccess) return err;
-  count_launch();
-  kernel<<<(unsigned)blocks, THREADS, smem, stream>>>(a, r, tpr, err_word);
-  err = cudaGetLastError();
+  err = launch_early(kernel, blocks, THREADS, smem, stream, a, r, tpr, err_word);
   if (err == cudaSuccess && a.dgamma) err = launch_grad_sum(a, (int)blocks, stream);
   return err;
 }

@@ -368,12 +368,19 @@ def test_matmul(T, N, k, dtype):
 
 
 @pytest.mark.parametrize("T,N,k", [(16, 4096, 4096), (3, 300, 16384), (600, 4096, 1024), (2500, 2056, 1000), (5000, 1000, 260),
-                                   (20000, 40, 72), (40, 20000, 72)])
-def test_matmul_larger(T, N, k):
+                                   (20000, 40, 72), (40, 20000, 72), (5001, 5001, 2100), (300, 9000, 5000), (1999, 1021, 130)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_matmul_larger(T, N, k, dtype):
     A, sa, B, sb = operands(gen(T), T, N, k)
-    Y = torch.empty(T, (N + 7) // 8 * 8, dtype=BF, device="cuda")[:, :N]
-    rgs.matmul_blocks(A, sa, B, sb, Y)
-    check_product(A, sa, B, sb, Y)
+    Y = torch.full((T, (N + 7) // 8 * 8), 7.0, dtype=dtype, device="cuda")
+    rgs.matmul_blocks(A, sa, B, sb, Y[:, :N])
+    check_product(A, sa, B, sb, Y[:, :N])
+    assert bool((Y[:, N:] == 7.0).all())
+    if dtype == F32:
+        before = Y[:, :N].clone()
+        rgs.matmul_blocks(A, sa, B, sb, Y[:, :N], overwrite=False)
+        check_product(A, sa, B, sb, Y[:, :N], before)
+        assert bool((Y[:, N:] == 7.0).all())
 
 
 @pytest.mark.parametrize("T", [3, 40, 300, 1000])
