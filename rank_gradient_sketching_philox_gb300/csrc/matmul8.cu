@@ -373,6 +373,20 @@ __device__ __forceinline__ void add_and_load(Pair (&acc)[8], const uint32_t (&v)
       : "memory");
 }
 
+// The last values of a row of Y from its 64 bytes in shared memory.
+__device__ __noinline__ void put_end(const Product8& a, int64_t row, int col, uint32_t mine, uint32_t swizzle) {
+  const bool fp32 = a.y_type == SKETCH_FP32;
+  for (int e = 0; col + e < a.N; ++e) {
+    const uint32_t byte = (uint32_t)e * (fp32 ? 4u : 2u), at = mine + (((byte >> 4) ^ swizzle) << 4) + (byte & 15u);
+    if (fp32) {
+      float* y = static_cast<float*>(a.Y) + row * a.ld_y + col + e;
+      *y = a.overwrite ? tc::lds_f32(at) : *y + tc::lds_f32(at);
+    } else {
+      store_one(static_cast<__nv_bfloat16*>(a.Y) + row * a.ld_y + col + e, read_one<__nv_bfloat16>(at));
+    }
+  }
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     matmul8_tile_kernel(const __grid_constant__ Product8 a) {
   extern __shared__ uint8_t smem_raw[];
@@ -613,33 +627,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const bool fp32 = a.y_type == SKETCH_FP32;
       const uint32_t mine = box + (uint32_t)lane * 64u, swizzle = (uint32_t)(lane >> 1) & 3u;
       auto send = [&](int c, const uint4(&w)[4]) {
-        const int cols = fp32 ? 16 : 32;
-        if (c + cols > a.N && a.N % (fp32 ? 4 : 8) != 0) {
-          if (row0 + lane >= a.T) return;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t r[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (fp32) {
-                float* y = static_cast<float*>(a.Y) + (int64_t)(row0 + lane) * a.ld_y + c + 4 * j + i;
-                if (c + 4 * j + i < a.N) *y = a.overwrite ? __uint_as_float(r[i]) : *y + __uint_as_float(r[i]);
-              } else {
-                uint16_t* y = static_cast<uint16_t*>(a.Y) + (int64_t)(row0 + lane) * a.ld_y + c + 8 * j + 2 * i;
-                if (c + 8 * j + 2 * i < a.N) y[0] = (uint16_t)r[i];
-                if (c + 8 * j + 2 * i + 1 < a.N) y[1] = (uint16_t)(r[i] >> 16);
-              }
-            }
-          }
-          return;
-        }
         if (lane == 0) tc::bulk_wait_read<0>();  // the box's last copy has left
         __syncwarp();
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) tc::sts128(mine + ((j ^ swizzle) << 4), w[j]);
         tc::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && row0 < a.T && c < a.N) {
+        if (a.N - c < (fp32 ? 16 : 32) && (a.N & (fp32 ? 3 : 7)) != 0) {
+          if (row0 + lane < a.T) put_end(a, row0 + lane, c, mine, swizzle);
+        } else if (lane == 0 && row0 < a.T && c < a.N) {
           if (fp32 && !a.overwrite) tc::tma_add_2d(&a.tmY, box, c, row0);
           else tc::tma_store_2d_at(&a.tmY, box, c, row0);
           tc::bulk_commit();
