@@ -460,7 +460,7 @@ SKETCH_API sketch_status sketch_rms_norm_forward(const void* X, sketch_dtype x_t
  * xh)) + dS, the gradient of x and of r alike; dgamma (+)= sum over rows of dY xh (k
  * fp32).  dS (nullable, only with dX) is the gradient that reaches S from the rest of the stream.  dY,
  * S, dS and dX have one type; dX may be dY or dS.  dX and dgamma may be NULL, not both.
- * overwrite = 1 replaces dgamma, 0 adds to it. */
+ * overwrite = 1 replaces dgamma, 0 adds to it.  The workspace is for dgamma alone. */
 SKETCH_API sketch_status sketch_rms_norm_backward(const void* dY, int64_t ld_dy, const void* S, sketch_dtype x_type,
                                                   int64_t T, int64_t k, int64_t ld_s, const void* gamma,
                                                   sketch_dtype w_type, const float* rstd, const void* dS,

@@ -913,7 +913,10 @@ def rms_norm_backward(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, overwri
     if dgamma is not None:
         _vector(dgamma, k, torch.float32, dev, "dgamma")
     _check_stream(stream, dev)
-    keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
+    keep = ws_at = None
+    nbytes = 0
+    if dgamma is not None:
+        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
     _launch(dev, lib().sketch_rms_norm_backward, dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
             _addr(gamma), w_type, rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
             1 if overwrite else 0, ws_at, nbytes, _stream_of(stream, dev))

@@ -764,7 +764,7 @@ sketch_status sketch_rms_norm_backward(const void* dY, int64_t ld_dy, const void
     CHECK_ELEM_PTR(dS, x_type);
   }
   CHECK_OPT_ALIGN(dgamma, 4);
-  TRY(check_ws(ws, ws_bytes, rgs::rms_backward_workspace_bytes(T, k)));
+  if (dgamma) TRY(check_ws(ws, ws_bytes, rgs::rms_backward_workspace_bytes(T, k)));
   const rgs::RmsBackward a = {dY,   S,  (int)x_type, T,  k,     ld_dy,  ld_s,      gamma, (int)w_type,
                               rstd, dS, ld_ds,       dX, ld_dx, dgamma, overwrite, static_cast<float*>(ws)};
   return launch_result(rgs::launch_rms_backward(a, static_cast<cudaStream_t>(stream)), "rms_norm_backward");
@@ -790,7 +790,7 @@ sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_type, int64_t
     CHECK_PTR(Qt);
   }
   CHECK_ELEM_PTR(scale, SKETCH_FP32);
-  if (rows == 128 && rgs::ceil_div(T, 128) * rgs::ceil_div(k, 128) > kMaxDim)
+  if (rgs::ceil_div(T, rows == 1 ? 32 : 128) * rgs::ceil_div(k, 128) > kMaxDim)  // a launch's blocks of threads
     return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld and k=%lld span 2^31 blocks or more", (long long)T, (long long)k);
   const rgs::Quantize a = {X, (int)x_type, T, k, ld_x, rows, Q, ld_q, scale, Qt, ld_qt};
   return launch_result(rgs::launch_quantize(a, static_cast<cudaStream_t>(stream)), "quantize_blocks");

@@ -109,28 +109,32 @@ __global__ void __launch_bounds__(kThreads) rms_dx_wide_kernel(const RmsBackward
   }
 }
 
-// Adds the partial rows: 32 columns per block, the partials dealt over eight warps.
-__global__ void __launch_bounds__(kThreads) rms_grad_sum_kernel(const float* ws, int64_t k, int partials, float* dgamma,
-                                                                int overwrite) {
-  __shared__ float part[kWarps][32];
-  cudaGridDependencySynchronize();
+// Adds the partial rows: 32 columns per block, the partials dealt over 32 warps (over
+// eight, 1021 x 1001 fp32 took 12.1 us in all, not 10).
+constexpr int kGradThreads = 1024;
+__global__ void __launch_bounds__(kGradThreads) rms_grad_sum_kernel(const float* ws, int64_t k, int partials, float* dgamma,
+                                                                    int overwrite) {
+  __shared__ float part[32][33];
+  start_early();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
   if (col < k) {
-#pragma unroll 8
-    for (int p = warp; p < partials; p += kWarps) s += ws[(int64_t)p * k + col];
+#pragma unroll
+    for (int i = 0; i < kMaxPartials / 32; ++i) {
+      const int p = i * 32 + warp;
+      if (p < partials) s += ws[(int64_t)p * k + col];
+    }
   }
   part[warp][lane] = s;
   __syncthreads();
-  if (warp == 0 && col < k) {
-    for (int w = 1; w < kWarps; ++w) s += part[w][lane];
-    dgamma[col] = overwrite ? s : dgamma[col] + s;
-  }
+  s = lane_sum<true>(part[lane][warp], 32);  // warp w joins column w
+  const int64_t mine = (int64_t)blockIdx.x * 32 + warp;
+  if (lane == 0 && mine < k) dgamma[mine] = overwrite ? s : dgamma[mine] + s;
 }
 
 cudaError_t launch_grad_sum(const RmsBackward& a, int partials, cudaStream_t stream) {
-  return launch_early(rms_grad_sum_kernel, ceil_div(a.k, 32), kThreads, 0, stream, (const float*)a.ws, a.k, partials,
+  return launch_early(rms_grad_sum_kernel, ceil_div(a.k, 32), kGradThreads, 0, stream, (const float*)a.ws, a.k, partials,
                       a.dgamma, a.overwrite);
 }
 
@@ -240,15 +244,13 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) rms_forward_
       }
       if constexpr (CODES) {  // what lies past the row's end counts as zeros
         float y[VE];
-        uint32_t top = 0;
 #pragma unroll
         for (int i = 0; i < P; ++i) {
           const float2 f = split(q[i]);
           y[2 * i] = f.x;
           y[2 * i + 1] = f.y;
-          top = max(top, max(magnitude(f.x), magnitude(f.y)));
         }
-        if (!has) top = 0;
+        uint32_t top = has ? top_magnitude(y) : 0;
 #pragma unroll
         for (int o = 64 / VE; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
         float inv;
@@ -269,79 +271,119 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) rms_forward_
   }
 }
 
-// Rows of any alignment: a warp to 128 columns at a time, four to a lane, `G` times; `wpr`
-// (a power of two) warps to a row.
-template <typename X, int G, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 ? (G > 4 ? 2 : 3) : 1) rms_forward_single_kernel(const RmsForward a, int wpr) {
+// Rows of any alignment: a warp to 128 columns at a time, four to a lane, G times; `wpr`
+// (a power of two) warps to a row.  The rows of X and R come through a ring in shared
+// memory, by bulk copies between the 16-byte boundaries around them, and are read there
+// once, element by element (read so from global memory, 32768 x 4095 BF16 with residual
+// and codes took 711 us).
+template <typename X, int G, int THREADS, bool RES>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 ? 2 : 1) rms_forward_ring_kernel(const RmsForward a, const Ring ring, int wpr, int* err) {
+  constexpr int NM = RES ? 2 : 1;
+  extern __shared__ __align__(128) uint8_t ring_mem[];
+  __shared__ __align__(8) uint64_t full[kMaxSlots];
   __shared__ float part[2][THREADS / 32];
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) & (wpr - 1), k = (int)a.k;
-  const int groups = (k + kScaleBlock - 1) / kScaleBlock, rows = THREADS / 32 / wpr;
+  __shared__ volatile int abort_flag;
+  Ring r = ring;
+  r.smem = tc::smem_u32(ring_mem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w = warp & (wpr - 1), k = (int)a.k;
+  const int groups = (k + kScaleBlock - 1) / kScaleBlock;
   const float inv_k = 1.f / (float)k;
-  const int64_t stride = (int64_t)gridDim.x * rows;
+  auto source = [&](const void* p, int64_t ld) {
+    return RowSource{static_cast<const char*>(p), ld * (int64_t)sizeof(X), a.T, (uint32_t)(a.k * sizeof(X))};
+  };
+  RowSource m[NM] = {source(a.X, a.ld_x)};
+  if constexpr (RES) m[NM - 1] = source(a.R, a.ld_r);
+  const int64_t stride = (int64_t)gridDim.x * r.rows, first = (int64_t)blockIdx.x * r.rows;
+  const int passes = first < a.T ? (int)((a.T - first + stride - 1) / stride) : 0;
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < r.slots; ++s) tc::mbar_init(&full[s], 1);
+    tc::fence_mbar_init();
+  }
   start_early();
-  int p = 0;
-  for (int64_t base = (int64_t)blockIdx.x * rows; base < a.T; base += stride, p ^= 1) {
-    const int64_t row = base + (threadIdx.x >> 5) / wpr;
+  __syncthreads();
+  int filled = 0;  // warp 0's: sets whose copies have begun
+  if (warp == 0)
+    for (; filled < passes && filled < r.slots; ++filled)
+      fill_slot<true, false, NM>(r, m, filled, first + filled * stride, &full[filled]);
+  float gamma[G][4];  // a thread's columns stay the same
+#pragma unroll
+  for (int j = 0; j < G; ++j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int c = (j * wpr + w) * kScaleBlock + i * 32 + lane;
+      gamma[j][i] = c < k ? weight(a.gamma, a.w_type, c, 1.f) : 0.f;
+    }
+  }
+  int64_t row = first + warp / wpr;
+  int s = 0;
+  uint32_t ph = 0;
+  for (int p = 0; p < passes; ++p, row += stride) {
+    tc::mbar_wait(&full[s], ph, &abort_flag, err, tc::kErrTimeoutLoad);
+    const uint32_t at = r.smem + (uint32_t)s * r.slot + (uint32_t)(warp / wpr) * r.pitch;
+    uint32_t from[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) from[i] = at + (uint32_t)(i * r.rows) * r.pitch + phase(m[i], row);
     const bool in = row < a.T;
-    const X* x = static_cast<const X*>(a.X) + row * a.ld_x;
-    float f[G][4];
+    float f[G][4], sum = 0.f;
 #pragma unroll
     for (int j = 0; j < G; ++j) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int c = (j * wpr + w) * kScaleBlock + i * 32 + lane;
-        f[j][i] = in && c < k ? (float)__ldcs(x + c) : 0.f;
+        f[j][i] = 0.f;
+        if (in && c < k) {
+          f[j][i] = read_one<X>(from[0] + (uint32_t)(c * sizeof(X)));
+          if constexpr (RES) f[j][i] += read_one<X>(from[NM - 1] + (uint32_t)(c * sizeof(X)));
+        }
+        sum = fmaf(f[j][i], f[j][i], sum);
       }
     }
-    if (a.R) {
-      const X* r = static_cast<const X*>(a.R) + row * a.ld_r;
+    sum = lane_sum<true>(sum, 32);
+    if (lane == 0) part[p & 1][warp] = sum;  // alternates, as in row_sum
+    __syncthreads();
+    if (warp == 0 && filled < passes) {  // every thread has its values of this slot
+      fill_slot<true, false, NM>(r, m, s, first + filled * stride, &full[s]);
+      ++filled;
+    }
+    float js[1] = {part[p & 1][(warp & ~(wpr - 1)) + (lane & (wpr - 1))]};
+    join_sums(js, wpr);
+    const float rstd = 1.f / sqrtf(js[0] * inv_k + a.eps);
+    if (in) {
 #pragma unroll
       for (int j = 0; j < G; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int c = (j * wpr + w) * kScaleBlock + i * 32 + lane;
-          if (in && c < k) f[j][i] += (float)__ldcs(r + c);
-        }
-      }
-    }
-    float sum = 0.f;
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum = fmaf(f[j][i], f[j][i], sum);
-    }
-    const float rstd = 1.f / sqrtf(row_sum(sum, 32 * wpr, part[p]) * inv_k + a.eps);
-    if (!in) continue;
-#pragma unroll
-    for (int j = 0; j < G; ++j) {
-      const int g = j * wpr + w;
-      if (g >= groups) break;
-      float y[4];
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = g * kScaleBlock + i * 32 + lane;
-        y[i] = 0.f;
-        if (c < k) {
-          y[i] = f[j][i] * rstd * weight(a.gamma, a.w_type, c, 1.f);
-          if (a.S) store_one(static_cast<X*>(a.S) + row * a.ld_s + c, f[j][i]);
-          if (a.Y) store_one(static_cast<X*>(a.Y) + row * a.ld_y + c, y[i]);
-        }
-        top = max(top, magnitude(y[i]));
-      }
-      if (a.Q) {
-        float inv;
-        const float scale = code_scale(__reduce_max_sync(0xFFFFFFFFu, top), inv);
-        if (lane == 0) a.scale[row * groups + g] = scale;
+        const int g = j * wpr + w;
+        if (g >= groups) break;
+        float y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int c = g * kScaleBlock + i * 32 + lane;
-          if (c < k) a.Q[row * a.ld_q + c] = (uint8_t)codes2(y[i] * inv, 0.f);
+          y[i] = 0.f;
+          if (c < k) {
+            y[i] = f[j][i] * rstd * gamma[j][i];
+            if (RES && a.S) store_one(static_cast<X*>(a.S) + row * a.ld_s + c, f[j][i]);
+            if (a.Y) store_one(static_cast<X*>(a.Y) + row * a.ld_y + c, y[i]);
+          }
+        }
+        if (a.Q) {
+          float inv;
+          const float scale = code_scale(__reduce_max_sync(0xFFFFFFFFu, top_magnitude(y)), inv);
+          if (lane == 0) a.scale[row * groups + g] = scale;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = g * kScaleBlock + i * 32 + lane;
+            if (c < k) a.Q[row * a.ld_q + c] = (uint8_t)codes2(y[i] * inv, 0.f);
+          }
         }
       }
+      if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
     }
-    if (a.rstd && w == 0 && lane == 0) a.rstd[row] = rstd;
+    if (++s == r.slots) {
+      s = 0;
+      ph ^= 1u;
+    }
   }
+  if (threadIdx.x == 0 && abort_flag) drain(full, r.slots, filled);
 }
 
 constexpr int64_t kMaxRowWidth = 16384;
@@ -360,12 +402,36 @@ cudaError_t forward_vectors(const RmsForward& a, int tpr, cudaStream_t stream) {
   return a.Q ? launch(rms_forward_kernel<X, THREADS, false, true>) : launch(rms_forward_kernel<X, THREADS, false, false>);
 }
 
-template <typename X, int G, int THREADS>
-cudaError_t forward_singles(const RmsForward& a, int wpr, cudaStream_t stream) {
-  int64_t blocks = ceil_div(a.T, THREADS / 32 / wpr);
-  const int64_t most = (int64_t)num_sms() * (THREADS == 256 ? 6 : 2);
-  if (blocks > most) blocks = most;
-  return launch_early(rms_forward_single_kernel<X, G, THREADS>, blocks, THREADS, 0, stream, a, wpr);
+template <typename X, int G, int THREADS, bool RES>
+cudaError_t forward_ring(const RmsForward& a, int wpr, cudaStream_t stream) {
+  constexpr int kPerSm = THREADS == 256 ? 2 : 1;
+  Ring r = {};
+  r.rows = THREADS / 32 / wpr;
+  r.each = 1;
+  r.pitch = (uint32_t)((a.k * sizeof(X) + 15) / 16 * 16 + 16);  // room for the 16-byte boundaries around a row
+  r.slot = r.pitch * (uint32_t)(r.rows * (RES ? 2 : 1));
+  r.slots = (int)(kMostSmem / kPerSm / r.slot);  // at least one: 128 KB for 16384 fp32 values of X and R
+  if (r.slots > kMaxSlots) r.slots = kMaxSlots;
+  int64_t blocks = ceil_div(a.T, r.rows);
+  if (blocks > kPerSm * (int64_t)num_sms()) blocks = kPerSm * (int64_t)num_sms();
+  int* err_word = nullptr;
+  cudaError_t err = device_error_word(&err_word);
+  if (err != cudaSuccess) return err;
+  const size_t smem = (size_t)r.slots * r.slot;
+  auto kernel = rms_forward_ring_kernel<X, G, THREADS, RES>;
+  err = allow_smem(kernel, smem);
+  return err == cudaSuccess ? launch_early(kernel, blocks, THREADS, smem, stream, a, r, wpr, err_word) : err;
+}
+
+template <typename X, bool RES>
+cudaError_t forward_any_place(const RmsForward& a, cudaStream_t stream) {
+  const int64_t groups = ceil_div(a.k, kScaleBlock);
+  if (groups > 64) return forward_ring<X, 8, 512, RES>(a, 16, stream);
+  if (groups > 32) return forward_ring<X, 4, 512, RES>(a, 16, stream);
+  int wpr = 1;
+  while (wpr < 8 && 4 * wpr < groups) wpr *= 2;
+  while (wpr < 8 && wpr < groups && a.T * wpr < 16 * (int64_t)num_sms()) wpr *= 2;
+  return groups <= wpr ? forward_ring<X, 1, 256, RES>(a, wpr, stream) : forward_ring<X, 4, 256, RES>(a, wpr, stream);
 }
 
 template <typename X>
@@ -380,14 +446,7 @@ cudaError_t forward_any(const RmsForward& a, cudaStream_t stream) {
       if (tpr == 512) return forward_vectors<X, 512>(a, tpr, stream);
       return forward_vectors<X, 1024>(a, tpr, stream);
     }
-    const int64_t groups = ceil_div(a.k, kScaleBlock);
-    int wpr = 1;
-    while (wpr < 8 && 8 * wpr < groups) wpr *= 2;
-    while (wpr < 8 && wpr < groups && a.T * wpr < 16 * (int64_t)num_sms()) wpr *= 2;
-    if (groups <= wpr) return forward_singles<X, 1, 256>(a, wpr, stream);
-    if (groups <= 4 * wpr) return forward_singles<X, 4, 256>(a, wpr, stream);
-    if (groups <= 8 * wpr) return forward_singles<X, 8, 256>(a, wpr, stream);
-    return forward_singles<X, 8, 512>(a, 16, stream);
+    return a.R ? forward_any_place<X, true>(a, stream) : forward_any_place<X, false>(a, stream);
   }
   count_launch();
   rms_forward_wide_kernel<X><<<(unsigned)a.T, kThreads, 0, stream>>>(a);

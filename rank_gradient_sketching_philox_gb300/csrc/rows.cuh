@@ -219,13 +219,23 @@ constexpr float kScaleLeast = 1.17549435e-38f;  // 2^-126
 
 // Bits of a magnitude: as integers they are ordered like the numbers, NaN above all.
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+// Bits of the largest magnitude of N values (an even number of them); NaN where one is.
+template <int N>
+__device__ __forceinline__ uint32_t top_magnitude(const float (&x)[N]) {
+  float top = fabsf(x[0]);
+#pragma unroll
+  for (int i = 1; i < N; i += 2)
+    asm("max.NaN.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(fabsf(x[i])), "f"(fabsf(x[i + 1 < N ? i + 1 : i])));
+  return __float_as_uint(top);
+}
 
 // A block's scale from the bits of its largest magnitude, and what its values are
-// multiplied by.
+// multiplied by: an approximate reciprocal, good to 2^-23, where a code's own rounding
+// is 2^-4.  The scale is a normal number, so that the reciprocal is one too.
 __device__ __forceinline__ float code_scale(uint32_t top, float& inv) {
-  float scale = fmaxf(__uint_as_float(top) / 448.f, kScaleLeast);
-  if (top >= 0x7F800000u) scale = __uint_as_float(0x7FC00000u);
-  inv = 1.f / scale;
+  float scale = fmaxf(__uint_as_float(top) * (1.f / 448.f), kScaleLeast);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));
+  if (top >= 0x7F800000u) scale = inv = __uint_as_float(0x7FC00000u);
   return scale;
 }
 // Two values' codes (the first in the low byte), rounded to nearest, ties to even; a
