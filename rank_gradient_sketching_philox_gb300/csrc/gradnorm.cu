@@ -4,8 +4,8 @@
 //   norm = sqrt(sum over all tensors of g^2),  scale = 1 where norm <= max_norm, else max_norm / norm
 //
 // Bound by HBM: the norm reads each gradient once.  The tensors are cut into units of
-// kUnit values, dealt in their order to at most kBlocks blocks, whatever the GPU's size, so
-// that the sums' order depends on the tensors' sizes alone.  A thread adds its 32
+// kUnit values, dealt to at most kBlocks blocks, whatever the GPU's size, so that the
+// sums' order depends on the tensors' sizes alone.  A thread adds its 32
 // squares of a unit in fp32 (four chains), the rest in fp64.  Squares that fp32 cannot
 // hold (sums that overflow, or small ones of values that are not zero) are taken again
 // in fp64, so that the norm is right for every finite gradient.
@@ -21,7 +21,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kEach = 32;                  // values of a unit per thread
 constexpr int kUnit = kThreads * kEach;
-constexpr int kBlocks = 1024;              // partial sums of a launch
+constexpr int kBlocks = 1216;              // partial sums of a launch: eight blocks for each of 152 SMs
+constexpr int kScaleBlocks = 1 << 20;      // of a launch that scales: a unit to each up to 8.6 G values
 constexpr int kTensors = 256;              // per launch
 
 struct GradBatch {
@@ -33,28 +34,22 @@ struct GradBatch {
 // Whether 16-byte vectors of the tensor start on 16 bytes.
 __device__ __forceinline__ bool on_vector(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// The units of block `block` of `blocks`, one after another: f(problem, first value).
-// BACK: the last one first.
+// Every gridDim.x-th unit from this block's first one on, so that the blocks go through
+// the tensors together: f(problem, first value).  BACK: from the last unit.
 template <bool BACK, typename F>
-__device__ __forceinline__ void walk_units(const GradBatch& a, int block, int blocks, F f) {
-  const int64_t units = a.begin[a.n], begin = units * block / blocks, end = units * (block + 1) / blocks;
-  if (begin >= end) return;
-  int64_t u = BACK ? end - 1 : begin;
-  int lo = 0, hi = a.n;  // the last tensor that begins at or before the unit
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.begin[mid] <= u) lo = mid;
-    else hi = mid;
-  }
-  for (int64_t left = end - begin; left > 0; --left) {
-    f(a.p[lo], (u - a.begin[lo]) * kUnit);
-    if constexpr (BACK) {
-      --u;
-      while (lo > 0 && u < a.begin[lo]) --lo;
-    } else {
-      ++u;
-      while (lo + 1 < a.n && u >= a.begin[lo + 1]) ++lo;
+__device__ __forceinline__ void walk_units(const GradBatch& a, F f) {
+  const int64_t units = a.begin[a.n];
+  int lo = 0, hi = a.n;
+  for (int64_t i = blockIdx.x; i < units; i += gridDim.x) {
+    const int64_t u = BACK ? units - 1 - i : i;
+    if (BACK) lo = 0;
+    else hi = a.n;
+    while (hi - lo > 1) {  // the last tensor that begins at or before the unit
+      const int mid = (lo + hi) >> 1;
+      if (a.begin[mid] <= u) lo = mid;
+      else hi = mid;
     }
+    f(a.p[lo], (u - a.begin[lo]) * kUnit);
   }
 }
 
@@ -123,7 +118,7 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
   __shared__ double part[kThreads / 32];
   start_early();
   double sum = 0.0;
-  walk_units<false>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+  walk_units<false>(a, [&](const sketch_grad_problem& p, int64_t first) {
     float v[kEach];
     if (p.type == SKETCH_BF16) load_unit(static_cast<const __nv_bfloat16*>(p.G), p.count, first, v);
     else load_unit(static_cast<const float*>(p.G), p.count, first, v);
@@ -171,12 +166,11 @@ __device__ __forceinline__ void scale_unit(const G* g, G* out, int64_t n, int64_
   }
 }
 
-// Each block walks the units that it has in the norm, but from their end: what that
-// read last is still in L2.
+// From the last unit: what the norm read last is still in L2.
 __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_constant__ GradBatch a, const float* scale) {
   start_early();
   const float s = *scale;
-  walk_units<true>(a, blockIdx.x, gridDim.x, [&](const sketch_grad_problem& p, int64_t first) {
+  walk_units<true>(a, [&](const sketch_grad_problem& p, int64_t first) {
     if (s == 1.f && p.out == p.G) return;
     if (p.type == SKETCH_BF16)
       scale_unit(static_cast<const __nv_bfloat16*>(p.G), static_cast<__nv_bfloat16*>(p.out), p.count, first, s);
@@ -187,7 +181,7 @@ __global__ void __launch_bounds__(kThreads) grad_scale_kernel(const __grid_const
 
 // The launches of a batch, up to kTensors tensors each: f(table, blocks).
 template <typename F>
-cudaError_t for_batches(int n, const sketch_grad_problem* probs, F f) {
+cudaError_t for_batches(int n, const sketch_grad_problem* probs, int most, F f) {
   static thread_local GradBatch a;
   for (int i = 0; i < n;) {
     a.n = 0;
@@ -198,7 +192,7 @@ cudaError_t for_batches(int n, const sketch_grad_problem* probs, F f) {
       ++a.n;
     }
     const int64_t units = a.begin[a.n];
-    const cudaError_t err = f(a, (int)(units < 1 ? 1 : units < kBlocks ? units : kBlocks));
+    const cudaError_t err = f(a, (int)(units < 1 ? 1 : units < most ? units : most));
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -216,7 +210,7 @@ size_t grad_norm_workspace_bytes(int64_t n) {
 cudaError_t launch_grad_norm(int n, const sketch_grad_problem* probs, float max_norm, float* norm, float* scale,
                              double* ws, cudaStream_t stream) {
   int64_t partials = 0;
-  const cudaError_t err = for_batches(n, probs, [&](const GradBatch& a, int blocks) {
+  const cudaError_t err = for_batches(n, probs, kBlocks, [&](const GradBatch& a, int blocks) {
     double* to = ws + partials;
     partials += blocks;
     return launch_early(grad_norm_kernel, blocks, kThreads, 0, stream, a, to);
@@ -226,7 +220,7 @@ cudaError_t launch_grad_norm(int n, const sketch_grad_problem* probs, float max_
 }
 
 cudaError_t launch_grad_scale(int n, const sketch_grad_problem* probs, const float* scale, cudaStream_t stream) {
-  return for_batches(n, probs, [&](const GradBatch& a, int blocks) {
+  return for_batches(n, probs, kScaleBlocks, [&](const GradBatch& a, int blocks) {
     return launch_early(grad_scale_kernel, blocks, kThreads, 0, stream, a, scale);
   });
 }

@@ -144,7 +144,9 @@ cudaError_t launch_grad_sum(const RmsBackward& a, int partials, cudaStream_t str
 // Vector j tpr + t is thread t's j-th, so that 16 neighbouring lanes (BF16; fp32: 32)
 // hold the 128 columns of a scale.
 constexpr int kForwardVectors = 4;
-constexpr int forward_blocks(int threads) { return threads == 256 ? 3 : 1; }
+// Blocks per SM: with the residual two (32768 x 4096 BF16 with codes 191 us, with three
+// 200, with four 199), without it four (BF16 output 85.7 us, with three 89.7, two 105).
+constexpr int forward_blocks(int threads, bool res) { return threads == 256 ? (res ? 2 : 4) : threads == 512 ? 2 : 1; }
 
 // The row's sum from its threads' ones.  `part` alternates between rows: a thread that
 // writes it again has passed the barrier of the row between, after which nobody reads
@@ -165,7 +167,7 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float* part) {
 }
 
 template <typename X, int THREADS, bool RES, bool CODES>
-__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS)) rms_forward_kernel(const RmsForward a, int tpr) {
+__global__ void __launch_bounds__(THREADS, forward_blocks(THREADS, RES)) rms_forward_kernel(const RmsForward a, int tpr) {
   constexpr int VE = 16 / (int)sizeof(X), NV = kForwardVectors, P = VE / 2;
   extern __shared__ __align__(128) float weights[];
   __shared__ float part[2][THREADS / 32];
@@ -392,7 +394,7 @@ template <typename X, int THREADS>
 cudaError_t forward_vectors(const RmsForward& a, int tpr, cudaStream_t stream) {
   const size_t smem = (size_t)a.k * 4;
   int64_t blocks = ceil_div(a.T, THREADS / tpr);
-  const int64_t most = (int64_t)num_sms() * forward_blocks(THREADS);
+  const int64_t most = (int64_t)num_sms() * forward_blocks(THREADS, a.R != nullptr);
   if (blocks > most) blocks = most;
   auto launch = [&](auto kernel) {
     const cudaError_t err = allow_smem(kernel, smem);
