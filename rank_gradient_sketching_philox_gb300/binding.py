@@ -828,9 +828,9 @@ SCALE_BLOCK = 128  # columns, or rows and columns of a weight, that share a scal
 _set_device = torch._C._cuda_exchangeDevice  # returns the one before
 
 
-def _launch(device, fn, *args):
-    """Call the library with ``device`` current, whatever device was."""
-    index = device.index
+def _launch(index, name, *args):
+    """Call the library with device ``index`` current, whatever device was."""
+    fn = getattr(_lib or lib(), name)
     before = _set_device(index)
     try:
         st = fn(*args)
@@ -841,9 +841,13 @@ def _launch(device, fn, *args):
         _check(st)
 
 
-def _check_stream(stream, device):
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream is not one of %s" % device)
+def _stream_on(stream, index):
+    """Handle of the given stream, or of the device's current one."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    if stream.device.index != index:
+        raise ValueError("the stream is not one of cuda:%d" % index)
+    return stream.cuda_stream
 
 
 def code_rows(T, k, device="cuda"):
@@ -852,19 +856,48 @@ def code_rows(T, k, device="cuda"):
     return torch.empty(T, (k + 15) // 16 * 16, dtype=torch.float8_e4m3fn, device=device)[:, :k]
 
 
-def _codes(t, T, k, device, name):
+def _matrix(t, name):
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError("%s must be a 2-D CUDA tensor" % name)
+    return t.shape, t.dtype, t.get_device()
+
+
+def _like(t, shape, dtype, index, name):
+    """Row stride of an activation matrix of this shape and type, on device ``index``."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != index:
+        raise ValueError("%s must be a %d x %d %s matrix on cuda:%d" % (name, *shape, dtype, index))
+    ld, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return ld if shape[0] > 1 else shape[1]
+
+
+def _flat(t, n, dtype, index, name):
+    """Check n contiguous values of ``dtype`` on device ``index``."""
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != index or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous %s tensor of %d values on cuda:%d" % (name, dtype, n, index))
+
+
+def _gamma(t, k, index):
+    if t is None:
+        return DTYPE_FP32
+    _flat(t, k, t.dtype, index, "gamma")
+    return _dtype(t, "gamma")
+
+
+def _codes(t, T, k, index, name):
     """Row stride of a T x k matrix of codes."""
-    if t.dtype != torch.float8_e4m3fn or t.device != device or t.shape != (T, k):
-        raise ValueError("%s must be a %d x %d float8_e4m3fn matrix on %s" % (name, T, k, device))
+    if t.dtype is not torch.float8_e4m3fn or t.get_device() != index or t.shape != (T, k):
+        raise ValueError("%s must be a %d x %d float8_e4m3fn matrix on cuda:%d" % (name, T, k, index))
     ld, unit = t.stride()
     if unit != 1 and k > 1:
         raise ValueError("%s must have unit column stride" % name)
     return ld if T > 1 else (k + 15) // 16 * 16
 
 
-def _scales(t, rows, cols, device, name):
-    if t.dtype != torch.float32 or t.device != device or t.shape != (rows, cols):
-        raise ValueError("%s must be a %d x %d float32 matrix on %s" % (name, rows, cols, device))
+def _scales(t, rows, cols, index, name):
+    if t.dtype is not torch.float32 or t.get_device() != index or t.shape != (rows, cols):
+        raise ValueError("%s must be a %d x %d float32 matrix on cuda:%d" % (name, rows, cols, index))
     return t.stride()
 
 
@@ -878,23 +911,22 @@ def rms_norm_forward(X, gamma, rstd=None, R=None, S=None, Y=None, Q=None, scale=
     y, and Q with scale (T x ceil(k / 128) fp32) y as E4M3 codes with a scale for each
     row's 128 columns; Y or Q is given.  rstd (T fp32) is for the backward pass.  gamma
     (k, BF16 or fp32) may be None."""
+    shape, dtype, dev = _matrix(X, "X")
     x_type = _dtype(X, "X")
-    shape, dtype, dev = _norm_x(X)
     T, k = shape
-    ld_x = _norm_rows(X, shape, dtype, dev, "X")
-    ld_r = 0 if R is None else _norm_rows(R, shape, dtype, dev, "R")
-    ld_s = 0 if S is None else _norm_rows(S, shape, dtype, dev, "S")
-    ld_y = 0 if Y is None else _norm_rows(Y, shape, dtype, dev, "Y")
+    ld_x = _like(X, shape, dtype, dev, "X")
+    ld_r = 0 if R is None else _like(R, shape, dtype, dev, "R")
+    ld_s = 0 if S is None else _like(S, shape, dtype, dev, "S")
+    ld_y = 0 if Y is None else _like(Y, shape, dtype, dev, "Y")
     ld_q = 0 if Q is None else _codes(Q, T, k, dev, "Q")
     if scale is not None:
-        _vector(scale, T * _groups(k), torch.float32, dev, "scale")
-    w_type = _norm_weights(gamma, None, k, dev)
+        _flat(scale, T * _groups(k), torch.float32, dev, "scale")
+    w_type = _gamma(gamma, k, dev)
     if rstd is not None:
-        _vector(rstd, T, torch.float32, dev, "rstd")
-    _check_stream(stream, dev)
-    _launch(dev, lib().sketch_rms_norm_forward, X.data_ptr(), x_type, T, k, ld_x, _addr(R), ld_r, _addr(S),
+        _flat(rstd, T, torch.float32, dev, "rstd")
+    _launch(dev, "sketch_rms_norm_forward", X.data_ptr(), x_type, T, k, ld_x, _addr(R), ld_r, _addr(S),
             ld_s, _addr(gamma), w_type, eps, _addr(Y), ld_y, _addr(Q), ld_q, _addr(scale), _addr(rstd),
-            _stream_of(stream, dev))
+            _stream_on(stream, dev))
     return Y if Y is not None else Q
 
 
@@ -902,24 +934,23 @@ def rms_norm_backward(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, overwri
     """dX (may be dY or dS) and dgamma (k fp32; replaced with overwrite, else added
     to) of rms_norm_forward; each may be None.  dS: the gradient that reaches S
     from the rest of the stream, added to dX, which is the gradient of X and of R."""
+    shape, dtype, dev = _matrix(S, "S")
     x_type = _dtype(S, "S")
-    shape, dtype, dev = _norm_x(S)
     T, k = shape
-    ld_s, ld_dy = _norm_rows(S, shape, dtype, dev, "S"), _norm_rows(dY, shape, dtype, dev, "dY")
-    ld_ds = 0 if dS is None else _norm_rows(dS, shape, dtype, dev, "dS")
-    ld_dx = 0 if dX is None else _norm_rows(dX, shape, dtype, dev, "dX")
-    w_type = _norm_weights(gamma, None, k, dev)
-    _vector(rstd, T, torch.float32, dev, "rstd")
+    ld_s, ld_dy = _like(S, shape, dtype, dev, "S"), _like(dY, shape, dtype, dev, "dY")
+    ld_ds = 0 if dS is None else _like(dS, shape, dtype, dev, "dS")
+    ld_dx = 0 if dX is None else _like(dX, shape, dtype, dev, "dX")
+    w_type = _gamma(gamma, k, dev)
+    _flat(rstd, T, torch.float32, dev, "rstd")
     if dgamma is not None:
-        _vector(dgamma, k, torch.float32, dev, "dgamma")
-    _check_stream(stream, dev)
+        _flat(dgamma, k, torch.float32, dev, "dgamma")
     keep = ws_at = None
     nbytes = 0
     if dgamma is not None:
-        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, dev, stream, ws)
-    _launch(dev, lib().sketch_rms_norm_backward, dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
+        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, S.device, stream, ws)
+    _launch(dev, "sketch_rms_norm_backward", dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
             _addr(gamma), w_type, rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
-            1 if overwrite else 0, ws_at, nbytes, _stream_of(stream, dev))
+            1 if overwrite else 0, ws_at, nbytes, _stream_on(stream, dev))
     return dX
 
 
@@ -928,16 +959,15 @@ def quantize_blocks(X, Q, scale, rows=1, Qt=None, stream=None):
     or with rows=128 (weights) for each 128 rows and 128 columns; scale:
     ceil(T / rows) x ceil(k / 128) fp32.  Qt (k x T, rows=128 only): the same codes transposed,
     with scales scale.t(); Q may then be None."""
+    shape, dtype, dev = _matrix(X, "X")
     x_type = _dtype(X, "X")
-    shape, dtype, dev = _norm_x(X)
     T, k = shape
-    ld_x = _norm_rows(X, shape, dtype, dev, "X")
+    ld_x = _like(X, shape, dtype, dev, "X")
     ld_q = 0 if Q is None else _codes(Q, T, k, dev, "Q")
     ld_qt = 0 if Qt is None else _codes(Qt, k, T, dev, "Qt")
-    _vector(scale, (T + rows - 1) // rows * _groups(k) if rows > 0 else 0, torch.float32, dev, "scale")
-    _check_stream(stream, dev)
-    _launch(dev, lib().sketch_quantize_blocks, X.data_ptr(), x_type, T, k, ld_x, rows, _addr(Q), ld_q,
-            scale.data_ptr(), _addr(Qt), ld_qt, _stream_of(stream, dev))
+    _flat(scale, (T + rows - 1) // rows * _groups(k) if rows > 0 else 0, torch.float32, dev, "scale")
+    _launch(dev, "sketch_quantize_blocks", X.data_ptr(), x_type, T, k, ld_x, rows, _addr(Q), ld_q,
+            scale.data_ptr(), _addr(Qt), ld_qt, _stream_on(stream, dev))
     return Q
 
 
@@ -946,11 +976,8 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
     128)), B (N x k) with b_scale (ceil(N / 128) x ceil(k / 128), any strides).  A layer's output
     takes B = Q of its weight W and b_scale = scale, its input's gradient B = Qt
     and b_scale = scale.t().  Y (T x N) BF16, or fp32, which overwrite=False adds to."""
-    dev = A.device
-    if not A.is_cuda or A.dim() != 2 or B.dim() != 2 or Y.dim() != 2:
-        raise ValueError("A, B and Y must be 2-D CUDA tensors")
-    T, k = A.shape
-    N = B.shape[0]
+    (T, k), _, dev = _matrix(A, "A")
+    N = _matrix(B, "B")[0][0]
     ld_a, ld_b = _codes(A, T, k, dev, "A"), _codes(B, N, k, dev, "B")
     ld_as, unit = _scales(a_scale, T, _groups(k), dev, "a_scale")
     if unit != 1 and _groups(k) > 1:
@@ -959,13 +986,12 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
         ld_as = _groups(k)
     bs_row, bs_col = _scales(b_scale, _groups(N), _groups(k), dev, "b_scale")
     y_type = _dtype(Y, "Y")
-    if Y.shape != (T, N) or Y.device != dev or (N > 1 and Y.stride(1) != 1):
-        raise ValueError("Y must be a %d x %d matrix on %s with unit column stride" % (T, N, dev))
-    ld_y = Y.stride(0) if T > 1 else (N + 7) // 8 * 8
-    _check_stream(stream, dev)
-    _launch(dev, lib().sketch_matmul_blocks, A.data_ptr(), T, k, ld_a, a_scale.data_ptr(), ld_as, B.data_ptr(),
+    ld_y = _like(Y, (T, N), Y.dtype, dev, "Y")
+    if T == 1:
+        ld_y = (N + 7) // 8 * 8
+    _launch(dev, "sketch_matmul_blocks", A.data_ptr(), T, k, ld_a, a_scale.data_ptr(), ld_as, B.data_ptr(),
             N, ld_b, b_scale.data_ptr(), bs_row, bs_col, Y.data_ptr(), y_type, ld_y, 1 if overwrite else 0,
-            _stream_of(stream, dev))
+            _stream_on(stream, dev))
     return Y
 
 
@@ -990,24 +1016,22 @@ def grad_problems(Gs, outs=None):
 def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=None):
     """norm = sqrt(sum of squares over the tensors of grad_problems), and scale = 1
     where norm <= max_norm, else max_norm / norm (one-element fp32 tensors)."""
-    dev = norm.device
     if not norm.is_cuda:
         raise ValueError("norm must be a CUDA tensor")
-    _vector(norm, 1, torch.float32, dev, "norm")
+    dev = norm.get_device()
+    _flat(norm, 1, torch.float32, dev, "norm")
     if scale is not None:
-        _vector(scale, 1, torch.float32, dev, "scale")
-    _check_stream(stream, dev)
-    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, dev, stream, ws)
-    _launch(dev, lib().sketch_grad_norm_batched, len(probs), probs, max_norm, norm.data_ptr(), _addr(scale),
-            ws_at, nbytes, _stream_of(stream, dev))
+        _flat(scale, 1, torch.float32, dev, "scale")
+    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, norm.device, stream, ws)
+    _launch(dev, "sketch_grad_norm_batched", len(probs), probs, max_norm, norm.data_ptr(), _addr(scale),
+            ws_at, nbytes, _stream_on(stream, dev))
     return norm
 
 
 def grad_scale_batched(probs, scale, stream=None):
     """out = G * scale for the tensors of grad_problems; scale: a one-element fp32 tensor."""
-    dev = scale.device
     if not scale.is_cuda:
         raise ValueError("scale must be a CUDA tensor")
-    _vector(scale, 1, torch.float32, dev, "scale")
-    _check_stream(stream, dev)
-    _launch(dev, lib().sketch_grad_scale_batched, len(probs), probs, scale.data_ptr(), _stream_of(stream, dev))
+    dev = scale.get_device()
+    _flat(scale, 1, torch.float32, dev, "scale")
+    _launch(dev, "sketch_grad_scale_batched", len(probs), probs, scale.data_ptr(), _stream_on(stream, dev))

@@ -336,18 +336,19 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
 // each CTA add the others, times their scales, to the tile's sums in registers: 128
 // columns of a row to a thread.
 constexpr int kTile = 256;
-constexpr int kTileStages = 5;
+constexpr int kTileStages = 4;
 constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
 constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;    // copies, MMAs, scales, an idle warp; sums
 constexpr int kSumCols = 128;                         // of a thread
 constexpr int kLoads = kSumCols / 16;                 // from TMEM, of 16 columns
-// Registers: the launch has 168 for each thread, 384 * 168 = 128 * 88 + 256 * 208; with
-// fewer for the first the waits of the copies and MMAs spill (72: 312 us, 56: 355).
-constexpr int kFewRegisters = 88, kSumRegisters = 208;
+// Registers: the launch has 168 for each thread, 384 * 168 = 128 * 120 + 256 * 192; with
+// fewer for the first, 8192 x 12288 x 4096 takes longer (104: 298 us, 88: 313, 72: 334; 120: 294).
+constexpr int kFewRegisters = 120, kSumRegisters = 192;
 constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
+constexpr int kBoxes = 4;                             // of a warp: a BF16 tile's part leaves without a wait
 constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
-constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxBytes + 1024;
+constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxes * kBoxBytes + 1024;
 constexpr int kGroupM = 16;                           // tile rows walked together
 
 // acc += f * (16 columns in v), while the next 16 columns come from TMEM into w.  One
@@ -397,7 +398,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __shared__ __align__(8) uint64_t tempty_bar[4];           // the even CTA's: both CTAs have read them
   __shared__ __align__(8) uint64_t scale_bar[2];  // each CTA's: the scales of some groups are there
   __shared__ __align__(8) uint64_t read_bar[2];   // each CTA's: its sums' warps have read them
-  __shared__ float a_scales[2][kScaleGroups][128], b_scales[2][kScaleGroups][2];
+  __shared__ float scales[2][kScaleGroups][2][128];  // of a row, times those of the tile's two column blocks
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile int issued, consumed[2];
@@ -519,7 +520,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
     if (lane == 0) consumed[warp >> 1] = it;
   } else if (warp == 2) {
-    // ---- scales: of the CTA's 128 rows and of the tile's two column blocks ----
+    // ---- scales: of the CTA's 128 rows, times those of the tile's two column blocks ----
     int batch = 0;
     bool live = true;
     for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
@@ -529,19 +530,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const int row = m0 + 128 * (int)rank + lane;
 #pragma unroll
       for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as : nullptr;
-      const int col = n0 + (lane & 1) * kScaleBlock;
-      const float* bs = lane < 2 && col < a.N ? a.b_scale + (int64_t)(col / kScaleBlock) * a.bs_row : nullptr;
+      const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row;
+      const bool second = n0 + kScaleBlock < a.N;
       for (int c0 = 0; c0 < a.chunks && live; c0 += kScaleGroups, ++batch) {
         const int slot = batch & 1;
 #pragma unroll
         for (int half = 0; half < kScaleGroups; half += kScaleGroups / 2) {
-          float sa[kScaleGroups / 2][4], sb[kScaleGroups / 2];
+          float sa[kScaleGroups / 2][4], sb[kScaleGroups / 2][2];
 #pragma unroll
           for (int j = 0; j < kScaleGroups / 2; ++j) {
             const int c = c0 + half + j;
 #pragma unroll
             for (int i = 0; i < 4; ++i) sa[j][i] = as[i] && c < a.chunks ? as[i][c] : 0.f;
-            sb[j] = bs && c < a.chunks ? bs[c * a.bs_col] : 0.f;
+            sb[j][0] = c < a.chunks ? bs[c * a.bs_col] : 0.f;
+            sb[j][1] = second && c < a.chunks ? bs[a.bs_row + c * a.bs_col] : 0.f;
           }
           if (half == 0 && batch >= 2)
             live = tc::mbar_wait(&read_bar[slot], ((batch >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
@@ -550,8 +552,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 #pragma unroll
           for (int j = 0; j < kScaleGroups / 2; ++j) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) a_scales[slot][half + j][32 * i + lane] = sa[j][i];
-            if (lane < 2) b_scales[slot][half + j][lane] = sb[j];
+            for (int i = 0; i < 4; ++i) {
+              scales[slot][half + j][0][32 * i + lane] = sa[j][i] * sb[j][0];
+              scales[slot][half + j][1][32 * i + lane] = sa[j][i] * sb[j][1];
+            }
           }
         }
         if (!live) break;
@@ -569,9 +573,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
     const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0) + 8u * half;
     const uint32_t tfull0 = tc::smem_u32(tfull_bar) + 8u * half;
-    const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * kBoxBytes;
-    const uint32_t sa0 = tc::smem_u32(a_scales) + (uint32_t)(quarter * 32 + lane) * 4u;
-    const uint32_t sb0 = tc::smem_u32(b_scales) + 4u * half;
+    const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * (kBoxes * kBoxBytes);
+    const uint32_t scale0 = tc::smem_u32(scales) + half * 512u + (uint32_t)(quarter * 32 + lane) * 4u;
     uint32_t b = 0, ph = 0;  // accumulators of the next group, and their barriers' parity
     uint32_t slot = 0, slot_ph = 0;
     bool live = true;
@@ -584,8 +587,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       for (int i = 0; i < kSumCols / 2; ++i) acc[i / 8][i % 8] = 0;
       // A wait that gives up makes all later ones give up too; that is looked at once in
       // eight groups.
-      auto group = [&](uint32_t sa, uint32_t sb) {
-        const float f = tc::lds_f32(sa) * tc::lds_f32(sb);
+      auto group = [&](uint32_t scale) {
+        const float f = tc::lds_f32(scale);
         const Pair f2 = pair(f, f);
         live = tc::mbar_wait(tfull0 + 16u * b, ph, &abort_flag, a.err, tc::kErrTimeoutMma) && live;
         __syncwarp();  // the loads are the whole warp's
@@ -609,11 +612,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       };
       for (int c = 0; c < a.chunks; c += kScaleGroups) {
         live = tc::mbar_wait(&scale_bar[slot], slot_ph, &abort_flag, a.err, tc::kErrTimeoutStage) && live;
-        const uint32_t sa = sa0 + slot * (kScaleGroups * 512u), sb = sb0 + slot * (kScaleGroups * 8u);
+        const uint32_t scale = scale0 + slot * (kScaleGroups * 1024u);
         const int n = a.chunks - c;
 #pragma unroll
         for (uint32_t j = 0; j < kScaleGroups; ++j)
-          if ((int)j < n) group(sa + j * 512u, sb + j * 8u);
+          if ((int)j < n) group(scale + j * 1024u);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&read_bar[slot]);
         slot ^= 1u;
@@ -625,10 +628,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle; a row's last values
       // singly where they do not fill 16 bytes, which TMA would write whole
       const bool fp32 = a.y_type == SKETCH_FP32;
-      const uint32_t mine = box + (uint32_t)lane * 64u, swizzle = (uint32_t)(lane >> 1) & 3u;
-      auto send = [&](int c, const uint4(&w)[4]) {
-        if (lane == 0) tc::bulk_wait_read<0>();  // the box's last copy has left
-        __syncwarp();
+      const uint32_t swizzle = (uint32_t)(lane >> 1) & 3u;
+      auto send = [&](int c, int at, const uint4(&w)[4]) {  // in box `at` of the warp's
+        const uint32_t to = box + (uint32_t)(at % kBoxes) * kBoxBytes, mine = to + (uint32_t)lane * 64u;
+        if (at % kBoxes == 0) {  // the boxes' last copies have left
+          if (lane == 0) tc::bulk_wait_read<0>();
+          __syncwarp();
+        }
 #pragma unroll
         for (uint32_t j = 0; j < 4; ++j) tc::sts128(mine + ((j ^ swizzle) << 4), w[j]);
         tc::fence_proxy_async_smem();
@@ -636,8 +642,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (a.N - c < (fp32 ? 16 : 32) && (a.N & (fp32 ? 3 : 7)) != 0) {
           if (row0 + lane < a.T) put_end(a, row0 + lane, c, mine, swizzle);
         } else if (lane == 0 && row0 < a.T && c < a.N) {
-          if (fp32 && !a.overwrite) tc::tma_add_2d(&a.tmY, box, c, row0);
-          else tc::tma_store_2d_at(&a.tmY, box, c, row0);
+          if (fp32 && !a.overwrite) tc::tma_add_2d(&a.tmY, to, c, row0);
+          else tc::tma_store_2d_at(&a.tmY, to, c, row0);
           tc::bulk_commit();
         }
       };
@@ -656,7 +662,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             }
             w[j] = make_uint4(r[0], r[1], r[2], r[3]);
           }
-          send(col0 + 32 * h, w);
+          send(col0 + 32 * h, h, w);
         }
       } else {
 #pragma unroll
@@ -666,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             const float2 lo = split(acc[h][2 * j]), hi = split(acc[h][2 * j + 1]);
             w[j] = make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y), __float_as_uint(hi.x), __float_as_uint(hi.y));
           }
-          send(col0 + 16 * h, w);
+          send(col0 + 16 * h, h, w);
         }
       }
     }
