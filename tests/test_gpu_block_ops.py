@@ -592,6 +592,46 @@ def test_captured_and_replayed():
         assert all(torch.equal(a, b) for a, b in zip(a_step(other), out))
 
 
+def test_the_example_runs_with_these_operators():
+    from rank_gradient_sketching_philox_gb300 import train_example
+    losses = train_example.main(["--steps", "3", "--tokens", "200", "--norm", "rms", "--products", "8bit", "--clip", "0.5"])
+    assert len(losses) == 3 and all(math.isfinite(x) for x in losses)
+
+
+@pytest.mark.parametrize("products", ["bf16", "8bit"])
+def test_the_examples_gradients(products):
+    """A microbatch's gradients of the stream, through every norm and product, against autograd in 64 bits."""
+    from rank_gradient_sketching_philox_gb300 import train_example
+    model = train_example.Model(vocabulary=64, width=128, blocks=2, rank=16, norm="rms", products=products)
+    g = gen(20)
+    for n in model.norms:
+        n.gamma.copy_(1 + normal(g, 128, std=0.2))
+    rgs.sample_projection_batched(rgs.PROJ_GAUSSIAN_QR, 0, 0, [m.P for m in model.linears[:-1]], [m.layer for m in model.linears[:-1]])
+    rgs.sample_projection(rgs.PROJ_GAUSSIAN_QR, 0, model.head.layer, 0, model.head.P)
+    tokens = torch.randint(0, 64, (96,), generator=g, device="cuda")
+    targets = torch.randint(0, 64, (96,), generator=g, device="cuda")
+    losses = model.microbatch(tokens, targets, True, 1.0 / 96)
+    leaf = lambda t: t.double().requires_grad_()  # noqa: E731
+    E, gammas = leaf(model.embedding), [leaf(n.gamma) for n in model.norms]
+
+    def rms(x, gamma):
+        return x * (x.square().mean(1, keepdim=True) + 1e-6).rsqrt() * gamma
+
+    x = E[tokens]
+    for gamma, (up, down) in zip(gammas, model.pairs):
+        # relu's pieces are the model's own: a value that a rounding moves across zero would change a whole term
+        x = x + torch.where(up.active, rms(x, gamma) @ up.W.double().t(), 0.0) @ down.W.double().t()
+    want = torch.nn.functional.cross_entropy(rms(x, gammas[-1]) @ model.head.W.double().t(), targets, reduction="none")
+    want.mean().backward()
+    # Roundings of activations and derivatives on the way: in BF16 some twenty of 2^-8 at most each; in 8 bits sixteen
+    # more of 2^-4 (eight products, each with two operands).  As independent errors they add up as squares, a uniform
+    # one of half-width e to e / sqrt(3): sqrt(20) 2^-8 / sqrt(3) = 0.010 and sqrt(16) 2^-4 / sqrt(3) = 0.144; doubled,
+    # since not all are independent.
+    most = 2 * (0.010 if products == "bf16" else 0.144)
+    for got, exact in [(losses, want.detach()), (model.dembedding, E.grad)] + [(n.dgamma, q.grad) for n, q in zip(model.norms, gammas)]:
+        assert float((got.double() - exact).norm() / exact.norm()) < most
+
+
 def test_workspaces_are_checked_and_need_no_zeros():
     g, T, k = gen(14), 500, 264
     s, dy, rstd = normal(g, T, k).to(BF), normal(g, T, k).to(BF), torch.ones(T, device="cuda")
