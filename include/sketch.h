@@ -449,7 +449,8 @@ SKETCH_API sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem*
  * contiguous, the block's largest magnitude over 448 (at least 2^-126).  A block that
  * holds an infinity or a NaN has a NaN scale and NaN codes.  gamma: k contiguous
  * values of w_type, or NULL (ones).  rstd (T fp32, nullable) is for the backward pass.
- * All sums are fp32: S's rounding does not enter Y, nor Y's Q.  T, k >= 1; eps >= 0. */
+ * All sums are fp32: S's rounding does not enter Y, nor Y's Q; a row whose squares
+ * pass fp32's range has rstd 0.  T, k >= 1; eps >= 0. */
 SKETCH_API sketch_status sketch_rms_norm_forward(const void* X, sketch_dtype x_type, int64_t T, int64_t k, int64_t ld_x,
                                                  const void* R, int64_t ld_r, void* S, int64_t ld_s,
                                                  const void* gamma, sketch_dtype w_type, float eps, void* Y,
@@ -494,7 +495,8 @@ SKETCH_API sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_ty
  * multiple of 8.  overwrite = 1 replaces Y, 0 adds to an fp32 Y; a BF16 Y is always
  * replaced.  T, N and k are at most 2^24 each, T and N spanning at most 2^28
  * tiles of 256 x 256 (else SKETCH_ERR_UNSUPPORTED).  A block's products add up in fp32
- * on the tensor cores, the blocks in fp32.  Y must not overlap an input. */
+ * on the tensor cores, the blocks in fp32; where an fp32 Y is added to, subnormal sums
+ * may become zeros.  Y must not overlap an input. */
 SKETCH_API sketch_status sketch_matmul_blocks(const uint8_t* A, int64_t T, int64_t k, int64_t ld_a,
                                               const float* a_scale, int64_t ld_as, const uint8_t* B, int64_t N,
                                               int64_t ld_b, const float* b_scale, int64_t bs_row, int64_t bs_col,

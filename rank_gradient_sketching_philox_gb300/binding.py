@@ -1010,7 +1010,16 @@ def grad_problems(Gs, outs=None):
         _vector(G, G.numel(), None, dev, "G")
         _vector(out, G.numel(), G.dtype, dev, "out")
         probs[i] = GradProblem(G.data_ptr(), out.data_ptr(), G.numel(), _dtype(G, "G"))
+    probs.tensors = Gs, outs  # kept as long as the table
     return probs
+
+
+def _problems_on(probs, index):
+    """Number of a table's tensors, which lie on device ``index``."""
+    tensors = getattr(probs, "tensors", None)
+    if tensors is not None and tensors[0][0].get_device() != index:
+        raise ValueError("the tensors of the table are not on cuda:%d" % index)
+    return len(probs)
 
 
 def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=None):
@@ -1022,8 +1031,9 @@ def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=Non
     _flat(norm, 1, torch.float32, dev, "norm")
     if scale is not None:
         _flat(scale, 1, torch.float32, dev, "scale")
-    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, len(probs), 0, 0, 0, norm.device, stream, ws)
-    _launch(dev, "sketch_grad_norm_batched", len(probs), probs, max_norm, norm.data_ptr(), _addr(scale),
+    n = _problems_on(probs, dev)
+    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, n, 0, 0, 0, norm.device, stream, ws)
+    _launch(dev, "sketch_grad_norm_batched", n, probs, max_norm, norm.data_ptr(), _addr(scale),
             ws_at, nbytes, _stream_on(stream, dev))
     return norm
 
@@ -1034,4 +1044,4 @@ def grad_scale_batched(probs, scale, stream=None):
         raise ValueError("scale must be a CUDA tensor")
     dev = scale.get_device()
     _flat(scale, 1, torch.float32, dev, "scale")
-    _launch(dev, "sketch_grad_scale_batched", len(probs), probs, scale.data_ptr(), _stream_on(stream, dev))
+    _launch(dev, "sketch_grad_scale_batched", _problems_on(probs, dev), probs, scale.data_ptr(), _stream_on(stream, dev))

@@ -124,11 +124,12 @@ __global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_ker
     cudaGridDependencySynchronize();
     for (int i = 0; i < early; ++i) fetch(i, i);  // while the others set up
   }
+  cudaGridDependencySynchronize();
   if (warp == 1) tc::tmem_alloc(&tmem_slot, few_columns(TN));
-  start_early();
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t tmem = tmem_slot;
   Pair acc[kCols / 2];
 #pragma unroll
@@ -424,10 +425,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
     tc::fence_mbar_init();
   }
+  cudaGridDependencySynchronize();
   if (warp == 0) tc::tmem_alloc_pair(&tmem_slot, 512);
-  start_early();
   tc::tc_fence_before();
   __syncthreads();
+  cudaTriggerProgrammaticLaunchCompletion();
   tc::cluster_sync();  // both CTAs' barriers exist before either signals one
   tc::tc_fence_after();
   const uint32_t tmem = tmem_slot;
@@ -707,6 +709,11 @@ cudaError_t tile_pairs(int* out) {
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
   if (pairs[dev] == 0) {
+    // what the warpgroups take must be there, or they would wait for it forever
+    cudaFuncAttributes f;
+    err = cudaFuncGetAttributes(&f, matmul8_tile_kernel);
+    if (err != cudaSuccess) return err;
+    if (f.numRegs * kTileThreads < 128 * kFewRegisters + 32 * kSumWarps * kSumRegisters) return cudaErrorInvalidConfiguration;
     err = cudaFuncSetAttribute(matmul8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};

@@ -291,7 +291,9 @@ cudaError_t launch_early(void (*kernel)(Params...), int64_t blocks, int threads,
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 // The other half, at a kernel's start: the kernel after this one may come up as blocks
-// leave; the one before has ended.
+// leave; the one before has ended.  A kernel that takes TMEM takes it between the two: it
+// holds none while it waits for the kernel before, which may still want some, and nothing
+// after it comes up before it has its own.
 __device__ __forceinline__ void start_early() {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();

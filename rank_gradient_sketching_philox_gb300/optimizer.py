@@ -71,7 +71,7 @@ class GradClip:
     1 where norm <= max_norm, else max_norm / norm, one-element fp32 tensors that
     the host does not wait for: ``AdamW.step(..., grad_scale=clip.scale)``.  With
     ``outs`` (tensors of the same sizes and types, or the gradients themselves) it
-    also writes the scaled gradients there.  The object is bound to its tensors
+    also writes the scaled gradients there.  Before the first step norm and scale hold nothing.  The object is bound to its tensors
     and keeps the call's workspace, so its steps are ordered on one stream.
     """
 
@@ -83,8 +83,8 @@ class GradClip:
             raise ValueError("max_norm must be finite and > 0, got %r" % (max_norm,))
         self._problems = binding.grad_problems(self.grads, self.outs)
         dev = self.grads[0].device
-        self.norm = torch.zeros(1, dtype=torch.float32, device=dev)
-        self.scale = torch.ones(1, dtype=torch.float32, device=dev)
+        self.norm = torch.empty(1, dtype=torch.float32, device=dev)
+        self.scale = torch.empty(1, dtype=torch.float32, device=dev)
         self._ws = torch.empty(binding.workspace_bytes(binding.OP_GRAD_NORM, len(self.grads)), dtype=torch.uint8,
                                device=dev)
 

@@ -416,6 +416,57 @@ def test_matmul_padding_and_values_that_are_not_finite(T):
     assert torch.equal(bad[keep], Y[keep])
 
 
+@pytest.mark.parametrize("T,N,k", [(5, 100, 300), (70, 100, 300), (1501, 515, 130)])
+def test_matmul_scales_of_any_strides_and_rows_behind(T, N, k):
+    """a_scale with rows apart, b_scale one value for all blocks; Y's rows from T on stay."""
+    g = gen(15)
+    A, sa, B, _ = operands(g, T, N, k)
+    apart = torch.full((T, groups(k) + 3), math.nan, device="cuda")
+    apart[:, :groups(k)] = sa
+    one = torch.full((1, 1), 0.25, device="cuda")
+    for dtype in (BF, F32):
+        Y = torch.full((T + 40, 520), 7.0, dtype=dtype, device="cuda")
+        rgs.matmul_blocks(A, apart[:, :groups(k)], B, one.expand(groups(N), groups(k)), Y[:T, :N])
+        check_product(A, sa, B, one.expand(groups(N), groups(k)).contiguous(), Y[:T, :N])
+        assert bool((Y[T:] == 7.0).all()) and bool((Y[:, N:] == 7.0).all())
+
+
+def test_offsets_past_32_bits():
+    """Matrices and gradients of more than 2^31 values, looked at where they end."""
+    T, N, k = 66000, 33000, 128
+    A, sa, B, sb = operands(gen(16), T, N, k)
+    Y = torch.empty(T, N, dtype=BF, device="cuda")
+    rgs.matmul_blocks(A, sa, B, sb, Y)
+    check_product(A[-300:], sa[-300:], B, sb, Y[-300:])
+    del A, B
+    X = Y.view(66000, 33000)
+    Q, scale = rgs.code_rows(T, N), torch.empty(T, groups(N), device="cuda")
+    rgs.quantize_blocks(X, Q, scale)
+    check_codes(Q[-50:], scale[-50:], X[-50:].double(), 1, 0.0)
+    tiles, Qt = torch.empty(groups(T), groups(N), device="cuda"), rgs.code_rows(N, T)
+    rgs.quantize_blocks(X, Q, tiles, rows=128, Qt=Qt)
+    check_codes(Q[-80:], tiles[-1:], X[-80:].double(), 128, 0.0)
+    assert torch.equal(Qt[:, -80:].t().float(), Q[-80:].float())
+    del Qt, Q
+    for k in (16384, 33000):  # rows in registers; rows read twice
+        T = Y.numel() // k
+        X = Y.view(-1)[:T * k].view(T, k)
+        O, rstd = torch.empty_like(X), torch.empty(T, device="cuda")
+        rgs.rms_norm_forward(X, None, rstd, Y=O)
+        check_forward(X[-9:], None, None, 1e-6, None, O[-9:], None, None, rstd[-9:])
+        dX = torch.empty_like(X)
+        rgs.rms_norm_backward(O, X, None, rstd, dX=dX)
+        check_backward(O[-9:], X[-9:], None, rstd[-9:], None, dX[-9:], None)
+        del dX, O
+    X.fill_(0.5)
+    X.view(-1)[-3:] = 4096.0
+    clip = rgs.GradClip([X], 1.0, outs=[X])
+    clip.step()
+    want = math.sqrt(0.25 * (X.numel() - 3) + 3 * 4096.0 ** 2)
+    assert float(clip.norm) == pytest.approx(want, rel=8 * U)
+    assert float(X.view(-1)[-1]) == pytest.approx(4096.0 / want, rel=2.0 ** -8)
+
+
 @pytest.mark.parametrize("T", [4, 500])
 def test_layer_and_its_input_gradient(T):
     """The path as a layer uses it: norm into 8 bits, product; derivatives into 8 bits, product with the transposed weight."""
