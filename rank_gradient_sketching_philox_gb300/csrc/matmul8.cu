@@ -278,15 +278,20 @@ __global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_ker
   if (warp == 1) tc::tmem_dealloc(tmem, few_columns(TN));
 }
 
-// Clusters' size for `tiles` tiles: the one with the fewest groups one after another,
-// over the rounds that the CTAs take; of a tie's two the smaller one.
+// Clusters' size for `tiles` tiles, and the groups one after another, over the rounds that
+// the CTAs take.  As many CTAs as the GPU holds at once (in two rounds 64 x 12288 x 4096
+// takes 25 us, with clusters of 3 beside each other 14.8), not five to seven to a cluster
+// (clusters of 6 do not all fit beside each other: 32 x 6144 x 2048 takes 15.9 us with
+// them, 6.9 with 4), and more where that saves three groups at least (16 x 2048 x 2048:
+// 4.3 us with 4, 4.9 with 8; 16 x 1024 x 4096: 5.7 and 4.6).
 unsigned few_split(int64_t tiles, int chunks, int64_t* steps) {
   const int64_t slots = (int64_t)num_sms() * kFewResident;
   unsigned S = 1;
-  *steps = INT64_MAX;
-  for (int s = 1; s <= 8 && s <= chunks; ++s) {
-    const int64_t n = ceil_div(tiles * s, slots) * ceil_div(chunks, s);
-    if (n < *steps) {
+  *steps = ceil_div(tiles, slots) * chunks;
+  for (int s : {2, 3, 4, 8}) {
+    if (s > chunks || tiles * s > slots) break;
+    const int64_t n = ceil_div(chunks, s);
+    if (n + 3 <= *steps) {
       *steps = n;
       S = (unsigned)s;
     }
