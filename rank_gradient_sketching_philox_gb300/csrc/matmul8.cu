@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_ker
     int s = 0, b = 0;
     uint32_t ph = 0, bph = 0;
     for (int i = 0; i < n_mine; ++i) {
-      if (!tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
-      if (i >= kBuffers && !tc::mbar_wait(&tempty_bar[b], bph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) break;
+      bool live = tc::mbar_wait(&full_bar[s], ph, &abort_flag, a.err, tc::kErrTimeoutLoad);
+      if (i >= kBuffers) live = tc::mbar_wait(&tempty_bar[b], bph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage) && live;
+      if (!__all_sync(0xFFFFFFFFu, live)) break;
       tc::tc_fence_after();
       const uint32_t sa = tc::smem_u32(smem + (size_t)s * kStageBytes);
       if (tc::elect_one()) {
@@ -340,7 +341,9 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
 // Pairs of CTAs (cta_group::2) on 256 x 256 tiles, persistent.  A group's MMAs fill two
 // of four accumulators in TMEM (256 x 128 each, 512 columns in all) while eight warps of
 // each CTA add the others, times their scales, to the tile's sums in registers: 128
-// columns of a row to a thread.
+// columns of a row to a thread.  Where there are few tiles, a cluster of several pairs
+// takes one, each pair a part of its groups; the parts meet in shared memory and are
+// added in the pairs' order.
 constexpr int kTile = 256;
 constexpr int kTileStages = 4;
 constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
@@ -356,6 +359,7 @@ constexpr int kBoxes = 4;                             // of a warp: a BF16 tile'
 constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
 constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxes * kBoxBytes + 1024;
 constexpr int kGroupM = 16;                           // tile rows walked together
+constexpr int kMostPairs = 4;                         // of a cluster
 
 // acc += f * (16 columns in v), while the next 16 columns come from TMEM into w.  One
 // piece, so that nothing touches w between the load and its wait.
@@ -394,8 +398,10 @@ __device__ __noinline__ void put_end(const Product8& a, int64_t row, int col, ui
   }
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
-    matmul8_tile_kernel(const __grid_constant__ Product8 a) {
+// SPLIT: clusters of several pairs (one kernel for both took 307 us for 8192 x 12288 x
+// 4096, not 296).
+template <bool SPLIT>
+__global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __grid_constant__ Product8 a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ __align__(8) uint64_t full_bar[kTileStages];   // the even CTA's: both CTAs' rows have landed
@@ -410,8 +416,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __shared__ volatile int issued, consumed[2];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = tc::cluster_ctarank();
-  const int n_pairs = (int)gridDim.x >> 1, items = a.m_tiles * a.n_tiles;
+  uint32_t ctas = 2;
+  if constexpr (SPLIT) asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  // the CTA in its pair, the pair's even CTA, the pair's part of a tile's groups
+  const uint32_t in_cluster = tc::cluster_ctarank(), rank = in_cluster & 1u, even = SPLIT ? in_cluster & ~1u : 0u;
+  const uint16_t both = (uint16_t)(3u << even);
+  const int pairs = SPLIT ? (int)ctas >> 1 : 1, part = (int)even >> 1;
+  const int c0 = (int)((int64_t)a.chunks * part / pairs), chunks = (int)((int64_t)a.chunks * (part + 1) / pairs) - c0;
+  const int first_item = (int)(blockIdx.x / ctas), step = (int)(gridDim.x / ctas), items = a.m_tiles * a.n_tiles;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     issued = 0;
@@ -453,19 +465,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     // ---- copies: this CTA's half of each operand's rows ----
     // The whole warp walks, one thread issues: what it needs stays in uniform registers,
     // and a stage takes it less than its MMAs' 512 cycles beside the sums' warps.
-    const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), 0);  // the even CTA's
+    const uint32_t full0 = tc::mapa_shared(tc::smem_u32(full_bar), even);  // the even CTA's
     const uint32_t mine0 = tc::smem_u32(full_bar), empty0 = tc::smem_u32(empty_bar), stage0 = tc::smem_u32(smem);
     int s = 0, it = 0;
     uint32_t ph = 0;
     bool stop = false;
-    for (int item = (int)blockIdx.x >> 1; item < items && !stop; item += n_pairs) {
+    for (int item = first_item; item < items && !stop; item += step) {
       int m0, n0;
       place(item, m0, n0);
       const int ar = m0 + 128 * (int)rank, br = n0 + 64 * (int)rank;  // of each 128 columns, half from each CTA
-      for (int c = 0; c < a.chunks; ++c, ++it) {
-        if (it >= kTileStages && !tc::mbar_wait(empty0 + 8u * s, ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage)) {
-          stop = true;
-          break;
+      for (int c = c0; c < c0 + chunks; ++c, ++it) {
+        if (it >= kTileStages) {
+          stop = !tc::mbar_wait(empty0 + 8u * s, ph ^ 1u, &abort_flag, a.err, tc::kErrTimeoutStage);
+          stop = __any_sync(0xFFFFFFFFu, stop);
+          if (stop) break;
         }
         const uint32_t st = stage0 + (uint32_t)s * kTileStageBytes, bar = full0 + 8u * s;
         if (tc::elect_one()) {
@@ -480,7 +493,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           ph ^= 1u;
         }
       }
-      stop = __any_sync(0xFFFFFFFFu, stop);
     }
     if (lane == 0) issued = it;
   } else if ((warp & 1) && rank == 0) {
@@ -494,30 +506,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t b0 = (uint32_t)(warp & 2);  // the first of this warp's two accumulators
     const uint32_t full0 = tc::smem_u32(full_bar), tempty0 = tc::smem_u32(tempty_bar) + 8u * b0;
     int total = 0;
-    for (int item = (int)blockIdx.x >> 1; item < items; item += n_pairs) total += a.chunks;
+    for (int item = first_item; item < items; item += step) total += chunks;
     int s = warp >> 1, it = warp >> 1;
     uint32_t ph = 0, tph = 1;
     bool live = true;
     for (; it < total; it += 2) {
-      if (!tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad)) break;
+      live = tc::mbar_wait(full0 + 8u * s, ph, &abort_flag, a.err, tc::kErrTimeoutLoad) && live;
       const uint32_t al = (uint32_t)ad0 + (uint32_t)s * (kTileStageBytes >> 4);
       const uint32_t bl = (uint32_t)bd0 + (uint32_t)s * (kTileStageBytes >> 4);
 #pragma unroll
       for (uint32_t h = 0; h < 2; ++h) {
-        if (it >= 2 && live) live = tc::mbar_wait(tempty0 + 8u * h, tph, &abort_flag, a.err, tc::kErrTimeoutStage);
-        if (!live) break;
+        if (it >= 2) live = tc::mbar_wait(tempty0 + 8u * h, tph, &abort_flag, a.err, tc::kErrTimeoutStage) && live;
+        __syncwarp();
         tc::tc_fence_after();
         if (tc::elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < kChunk / 32; ++kk)
             tc::mma_e4m3_pair(tmem + (b0 + h) * (kTile / 2), al + kk * 2, a_hi, bl + h * (kRowsBytes / 2 >> 4) + kk * 2,
                               b_hi, idesc, kk > 0);
-          tc::mma_commit_pair(&tfull_bar[b0 + h]);
-          if (h == 1) tc::mma_commit_pair(&empty_bar[s]);
+          tc::mma_commit_pair(&tfull_bar[b0 + h], both);
+          if (h == 1) tc::mma_commit_pair(&empty_bar[s], both);
         }
         __syncwarp();
       }
-      if (!live) break;
+      // a wait that gives up makes all later ones give up too; looked at now and then (each
+      // time, 8192 x 12288 x 4096 took 303 us, not 296)
+      if ((it & 14) == 14 && !__all_sync(0xFFFFFFFFu, live)) break;
       tph ^= 1u;
       s += 2;
       if (s >= kTileStages) {
@@ -525,32 +539,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         ph ^= 1u;
       }
     }
-    if (lane == 0) consumed[warp >> 1] = it;
+    if (lane == 0 && live) consumed[warp >> 1] = it;
   } else if (warp == 2) {
     // ---- scales: of the CTA's 128 rows, times those of the tile's two column blocks ----
     int batch = 0;
     bool live = true;
-    for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
+    for (int item = first_item; item < items && live; item += step) {
       int m0, n0;
       place(item, m0, n0);
       const float* as[4];
       const int row = m0 + 128 * (int)rank + lane;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as : nullptr;
-      const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row;
+      for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as + c0 : nullptr;
+      const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row + c0 * a.bs_col;
       const bool second = n0 + kScaleBlock < a.N;
-      for (int c0 = 0; c0 < a.chunks && live; c0 += kScaleGroups, ++batch) {
+      for (int first = 0; first < chunks && live; first += kScaleGroups, ++batch) {
         const int slot = batch & 1;
 #pragma unroll
         for (int half = 0; half < kScaleGroups; half += kScaleGroups / 2) {
           float sa[kScaleGroups / 2][4], sb[kScaleGroups / 2][2];
 #pragma unroll
           for (int j = 0; j < kScaleGroups / 2; ++j) {
-            const int c = c0 + half + j;
+            const int c = first + half + j;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sa[j][i] = as[i] && c < a.chunks ? as[i][c] : 0.f;
-            sb[j][0] = c < a.chunks ? bs[c * a.bs_col] : 0.f;
-            sb[j][1] = second && c < a.chunks ? bs[a.bs_row + c * a.bs_col] : 0.f;
+            for (int i = 0; i < 4; ++i) sa[j][i] = as[i] && c < chunks ? as[i][c] : 0.f;
+            sb[j][0] = c < chunks ? bs[c * a.bs_col] : 0.f;
+            sb[j][1] = second && c < chunks ? bs[a.bs_row + c * a.bs_col] : 0.f;
           }
           if (half == 0 && batch >= 2)
             live = tc::mbar_wait(&read_bar[slot], ((batch >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
@@ -578,14 +592,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t half = (uint32_t)(warp - 4) >> 2;
     const int col = (int)half * kSumCols;
     const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)col;
-    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), 0) + 8u * half;
+    const uint32_t tempty0 = tc::mapa_shared(tc::smem_u32(tempty_bar), even) + 8u * half;
     const uint32_t tfull0 = tc::smem_u32(tfull_bar) + 8u * half;
     const uint32_t box = tc::smem_u32(smem) + kTileStages * kTileStageBytes + (uint32_t)(warp - 4) * (kBoxes * kBoxBytes);
     const uint32_t scale0 = tc::smem_u32(scales) + half * 512u + (uint32_t)(quarter * 32 + lane) * 4u;
     uint32_t b = 0, ph = 0;  // accumulators of the next group, and their barriers' parity
     uint32_t slot = 0, slot_ph = 0;
     bool live = true;
-    for (int item = (int)blockIdx.x >> 1; item < items && live; item += n_pairs) {
+    for (int item = first_item; item < items && live; item += step) {
       int m0, n0;
       place(item, m0, n0);
       const int row0 = m0 + 128 * (int)rank + quarter * 32, col0 = n0 + col;
@@ -617,10 +631,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         b ^= 1u;
         ph ^= b ^ 1u;
       };
-      for (int c = 0; c < a.chunks; c += kScaleGroups) {
+      for (int c = 0; c < chunks; c += kScaleGroups) {
         live = tc::mbar_wait(&scale_bar[slot], slot_ph, &abort_flag, a.err, tc::kErrTimeoutStage) && live;
         const uint32_t scale = scale0 + slot * (kScaleGroups * 1024u);
-        const int n = a.chunks - c;
+        const int n = chunks - c;
 #pragma unroll
         for (uint32_t j = 0; j < kScaleGroups; ++j)
           if ((int)j < n) group(scale + j * 1024u);
@@ -630,6 +644,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         slot_ph ^= slot ^ 1u;
         live = __all_sync(0xFFFFFFFFu, live);
         if (!live) break;
+      }
+      if constexpr (SPLIT) {
+        // the part to where the stages were, 16 bytes of a row's 1024 at 16 (i ^ row % 8);
+        // every warp has seen the last MMAs' end (or given up)
+        tc::named_barrier(1, 32 * kSumWarps);
+        if (!live) break;
+        const uint32_t to = tc::smem_u32(smem) + (uint32_t)(quarter * 32 + lane) * 1024u + half * 512u;
+#pragma unroll
+        for (uint32_t i = 0; i < kSumCols / 4; ++i) {
+          const float2 lo = split(acc[i / 4][2 * (i % 4)]), hi = split(acc[i / 4][2 * (i % 4) + 1]);
+          tc::sts128(to + ((i ^ ((uint32_t)lane & 7u)) << 4), make_uint4(__float_as_uint(lo.x), __float_as_uint(lo.y),
+                                                                        __float_as_uint(hi.x), __float_as_uint(hi.y)));
+        }
+        break;
       }
       if (!live) break;
       // to Y, 64 bytes of 32 rows at a time, in TMA's 64-byte swizzle; a row's last values
@@ -703,46 +731,82 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __syncthreads();
   tc::cluster_sync();  // neither CTA leaves while the other may still signal it
   if (warp == 0) tc::tmem_dealloc_pair(tmem, 512);
+  if constexpr (!SPLIT) return;
+  // ---- the parts' sum: a share of the CTA's 128 rows for each pair ----
+  int m0, n0;
+  place(first_item, m0, n0);
+  const int row_end = 128 * (part + 1) / pairs;
+  const uint32_t from = tc::smem_u32(smem);
+  for (int e = 128 * part / pairs * 64 + (int)threadIdx.x; e < row_end * 64; e += kTileThreads) {
+    const int r = e >> 6, i = e & 63, row = m0 + 128 * (int)rank + r, col = n0 + 4 * i;
+    if (row >= a.T || col >= a.N) continue;
+    const uint32_t at = from + (uint32_t)r * 1024u + (uint32_t)((i ^ (r & 7)) << 4);
+    float4 v[kMostPairs];
+#pragma unroll
+    for (int q = 0; q < kMostPairs; ++q) {
+      v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (q < pairs) v[q] = tc::ld_dsmem_f4(tc::mapa_shared(at, 2u * (uint32_t)q + rank));
+    }
+#pragma unroll
+    for (int q = 1; q < kMostPairs; ++q)
+      v[0] = make_float4(v[0].x + v[q].x, v[0].y + v[q].y, v[0].z + v[q].z, v[0].w + v[q].w);
+    if (!abort_flag) put4(a, row, col, v[0]);
+  }
+  tc::cluster_sync();  // no CTA leaves while its part may still be read
 }
 
-// CTA pairs that the device holds at once (its SMs need not all pair up).
-cudaError_t tile_pairs(int* out) {
+cudaLaunchConfig_t tile_config(int clusters, int pairs, cudaStream_t stream, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (unsigned)(clusters * pairs), 1, 1);
+  cfg.blockDim = dim3(kTileThreads, 1, 1);
+  cfg.dynamicSmemBytes = kTileSmem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2 * (unsigned)pairs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+// Clusters of 1 to kMostPairs pairs that the device holds at once (its SMs need not all
+// find a place in one).
+cudaError_t tile_clusters(int (&out)[kMostPairs + 1]) {
   constexpr int kMaxDevices = 64;
-  static std::atomic<int> pairs[kMaxDevices];
+  static std::atomic<int> known[kMaxDevices][kMostPairs + 1];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
-  if (pairs[dev] == 0) {
-    // what the warpgroups take must be there, or they would wait for it forever
-    cudaFuncAttributes f;
-    err = cudaFuncGetAttributes(&f, matmul8_tile_kernel);
-    if (err != cudaSuccess) return err;
-    if (f.numRegs * kTileThreads < 128 * kFewRegisters + 32 * kSumWarps * kSumRegisters) return cudaErrorInvalidConfiguration;
-    err = cudaFuncSetAttribute(matmul8_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2 * (unsigned)num_sms(), 1, 1);
-    cfg.blockDim = dim3(kTileThreads, 1, 1);
-    cfg.dynamicSmemBytes = kTileSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    err = cudaOccupancyMaxActiveClusters(&n, matmul8_tile_kernel, &cfg);
-    if (err != cudaSuccess) return err;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    pairs[dev] = n;
+  if (known[dev][1] == 0) {
+    for (auto kernel : {matmul8_tile_kernel<false>, matmul8_tile_kernel<true>}) {
+      // what the warpgroups take must be there, or they would wait for it forever
+      cudaFuncAttributes f;
+      err = cudaFuncGetAttributes(&f, kernel);
+      if (err != cudaSuccess) return err;
+      if (f.numRegs * kTileThreads < 128 * kFewRegisters + 32 * kSumWarps * kSumRegisters) return cudaErrorInvalidConfiguration;
+      err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTileSmem);
+      if (err != cudaSuccess) return err;
+    }
+    for (int p = kMostPairs; p >= 1; --p) {  // the first entry last: it says that all are there
+      cudaLaunchAttribute attr[2];
+      cudaLaunchConfig_t cfg = tile_config(num_sms(), p, nullptr, attr);
+      cfg.numAttrs = 1;
+      int n = 0;
+      err = cudaOccupancyMaxActiveClusters(&n, p > 1 ? matmul8_tile_kernel<true> : matmul8_tile_kernel<false>, &cfg);
+      if (err != cudaSuccess) return err;
+      if (n < 1 && p == 1) return cudaErrorInvalidConfiguration;
+      known[dev][p] = n;
+    }
   }
-  *out = pairs[dev];
+  for (int p = 1; p <= kMostPairs; ++p) out[p] = known[dev][p];
   return cudaSuccess;
 }
 
-cudaError_t launch_tiles(Product8& p, int pairs, const MatmulBlocks& a, cudaStream_t stream) {
+cudaError_t launch_tiles(Product8& p, int clusters, int pairs, const MatmulBlocks& a, cudaStream_t stream) {
   cudaError_t err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
   if (err == cudaSuccess)
     err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 64);
@@ -752,8 +816,10 @@ cudaError_t launch_tiles(Product8& p, int pairs, const MatmulBlocks& a, cudaStre
   if (err != cudaSuccess) return err;
   p.m_tiles = (int)ceil_div(a.T, kTile);
   p.n_tiles = (int)ceil_div(a.N, kTile);
-  const int items = p.m_tiles * p.n_tiles;
-  return launch_early(matmul8_tile_kernel, 2 * (items < pairs ? items : pairs), kTileThreads, kTileSmem, stream, p);
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = tile_config(clusters, pairs, stream, attr);
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, pairs > 1 ? matmul8_tile_kernel<true> : matmul8_tile_kernel<false>, p);
 }
 
 }  // namespace
@@ -777,17 +843,27 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   if (a.T <= 16) return launch_few<16>(p, a, stream);
   if (a.T <= 32) return launch_few<32>(p, a, stream);
   // Which takes less, in us as measured: few tokens' kernel 5 and 0.85 for each group one
-  // after another, the pairs of CTAs 5 and 0.37 for each group and 1.5 for each further
-  // round of tiles.  4096 x 4096 with 192 tokens 14.7 against 16.7, with 256 18.5
-  // against 16.8; 12288 x 4096 with 64 14.8 against 16.3, with 96 25 against 16.5.
-  int pairs = 0;
-  err = tile_pairs(&pairs);
+  // after another; the pairs of CTAs 5 and 0.37 for each group, 1.5 for each further round
+  // of tiles, and 1.5 more for the join where several pairs share a tile (each two groups
+  // at least).
+  int fit[kMostPairs + 1];
+  err = tile_clusters(fit);
   if (err != cudaSuccess) return err;
+  const int64_t items = ceil_div(a.T, kTile) * ceil_div(a.N, kTile);
+  const int64_t rounds = ceil_div(items, fit[1]);
+  double best = 0.37 * (double)(rounds * p.chunks) + 1.5 * (double)(rounds - 1);
+  int pairs = 1;
+  for (int q = 2; q <= kMostPairs && 2 * q <= p.chunks; ++q) {
+    const double us = 0.37 * (double)ceil_div(p.chunks, q) + 1.5;
+    if (items <= fit[q] && us < best) {
+      best = us;
+      pairs = q;
+    }
+  }
   int64_t steps;
   few_split(ceil_div(a.T, 64) * ceil_div(a.N, 128), p.chunks, &steps);
-  const int64_t rounds = ceil_div(ceil_div(a.T, kTile) * ceil_div(a.N, kTile), pairs);
-  if (0.85 * (double)steps <= 0.37 * (double)(rounds * p.chunks) + 1.5 * (double)(rounds - 1)) return launch_few<64>(p, a, stream);
-  return launch_tiles(p, pairs, a, stream);
+  if (0.85 * (double)steps <= best) return launch_few<64>(p, a, stream);
+  return launch_tiles(p, (int)(pairs > 1 || items < fit[1] ? items : fit[1]), pairs, a, stream);
 }
 
 }  // namespace rgs

@@ -425,12 +425,13 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t d_tmem, uint32_t a_lo, ui
       "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Arrive on `bar` at this offset in both CTAs when the MMAs issued so far complete.
-__device__ __forceinline__ void mma_commit_pair(uint64_t* bar) {
+// Arrive on `bar` at this offset in both CTAs (a bit for each of the cluster's) when the
+// MMAs issued so far complete.
+__device__ __forceinline__ void mma_commit_pair(uint64_t* bar, uint16_t ctas = 3) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"((uint16_t)3)
+      "h"(ctas)
       : "memory");
 }
 // Load a tile into this CTA's shared memory, completing on a barrier of either
