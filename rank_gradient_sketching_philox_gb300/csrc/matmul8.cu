@@ -33,6 +33,7 @@ struct Product8 {
   int y_type, overwrite;
   int T, N, chunks;
   int stages, m_tiles, n_tiles;
+  int first, items;  // tiles of a launch of many tokens' kernel
   int* err;
 };
 
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
   const uint16_t both = (uint16_t)(3u << even);
   const int pairs = SPLIT ? (int)ctas >> 1 : 1, part = (int)even >> 1;
   const int c0 = (int)((int64_t)a.chunks * part / pairs), chunks = (int)((int64_t)a.chunks * (part + 1) / pairs) - c0;
-  const int first_item = (int)(blockIdx.x / ctas), step = (int)(gridDim.x / ctas), items = a.m_tiles * a.n_tiles;
+  const int first_item = (int)(blockIdx.x / ctas), step = (int)(gridDim.x / ctas), items = a.items;
   if (threadIdx.x == 0) {
     abort_flag = 0;
     issued = 0;
@@ -452,6 +453,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
   const uint32_t tmem = tmem_slot;
   // first row and column of a tile
   auto place = [&](int item, int& m0, int& n0) {
+    item += a.first;
     const int per_group = kGroupM * a.n_tiles, g = item / per_group, rem = item - g * per_group;
     const int left = a.m_tiles - g * kGroupM, gm = left < kGroupM ? left : kGroupM;
     const int n = rem / gm;
@@ -806,16 +808,10 @@ cudaError_t tile_clusters(int (&out)[kMostPairs + 1]) {
   return cudaSuccess;
 }
 
-cudaError_t launch_tiles(Product8& p, int clusters, int pairs, const MatmulBlocks& a, cudaStream_t stream) {
-  cudaError_t err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
-  if (err == cudaSuccess)
-    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 64);
-  const uint32_t size = a.y_type == SKETCH_BF16 ? 2 : 4;
-  if (err == cudaSuccess)
-    err = make_tmap_out_2d(&p.tmY, a.y_type, a.Y, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)a.ld_y * size, 64 / size, 32);
-  if (err != cudaSuccess) return err;
-  p.m_tiles = (int)ceil_div(a.T, kTile);
-  p.n_tiles = (int)ceil_div(a.N, kTile);
+// Tiles [first, first + items), `pairs` pairs to each, `clusters` at once.
+cudaError_t launch_tiles(Product8& p, int first, int items, int clusters, int pairs, cudaStream_t stream) {
+  p.first = first;
+  p.items = items;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = tile_config(clusters, pairs, stream, attr);
   count_launch();
@@ -844,17 +840,20 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   if (a.T <= 32) return launch_few<32>(p, a, stream);
   // Which takes less, in us as measured: few tokens' kernel 5 and 0.85 for each group one
   // after another; the pairs of CTAs 5 and 0.37 for each group, 1.5 for each further round
-  // of tiles, and 1.5 more for the join where several pairs share a tile (each two groups
-  // at least).
+  // of tiles, and 4 more for the join where several pairs share a tile (two groups or
+  // more each).  4096 x 4096 with 64 tokens 9.6 against 12.9, with 192 15.9 against 13.4;
+  // 12288 x 4096 with 64 16.1 against 17.3, with 96 25 against 17.7; 4096 x 12288 with
+  // 256 tokens 21.7 with three pairs to a tile, 42 with one.
   int fit[kMostPairs + 1];
   err = tile_clusters(fit);
   if (err != cudaSuccess) return err;
-  const int64_t items = ceil_div(a.T, kTile) * ceil_div(a.N, kTile);
-  const int64_t rounds = ceil_div(items, fit[1]);
-  double best = 0.37 * (double)(rounds * p.chunks) + 1.5 * (double)(rounds - 1);
+  p.m_tiles = (int)ceil_div(a.T, kTile);
+  p.n_tiles = (int)ceil_div(a.N, kTile);
+  const int items = p.m_tiles * p.n_tiles, rounds = (int)ceil_div(items, fit[1]);
+  double best = 0.37 * ((double)rounds * p.chunks) + 1.5 * (rounds - 1);
   int pairs = 1;
   for (int q = 2; q <= kMostPairs && 2 * q <= p.chunks; ++q) {
-    const double us = 0.37 * (double)ceil_div(p.chunks, q) + 1.5;
+    const double us = 0.37 * (double)ceil_div(p.chunks, q) + 4.0;
     if (items <= fit[q] && us < best) {
       best = us;
       pairs = q;
@@ -863,7 +862,27 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   int64_t steps;
   few_split(ceil_div(a.T, 64) * ceil_div(a.N, 128), p.chunks, &steps);
   if (0.85 * (double)steps <= best) return launch_few<64>(p, a, stream);
-  return launch_tiles(p, (int)(pairs > 1 || items < fit[1] ? items : fit[1]), pairs, a, stream);
+  err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
+  if (err == cudaSuccess)
+    err = make_tmap_u8_2d(&p.tmB, a.B, (uint64_t)a.k, (uint64_t)a.N, (uint64_t)a.ld_b, kChunk, 64);
+  const uint32_t size = a.y_type == SKETCH_BF16 ? 2 : 4;
+  if (err == cudaSuccess)
+    err = make_tmap_out_2d(&p.tmY, a.y_type, a.Y, (uint64_t)a.N, (uint64_t)a.T, (uint64_t)a.ld_y * size, 64 / size, 32);
+  if (err != cudaSuccess) return err;
+  if (pairs > 1) return launch_tiles(p, 0, items, items, pairs, stream);
+  // The last round's tiles, where they are few: two or more pairs to each in a launch of
+  // their own, which costs some 18 us (4096 x 5120 x 16384 268 us without, 253 with;
+  // 4096 x 4096 x 12288 163 and 160; 4096 x 4096 x 6144 85 and 91).
+  const int whole = items / fit[1] * fit[1], last = items - whole;
+  if (whole > 0 && last > 0) {
+    int q = kMostPairs;
+    while (q > 1 && last > fit[q]) --q;
+    if (q > 1 && 0.4 * (double)(p.chunks - ceil_div(p.chunks, q)) > 18.0) {
+      err = launch_tiles(p, 0, whole, fit[1], 1, stream);
+      return err == cudaSuccess ? launch_tiles(p, whole, last, last, q, stream) : err;
+    }
+  }
+  return launch_tiles(p, 0, items, items < fit[1] ? items : fit[1], 1, stream);
 }
 
 }  // namespace rgs

@@ -369,7 +369,7 @@ def test_matmul(T, N, k, dtype):
 
 @pytest.mark.parametrize("T,N,k", [(16, 4096, 4096), (3, 300, 16384), (600, 4096, 1024), (2500, 2056, 1000), (5000, 1000, 260),
                                    (20000, 40, 72), (40, 20000, 72), (5001, 5001, 2100), (300, 9000, 5000), (1999, 1021, 130),
-                                   (256, 2048, 4096), (511, 1027, 3000), (513, 2049, 2500), (700, 300, 16384), (260, 520, 1300)])
+                                   (256, 2048, 4096), (511, 1027, 3000), (513, 2049, 2500), (700, 300, 16384), (260, 520, 1300), (2560, 2100, 16400)])
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_matmul_larger(T, N, k, dtype):
     A, sa, B, sb = operands(gen(T), T, N, k)
