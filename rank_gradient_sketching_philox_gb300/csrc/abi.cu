@@ -790,7 +790,7 @@ sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_type, int64_t
     CHECK_PTR(Qt);
   }
   CHECK_ELEM_PTR(scale, SKETCH_FP32);
-  if (rgs::ceil_div(T, rows == 1 ? 32 : 128) * rgs::ceil_div(k, 128) > kMaxDim)  // a launch's blocks of threads
+  if (rgs::ceil_div(T, rows == 1 ? 16 : 128) * rgs::ceil_div(k, 128) > kMaxDim)  // a launch's blocks of threads
     return fail(SKETCH_ERR_UNSUPPORTED, "T=%lld and k=%lld span 2^31 blocks or more", (long long)T, (long long)k);
   const rgs::Quantize a = {X, (int)x_type, T, k, ld_x, rows, Q, ld_q, scale, Qt, ld_qt};
   return launch_result(rgs::launch_quantize(a, static_cast<cudaStream_t>(stream)), "quantize_blocks");
