@@ -8,21 +8,23 @@
 // another; each group's result is read back, multiplied by its scales and added up in
 // fp32 registers, groups in their order.
 //
-// What bounds it, one GB300.  Many tokens: the groups' way back.  8192 x 12288 x 4096
-// (T x N x k) takes 296 to 302 us, 2.75 PFLOP/s, and in a long run of passes, at the power
-// limit, 325 to 339; a library product with one scale for each matrix takes 221 and 244.  The
-// tensor cores are busy for 63 % of the time.  The same kernel without the sums takes 222 us, without their multiply-adds 272: a group's
-// MMAs take 512 cycles, and in that time eight warps have to wait for them, read 256
-// columns of 128 rows from TMEM, add them and hand the accumulator back, over some 1200
-// cycles of latency from one CTA to the other.  What hid most of that: an arrival on the
-// other CTA's barrier without a release to the cluster (870 -> 395 us), the scales through
-// shared memory, whole warps that walk the issuing loops (363 -> 352), four accumulators
-// and two MMA warps with the loads from TMEM beside the sums (352 -> 302).  Tried and
-// dropped: 16 warps of 64 columns (345), an arrival of one thread for a CTA (397 of then
-// 366), registers for 64 columns at a time (371 to 437), the next group's scales or
-// barrier looked at ahead (318 to 353).  Few tokens: B's bytes and the start: 16 x
-// 4096 x 4096 7.2 us on the device, of which 2.5 are its 17 MB, 16 x 12288 x 4096 13.5
-// (50 MB, 7.4); a call takes 8 to 10.
+// What bounds it, one GB300.  Many tokens: the sums.  8192 x 12288 x 4096 (T x N x k)
+// takes 296 to 302 us, 2.75 PFLOP/s, and in a long run of passes, at the power limit, 325
+// to 339; a library product with one scale for each matrix takes 221 and 244.  The tensor
+// cores are busy for 63 % of the time.  The same kernel without the sums takes 222 us,
+// without their multiply-adds 272: a group's MMAs take 512 cycles, and in that time eight
+// warps have to see their end, read 256 columns of 128 rows from TMEM, add them, times
+// their scales, and hand the accumulators back, which takes them some 800.  What brought
+// it there: an arrival on the other CTA's barrier without a release to the cluster (870
+// -> 395 us), the scales through shared memory, whole warps that walk the issuing loops
+// (363 -> 352), four accumulators and two MMA warps with the loads from TMEM beside the
+// sums (352 -> 302).  Tried and dropped: 16 warps of 64 columns (345), an arrival of one
+// thread for a CTA (397 of then 366), pieces of 32 columns (297, but 4096 x 4096 x 12288
+// 179 for 164) or 64 (371 to 437), the next group's scales or barrier looked at ahead
+// (318 to 353), scales by asynchronous copies (308).
+//
+// Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.2 us on the device, of which 2.5
+// are its 17 MB, 16 x 12288 x 4096 13.5 (50 MB, 7.4); a call takes 8 to 10.
 #include <cuda_bf16.h>
 
 #include <atomic>
