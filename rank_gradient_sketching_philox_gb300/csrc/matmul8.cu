@@ -94,6 +94,10 @@ constexpr int few_cols(int TN) { return TN <= 32 ? TN : TN / 2; }
 constexpr int few_warps(int TN) { return 4 * (TN / few_cols(TN)); }
 constexpr int few_threads(int TN) { return 64 + 32 * few_warps(TN); }  // copies, MMAs, sums
 constexpr int kFewResident = 2;                                        // CTAs per SM
+// Shared memory of a launch, whatever it needs (105 KB at most): so much that an SM never
+// holds more CTAs than TMEM has columns for.  One that waited for columns while its cluster
+// holds some on another SM could wait for a cluster that waits for those.
+constexpr size_t kFewSmem = 110u << 10;
 constexpr uint32_t few_stage_bytes(int TN) { return kRowsBytes + TN * kChunk; }
 
 template <int TN>
@@ -333,15 +337,13 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
   p.stages = (int)ceil_div(p.chunks, S);
   const int most = (int)((104u << 10) / kStageBytes);
   if (p.stages > most) p.stages = most;
-  size_t smem = (size_t)p.stages * kStageBytes;
-  if (smem < (size_t)TN * 512) smem = (size_t)TN * 512;  // a part of the sum
-  smem += 1024;
-  err = allow_smem(matmul8_few_kernel<TN>, smem);
+  static_assert(104u << 10 <= kFewSmem - 1024 && TN * 512 <= kFewSmem - 1024, "stages, and a part of the sum");
+  err = allow_smem(matmul8_few_kernel<TN>, kFewSmem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
   cfg.blockDim = dim3(few_threads(TN), 1, 1);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = kFewSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;

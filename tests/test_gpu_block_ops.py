@@ -629,6 +629,24 @@ def test_on_two_streams_at_once():
         assert all(torch.equal(a, b) for a, b in zip(w, o))
 
 
+def test_products_on_many_streams_at_once():
+    """Clusters of several sizes and pairs of CTAs beside each other, which share the SMs' TMEM."""
+    shapes = [(8, 2048, 2048), (24, 1024, 4096), (48, 3000, 1000), (16, 300, 512), (200, 2048, 2048), (700, 1024, 1024)]
+    work = []
+    for i, (T, N, k) in enumerate(shapes):
+        ops = operands(gen(30 + i), T, N, k)
+        want = torch.empty(T, (N + 7) // 8 * 8, dtype=BF, device="cuda")[:, :N]
+        rgs.matmul_blocks(*ops, want)
+        work.append((ops, want, torch.zeros(T, (N + 7) // 8 * 8, dtype=BF, device="cuda")[:, :N], torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for ops, _, Y, stream in work:
+            rgs.matmul_blocks(*ops, Y, stream=stream)
+    torch.cuda.synchronize()
+    for _, want, Y, _ in work:
+        assert torch.equal(Y, want)
+
+
 def test_captured_and_replayed():
     a_step(a_state(3))
     s = a_state(3)
