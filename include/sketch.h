@@ -525,7 +525,8 @@ SKETCH_API sketch_status sketch_grad_norm_batched(int n, const sketch_grad_probl
                                                   void* stream);
 
 /* out = G * scale (a device scalar), rounded once to the tensor's type.  Where out is G
- * and the scale is 1, nothing is read or written. */
+ * and the scale is 1, nothing is read or written.  No out overlaps another out, or a G
+ * that is not it: blocks of one launch would race for it. */
 SKETCH_API sketch_status sketch_grad_scale_batched(int n, const sketch_grad_problem* problems, const float* scale,
                                                    void* stream);
 

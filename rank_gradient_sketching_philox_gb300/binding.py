@@ -995,14 +995,29 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
     return Y
 
 
+def _written_twice(spans):
+    """Whether one of the (address, bytes, written) that is written overlaps another one."""
+    end = end_written = 0
+    for start, size, written in sorted(s for s in spans if s[1]):
+        if start < (end if written else end_written):
+            return True
+        end = max(end, start + size)
+        if written:
+            end_written = max(end_written, start + size)
+    return False
+
+
 def grad_problems(Gs, outs=None):
     """The problem table of grad_norm_batched and grad_scale_batched: contiguous
-    tensors of any shapes, and those that receive the scaled ones (the same by default)."""
+    tensors of any shapes, and those that receive the scaled ones (the same by default).
+    The norm counts a tensor as often as it is listed; the scaling refuses a table in
+    which what it writes overlaps another tensor."""
     Gs = list(Gs)
     outs = Gs if outs is None else list(outs)
     if not Gs or len(outs) != len(Gs):
         raise ValueError("the lists of a batch have one length, and at least one tensor")
     probs = (GradProblem * len(Gs))()
+    spans = []
     for i, (G, out) in enumerate(zip(Gs, outs)):
         dev = G.device
         if dev.type != "cuda" or dev != Gs[0].device:
@@ -1010,7 +1025,12 @@ def grad_problems(Gs, outs=None):
         _vector(G, G.numel(), None, dev, "G")
         _vector(out, G.numel(), G.dtype, dev, "out")
         probs[i] = GradProblem(G.data_ptr(), out.data_ptr(), G.numel(), _dtype(G, "G"))
+        size = G.numel() * G.element_size()
+        spans.append((out.data_ptr(), size, True))
+        if out.data_ptr() != G.data_ptr():
+            spans.append((G.data_ptr(), size, False))
     probs.tensors = Gs, outs  # kept as long as the table
+    probs.written_twice = _written_twice(spans)
     return probs
 
 
@@ -1042,6 +1062,8 @@ def grad_scale_batched(probs, scale, stream=None):
     """out = G * scale for the tensors of grad_problems; scale: a one-element fp32 tensor."""
     if not scale.is_cuda:
         raise ValueError("scale must be a CUDA tensor")
+    if getattr(probs, "written_twice", False):
+        raise ValueError("a tensor that is written overlaps another one of the table")
     dev = scale.get_device()
     _flat(scale, 1, torch.float32, dev, "scale")
     _launch(dev, "sketch_grad_scale_batched", _problems_on(probs, dev), probs, scale.data_ptr(), _stream_on(stream, dev))

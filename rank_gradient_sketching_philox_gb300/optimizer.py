@@ -71,7 +71,8 @@ class GradClip:
     1 where norm <= max_norm, else max_norm / norm, one-element fp32 tensors that
     the host does not wait for: ``AdamW.step(..., grad_scale=clip.scale)``.  With
     ``outs`` (tensors of the same sizes and types, or the gradients themselves) it
-    also writes the scaled gradients there.  Before the first step norm and scale hold nothing.  The object is bound to its tensors
+    also writes the scaled gradients there; none of them overlaps another, or another's
+    gradient.  Before the first step norm and scale hold nothing.  The object is bound to its tensors
     and keeps the call's workspace, so its steps are ordered on one stream.
     """
 
@@ -82,6 +83,8 @@ class GradClip:
         if not 0.0 < self.max_norm < float("inf"):
             raise ValueError("max_norm must be finite and > 0, got %r" % (max_norm,))
         self._problems = binding.grad_problems(self.grads, self.outs)
+        if self.outs is not None and self._problems.written_twice:
+            raise ValueError("a tensor of outs overlaps another one, or another's gradient")
         dev = self.grads[0].device
         self.norm = torch.empty(1, dtype=torch.float32, device=dev)
         self.scale = torch.empty(1, dtype=torch.float32, device=dev)

@@ -185,3 +185,21 @@ def test_problem_layout_matches_the_header():
     """sketch_grad_problem is two pointers, an int64 and an enum."""
     assert ctypes.sizeof(binding.GradProblem) == 32
     assert binding.GradProblem.count.offset == 16 and binding.GradProblem.type.offset == 24
+
+
+@pytest.mark.parametrize("spans,want", [
+    ([], False),
+    ([(0, 16, True), (16, 16, True), (32, 4, False)], False),
+    ([(64, 16, True), (64, 16, True)], True),                    # one tensor listed twice
+    ([(64, 16, False), (64, 16, False)], False),                 # read twice
+    ([(64, 16, True), (79, 16, False)], True),                   # its last byte read by another
+    ([(79, 16, False), (64, 16, True)], True),
+    ([(79, 16, True), (64, 16, False)], True),                   # its first byte
+    ([(0, 1000, True), (10, 10, False)], True),                  # inside
+    ([(0, 1000, False), (10, 10, True), (2000, 8, True)], True),
+    ([(0, 1000, False), (10, 10, False), (1000, 8, True)], False),
+    ([(0, 0, True), (0, 0, True), (0, 8, True)], False),         # empty tensors have no place
+    ([(0, 64, True), (8, 0, True)], False),
+])
+def test_tensors_that_a_scaling_would_write_twice(spans, want):
+    assert binding._written_twice(spans) is want

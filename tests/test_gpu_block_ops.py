@@ -743,3 +743,23 @@ def test_binding_refuses_mismatches():
     with pytest.raises(rgs.SketchError):  # rows of codes that do not start on 16 bytes
         rgs.quantize_blocks(x, torch.empty(T, k + 1, dtype=E4, device="cuda")[:, :k], sc)
     assert rgs.kernel_launches() == before
+
+
+def test_grad_clip_refuses_what_it_would_write_twice():
+    """A tensor that is listed twice counts twice in the norm, and is not scaled."""
+    G, o = torch.full((4000,), 0.5, device="cuda"), torch.empty(4000, device="cuda")
+    twice = rgs.GradClip([G, G], 1.0)
+    twice.step()
+    check_norm([G, G], twice.norm, twice.scale, 1.0)
+    before = rgs.kernel_launches()
+    for Gs, outs in (([G, G], [G, G]), ([G, G[:100]], [G, G[:100]]), ([G, G], [o, o]), ([G, o], [o, G]),
+                     ([G[:100]], [G[50:150]])):
+        with pytest.raises(ValueError):
+            rgs.GradClip(Gs, 1.0, outs=outs)
+        with pytest.raises(ValueError):
+            rgs.grad_scale_batched(rgs.grad_problems(Gs, outs), twice.scale)
+    assert rgs.kernel_launches() == before
+    halves = rgs.GradClip([G, G], 1.0, outs=[o, torch.empty_like(o)])  # read twice, written apart
+    halves.step()
+    for out in halves.outs:
+        close(out, G.double() * float(halves.scale), G.double().abs() * float(halves.scale) * U)
