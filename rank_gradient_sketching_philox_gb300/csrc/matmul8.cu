@@ -23,8 +23,8 @@
 // 179 for 164) or 64 (371 to 437), the next group's scales or barrier looked at ahead
 // (318 to 353), scales by asynchronous copies (308).
 //
-// Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.2 us on the device, of which 2.5
-// are its 17 MB, 16 x 12288 x 4096 13.5 (50 MB, 7.4); a call takes 8 to 10.
+// Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.3 us on the device, of which 2.5
+// are its 17 MB, 16 x 12288 x 4096 13.5 to 15 (50 MB, 7.4); a call takes 8 to 10.
 #include <cuda_bf16.h>
 
 #include <atomic>
