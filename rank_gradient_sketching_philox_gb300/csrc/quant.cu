@@ -3,15 +3,18 @@
 //
 // Bound by HBM: 3 bytes for a BF16 value, 4 with the transpose.  One GB300, of the copy
 // rate: 4096 x 12288 rows 24.3 us, 0.92 (four pieces of a row to a thread 25.6, 64-bit
-// divisions for each 28.5); 12288 x 4096 weights with their transpose 33.4 us, 0.89, without
-// 25.3; fp32 rows 16384 x 4096 52 us, 0.95.  Rows that are not whole vectors are gathered
-// from L1, value by value: 4096 x 12287 35 us, 12287 x 4095 weights with their
-// transpose 69.  Of 6144 x 2048 weights, 11 us, 0.68, the blocks are one round.
+// divisions for each 28.5); 12288 x 4096 weights with their transpose 32.3 us, 0.92, without
+// 24.5; fp32 rows 16384 x 4096 52 us, 0.95, weights 8192 x 4096 with their transpose 32.2,
+// 0.92.  Of 6144 x 2048 weights, 9.6 us, 0.77, the blocks are one round, in which all load
+// before they store.  Rows that are not whole vectors are gathered from L1, value by value:
+// 4096 x 12287 36 us, 12287 x 4095 weights with their transpose 68 (their values cut from
+// whole 16-byte pieces took as many instructions: rows 41 to 47 us, weights 64 to 67).
 #include <cuda_bf16.h>
 
 #include "common.cuh"
 #include "internal.h"
 #include "rows.cuh"
+#include "tc.cuh"
 
 namespace rgs {
 namespace {
@@ -69,6 +72,12 @@ __device__ __forceinline__ uint4 get_vector(const X* x, int64_t n) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// Copies of single vectors to shared memory, which their thread alone waits for.
+__device__ __forceinline__ void copy_vector(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_landed() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // A scale per row and 128 columns: 16 lanes (BF16; fp32: 32)
 // to such a piece, kPieces of them under way at once.
 constexpr int kPieces = 2;
@@ -115,41 +124,54 @@ __global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const Quantize 
   }
 }
 
-// A scale per 128 rows and 128 columns: a block to each.  A
-// thread has four rows of VE columns (twice, fp32 four times), whose codes it turns by
-// 4 x 4 bytes into words of Qt's rows; those go through shared memory, word w of column
-// c at w ^ 4 (c / 8 % 8), where a warp's words meet in a bank twice at most.
+// A scale per 128 rows and 128 columns: a block to each.  A thread has four rows of VE
+// columns (twice, fp32 four times).  Whole vectors wait in shared memory, not in
+// registers, where they leave room for five blocks on an SM (fp32 three) instead of three
+// (two): 6144 x 2048 BF16 9.6 us for 10.8 (four blocks 10.4, six 10.1), fp32 8192 x 4096 32.2 for
+// 40.  A thread turns its codes by 4 x 4 bytes into words of Qt's rows; those go through
+// shared memory, too, word w of column c at w ^ 4 (c / 8 % 8), where a warp's words meet
+// in a bank twice at most.
+template <typename X>
+constexpr size_t tile_smem() { return kScaleBlock * kScaleBlock * sizeof(X); }
+constexpr int tile_blocks(size_t size, bool whole) { return size == 2 ? (whole ? 5 : 3) : whole ? 3 : 2; }  // per SM
+
 template <typename X, bool WHOLE>
-__global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const Quantize a) {
+__global__ void __launch_bounds__(kThreads, tile_blocks(sizeof(X), WHOLE)) quantize_tiles_kernel(const Quantize a) {
   constexpr int VE = 16 / (int)sizeof(X), LANES = kScaleBlock / VE, QUADS = kThreads / LANES, STEPS = 32 / QUADS;
   __shared__ uint32_t part[kWarps];
-  __shared__ __align__(16) uint32_t tile[kScaleBlock][32];
+  extern __shared__ __align__(128) uint8_t tile_mem[];  // the vectors; then Qt's words
   const int t = threadIdx.x % LANES, quad0 = threadIdx.x / LANES;
   const int64_t groups = ceil_div(a.k, kScaleBlock);
   const int64_t r0 = blockIdx.x / groups * kScaleBlock, c0 = blockIdx.x % groups * kScaleBlock;
   const int64_t left = a.k - c0 - t * VE;  // columns from this thread's first one on
   const bool has = left > 0;
+  const uint32_t mine = tc::smem_u32(tile_mem) + threadIdx.x * 16;  // vector v at + v * kThreads * 16
   start_early();
-  uint4 raw[STEPS][4];
-  uint32_t top = 0;
+  uint4 raw[WHOLE ? 1 : STEPS * 4];
+  const X* x = static_cast<const X*>(a.X) + (r0 + quad0 * 4) * a.ld_x + c0 + t * VE;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t row = r0 + (s * QUADS + quad0) * 4 + i;
-      raw[s][i] = make_uint4(0, 0, 0, 0);
-      if (has && row < a.T)
-        raw[s][i] = get_vector<X, WHOLE>(static_cast<const X*>(a.X) + row * a.ld_x + c0 + t * VE, left);
+  for (int v = 0; v < STEPS * 4; ++v) {
+    const int at = v / 4 * QUADS * 4 + v % 4;  // rows from quad0's first one on
+    const bool in = has && r0 + quad0 * 4 + at < a.T;
+    if constexpr (WHOLE) {
+      if (in) copy_vector(mine + v * (kThreads * 16), x + at * a.ld_x);
+      else tc::sts128(mine + v * (kThreads * 16), make_uint4(0, 0, 0, 0));
+    } else {
+      raw[v] = make_uint4(0, 0, 0, 0);
+      if (in) raw[v] = get_vector<X, false>(x + at * a.ld_x, left);
     }
   }
+  if constexpr (WHOLE) copies_landed();
+  auto vector = [&](int v) {
+    if constexpr (WHOLE) return tc::lds128(mine + v * (kThreads * 16));
+    else return raw[v];
+  };
+  uint32_t top = 0;
 #pragma unroll
-  for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Pair v[VE / 2];
-      vec_pairs<X>(raw[s][i], v);
-      top = max(top, vector_top<VE>(v));
-    }
+  for (int v = 0; v < STEPS * 4; ++v) {
+    Pair p[VE / 2];
+    vec_pairs<X>(vector(v), p);
+    top = max(top, vector_top<VE>(p));
   }
   top = __reduce_max_sync(0xFFFFFFFFu, top);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
@@ -158,34 +180,35 @@ __global__ void __launch_bounds__(kThreads) quantize_tiles_kernel(const Quantize
   float inv;
   const float scale = code_scale(top, inv);
   if (threadIdx.x == 0) a.scale[blockIdx.x] = scale;
+  uint32_t c[STEPS * 4][VE / 4];
+#pragma unroll
+  for (int v = 0; v < STEPS * 4; ++v) {
+    Pair p[VE / 2];
+    vec_pairs<X>(vector(v), p);
+    vector_codes<VE>(p, inv, c[v]);
+    const int64_t row = r0 + quad0 * 4 + v / 4 * QUADS * 4 + v % 4;
+    if (a.Q && has && row < a.T) put_codes<VE, WHOLE>(a.Q + row * a.ld_q + c0 + t * VE, c[v], left);
+  }
+  if (a.Qt == nullptr) return;
+  if constexpr (WHOLE) __syncthreads();  // every thread has read its vectors
+  uint32_t(*tile)[32] = reinterpret_cast<uint32_t(*)[32]>(tile_mem);
 #pragma unroll
   for (int s = 0; s < STEPS; ++s) {
     const int quad = s * QUADS + quad0;
-    uint32_t c[4][VE / 4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      Pair v[VE / 2];
-      vec_pairs<X>(raw[s][i], v);
-      vector_codes<VE>(v, inv, c[i]);
-      const int64_t row = r0 + quad * 4 + i;
-      if (a.Q && has && row < a.T) put_codes<VE, WHOLE>(a.Q + row * a.ld_q + c0 + t * VE, c[i], left);
-    }
-    if (a.Qt) {
+    for (int h = 0; h < VE / 4; ++h) {
+      const uint32_t c0h = c[4 * s][h], c1h = c[4 * s + 1][h], c2h = c[4 * s + 2][h], c3h = c[4 * s + 3][h];
+      const uint32_t ab_lo = __byte_perm(c0h, c1h, 0x5140), ab_hi = __byte_perm(c0h, c1h, 0x7362);
+      const uint32_t cd_lo = __byte_perm(c2h, c3h, 0x5140), cd_hi = __byte_perm(c2h, c3h, 0x7362);
+      const uint32_t w[4] = {__byte_perm(ab_lo, cd_lo, 0x5410), __byte_perm(ab_lo, cd_lo, 0x7632),
+                             __byte_perm(ab_hi, cd_hi, 0x5410), __byte_perm(ab_hi, cd_hi, 0x7632)};
 #pragma unroll
-      for (int h = 0; h < VE / 4; ++h) {
-        const uint32_t ab_lo = __byte_perm(c[0][h], c[1][h], 0x5140), ab_hi = __byte_perm(c[0][h], c[1][h], 0x7362);
-        const uint32_t cd_lo = __byte_perm(c[2][h], c[3][h], 0x5140), cd_hi = __byte_perm(c[2][h], c[3][h], 0x7362);
-        const uint32_t w[4] = {__byte_perm(ab_lo, cd_lo, 0x5410), __byte_perm(ab_lo, cd_lo, 0x7632),
-                               __byte_perm(ab_hi, cd_hi, 0x5410), __byte_perm(ab_hi, cd_hi, 0x7632)};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int col = t * VE + 4 * h + i;
-          tile[col][quad ^ (4 * ((col >> 3) & 7))] = w[i];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int col = t * VE + 4 * h + i;
+        tile[col][quad ^ (4 * ((col >> 3) & 7))] = w[i];
       }
     }
   }
-  if (a.Qt == nullptr) return;
   __syncthreads();
 #pragma unroll
   for (int e = threadIdx.x; e < kScaleBlock * 8; e += kThreads) {
@@ -216,8 +239,9 @@ cudaError_t quantize(const Quantize& a, cudaStream_t stream) {
     return launch_early(whole ? quantize_rows_kernel<X, true> : quantize_rows_kernel<X, false>, blocks, kThreads, 0, stream,
                         a, a.T * groups, (uint32_t)groups, (uint32_t)(kOn / groups), (uint32_t)(kOn % groups));
   }
-  return whole ? launch_early(quantize_tiles_kernel<X, true>, blocks, kThreads, 0, stream, a)
-               : launch_early(quantize_tiles_kernel<X, false>, blocks, kThreads, 0, stream, a);
+  auto kernel = whole ? quantize_tiles_kernel<X, true> : quantize_tiles_kernel<X, false>;
+  const cudaError_t err = allow_smem(kernel, tile_smem<X>());
+  return err == cudaSuccess ? launch_early(kernel, blocks, kThreads, tile_smem<X>(), stream, a) : err;
 }
 
 }  // namespace
