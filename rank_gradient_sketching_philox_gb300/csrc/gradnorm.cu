@@ -60,7 +60,8 @@ __device__ __forceinline__ void walk_units(const GradBatch& a, F f) {
 
 // A thread's values of a unit: vectors threadIdx.x, + 256, ... of it, or single
 // elements where the tensor does not start on 16 bytes or ends.  Values past the end
-// are zeros.
+// are zeros.  Not by way of the read-only cache: the kernel may come up while the one
+// before still writes the gradients.
 template <typename G>
 __device__ __forceinline__ void load_unit(const G* g, int64_t n, int64_t first, float (&v)[kEach]) {
   constexpr int VE = 16 / (int)sizeof(G);
@@ -68,7 +69,7 @@ __device__ __forceinline__ void load_unit(const G* g, int64_t n, int64_t first, 
     uint4 raw[kEach / VE];
     const uint4* p = reinterpret_cast<const uint4*>(g + first) + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kEach / VE; ++j) raw[j] = __ldg(p + j * kThreads);
+    for (int j = 0; j < kEach / VE; ++j) raw[j] = p[j * kThreads];
 #pragma unroll
     for (int j = 0; j < kEach / VE; ++j) {
       Pair q[VE / 2];
