@@ -23,8 +23,8 @@
 // 179 for 164) or 64 (371 to 437), the next group's scales or barrier looked at ahead
 // (318 to 353), scales by asynchronous copies (308).
 //
-// Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.3 us on the device, of which 2.5
-// are its 17 MB, 16 x 12288 x 4096 13.5 to 15 (50 MB, 7.4); a call takes 8 to 10.
+// Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.4 us on the device, of which 2.5
+// are its 17 MB, 16 x 12288 x 4096 12.1 (50 MB, 7.4); a call takes 8 to 10.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -86,22 +86,25 @@ __device__ __forceinline__ void put4(const Product8& a, int64_t row, int col, fl
 // B's rows are the MMA's M (128 of them), TN tokens its N.  A cluster of S CTAs splits
 // the groups of a tile and joins its parts through distributed shared memory, each CTA
 // a share of the tokens, in the CTAs' order.
-constexpr int kFewStages = 5;   // at most: 104 KB, for two CTAs per SM
+constexpr int kFewStages = 5;   // at most
 constexpr int few_buffers(int TN) { return TN == 64 ? 4 : 8; }
 constexpr int few_columns(int TN) { return TN * few_buffers(TN); }  // of TMEM: 128 or 256 of 512
 // Tokens of a thread of the sums' warps: 32 at most, then two warps share 32 rows of B.
 constexpr int few_cols(int TN) { return TN <= 32 ? TN : TN / 2; }
 constexpr int few_warps(int TN) { return 4 * (TN / few_cols(TN)); }
 constexpr int few_threads(int TN) { return 64 + 32 * few_warps(TN); }  // copies, MMAs, sums
-constexpr int kFewResident = 2;                                        // CTAs per SM
-// Shared memory of a launch, whatever it needs (105 KB at most): so much that an SM never
-// holds more CTAs than TMEM has columns for.  One that waited for columns while its cluster
-// holds some on another SM could wait for a cluster that waits for those.
-constexpr size_t kFewSmem = 110u << 10;
+// CTAs per SM: as many as TMEM has columns for (16 tokens, 12288 x 4096: 12.1 us with four,
+// 14 to 15 with two).
+constexpr int few_resident(int TN) { return 512 / few_columns(TN); }
+// Shared memory of a launch, whatever it needs: so much that an SM never holds more CTAs,
+// of this kernel in its forms and of others whose clusters take TMEM, than it has columns
+// for.  One that waited for columns while its cluster holds some on another SM could wait for
+// a cluster that waits for those.
+constexpr size_t few_smem(int TN) { return (220u << 10) / few_resident(TN); }
 constexpr uint32_t few_stage_bytes(int TN) { return kRowsBytes + TN * kChunk; }
 
 template <int TN>
-__global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_kernel(const __grid_constant__ Product8 a) {
+__global__ void __launch_bounds__(few_threads(TN), few_resident(TN)) matmul8_few_kernel(const __grid_constant__ Product8 a) {
   constexpr int kBuffers = few_buffers(TN), kCols = few_cols(TN), kSums = few_warps(TN);
   constexpr uint32_t kStageBytes = few_stage_bytes(TN);
   extern __shared__ uint8_t smem_raw[];
@@ -308,8 +311,8 @@ __global__ void __launch_bounds__(few_threads(TN), kFewResident) matmul8_few_ker
 // (clusters of 6 do not all fit beside each other: 32 x 6144 x 2048 takes 15.9 us with
 // them, 6.9 with 4), and more where that saves three groups at least (16 x 2048 x 2048:
 // 4.3 us with 4, 4.9 with 8; 16 x 1024 x 4096: 5.7 and 4.6).
-unsigned few_split(int64_t tiles, int chunks, int64_t* steps) {
-  const int64_t slots = (int64_t)num_sms() * kFewResident;
+unsigned few_split(int64_t tiles, int chunks, int resident, int64_t* steps) {
+  const int64_t slots = (int64_t)num_sms() * resident;
   unsigned S = 1;
   *steps = ceil_div(tiles, slots) * chunks;
   for (int s : {2, 3, 4, 8}) {
@@ -333,17 +336,18 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
   p.n_tiles = (int)ceil_div(a.N, 128);
   const int64_t tiles = (int64_t)p.n_tiles * ceil_div(a.T, TN);
   int64_t steps;
-  const unsigned S = few_split(tiles, p.chunks, &steps);
+  const unsigned S = few_split(tiles, p.chunks, few_resident(TN), &steps);
   p.stages = (int)ceil_div(p.chunks, S);
-  const int most = (int)((104u << 10) / kStageBytes);
-  if (p.stages > most) p.stages = most;
-  static_assert(104u << 10 <= kFewSmem - 1024 && TN * 512 <= kFewSmem - 1024, "stages, and a part of the sum");
-  err = allow_smem(matmul8_few_kernel<TN>, kFewSmem);
+  constexpr int kMost = (int)((few_smem(TN) - 1024) / kStageBytes);  // 1 KB: the stages' alignment
+  static_assert(kMost >= 3 && TN * 512 <= few_smem(TN) - 1024, "stages, and a part of the sum");
+  if (p.stages > kMost) p.stages = kMost;
+  if (p.stages > kFewStages) p.stages = kFewStages;
+  err = allow_smem(matmul8_few_kernel<TN>, few_smem(TN));
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
   cfg.blockDim = dim3(few_threads(TN), 1, 1);
-  cfg.dynamicSmemBytes = kFewSmem;
+  cfg.dynamicSmemBytes = few_smem(TN);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -880,7 +884,7 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
     }
   }
   int64_t steps;
-  few_split(ceil_div(a.T, 64) * ceil_div(a.N, 128), p.chunks, &steps);
+  few_split(ceil_div(a.T, 64) * ceil_div(a.N, 128), p.chunks, few_resident(64), &steps);
   if (0.85 * (double)steps <= best) return launch_few<64>(p, a, stream);
   err = make_tmap_u8_2d(&p.tmA, a.A, (uint64_t)a.k, (uint64_t)a.T, (uint64_t)a.ld_a, kChunk, 128);
   if (err == cudaSuccess)
