@@ -10,8 +10,9 @@
 // before S rounds it, q takes y before Y does.
 //
 // Bound by HBM.  One GB300, of the copy rate, 32768 x 4096 BF16: forward with residual,
-// BF16 and 8-bit output 191 us, 0.94 (9 bytes a value); with residual and BF16 output
-// 164, 0.96; BF16 output alone 86, 0.92; 8-bit output alone 96, 0.62, where the codes'
+// BF16 and 8-bit output 188 us, 0.95 (9 bytes a value; with loads that go first from the
+// caches 191); with residual and BF16 output 164, 0.97; BF16 output alone 84, 0.94; 8-bit
+// output alone 93, 0.64, where the codes'
 // instructions take 62 % of the issue slots; backward with the stream's gradient 164 us,
 // 0.96 (8 bytes), without it 140, 0.85.  8192 x 16384 forward 194 us, 0.92, backward 178,
 // 0.89; fp32 16384 x 4096 176 and 160.  Rows on other places than 16 bytes: 32768 x
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS, RES)) rms_for
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       raw[j] = make_uint4(0, 0, 0, 0);
-      if (in && j * tpr + t < nvec) raw[j] = __ldcs(x + j * tpr + t);
+      if (in && j * tpr + t < nvec) raw[j] = x[j * tpr + t];
     }
     if constexpr (RES) {
       const uint4* r = reinterpret_cast<const uint4*>(static_cast<const X*>(a.R) + row * a.ld_r);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(THREADS, forward_blocks(THREADS, RES)) rms_for
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         add[j] = make_uint4(0, 0, 0, 0);
-        if (in && j * tpr + t < nvec) add[j] = __ldcs(r + j * tpr + t);
+        if (in && j * tpr + t < nvec) add[j] = r[j * tpr + t];
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
