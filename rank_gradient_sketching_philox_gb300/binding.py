@@ -850,6 +850,30 @@ def _stream_on(stream, index):
     return stream.cuda_stream
 
 
+_lend = torch._C._cuda_cudaCachingAllocator_raw_alloc  # (bytes, stream) on the current device
+_take_back = torch._C._cuda_cudaCachingAllocator_raw_delete
+
+
+def _borrow(op, T, k, index, handle, given):
+    """(address, size, what _take_back gets after the call) of a call's workspace: the
+    caller's, or one that PyTorch's allocator lends to the call's stream, where its next
+    user comes after the call.  Not a tensor, whose making takes as long as two launches."""
+    nbytes = lib().sketch_workspace_bytes(op, T, 0, k, 0)
+    if given is not None:
+        if given.get_device() != index or not given.is_contiguous() or given.numel() * given.element_size() < nbytes:
+            raise ValueError("workspace needs %d contiguous bytes on cuda:%d" % (nbytes, index))
+        return given.data_ptr(), nbytes, None
+    if nbytes == 0:
+        return None, 0, None
+    before = _set_device(index)
+    try:
+        at = _lend(nbytes, handle)
+    finally:
+        if before != index:
+            _set_device(before)
+    return at, nbytes, at
+
+
 def code_rows(T, k, device="cuda"):
     """An uninitialised T x k matrix of E4M3 codes whose rows start on 16 bytes, as
     the 8-bit calls want them."""
@@ -944,13 +968,15 @@ def rms_norm_backward(dY, S, gamma, rstd, dS=None, dX=None, dgamma=None, overwri
     _flat(rstd, T, torch.float32, dev, "rstd")
     if dgamma is not None:
         _flat(dgamma, k, torch.float32, dev, "dgamma")
-    keep = ws_at = None
-    nbytes = 0
-    if dgamma is not None:
-        keep, ws_at, nbytes = _scratch(OP_RMS_NORM_BACKWARD, T, 0, k, 0, S.device, stream, ws)
-    _launch(dev, "sketch_rms_norm_backward", dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
-            _addr(gamma), w_type, rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
-            1 if overwrite else 0, ws_at, nbytes, _stream_on(stream, dev))
+    handle = _stream_on(stream, dev)
+    ws_at, nbytes, lent = (None, 0, None) if dgamma is None else _borrow(OP_RMS_NORM_BACKWARD, T, k, dev, handle, ws)
+    try:
+        _launch(dev, "sketch_rms_norm_backward", dY.data_ptr(), ld_dy, S.data_ptr(), x_type, T, k, ld_s,
+                _addr(gamma), w_type, rstd.data_ptr(), _addr(dS), ld_ds, _addr(dX), ld_dx, _addr(dgamma),
+                1 if overwrite else 0, ws_at, nbytes, handle)
+    finally:
+        if lent is not None:
+            _take_back(lent)
     return dX
 
 
@@ -1052,9 +1078,13 @@ def grad_norm_batched(probs, norm, scale=None, max_norm=1.0, ws=None, stream=Non
     if scale is not None:
         _flat(scale, 1, torch.float32, dev, "scale")
     n = _problems_on(probs, dev)
-    keep, ws_at, nbytes = _scratch(OP_GRAD_NORM, n, 0, 0, 0, norm.device, stream, ws)
-    _launch(dev, "sketch_grad_norm_batched", n, probs, max_norm, norm.data_ptr(), _addr(scale),
-            ws_at, nbytes, _stream_on(stream, dev))
+    handle = _stream_on(stream, dev)
+    ws_at, nbytes, lent = _borrow(OP_GRAD_NORM, n, 0, dev, handle, ws)
+    try:
+        _launch(dev, "sketch_grad_norm_batched", n, probs, max_norm, norm.data_ptr(), _addr(scale), ws_at, nbytes, handle)
+    finally:
+        if lent is not None:
+            _take_back(lent)
     return norm
 
 

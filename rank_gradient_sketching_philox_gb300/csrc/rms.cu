@@ -18,7 +18,7 @@
 // 0.89; fp32 16384 x 4096 176 and 160.  Rows on other places than 16 bytes: 32768 x
 // 4095 forward 287 us, 0.62, backward 249, 0.63; the elements' shared memory reads and
 // single stores take the rest.  8 x 2048 forward: 2.4 us on the device, a call 8 to 9; 1021
-// x 1001 fp32 backward: 9.6 us on the device, two launches, a call 17 to 20.
+// x 1001 fp32 backward: 9.6 us on the device, two launches, a call 12 to 13.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

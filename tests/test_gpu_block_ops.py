@@ -763,3 +763,49 @@ def test_grad_clip_refuses_what_it_would_write_twice():
     halves.step()
     for out in halves.outs:
         close(out, G.double() * float(halves.scale), G.double().abs() * float(halves.scale) * U)
+
+
+def test_borrowed_workspaces_are_given_back():
+    """A call's own workspace belongs to the call's stream, or to the graph that is captured, and to nobody after it."""
+    g, T, k = gen(21), 700, 1000
+    s, dy, rstd = normal(g, T, k), normal(g, T, k), torch.ones(T, device="cuda")
+    other_dy = normal(g, T, k)
+    dgamma, other, norm = (torch.zeros(n, device="cuda") for n in (k, k, 1))
+    probs = rgs.grad_problems([dy, s])
+
+    def calls(d, into, stream=None):
+        rgs.rms_norm_backward(d, s, None, rstd, dgamma=into, overwrite=True, stream=stream)
+        rgs.grad_norm_batched(probs, norm, stream=stream)
+
+    calls(dy, dgamma)
+    calls(other_dy, other)
+    torch.cuda.synchronize()
+    want, want_other, want_norm = dgamma.clone(), other.clone(), norm.clone()
+    before = torch.cuda.memory_allocated()
+    for stream in (None, torch.cuda.Stream()):
+        for _ in range(3):
+            calls(dy, dgamma, stream)
+    with pytest.raises(rgs.SketchError):  # refused after the workspace was lent
+        rgs.rms_norm_backward(dy, s, None, rstd, dS=dy, dgamma=dgamma)
+    torch.cuda.synchronize()
+    assert torch.cuda.memory_allocated() == before
+    assert torch.equal(dgamma, want) and torch.equal(norm, want_norm)
+
+    graphs, streams = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], [torch.cuda.Stream(), torch.cuda.Stream()]
+    with torch.cuda.graph(graphs[0]):
+        calls(dy, dgamma)
+        held = torch.zeros(400_000, device="cuda")  # may lie where the workspaces were, after them
+        calls(dy, dgamma)
+    with torch.cuda.graph(graphs[1]):
+        rgs.rms_norm_backward(other_dy, s, None, rstd, dgamma=other, overwrite=True)
+    for _ in range(5):
+        dgamma.zero_(), other.zero_()
+        junk = [torch.full((T * k,), float("nan"), device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        del junk
+        assert torch.equal(dgamma, want) and torch.equal(other, want_other) and torch.equal(norm, want_norm)
+        assert not held.any()
