@@ -9,8 +9,8 @@
 // fp32 registers, groups in their order.
 //
 // What bounds it, one GB300.  Many tokens: the sums.  8192 x 12288 x 4096 (T x N x k)
-// takes 296 to 302 us, 2.75 PFLOP/s, and in a long run of passes, at the power limit, 325
-// to 339; a library product with one scale for each matrix takes 221 and 244.  The tensor
+// takes 284 to 287 us, 2.9 PFLOP/s, and in a long run of passes, at the power limit,
+// 322; a library product with one scale for each matrix takes 221 and 244.  The tensor
 // cores are busy for 63 % of the time.  The same kernel without the sums takes 222 us,
 // without their multiply-adds 272: a group's MMAs take 512 cycles, and in that time eight
 // warps have to see their end, read 256 columns of 128 rows from TMEM, add them, times
@@ -18,10 +18,11 @@
 // it there: an arrival on the other CTA's barrier without a release to the cluster (870
 // -> 395 us), the scales through shared memory, whole warps that walk the issuing loops
 // (363 -> 352), four accumulators and two MMA warps with the loads from TMEM beside the
-// sums (352 -> 302).  Tried and dropped: 16 warps of 64 columns (345), an arrival of one
-// thread for a CTA (397 of then 366), pieces of 32 columns (297, but 4096 x 4096 x 12288
-// 179 for 164) or 64 (371 to 437), the next group's scales or barrier looked at ahead
-// (318 to 353), scales by asynchronous copies (308).
+// sums (352 -> 302), fewer and wider loads of the scales and the registers that they leave
+// (302 -> 287).  Tried and dropped: 16 warps of 64 columns (345), an arrival of one thread
+// for a CTA (397 of then 366), pieces of 24 columns (287 of then 289), 32 (294, but 4096 x
+// 4096 x 12288 168 for 154) or 64 (371 to 437), the next group's scales or barrier looked
+// at ahead (318 to 353), scales by asynchronous copies (308).
 //
 // Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.4 us on the device, of which 2.5
 // are its 17 MB, 16 x 12288 x 4096 12.1 (50 MB, 7.4); a call takes 8 to 10.
@@ -370,17 +371,18 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
 // takes one, each pair a part of its groups; the parts meet in shared memory and are
 // added in the pairs' order.
 constexpr int kTile = 256;
-constexpr int kTileStages = 4;
+constexpr int kTileStages = 5;  // 8192 x 12288 x 4096 284 us, with four and twice the boxes 286
 constexpr uint32_t kTileStageBytes = 2 * kRowsBytes;  // 128 rows of A, 128 of B
 constexpr int kSumWarps = 8;
 constexpr int kTileThreads = 128 + 32 * kSumWarps;    // copies, MMAs, scales, an idle warp; sums
 constexpr int kSumCols = 128;                         // of a thread
 constexpr int kLoads = kSumCols / 16;                 // from TMEM, of 16 columns
-// Registers: the launch has 168 for each thread, 384 * 168 = 128 * 120 + 256 * 192; with
-// fewer for the first, 8192 x 12288 x 4096 takes longer (104: 298 us, 88: 313, 72: 334; 120: 294).
-constexpr int kFewRegisters = 120, kSumRegisters = 192;
+// Registers: the launch has 168 for each thread, 384 * 168 = 128 * 88 + 256 * 208.  8192 x
+// 12288 x 4096 takes 290 us with them, with 72 and 216 301, with 104 and 200 304, with 120
+// and 192 303.
+constexpr int kFewRegisters = 88, kSumRegisters = 208;
 constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
-constexpr int kBoxes = 4;                             // of a warp: a BF16 tile's part leaves without a wait
+constexpr int kBoxes = 2;                             // of a warp
 constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
 constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxes * kBoxBytes + 1024;
 constexpr int kGroupM = 16;                           // tile rows walked together
@@ -424,7 +426,7 @@ __device__ __noinline__ void put_end(const Product8& a, int64_t row, int col, ui
 }
 
 // SPLIT: clusters of several pairs (one kernel for both took 307 us for 8192 x 12288 x
-// 4096, not 296).
+// 4096, not 296 as then).
 template <bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __grid_constant__ Product8 a) {
   extern __shared__ uint8_t smem_raw[];
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
         __syncwarp();
       }
       // a wait that gives up makes all later ones give up too; looked at now and then (each
-      // time, 8192 x 12288 x 4096 took 303 us, not 296)
+      // time, 8192 x 12288 x 4096 took 303 us, not 296 as then)
       if ((it & 14) == 14 && !__all_sync(0xFFFFFFFFu, live)) break;
       tph ^= 1u;
       s += 2;
@@ -568,40 +570,48 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
     if (lane == 0 && live) consumed[warp >> 1] = it;
   } else if (warp == 2) {
     // ---- scales: of the CTA's 128 rows, times those of the tile's two column blocks ----
+    // Four groups' of a row in one load, where they lie on 16 bytes.  With each read singly,
+    // the columns' by every lane, this warp took longer than eight groups' MMAs, or the
+    // registers that the sums' warps want (8192 x 12288 x 4096 313 us with 88, not 290).
+    const bool fours = ((reinterpret_cast<uintptr_t>(a.a_scale) | (uintptr_t)(a.ld_as * 4) | (uintptr_t)(c0 * 4)) & 15u) == 0;
     int batch = 0;
     bool live = true;
     for (int item = first_item; item < items && live; item += step) {
       int m0, n0;
       place(item, m0, n0);
-      const float* as[4];
-      const int row = m0 + 128 * (int)rank + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) as[i] = row + 32 * i < a.T ? a.a_scale + (int64_t)(row + 32 * i) * a.ld_as + c0 : nullptr;
-      const float* bs = a.b_scale + (int64_t)(n0 / kScaleBlock) * a.bs_row + c0 * a.bs_col;
-      const bool second = n0 + kScaleBlock < a.N;
+      const int row = m0 + 128 * (int)rank + lane, left = a.T - row;
+      const float* as = a.a_scale + (int64_t)(left > 0 ? row : 0) * a.ld_as + c0;
+      // lane c + 8 j: group c's, column block j's
+      const int block = n0 / kScaleBlock + ((lane >> 3) & 1);
+      const float* bs = a.b_scale + (int64_t)(block * kScaleBlock < a.N ? block : 0) * a.bs_row + (int64_t)c0 * a.bs_col;
       for (int first = 0; first < chunks && live; first += kScaleGroups, ++batch) {
         const int slot = batch & 1;
+        const float mine = block * kScaleBlock < a.N && first + (lane & 7) < chunks ? bs[(int64_t)(first + (lane & 7)) * a.bs_col] : 0.f;
 #pragma unroll
-        for (int half = 0; half < kScaleGroups; half += kScaleGroups / 2) {
-          float sa[kScaleGroups / 2][4], sb[kScaleGroups / 2][2];
+        for (int half = 0; half < kScaleGroups; half += 4) {
+          float sa[4][4];  // row, group
 #pragma unroll
-          for (int j = 0; j < kScaleGroups / 2; ++j) {
-            const int c = first + half + j;
+          for (int i = 0; i < 4; ++i) {
+            const float* from = as + (int64_t)(32 * i) * a.ld_as + first + half;
+            if (fours && first + half + 4 <= chunks) {
+              const float4 v = 32 * i < left ? *reinterpret_cast<const float4*>(from) : make_float4(0.f, 0.f, 0.f, 0.f);
+              sa[i][0] = v.x, sa[i][1] = v.y, sa[i][2] = v.z, sa[i][3] = v.w;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sa[j][i] = as[i] && c < chunks ? as[i][c] : 0.f;
-            sb[j][0] = c < chunks ? bs[c * a.bs_col] : 0.f;
-            sb[j][1] = second && c < chunks ? bs[a.bs_row + c * a.bs_col] : 0.f;
+              for (int j = 0; j < 4; ++j) sa[i][j] = 32 * i < left && first + half + j < chunks ? from[j] : 0.f;
+            }
           }
           if (half == 0 && batch >= 2)
             live = tc::mbar_wait(&read_bar[slot], ((batch >> 1) - 1) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
           live = __all_sync(0xFFFFFFFFu, live);
           if (!live) break;
 #pragma unroll
-          for (int j = 0; j < kScaleGroups / 2; ++j) {
+          for (int j = 0; j < 4; ++j) {
+            const float b0 = __shfl_sync(0xFFFFFFFFu, mine, half + j), b1 = __shfl_sync(0xFFFFFFFFu, mine, half + j + 8);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              scales[slot][half + j][0][32 * i + lane] = sa[j][i] * sb[j][0];
-              scales[slot][half + j][1][32 * i + lane] = sa[j][i] * sb[j][1];
+              scales[slot][half + j][0][32 * i + lane] = sa[i][j] * b0;
+              scales[slot][half + j][1][32 * i + lane] = sa[i][j] * b1;
             }
           }
         }
