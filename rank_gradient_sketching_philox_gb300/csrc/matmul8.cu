@@ -10,19 +10,22 @@
 //
 // What bounds it, one GB300.  Many tokens: the sums.  8192 x 12288 x 4096 (T x N x k)
 // takes 284 to 287 us, 2.9 PFLOP/s, and in a long run of passes, at the power limit,
-// 322; a library product with one scale for each matrix takes 221 and 244.  The tensor
-// cores are busy for 63 % of the time.  The same kernel without the sums takes 222 us,
-// without their multiply-adds 272: a group's MMAs take 512 cycles, and in that time eight
-// warps have to see their end, read 256 columns of 128 rows from TMEM, add them, times
-// their scales, and hand the accumulators back, which takes them some 800.  What brought
-// it there: an arrival on the other CTA's barrier without a release to the cluster (870
-// -> 395 us), the scales through shared memory, whole warps that walk the issuing loops
-// (363 -> 352), four accumulators and two MMA warps with the loads from TMEM beside the
-// sums (352 -> 302), fewer and wider loads of the scales and the registers that they leave
-// (302 -> 287).  Tried and dropped: 16 warps of 64 columns (345), an arrival of one thread
-// for a CTA (397 of then 366), pieces of 24 columns (287 of then 289), 32 (294, but 4096 x
-// 4096 x 12288 168 for 154) or 64 (371 to 437), the next group's scales or barrier looked
-// at ahead (318 to 353), scales by asynchronous copies (308).
+// 322; a library product with one scale for each matrix takes 221 and 244.  The same
+// kernel without the sums takes 222 us: a group's MMAs take 512 cycles, and in that time
+// eight warps have to see their end, read 256 columns of 128 rows from TMEM, add them,
+// times their scales, and hand the accumulators back.  What brought it there: an arrival on
+// the other CTA's barrier without a release to the cluster (870 -> 395 us), the scales
+// through shared memory, whole warps that walk the issuing loops (363 -> 352), four
+// accumulators and two MMA warps with the loads from TMEM beside the sums (352 -> 302),
+// fewer and wider loads of the scales and the registers that they leave (302 -> 287).
+// Without the multiply-adds it takes 240, without the loads from TMEM 266, without either
+// 238: what is left is the accumulators' way between the CTAs, some 800 cycles of the 1024
+// that TMEM holds, and the multiply-adds.  Tried and dropped: MMAs of each CTA alone, B's
+// rows sent to both (301; these MMAs by themselves take 288), 16 warps of 64 columns (345),
+// an arrival of one thread for a CTA (397 of then 366), pieces of 24 columns (287 of then
+// 289), 32 (294, but 4096 x 4096 x 12288 168 for 154) or 64 (371 to 437), the next group's
+// scales or barrier looked at ahead (318 to 353), waits that spin (285 to 304), scales by
+// asynchronous copies (308).
 //
 // Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.4 us on the device, of which 2.5
 // are its 17 MB, 16 x 12288 x 4096 12.1 (50 MB, 7.4); a call takes 8 to 10.
@@ -523,6 +526,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
       }
     }
     if (lane == 0) issued = it;
+    // the even CTA's commits have arrived on this one's barriers before it leaves
+    for (int i = it > kTileStages ? it - kTileStages : 0; i < it && !stop; ++i) {
+      stop = !tc::mbar_wait(empty0 + 8u * (i % kTileStages), (i / kTileStages) & 1, &abort_flag, a.err, tc::kErrTimeoutStage);
+      stop = __any_sync(0xFFFFFFFFu, stop);
+    }
   } else if ((warp & 1) && rank == 0) {
     // ---- MMAs, for both CTAs: warp 1 the even groups, warp 3 the odd ones ----
     // A group's waits, MMAs and commits take a warp some 800 cycles, one after another,
