@@ -10,7 +10,7 @@
 //
 // What bounds it, one GB300.  Many tokens: the sums.  8192 x 12288 x 4096 (T x N x k)
 // takes 284 to 287 us, 2.9 PFLOP/s, and in a long run of passes, at the power limit,
-// 322; a library product with one scale for each matrix takes 221 and 244.  The same
+// 322 to 328; a library product with one scale for each matrix takes 221 and 244.  The same
 // kernel without the sums takes 222 us: a group's MMAs take 512 cycles, and in that time
 // eight warps have to see their end, read 256 columns of 128 rows from TMEM, add them,
 // times their scales, and hand the accumulators back.  What brought it there: an arrival on
