@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
@@ -41,19 +42,6 @@ __device__ __forceinline__ void acc2(float& hi, float& lo, float x) {
 // the accumulators and scale the sums by 2^-2e into the chunk's partial (written with a
 // zero low word), which gram_reduce_kernel adds up in chunk order.
 constexpr int kGtcThreads = 256;
-constexpr int kGtcStep = 64;  // rows per step: one 128-byte swizzled row of FP16 per column of A
-__host__ __device__ inline int gtc_mpad(int r) { return r <= 128 ? 128 : 256; }
-__host__ __device__ inline int gtc_npad(int r) { return (r + 15) / 16 * 16; }
-// TMEM columns: the accumulators (nacc x M halves x npad), and at least the
-// span the epilogue's 32-column reads cover
-__host__ __device__ inline uint32_t gtc_tmem_cols(int r) {
-  const int npad = gtc_npad(r), nmh = gtc_mpad(r) / 128, nacc = gram_tc_accs(r);
-  const int reads = (nacc * nmh - 1) * npad + (npad + 31) / 32 * 32;
-  const int cols = nacc * nmh * npad > reads ? nacc * nmh * npad : reads;
-  uint32_t c = 32;
-  while ((int)c < cols) c <<= 1;
-  return c;
-}
 __device__ __forceinline__ uint8_t* gtc_align1024(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
@@ -91,7 +79,6 @@ __device__ __forceinline__ float gtc_chunk_max(const float* __restrict__ p, int6
 // into the ring with a bulk copy, raw_stages steps ahead, and the threads
 // convert from there.  Otherwise each thread loads the next step's items into
 // registers while this step's are converted.
-constexpr int kGtcMaxRaw = 4;
 template <int IPT, bool BULK>
 __global__ void __launch_bounds__(kGtcThreads) gram_tc_kernel(const GramBatch batch) {
   extern __shared__ uint8_t gtc_raw[];
@@ -384,26 +371,12 @@ cudaError_t launch_gram(const GramBatch& batch_in, cudaStream_t stream) {
   batch.chunk_begin[0] = 0;
   for (int i = 0; i < batch.n; ++i)
     batch.chunk_begin[i + 1] = batch.chunk_begin[i] + gram_chunks_tc(batch.e[i].rows, r).nchunks;
-  // shared memory: two buffers of two tiles, or more, so that the blocks
-  // resident on an SM never ask for more than its 512 TMEM columns
-  const size_t tiles = (size_t)4 * gtc_mpad(r) * 128 + 1024;
-  const int max_blocks = 512 / (int)gtc_tmem_cols(r);
-  const size_t tmem_bound = (size_t)233472 / (size_t)(max_blocks + 1) - 1024 + 16;
-  size_t smem = tiles > tmem_bound ? tiles : tmem_bound;
-  // the ring of fp32 row copies in what the blocks an SM's TMEM admits leave
-  // (each block also holds 1 KB reserved by the system and the kernel's
-  // static shared memory)
-  // (the static size is a property of the compiled kernel: asked once)
-  static const size_t static_smem = [] {
-    cudaFuncAttributes fa;
-    return cudaFuncGetAttributes(&fa, gram_tc_kernel<2, true>) == cudaSuccess ? fa.sharedSizeBytes : (size_t)1024;
-  }();
-  cudaError_t err = cudaSuccess;
-  const size_t per_block = (size_t)233472 / (size_t)max_blocks - 1024 - static_smem;
-  const size_t raw_bytes = (size_t)kGtcStep * r * 4;
-  int stages = per_block > tiles ? (int)((per_block - tiles) / raw_bytes) : 0;
-  if (stages > kGtcMaxRaw) stages = kGtcMaxRaw;
-  if (stages < 2 || r > 128) stages = 0;
+  static std::atomic<size_t> known;  // the kernel's variants have the same static arrays
+  size_t fixed = 0;
+  cudaError_t err = static_smem(gram_tc_kernel<2, true>, known, &fixed);
+  if (err != cudaSuccess) return err;
+  const GramSizes z = gram_sizes(r, fixed);
+  int stages = z.raw_stages;
   // the bulk copies need every A on 16 bytes and a whole number of 16-byte
   // pieces per chunk (chunks start on multiples of 64 rows)
   for (int i = 0; i < batch.n && stages > 0; ++i)
@@ -414,7 +387,8 @@ cudaError_t launch_gram(const GramBatch& batch_in, cudaStream_t stream) {
               : ipt == 2 ? (stages ? gram_tc_kernel<2, true> : gram_tc_kernel<2, false>)
               : ipt == 4 ? (stages ? gram_tc_kernel<4, true> : gram_tc_kernel<4, false>)
                          : gram_tc_kernel<8, false>;
-  if (stages > 0 && tiles + stages * raw_bytes > smem) smem = tiles + stages * raw_bytes;
+  const size_t smem = gram_ring_smem(z, r, stages);
+  if (!tmem_safe(gtc_tmem_cols(r), smem + fixed + kBlockSmem, false)) return cudaErrorInvalidConfiguration;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   count_launch();

@@ -67,6 +67,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
@@ -944,6 +945,7 @@ int dx_parts(int64_t T, int64_t V, int64_t k) {
 }
 
 constexpr size_t kHeadSmem = (size_t)kStages * kStageBytes + 1024;
+static_assert(tmem_alone(kHeadSmem));
 
 // CTA pairs that the device holds at once (its SMs need not all pair up).
 cudaError_t head_pairs(int* out) {

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "sketch.h"
 
 namespace rgs {
@@ -46,6 +48,19 @@ cudaError_t device_error_word(int** out);
 // sketch_read_exact_count).
 cudaError_t device_exact_counter(unsigned long long** out);
 int num_sms();
+// Static shared memory of a kernel, a property of the compiled code: asked once, `known`
+// being one more than it from then on.
+template <typename Kernel>
+cudaError_t static_smem(Kernel kernel, std::atomic<size_t>& known, size_t* bytes) {
+  if (known == 0) {
+    cudaFuncAttributes f;
+    const cudaError_t err = cudaFuncGetAttributes(&f, kernel);
+    if (err != cudaSuccess) return err;
+    known = f.sharedSizeBytes + 1;
+  }
+  *bytes = known - 1;
+  return cudaSuccess;
+}
 // Counts one kernel launch issued by this library (sketch_kernel_launches).
 void count_launch();
 uint64_t launches_issued();

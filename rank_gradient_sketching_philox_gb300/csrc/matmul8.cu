@@ -37,6 +37,7 @@
 #include "internal.h"
 #include "rows.cuh"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
@@ -91,20 +92,10 @@ __device__ __forceinline__ void put4(const Product8& a, int64_t row, int col, fl
 // the groups of a tile and joins its parts through distributed shared memory, each CTA
 // a share of the tokens, in the CTAs' order.
 constexpr int kFewStages = 5;   // at most
-constexpr int few_buffers(int TN) { return TN == 64 ? 4 : 8; }
-constexpr int few_columns(int TN) { return TN * few_buffers(TN); }  // of TMEM: 128 or 256 of 512
 // Tokens of a thread of the sums' warps: 32 at most, then two warps share 32 rows of B.
 constexpr int few_cols(int TN) { return TN <= 32 ? TN : TN / 2; }
 constexpr int few_warps(int TN) { return 4 * (TN / few_cols(TN)); }
 constexpr int few_threads(int TN) { return 64 + 32 * few_warps(TN); }  // copies, MMAs, sums
-// CTAs per SM: as many as TMEM has columns for (16 tokens, 12288 x 4096: 12.1 us with four,
-// 14 to 15 with two).
-constexpr int few_resident(int TN) { return 512 / few_columns(TN); }
-// Shared memory of a launch, whatever it needs: so much that an SM never holds more CTAs,
-// of this kernel in its forms and of others whose clusters take TMEM, than it has columns
-// for.  One that waited for columns while its cluster holds some on another SM could wait for
-// a cluster that waits for those.
-constexpr size_t few_smem(int TN) { return (220u << 10) / few_resident(TN); }
 constexpr uint32_t few_stage_bytes(int TN) { return kRowsBytes + TN * kChunk; }
 
 template <int TN>
@@ -342,16 +333,22 @@ cudaError_t launch_few(Product8& p, const MatmulBlocks& a, cudaStream_t stream) 
   int64_t steps;
   const unsigned S = few_split(tiles, p.chunks, few_resident(TN), &steps);
   p.stages = (int)ceil_div(p.chunks, S);
-  constexpr int kMost = (int)((few_smem(TN) - 1024) / kStageBytes);  // 1 KB: the stages' alignment
-  static_assert(kMost >= 3 && TN * 512 <= few_smem(TN) - 1024, "stages, and a part of the sum");
-  if (p.stages > kMost) p.stages = kMost;
+  static std::atomic<size_t> known;
+  size_t fixed = 0;
+  err = static_smem(matmul8_few_kernel<TN>, known, &fixed);
+  if (err != cudaSuccess) return err;
+  const size_t smem = few_smem(TN, fixed);
+  const int most = (int)((smem - 1024) / kStageBytes);  // 1 KB: the stages' alignment
+  if (most < 3 || TN * 512 > smem - 1024 || !tmem_safe(few_columns(TN), smem + fixed + kBlockSmem, true))
+    return cudaErrorInvalidConfiguration;  // stages, a part of the sum, TMEM
+  if (p.stages > most) p.stages = most;
   if (p.stages > kFewStages) p.stages = kFewStages;
-  err = allow_smem(matmul8_few_kernel<TN>, few_smem(TN));
+  err = allow_smem(matmul8_few_kernel<TN>, smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(tiles * S), 1, 1);
   cfg.blockDim = dim3(few_threads(TN), 1, 1);
-  cfg.dynamicSmemBytes = few_smem(TN);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -388,6 +385,7 @@ constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 
 constexpr int kBoxes = 2;                             // of a warp
 constexpr int kScaleGroups = 8;                       // groups whose scales are handed over together
 constexpr size_t kTileSmem = kTileStages * kTileStageBytes + kSumWarps * kBoxes * kBoxBytes + 1024;
+static_assert(tmem_alone(kTileSmem));
 constexpr int kGroupM = 16;                           // tile rows walked together
 constexpr int kMostPairs = 4;                         // of a cluster
 

@@ -20,6 +20,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
@@ -284,18 +285,6 @@ struct TriGrid {
 // reads.  Zero padding past r in both operands keeps the padded sums exact.
 constexpr int kTtcRows = 1024;
 constexpr int kTtcThreads = 256;
-__host__ __device__ inline int ttc_npad(int r) { return (r + 15) / 16 * 16; }
-__host__ __device__ inline int ttc_kc(int r) { return (ttc_npad(r) + 63) / 64; }
-// chunks of X^T held at once: all of them up to rank 128, else one at a time
-__host__ __device__ inline int ttc_bchunks(int r) { return ttc_kc(r) <= 2 ? ttc_kc(r) : 1; }
-__host__ __device__ inline size_t ttc_smem_bytes(int r) {
-  return (size_t)ttc_kc(r) * 2 * 16384 + (size_t)ttc_bchunks(r) * 2 * ttc_npad(r) * 128 + 1024;
-}
-__host__ __device__ inline uint32_t ttc_tmem_cols(int r) {
-  uint32_t c = 32;
-  while ((int)c < ttc_npad(r)) c <<= 1;
-  return c;
-}
 // 2^e that brings a largest magnitude m into [2^14, 2^15) (0 for m = 0 or not finite)
 __device__ __forceinline__ int ttc_exponent(float m) {
   if (!(m > 0.f) || !(m <= 3.4028234e38f)) return 0;
@@ -725,6 +714,7 @@ cudaError_t launch_gaussian_qr(const ProjBatch& batch, int64_t max_k, cudaStream
   if (err != cudaSuccess) return err;
   // the triangular products on the tensor cores, kTtcRows rows of one problem per block
   const size_t tc_smem = ttc_smem_bytes(r);
+  if (!tmem_safe(ttc_tmem_cols(r), tc_smem + kBlockSmem, false)) return cudaErrorInvalidConfiguration;
   err = cudaFuncSetAttribute(tri_apply_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tc_smem);
   if (err != cudaSuccess) return err;
   static thread_local TriGrid tg;

@@ -26,13 +26,14 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
 
 constexpr int kThreads = 128;
 constexpr int kChunk = 64;  // K elements per pipeline stage (one 128-byte swizzle row)
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = kSkinnyMaxStages;
 constexpr int kAccStripTiles = 1;  // 128-row tiles of C per persistent accumulation item
 
 // A launch covers up to kMaxProblems independent problems that share r (and so
@@ -760,12 +761,6 @@ __global__ void __launch_bounds__(256) split_transpose_kernel(const __grid_const
 
 int round16(int r) { return (r + 15) / 16 * 16; }
 
-uint32_t tmem_cols_for(int n_pad) {
-  uint32_t c = 32;
-  while ((int)c < n_pad) c <<= 1;
-  return c;
-}
-
 // Cluster split: enough CTAs for two per SM, at most 8 per cluster and at
 // least one K chunk per CTA.
 int choose_split(int m_tiles, int kchunks) {
@@ -782,26 +777,19 @@ cudaError_t launch_skinny(SkinnyBatch& a, cudaStream_t stream) {
   int min_chunks = a.kchunks[0];
   for (int i = 1; i < a.n; ++i) min_chunks = a.kchunks[i] < min_chunks ? a.kchunks[i] : min_chunks;
   const int split = choose_split(tiles, min_chunks);
-  a.stage_bytes = a.a_bytes + NB * a.b_bytes;
-  // two CTAs per SM when the stages fit in half of shared memory; stages wider
-  // than 48 KB (a B of 192+ rank columns, as grouped projections have) get
-  // the whole SM, since two of them per CTA would leave too few K chunks in
-  // flight to cover the loads
-  const uint32_t budget = a.stage_bytes > 48u * 1024u ? 208u * 1024u : 96u * 1024u;
-  int stages = (int)(budget / a.stage_bytes);
-  if (stages < 2) stages = 2;
-  if (stages > kMaxStages) stages = kMaxStages;
-  a.stages = stages;
-  a.red_stride = (a.n_pad + 31) / 32 * 32 + 4;
-  a.tmem_cols = tmem_cols_for(a.n_pad);
-  size_t smem = (size_t)stages * a.stage_bytes;
-  const size_t red_bytes = (size_t)128 * a.red_stride * sizeof(float);
-  if (red_bytes > smem) smem = red_bytes;
-  // at most two CTAs per SM, so their TMEM (<= 2 x 256 columns) always fits
-  if (smem < 80 * 1024) smem = 80 * 1024;
-  smem += 1024;  // alignment slack
   auto kernel = skinny_gemm_kernel<A_MN, B_MN, NB>;
-  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<size_t> known;
+  size_t fixed = 0;
+  cudaError_t err = static_smem(kernel, known, &fixed);
+  if (err != cudaSuccess) return err;
+  const SkinnySizes z = skinny_sizes(a.n_pad, a.a_bytes, a.b_bytes, NB, fixed);
+  if (!tmem_safe(z.tmem_cols, z.smem + fixed + kBlockSmem, true)) return cudaErrorInvalidConfiguration;
+  a.stage_bytes = z.stage_bytes;
+  a.stages = z.stages;
+  a.red_stride = z.red_stride;
+  a.tmem_cols = z.tmem_cols;
+  const size_t smem = z.smem;
+  err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)split, (unsigned)tiles, 1);
@@ -828,13 +816,12 @@ int acc_strip_tiles(int n_pad) {
 
 template <int MT, int NB>
 cudaError_t launch_acc_persistent(SkinnyBatch& a, cudaStream_t stream) {
-  a.stage_bytes = MT * 16384u + NB * a.b_bytes;
-  int stages = (int)((200u * 1024u) / a.stage_bytes);
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < 2) return cudaErrorInvalidConfiguration;
-  a.stages = stages;
-  a.tmem_cols = tmem_cols_for(2 * MT * a.n_pad);
-  const size_t smem = (size_t)stages * a.stage_bytes + 1024;
+  const PersistentSizes z = accumulate_sizes(a.n_pad, a.b_bytes, MT, NB);
+  if (z.stages < 2 || !tmem_safe(z.tmem_cols, z.smem + kBlockSmem, false)) return cudaErrorInvalidConfiguration;
+  a.stage_bytes = z.stage_bytes;
+  a.stages = z.stages;
+  a.tmem_cols = z.tmem_cols;
+  const size_t smem = z.smem;
   auto kernel = acc_persistent_kernel<MT, NB>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
@@ -846,34 +833,16 @@ cudaError_t launch_acc_persistent(SkinnyBatch& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_proj_persistent(SkinnyBatch& a, cudaStream_t stream) {
-  // two 64-wide K chunks per stage (longer runs of each token row of X, half
-  // the per-stage work of the issuing threads) where three such stages fit
-  const uint32_t one = a.a_bytes + 2 * a.b_bytes;
-  const int cb = (3 * 2 * one <= 200u * 1024u) ? 2 : 1;
-  // both parts of the split in one MMA (N = 2 n_pad): half the MMA
-  // instructions.  Up to rank 64 this keeps two tiles of accumulators in
-  // TMEM; above, the wider accumulators would leave room for one tile only,
-  // which measured slower than twice the MMAs (rank 128: 0.66 against 0.67 of HBM)
-  const bool stack = a.n_pad <= 64;
-  const int acc_n = stack ? 2 * a.n_pad : a.n_pad;
-  a.stage_bytes = cb * one;
-  int stages = (int)((200u * 1024u) / a.stage_bytes);
-  if (stages > kMaxStages) stages = kMaxStages;
-  if (stages < 2) return cudaErrorInvalidConfiguration;
-  a.stages = stages;
-  // partial accumulators: up to 4 per tile, two tiles in flight where TMEM
-  // holds them, else one tile of two
-  a.acc_bufs = 2;
-  a.k_parts = 4;
-  while (a.k_parts > 1 && a.acc_bufs * a.k_parts * acc_n > 512) a.k_parts >>= 1;
-  if (a.k_parts == 1) {
-    a.acc_bufs = 1;
-    a.k_parts = 2;
-  }
-  a.tmem_cols = tmem_cols_for(a.acc_bufs * a.k_parts * acc_n);
-  const size_t smem = (size_t)stages * a.stage_bytes + 1024;
-  auto kernel = stack ? (cb == 2 ? proj_persistent_kernel<2, 2, true> : proj_persistent_kernel<2, 1, true>)
-                      : (cb == 2 ? proj_persistent_kernel<2, 2, false> : proj_persistent_kernel<2, 1, false>);
+  const ProjectSizes z = project_sizes(a.n_pad, a.a_bytes, a.b_bytes);
+  if (z.p.stages < 2 || !tmem_safe(z.p.tmem_cols, z.p.smem + kBlockSmem, false)) return cudaErrorInvalidConfiguration;
+  a.stage_bytes = z.p.stage_bytes;
+  a.stages = z.p.stages;
+  a.acc_bufs = z.acc_bufs;
+  a.k_parts = z.k_parts;
+  a.tmem_cols = z.p.tmem_cols;
+  const size_t smem = z.p.smem;
+  auto kernel = z.stack ? (z.chunks == 2 ? proj_persistent_kernel<2, 2, true> : proj_persistent_kernel<2, 1, true>)
+                        : (z.chunks == 2 ? proj_persistent_kernel<2, 2, false> : proj_persistent_kernel<2, 1, false>);
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (err != cudaSuccess) return err;
   const int items = a.tile_begin[a.n];

@@ -16,6 +16,7 @@
 #include "common.cuh"
 #include "internal.h"
 #include "tc.cuh"
+#include "tmem.h"
 
 namespace rgs {
 namespace {
@@ -360,8 +361,6 @@ constexpr int kStoreWarps = 2;                    // tiles alternate between the
 constexpr int kCtlWarps = 2 + kStoreWarps;        // producer, MMA issuer, store warps
 constexpr int kEpiWarps = 16;                     // warps 4..19: four per TMEM lane quarter
 constexpr int kUpdThreads = (kCtlWarps + kEpiWarps) * 32;
-constexpr int kMaxStagesUpd = 8;
-constexpr int kTmemBufs = 4;                      // accumulator tiles in flight
 constexpr int kNormSlots = 8;                     // units whose ||W_new||^2 partials may be open at once
 
 struct Unit {
@@ -952,28 +951,16 @@ cudaError_t launch_update_tc(int n, const UpdateProblem* probs, const UpdateWork
   a.w_bytes = (uint32_t)(NCOLS / 64) * 16384u;
   a.err = errw;
   a.exact_count = exact;
-  // dynamic shared memory: what the opt-in limit leaves next to the static arrays
   cudaFuncAttributes fa;
   err = cudaFuncGetAttributes(&fa, update_persistent_kernel<NCOLS>);
   if (err != cudaSuccess) return err;
-  const size_t max_smem = 227 * 1024 - fa.sharedSizeBytes;
-  const size_t fixed = (size_t)parts * a.a_bytes + 1024;
-  const size_t p_stage = (size_t)parts * a.b_bytes;
-  // P stages (each one 64-wide chunk of r): up to rank 128 two, when they
-  // still leave three W stages (W comes from HBM and needs the deeper ring),
-  // else one; above, as many as leave two W stages (rank 256: a tile's four
-  // chunks, 4% faster than two).  The rest of shared memory goes to the W ring.
-  int p_stages = (fixed + 2 * p_stage + 3 * (size_t)a.w_bytes <= max_smem) ? 2 : 1;
-  if (a.kchunks > 2) {
-    p_stages = 2 * a.kchunks;
-    while (p_stages > 1 && fixed + p_stages * p_stage + 2 * (size_t)a.w_bytes > max_smem) --p_stages;
-  }
-  int w_stages = (int)((max_smem - fixed - p_stages * p_stage) / a.w_bytes);
-  if (w_stages > kMaxStagesUpd) w_stages = kMaxStagesUpd;
-  if (w_stages < 1) return cudaErrorInvalidConfiguration;
-  a.p_stages = p_stages;
-  a.w_stages = w_stages;
-  const size_t smem = fixed + p_stages * p_stage + (size_t)w_stages * a.w_bytes;
+  const UpdateSizes z =
+      update_sizes(a.kchunks, (size_t)parts * a.a_bytes, (size_t)parts * a.b_bytes, a.w_bytes, fa.sharedSizeBytes);
+  if (z.w_stages < 1 || !tmem_safe(kTmemBufs * NCOLS, z.smem + fa.sharedSizeBytes + kBlockSmem, false))
+    return cudaErrorInvalidConfiguration;
+  a.p_stages = z.p_stages;
+  a.w_stages = z.w_stages;
+  const size_t smem = z.smem;
   err = cudaFuncSetAttribute(update_persistent_kernel<NCOLS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (int)smem);
   if (err != cudaSuccess) return err;
