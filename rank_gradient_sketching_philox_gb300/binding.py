@@ -825,7 +825,10 @@ def adamw_batched(probs, lr, betas, eps, weight_decay, seed, step, grad_scale=No
 SCALE_BLOCK = 128  # columns, or rows and columns of a weight, that share a scale
 
 
-_set_device = torch._C._cuda_exchangeDevice  # returns the one before
+def _set_device(index):
+    """Make device ``index`` current; returns the one before.  (Looked up here, as below: a
+    PyTorch without CUDA has none of these functions, and imports this module all the same.)"""
+    return torch._C._cuda_exchangeDevice(index)
 
 
 def _launch(index, name, *args):
@@ -850,8 +853,8 @@ def _stream_on(stream, index):
     return stream.cuda_stream
 
 
-_lend = torch._C._cuda_cudaCachingAllocator_raw_alloc  # (bytes, stream) on the current device
-_take_back = torch._C._cuda_cudaCachingAllocator_raw_delete
+def _take_back(at):
+    torch._C._cuda_cudaCachingAllocator_raw_delete(at)
 
 
 def _borrow(op, T, k, index, handle, given):
@@ -867,7 +870,7 @@ def _borrow(op, T, k, index, handle, given):
         return None, 0, None
     before = _set_device(index)
     try:
-        at = _lend(nbytes, handle)
+        at = torch._C._cuda_cudaCachingAllocator_raw_alloc(nbytes, handle)  # of the current device
     finally:
         if before != index:
             _set_device(before)
