@@ -58,18 +58,24 @@ __device__ __forceinline__ void walk_units(const GradBatch& a, F f) {
   }
 }
 
-// A thread's values of a unit: vectors threadIdx.x, + 256, ... of it, or single
-// elements where the tensor does not start on 16 bytes or ends.  Values past the end
-// are zeros.  Not by way of the read-only cache: the kernel may come up while the one
-// before still writes the gradients.
+// A thread's values of a unit: the vectors threadIdx.x, + 256, ... of it, whole or, where the
+// tensor does not start on 16 bytes or ends, element by element, with zeros behind the
+// tensor.  Which they are does not depend on the tensor's place, nor does the sums' order.
+// (In steps of 256 elements, 268M BF16 values off 16 bytes took 186 us, not 152.)  Not by
+// way of the read-only cache: the kernel may come up while the one before still writes the
+// gradients.
 template <typename G>
 __device__ __forceinline__ void load_unit(const G* g, int64_t n, int64_t first, float (&v)[kEach]) {
   constexpr int VE = 16 / (int)sizeof(G);
-  if (first + kUnit <= n && on_vector(g)) {
+  const int left = (int)(n - first < kUnit ? n - first : kUnit);
+  const G* p = g + first + threadIdx.x * VE;
+  if (on_vector(g)) {
     uint4 raw[kEach / VE];
-    const uint4* p = reinterpret_cast<const uint4*>(g + first) + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < kEach / VE; ++j) raw[j] = p[j * kThreads];
+    for (int j = 0; j < kEach / VE; ++j) {
+      raw[j] = make_uint4(0, 0, 0, 0);
+      if ((j * kThreads + (int)threadIdx.x + 1) * VE <= left) raw[j] = *reinterpret_cast<const uint4*>(p + j * (kThreads * VE));
+    }
 #pragma unroll
     for (int j = 0; j < kEach / VE; ++j) {
       Pair q[VE / 2];
@@ -81,11 +87,17 @@ __device__ __forceinline__ void load_unit(const G* g, int64_t n, int64_t first, 
         v[j * VE + 2 * i + 1] = f.y;
       }
     }
+    if (left % VE == 0 || left / VE % kThreads != (int)threadIdx.x) return;
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {  // the tensor's last, cut vector
+      if (j / VE != left / VE / kThreads) continue;
+      v[j] = j % VE < left % VE ? (float)p[j / VE * (kThreads * VE) + j % VE] : 0.f;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < kEach; ++j) {
-      const int64_t e = first + j * kThreads + threadIdx.x;
-      v[j] = e < n ? (float)g[e] : 0.f;
+      const int at = j / VE * (kThreads * VE) + j % VE;
+      v[j] = at + (int)threadIdx.x * VE < left ? (float)p[at] : 0.f;
     }
   }
 }

@@ -809,3 +809,20 @@ def test_borrowed_workspaces_are_given_back():
         del junk
         assert torch.equal(dgamma, want) and torch.equal(other, want_other) and torch.equal(norm, want_norm)
         assert not held.any()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 7, 8191, 8192, 100_003, 3_000_001])
+def test_grad_norm_does_not_depend_on_the_gradients_place(n, dtype):
+    """Equal bits of the norm and of the scale, wherever a gradient starts between two 16-byte boundaries."""
+    g = gen(n)
+    values = (normal(g, n) * torch.exp(normal(g, n))).to(dtype)
+    got = []
+    for place in range(8 if dtype == BF else 4):
+        G = torch.full((place + n + 8,), math.nan, dtype=dtype, device="cuda")[place:place + n]
+        G.copy_(values)
+        clip = rgs.GradClip([G], 0.25)
+        clip.step()
+        check_norm([G], clip.norm, clip.scale, 0.25)
+        got.append((clip.norm, clip.scale))
+    assert all(torch.equal(norm, got[0][0]) and torch.equal(scale, got[0][1]) for norm, scale in got)
