@@ -492,8 +492,8 @@ SKETCH_API sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_ty
  * bs_col = 1), and dX = D W with B = Qt of W and the scales' strides exchanged.  A and
  * B are 16-byte aligned, ld_a and ld_b >= k and multiples of 16; k is any number >= 1, and what
  * lies between rows reaches no result.  Y: T x N BF16 or fp32, 16-byte aligned, ld_y a
- * multiple of 8.  overwrite = 1 replaces Y, 0 adds to an fp32 Y; a BF16 Y is always
- * replaced.  T, N and k are at most 2^24 each, T and N spanning at most 2^28
+ * multiple of 8.  overwrite = 1 replaces Y, 0 adds to it, which must be fp32
+ * then.  T, N and k are at most 2^24 each, T and N spanning at most 2^28
  * tiles of 256 x 256 (else SKETCH_ERR_UNSUPPORTED).  A block's products add up in fp32
  * on the tensor cores, the blocks in fp32; where an fp32 Y is added to, subnormal sums
  * may become zeros.  Y must not overlap an input. */

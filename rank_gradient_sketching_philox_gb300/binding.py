@@ -1004,7 +1004,8 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
     """Y = A B^T of codes with block scales: A (T x k) with a_scale (T x ceil(k /
     128)), B (N x k) with b_scale (ceil(N / 128) x ceil(k / 128), any strides).  A layer's output
     takes B = Q of its weight W and b_scale = scale, its input's gradient B = Qt
-    and b_scale = scale.t().  Y (T x N) BF16, or fp32, which overwrite=False adds to."""
+    and b_scale = scale.t().  Y (T x N) BF16, or fp32, which overwrite=False adds to
+    (a BF16 Y is refused then: its earlier terms would be lost)."""
     (T, k), _, dev = _matrix(A, "A")
     N = _matrix(B, "B")[0][0]
     ld_a, ld_b = _codes(A, T, k, dev, "A"), _codes(B, N, k, dev, "B")
@@ -1015,6 +1016,8 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
         ld_as = _groups(k)
     bs_row, bs_col = _scales(b_scale, _groups(N), _groups(k), dev, "b_scale")
     y_type = _dtype(Y, "Y")
+    if not overwrite and y_type == DTYPE_BF16:
+        raise ValueError("overwrite=False needs a float32 Y")
     ld_y = _like(Y, (T, N), Y.dtype, dev, "Y")
     if T == 1:
         ld_y = (N + 7) // 8 * 8

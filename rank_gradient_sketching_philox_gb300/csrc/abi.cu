@@ -822,6 +822,7 @@ sketch_status sketch_matmul_blocks(const uint8_t* A, int64_t T, int64_t k, int64
   CHECK_ELEM_PTR(b_scale, SKETCH_FP32);
   CHECK_PTR(Y);
   if (overwrite != 0 && overwrite != 1) return fail(SKETCH_ERR_INVALID_ARG, "overwrite must be 0 or 1");
+  if (!overwrite && y_type == SKETCH_BF16) return fail(SKETCH_ERR_INVALID_ARG, "overwrite=0 needs an fp32 Y");
   const rgs::MatmulBlocks a = {A,       T,      k,      ld_a, a_scale,     ld_as, B,        N,
                                ld_b,    b_scale, bs_row, bs_col, Y, (int)y_type, ld_y, overwrite};
   return launch_result(rgs::launch_matmul_blocks(a, static_cast<cudaStream_t>(stream)), "matmul_blocks");

@@ -112,6 +112,10 @@ def test_matmul_refuses(lib, kw, status, message):
     refused(lib, matmul(lib, **kw), status, message)
 
 
+def test_matmul_does_not_replace_what_it_is_to_add_to(lib):
+    refused(lib, matmul(lib, overwrite=0), BAD, "overwrite=0 needs an fp32 Y")
+
+
 def grads(**kw):
     a = dict(G=A, out=A, count=8, type=0)
     a.update(kw)

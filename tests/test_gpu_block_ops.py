@@ -826,3 +826,13 @@ def test_grad_norm_does_not_depend_on_the_gradients_place(n, dtype):
         check_norm([G], clip.norm, clip.scale, 0.25)
         got.append((clip.norm, clip.scale))
     assert all(torch.equal(norm, got[0][0]) and torch.equal(scale, got[0][1]) for norm, scale in got)
+
+
+def test_a_product_does_not_replace_what_it_is_to_add_to():
+    """A sum in BF16 would lose its earlier terms: refused, and Y stays."""
+    A, sa, B, sb = operands(gen(1), 4, 16, 128)
+    Y = torch.full((4, 16), 3.0, dtype=BF, device="cuda")
+    before = rgs.kernel_launches()
+    with pytest.raises(ValueError, match="overwrite=False"):
+        rgs.matmul_blocks(A, sa, B, sb, Y, overwrite=False)
+    assert rgs.kernel_launches() == before and bool((Y == 3.0).all())
