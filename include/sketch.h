@@ -492,11 +492,16 @@ SKETCH_API sketch_status sketch_quantize_blocks(const void* X, sketch_dtype x_ty
  * bs_col = 1), and dX = D W with B = Qt of W and the scales' strides exchanged.  A and
  * B are 16-byte aligned, ld_a and ld_b >= k and multiples of 16; k is any number >= 1, and what
  * lies between rows reaches no result.  Y: T x N BF16 or fp32, 16-byte aligned, ld_y a
- * multiple of 8.  overwrite = 1 replaces Y, 0 adds to it, which must be fp32
- * then.  T, N and k are at most 2^24 each, T and N spanning at most 2^28
- * tiles of 256 x 256 (else SKETCH_ERR_UNSUPPORTED).  A block's products add up in fp32
- * on the tensor cores, the blocks in fp32; where an fp32 Y is added to, subnormal sums
- * may become zeros.  Y must not overlap an input. */
+ * multiple of 8.  overwrite = 1 replaces Y, 0 adds to it, which must be fp32 then.  T, N
+ * and k are at most 2^24 each, T and N spanning at most 2^28 tiles of 256 x 256 (else
+ * SKETCH_ERR_UNSUPPORTED).  A block's products add up in fp32 on the tensor cores, the
+ * blocks in fp32; where an fp32 Y is added to, subnormal sums may become zeros.
+ * A block's two scales are multiplied by each other first, in fp32, and their product
+ * has to be a normal number, from 2^-126 up to below 2^128, where the block's sum is not zero.
+ * It is for scales of sketch_quantize_blocks or sketch_rms_norm_forward whose blocks' largest
+ * magnitudes multiply to 2.4e-33 at least and to less than 6.8e43.  Below the range the
+ * block's part of Y loses bits and then is zero; above it it is an infinity, and NaN where
+ * the sum is zero.  Y must not overlap an input. */
 SKETCH_API sketch_status sketch_matmul_blocks(const uint8_t* A, int64_t T, int64_t k, int64_t ld_a,
                                               const float* a_scale, int64_t ld_as, const uint8_t* B, int64_t N,
                                               int64_t ld_b, const float* b_scale, int64_t bs_row, int64_t bs_col,

@@ -1005,7 +1005,8 @@ def matmul_blocks(A, a_scale, B, b_scale, Y, overwrite=True, stream=None):
     128)), B (N x k) with b_scale (ceil(N / 128) x ceil(k / 128), any strides).  A layer's output
     takes B = Q of its weight W and b_scale = scale, its input's gradient B = Qt
     and b_scale = scale.t().  Y (T x N) BF16, or fp32, which overwrite=False adds to
-    (a BF16 Y is refused then: its earlier terms would be lost)."""
+    (a BF16 Y is refused then: its earlier terms would be lost).  A block's two scales are
+    multiplied by each other first: their product stays in fp32's normal range, 2^-126 to 2^128."""
     (T, k), _, dev = _matrix(A, "A")
     N = _matrix(B, "B")[0][0]
     ld_a, ld_b = _codes(A, T, k, dev, "A"), _codes(B, N, k, dev, "B")

@@ -384,6 +384,29 @@ def test_matmul_larger(T, N, k, dtype):
         assert bool((Y[:, N:] == 7.0).all())
 
 
+@pytest.mark.parametrize("T", [5, 24, 60, 300, 1500])
+@pytest.mark.parametrize("a_exp,b_exp", [(-63, -63), (-126, 0), (0, -126), (-20, -106), (63, 64), (127, 0), (0, 127)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_matmul_scales_at_the_ends_of_their_products_range(T, a_exp, b_exp, dtype):
+    """Scales whose products are fp32's smallest and largest normal powers of two: results are as exact as any, and
+    rows of zeros give zeros."""
+    N, k = 270, 500
+    A, sa, B, sb = operands(gen(T), T, N, k)
+    if a_exp + b_exp > 0:  # values of 2^-6 at most: 500 products of them add up to 2^-3, times 2^127 that is no infinity
+        A.copy_(A.float() / 448 * 2.0 ** -6), B.copy_(B.float() / 448 * 2.0 ** -6)
+    sa.fill_(2.0 ** a_exp), sb.fill_(2.0 ** b_exp)
+    A[3], B[7], B[130:256] = 0, 0, 0
+    Y = torch.full((T, 272), 7.0, dtype=dtype, device="cuda")[:, :N]
+    rgs.matmul_blocks(A, sa, B, sb, Y)
+    a, b = A.double() * wide(sa, 1, T, k), B.double() * wide(sb, 128, N, k)
+    want, size = a @ b.t(), a.abs() @ b.abs().t()
+    # as in check_product; below 2^-126 a step is 2^-149 (BF16 2^-133) whatever the value: half of it for the result's
+    # rounding, and for each block's
+    least = (groups(k) + 3) * 2.0 ** -150 + (2.0 ** -134 if dtype == BF else 0.0)
+    close(Y, want, size * (2.0 ** -16 + (groups(k) + 3) * U) + want.abs() * (HALF[dtype] + 2 * U) + least)
+    assert not Y[3].any() and not Y[:, 7].any() and not Y[:, 130:256].any()
+
+
 @pytest.mark.parametrize("T", [3, 40, 300, 1000])
 def test_matmul_adds_to_fp32(T):
     g = gen(T)
