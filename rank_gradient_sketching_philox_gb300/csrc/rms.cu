@@ -672,7 +672,7 @@ __global__ void __launch_bounds__(THREADS, backward_blocks(THREADS))
 }
 
 template <typename X, int VE, int NV, int THREADS, bool DS>
-cudaError_t backward_rows(const RmsBackward& a, int tpr, bool& done, cudaStream_t stream) {
+cudaError_t backward_rows(const RmsBackward& a, int tpr, cudaStream_t stream) {
   const int groups = THREADS / tpr, matrices = DS ? 3 : 2, per_sm = backward_blocks(THREADS);
   // rows side by side: as many as the kernel takes while every block still has a set
   int each = 1;
@@ -688,8 +688,7 @@ cudaError_t backward_rows(const RmsBackward& a, int tpr, bool& done, cudaStream_
   r.slot = r.pitch * (uint32_t)(r.rows * matrices);
   const uint32_t room = (uint32_t)(kMostSmem / per_sm);
   r.slots = (int)(room / r.slot < kMaxSlots ? room / r.slot : kMaxSlots);
-  if (r.slots < 1) return cudaSuccess;
-  done = true;
+  if (r.slots < 1) return cudaErrorInvalidConfiguration;  // the widest set, 16384 fp32 values of three matrices, has 192 KB
   int* err_word = nullptr;
   cudaError_t err = device_error_word(&err_word);
   if (err != cudaSuccess) return err;
@@ -704,13 +703,13 @@ cudaError_t backward_rows(const RmsBackward& a, int tpr, bool& done, cudaStream_
 }
 
 template <typename X, int VE, bool DS>
-cudaError_t backward(const RmsBackward& a, bool& done, cudaStream_t stream) {
+cudaError_t backward(const RmsBackward& a, cudaStream_t stream) {
   constexpr int NV = 16 / VE;  // 16 elements of a row per thread, 32 above 8192
   int tpr = threads_per_row(a.k / VE, NV, a.T, 512);
   if (tpr < 32) tpr = 32;
-  if (tpr <= 256) return backward_rows<X, VE, NV, 256, DS>(a, tpr, done, stream);
-  if (a.k <= 8192) return backward_rows<X, VE, NV, 512, DS>(a, 512, done, stream);
-  return backward_rows<X, VE, 2 * NV, 512, DS>(a, 512, done, stream);
+  if (tpr <= 256) return backward_rows<X, VE, NV, 256, DS>(a, tpr, stream);
+  if (a.k <= 8192) return backward_rows<X, VE, NV, 512, DS>(a, 512, stream);
+  return backward_rows<X, VE, 2 * NV, 512, DS>(a, 512, stream);
 }
 
 template <typename X>
@@ -719,11 +718,8 @@ cudaError_t backward_any(const RmsBackward& a, cudaStream_t stream) {
   if (a.k <= kMaxRowWidth) {
     auto whole = [&](const void* p, int64_t ld) { return p == nullptr || whole_vectors(p, ld, a.k, VE, sizeof(X)); };
     const bool vectors = whole(a.S, a.ld_s) && whole(a.dY, a.ld_dy) && whole(a.dS, a.ld_ds) && whole(a.dX, a.ld_dx);
-    bool done = false;
-    cudaError_t err;
-    if (a.dS) err = vectors ? backward<X, VE, true>(a, done, stream) : backward<X, 1, true>(a, done, stream);
-    else err = vectors ? backward<X, VE, false>(a, done, stream) : backward<X, 1, false>(a, done, stream);
-    if (done || err != cudaSuccess) return err;
+    if (a.dS) return vectors ? backward<X, VE, true>(a, stream) : backward<X, 1, true>(a, stream);
+    return vectors ? backward<X, VE, false>(a, stream) : backward<X, 1, false>(a, stream);
   }
   if (a.dgamma) {
     const int64_t rows = ceil_div(a.T, kMaxPartials) > 32 ? ceil_div(a.T, kMaxPartials) : 32;

@@ -223,6 +223,19 @@ def test_rms_backward(T, k, dtype, w, res):
     check_backward(dy, s, gamma, rstd, ds, None, dgamma, before)
 
 
+@pytest.mark.parametrize("dtype,k", [(F32, 16384), (F32, 16383), (BF, 16384), (BF, 16381)])
+@pytest.mark.parametrize("res", [True, False])
+def test_rms_backward_of_the_widest_rows_one_after_another(dtype, k, res):
+    """Rows of which shared memory holds a single set (fp32 with the stream's gradient) or few, several to a block."""
+    g, T = gen(k), 500
+    s, dy, ds = (normal(g, T, k, std=std).to(dtype) for std in (2.0, 1e-3, 1e-3))
+    ds = ds if res else None
+    rstd = (s.double().square().mean(1) + 1e-6).rsqrt().float()
+    dX, dgamma = torch.empty_like(s), torch.empty(k, device="cuda")
+    rgs.rms_norm_backward(dy, s, None, rstd, dS=ds, dX=dX, dgamma=dgamma, overwrite=True)
+    check_backward(dy, s, None, rstd, ds, dX, dgamma)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("k", [40, 264, 1001, 4096])
 @pytest.mark.parametrize("place", [0, 1, 3, 8])
