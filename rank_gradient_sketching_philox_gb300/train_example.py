@@ -137,7 +137,7 @@ class Model:
         params = [self.embedding] + [getattr(n, w) for n in self.norms for w in names]
         grads = [self.dembedding] + [getattr(n, "d" + w) for n in self.norms for w in names]
         self.adam = AdamW(params, grads, state_bits=8, seed=seed, layers=range(1000, 1000 + len(params)))
-        self.clip = GradClip(grads, clip) if clip else None
+        self.clip = None if clip is None else GradClip(grads, clip)
 
     def microbatch(self, tokens, targets, first, weight):
         """Forward and backward of one microbatch; returns its tokens' losses.  A negative target is ignored."""

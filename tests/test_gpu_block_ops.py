@@ -704,6 +704,14 @@ def test_the_example_runs_with_these_operators():
     assert len(losses) == 3 and all(math.isfinite(x) for x in losses)
 
 
+@pytest.mark.parametrize("most", ["0", "-1", "nan"])
+def test_the_example_refuses_a_norm_that_is_no_bound(most):
+    """As GradClip does; 0 is not taken for no clipping."""
+    from rank_gradient_sketching_philox_gb300 import train_example
+    with pytest.raises(ValueError, match="max_norm"):
+        train_example.main(["--steps", "1", "--tokens", "64", "--clip=" + most])
+
+
 @pytest.mark.parametrize("products", ["bf16", "8bit"])
 def test_the_examples_gradients(products):
     """A microbatch's gradients of the stream, through every norm and product, against autograd in 64 bits."""
