@@ -446,7 +446,8 @@ SKETCH_API sketch_status sketch_adamw_batched(int n, const sketch_adamw_problem*
  * may be X or R where S is not that one.  Q and scale (nullable, both or neither; Y or Q is given)
  * receive y in 8 bits for sketch_matmul_blocks, rows on 16 bytes (ld_q a multiple of
  * 16): E4M3 codes and an fp32 scale for each row's 128 columns, T x ceil(k / 128)
- * contiguous, the block's largest magnitude over 448 (at least 2^-126).  A block that
+ * contiguous, the block's largest magnitude over 448 (at least 2^-126), rounded as
+ * sketch_quantize_blocks does.  A block that
  * holds an infinity or a NaN has a NaN scale and NaN codes.  gamma: k contiguous
  * values of w_type, or NULL (ones).  rstd (T fp32, nullable) is for the backward pass.
  * All sums are fp32: S's rounding does not enter Y, nor Y's Q; a row whose squares
@@ -477,7 +478,9 @@ SKETCH_API sketch_status sketch_rms_norm_backward(const void* dY, int64_t ld_dy,
  *
  * Codes and scales of X (T x k of x_type, any row stride >= k): rows = 1, or 128 for
  * weights; scale: ceil(T / rows) x ceil(k / 128) contiguous, the block's largest magnitude
- * over 448 (at least 2^-126); codes round to nearest, ties to even.  Q: T x k.  Qt
+ * over 448 (at least 2^-126), to within 2^-23 of it; codes are those nearest to x / scale,
+ * ties to even, where the quotient is known to within 2^-22 of itself: one that near to the
+ * middle between two codes may have either.  Q: T x k.  Qt
  * (nullable, rows = 128 only): the same codes transposed, k x T, for the product D W;
  * its scales are those of Q, transposed.  Q may then be NULL.  Q and Qt are 16-byte
  * aligned with row strides that are multiples of 16; what lies between rows is left as

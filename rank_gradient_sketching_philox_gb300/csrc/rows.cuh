@@ -230,8 +230,11 @@ __device__ __forceinline__ uint32_t top_magnitude(const float (&x)[N]) {
 }
 
 // A block's scale from the bits of its largest magnitude, and what its values are
-// multiplied by: an approximate reciprocal, good to 2^-23, where a code's own rounding
-// is 2^-4.  The scale is a normal number, so that the reciprocal is one too.
+// multiplied by.  Both roundings are choices: the scale is the magnitude times the rounded
+// 1 / 448, within 2^-23 of the quotient, and the reciprocal an approximate one, good to
+// 2^-23, so that a value comes within 2^-22 of its quotient by the scale before its code's own
+// rounding, 2^-4.  One value in some 200,000 lies that near to the middle between two codes.  The
+// scale is a normal number, so that the reciprocal is one too.
 __device__ __forceinline__ float code_scale(uint32_t top, float& inv) {
   float scale = fmaxf(__uint_as_float(top) * (1.f / 448.f), kScaleLeast);
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(scale));

@@ -323,6 +323,26 @@ def test_quantize_rounds_to_nearest_even():
     assert torch.equal(Q.view(torch.uint8), x.to(E4).view(torch.uint8))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [1, 128])
+@pytest.mark.parametrize("size", [1.0, 1e-30, 1e-36, 1e-38, 1e30, 5e36])
+def test_quantize_keeps_to_its_bounds(dtype, rows, size):
+    """Scales within 2^-23 of the quotient; codes that are nearest to a number within 2^-22 of x / scale."""
+    T, k = 1024, 1000
+    g = gen(rows)
+    x = (normal(g, T, k).clamp(-8, 8) * torch.exp(normal(g, T, 1)).clamp(max=4.0) * size).to(dtype)
+    Q, scale = rgs.code_rows(T, k), torch.empty(-(-T // rows), groups(k), device="cuda")
+    rgs.quantize_blocks(x, Q, scale, rows=rows)
+    want = (tops(x.double(), rows) / 448.0).clamp(min=2.0 ** -126)
+    close(scale, want, want * 2.0 ** -23)
+    units = (x.double() / wide(scale, rows, T, k)).abs()
+    # the conversions to fp32 here may bring the two ends 2^-24 nearer: the codes' bound is 3/4 of 2^-22
+    low, high = ((units * (1 + f)).float().clamp(max=448.0).to(E4).float() for f in (-2.0 ** -22, 2.0 ** -22))
+    q = Q.float().abs()
+    assert bool(((low <= q) & (q <= high)).all())
+    assert bool(((Q.float() * x.float()) >= 0).all())
+
+
 @pytest.mark.parametrize("rows", [1, 128])
 def test_quantize_extremes(rows):
     x = torch.zeros(128 * 5, 130, device="cuda")
