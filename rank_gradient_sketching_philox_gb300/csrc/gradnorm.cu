@@ -4,9 +4,9 @@
 //   norm = sqrt(sum over all tensors of g^2),  scale = 1 where norm <= max_norm, else max_norm / norm
 //
 // Bound by HBM: the norm reads each gradient once, the scaling reads and writes it.  268M
-// BF16 values on one GB300: norm 83 us, 0.95 of the copy rate, scaling 153, 1.03 (a unit to
-// a block; 1216 blocks of many units 167), both 238.  114 tensors of 2048 values: 7.5 us on
-// the device, two launches, a call 8 to 9.
+// BF16 values on one GB300: norm 81 us, 0.98 of the copy rate, scaling 153, 1.03 (a unit to
+// a block; 1216 blocks of many units 167), both 238; off 16 bytes the norm takes 151, the
+// scaling 600.  114 tensors of 2048 values: 6.4 us on the device, two launches, a call 8 to 10.
 //
 // The tensors are cut into units of
 // kUnit values, dealt to at most kBlocks blocks, whatever the GPU's size, so that the

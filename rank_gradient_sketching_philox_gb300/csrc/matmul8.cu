@@ -9,26 +9,29 @@
 // fp32 registers, groups in their order.
 //
 // What bounds it, one GB300.  Many tokens: the sums.  8192 x 12288 x 4096 (T x N x k)
-// takes 284 to 287 us, 2.9 PFLOP/s, and in a long run of passes, at the power limit,
-// 322 to 328; a library product with one scale for each matrix takes 221 and 244.  The same
-// kernel without the sums takes 222 us: a group's MMAs take 512 cycles, and in that time
-// eight warps have to see their end, read 256 columns of 128 rows from TMEM, add them,
-// times their scales, and hand the accumulators back.  What brought it there: an arrival on
-// the other CTA's barrier without a release to the cluster (870 -> 395 us), the scales
-// through shared memory, whole warps that walk the issuing loops (363 -> 352), four
-// accumulators and two MMA warps with the loads from TMEM beside the sums (352 -> 302),
-// fewer and wider loads of the scales and the registers that they leave (302 -> 287).
-// Without the multiply-adds it takes 240, without the loads from TMEM 266, without either
-// 238: what is left is the accumulators' way between the CTAs, some 800 cycles of the 1024
-// that TMEM holds, and the multiply-adds.  Tried and dropped: MMAs of each CTA alone, B's
-// rows sent to both (301; these MMAs by themselves take 288), 16 warps of 64 columns (345),
-// an arrival of one thread for a CTA (397 of then 366), pieces of 24 columns (287 of then
-// 289), 32 (294, but 4096 x 4096 x 12288 168 for 154) or 64 (371 to 437), the next group's
-// scales or barrier looked at ahead (318 to 353), waits that spin (285 to 304), scales by
-// asynchronous copies (308).
+// takes 285 us, 2.9 PFLOP/s, and in a long run of passes, at the power limit, 321 to 328; a
+// library product with one scale for each matrix takes 221 and 244.  An fp32 Y, whose 400 MB
+// are 59 us of writing, takes 330 to 340 there, one that is added to 355 to 370.  Rows of
+// scales off 16 bytes cost nothing: 8192 x 12288 takes 8.4 us for each group at k = 11008 (86
+// groups) and at 11264 (88).  Without the sums the kernel takes 222 us: a group's MMAs take
+// 512 cycles, and in that time eight warps have to see their end, read 256 columns of 128
+// rows from TMEM, add them, times their scales, and hand the accumulators back.  Without the
+// multiply-adds it takes 240, without the loads from TMEM 266, without either 238: what
+// is left is the accumulators' way between the CTAs, some 800 cycles of the 1024 that TMEM
+// holds, and the multiply-adds.  What brought it there, each step from the time before it:
+// an arrival on the other CTA's barrier without a release to the cluster (870 to 395 us),
+// the scales through shared memory (363), whole warps that walk the issuing loops (352), four
+// accumulators and two MMA warps with the loads from TMEM beside the sums (302), scales
+// multiplied ahead and four boxes a warp (294), fewer and wider loads of the scales and
+// the registers that they leave (285).  Tried and dropped, against the kernel of their day:
+// MMAs of each CTA alone, B's rows sent to both (1 % longer; these MMAs by themselves take
+// as long as the whole kernel), an arrival of one thread for a CTA (8 %), scales by
+// asynchronous copies (3 %), pieces of 24 columns (as long), of 32 (as long, but 4096 x 4096 x
+// 12288 9 % longer); slower, too, were pieces of 64 columns, 16 warps of 64 columns, the next
+// group's scales or barrier looked at ahead, and waits that spin.
 //
 // Few tokens: B's bytes and the start: 16 x 4096 x 4096 7.4 us on the device, of which 2.5
-// are its 17 MB, 16 x 12288 x 4096 12.1 (50 MB, 7.4); a call takes 8 to 10.
+// are its 17 MB, 16 x 12288 x 4096 12.0 (50 MB, 7.4); a call takes 8 to 10.
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -378,8 +381,7 @@ constexpr int kTileThreads = 128 + 32 * kSumWarps;    // copies, MMAs, scales, a
 constexpr int kSumCols = 128;                         // of a thread
 constexpr int kLoads = kSumCols / 16;                 // from TMEM, of 16 columns
 // Registers: the launch has 168 for each thread, 384 * 168 = 128 * 88 + 256 * 208.  8192 x
-// 12288 x 4096 takes 290 us with them, with 72 and 216 301, with 104 and 200 304, with 120
-// and 192 303.
+// 12288 x 4096 takes 4 to 5 % longer with 72 and 216, 104 and 200, or 120 and 192.
 constexpr int kFewRegisters = 88, kSumRegisters = 208;
 constexpr uint32_t kBoxBytes = 32 * 64;               // a warp's 32 rows of 64 bytes, on their way to Y
 constexpr int kBoxes = 2;                             // of a warp
@@ -426,8 +428,8 @@ __device__ __noinline__ void put_end(const Product8& a, int64_t row, int col, ui
   }
 }
 
-// SPLIT: clusters of several pairs (one kernel for both took 307 us for 8192 x 12288 x
-// 4096, not 296 as then).
+// SPLIT: clusters of several pairs (one kernel for both took 4 % longer for 8192 x 12288 x
+// 4096).
 template <bool SPLIT>
 __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __grid_constant__ Product8 a) {
   extern __shared__ uint8_t smem_raw[];
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
         __syncwarp();
       }
       // a wait that gives up makes all later ones give up too; looked at now and then (each
-      // time, 8192 x 12288 x 4096 took 303 us, not 296 as then)
+      // time, 8192 x 12288 x 4096 took 2 % longer)
       if ((it & 14) == 14 && !__all_sync(0xFFFFFFFFu, live)) break;
       tph ^= 1u;
       s += 2;
@@ -578,7 +580,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) matmul8_tile_kernel(const __g
     // ---- scales: of the CTA's 128 rows, times those of the tile's two column blocks ----
     // Four groups' of a row in one load, where they lie on 16 bytes.  With each read singly,
     // the columns' by every lane, this warp took longer than eight groups' MMAs, or the
-    // registers that the sums' warps want (8192 x 12288 x 4096 313 us with 88, not 290).
+    // registers that the sums' warps want (8192 x 12288 x 4096 8 % longer with 88).  Rows off 16
+    // bytes, four loads for one, keep up (8.4 us a group at 86 groups and at 88).
     const bool fours = ((reinterpret_cast<uintptr_t>(a.a_scale) | (uintptr_t)(a.ld_as * 4) | (uintptr_t)(c0 * 4)) & 15u) == 0;
     int batch = 0;
     bool live = true;
@@ -881,7 +884,9 @@ cudaError_t launch_matmul_blocks(const MatmulBlocks& a, cudaStream_t stream) {
   // Which takes less, in us as measured: few tokens' kernel 5 and 0.85 for each group one
   // after another; the pairs of CTAs 5 and 0.37 for each group, 1.5 for each further round
   // of tiles, and 4 more for the join where several pairs share a tile (two groups or
-  // more each).  4096 x 4096 with 64 tokens 9.6 against 12.9, with 192 15.9 against 13.4;
+  // more each).  Of BF16 outputs; what an fp32 one takes longer (256 tokens, 4096 x 4096,
+  // 15.5 for 14.2, added to 16.8) is left out of the rule.
+  // 4096 x 4096 with 64 tokens 9.6 against 12.9, with 192 15.9 against 13.4;
   // 12288 x 4096 with 64 16.1 against 17.3, with 96 25 against 17.7; 4096 x 12288 with
   // 256 tokens 21.7 with three pairs to a tile, 42 with one.
   int fit[kMostPairs + 1];

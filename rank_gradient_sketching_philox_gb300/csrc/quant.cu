@@ -2,12 +2,12 @@
 // or of 128 rows and 128 columns (rows.cuh), and of its transpose beside it.
 //
 // Bound by HBM: 3 bytes for a BF16 value, 4 with the transpose.  One GB300, of the copy
-// rate: 4096 x 12288 rows 24.3 us, 0.92 (four pieces of a row to a thread 25.6, 64-bit
-// divisions for each 28.5); 12288 x 4096 weights with their transpose 32.3 us, 0.92, without
-// 24.5; fp32 rows 16384 x 4096 52 us, 0.95, weights 8192 x 4096 with their transpose 32.2,
-// 0.92.  Of 6144 x 2048 weights, 9.6 us, 0.77, the blocks are one round, in which all load
+// rate: 4096 x 12288 rows 24.1 us, 0.93 (four pieces of a row to a thread 25.6, 64-bit
+// divisions for each 28.5); 12288 x 4096 weights with their transpose 32.5 us, 0.91, without
+// 24.5; fp32 rows 16384 x 4096 54 us, 0.92, weights 8192 x 4096 with their transpose 32.5,
+// 0.91.  Of 6144 x 2048 weights, 9.6 us, 0.77, the blocks are one round, in which all load
 // before they store.  Rows that are not whole vectors are gathered from L1, value by value:
-// 4096 x 12287 36 us, 12287 x 4095 weights with their transpose 68 (their values cut from
+// 4096 x 12287 36 us, 12287 x 4095 weights with their transpose 69 (their values cut from
 // whole 16-byte pieces took as many instructions: rows 41 to 47 us, weights 64 to 67).
 #include <cuda_bf16.h>
 

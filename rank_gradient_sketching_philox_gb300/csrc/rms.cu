@@ -12,13 +12,14 @@
 // Bound by HBM.  One GB300, of the copy rate, 32768 x 4096 BF16: forward with residual,
 // BF16 and 8-bit output 188 us, 0.95 (9 bytes a value; with loads that go first from the
 // caches 191); with residual and BF16 output 164, 0.97; BF16 output alone 84, 0.94; 8-bit
-// output alone 93, 0.64, where the codes'
-// instructions take 62 % of the issue slots; backward with the stream's gradient 164 us,
-// 0.96 (8 bytes), without it 140, 0.85.  8192 x 16384 forward 194 us, 0.92, backward 178,
-// 0.89; fp32 16384 x 4096 176 and 160.  Rows on other places than 16 bytes: 32768 x
-// 4095 forward 287 us, 0.62, backward 249, 0.63; the elements' shared memory reads and
-// single stores take the rest.  8 x 2048 forward: 2.4 us on the device, a call 8 to 9; 1021
-// x 1001 fp32 backward: 9.6 us on the device, two launches, a call 12 to 13.
+// output alone 93, 0.64: its instructions take 67 % of the issue slots of warps that have
+// 45 % of their places; backward with the stream's gradient 163 us, 0.97 (8 bytes), without
+// it 140, 0.85.  8192 x 16384 forward 206 us, 0.87, backward 179, 0.88; fp32 16384 x 4096 185,
+// 0.91, and 160, 0.99.  Rows on other places than 16 bytes: 32768 x 4095 forward 289 us, 0.62,
+// backward 248, 0.64; the elements' shared memory reads and single stores take the rest.
+// Wider rows than 16384 are read twice, value by value: 6554 x 20480 forward 412 us, 0.43,
+// backward 742, 0.21.  8 x 2048 forward: 2.7 us on the device, a call 8 to 9; 1021 x 1001
+// fp32 backward: 10.2 us on the device, two launches, a call 12 to 14.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -265,8 +265,8 @@ inline int threads_per_row(int64_t nvec, int most, int64_t T, int limit) {
 }
 
 // Let a kernel have `smem` bytes of dynamic shared memory, kMostSmem at most.  Static
-// and dynamic parts of up to 48 KB together need no asking; the kernels' static parts
-// stay below 1 KB.  The limit is the kernel's, not the launch's: it is the same for
+// and dynamic parts of up to 48 KB together need no asking; the static parts of the kernels
+// that come here with up to 47 KB stay below 1 KB.  The limit is the kernel's, not the launch's: it is the same for
 // every size, so that another host thread's launch never finds it lowered.
 template <typename Kernel>
 cudaError_t allow_smem(Kernel kernel, size_t smem) {

@@ -73,7 +73,10 @@ class GradClip:
     ``outs`` (tensors of the same sizes and types, or the gradients themselves) it
     also writes the scaled gradients there; none of them overlaps another, or another's
     gradient.  Before the first step norm and scale hold nothing.  The object is bound to its tensors
-    and keeps the call's workspace, so its steps are ordered on one stream.
+    and keeps the call's workspace, so its steps are ordered on one stream.  Building it checks
+    every tensor, which takes the host some 2.4 us for each (0.3 ms for 114, a step 9 us): gradients
+    that are new tensors in every step (``zero_grad(set_to_none=True)``) need a new object each
+    time, gradients that stay where they are, as sketches do, one for all steps.
     """
 
     def __init__(self, grads, max_norm, outs=None):
